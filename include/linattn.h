@@ -51,7 +51,8 @@ typedef enum {
     LA_ERR_INVALID_ARG = 1, /* null/misaligned pointer, negative size, overflow */
     LA_ERR_UNSUPPORTED = 2, /* D or M not in {32, 64, 128}, unknown dtype */
     LA_ERR_CUDA = 3,        /* a CUDA runtime call failed (message has details) */
-    LA_ERR_TIMEOUT = 4      /* a bounded device-side wait gave up (see la_check_device_status) */
+    LA_ERR_TIMEOUT = 4,     /* a bounded device-side wait gave up (see la_check_device_status) */
+    LA_ERR_BAD_INDEX = 5    /* a length, page or slot in device memory was out of range (likewise) */
 } la_status;
 
 typedef enum { LA_DTYPE_F32 = 0, LA_DTYPE_BF16 = 1 } la_dtype;
@@ -234,6 +235,136 @@ la_status la_softmax_decode_step(const void* q, const void* k, const void* v, vo
                                  int M, la_dtype dtype, void* stream);
 
 /*
+ * Gated linear recurrence, one decay per token and channel (gated retention's
+ * gamma_t, "Transformer and Variants" section 1.3.4, with a state of one value
+ * per channel): over the rows t of each sequence and every channel c,
+ *   LA_GATE_DECAY   h_t = a_t h_{t-1} + x_t                 (a_t the decay itself)
+ *   LA_GATE_LOGIT   h_t = s_t h_{t-1} + (1 - s_t) x_t,  s_t = sigmoid(a_t)
+ * from h_init (or 0).  Token-major rows, any channel count C >= 1.
+ *   A, X  [B][N][C] dtype                       (read)
+ *   Out   [B][N][C] dtype                       (written) h_t rounded to dtype
+ *   seq_starts [num_seqs + 1] int32, nullable   (read) packed sequences: with it
+ *         B must be 1, and rows seq_starts[i] .. seq_starts[i+1] - 1 are sequence
+ *         i (non-decreasing, from 0 up; empty sequences allowed).  Rows behind
+ *         the last sequence are not written.  Values outside 0 .. N act as if
+ *         cut to that range.  NULL: every batch row is a sequence, num_seqs 0.
+ *   h_init  [sequences][C] fp32, nullable (read)     state before the first row
+ *   h_final [sequences][C] fp32, nullable (written)  state after the last row
+ *         (of an empty sequence: h_init, or 0)
+ *   Ckpt  fp32, nullable (written) la_gated_scan_ckpt_floats(B, N, C) words: the
+ *         running state before every 256th row, for the backward
+ * Decays lie in [-1, 1]; the state is fp32 throughout.  A sequence's rows do
+ * not depend on other sequences, whatever values those hold.  Out, h_final and
+ * Ckpt may not alias inputs or each other.
+ */
+typedef enum { LA_GATE_DECAY = 0, LA_GATE_LOGIT = 1 } la_gate_form;
+la_status la_forward_gated_scan(const void* A, const void* X, void* Out, int B, int N, int C,
+                                la_dtype dtype, la_gate_form form, const int* seq_starts, int num_seqs,
+                                const float* h_init, float* h_final, float* Ckpt, void* stream);
+
+/* Size in fp32 words of the gated scan's checkpoints: B * ceil(N / 256) * C, or
+ * 0 for non-positive sizes.  Pure arithmetic; no device call. */
+size_t la_gated_scan_ckpt_floats(int B, int N, int C);
+
+/*
+ * Gradient of la_forward_gated_scan: with s_t the decay and g_t the whole
+ * gradient at h_t,
+ *   g_t = dOut_t + s_{t+1} g_{t+1}   (last row of a sequence: dOut_t + dh_final)
+ *   LA_GATE_DECAY   dA_t = g_t h_{t-1},                          dX_t = g_t
+ *   LA_GATE_LOGIT   dA_t = s_t (1 - s_t) g_t (h_{t-1} - x_t),    dX_t = (1 - s_t) g_t
+ *   dh_init = s_1 g_1 (first row of a sequence; dh_final or 0 for an empty one)
+ *   A, X, dOut [B][N][C] dtype                  (read)
+ *   dA, dX     [B][N][C] dtype                  (written; rows behind the last
+ *              packed sequence are not)
+ *   seq_starts, num_seqs, h_init                as given to the forward
+ *   dh_final [sequences][C] fp32, nullable (read)    dL/dh_final (0 if NULL)
+ *   dh_init  [sequences][C] fp32, nullable (written) dL/dh_init
+ *   Ckpt  nullable (read) the forward's checkpoints from the same inputs; the
+ *         call computes them itself when NULL
+ * The states are recomputed in fp32 from the inputs; the forward's rounded Out
+ * is not used.  Outputs may not alias inputs or each other.
+ */
+la_status la_backward_gated_scan(const void* A, const void* X, const void* dOut, void* dA, void* dX,
+                                 int B, int N, int C, la_dtype dtype, la_gate_form form,
+                                 const int* seq_starts, int num_seqs, const float* h_init,
+                                 const float* dh_final, float* dh_init, const float* Ckpt,
+                                 void* stream);
+
+/*
+ * One token of the gated recurrence for B sequences: h is updated in place and
+ * out receives it rounded to dtype.
+ *   a, x [B][C] dtype (read);  h [B][C] fp32 (read and updated);  out [B][C] dtype (written)
+ */
+la_status la_gated_scan_decode_step(const void* a, const void* x, float* h, void* out, int B, int C,
+                                    la_dtype dtype, la_gate_form form, void* stream);
+
+/*
+ * Paged key-value cache, the ragged form of la_softmax_decode_step's cache.
+ * Two pools K_pages, V_pages [num_pages][Hkv][page_size][D] hold the positions
+ * of many requests; position p of request r is on page
+ * block_table[r][p / page_size] at offset p % page_size, and its slot number is
+ * page * page_size + offset.  page_size is a power of two up to 1024, and
+ * num_pages * page_size < 2^31.  Lengths, pages and slots are read on the GPU:
+ * one that is out of range has its access skipped and is reported by the next
+ * la_check_device_status as LA_ERR_BAD_INDEX.
+ *
+ * la_page_map: the step's bookkeeping, from request lengths.  Request r holds
+ * cached_lens[r] positions and gets new_lens[r] more; the pages that these open
+ * are taken from free_pages in the order of the requests.
+ *   cached_lens, new_lens [R] int32   (read)
+ *   free_pages [num_free] int32       (read) page numbers that no request holds
+ *   block_table [R][max_pages] int32  (the pages held are read, those opened are
+ *              written, the rest is left as it is; a request's positions past
+ *              max_pages * page_size are out of range and get slot -1)
+ *   slot_map [max_tokens] int32       (written) the slots of the new positions,
+ *              request after request; -1 behind the last one, and where a page
+ *              is missing (no free page left: its table entry is -1 too)
+ *   seq_starts [R + 1] int32          (written) exclusive sums of new_lens: the
+ *              rows of each request among the packed new rows
+ *   counts [2] int32                  (written) new positions, pages wanted
+ * A call changes neither lengths nor free_pages: the caller moves on by
+ * counts[1] pages and adds new_lens to cached_lens.  A negative length acts as 0.
+ */
+la_status la_page_map(const int* cached_lens, const int* new_lens, int R, const int* free_pages,
+                      int num_free, int page_size, int num_pages, int* block_table, int max_pages,
+                      int* slot_map, int max_tokens, int* seq_starts, int* counts, void* stream);
+
+/*
+ * Rows of keys and values into the paged cache.
+ *   k, v [T][Hkv][D] dtype (read);  slot_map [T] int32 (read), -1: the row is skipped
+ *   K_pages, V_pages [num_pages][Hkv][page_size][D] dtype (the rows' slots written)
+ * D in {32, 64, 128}.  A slot that appears twice holds parts of either row.
+ */
+la_status la_paged_append(const void* k, const void* v, void* K_pages, void* V_pages,
+                          const int* slot_map, int T, int Hkv, int D, int num_pages, int page_size,
+                          la_dtype dtype, void* stream);
+
+/*
+ * One decode step of softmax attention over the paged cache: the step's k, v
+ * are appended at position cached_lens[r] of every request (as in
+ * la_softmax_decode_step, "Transformer与RNN的深层联结" section 2), then
+ *   out = softmax(scale q K^T) V over the request's last `window` positions
+ * (all of them if window is 0).  Query head h reads key head h / (Hq / Hkv).
+ *   q [R][Hq][D]; k, v [R][Hkv][D] dtype, nullable together   (read)
+ *         NULL: nothing is appended and the cached positions alone are attended
+ *   K_pages, V_pages [num_pages][Hkv][page_size][D] dtype     (read; the new row written)
+ *   block_table [R][max_pages] int32, cached_lens [R] int32   (read)
+ *         a negative length marks a row without a request: nothing of it is read
+ *         or written
+ *   out [R][Hq][D] fp32                                       (written)
+ *   lse [R][Hq] fp32, nullable                                (written) log of the
+ *         sum of e^(scale q k); joins outputs over parts of a context
+ *   scale 0 means 1 / sqrt(D)
+ * A request without a position has out 0 and lse -infinity.  Positions whose
+ * page is out of range are left out.  D in {32, 64, 128}, Hq a multiple of Hkv.
+ * No page may be held by two requests that append to it.
+ */
+la_status la_paged_decode_step(const void* q, const void* k, const void* v, void* K_pages,
+                               void* V_pages, const int* block_table, const int* cached_lens, float* out,
+                               float* lse, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
+                               int max_pages, int window, float scale, la_dtype dtype, void* stream);
+
+/*
  * la_forward_noncausal with no device allocation.  The paper has no
  * counterpart: this is a service for callers that may not allocate device
  * memory inside an op -- a host framework that plans all device memory in
@@ -314,7 +445,8 @@ la_status la_debug_withhold_publication(int unit, unsigned spin_limit);
 
 /* Synchronises `stream`, then reads and clears the current device's error
  * word set by bounded device-side waits.  LA_ERR_TIMEOUT if one gave up since
- * the last check, LA_ERR_CUDA if the stream reported an error, else LA_OK. */
+ * the last check, LA_ERR_BAD_INDEX if only an index in device memory was out of
+ * range (the paged cache's calls), LA_ERR_CUDA if the stream reported an error, else LA_OK. */
 la_status la_check_device_status(void* stream);
 
 /* Launches one block whose two bounded device waits cannot be met -- an

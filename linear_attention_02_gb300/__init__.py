@@ -8,6 +8,8 @@ current CUDA stream; every step of the computation runs in liblinattn.so.
     la_backward_causal(Q, K, V, dOut, ...)
     la_forward_noncausal(Q, K, V, ...)   phi(Q)(phi(K)^T V) / phi(Q) sum phi(K)
     la_decode_step(q, k, v, S, Z, ...)   S += phi(k)v^T, Z += phi(k); read with q
+    la_forward_gated_scan(A, X, ...)     h_t = a_t h_{t-1} + x_t per channel; its backward and step
+    la_page_map, la_paged_append, la_paged_decode_step   softmax attention over a paged KV cache
 
 Shapes: Q, K [B,H,N,D]; V [B,H,N,M]; S [B,H,D,M] fp32; Z [B,H,D] fp32.
 """
@@ -355,6 +357,212 @@ def la_softmax_decode_step(q, k, v, K_cache, V_cache, T, out=None, stream=None):
                                            int(T), T_max, _ptr(out), B, H, D, M, _dtype(q),
                                            _stream_handle(stream)))
     return out
+
+
+_FORMS = {"decay": _native.LA_GATE_DECAY, "logit": _native.LA_GATE_LOGIT}
+
+
+def _shaped(t, name, shape, dtype, dev):
+    _need(t, name, dtype, dev)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _scan_args(A, X, form, seq_starts):
+    """(B, N, C, sequences, num_seqs, form code) of a gated scan call, its inputs checked."""
+    if form not in _FORMS:
+        raise ValueError(f"form must be one of {sorted(_FORMS)}, got {form!r}")
+    if not isinstance(A, torch.Tensor) or A.dim() != 3:
+        raise ValueError("A and X must be [B,N,C]")
+    B, N, C = A.shape
+    _need(A, "A", A.dtype)
+    _shaped(X, "X", (B, N, C), A.dtype, A.device)
+    if seq_starts is None:
+        return B, N, C, B, 0, _FORMS[form]
+    _need(seq_starts, "seq_starts", torch.int32, A.device)
+    if seq_starts.dim() != 1 or seq_starts.numel() < 1:
+        raise ValueError("seq_starts must be [num_seqs + 1]")
+    if B != 1:
+        raise ValueError(f"packed sequences need B == 1, got {B}")
+    return B, N, C, seq_starts.numel() - 1, seq_starts.numel() - 1, _FORMS[form]
+
+
+def la_gated_scan_ckpt_floats(B, N, C):
+    """fp32 words of the gated scan's checkpoints (la_forward_gated_scan(ckpt=...))."""
+    return int(_lib.la_gated_scan_ckpt_floats(B, N, C))
+
+
+def _check_scan_ckpt(c, name, B, N, C, dev):
+    if c is None:
+        return
+    _need(c, name, torch.float32, dev)
+    if c.numel() != la_gated_scan_ckpt_floats(B, N, C):
+        raise ValueError(f"{name} must hold la_gated_scan_ckpt_floats(...) = "
+                         f"{la_gated_scan_ckpt_floats(B, N, C)} floats, got {c.numel()}")
+
+
+def la_forward_gated_scan(A, X, form="decay", out=None, h_init=None, return_state=False, ckpt=None,
+                          seq_starts=None, stream=None):
+    """Gated recurrence over rows [B,N,C]: h_t = a_t h_{t-1} + x_t ("decay"), or with
+    s_t = sigmoid(a_t): h_t = s_t h_{t-1} + (1 - s_t) x_t ("logit").
+
+    seq_starts: optional int32 [S+1] cutting the rows of a B = 1 call into packed
+    sequences; h_init, and the final state with return_state, are then [S,C] (else [B,C]),
+    fp32.  ckpt: optional fp32 tensor of la_gated_scan_ckpt_floats(B, N, C) elements that
+    receives states for la_backward_gated_scan(Ckpt=...).  Returns Out, or (Out, h_final)."""
+    B, N, C, S, num, code = _scan_args(A, X, form, seq_starts)
+    dev = A.device
+    if out is None:
+        out = torch.empty_like(A)
+    _shaped(out, "out", (B, N, C), A.dtype, dev)
+    if h_init is not None:
+        _shaped(h_init, "h_init", (S, C), torch.float32, dev)
+    _check_scan_ckpt(ckpt, "ckpt", B, N, C, dev)
+    h_f = torch.empty((S, C), dtype=torch.float32, device=dev) if return_state else None
+    with torch.cuda.device(dev):
+        _check(_lib.la_forward_gated_scan(_ptr(A), _ptr(X), _ptr(out), B, N, C, _dtype(A), code,
+                                          _ptr(seq_starts), num, _ptr(h_init), _ptr(h_f), _ptr(ckpt),
+                                          _stream_handle(stream)))
+    return (out, h_f) if return_state else out
+
+
+def la_backward_gated_scan(A, X, dOut, form="decay", h_init=None, dh_final=None, return_dh_init=False,
+                           Ckpt=None, dA=None, dX=None, seq_starts=None, stream=None):
+    """Backward of la_forward_gated_scan; returns (dA, dX) or (dA, dX, dh_init).
+
+    dh_final: optional gradient at the final state; Ckpt: the forward's checkpoints
+    (computed by the call when absent)."""
+    B, N, C, S, num, code = _scan_args(A, X, form, seq_starts)
+    dev = A.device
+    _shaped(dOut, "dOut", (B, N, C), A.dtype, dev)
+    dA = torch.empty_like(A) if dA is None else dA
+    dX = torch.empty_like(X) if dX is None else dX
+    _shaped(dA, "dA", (B, N, C), A.dtype, dev)
+    _shaped(dX, "dX", (B, N, C), A.dtype, dev)
+    for t, n in ((h_init, "h_init"), (dh_final, "dh_final")):
+        if t is not None:
+            _shaped(t, n, (S, C), torch.float32, dev)
+    _check_scan_ckpt(Ckpt, "Ckpt", B, N, C, dev)
+    dh = torch.empty((S, C), dtype=torch.float32, device=dev) if return_dh_init else None
+    with torch.cuda.device(dev):
+        _check(_lib.la_backward_gated_scan(_ptr(A), _ptr(X), _ptr(dOut), _ptr(dA), _ptr(dX), B, N, C,
+                                           _dtype(A), code, _ptr(seq_starts), num, _ptr(h_init),
+                                           _ptr(dh_final), _ptr(dh), _ptr(Ckpt), _stream_handle(stream)))
+    return (dA, dX, dh) if return_dh_init else (dA, dX)
+
+
+def la_gated_scan_decode_step(a, x, h, form="decay", out=None, stream=None):
+    """One token of the gated recurrence: updates h [B,C] fp32 in place, returns out [B,C]."""
+    if form not in _FORMS:
+        raise ValueError(f"form must be one of {sorted(_FORMS)}, got {form!r}")
+    if not isinstance(a, torch.Tensor) or a.dim() != 2:
+        raise ValueError("a and x must be [B,C]")
+    B, C = a.shape
+    dev = a.device
+    _need(a, "a", a.dtype)
+    _shaped(x, "x", (B, C), a.dtype, dev)
+    _shaped(h, "h", (B, C), torch.float32, dev)
+    if out is None:
+        out = torch.empty_like(a)
+    _shaped(out, "out", (B, C), a.dtype, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.la_gated_scan_decode_step(_ptr(a), _ptr(x), _ptr(h), _ptr(out), B, C, _dtype(a),
+                                              _FORMS[form], _stream_handle(stream)))
+    return out
+
+
+def la_page_map(cached_lens, new_lens, free_pages, block_table, page_size, num_pages, slot_map,
+                seq_starts=None, counts=None, stream=None):
+    """Block table and slot map of a step from request lengths (all int32, on the GPU).
+
+    Pages that the new positions open are taken from free_pages in the order of the requests
+    and written into block_table [R,W]; slot_map [max_tokens] receives the new positions'
+    slots (-1 behind the last), seq_starts [R+1] their row ranges, counts [2] the new
+    positions and the pages wanted.  Returns (slot_map, seq_starts, counts)."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [R, max_pages]")
+    R, W = block_table.shape
+    dev = block_table.device
+    i32 = torch.int32
+    _need(block_table, "block_table", i32)
+    _shaped(cached_lens, "cached_lens", (R,), i32, dev)
+    _shaped(new_lens, "new_lens", (R,), i32, dev)
+    for t, n in ((free_pages, "free_pages"), (slot_map, "slot_map")):
+        _need(t, n, i32, dev)
+        if t.dim() != 1:
+            raise ValueError(f"{n} must have one dimension")
+    seq_starts = torch.empty(R + 1, dtype=i32, device=dev) if seq_starts is None else seq_starts
+    counts = torch.empty(2, dtype=i32, device=dev) if counts is None else counts
+    _shaped(seq_starts, "seq_starts", (R + 1,), i32, dev)
+    _shaped(counts, "counts", (2,), i32, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.la_page_map(_ptr(cached_lens), _ptr(new_lens), R, _ptr(free_pages),
+                                free_pages.numel(), int(page_size), int(num_pages), _ptr(block_table), W,
+                                _ptr(slot_map), slot_map.numel(), _ptr(seq_starts), _ptr(counts),
+                                _stream_handle(stream)))
+    return slot_map, seq_starts, counts
+
+
+def _pools(K_pages, V_pages):
+    if not isinstance(K_pages, torch.Tensor) or K_pages.dim() != 4:
+        raise ValueError("K_pages and V_pages must be [num_pages, Hkv, page_size, D]")
+    _need(K_pages, "K_pages", K_pages.dtype)
+    _shaped(V_pages, "V_pages", K_pages.shape, K_pages.dtype, K_pages.device)
+    return K_pages.shape
+
+
+def la_paged_append(k, v, K_pages, V_pages, slot_map, stream=None):
+    """Writes rows k, v [T,Hkv,D] into the slots slot_map [T] (int32; -1 skips a row) of the
+    pools K_pages, V_pages [num_pages,Hkv,page_size,D]."""
+    P, Hkv, page, D = _pools(K_pages, V_pages)
+    dev, dt = K_pages.device, K_pages.dtype
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k and v must be [T, Hkv, D]")
+    T = k.shape[0]
+    _shaped(k, "k", (T, Hkv, D), dt, dev)
+    _shaped(v, "v", (T, Hkv, D), dt, dev)
+    _shaped(slot_map, "slot_map", (T,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.la_paged_append(_ptr(k), _ptr(v), _ptr(K_pages), _ptr(V_pages), _ptr(slot_map), T, Hkv,
+                                    D, P, page, _dtype(K_pages), _stream_handle(stream)))
+
+
+def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, window=0, scale=None,
+                         out=None, return_lse=False, stream=None):
+    """Softmax attention decode step over a paged KV cache, one request per row.
+
+    Appends k, v [R,Hkv,D] at position cached_lens[r] of each request (None, None: appends
+    nothing) and returns out [R,Hq,D] fp32 = softmax(scale q K^T) V over the request's last
+    `window` positions (0: all), with return_lse also the log of the sum [R,Hq] fp32.  Rows with a
+    negative length are left as they are.  scale None: 1 / sqrt(D)."""
+    P, Hkv, page, D = _pools(K_pages, V_pages)
+    dev, dt = K_pages.device, K_pages.dtype
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [R, Hq, D]")
+    R, Hq = q.shape[:2]
+    _shaped(q, "q", (R, Hq, D), dt, dev)
+    if (k is None) != (v is None):
+        raise ValueError("give both k and v, or neither")
+    if k is not None:
+        _shaped(k, "k", (R, Hkv, D), dt, dev)
+        _shaped(v, "v", (R, Hkv, D), dt, dev)
+    _need(block_table, "block_table", torch.int32, dev)
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError(f"block_table must be [R, max_pages] with R = {R}")
+    _shaped(cached_lens, "cached_lens", (R,), torch.int32, dev)
+    if scale is not None and float(scale) == 0.0:
+        raise ValueError("scale must not be 0")
+    if out is None:
+        out = torch.empty((R, Hq, D), dtype=torch.float32, device=dev)
+    _shaped(out, "out", (R, Hq, D), torch.float32, dev)
+    lse = torch.empty((R, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    with torch.cuda.device(dev):
+        _check(_lib.la_paged_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(K_pages), _ptr(V_pages),
+                                         _ptr(block_table), _ptr(cached_lens), _ptr(out), _ptr(lse), R, Hq,
+                                         Hkv, D, P, page, block_table.shape[1], int(window),
+                                         0.0 if scale is None else float(scale), _dtype(K_pages),
+                                         _stream_handle(stream)))
+    return (out, lse) if return_lse else out
 
 
 def la_check_device_status(stream=None):

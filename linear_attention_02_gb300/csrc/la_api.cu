@@ -6,6 +6,7 @@
 
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstdarg>
 #include <cstdio>
@@ -127,6 +128,66 @@ la_status check_optional(const char* fn, const void* p, const char* name) {
 
 la_status finish(cudaError_t e, const char* fn) {
     if (e != cudaSuccess) return cuda_fail(e, fn);
+    return LA_OK;
+}
+
+// Checks a list of required device pointers against an alignment in bytes.
+la_status check_ptrs(const char* fn, const void* const* ptrs, const char* const* names, int n,
+                     unsigned align) {
+    for (int i = 0; i < n; ++i) {
+        if (!ptrs[i]) return fail(LA_ERR_INVALID_ARG, "%s: %s is NULL", fn, names[i]);
+        if (reinterpret_cast<uintptr_t>(ptrs[i]) & (align - 1))
+            return fail(LA_ERR_INVALID_ARG, "%s: %s is not %u-byte aligned", fn, names[i], align);
+    }
+    return LA_OK;
+}
+
+// Sizes, dtype and packed sequences of a gated scan call.
+la_status check_scan(const char* fn, int B, int N, int C, la_dtype dt, la_gate_form form,
+                     const int* starts, int num_seqs) {
+    if (B < 0 || N < 0 || C < 0 || num_seqs < 0)
+        return fail(LA_ERR_INVALID_ARG, "%s: negative size B=%d N=%d C=%d num_seqs=%d", fn, B, N, C,
+                    num_seqs);
+    if (dt != LA_DTYPE_F32 && dt != LA_DTYPE_BF16)
+        return fail(LA_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dt);
+    if (form != LA_GATE_DECAY && form != LA_GATE_LOGIT)
+        return fail(LA_ERR_UNSUPPORTED, "%s: unknown gate form %d", fn, (int)form);
+    if (starts && B != 1)
+        return fail(LA_ERR_INVALID_ARG, "%s: packed sequences need B == 1, got %d", fn, B);
+    if (!starts && num_seqs != 0)
+        return fail(LA_ERR_INVALID_ARG, "%s: num_seqs=%d without seq_starts", fn, num_seqs);
+    if (reinterpret_cast<uintptr_t>(starts) & 3u)
+        return fail(LA_ERR_INVALID_ARG, "%s: seq_starts is not 4-byte aligned", fn);
+    const unsigned long long rows = (unsigned long long)B * N;
+    if (rows >= (1ull << 40) || (C && rows * C >= (1ull << 40)) ||
+        (unsigned long long)(starts ? num_seqs : B) * C >= (1ull << 40))
+        return fail(LA_ERR_INVALID_ARG, "%s: tensor too large", fn);
+    return LA_OK;
+}
+
+// to = from (or zeros): the state of sequences without a row.
+cudaError_t copy_state(cudaStream_t st, float* to, const float* from, size_t words) {
+    if (!to || words == 0) return cudaSuccess;
+    return from ? cudaMemcpyAsync(to, from, words * sizeof(float), cudaMemcpyDeviceToDevice, st)
+                : cudaMemsetAsync(to, 0, words * sizeof(float), st);
+}
+
+// log2 of a supported page size, or -1.
+int page_log2(int page_size) {
+    for (int b = 0; b <= 10; ++b)
+        if (page_size == 1 << b) return b;
+    return -1;
+}
+
+// Page size and pool size of a paged cache call.
+la_status check_pages(const char* fn, int num_pages, int page_size, int* log2p) {
+    *log2p = page_log2(page_size);
+    if (*log2p < 0)
+        return fail(LA_ERR_UNSUPPORTED, "%s: page_size=%d, supported are powers of two up to 1024", fn,
+                    page_size);
+    if (num_pages < 0 || (unsigned long long)num_pages * page_size >= (1ull << 31))
+        return fail(LA_ERR_INVALID_ARG, "%s: num_pages=%d of %d positions: negative, or 2^31 slots or more",
+                    fn, num_pages, page_size);
     return LA_OK;
 }
 
@@ -571,6 +632,204 @@ la_status la_softmax_decode_step(const void* q, const void* k, const void* v, vo
     return finish(e, fn);
 }
 
+size_t la_gated_scan_ckpt_floats(int B, int N, int C) {
+    if (B <= 0 || N <= 0 || C <= 0) return 0;
+    return (size_t)B * (((size_t)N + plan::kScanTile - 1) / plan::kScanTile) * (size_t)C;
+}
+
+la_status la_forward_gated_scan(const void* A, const void* X, void* Out, int B, int N, int C,
+                                la_dtype dtype, la_gate_form form, const int* seq_starts, int num_seqs,
+                                const float* h_init, float* h_final, float* Ckpt, void* stream) {
+    static const char* fn = "la_forward_gated_scan";
+    la_status s = check_scan(fn, B, N, C, dtype, form, seq_starts, num_seqs);
+    if (s != LA_OK) return s;
+    if ((s = check_optional(fn, h_init, "h_init")) || (s = check_optional(fn, h_final, "h_final")) ||
+        (s = check_optional(fn, Ckpt, "Ckpt")))
+        return s;
+    const size_t states = (size_t)(seq_starts ? num_seqs : B) * C;
+    const bool empty = (size_t)B * N * C == 0 || (seq_starts && num_seqs == 0);
+    if (empty && (!h_final || states == 0)) return LA_OK;
+    if (!empty) {
+        const void* p[] = {A, X, Out};
+        const char* nm[] = {"A", "X", "Out"};
+        if ((s = check_ptrs(fn, p, nm, 3, 16)) != LA_OK) return s;
+    }
+    LaunchCtx ctx;
+    if ((s = get_ctx((cudaStream_t)stream, &ctx)) != LA_OK) return s;
+    if (empty) return finish(copy_state(ctx.stream, h_final, h_init, states), fn);
+    const ScanShape sh = {B, N, C, form == LA_GATE_LOGIT, seq_starts, num_seqs};
+    using bf = __nv_bfloat16;
+    return finish(dtype == LA_DTYPE_F32
+                      ? gated_scan_forward<float>(ctx, (const float*)A, (const float*)X, (float*)Out, sh,
+                                                  h_init, h_final, Ckpt)
+                      : gated_scan_forward<bf>(ctx, (const bf*)A, (const bf*)X, (bf*)Out, sh, h_init,
+                                               h_final, Ckpt),
+                  fn);
+}
+
+la_status la_backward_gated_scan(const void* A, const void* X, const void* dOut, void* dA, void* dX,
+                                 int B, int N, int C, la_dtype dtype, la_gate_form form,
+                                 const int* seq_starts, int num_seqs, const float* h_init,
+                                 const float* dh_final, float* dh_init, const float* Ckpt,
+                                 void* stream) {
+    static const char* fn = "la_backward_gated_scan";
+    la_status s = check_scan(fn, B, N, C, dtype, form, seq_starts, num_seqs);
+    if (s != LA_OK) return s;
+    if ((s = check_optional(fn, h_init, "h_init")) || (s = check_optional(fn, dh_final, "dh_final")) ||
+        (s = check_optional(fn, dh_init, "dh_init")) || (s = check_optional(fn, Ckpt, "Ckpt")))
+        return s;
+    const size_t states = (size_t)(seq_starts ? num_seqs : B) * C;
+    const bool empty = (size_t)B * N * C == 0 || (seq_starts && num_seqs == 0);
+    if (empty && (!dh_init || states == 0)) return LA_OK;
+    if (!empty) {
+        const void* p[] = {A, X, dOut, dA, dX};
+        const char* nm[] = {"A", "X", "dOut", "dA", "dX"};
+        if ((s = check_ptrs(fn, p, nm, 5, 16)) != LA_OK) return s;
+    }
+    LaunchCtx ctx;
+    if ((s = get_ctx((cudaStream_t)stream, &ctx)) != LA_OK) return s;
+    if (empty) return finish(copy_state(ctx.stream, dh_init, dh_final, states), fn);
+    const ScanShape sh = {B, N, C, form == LA_GATE_LOGIT, seq_starts, num_seqs};
+    using bf = __nv_bfloat16;
+    return finish(dtype == LA_DTYPE_F32
+                      ? gated_scan_backward<float>(ctx, (const float*)A, (const float*)X,
+                                                   (const float*)dOut, (float*)dA, (float*)dX, sh, h_init,
+                                                   dh_final, dh_init, Ckpt)
+                      : gated_scan_backward<bf>(ctx, (const bf*)A, (const bf*)X, (const bf*)dOut, (bf*)dA,
+                                                (bf*)dX, sh, h_init, dh_final, dh_init, Ckpt),
+                  fn);
+}
+
+la_status la_gated_scan_decode_step(const void* a, const void* x, float* h, void* out, int B, int C,
+                                    la_dtype dtype, la_gate_form form, void* stream) {
+    static const char* fn = "la_gated_scan_decode_step";
+    la_status s = check_scan(fn, B, 1, C, dtype, form, nullptr, 0);
+    if (s != LA_OK) return s;
+    const int64_t n = (int64_t)B * C;
+    if (n == 0) return LA_OK;
+    const void* p[] = {a, x, h, out};
+    const char* nm[] = {"a", "x", "h", "out"};
+    if ((s = check_ptrs(fn, p, nm, 4, 16)) != LA_OK) return s;
+    LaunchCtx ctx;
+    if ((s = get_ctx((cudaStream_t)stream, &ctx)) != LA_OK) return s;
+    using bf = __nv_bfloat16;
+    const bool lg = form == LA_GATE_LOGIT;
+    return finish(dtype == LA_DTYPE_F32
+                      ? gated_scan_step<float>(ctx, (const float*)a, (const float*)x, h, (float*)out, n, lg)
+                      : gated_scan_step<bf>(ctx, (const bf*)a, (const bf*)x, h, (bf*)out, n, lg),
+                  fn);
+}
+
+la_status la_page_map(const int* cached_lens, const int* new_lens, int R, const int* free_pages,
+                      int num_free, int page_size, int num_pages, int* block_table, int max_pages,
+                      int* slot_map, int max_tokens, int* seq_starts, int* counts, void* stream) {
+    static const char* fn = "la_page_map";
+    int log2p = 0;
+    la_status s = check_pages(fn, num_pages, page_size, &log2p);
+    if (s != LA_OK) return s;
+    if (R < 0 || num_free < 0 || max_pages < 0 || max_tokens < 0)
+        return fail(LA_ERR_INVALID_ARG, "%s: negative size R=%d num_free=%d max_pages=%d max_tokens=%d", fn,
+                    R, num_free, max_pages, max_tokens);
+    if ((unsigned long long)max_pages * page_size >= (1ull << 31))
+        return fail(LA_ERR_INVALID_ARG, "%s: max_pages=%d of %d positions: 2^31 positions or more", fn,
+                    max_pages, page_size);
+    const void* p[] = {seq_starts, counts, cached_lens, new_lens, block_table, free_pages, slot_map};
+    const char* nm[] = {"seq_starts", "counts", "cached_lens", "new_lens", "block_table", "free_pages",
+                        "slot_map"};
+    const bool need[] = {true, true, R > 0, R > 0, R > 0 && max_pages > 0, num_free > 0, max_tokens > 0};
+    for (int i = 0; i < 7; ++i)
+        if (need[i] && (s = check_ptrs(fn, p + i, nm + i, 1, 4)) != LA_OK) return s;
+    LaunchCtx ctx;
+    if ((s = get_ctx((cudaStream_t)stream, &ctx)) != LA_OK) return s;
+    return finish(page_map(ctx, cached_lens, new_lens, R, free_pages, num_free, log2p, num_pages,
+                           block_table, max_pages, slot_map, max_tokens, seq_starts, counts),
+                  fn);
+}
+
+la_status la_paged_append(const void* k, const void* v, void* K_pages, void* V_pages,
+                          const int* slot_map, int T, int Hkv, int D, int num_pages, int page_size,
+                          la_dtype dtype, void* stream) {
+    static const char* fn = "la_paged_append";
+    int log2p = 0;
+    la_status s = check_pages(fn, num_pages, page_size, &log2p);
+    if (s != LA_OK) return s;
+    if (T < 0 || Hkv < 0) return fail(LA_ERR_INVALID_ARG, "%s: negative size T=%d Hkv=%d", fn, T, Hkv);
+    if (dtype != LA_DTYPE_F32 && dtype != LA_DTYPE_BF16)
+        return fail(LA_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dtype);
+    if (!head_ok(D))
+        return fail(LA_ERR_UNSUPPORTED, "%s: D=%d, supported head sizes are 32, 64, 128", fn, D);
+    if ((unsigned long long)T * Hkv * D >= (1ull << 40) ||
+        (unsigned long long)num_pages * page_size * (Hkv ? Hkv : 1) >= (1ull << 40) / D)
+        return fail(LA_ERR_INVALID_ARG, "%s: tensor too large", fn);
+    if (T == 0 || Hkv == 0) return LA_OK;
+    const void* p[] = {k, v, K_pages, V_pages};
+    const char* nm[] = {"k", "v", "K_pages", "V_pages"};
+    if ((s = check_ptrs(fn, p, nm, num_pages ? 4 : 2, 16)) != LA_OK) return s;
+    const void* sp[] = {slot_map};
+    const char* sn[] = {"slot_map"};
+    if ((s = check_ptrs(fn, sp, sn, 1, 4)) != LA_OK) return s;
+    LaunchCtx ctx;
+    if ((s = get_ctx((cudaStream_t)stream, &ctx)) != LA_OK) return s;
+    return finish(paged_append(ctx, k, v, K_pages, V_pages, slot_map, T, Hkv,
+                               D * (dtype == LA_DTYPE_F32 ? 4 : 2), log2p, num_pages),
+                  fn);
+}
+
+la_status la_paged_decode_step(const void* q, const void* k, const void* v, void* K_pages,
+                               void* V_pages, const int* block_table, const int* cached_lens, float* out,
+                               float* lse, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
+                               int max_pages, int window, float scale, la_dtype dtype, void* stream) {
+    static const char* fn = "la_paged_decode_step";
+    int log2p = 0;
+    la_status s = check_pages(fn, num_pages, page_size, &log2p);
+    if (s != LA_OK) return s;
+    if (R < 0 || Hq < 0 || Hkv < 0 || max_pages < 0 || window < 0)
+        return fail(LA_ERR_INVALID_ARG, "%s: negative size R=%d Hq=%d Hkv=%d max_pages=%d window=%d", fn, R,
+                    Hq, Hkv, max_pages, window);
+    if (dtype != LA_DTYPE_F32 && dtype != LA_DTYPE_BF16)
+        return fail(LA_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dtype);
+    if (!head_ok(D))
+        return fail(LA_ERR_UNSUPPORTED, "%s: D=%d, supported head sizes are 32, 64, 128", fn, D);
+    if (Hq && (Hkv == 0 || Hq % Hkv))
+        return fail(LA_ERR_INVALID_ARG, "%s: Hq=%d query heads over Hkv=%d key heads: not a multiple", fn,
+                    Hq, Hkv);
+    if (!std::isfinite(scale)) return fail(LA_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+    if ((k == nullptr) != (v == nullptr))
+        return fail(LA_ERR_INVALID_ARG, "%s: k and v must both be given or both NULL", fn);
+    if ((unsigned long long)max_pages * page_size >= (1ull << 31) - 1)
+        return fail(LA_ERR_INVALID_ARG, "%s: max_pages=%d of %d positions: 2^31 - 1 positions or more", fn,
+                    max_pages, page_size);
+    if ((unsigned long long)R * Hq * D >= (1ull << 31) ||
+        (unsigned long long)num_pages * page_size * (Hkv ? Hkv : 1) >= (1ull << 40) / D)
+        return fail(LA_ERR_INVALID_ARG, "%s: tensor too large", fn);
+    if (R == 0 || Hq == 0) return LA_OK;
+    const void* p[] = {q, out, K_pages, V_pages};
+    const char* nm[] = {"q", "out", "K_pages", "V_pages"};
+    if ((s = check_ptrs(fn, p, nm, num_pages ? 4 : 2, 16)) != LA_OK) return s;
+    if ((s = check_optional(fn, k, "k")) || (s = check_optional(fn, v, "v"))) return s;
+    const void* ip[] = {cached_lens, block_table};
+    const char* in[] = {"cached_lens", "block_table"};
+    if ((s = check_ptrs(fn, ip, in, max_pages ? 2 : 1, 4)) != LA_OK) return s;
+    if (reinterpret_cast<uintptr_t>(lse) & 3u)
+        return fail(LA_ERR_INVALID_ARG, "%s: lse is not 4-byte aligned", fn);
+    LaunchCtx ctx;
+    if ((s = get_ctx((cudaStream_t)stream, &ctx)) != LA_OK) return s;
+    const PagedShape sh = {R, Hq, Hkv, num_pages, log2p, max_pages, window,
+                           scale == 0.f ? 1.f / sqrtf((float)D) : scale};
+    cudaError_t e = cudaErrorInvalidValue;
+#define LA_PD_CASE(Ty, d)                                                                              \
+    if (D == d)                                                                                        \
+        e = paged_decode_step<Ty, d>(ctx, (const Ty*)q, (const Ty*)k, (const Ty*)v, (Ty*)K_pages,      \
+                                     (Ty*)V_pages, block_table, cached_lens, out, lse, sh);
+    if (dtype == LA_DTYPE_F32) {
+        LA_PD_CASE(float, 32) else LA_PD_CASE(float, 64) else LA_PD_CASE(float, 128)
+    } else {
+        LA_PD_CASE(__nv_bfloat16, 32) else LA_PD_CASE(__nv_bfloat16, 64) else LA_PD_CASE(__nv_bfloat16, 128)
+    }
+#undef LA_PD_CASE
+    return finish(e, fn);
+}
+
 la_status la_selftest_expired_waits(void* stream) {
     LaunchCtx ctx;
     la_status s = get_ctx((cudaStream_t)stream, &ctx);
@@ -600,6 +859,9 @@ la_status la_check_device_status(void* stream) {
         const unsigned int zero = 0;
         if ((e = cudaMemcpy(ctx.status_word, &zero, sizeof(zero), cudaMemcpyHostToDevice)))
             return cuda_fail(e, "la_check_device_status");
+        if (!(word & ~kStatusBadIndex))
+            return fail(LA_ERR_BAD_INDEX, "a length, page or slot read from device memory was out of range "
+                        "(code 0x%x)", word);
         return fail(LA_ERR_TIMEOUT, "a bounded device wait gave up (code 0x%x)", word);
     }
     return LA_OK;
@@ -612,6 +874,7 @@ const char* la_status_string(la_status status) {
         case LA_ERR_UNSUPPORTED: return "LA_ERR_UNSUPPORTED";
         case LA_ERR_CUDA: return "LA_ERR_CUDA";
         case LA_ERR_TIMEOUT: return "LA_ERR_TIMEOUT";
+        case LA_ERR_BAD_INDEX: return "LA_ERR_BAD_INDEX";
     }
     return "LA_ERR_UNKNOWN";
 }

@@ -26,6 +26,10 @@ void note_launch(int n = 1);
 // Sets the text returned by la_last_error_message() on this host thread.
 void set_error_message(const char* msg);
 
+// Bit of the device error word: an index read from device memory (a request
+// length, a page number, a slot) was out of range and its access was skipped.
+constexpr unsigned kStatusBadIndex = 0x100u;
+
 // Optional checkpoints kept by the causal forward for the backward: the fp32
 // state [S | Z] (D*M + D words) of every head before every kCkptChunks-th chunk
 // of 128 tokens, laid out [BH][ceil(chunks / kCkptChunks)][D*M + D]; slot 0
@@ -125,6 +129,44 @@ cudaError_t poly2_forward(const LaunchCtx& c, const T* Q, const T* K, const T* V
 // The same on the tensor core for bf16 storage and M = 64 (D^2 = 1024 features).
 cudaError_t poly2_forward_tc(const LaunchCtx& c, const __nv_bfloat16* Q, const __nv_bfloat16* K,
                              const __nv_bfloat16* V, __nv_bfloat16* O, int BH, int N, bool causal);
+
+// Rows of a gated scan: [B][N][C], or with `starts` (device, [num_seqs + 1]) one
+// row axis (B = 1) cut into packed sequences.
+struct ScanShape {
+    int B, N, C;
+    bool logit;  // gates are logits (decay sigmoid(a), input scaled by 1 - decay)
+    const int* starts;
+    int num_seqs;
+};
+template <typename T>
+cudaError_t gated_scan_forward(const LaunchCtx& c, const T* A, const T* X, T* O, const ScanShape& s,
+                               const float* h_init, float* h_final, float* Ckpt);
+template <typename T>
+cudaError_t gated_scan_backward(const LaunchCtx& c, const T* A, const T* X, const T* G, T* dA, T* dX,
+                                const ScanShape& s, const float* h_init, const float* dh_final,
+                                float* dh_init, const float* Ckpt);
+template <typename T>
+cudaError_t gated_scan_step(const LaunchCtx& c, const T* a, const T* x, float* h, T* out, int64_t n,
+                            bool logit);
+
+// Block table and slot map from request lengths (page_size = 1 << log2p).
+cudaError_t page_map(const LaunchCtx& c, const int* cached, const int* fresh, int R,
+                     const int* free_pages, int num_free, int log2p, int num_pages, int* table,
+                     int max_pages, int* slots, int max_tokens, int* starts, int* counts);
+
+// Rows [T][Hkv][row_bytes] of keys and values into their slots of the pools.
+cudaError_t paged_append(const LaunchCtx& c, const void* k, const void* v, void* K, void* V,
+                         const int* slots, int T, int Hkv, int row_bytes, int log2p, int num_pages);
+
+// One decode step over the paged cache.
+struct PagedShape {
+    int R, Hq, Hkv, num_pages, log2p, max_pages, window;
+    float scale;
+};
+template <typename T, int D>
+cudaError_t paged_decode_step(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K, T* V,
+                              const int* table, const int* lens, float* out, float* lse,
+                              const PagedShape& s);
 
 template <typename T, int D, int M>
 cudaError_t decode_step(const LaunchCtx& c, const T* q, const T* k, const T* v, float* S,

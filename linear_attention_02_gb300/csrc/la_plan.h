@@ -117,6 +117,9 @@ inline size_t poly2_tc_scratch(int BH, int N) {
     return sizeof(float) * static_cast<size_t>(BH) * N * (64 + 16);
 }
 
+// Rows between two state checkpoints of the gated scan.
+constexpr int kScanTile = 256;
+
 // Tensor-core causal kernels: the chunks of all heads cut into equal ranges,
 // one per resident CTA (see tc_common.cuh, split_chunks).
 inline int tc_units(int BH, int chunks_per_head, int slots) {
