@@ -252,7 +252,7 @@ la_status la_softmax_decode_step(const void* q, const void* k, const void* v, vo
  *   h_final [sequences][C] fp32, nullable (written)  state after the last row
  *         (of an empty sequence: h_init, or 0)
  *   Ckpt  fp32, nullable (written) la_gated_scan_ckpt_floats(B, N, C) words: the
- *         running state before every 256th row, for the backward
+ *         running state at every 128th row, for the backward
  * Decays lie in [-1, 1]; the state is fp32 throughout.  A sequence's rows do
  * not depend on other sequences, whatever values those hold.  Out, h_final and
  * Ckpt may not alias inputs or each other.
@@ -262,7 +262,7 @@ la_status la_forward_gated_scan(const void* A, const void* X, void* Out, int B, 
                                 la_dtype dtype, la_gate_form form, const int* seq_starts, int num_seqs,
                                 const float* h_init, float* h_final, float* Ckpt, void* stream);
 
-/* Size in fp32 words of the gated scan's checkpoints: B * ceil(N / 256) * C, or
+/* Size in fp32 words of the gated scan's checkpoints: B * ceil(N / 128) * C, or
  * 0 for non-positive sizes.  Pure arithmetic; no device call. */
 size_t la_gated_scan_ckpt_floats(int B, int N, int C);
 

@@ -1,0 +1,697 @@
+// gated_scan.cuh -- the gated linear recurrence over token-major rows [B][N][C],
+// one decay per token and channel:
+//     decay form   h_t = a_t h_{t-1} + x_t
+//     logit form   h_t = s_t h_{t-1} + (1 - s_t) x_t,  s_t = sigmoid(a_t)
+// and its gradient (g_t the whole gradient at h_t; m_t = 1 or 1 - s_t):
+//     c_t = s_t (dOut_t + c_{t+1}),  g_t = dOut_t + c_{t+1},  dX_t = m_t g_t,
+//     dA_t = g_t h_{t-1}  or  s_t (1 - s_t) g_t (h_{t-1} - x_t).
+// A run of rows acts on the state that enters it as h -> A h + B, so runs
+// combine: (A1, B1) then (A2, B2) is (A1 A2, A2 B1 + B2); the gradient's carry c
+// runs through the rows backwards with the same A.
+//
+// The kernels are bound by memory: every element is read once and written once
+// (forward 2 streams in, 1 out; backward 3 in, 2 out).  A tile is 128 rows x 128
+// bytes of a row, worked by 128 threads; a thread owns 8 rows x 16 bytes, copied
+// by cp.async into shared memory slots of its own (no barrier between copy and
+// use), one tile ahead.  Per tile: each thread sums its 8 rows up to (A, B);
+// one thread per channel folds the 16 row groups, gets the state that enters the
+// tile from the tile before (below), and hands each row group its state; then
+// each thread runs its rows and writes them.
+//
+// Tiles of the same channels in time form a chain.  A tile publishes its end
+// state (flag 2), or first its (A, B) (flag 1) where the tile before is not done;
+// the next tile looks back over up to 32 flags at once to the nearest end state
+// and applies the (A, B) in between in order.  The result is the same whichever
+// it finds, since the end state of a tile is always fma(A, state before, B).
+// Tiles are numbered in time order and taken by an atomic ticket, so a tile only
+// waits for tiles that running blocks hold, each block working its own in
+// ascending order: the lowest unfinished one can always go on.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "la_common.cuh"
+#include "la_launch.h"
+#include "la_plan.h"
+#include "tc_common.cuh"
+
+namespace la {
+namespace scan {
+
+using tcf::ld_acquire;
+using tcf::st_release;
+
+constexpr int NT = 128;                 // threads
+constexpr int R = 8;                    // rows of a thread
+constexpr int LANES = 8;                // threads across a row: 128 bytes
+constexpr int RG = NT / LANES;          // row groups of a tile
+constexpr int TILE = RG * R;            // rows of a tile
+static_assert(TILE == plan::kScanTile, "checkpoints lie at tile borders");
+
+template <typename T>
+struct Geo {
+    static constexpr int VEC = 16 / static_cast<int>(sizeof(T));  // channels of a thread
+    static constexpr int CB = LANES * VEC;                        // channels of a tile
+};
+
+constexpr int kBegin = 1 << 30, kEnd = 1 << 29, kOwner = kEnd - 1;  // packed row info; kOwner: no sequence
+
+template <typename T>
+struct Args {
+    const T *A, *X, *G;
+    T *O, *dA, *dX;
+    int B, N, C, tiles, ncb;
+    unsigned total;             // B * tiles * ncb
+    const int* starts;          // packed sequences
+    int S;
+    const int* tile_first;      // [tiles + 1] first boundary at or after a tile's first row
+    const float* init;          // forward: h_init; backward: dh_final (state entering the chain)
+    float* fin;                 // forward: h_final; backward: dh_init
+    const float* h_init;        // backward: the forward's h_init
+    const float* states;        // backward: the forward's end state of each tile, [B][tiles][C]
+    float *incl, *aggA, *aggB;  // chain of this direction: end states and (A, B), [B][tiles][C]
+    unsigned* flags;            // [B][tiles][ncb][CB / 32]
+    unsigned* ticket;           // null: a single tile per chain, blocks take tiles by number
+    unsigned* status;
+};
+
+__device__ __forceinline__ void cp16(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp4(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(on ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// A thread's 16 bytes as fp32 values, and back (round to nearest even).
+__device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&x)[4]) {
+    x[0] = __uint_as_float(u.x);
+    x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z);
+    x[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                      __float_as_uint(x[3]));
+}
+
+// sigmoid(z) from e^-|z|, which does not overflow.  1 - s is taken as the fp32
+// difference wherever it is needed (exact for s >= 1/2), so that a constant
+// input stays a fixed point of the logit form.
+__device__ __forceinline__ float sigmoid(float z) {
+    const float e = tcf::ex2_approx(-1.4426950408889634f * fabsf(z));
+    const float r = __fdividef(1.f, 1.f + e);
+    return z >= 0.f ? r : e * r;
+}
+
+// A tile's place: batch row, time tile, channel block.
+struct Place {
+    int b, k, cb;
+};
+
+template <typename T, bool kRev>
+__device__ __forceinline__ Place place_of(const Args<T>& p, unsigned tile) {
+    const unsigned per = static_cast<unsigned>(p.B) * p.ncb;
+    const unsigned k = tile / per, rem = tile - k * per;
+    Place q;
+    q.b = static_cast<int>(rem / p.ncb);
+    q.cb = static_cast<int>(rem - q.b * p.ncb);
+    q.k = kRev ? p.tiles - 1 - static_cast<int>(k) : static_cast<int>(k);
+    return q;
+}
+
+// Copies a tile's streams into the thread's slots of a stage.  kVec: rows are
+// 16-byte aligned and a thread's channels are consecutive; otherwise the
+// channels lane, lane + 8, ... are copied one by one.
+template <typename T, bool kVec, int STREAMS>
+__device__ __forceinline__ void issue(const Args<T>& p, const Place& q, uint4* stage) {
+    constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
+    const int tid = threadIdx.x, lane = tid % LANES, rg = tid / LANES;
+    const T* src[3] = {p.A, p.X, p.G};
+#pragma unroll
+    for (int s = 0; s < STREAMS; ++s) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = q.k * TILE + rg * R + r;
+            const int64_t row = (static_cast<int64_t>(q.b) * p.N + t) * p.C;
+            uint4* slot = stage + (s * R + r) * NT + tid;
+            if constexpr (kVec) {
+                const int c = q.cb * CB + lane * VEC;
+                const bool on = t < p.N && c < p.C;
+                cp16(slot, on ? src[s] + row + c : src[s], on);
+            } else {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const int c = q.cb * CB + lane + LANES * v;
+                    const bool on = t < p.N && c < p.C;
+                    T* e = reinterpret_cast<T*>(slot) + v;
+                    if constexpr (sizeof(T) == 4) cp4(e, on ? src[s] + row + c : src[s], on);
+                    else *e = on ? src[s][row + c] : from_f<T>(0.f);
+                }
+            }
+        }
+    }
+    cp_commit();
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void store_row(T* dst, const Args<T>& p, const Place& q, int t,
+                                          const float (&y)[Geo<T>::VEC]) {
+    constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
+    const int lane = threadIdx.x % LANES;
+    const int64_t row = (static_cast<int64_t>(q.b) * p.N + t) * p.C;
+    if constexpr (kVec) {
+        const int c = q.cb * CB + lane * VEC;
+        if (c < p.C) *reinterpret_cast<uint4*>(dst + row + c) = pack(y);
+    } else {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const int c = q.cb * CB + lane + LANES * v;
+            if (c < p.C) dst[row + c] = from_f<T>(y[v]);
+        }
+    }
+}
+
+// A thread's channels of a [..][C] fp32 row (0 past C, or without a row).
+template <typename T, bool kVec>
+__device__ __forceinline__ void load_state(const float* row, const Args<T>& p, const Place& q,
+                                           float (&y)[Geo<T>::VEC]) {
+    const int lane = threadIdx.x % LANES;
+#pragma unroll
+    for (int v = 0; v < Geo<T>::VEC; ++v) {
+        const int c = q.cb * Geo<T>::CB + (kVec ? lane * Geo<T>::VEC + v : lane + LANES * v);
+        y[v] = row && c < p.C ? row[c] : 0.f;
+    }
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ void save_state(float* row, const Args<T>& p, const Place& q,
+                                           const float (&y)[Geo<T>::VEC]) {
+    const int lane = threadIdx.x % LANES;
+#pragma unroll
+    for (int v = 0; v < Geo<T>::VEC; ++v) {
+        const int c = q.cb * Geo<T>::CB + (kVec ? lane * Geo<T>::VEC + v : lane + LANES * v);
+        if (c < p.C) row[c] = y[v];
+    }
+}
+
+// Shared rows [RG][CB] of per-channel values.
+template <typename T, bool kVec>
+__device__ __forceinline__ void put(float* sm, const float (&y)[Geo<T>::VEC]) {
+    constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
+    float* row = sm + (threadIdx.x / LANES) * CB;
+    const int lane = threadIdx.x % LANES;
+    if constexpr (kVec) {
+#pragma unroll
+        for (int v = 0; v < VEC; v += 4)
+            *reinterpret_cast<float4*>(row + lane * VEC + v) = make_float4(y[v], y[v + 1], y[v + 2], y[v + 3]);
+    } else {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) row[lane + LANES * v] = y[v];
+    }
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ void get(const float* sm, float (&y)[Geo<T>::VEC]) {
+    constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
+    const float* row = sm + (threadIdx.x / LANES) * CB;
+    const int lane = threadIdx.x % LANES;
+    if constexpr (kVec) {
+#pragma unroll
+        for (int v = 0; v < VEC; v += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(row + lane * VEC + v);
+            y[v] = f.x, y[v + 1] = f.y, y[v + 2] = f.z, y[v + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) y[v] = row[lane + LANES * v];
+    }
+}
+
+// Packed sequences: info[row] = owner | kBegin | kEnd of a tile's rows, and each
+// row group's "a row begins" / "a row ends" bits.  An owner outside 0 .. S-1
+// becomes kOwner (a row of no sequence, which begins and ends itself).
+template <typename T>
+__device__ __forceinline__ void row_info(const Args<T>& p, int k, int* info, unsigned* grp) {
+    constexpr int LR = TILE / 32, PER = R / LR;  // rows of a lane, lanes of a row group
+    static_assert(TILE == 32 * LR && R == LR * PER && (PER == 1 || PER == 2), "lanes over rows");
+    const int tid = threadIdx.x, row0 = k * TILE;
+    for (int i = tid; i <= TILE; i += NT) info[i] = -1;
+    __syncthreads();
+    const int f0 = p.tile_first[k], f1 = p.tile_first[k + 1];
+    for (int i = f0 + tid; i <= min(f1, p.S); i += NT) {
+        const int r = min(max(p.starts[i], 0), p.N) - row0;
+        if (r >= 0 && r <= TILE) atomicMax(&info[r], i);  // of equal boundaries the last: the sequence with rows
+    }
+    __syncthreads();
+    if (tid < 32) {  // owners: running maximum over the rows
+        int m[LR + 1], run = f0 - 1, top = -1;
+#pragma unroll
+        for (int r = 0; r <= LR; ++r) m[r] = info[tid * LR + r];
+#pragma unroll
+        for (int r = 0; r < LR; ++r) top = max(top, m[r]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, top, o);
+            if (tid >= o) top = max(top, up);
+        }
+        const int up = __shfl_up_sync(0xffffffffu, top, 1);  // every lane has read its rows
+        if (tid) run = max(run, up);
+        unsigned g = 0;
+#pragma unroll
+        for (int r = 0; r < LR; ++r) {
+            const int t = row0 + tid * LR + r;
+            run = max(run, m[r]);
+            const bool none = run < 0 || run >= p.S || t >= p.N;
+            const bool b = none || m[r] >= 0, e = none || m[r + 1] >= 0 || t + 1 >= p.N;
+            info[tid * LR + r] = (none ? kOwner : run) | (b ? kBegin : 0) | (e ? kEnd : 0);
+            g |= (b ? 1u : 0u) | (e ? 2u : 0u);
+        }
+        if (PER == 2) g |= __shfl_xor_sync(0xffffffffu, g, 1);
+        if (tid % PER == 0) grp[tid / PER] = g;
+    }
+    __syncthreads();
+}
+
+// The state that enters chain tile `i` (numbered in the chain's direction) of
+// the warp's 32 channels: look back for the nearest published end state and
+// apply the published (A, B) after it in order.  Publishes this tile's own
+// (A, B) first if the tile before is not done (told: its end state is out
+// already).  All 32 lanes take part.
+template <typename T>
+__device__ float look_back(const Args<T>& p, const Place& q, int i, int c, bool on, float At, float Bt,
+                           int warp, bool told) {
+    constexpr int W = Geo<T>::CB / 32;
+    const int lane = threadIdx.x & 31;
+    const auto flag = [&](int j) {  // of chain tile j
+        return p.flags + ((static_cast<int64_t>(q.b) * p.tiles + j) * p.ncb + q.cb) * W + warp;
+    };
+    const auto at = [&](int j) { return (static_cast<int64_t>(q.b) * p.tiles + j) * p.C + c; };
+    int n = 32;
+    for (unsigned spin = 0;; ++spin) {
+        const int j = i - 1 - lane;
+        const unsigned f = j >= 0 ? ld_acquire(flag(j)) : 1u;
+        const unsigned done = __ballot_sync(0xffffffffu, f == 2u);
+        const unsigned none = __ballot_sync(0xffffffffu, f == 0u);
+        n = done ? __ffs(done) - 1 : 32;
+        if (n < 32 && (none & ((1u << n) - 1u)) == 0u) break;
+        if (!told) {
+            if (on) {
+                __stcg(p.aggA + at(i), At);
+                __stcg(p.aggB + at(i), Bt);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                __threadfence();
+                st_release(flag(i), 1u);
+            }
+            told = true;
+        } else if (spin > tcf::kSpinLimit) {  // never met unless the device is broken: report, go on
+            if (lane == 0) atomicOr(p.status, tcf::kErrLookback);
+            return 0.f;
+        } else if (spin > 64) {
+            __nanosleep(100);
+        }
+    }
+    __syncwarp();
+    if (!on) return 0.f;
+    float h = __ldcg(p.incl + at(i - 1 - n));
+#pragma unroll 4
+    for (int d = n - 1; d >= 0; --d) {
+        const float a = __ldcg(p.aggA + at(i - 1 - d)), b = __ldcg(p.aggB + at(i - 1 - d));
+        h = fmaf(a, h, b);
+    }
+    return h;
+}
+
+template <typename T>
+__device__ __forceinline__ void publish(const Args<T>& p, const Place& q, int i, int c, bool on, float h,
+                                        int warp) {
+    constexpr int W = Geo<T>::CB / 32;
+    if (on) __stcg(p.incl + (static_cast<int64_t>(q.b) * p.tiles + i) * p.C + c, h);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        __threadfence();
+        st_release(p.flags + ((static_cast<int64_t>(q.b) * p.tiles + i) * p.ncb + q.cb) * W + warp, 2u);
+    }
+}
+
+template <typename T, bool kPacked, int STREAMS>
+constexpr size_t smem_bytes() {
+    return static_cast<size_t>(2) * STREAMS * R * NT * 16 + sizeof(float) * STREAMS * RG * Geo<T>::CB +
+           (kPacked ? sizeof(int) * (TILE + 4 + RG) : 0) + 16;
+}
+
+// One channel's fold over the row groups: the tile's (A, B), and whether a row
+// group replaces the state (its "begin" bit, or for the backward pass "end").
+template <int CB, bool kPacked, bool kRev>
+__device__ __forceinline__ bool fold(const float* a, const float* b, const unsigned* grp, float& At,
+                                     float& Bt) {
+    At = 1.f, Bt = 0.f;
+    bool cut = false;
+#pragma unroll 8
+    for (int g0 = 0; g0 < RG; ++g0) {
+        const int g = kRev ? RG - 1 - g0 : g0;
+        const float A = a[g * CB], B = b[g * CB];
+        const bool x = kPacked && (grp[g] & (kRev ? 2u : 1u));
+        Bt = x ? B : fmaf(A, Bt, B);
+        At *= A;
+        cut |= x;
+    }
+    return cut;
+}
+
+template <typename T, bool kLogit, bool kPacked, bool kVec>
+__global__ void __launch_bounds__(NT, 3) scan_forward_kernel(const Args<T> p) {
+    constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
+    extern __shared__ __align__(16) uint8_t sm[];
+    uint4* stages = reinterpret_cast<uint4*>(sm);
+    float* sa = reinterpret_cast<float*>(stages + 2 * 2 * R * NT);
+    float* sb = sa + RG * CB;
+    int* info = reinterpret_cast<int*>(sb + RG * CB);
+    unsigned* grp = reinterpret_cast<unsigned*>(info + (kPacked ? TILE + 4 : 0));
+    unsigned* snext = grp + (kPacked ? RG : 0);
+    const int tid = threadIdx.x, rg = tid / LANES;
+
+    unsigned tile = blockIdx.x;
+    if (p.ticket) {
+        if (tid == 0) *snext = atomicAdd(p.ticket, 1u);
+        __syncthreads();
+        tile = *snext;
+        __syncthreads();
+    }
+    if (tile < p.total) issue<T, kVec, 2>(p, place_of<T, false>(p, tile), stages);
+    for (int st = 0; tile < p.total; st ^= 1) {
+        const Place q = place_of<T, false>(p, tile);
+        uint4* stage = stages + st * (2 * R * NT);
+        unsigned mine = 0;
+        if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) : tile + gridDim.x;
+        if constexpr (kPacked) row_info<T>(p, q.k, info, grp);
+        const int t0 = q.k * TILE + rg * R;
+        cp_wait_all();
+        // The thread's rows as one map (A, B); rows past N change nothing.
+        float s[kLogit ? R : 1][VEC];
+        float A[VEC], Bv[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) A[v] = 1.f, Bv[v] = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float a[VEC], x[VEC];
+            unpack(stage[r * NT + tid], a);
+            unpack(stage[(R + r) * NT + tid], x);
+            if constexpr (kLogit) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) s[r][v] = sigmoid(a[v]);
+            }
+            if (t0 + r < p.N) {
+                if constexpr (kPacked) {
+                    const int w = info[rg * R + r], o = w & kOwner;
+                    if (w & kBegin)
+                        load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr,
+                                            p, q, Bv);
+                }
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
+                    A[v] *= d;
+                    Bv[v] = fmaf(d, Bv[v], kLogit ? (1.f - d) * x[v] : x[v]);
+                }
+            }
+        }
+        put<T, kVec>(sa, A);
+        put<T, kVec>(sb, Bv);
+        if (tid == 0) *snext = mine;
+        __syncthreads();
+        const unsigned next = *snext;
+        if (next < p.total) issue<T, kVec, 2>(p, place_of<T, false>(p, next), stages + (st ^ 1) * (2 * R * NT));
+        if (tid < CB) {  // one thread a channel
+            const int c = q.cb * CB + tid, warp = tid >> 5;
+            const bool on = c < p.C, last = q.k + 1 == p.tiles;
+            float At, Bt, h = 0.f;
+            const bool cut = fold<CB, kPacked, false>(sa + tid, sb + tid, grp, At, Bt);
+            if (cut && !last) publish<T>(p, q, q.k, c, on, Bt, warp);
+            if (q.k == 0) h = !kPacked && p.init && on ? p.init[static_cast<int64_t>(q.b) * p.C + c] : 0.f;
+            else h = look_back<T>(p, q, q.k, c, on, At, Bt, warp, cut);
+            const float end = cut ? Bt : fmaf(At, h, Bt);
+            if (!last && !cut) publish<T>(p, q, q.k, c, on, end, warp);
+            if (!kPacked && last && p.fin && on) p.fin[static_cast<int64_t>(q.b) * p.C + c] = end;
+#pragma unroll 8
+            for (int g = 0; g < RG; ++g) {
+                const float ga = sa[g * CB + tid], gb = sb[g * CB + tid];
+                sa[g * CB + tid] = h;
+                h = kPacked && (grp[g] & 1u) ? gb : fmaf(ga, h, gb);
+            }
+        }
+        __syncthreads();
+        if (p.O || (kPacked && p.fin)) {
+            float h[VEC];
+            get<T, kVec>(sa, h);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (t0 + r >= p.N) break;
+                float a[VEC], x[VEC];
+                unpack(stage[r * NT + tid], a);
+                unpack(stage[(R + r) * NT + tid], x);
+                const int w = kPacked ? info[rg * R + r] : 0, o = w & kOwner;
+                if (kPacked && (w & kBegin))
+                    load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr, p,
+                                        q, h);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
+                    h[v] = fmaf(d, h[v], kLogit ? (1.f - d) * x[v] : x[v]);
+                }
+                if (p.O && (!kPacked || o != kOwner)) store_row<T, kVec>(p.O, p, q, t0 + r, h);
+                if (kPacked && (w & kEnd) && o != kOwner && p.fin)
+                    save_state<T, kVec>(p.fin + static_cast<int64_t>(o) * p.C, p, q, h);
+            }
+        }
+        if constexpr (kPacked) __syncthreads();  // info is rewritten for the next tile
+        tile = next;
+    }
+}
+
+// Backward: the forward state enters each tile from its checkpoint (no chain);
+// the carry c comes down the chain from the last tile.
+template <typename T, bool kLogit, bool kPacked, bool kVec>
+__global__ void __launch_bounds__(NT, 2) scan_backward_kernel(const Args<T> p) {
+    constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
+    extern __shared__ __align__(16) uint8_t sm[];
+    uint4* stages = reinterpret_cast<uint4*>(sm);
+    float* sa = reinterpret_cast<float*>(stages + 2 * 3 * R * NT);
+    float* sb = sa + RG * CB;
+    float* sc = sb + RG * CB;
+    int* info = reinterpret_cast<int*>(sc + RG * CB);
+    unsigned* grp = reinterpret_cast<unsigned*>(info + (kPacked ? TILE + 4 : 0));
+    unsigned* snext = grp + (kPacked ? RG : 0);
+    const int tid = threadIdx.x, rg = tid / LANES;
+
+    unsigned tile = blockIdx.x;
+    if (p.ticket) {
+        if (tid == 0) *snext = atomicAdd(p.ticket, 1u);
+        __syncthreads();
+        tile = *snext;
+        __syncthreads();
+    }
+    if (tile < p.total) issue<T, kVec, 3>(p, place_of<T, true>(p, tile), stages);
+    for (int st = 0; tile < p.total; st ^= 1) {
+        const Place q = place_of<T, true>(p, tile);
+        uint4* stage = stages + st * (3 * R * NT);
+        unsigned mine = 0;
+        if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) : tile + gridDim.x;
+        if constexpr (kPacked) row_info<T>(p, q.k, info, grp);
+        const int t0 = q.k * TILE + rg * R;
+        cp_wait_all();
+        float s[kLogit ? R : 1][VEC];
+        float A[VEC], Bf[VEC], Br[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) A[v] = 1.f, Bf[v] = 0.f, Br[v] = 0.f;
+        // forward over the rows: A, the state's Bf, and (without packed borders)
+        // the carry's Br = sum_i (s_0 .. s_i) dOut_i
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float a[VEC], x[VEC], g[VEC];
+            unpack(stage[r * NT + tid], a);
+            unpack(stage[(R + r) * NT + tid], x);
+            if constexpr (!kPacked) unpack(stage[(2 * R + r) * NT + tid], g);
+            if constexpr (kLogit) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) s[r][v] = sigmoid(a[v]);
+            }
+            if (t0 + r < p.N) {
+                if constexpr (kPacked) {
+                    const int w = info[rg * R + r], o = w & kOwner;
+                    if (w & kBegin)
+                        load_state<T, kVec>(
+                            p.h_init && o != kOwner ? p.h_init + static_cast<int64_t>(o) * p.C : nullptr, p, q, Bf);
+                }
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
+                    A[v] *= d;
+                    Bf[v] = fmaf(d, Bf[v], kLogit ? (1.f - d) * x[v] : x[v]);
+                    if constexpr (!kPacked) Br[v] = fmaf(A[v], g[v], Br[v]);
+                }
+            }
+        }
+        if constexpr (kPacked) {  // the carry row by row, from the last
+#pragma unroll
+            for (int r = R - 1; r >= 0; --r) {
+                if (t0 + r < p.N) {
+                    const int w = info[rg * R + r], o = w & kOwner;
+                    float a[VEC], g[VEC];
+                    unpack(stage[r * NT + tid], a);
+                    unpack(stage[(2 * R + r) * NT + tid], g);
+                    if (w & kEnd)
+                        load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr,
+                                            p, q, Br);
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) Br[v] = (kLogit ? s[kLogit ? r : 0][v] : a[v]) * (g[v] + Br[v]);
+                }
+            }
+        }
+        put<T, kVec>(sa, A);
+        put<T, kVec>(sb, Bf);
+        put<T, kVec>(sc, Br);
+        if (tid == 0) *snext = mine;
+        __syncthreads();
+        const unsigned next = *snext;
+        if (next < p.total) issue<T, kVec, 3>(p, place_of<T, true>(p, next), stages + (st ^ 1) * (3 * R * NT));
+        if (tid < CB) {
+            const int c = q.cb * CB + tid, warp = tid >> 5, i = p.tiles - 1 - q.k;
+            const bool on = c < p.C, last = q.k == 0;
+            float h = 0.f;
+            if (on) {
+                if (q.k == 0) h = !kPacked && p.h_init ? p.h_init[static_cast<int64_t>(q.b) * p.C + c] : 0.f;
+                else h = p.states[(static_cast<int64_t>(q.b) * p.tiles + q.k - 1) * p.C + c];
+            }
+            float At, Bt, y = 0.f;
+            const bool cut = fold<CB, kPacked, true>(sa + tid, sc + tid, grp, At, Bt);
+            if (cut && !last) publish<T>(p, q, i, c, on, Bt, warp);
+            if (i == 0) y = !kPacked && p.init && on ? p.init[static_cast<int64_t>(q.b) * p.C + c] : 0.f;
+            else y = look_back<T>(p, q, i, c, on, At, Bt, warp, cut);
+            const float end = cut ? Bt : fmaf(At, y, Bt);
+            if (!last && !cut) publish<T>(p, q, i, c, on, end, warp);
+            if (!kPacked && last && p.fin && on) p.fin[static_cast<int64_t>(q.b) * p.C + c] = end;
+            // the carry entering each row group replaces its Br, from the last group down
+#pragma unroll 8
+            for (int g = RG - 1; g >= 0; --g) {
+                const float ga = sa[g * CB + tid], gb = sc[g * CB + tid];
+                sc[g * CB + tid] = y;
+                y = kPacked && (grp[g] & 2u) ? gb : fmaf(ga, y, gb);
+            }
+#pragma unroll 8
+            for (int g = 0; g < RG; ++g) {
+                const float ga = sa[g * CB + tid], gb = sb[g * CB + tid];
+                sa[g * CB + tid] = h;
+                h = kPacked && (grp[g] & 1u) ? gb : fmaf(ga, h, gb);
+            }
+        }
+        __syncthreads();
+        float hp[R][VEC], h[VEC], y[VEC];
+        get<T, kVec>(sa, h);
+        get<T, kVec>(sc, y);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float a[VEC], x[VEC];
+            unpack(stage[r * NT + tid], a);
+            unpack(stage[(R + r) * NT + tid], x);
+            if constexpr (kPacked) {
+                const int w = info[rg * R + r], o = w & kOwner;
+                if (w & kBegin)
+                    load_state<T, kVec>(p.h_init && o != kOwner ? p.h_init + static_cast<int64_t>(o) * p.C : nullptr,
+                                        p, q, h);
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
+                hp[r][v] = h[v];
+                h[v] = fmaf(d, h[v], kLogit ? (1.f - d) * x[v] : x[v]);
+            }
+        }
+#pragma unroll
+        for (int r = R - 1; r >= 0; --r) {
+            if (t0 + r < p.N) {
+                float a[VEC], x[VEC], g[VEC];
+                unpack(stage[r * NT + tid], a);
+                unpack(stage[(R + r) * NT + tid], x);
+                unpack(stage[(2 * R + r) * NT + tid], g);
+                const int w = kPacked ? info[rg * R + r] : 0, o = w & kOwner;
+                if (kPacked && (w & kEnd))
+                    load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr, p,
+                                        q, y);
+                float da[VEC], dx[VEC];
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
+                    const float tot = g[v] + y[v];
+                    dx[v] = kLogit ? (1.f - d) * tot : tot;
+                    da[v] = kLogit ? d * dx[v] * (hp[r][v] - x[v]) : tot * hp[r][v];
+                    y[v] = d * tot;
+                }
+                if (!kPacked || o != kOwner) {
+                    store_row<T, kVec>(p.dA, p, q, t0 + r, da);
+                    store_row<T, kVec>(p.dX, p, q, t0 + r, dx);
+                }
+                if (kPacked && (w & kBegin) && o != kOwner && p.fin)
+                    save_state<T, kVec>(p.fin + static_cast<int64_t>(o) * p.C, p, q, y);
+            }
+        }
+        if constexpr (kPacked) __syncthreads();  // info is rewritten for the next tile
+        tile = next;
+    }
+}
+
+// Packed calls: each tile's first boundary, the states of empty sequences
+// (to = from, or 0), and cleared flags.
+static __global__ void scan_prepare_kernel(const int* __restrict__ starts, int S, int N, int C, int tiles,
+                                           int* __restrict__ tile_first, const float* __restrict__ from,
+                                           float* __restrict__ to, unsigned* __restrict__ flags, size_t words) {
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const int64_t all = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (size_t i = id; i < words; i += all) flags[i] = 0u;
+    for (int64_t k = id; k <= tiles; k += all) {
+        const int64_t row = k * TILE;
+        int lo = 0, hi = S + 1;  // first i in 0 .. S with starts[i] >= row, S + 1 if none
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (min(max(starts[mid], 0), N) < row) lo = mid + 1;
+            else hi = mid;
+        }
+        tile_first[k] = lo;
+    }
+    if (!to) return;
+    const int lane = threadIdx.x & 31;
+    for (int64_t i = id >> 5; i < S; i += all >> 5) {
+        if (min(max(starts[i], 0), N) < min(max(starts[i + 1], 0), N)) continue;
+        for (int c = lane; c < C; c += 32) to[i * C + c] = from ? from[i * C + c] : 0.f;
+    }
+}
+
+}  // namespace scan
+}  // namespace la

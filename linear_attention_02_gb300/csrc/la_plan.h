@@ -118,7 +118,7 @@ inline size_t poly2_tc_scratch(int BH, int N) {
 }
 
 // Rows between two state checkpoints of the gated scan.
-constexpr int kScanTile = 256;
+constexpr int kScanTile = 128;
 
 // Tensor-core causal kernels: the chunks of all heads cut into equal ranges,
 // one per resident CTA (see tc_common.cuh, split_chunks).

@@ -55,7 +55,7 @@ def test_scan_step_refusals():
 
 def test_scan_checkpoint_size():
     assert lib.la_gated_scan_ckpt_floats(2, 1, 5) == 10
-    assert lib.la_gated_scan_ckpt_floats(3, 257, 64) == 3 * 2 * 64
+    assert lib.la_gated_scan_ckpt_floats(3, 257, 64) == 3 * 3 * 64
     assert lib.la_gated_scan_ckpt_floats(0, 257, 64) == 0
 
 
