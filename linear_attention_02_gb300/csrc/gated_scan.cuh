@@ -18,11 +18,14 @@
 // tile from the tile before (below), and hands each row group its state; then
 // each thread runs its rows and writes them.
 //
-// Tiles of the same channels in time form a chain.  A tile publishes its end
-// state (flag 2), or first its (A, B) (flag 1) where the tile before is not done;
-// the next tile looks back over up to 32 flags at once to the nearest end state
-// and applies the (A, B) in between in order.  The result is the same whichever
-// it finds, since the end state of a tile is always fma(A, state before, B).
+// Tiles of the same channels in time form a chain.  A tile publishes the end
+// state of each channel, and its (A, B) before that where the tile before is not
+// done; the next tile looks back over up to kWindow tiles at once to the nearest
+// end state and applies the (A, B) in between in order.  The result is the same
+// whichever it finds, since the end state of a tile is always fma(A, state
+// before, B).  A published word is its own flag: the arrays start as all ones, a
+// NaN that no arithmetic gives, so neither side needs a fence (flags beside the
+// data, with their fences, took 1.5 us a hop of the chain).
 // Tiles are numbered in time order and taken by an atomic ticket, so a tile only
 // waits for tiles that running blocks hold, each block working its own in
 // ascending order: the lowest unfinished one can always go on.
@@ -40,9 +43,6 @@
 
 namespace la {
 namespace scan {
-
-using tcf::ld_acquire;
-using tcf::st_release;
 
 constexpr int NT = 128;                 // threads
 constexpr int R = 8;                    // rows of a thread
@@ -73,8 +73,7 @@ struct Args {
     const float* h_init;        // backward: the forward's h_init
     const float* states;        // backward: the forward's end state of each tile, [B][tiles][C]
     float *incl, *aggA, *aggB;  // chain of this direction: end states and (A, B), [B][tiles][C]
-    unsigned* flags;            // [B][tiles][ncb][CB / 32]
-    unsigned* ticket;           // null: a single tile per chain, blocks take tiles by number
+    unsigned* ticket;           // tiles taken - 1; null: one tile a chain, blocks take tiles by number
     unsigned* status;
 };
 
@@ -298,67 +297,62 @@ __device__ __forceinline__ void row_info(const Args<T>& p, int k, int* info, uns
     __syncthreads();
 }
 
-// The state that enters chain tile `i` (numbered in the chain's direction) of
-// the warp's 32 channels: look back for the nearest published end state and
-// apply the published (A, B) after it in order.  Publishes this tile's own
-// (A, B) first if the tile before is not done (told: its end state is out
-// already).  All 32 lanes take part.
-template <typename T>
-__device__ float look_back(const Args<T>& p, const Place& q, int i, int c, bool on, float At, float Bt,
-                           int warp, bool told) {
-    constexpr int W = Geo<T>::CB / 32;
-    const int lane = threadIdx.x & 31;
-    const auto flag = [&](int j) {  // of chain tile j
-        return p.flags + ((static_cast<int64_t>(q.b) * p.tiles + j) * p.ncb + q.cb) * W + warp;
-    };
-    const auto at = [&](int j) { return (static_cast<int64_t>(q.b) * p.tiles + j) * p.C + c; };
-    int n = 32;
-    for (unsigned spin = 0;; ++spin) {
-        const int j = i - 1 - lane;
-        const unsigned f = j >= 0 ? ld_acquire(flag(j)) : 1u;
-        const unsigned done = __ballot_sync(0xffffffffu, f == 2u);
-        const unsigned none = __ballot_sync(0xffffffffu, f == 0u);
-        n = done ? __ffs(done) - 1 : 32;
-        if (n < 32 && (none & ((1u << n) - 1u)) == 0u) break;
-        if (!told) {
-            if (on) {
-                __stcg(p.aggA + at(i), At);
-                __stcg(p.aggB + at(i), Bt);
-            }
-            __syncwarp();
-            if (lane == 0) {
-                __threadfence();
-                st_release(flag(i), 1u);
-            }
-            told = true;
-        } else if (spin > tcf::kSpinLimit) {  // never met unless the device is broken: report, go on
-            if (lane == 0) atomicOr(p.status, tcf::kErrLookback);
-            return 0.f;
-        } else if (spin > 64) {
-            __nanosleep(100);
-        }
-    }
-    __syncwarp();
-    if (!on) return 0.f;
-    float h = __ldcg(p.incl + at(i - 1 - n));
-#pragma unroll 4
-    for (int d = n - 1; d >= 0; --d) {
-        const float a = __ldcg(p.aggA + at(i - 1 - d)), b = __ldcg(p.aggB + at(i - 1 - d));
-        h = fmaf(a, h, b);
-    }
-    return h;
+constexpr unsigned kUnset = 0xFFFFFFFFu;  // a word that nothing has been published in
+constexpr int kWindow = 16;               // tiles looked back over at once
+
+__device__ __forceinline__ unsigned ld_relaxed(const float* p) {
+    unsigned v;
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_relaxed(float* p, float x) {
+    unsigned v = __float_as_uint(x);
+    if (v == kUnset) v = 0x7FFFFFFFu;  // a NaN that came in with the caller's state
+    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// The state that enters chain tile i > 0 (numbered in the chain's direction) of
+// a channel; `at` is the channel's place in tile 0, tiles are `step` words apart.
+// `first`: what the tile before had published when this tile began.  Publishes
+// this tile's own (A, B) if that is not enough (quiet: its end state is out).
 template <typename T>
-__device__ __forceinline__ void publish(const Args<T>& p, const Place& q, int i, int c, bool on, float h,
-                                        int warp) {
-    constexpr int W = Geo<T>::CB / 32;
-    if (on) __stcg(p.incl + (static_cast<int64_t>(q.b) * p.tiles + i) * p.C + c, h);
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-        __threadfence();
-        st_release(p.flags + ((static_cast<int64_t>(q.b) * p.tiles + i) * p.ncb + q.cb) * W + warp, 2u);
+__device__ float look_back(const Args<T>& p, int i, int64_t at, int64_t step, unsigned first, float At,
+                           float Bt, bool quiet) {
+    if (first != kUnset) return __uint_as_float(first);
+    if (!quiet) {
+        st_relaxed(p.aggA + at + i * step, At);
+        st_relaxed(p.aggB + at + i * step, Bt);
     }
+    for (unsigned spin = 0; spin < tcf::kSpinLimit; ++spin) {
+        unsigned e[kWindow], a[kWindow], b[kWindow];
+#pragma unroll
+        for (int d = 0; d < kWindow; ++d) {
+            const int64_t w = at + (i - 1 - d) * step;
+            const bool in = i - 1 - d >= 0;
+            e[d] = in ? ld_relaxed(p.incl + w) : kUnset;
+            a[d] = in ? ld_relaxed(p.aggA + w) : kUnset;
+            b[d] = in ? ld_relaxed(p.aggB + w) : kUnset;
+        }
+        int n = -1;
+        bool all = true;
+#pragma unroll
+        for (int d = 0; d < kWindow; ++d) {
+            if (n < 0 && all && e[d] != kUnset) n = d;
+            all = all && a[d] != kUnset && b[d] != kUnset;
+        }
+        if (n >= 0) {
+            float h = 0.f;
+#pragma unroll
+            for (int d = kWindow - 1; d >= 0; --d) {
+                if (d == n) h = __uint_as_float(e[d]);
+                else if (d < n) h = fmaf(__uint_as_float(a[d]), h, __uint_as_float(b[d]));
+            }
+            return h;
+        }
+        if (spin > 64) __nanosleep(100);
+    }
+    atomicOr(p.status, tcf::kErrLookback);  // the tiles before never came: report it and go on
+    return 0.f;
 }
 
 template <typename T, bool kPacked, int STREAMS>
@@ -400,7 +394,7 @@ __global__ void __launch_bounds__(NT, 3) scan_forward_kernel(const Args<T> p) {
 
     unsigned tile = blockIdx.x;
     if (p.ticket) {
-        if (tid == 0) *snext = atomicAdd(p.ticket, 1u);
+        if (tid == 0) *snext = atomicAdd(p.ticket, 1u) + 1u;
         __syncthreads();
         tile = *snext;
         __syncthreads();
@@ -410,9 +404,12 @@ __global__ void __launch_bounds__(NT, 3) scan_forward_kernel(const Args<T> p) {
         const Place q = place_of<T, false>(p, tile);
         uint4* stage = stages + st * (2 * R * NT);
         unsigned mine = 0;
-        if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) : tile + gridDim.x;
+        if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
         if constexpr (kPacked) row_info<T>(p, q.k, info, grp);
-        const int t0 = q.k * TILE + rg * R;
+        const int t0 = q.k * TILE + rg * R, c = q.cb * CB + tid;
+        const bool on = tid < CB && c < p.C;  // this thread has a channel of the chain
+        const int64_t at = static_cast<int64_t>(q.b) * p.tiles * p.C + c;
+        const unsigned first = on && q.k ? ld_relaxed(p.incl + at + static_cast<int64_t>(q.k - 1) * p.C) : 0u;
         cp_wait_all();
         // The thread's rows as one map (A, B); rows past N change nothing.
         float s[kLogit ? R : 1][VEC];
@@ -449,17 +446,17 @@ __global__ void __launch_bounds__(NT, 3) scan_forward_kernel(const Args<T> p) {
         __syncthreads();
         const unsigned next = *snext;
         if (next < p.total) issue<T, kVec, 2>(p, place_of<T, false>(p, next), stages + (st ^ 1) * (2 * R * NT));
-        if (tid < CB) {  // one thread a channel
-            const int c = q.cb * CB + tid, warp = tid >> 5;
-            const bool on = c < p.C, last = q.k + 1 == p.tiles;
+        if (on) {
+            const bool last = q.k + 1 == p.tiles;
             float At, Bt, h = 0.f;
             const bool cut = fold<CB, kPacked, false>(sa + tid, sb + tid, grp, At, Bt);
-            if (cut && !last) publish<T>(p, q, q.k, c, on, Bt, warp);
-            if (q.k == 0) h = !kPacked && p.init && on ? p.init[static_cast<int64_t>(q.b) * p.C + c] : 0.f;
-            else h = look_back<T>(p, q, q.k, c, on, At, Bt, warp, cut);
+            float* out = p.incl + at + static_cast<int64_t>(q.k) * p.C;
+            if (cut && !last) st_relaxed(out, Bt);
+            if (q.k) h = look_back<T>(p, q.k, at, p.C, first, At, Bt, cut);
+            else if (!kPacked && p.init) h = p.init[static_cast<int64_t>(q.b) * p.C + c];
             const float end = cut ? Bt : fmaf(At, h, Bt);
-            if (!last && !cut) publish<T>(p, q, q.k, c, on, end, warp);
-            if (!kPacked && last && p.fin && on) p.fin[static_cast<int64_t>(q.b) * p.C + c] = end;
+            if (!last && !cut) st_relaxed(out, end);
+            if (!kPacked && last && p.fin) p.fin[static_cast<int64_t>(q.b) * p.C + c] = end;
 #pragma unroll 8
             for (int g = 0; g < RG; ++g) {
                 const float ga = sa[g * CB + tid], gb = sb[g * CB + tid];
@@ -513,7 +510,7 @@ __global__ void __launch_bounds__(NT, 2) scan_backward_kernel(const Args<T> p) {
 
     unsigned tile = blockIdx.x;
     if (p.ticket) {
-        if (tid == 0) *snext = atomicAdd(p.ticket, 1u);
+        if (tid == 0) *snext = atomicAdd(p.ticket, 1u) + 1u;
         __syncthreads();
         tile = *snext;
         __syncthreads();
@@ -523,9 +520,15 @@ __global__ void __launch_bounds__(NT, 2) scan_backward_kernel(const Args<T> p) {
         const Place q = place_of<T, true>(p, tile);
         uint4* stage = stages + st * (3 * R * NT);
         unsigned mine = 0;
-        if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) : tile + gridDim.x;
+        if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
         if constexpr (kPacked) row_info<T>(p, q.k, info, grp);
-        const int t0 = q.k * TILE + rg * R;
+        const int t0 = q.k * TILE + rg * R, c = q.cb * CB + tid, i = p.tiles - 1 - q.k;
+        const bool on = tid < CB && c < p.C;  // this thread has a channel of the chain
+        const int64_t at = static_cast<int64_t>(q.b) * p.tiles * p.C + c;
+        const unsigned first = on && i ? ld_relaxed(p.incl + at + static_cast<int64_t>(i - 1) * p.C) : 0u;
+        float h0 = 0.f;  // the state that enters the tile
+        if (on && q.k) h0 = p.states[at + static_cast<int64_t>(q.k - 1) * p.C];
+        else if (on && !kPacked && p.h_init) h0 = p.h_init[static_cast<int64_t>(q.b) * p.C + c];
         cp_wait_all();
         float s[kLogit ? R : 1][VEC];
         float A[VEC], Bf[VEC], Br[VEC];
@@ -582,22 +585,17 @@ __global__ void __launch_bounds__(NT, 2) scan_backward_kernel(const Args<T> p) {
         __syncthreads();
         const unsigned next = *snext;
         if (next < p.total) issue<T, kVec, 3>(p, place_of<T, true>(p, next), stages + (st ^ 1) * (3 * R * NT));
-        if (tid < CB) {
-            const int c = q.cb * CB + tid, warp = tid >> 5, i = p.tiles - 1 - q.k;
-            const bool on = c < p.C, last = q.k == 0;
-            float h = 0.f;
-            if (on) {
-                if (q.k == 0) h = !kPacked && p.h_init ? p.h_init[static_cast<int64_t>(q.b) * p.C + c] : 0.f;
-                else h = p.states[(static_cast<int64_t>(q.b) * p.tiles + q.k - 1) * p.C + c];
-            }
-            float At, Bt, y = 0.f;
+        if (on) {
+            const bool last = q.k == 0;
+            float At, Bt, y = 0.f, h = h0;
             const bool cut = fold<CB, kPacked, true>(sa + tid, sc + tid, grp, At, Bt);
-            if (cut && !last) publish<T>(p, q, i, c, on, Bt, warp);
-            if (i == 0) y = !kPacked && p.init && on ? p.init[static_cast<int64_t>(q.b) * p.C + c] : 0.f;
-            else y = look_back<T>(p, q, i, c, on, At, Bt, warp, cut);
+            float* out = p.incl + at + static_cast<int64_t>(i) * p.C;
+            if (cut && !last) st_relaxed(out, Bt);
+            if (i) y = look_back<T>(p, i, at, p.C, first, At, Bt, cut);
+            else if (!kPacked && p.init) y = p.init[static_cast<int64_t>(q.b) * p.C + c];
             const float end = cut ? Bt : fmaf(At, y, Bt);
-            if (!last && !cut) publish<T>(p, q, i, c, on, end, warp);
-            if (!kPacked && last && p.fin && on) p.fin[static_cast<int64_t>(q.b) * p.C + c] = end;
+            if (!last && !cut) st_relaxed(out, end);
+            if (!kPacked && last && p.fin) p.fin[static_cast<int64_t>(q.b) * p.C + c] = end;
             // the carry entering each row group replaces its Br, from the last group down
 #pragma unroll 8
             for (int g = RG - 1; g >= 0; --g) {
@@ -668,13 +666,13 @@ __global__ void __launch_bounds__(NT, 2) scan_backward_kernel(const Args<T> p) {
 }
 
 // Packed calls: each tile's first boundary, the states of empty sequences
-// (to = from, or 0), and cleared flags.
+// (to = from, or 0), and the chain's words unset.
 static __global__ void scan_prepare_kernel(const int* __restrict__ starts, int S, int N, int C, int tiles,
                                            int* __restrict__ tile_first, const float* __restrict__ from,
-                                           float* __restrict__ to, unsigned* __restrict__ flags, size_t words) {
+                                           float* __restrict__ to, unsigned* __restrict__ chain, size_t words) {
     const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const int64_t all = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (size_t i = id; i < words; i += all) flags[i] = 0u;
+    for (size_t i = id; i < words; i += all) chain[i] = kUnset;
     for (int64_t k = id; k <= tiles; k += all) {
         const int64_t row = k * TILE;
         int lo = 0, hi = S + 1;  // first i in 0 .. S with starts[i] >= row, S + 1 if none

@@ -7,22 +7,18 @@ namespace {
 
 using namespace scan;
 
-// Scratch of one pass: [ticket | flags], per-tile first boundaries of a packed
-// call, end states (unless they go to the caller's checkpoints), A and B.
+// Scratch of one pass: [ticket, A, B, end states (unless they go to the caller's
+// checkpoints)], all unset at first, then per-tile first boundaries of a packed call.
 struct Parts {
-    size_t words, first, incl, agg, bytes;
+    size_t states, words, first, bytes;
 };
-Parts parts_of(int B, int N, int C, int es, bool packed, bool own_incl) {
-    const int cb = LANES * (16 / es);
-    const size_t tiles = (static_cast<size_t>(N) + TILE - 1) / TILE, ncb = (static_cast<size_t>(C) + cb - 1) / cb;
+Parts parts_of(int B, int N, int C, bool packed, bool own_incl) {
+    const size_t tiles = (static_cast<size_t>(N) + TILE - 1) / TILE;
     Parts s = {};
-    const bool chain = tiles > 1;
-    s.words = chain ? 1 + static_cast<size_t>(B) * tiles * ncb * (cb / 32) : 0;
+    s.states = tiles > 1 ? static_cast<size_t>(B) * tiles * C : 0;
+    s.words = s.states ? 4 + (own_incl ? 3 : 2) * s.states : 0;
     s.first = plan::up256(s.words * 4);
-    s.incl = s.first + (packed ? plan::up256((tiles + 1) * 4) : 0);
-    const size_t states = chain ? plan::up256(static_cast<size_t>(B) * tiles * C * 4) : 0;
-    s.agg = s.incl + (own_incl ? states : 0);
-    s.bytes = s.agg + 2 * states;
+    s.bytes = s.first + (packed ? (tiles + 1) * 4 : 0);
     return s;
 }
 
@@ -51,16 +47,16 @@ cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl) {
     a.total = static_cast<unsigned>(a.B * tiles * ncb);
     a.status = c.status_word;
 
-    const Parts s = parts_of(a.B, a.N, a.C, sizeof(T), packed, own_incl);
+    const Parts s = parts_of(a.B, a.N, a.C, packed, own_incl);
     uint8_t* base = nullptr;
     cudaError_t e = cudaSuccess;
     if (s.bytes && (e = scratch_alloc(c, reinterpret_cast<void**>(&base), s.bytes)) != cudaSuccess) return e;
     if (tiles > 1) {
         a.ticket = reinterpret_cast<unsigned*>(base);
-        a.flags = a.ticket + 1;
-        if (own_incl) a.incl = reinterpret_cast<float*>(base + s.incl);
-        a.aggA = reinterpret_cast<float*>(base + s.agg);
-        a.aggB = a.aggA + (s.bytes - s.agg) / 8;
+        a.aggA = reinterpret_cast<float*>(base) + 4;
+        a.aggB = a.aggA + s.states;
+        if (own_incl) a.incl = a.aggB + s.states;
+        else e = cudaMemsetAsync(a.incl, 0xFF, s.states * 4, c.stream);
     }
     int* first = reinterpret_cast<int*>(base + s.first);
     if (packed) {
@@ -70,8 +66,8 @@ cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl) {
         scan_prepare_kernel<<<blocks, 256, 0, c.stream>>>(a.starts, a.S, a.N, a.C, a.tiles, first, a.init, a.fin,
                                                           a.ticket, s.words);
         note_launch();
-    } else if (s.words) {
-        e = cudaMemsetAsync(base, 0, s.words * 4, c.stream);
+    } else if (s.words && e == cudaSuccess) {
+        e = cudaMemsetAsync(base, 0xFF, s.words * 4, c.stream);
     }
 
     const auto go = [&](auto* kernel, size_t smem) {
@@ -148,10 +144,10 @@ cudaError_t gated_scan_backward(const LaunchCtx& c, const T* A, const T* X, cons
 }
 
 size_t LA_SCAN_SCRATCH(int B, int N, int C, bool packed, bool backward, bool ckpt) {
-    const size_t pass = parts_of(B, N, C, sizeof(LA_SCAN_T), packed, backward || !ckpt).bytes;
+    const size_t pass = parts_of(B, N, C, packed, backward || !ckpt).bytes;
     if (!backward || ckpt || N <= TILE) return pass;
     // the states, and on top of them the larger of the two passes, one after the other
-    const size_t fwd = parts_of(B, N, C, sizeof(LA_SCAN_T), packed, false).bytes;
+    const size_t fwd = parts_of(B, N, C, packed, false).bytes;
     return sizeof(float) * B * ((static_cast<size_t>(N) + TILE - 1) / TILE) * C + std::max(pass, fwd);
 }
 
