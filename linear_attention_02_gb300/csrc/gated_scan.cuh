@@ -49,6 +49,7 @@ constexpr int R = 8;                    // rows of a thread
 constexpr int LANES = 8;                // threads across a row: 128 bytes
 constexpr int RG = NT / LANES;          // row groups of a tile
 constexpr int TILE = RG * R;            // rows of a tile
+constexpr int FWD_STAGES = 1, FWD_BLOCKS = 5, BWD_STAGES = 1, BWD_BLOCKS = 3;
 static_assert(TILE == plan::kScanTile, "checkpoints lie at tile borders");
 
 template <typename T>
@@ -121,13 +122,17 @@ __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
                       __float_as_uint(x[3]));
 }
 
-// sigmoid(z) from e^-|z|, which does not overflow.  1 - s is taken as the fp32
-// difference wherever it is needed (exact for s >= 1/2), so that a constant
-// input stays a fixed point of the logit form.
+// sigmoid(z) = 1 / (1 + 2^(-z log2 e)): an overflow of the power gives 0.
 __device__ __forceinline__ float sigmoid(float z) {
-    const float e = tcf::ex2_approx(-1.4426950408889634f * fabsf(z));
-    const float r = __fdividef(1.f, 1.f + e);
-    return z >= 0.f ? r : e * r;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + tcf::ex2_approx(-1.4426950408889634f * z)));
+    return r;
+}
+
+// What a row adds to the state: x, or (1 - d) x as one rounding of x - d x.
+template <bool kLogit>
+__device__ __forceinline__ float added(float d, float x) {
+    return kLogit ? fmaf(-d, x, x) : x;
 }
 
 // A tile's place: batch row, time tile, channel block.
@@ -154,25 +159,25 @@ __device__ __forceinline__ void issue(const Args<T>& p, const Place& q, uint4* s
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
     const int tid = threadIdx.x, lane = tid % LANES, rg = tid / LANES;
     const T* src[3] = {p.A, p.X, p.G};
+    const int t0 = q.k * TILE + rg * R, c0 = q.cb * CB + (kVec ? lane * VEC : lane);
+    const int64_t at = (static_cast<int64_t>(q.b) * p.N + t0) * p.C + c0;
 #pragma unroll
     for (int s = 0; s < STREAMS; ++s) {
+        const T* from = src[s] + at;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int t = q.k * TILE + rg * R + r;
-            const int64_t row = (static_cast<int64_t>(q.b) * p.N + t) * p.C;
+        for (int r = 0; r < R; ++r, from += p.C) {
             uint4* slot = stage + (s * R + r) * NT + tid;
+            const bool row = t0 + r < p.N;
             if constexpr (kVec) {
-                const int c = q.cb * CB + lane * VEC;
-                const bool on = t < p.N && c < p.C;
-                cp16(slot, on ? src[s] + row + c : src[s], on);
+                const bool in = row && c0 < p.C;
+                cp16(slot, in ? from : src[s], in);
             } else {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
-                    const int c = q.cb * CB + lane + LANES * v;
-                    const bool on = t < p.N && c < p.C;
+                    const bool in = row && c0 + LANES * v < p.C;
                     T* e = reinterpret_cast<T*>(slot) + v;
-                    if constexpr (sizeof(T) == 4) cp4(e, on ? src[s] + row + c : src[s], on);
-                    else *e = on ? src[s][row + c] : from_f<T>(0.f);
+                    if constexpr (sizeof(T) == 4) cp4(e, in ? from + LANES * v : src[s], in);
+                    else *e = in ? from[LANES * v] : from_f<T>(0.f);
                 }
             }
         }
@@ -298,7 +303,7 @@ __device__ __forceinline__ void row_info(const Args<T>& p, int k, int* info, uns
 }
 
 constexpr unsigned kUnset = 0xFFFFFFFFu;  // a word that nothing has been published in
-constexpr int kWindow = 16;               // tiles looked back over at once
+constexpr int kWindow = 8;                // tiles looked back over at once
 
 __device__ __forceinline__ unsigned ld_relaxed(const float* p) {
     unsigned v;
@@ -323,33 +328,39 @@ __device__ float look_back(const Args<T>& p, int i, int64_t at, int64_t step, un
         st_relaxed(p.aggA + at + i * step, At);
         st_relaxed(p.aggB + at + i * step, Bt);
     }
+    // (A, B) of the tiles before, nearest first, as far as they are out without a
+    // gap; the end state before that run is the first to come.  Only words that
+    // have not come yet are read again.
+    unsigned a[kWindow], b[kWindow];
+#pragma unroll
+    for (int d = 0; d < kWindow; ++d) a[d] = b[d] = kUnset;
+    const int most = min(i - 1, kWindow);
     for (unsigned spin = 0; spin < tcf::kSpinLimit; ++spin) {
-        unsigned e[kWindow], a[kWindow], b[kWindow];
 #pragma unroll
         for (int d = 0; d < kWindow; ++d) {
-            const int64_t w = at + (i - 1 - d) * step;
-            const bool in = i - 1 - d >= 0;
-            e[d] = in ? ld_relaxed(p.incl + w) : kUnset;
-            a[d] = in ? ld_relaxed(p.aggA + w) : kUnset;
-            b[d] = in ? ld_relaxed(p.aggB + w) : kUnset;
-        }
-        int n = -1;
-        bool all = true;
-#pragma unroll
-        for (int d = 0; d < kWindow; ++d) {
-            if (n < 0 && all && e[d] != kUnset) n = d;
-            all = all && a[d] != kUnset && b[d] != kUnset;
-        }
-        if (n >= 0) {
-            float h = 0.f;
-#pragma unroll
-            for (int d = kWindow - 1; d >= 0; --d) {
-                if (d == n) h = __uint_as_float(e[d]);
-                else if (d < n) h = fmaf(__uint_as_float(a[d]), h, __uint_as_float(b[d]));
+            if (d < most && (a[d] == kUnset || b[d] == kUnset)) {
+                const int64_t w = at + (i - 1 - d) * step;
+                a[d] = ld_relaxed(p.aggA + w);
+                b[d] = ld_relaxed(p.aggB + w);
             }
+        }
+        int n = 0;
+#pragma unroll
+        for (int d = 0; d < kWindow; ++d)
+            if (n == d && a[d] != kUnset && b[d] != kUnset) n = d + 1;
+        // end states at distance n (before the run) and, when a tile published its
+        // end state alone, the nearest
+        const unsigned far = ld_relaxed(p.incl + at + (i - 1 - n) * step);
+        const unsigned near = n ? ld_relaxed(p.incl + at + (i - 1) * step) : kUnset;
+        if (near != kUnset) return __uint_as_float(near);
+        if (far != kUnset) {
+            float h = __uint_as_float(far);
+#pragma unroll
+            for (int d = kWindow - 1; d >= 0; --d)
+                if (d < n) h = fmaf(__uint_as_float(a[d]), h, __uint_as_float(b[d]));
             return h;
         }
-        if (spin > 64) __nanosleep(100);
+        if (spin > 256) __nanosleep(100);
     }
     atomicOr(p.status, tcf::kErrLookback);  // the tiles before never came: report it and go on
     return 0.f;
@@ -357,7 +368,7 @@ __device__ float look_back(const Args<T>& p, int i, int64_t at, int64_t step, un
 
 template <typename T, bool kPacked, int STREAMS>
 constexpr size_t smem_bytes() {
-    return static_cast<size_t>(2) * STREAMS * R * NT * 16 + sizeof(float) * STREAMS * RG * Geo<T>::CB +
+    return static_cast<size_t>(STREAMS == 2 ? FWD_STAGES : BWD_STAGES) * STREAMS * R * NT * 16 + sizeof(float) * STREAMS * RG * Geo<T>::CB +
            (kPacked ? sizeof(int) * (TILE + 4 + RG) : 0) + 16;
 }
 
@@ -381,11 +392,11 @@ __device__ __forceinline__ bool fold(const float* a, const float* b, const unsig
 }
 
 template <typename T, bool kLogit, bool kPacked, bool kVec>
-__global__ void __launch_bounds__(NT, 3) scan_forward_kernel(const Args<T> p) {
+__global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 : FWD_BLOCKS) scan_forward_kernel(const Args<T> p) {
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
     extern __shared__ __align__(16) uint8_t sm[];
     uint4* stages = reinterpret_cast<uint4*>(sm);
-    float* sa = reinterpret_cast<float*>(stages + 2 * 2 * R * NT);
+    float* sa = reinterpret_cast<float*>(stages + FWD_STAGES * 2 * R * NT);
     float* sb = sa + RG * CB;
     int* info = reinterpret_cast<int*>(sb + RG * CB);
     unsigned* grp = reinterpret_cast<unsigned*>(info + (kPacked ? TILE + 4 : 0));
@@ -402,7 +413,7 @@ __global__ void __launch_bounds__(NT, 3) scan_forward_kernel(const Args<T> p) {
     if (tile < p.total) issue<T, kVec, 2>(p, place_of<T, false>(p, tile), stages);
     for (int st = 0; tile < p.total; st ^= 1) {
         const Place q = place_of<T, false>(p, tile);
-        uint4* stage = stages + st * (2 * R * NT);
+        uint4* stage = stages + (FWD_STAGES > 1 ? st : 0) * (2 * R * NT);
         unsigned mine = 0;
         if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
         if constexpr (kPacked) row_info<T>(p, q.k, info, grp);
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(NT, 3) scan_forward_kernel(const Args<T> p) {
                 for (int v = 0; v < VEC; ++v) {
                     const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
                     A[v] *= d;
-                    Bv[v] = fmaf(d, Bv[v], kLogit ? (1.f - d) * x[v] : x[v]);
+                    Bv[v] = fmaf(d, Bv[v], added<kLogit>(d, x[v]));
                 }
             }
         }
@@ -445,7 +456,8 @@ __global__ void __launch_bounds__(NT, 3) scan_forward_kernel(const Args<T> p) {
         if (tid == 0) *snext = mine;
         __syncthreads();
         const unsigned next = *snext;
-        if (next < p.total) issue<T, kVec, 2>(p, place_of<T, false>(p, next), stages + (st ^ 1) * (2 * R * NT));
+        if (FWD_STAGES > 1 && next < p.total)
+            issue<T, kVec, 2>(p, place_of<T, false>(p, next), stages + (st ^ 1) * (2 * R * NT));
         if (on) {
             const bool last = q.k + 1 == p.tiles;
             float At, Bt, h = 0.f;
@@ -481,13 +493,14 @@ __global__ void __launch_bounds__(NT, 3) scan_forward_kernel(const Args<T> p) {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
-                    h[v] = fmaf(d, h[v], kLogit ? (1.f - d) * x[v] : x[v]);
+                    h[v] = fmaf(d, h[v], added<kLogit>(d, x[v]));
                 }
                 if (p.O && (!kPacked || o != kOwner)) store_row<T, kVec>(p.O, p, q, t0 + r, h);
                 if (kPacked && (w & kEnd) && o != kOwner && p.fin)
                     save_state<T, kVec>(p.fin + static_cast<int64_t>(o) * p.C, p, q, h);
             }
         }
+        if (FWD_STAGES == 1 && next < p.total) issue<T, kVec, 2>(p, place_of<T, false>(p, next), stages);
         if constexpr (kPacked) __syncthreads();  // info is rewritten for the next tile
         tile = next;
     }
@@ -496,11 +509,11 @@ __global__ void __launch_bounds__(NT, 3) scan_forward_kernel(const Args<T> p) {
 // Backward: the forward state enters each tile from its checkpoint (no chain);
 // the carry c comes down the chain from the last tile.
 template <typename T, bool kLogit, bool kPacked, bool kVec>
-__global__ void __launch_bounds__(NT, 2) scan_backward_kernel(const Args<T> p) {
+__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS + 1) scan_backward_kernel(const Args<T> p) {
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
     extern __shared__ __align__(16) uint8_t sm[];
     uint4* stages = reinterpret_cast<uint4*>(sm);
-    float* sa = reinterpret_cast<float*>(stages + 2 * 3 * R * NT);
+    float* sa = reinterpret_cast<float*>(stages + BWD_STAGES * 3 * R * NT);
     float* sb = sa + RG * CB;
     float* sc = sb + RG * CB;
     int* info = reinterpret_cast<int*>(sc + RG * CB);
@@ -518,7 +531,7 @@ __global__ void __launch_bounds__(NT, 2) scan_backward_kernel(const Args<T> p) {
     if (tile < p.total) issue<T, kVec, 3>(p, place_of<T, true>(p, tile), stages);
     for (int st = 0; tile < p.total; st ^= 1) {
         const Place q = place_of<T, true>(p, tile);
-        uint4* stage = stages + st * (3 * R * NT);
+        uint4* stage = stages + (BWD_STAGES > 1 ? st : 0) * (3 * R * NT);
         unsigned mine = 0;
         if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
         if constexpr (kPacked) row_info<T>(p, q.k, info, grp);
@@ -557,7 +570,7 @@ __global__ void __launch_bounds__(NT, 2) scan_backward_kernel(const Args<T> p) {
                 for (int v = 0; v < VEC; ++v) {
                     const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
                     A[v] *= d;
-                    Bf[v] = fmaf(d, Bf[v], kLogit ? (1.f - d) * x[v] : x[v]);
+                    Bf[v] = fmaf(d, Bf[v], added<kLogit>(d, x[v]));
                     if constexpr (!kPacked) Br[v] = fmaf(A[v], g[v], Br[v]);
                 }
             }
@@ -584,7 +597,8 @@ __global__ void __launch_bounds__(NT, 2) scan_backward_kernel(const Args<T> p) {
         if (tid == 0) *snext = mine;
         __syncthreads();
         const unsigned next = *snext;
-        if (next < p.total) issue<T, kVec, 3>(p, place_of<T, true>(p, next), stages + (st ^ 1) * (3 * R * NT));
+        if (BWD_STAGES > 1 && next < p.total)
+            issue<T, kVec, 3>(p, place_of<T, true>(p, next), stages + (st ^ 1) * (3 * R * NT));
         if (on) {
             const bool last = q.k == 0;
             float At, Bt, y = 0.f, h = h0;
@@ -629,7 +643,7 @@ __global__ void __launch_bounds__(NT, 2) scan_backward_kernel(const Args<T> p) {
             for (int v = 0; v < VEC; ++v) {
                 const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
                 hp[r][v] = h[v];
-                h[v] = fmaf(d, h[v], kLogit ? (1.f - d) * x[v] : x[v]);
+                h[v] = fmaf(d, h[v], added<kLogit>(d, x[v]));
             }
         }
 #pragma unroll
@@ -660,6 +674,7 @@ __global__ void __launch_bounds__(NT, 2) scan_backward_kernel(const Args<T> p) {
                     save_state<T, kVec>(p.fin + static_cast<int64_t>(o) * p.C, p, q, y);
             }
         }
+        if (BWD_STAGES == 1 && next < p.total) issue<T, kVec, 3>(p, place_of<T, true>(p, next), stages);
         if constexpr (kPacked) __syncthreads();  // info is rewritten for the next tile
         tile = next;
     }
