@@ -13,15 +13,20 @@
 //
 // A warp works alone.  Each lane copies (cp.async) exactly the 16-byte pieces it
 // will use itself as matrix operands, a ring of steps ahead, so there is no
-// barrier and no exchange: scores are m16n8k16 products of the query heads (rows)
-// with 8 keys, values m16n8k16 products of the weights with 16 value rows, with
-// the contraction index and the output columns in the order in which the pieces
-// lie in memory.  fp32 storage takes m16n8k8 tf32 products of two-term splits
-// (three products; relative error 2^-21).  bf16 storage: q, k, v are exact
-// operands; the weights are fp32 and go in as three bf16 terms (24 bits), so no
-// precision is lost against fp32 arithmetic.  The warp-level matrix instruction
-// is enough here: a step of 16 x 64 bf16 keys and values is 4 KB of memory
-// traffic, about 170 cycles of an SM's share of the bandwidth, and 32 products.
+// barrier: scores are products of the query heads (rows) with 8 keys, outputs
+// products of the weights with 16 value rows, with the contraction index and the
+// output columns in the order in which the pieces lie in memory.
+// bf16 storage: m16n8k16; q, k, v are exact operands, the weights are fp32 and go
+// in as three bf16 terms (24 bits), so no precision is lost against fp32
+// arithmetic.  fp32 storage: m16n8k8 tf32 products of two-term splits (relative
+// error 2^-21).  With up to 8 query heads a key head (kHeads = 8), the operand's
+// rows 8 to 15 hold a second term of the same heads instead of nothing; with more,
+// they hold heads 8 to 15, and heads past 16 take further passes.  (Keys as rows
+// and heads as columns needs fewer products, but the weights must be transposed
+// between the two: 829 us against 760 us at 256 x 16 x 4096 x 64.)
+// The warp-level matrix instruction is enough here: a step of 16 x 64 bf16 keys
+// and values is 4 KB of memory traffic, about 170 cycles of an SM's share of the
+// bandwidth, against 24 small products.
 //
 // The maximum is kept lazily: it is raised, and the sums rescaled, only when a
 // score passes it by more than 2^8, so most steps need no exchange between lanes.
@@ -31,6 +36,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "la_common.cuh"
 #include "la_launch.h"
@@ -42,7 +48,6 @@ namespace {
 constexpr int kWarps = 4;       // warps of a block
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 16;       // positions of a step
-constexpr int kTile = 16;       // query heads of a step
 constexpr float kSlack = 8.f;   // log2 by which a score may pass the maximum kept
 
 template <typename T, int D>
@@ -102,7 +107,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 struct PagedArgs {
     PagedShape s;
-    int G, HT, tiles_per_kh;    // query heads a key head, columns of a request, tiles of a key head
+    int G, HT, tiles_per_kh;    // query heads a key head, columns of a request, columns of a key head
     int append, direct;         // direct: descriptors by column, else by worker
     const int *table, *lens;
     float *out, *lse, *part;
@@ -131,13 +136,20 @@ struct Row {
 
 // A warp's place in the steps.
 struct Cursor {
-    int r, col, j;
+    int r, kh, tile, j;  // request, key head, tile of its query heads, step
     Row row;
-    __device__ Cursor(const PagedArgs& p, int r_) : r(r_), col(0), j(0), row(p, r_) {}
+    __device__ Cursor(const PagedArgs& p, int r_, int64_t off) : r(r_), row(p, r_) {
+        const int n = row.steps(), col = static_cast<int>(off / n);
+        j = row.j0 + static_cast<int>(off - static_cast<int64_t>(col) * n);
+        kh = col / p.tiles_per_kh;
+        tile = col - kh * p.tiles_per_kh;
+    }
+    __device__ int col(const PagedArgs& p) const { return kh * p.tiles_per_kh + tile; }
     __device__ void advance(const PagedArgs& p) {
         if (++j < row.j1) return;
-        if (++col == p.HT) {
-            col = 0;
+        if (++tile == p.tiles_per_kh) tile = 0, ++kh;
+        if (kh == p.s.Hkv) {
+            kh = 0;
             do {
                 ++r;
                 row = Row(p, min(r, p.s.R - 1));
@@ -151,8 +163,8 @@ struct Cursor {
 // step u0 - base of request r.  Every block sums up all requests (R lengths from
 // L2), each warp finds its place from the block's sums.
 struct Share {
-    int64_t left, per, base;
-    int r;
+    int64_t per, base;
+    int left, r;
 };
 __device__ __forceinline__ Share find_share(const PagedArgs& p, int worker, int workers, int min_per) {
     __shared__ int64_t s_sum[kThreads];
@@ -182,7 +194,7 @@ __device__ __forceinline__ Share find_share(const PagedArgs& p, int worker, int 
     total *= p.HT;
     w.per = max(static_cast<int64_t>(min_per), (total + workers - 1) / workers);
     const int64_t u0 = worker * w.per;
-    w.left = max(static_cast<int64_t>(0), min(w.per, total - u0));
+    w.left = static_cast<int>(max(static_cast<int64_t>(0), min(w.per, total - u0)));
     w.base = 0;
     w.r = 0;
     if (w.left == 0) return w;
@@ -216,32 +228,31 @@ __device__ __forceinline__ Share find_share(const PagedArgs& p, int worker, int 
 }
 
 // fp32 scores of a step by plain products, for the step whose split products gave
-// a NaN (an infinite key or query): the lane's 8 scores from the warp's pieces in
-// the ring and the query rows in memory.
+// a NaN (an infinite key or query): the lane's scores of head h (x of keys 2 t and
+// 2 t + 1 of key tile n) from the warp's pieces in the ring and the query row in memory.
 template <int D>
-__device__ __noinline__ void exact_scores(const uint8_t* st, const float* q, int heads, float (&s)[2][4]) {
+__device__ __noinline__ float2 exact_scores(const uint8_t* st, const float* q, bool on, int n, float sign) {
     constexpr int KC = Lay<float, D>::KC;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int t = threadIdx.x & 3;
+    float x[2] = {0.f, 0.f};
     __syncwarp();  // every lane's pieces have come
-    for (int n = 0; n < 2; ++n)
-        for (int e = 0; e < 4; ++e) {
-            const int h = g + 8 * (e >> 1), key = 2 * t + (e & 1);
-            float x = 0.f;
-            if (h < heads)
-                for (int c = 0; c < D; ++c)  // value c is word c % 4 of piece c / 16 of lane (key, c / 4 % 4)
-                    x += q[h * D + c] * reinterpret_cast<const float*>(
-                                            st + (n * KC + c / 16) * 512 + (key * 4 + c / 4 % 4) * 16)[c & 3];
-            s[n][e] = x;
-        }
+    if (on)
+        for (int e = 0; e < 2; ++e)
+            for (int c = 0; c < D; ++c)  // value c is word c % 4 of piece c / 16 of lane (key, c / 4 % 4)
+                x[e] += sign * q[c] * reinterpret_cast<const float*>(
+                                          st + (n * KC + c / 16) * 512 + ((2 * t + e) * 4 + c / 4 % 4) * 16)[c & 3];
     __syncwarp();  // before any lane copies into this stage again
+    return make_float2(x[0], x[1]);
 }
 
-template <typename T, int D>
+// kHeads: 8 or 16 query heads a step.
+template <typename T, int D, int kHeads>
 __global__ void __launch_bounds__(kThreads, Lay<T, D>::BLOCKS)
 paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* __restrict__ vn, T* K, T* V,
                     const PagedArgs p, int min_per) {
     using Ly = Lay<T, D>;
-    constexpr int KC = Ly::KC, VPL = Ly::VPL, VB = Ly::VB, NI = Ly::NI, NT = D / 8, STAGES = Ly::STAGES;
+    constexpr int KC = Ly::KC, VPL = Ly::VPL, VB = Ly::VB, NI = Ly::NI, ROWS = kHeads / 8, NT = D / 8;
+    constexpr int STAGES = Ly::STAGES, KOFF = 64 / static_cast<int>(sizeof(T));  // values from piece to piece
     constexpr bool kBf16 = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t sm[];
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
@@ -252,16 +263,10 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
     if (sh.left == 0) return;
     uint8_t* ring = sm + warp * (STAGES * Ly::STAGE);
     const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-    const int row16 = 1 << p.s.log2p;
+    const int off_mask = (1 << p.s.log2p) - 1;
     bool bad = false;
 
-    Cursor ld(p, sh.r);
-    {
-        const int64_t off = static_cast<int64_t>(worker) * sh.per - sh.base;
-        const int n = ld.row.steps();
-        ld.col = static_cast<int>(off / n);
-        ld.j = ld.row.j0 + static_cast<int>(off - static_cast<int64_t>(ld.col) * n);
-    }
+    Cursor ld(p, sh.r, static_cast<int64_t>(worker) * sh.per - sh.base);
     Cursor cs = ld;
     bool whole = cs.j == cs.row.j0;  // the column's first step is this warp's
     bool first_seg = true;
@@ -269,9 +274,9 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
     const auto page_of = [&](const Cursor& c) {  // page of the lane's position (lane & 15) of a step
         const int pos = c.j * kStep + (lane & 15);
         const int at = pos >> p.s.log2p;
-        return pos < c.row.len && at < p.s.max_pages ? p.table[static_cast<int64_t>(c.r) * p.s.max_pages + at] : -1;
+        return pos < c.row.len ? p.table[static_cast<int64_t>(c.r) * p.s.max_pages + at] : -1;
     };
-    int64_t to_load = sh.left;
+    int to_load = sh.left;
     int pg = page_of(ld);
     uint32_t seen[STAGES];  // positions that count, a bit each, of the steps in the ring, the current one first
 #pragma unroll
@@ -279,45 +284,42 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
 
     // Copies the lane's pieces of step `ld` into a stage and moves on; returns the
     // positions that count.
+    const T* const kbase = K + g * D + t * (16 / static_cast<int>(sizeof(T)));
+    const T* const vbase = V + 2 * t * D + g * VPL;
     const auto issue = [&](int stage) -> uint32_t {
         uint32_t mask = 0xFFFFu;
         if (to_load > 0) {
             const uint32_t kd = ring32 + stage * Ly::STAGE + lane * 16;
             const uint32_t vd = ring32 + stage * Ly::STAGE + Ly::KBYTES + lane * VB;
-            const int pos0 = ld.j * kStep, kh = ld.col / p.tiles_per_kh;
-            const int page = pg;
-            const Cursor now = ld;
-            ld.advance(p);
-            if (--to_load > 0) pg = page_of(ld);
-            const bool inside = p.s.log2p >= 4 && pos0 >= now.row.first && pos0 + kStep <= now.row.len &&
+            const int pos0 = ld.j * kStep, page = pg;
+            const bool inside = p.s.log2p >= 4 && pos0 >= ld.row.first && pos0 + kStep <= ld.row.len &&
                                 static_cast<unsigned>(page) < static_cast<unsigned>(p.s.num_pages);
             if (__all_sync(0xffffffffu, inside)) {  // one page, every position the request's
-                const int64_t row = ((static_cast<int64_t>(page) * p.s.Hkv + kh) << p.s.log2p) + (pos0 & (row16 - 1));
-                const T* kr = K + (row + g) * D + t * (16 / static_cast<int>(sizeof(T)));
-                const T* vr = V + (row + 2 * t) * D + g * VPL;
+                const int64_t row = ((static_cast<int64_t>(page) * p.s.Hkv + ld.kh) << p.s.log2p) + (pos0 & off_mask);
+                const T* kr = kbase + row * D;
+                const T* vr = vbase + row * D;
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int i = 0; i < KC; ++i)
-                        cp16(kd + (n * KC + i) * 512, kr + n * 8 * D + i * (64 / static_cast<int>(sizeof(T))), true);
+                    for (int i = 0; i < KC; ++i) cp16(kd + (n * KC + i) * 512, kr + n * 8 * D + i * KOFF, true);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
                     for (int i = 0; i < NI; ++i)
                         cpv<VB>(vd + (e * NI + i) * VB * 32, vr + ((e >> 1) * 8 + (e & 1)) * D + i * 8 * VPL, true);
             } else {
-                const int mypos = pos0 + (lane & 15);
-                const bool mine = mypos >= now.row.first && mypos < now.row.total;
+                const int mypos = pos0 + (lane & 15), len = ld.row.len;
+                const bool mine = mypos >= ld.row.first && mypos < ld.row.total;
                 const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.s.num_pages);
-                bad |= mine && mypos < now.row.len && !there;
-                mask = __ballot_sync(0xffffffffu, mine && (there || mypos == now.row.len)) & 0xFFFFu;
-                const int64_t nrow = static_cast<int64_t>(now.r) * p.s.Hkv + kh;
+                bad |= mine && mypos < len && !there;
+                mask = __ballot_sync(0xffffffffu, mine && (there || mypos == len)) & 0xFFFFu;
+                const int64_t nrow = static_cast<int64_t>(ld.r) * p.s.Hkv + ld.kh;
                 const auto key_row = [&](int key, const T* pool, const T* fresh, bool& on) -> const T* {
                     const int pos = pos0 + key;
                     const int id = __shfl_sync(0xffffffffu, page, key);
                     on = mask >> key & 1u;
-                    if (on && pos == now.row.len) return fresh + nrow * D;
-                    const int64_t row = ((static_cast<int64_t>(id) * p.s.Hkv + kh) << p.s.log2p) + (pos & (row16 - 1));
+                    if (on && pos == len) return fresh + nrow * D;
+                    const int64_t row = ((static_cast<int64_t>(id) * p.s.Hkv + ld.kh) << p.s.log2p) + (pos & off_mask);
                     return on ? pool + row * D : q;
                 };
 #pragma unroll
@@ -325,8 +327,7 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
                     bool on;
                     const T* kr = key_row(8 * n + g, K, kn, on) + t * (16 / static_cast<int>(sizeof(T)));
 #pragma unroll
-                    for (int i = 0; i < KC; ++i)
-                        cp16(kd + (n * KC + i) * 512, on ? kr + i * (64 / static_cast<int>(sizeof(T))) : q, on);
+                    for (int i = 0; i < KC; ++i) cp16(kd + (n * KC + i) * 512, on ? kr + i * KOFF : q, on);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -337,40 +338,57 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
                         cpv<VB>(vd + (e * NI + i) * VB * 32, on ? vr + i * 8 * VPL : q, on);
                 }
             }
+            if (--to_load > 0) {
+                ld.advance(p);
+                pg = page_of(ld);
+            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         return mask;
     };
 
-    // query operands of a column: rows g and g + 8 of the tile (0 past the heads)
-    uint4 qa[KC], qb[KC];
+    // query operands of a column: head g, and g + 8 with 16 heads (0 past the heads);
+    // a negative scale goes into their sign, so that larger products stay larger
+    // scores.  fp32 with 8 heads keeps both terms of the split.
+    constexpr int QT = kBf16 ? ROWS : 2;
+    const uint32_t flip = p.s.scale < 0.f ? (kBf16 ? 0x80008000u : 0x80000000u) : 0u;
+    const float sc = fabsf(p.s.scale) * 1.4426950408889634f;
+    uint32_t qf[QT][KC][4];
     const auto load_q = [&]() {
-        const int kh = cs.col / p.tiles_per_kh, h0 = (cs.col - kh * p.tiles_per_kh) * kTile;
-        const int64_t row = static_cast<int64_t>(cs.r) * p.s.Hq + kh * p.G + h0;
+        const int h0 = cs.tile * kHeads;
+        const int64_t row = static_cast<int64_t>(cs.r) * p.s.Hq + cs.kh * p.G + h0;
         const T* src = q + (row + g) * D + t * (16 / static_cast<int>(sizeof(T)));
 #pragma unroll
-        for (int i = 0; i < KC; ++i) {
-            const int off = i * (64 / static_cast<int>(sizeof(T)));
-            qa[i] = h0 + g < p.G ? *reinterpret_cast<const uint4*>(src + off) : make_uint4(0, 0, 0, 0);
-            qb[i] = h0 + g + 8 < p.G ? *reinterpret_cast<const uint4*>(src + 8 * D + off) : make_uint4(0, 0, 0, 0);
-        }
+        for (int z = 0; z < ROWS; ++z)
+#pragma unroll
+            for (int i = 0; i < KC; ++i) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (h0 + 8 * z + g < p.G) u = *reinterpret_cast<const uint4*>(src + 8 * z * D + i * KOFF);
+                const uint32_t w[4] = {u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if constexpr (!kBf16 && ROWS == 1) split_tf32(w[x], qf[0][i][x], qf[1][i][x]);
+                    else qf[z][i][x] = w[x];
+                }
+            }
     };
 
-    float o[NT][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    // of head g (and g + 8): output sums (with 8 heads in two parts), maximum (log2),
+    // sum of the weights of the lane's positions
+    float o[NT][4], m[ROWS], l[ROWS];
     const auto clear = [&]() {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-        m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
+        for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+#pragma unroll
+        for (int z = 0; z < ROWS; ++z) m[z] = -INFINITY, l[z] = 0.f;
     };
     clear();
     load_q();
-    const float sc = p.s.scale * 1.4426950408889634f;
 
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) seen[s] = issue(s);
     int stage = 0;
-    for (int64_t n_left = sh.left; n_left > 0; --n_left) {
+    for (int n_left = sh.left; n_left > 0; --n_left) {
         {
             const int to = stage + STAGES - 1;
             seen[STAGES - 1] = issue(to >= STAGES ? to - STAGES : to);
@@ -378,32 +396,38 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
         const uint8_t* st = ring + stage * Ly::STAGE;
 
-        // scores of 16 heads x 16 keys
+        // scores of 16 keys: s[n][2 z + e] of head g + 8 z, key 8 n + 2 t + e
         float s[2][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
-            for (int i = 0; i < KC; ++i) {
+        for (int i = 0; i < KC; ++i) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
                 const uint4 k = *reinterpret_cast<const uint4*>(st + (n * KC + i) * 512 + lane * 16);
-                if constexpr (kBf16) {
-                    mma_bf16(s[n], qa[i].x, qb[i].x, qa[i].y, qb[i].y, k.x, k.y);
-                    mma_bf16(s[n], qa[i].z, qb[i].z, qa[i].w, qb[i].w, k.z, k.w);
-                } else {
-                    const uint32_t kw[4] = {k.x, k.y, k.z, k.w}, aw[4] = {qa[i].x, qa[i].y, qa[i].z, qa[i].w},
-                                   bw[4] = {qb[i].x, qb[i].y, qb[i].z, qb[i].w};
+                const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-                    for (int h = 0; h < 4; h += 2) {
-                        uint32_t kh0, kl0, kh1, kl1, ah0, al0, ah1, al1, bh0, bl0, bh1, bl1;
+                for (int h = 0; h < 4; h += 2) {
+                    if constexpr (kBf16) {
+                        mma_bf16(s[n], qf[0][i][h], ROWS == 2 ? qf[ROWS - 1][i][h] : 0u, qf[0][i][h + 1],
+                                 ROWS == 2 ? qf[ROWS - 1][i][h + 1] : 0u, kw[h], kw[h + 1]);
+                    } else {
+                        uint32_t kh0, kl0, kh1, kl1;
                         split_tf32(kw[h], kh0, kl0);
                         split_tf32(kw[h + 1], kh1, kl1);
-                        split_tf32(aw[h], ah0, al0);
-                        split_tf32(aw[h + 1], ah1, al1);
-                        split_tf32(bw[h], bh0, bl0);
-                        split_tf32(bw[h + 1], bh1, bl1);
-                        mma_tf32(s[n], ah0, bh0, ah1, bh1, kh0, kh1);
-                        mma_tf32(s[n], ah0, bh0, ah1, bh1, kl0, kl1);
-                        mma_tf32(s[n], al0, bl0, al1, bl1, kh0, kh1);
+                        if constexpr (ROWS == 1) {  // rows: both terms of q
+                            mma_tf32(s[n], qf[0][i][h], qf[1][i][h], qf[0][i][h + 1], qf[1][i][h + 1], kh0, kh1);
+                            mma_tf32(s[n], qf[0][i][h], qf[1][i][h], qf[0][i][h + 1], qf[1][i][h + 1], kl0, kl1);
+                        } else {
+                            uint32_t ah[4], al[4];
+                            split_tf32(qf[0][i][h], ah[0], al[0]);
+                            split_tf32(qf[1][i][h], ah[1], al[1]);
+                            split_tf32(qf[0][i][h + 1], ah[2], al[2]);
+                            split_tf32(qf[1][i][h + 1], ah[3], al[3]);
+                            mma_tf32(s[n], ah[0], ah[1], ah[2], ah[3], kh0, kh1);
+                            mma_tf32(s[n], ah[0], ah[1], ah[2], ah[3], kl0, kl1);
+                            mma_tf32(s[n], al[0], al[1], al[2], al[3], kh0, kh1);
+                        }
                     }
                 }
             }
@@ -411,72 +435,83 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
         if constexpr (!kBf16) {
             bool nan = false;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2; ++n) {
+                if constexpr (ROWS == 1) s[n][0] += s[n][2], s[n][1] += s[n][3];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) nan |= s[n][e] != s[n][e];
+                for (int e = 0; e < 2 * ROWS; ++e) nan |= s[n][e] != s[n][e];
+            }
             if (__any_sync(0xffffffffu, nan)) {
-                const int kh = cs.col / p.tiles_per_kh, h0 = (cs.col - kh * p.tiles_per_kh) * kTile;
-                exact_scores<D>(st, q + (static_cast<int64_t>(cs.r) * p.s.Hq + kh * p.G + h0) * D, p.G - h0, s);
+#pragma unroll
+                for (int z = 0; z < ROWS; ++z) {
+                    const int h = cs.tile * kHeads + 8 * z + g;
+                    const float* src = q + (static_cast<int64_t>(cs.r) * p.s.Hq + cs.kh * p.G + h) * D;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const float2 x = exact_scores<D>(st, src, h < p.G, n, flip ? -1.f : 1.f);
+                        s[n][2 * z] = x.x, s[n][2 * z + 1] = x.y;
+                    }
+                }
             }
         }
-        const int pos0 = cs.j * kStep;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] *= sc;
         if (seen[0] != 0xFFFFu) {
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < 2 * ROWS; ++e)
                     if (!(seen[0] >> (8 * n + 2 * t + (e & 1)) & 1u)) s[n][e] = -INFINITY;
         }
-        const float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        const float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-        if (__any_sync(0xffffffffu, x0 > m0 + kSlack || x1 > m1 + kSlack)) {
-            float y0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1)), y1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-            y0 = fmaxf(m0, fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, 2)));
-            y1 = fmaxf(m1, fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, 2)));
-            const float f0 = m0 == y0 ? 1.f : ex2(m0 - y0), f1 = m1 == y1 ? 1.f : ex2(m1 - y1);
-            l0 *= f0;
-            l1 *= f1;
+        bool up = false;
+        float top[ROWS];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                o[n][0] *= f0;
-                o[n][1] *= f0;
-                o[n][2] *= f1;
-                o[n][3] *= f1;
-            }
-            m0 = y0;
-            m1 = y1;
+        for (int z = 0; z < ROWS; ++z) {
+            top[z] = fmaxf(fmaxf(s[0][2 * z], s[0][2 * z + 1]), fmaxf(s[1][2 * z], s[1][2 * z + 1])) * sc;
+            up |= top[z] > m[z] + kSlack;
         }
-        const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-        float w[2][4];
+        if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            w[n][0] = ex2(s[n][0] - z0);
-            w[n][1] = ex2(s[n][1] - z0);
-            w[n][2] = ex2(s[n][2] - z1);
-            w[n][3] = ex2(s[n][3] - z1);
-            l0 += w[n][0] + w[n][1];
-            l1 += w[n][2] + w[n][3];
+            for (int z = 0; z < ROWS; ++z) {
+                float y = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], 1));
+                y = fmaxf(m[z], fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2)));
+                const float f = m[z] == y ? 1.f : ex2(m[z] - y);
+                m[z] = y;
+                l[z] *= f;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    o[i][2 * z] *= f;
+                    o[i][2 * z + 1] *= f;
+                    if constexpr (ROWS == 1) o[i][2] *= f, o[i][3] *= f;
+                }
+            }
+        }
+        // weights; all of them 0 while no score is above -infinity
+#pragma unroll
+        for (int z = 0; z < ROWS; ++z) {
+            const float at = m[z] == -INFINITY ? 0.f : m[z];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                s[n][2 * z] = ex2(fmaf(s[n][2 * z], sc, -at));
+                s[n][2 * z + 1] = ex2(fmaf(s[n][2 * z + 1], sc, -at));
+                l[z] += s[n][2 * z] + s[n][2 * z + 1];
+            }
         }
         const uint8_t* vs = st + Ly::KBYTES + lane * VB;
         if constexpr (kBf16) {
-            uint32_t a[3][4];  // three terms of the weights
+            uint32_t w[3][ROWS][2];  // three terms of the weights
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                float x = w[u >> 1][2 * (u & 1)], y = w[u >> 1][2 * (u & 1) + 1];
+            for (int z = 0; z < ROWS; ++z)
 #pragma unroll
-                for (int z = 0; z < 3; ++z) {
-                    a[z][u] = pack2(x, y);
-                    x -= __uint_as_float(a[z][u] << 16);
-                    y -= __uint_as_float(a[z][u] & 0xFFFF0000u);
+                for (int n = 0; n < 2; ++n) {
+                    float x = s[n][2 * z], y = s[n][2 * z + 1];
+#pragma unroll
+                    for (int u = 0; u < 3; ++u) {
+                        w[u][z][n] = pack2(x, y);
+                        x -= __uint_as_float(w[u][z][n] << 16);
+                        y -= __uint_as_float(w[u][z][n] & 0xFFFF0000u);
+                    }
                 }
-            }
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                uint32_t v[4][VPL / 2];
+                uint32_t v[4][VPL / 2], b[VPL][2];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if constexpr (VB == 16) {
@@ -490,47 +525,75 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
                     const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-                    const uint32_t b0 = __byte_perm(v[0][j / 2], v[1][j / 2], sel);
-                    const uint32_t b1 = __byte_perm(v[2][j / 2], v[3][j / 2], sel);
+                    b[j][0] = __byte_perm(v[0][j / 2], v[1][j / 2], sel);
+                    b[j][1] = __byte_perm(v[2][j / 2], v[3][j / 2], sel);
+                }
+                if constexpr (ROWS == 1) {  // rows: the first two terms, then the third
 #pragma unroll
-                    for (int z = 0; z < 3; ++z)
-                        mma_bf16(o[i * VPL + j], a[z][0], a[z][1], a[z][2], a[z][3], b0, b1);
+                    for (int j = 0; j < VPL; ++j)
+                        mma_bf16(o[i * VPL + j], w[0][0][0], w[1][0][0], w[0][0][1], w[1][0][1], b[j][0], b[j][1]);
+#pragma unroll
+                    for (int j = 0; j < VPL; ++j)
+                        mma_bf16(o[i * VPL + j], w[2][0][0], 0u, w[2][0][1], 0u, b[j][0], b[j][1]);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 3; ++u)
+#pragma unroll
+                        for (int j = 0; j < VPL; ++j)
+                            mma_bf16(o[i * VPL + j], w[u][0][0], w[u][ROWS - 1][0], w[u][0][1], w[u][ROWS - 1][1],
+                                     b[j][0], b[j][1]);
                 }
             }
         } else {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                uint32_t ah[4], al[4];  // keys 2t (operand k = t) and 2t + 1 (k = t + 4)
-                split_tf32(__float_as_uint(w[n][0]), ah[0], al[0]);
-                split_tf32(__float_as_uint(w[n][2]), ah[1], al[1]);
-                split_tf32(__float_as_uint(w[n][1]), ah[2], al[2]);
-                split_tf32(__float_as_uint(w[n][3]), ah[3], al[3]);
+                uint32_t wh[ROWS][2], wl[ROWS][2];  // keys 2t (operand k = t) and 2t + 1 (k = t + 4)
+#pragma unroll
+                for (int z = 0; z < ROWS; ++z)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) split_tf32(__float_as_uint(s[n][2 * z + e]), wh[z][e], wl[z][e]);
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
                     const uint4 v0 = *reinterpret_cast<const uint4*>(vs + ((2 * n) * NI + i) * VB * 32);
                     const uint4 v1 = *reinterpret_cast<const uint4*>(vs + ((2 * n + 1) * NI + i) * VB * 32);
-                    const uint32_t x0w[4] = {v0.x, v0.y, v0.z, v0.w}, x1w[4] = {v1.x, v1.y, v1.z, v1.w};
+                    const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
+                    uint32_t h0[4], h1[4], c0[4], c1[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        uint32_t h0, c0, h1, c1;
-                        split_tf32(x0w[j], h0, c0);
-                        split_tf32(x1w[j], h1, c1);
-                        mma_tf32(o[i * 4 + j], ah[0], ah[1], ah[2], ah[3], h0, h1);
-                        mma_tf32(o[i * 4 + j], ah[0], ah[1], ah[2], ah[3], c0, c1);
-                        mma_tf32(o[i * 4 + j], al[0], al[1], al[2], al[3], h0, h1);
+                        split_tf32(x0[j], h0[j], c0[j]);
+                        split_tf32(x1[j], h1[j], c1[j]);
+                    }
+                    if constexpr (ROWS == 1) {  // rows: both terms of the weights
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_tf32(o[i * 4 + j], wh[0][0], wl[0][0], wh[0][1], wl[0][1], h0[j], h1[j]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_tf32(o[i * 4 + j], wh[0][0], wl[0][0], wh[0][1], wl[0][1], c0[j], c1[j]);
+                    } else {
+                        constexpr int Z = ROWS - 1;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_tf32(o[i * 4 + j], wh[0][0], wh[Z][0], wh[0][1], wh[Z][1], h0[j], h1[j]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_tf32(o[i * 4 + j], wh[0][0], wh[Z][0], wh[0][1], wh[Z][1], c0[j], c1[j]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_tf32(o[i * 4 + j], wl[0][0], wl[Z][0], wl[0][1], wl[Z][1], h0[j], h1[j]);
                     }
                 }
             }
         }
 
         // the new row goes into the cache, once a key head
-        if (p.append && cs.row.len >= pos0 && cs.row.len < pos0 + kStep && cs.col % p.tiles_per_kh == 0) {
-            const int kh = cs.col / p.tiles_per_kh, at = cs.row.len >> p.s.log2p;
+        if (p.append && cs.row.len >> 4 == cs.j && cs.tile == 0) {
+            const int at = cs.row.len >> p.s.log2p;
             const int id = at < p.s.max_pages ? p.table[static_cast<int64_t>(cs.r) * p.s.max_pages + at] : -1;
             if (static_cast<unsigned>(id) < static_cast<unsigned>(p.s.num_pages)) {
                 constexpr int PIECES = D * static_cast<int>(sizeof(T)) / 16;
-                const int64_t to = ((static_cast<int64_t>(id) * p.s.Hkv + kh) << p.s.log2p) + (cs.row.len & (row16 - 1));
-                const int64_t from = static_cast<int64_t>(cs.r) * p.s.Hkv + kh;
+                const int64_t to = ((static_cast<int64_t>(id) * p.s.Hkv + cs.kh) << p.s.log2p) + (cs.row.len & off_mask);
+                const int64_t from = static_cast<int64_t>(cs.r) * p.s.Hkv + cs.kh;
                 if (lane < PIECES) {
                     reinterpret_cast<uint4*>(K + to * D)[lane] = reinterpret_cast<const uint4*>(kn + from * D)[lane];
                     reinterpret_cast<uint4*>(V + to * D)[lane] = reinterpret_cast<const uint4*>(vn + from * D)[lane];
@@ -543,48 +606,49 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
         const bool col_end = cs.j + 1 == cs.row.j1;
         if (col_end || n_left == 1) {  // end of the column, or of the warp's range inside it
             bad |= cs.row.bad;
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-            l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-            const int kh = cs.col / p.tiles_per_kh, h0 = (cs.col - kh * p.tiles_per_kh) * kTile;
-            const int64_t row0 = static_cast<int64_t>(cs.r) * p.s.Hq + kh * p.G + h0;
+            const int h0 = cs.tile * kHeads;
+            const int64_t row0 = static_cast<int64_t>(cs.r) * p.s.Hq + cs.kh * p.G + h0;
             const bool done = whole && col_end;
             const int slot = first_seg ? 0 : 1;
-            float* part = p.part + (static_cast<int64_t>(worker) * 2 + slot) * kTile * (D + 2);
+            float* part = p.part + (static_cast<int64_t>(worker) * 2 + slot) * kHeads * (D + 2);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int h = g + 8 * half;
-                if (h0 + h >= p.G) continue;
-                const float l = half ? l1 : l0, m = half ? m1 : m0;
-                const float f = done ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-                float* dst = done ? p.out + (row0 + h) * D : part + h * D;
+            for (int z = 0; z < ROWS; ++z) {
+                float sum = l[z] + __shfl_xor_sync(0xffffffffu, l[z], 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                const int h = g + 8 * z;
+                if (h0 + h < p.G) {
+                    const float f = done ? (sum > 0.f || sum != sum ? 1.f / sum : 0.f) : 1.f;
+                    float* dst = done ? p.out + (row0 + h) * D : part + h * D;
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
+                    for (int i = 0; i < NI; ++i)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int j = 0; j < VPL; j += 4) {
-                            const int b = i * VPL + j, e = 2 * half + c;
-                            const int d = (2 * t + c + 8 * i) * VPL + j;
-                            *reinterpret_cast<float4*>(dst + d) =
-                                make_float4(o[b][e] * f, o[b + 1][e] * f, o[b + 2][e] * f, o[b + 3][e] * f);
+                            for (int j = 0; j < VPL; j += 4) {
+                                float y[4];
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    const float(&b)[4] = o[i * VPL + j + x];
+                                    y[x] = (ROWS == 1 ? b[c] + b[2 + c] : b[2 * z + c]) * f;
+                                }
+                                *reinterpret_cast<float4*>(dst + (2 * t + c + 8 * i) * VPL + j) =
+                                    make_float4(y[0], y[1], y[2], y[3]);
+                            }
+                    if (t == 0) {
+                        if (!done) {
+                            part[kHeads * D + 2 * h] = m[z];
+                            part[kHeads * D + 2 * h + 1] = sum;
+                        } else if (p.lse) {
+                            p.lse[row0 + h] = (m[z] + log2f(sum)) * 0.6931471805599453f;
                         }
-                if (t == 0) {
-                    if (!done) {
-                        part[kTile * D + 2 * h] = m;
-                        part[kTile * D + 2 * h + 1] = l;
-                    } else if (p.lse) {
-                        p.lse[row0 + h] = (m + log2f(l)) * 0.6931471805599453f;
                     }
                 }
             }
             if (lane == 0) {
-                const int64_t index = p.direct ? static_cast<int64_t>(cs.r) * p.HT + cs.col : worker;
+                const int col = cs.r * p.HT + cs.col(p), index = p.direct ? col : worker;
                 if (whole && !col_end) {  // first range of a split column
                     const int64_t rest = cs.row.j1 - (cs.j + 1);
-                    p.desc[index] = make_int4(worker, static_cast<int>(1 + (rest + sh.per - 1) / sh.per), slot,
-                                              p.direct ? 0 : cs.r * p.HT + cs.col);
+                    p.desc[index] = make_int4(worker, static_cast<int>(1 + (rest + sh.per - 1) / sh.per), slot, col);
                 } else if (whole && p.direct) {
                     p.desc[index] = make_int4(0, 0, 0, 0);
                 }
@@ -610,7 +674,7 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
 // Joins the ranges of a split column, one block a query head: the maximum of the
 // ranges' maxima, then sums scaled to it, in the order of the ranges within each
 // of the block's warps and of the warps.
-template <int D>
+template <int D, int kHeads>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs p) {
     __shared__ float s_m[kWarps], s_l[kWarps], s_a[kWarps][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -622,7 +686,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs p)
     if (d.y == 0) return;
     if (!p.direct) col = d.w;
     const int64_t r = col / p.HT;
-    const int c = static_cast<int>(col - r * p.HT), kh = c / p.tiles_per_kh, h0 = (c - kh * p.tiles_per_kh) * kTile;
+    const int c = static_cast<int>(col - r * p.HT), kh = c / p.tiles_per_kh, h0 = (c - kh * p.tiles_per_kh) * kHeads;
     if (h0 + h >= p.G) return;
     constexpr int E = D / 32;
     float m = -INFINITY, l = 0.f, a[E];
@@ -631,8 +695,8 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs p)
     const int each = (d.y + kWarps - 1) / kWarps, i1 = min(d.y, (warp + 1) * each);
 #pragma unroll 4
     for (int i = warp * each; i < i1; ++i) {
-        const float* part = p.part + ((static_cast<int64_t>(d.x) + i) * 2 + (i ? 0 : d.z)) * kTile * (D + 2);
-        const float pm = part[kTile * D + 2 * h], pl = part[kTile * D + 2 * h + 1];
+        const float* part = p.part + ((static_cast<int64_t>(d.x) + i) * 2 + (i ? 0 : d.z)) * kHeads * (D + 2);
+        const float pm = part[kHeads * D + 2 * h], pl = part[kHeads * D + 2 * h + 1];
         float v[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = part[h * D + lane + 32 * e];
@@ -668,19 +732,20 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs p)
 // Ranges are of at least this many steps, so that few partial sums are written.
 constexpr int kMinSteps = 4;
 
-template <typename T, int D>
-cudaError_t paged_decode_step(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K, T* V,
-                              const int* table, const int* lens, float* out, float* lse,
-                              const PagedShape& s) {
+namespace {
+
+template <typename T, int D, int kHeads>
+cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K, T* V, const int* table,
+                   const int* lens, float* out, float* lse, const PagedShape& s) {
     using Ly = Lay<T, D>;
-    auto* kernel = paged_decode_kernel<T, D>;
+    auto* kernel = paged_decode_kernel<T, D, kHeads>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM);
     if (e != cudaSuccess) return e;
     const int blocks = Ly::BLOCKS * c.num_sms, workers = blocks * kWarps;
     PagedArgs p = {};
     p.s = s;
     p.G = s.Hq / s.Hkv;
-    p.tiles_per_kh = (p.G + kTile - 1) / kTile;
+    p.tiles_per_kh = (p.G + kHeads - 1) / kHeads;
     p.HT = s.Hkv * p.tiles_per_kh;
     p.append = k ? 1 : 0;
     p.table = table;
@@ -689,9 +754,11 @@ cudaError_t paged_decode_step(const LaunchCtx& c, const T* q, const T* k, const 
     p.lse = lse;
     p.status = c.status_word;
     const int64_t cols = static_cast<int64_t>(s.R) * p.HT;
+    if (cols * ((static_cast<int64_t>(s.max_pages) << s.log2p) / kStep + 2) / workers >= INT_MAX)
+        return cudaErrorInvalidValue;  // a warp's steps are counted in 32 bits
     p.direct = cols <= workers;
     uint8_t* base = nullptr;
-    const size_t part = sizeof(float) * workers * 2 * kTile * (D + 2);
+    const size_t part = sizeof(float) * workers * 2 * kHeads * (D + 2);
     e = scratch_alloc(c, reinterpret_cast<void**>(&base), part + sizeof(int4) * workers);
     if (e != cudaSuccess) return e;
     p.part = reinterpret_cast<float*>(base);
@@ -701,7 +768,7 @@ cudaError_t paged_decode_step(const LaunchCtx& c, const T* q, const T* k, const 
     e = cudaGetLastError();
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(p.direct ? cols : workers), std::min(p.G, kTile));
+        cfg.gridDim = dim3(static_cast<unsigned>(p.direct ? cols : workers), std::min(p.G, kHeads));
         cfg.blockDim = dim3(kThreads);
         cfg.stream = c.stream;
         cudaLaunchAttribute at[1];
@@ -709,10 +776,20 @@ cudaError_t paged_decode_step(const LaunchCtx& c, const T* q, const T* k, const 
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p);
+        e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kHeads>, p);
     }
     scratch_free(c, base);
     return e;
+}
+
+}  // namespace
+
+template <typename T, int D>
+cudaError_t paged_decode_step(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K, T* V,
+                              const int* table, const int* lens, float* out, float* lse,
+                              const PagedShape& s) {
+    return s.Hq / s.Hkv <= 8 ? launch<T, D, 8>(c, q, k, v, K, V, table, lens, out, lse, s)
+                             : launch<T, D, 16>(c, q, k, v, K, V, table, lens, out, lse, s);
 }
 
 #define LA_INST_PD(T, D)                                                                          \
