@@ -108,10 +108,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 struct PagedArgs {
     PagedShape s;
     int G, HT, tiles_per_kh;    // query heads a key head, columns of a request, columns of a key head
-    int append, direct;         // direct: descriptors by column, else by worker
+    int append, direct;         // direct: descriptors by column, else by range
+    int heads;                  // rows of a partial result: the column's query heads
+    int max_ranges;
+    unsigned* next;             // ranges taken beyond the first of each warp (null: one each is enough)
     const int *table, *lens;
-    float *out, *lse, *part;
-    int4* desc;                 // {first worker, ranges, its slot, column} of a split column; ranges 0: none
+    float *out, *lse;
+    float* part;                // [ranges][2][heads x (D + 4)]: output sums [heads][D], then maximum, sum of each head
+    int4* desc;                 // {first range, ranges, its slot, column} of a split column; ranges 0: none
     unsigned* status;
 };
 
@@ -159,71 +163,51 @@ struct Cursor {
     }
 };
 
-// The warp's share: steps [u0, u0 + left) of all, `per` a warp; its first step is
-// step u0 - base of request r.  Every block sums up all requests (R lengths from
-// L2), each warp finds its place from the block's sums.
-struct Share {
-    int64_t per, base;
-    int left, r;
-};
-__device__ __forceinline__ Share find_share(const PagedArgs& p, int worker, int workers, int min_per) {
-    __shared__ int64_t s_sum[kThreads];
+// Inclusive sums of the steps of all requests, chunk by chunk of requests (a chunk
+// a thread); returns their total.  Every block does it for itself (R lengths from L2).
+__device__ __forceinline__ int64_t sum_steps(const PagedArgs& p, int64_t* s_pre) {
     const int tid = threadIdx.x, lane = tid & 31;
-    const int chunk = (p.s.R + kThreads - 1) / kThreads;  // requests of a thread
-    int64_t sum = 0;
+    const int chunk = (p.s.R + kThreads - 1) / kThreads;
+    int64_t x = 0;
     for (int i = 0; i < chunk; ++i) {
         const int r = tid * chunk + i;
-        if (r < p.s.R) sum += Row(p, r).steps();
+        if (r < p.s.R) x += Row(p, r).steps();
     }
-    s_sum[tid] = sum;
+    x *= p.HT;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    s_pre[tid] = x;
     __syncthreads();
-    // inclusive sums of the threads' chunks, each warp for itself
-    int64_t pre[kThreads / 32], total = 0;
-#pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) {
-        int64_t x = s_sum[k * 32 + lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        pre[k] = x + total;
-        total = __shfl_sync(0xffffffffu, pre[k], 31);
-    }
-    Share w;
-    total *= p.HT;
-    w.per = max(static_cast<int64_t>(min_per), (total + workers - 1) / workers);
-    const int64_t u0 = worker * w.per;
-    w.left = static_cast<int>(max(static_cast<int64_t>(0), min(w.per, total - u0)));
-    w.base = 0;
-    w.r = 0;
-    if (w.left == 0) return w;
-    // the chunk with step u0, then the request in it
+    int64_t before = 0;
+    for (int w = 0; w < tid / 32; ++w) before += s_pre[w * 32 + 31];
+    __syncthreads();
+    s_pre[tid] = x + before;
+    __syncthreads();
+    return s_pre[kThreads - 1];
+}
+
+// The request with step u0 < total, and its first step's number.  For a whole warp.
+__device__ __forceinline__ int locate(const PagedArgs& p, const int64_t* s_pre, int64_t u0, int64_t& base) {
+    const int lane = threadIdx.x & 31, chunk = (p.s.R + kThreads - 1) / kThreads;
     int at = 0;
 #pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) {
-        const unsigned behind = __ballot_sync(0xffffffffu, pre[k] * p.HT <= u0);
-        at += __popc(behind);
-        const int n = __popc(behind);
-        if (n) w.base = __shfl_sync(0xffffffffu, pre[k], n - 1) * p.HT;
-    }
-    int r = at * chunk;
-    for (;; r += 32) {  // 32 requests at once
+    for (int k = 0; k < kThreads / 32; ++k) at += __popc(__ballot_sync(0xffffffffu, s_pre[k * 32 + lane] <= u0));
+    base = at ? s_pre[at - 1] : 0;
+    for (int r = at * chunk;; r += 32) {  // 32 requests at once
         const int mine = r + lane;
-        int64_t x = mine < p.s.R ? Row(p, mine).steps() : 0;
+        int64_t x = mine < p.s.R ? static_cast<int64_t>(Row(p, mine).steps()) * p.HT : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        const unsigned behind = __ballot_sync(0xffffffffu, w.base + x * p.HT <= u0);
-        const int n = __popc(behind);
-        const int64_t skip = n ? __shfl_sync(0xffffffffu, x, n ? n - 1 : 0) * p.HT : 0;
-        w.base += skip;
-        if (n < 32 || r + 32 >= p.s.R) {
-            w.r = min(r + n, p.s.R - 1);
-            return w;
-        }
+        const int n = __popc(__ballot_sync(0xffffffffu, base + x <= u0));
+        const int64_t skip = __shfl_sync(0xffffffffu, x, n ? n - 1 : 0);
+        if (n) base += skip;
+        if (n < 32 || r + 32 >= p.s.R) return min(r + n, p.s.R - 1);
     }
 }
 
@@ -257,26 +241,40 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
     extern __shared__ __align__(16) uint8_t sm[];
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
     const int workers = gridDim.x * kWarps, worker = blockIdx.x * kWarps + warp;
+    __shared__ int64_t s_pre[kThreads];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Share sh = find_share(p, worker, workers, min_per);
-    if (!p.direct && lane == 0) p.desc[worker] = make_int4(0, 0, 0, 0);
-    if (sh.left == 0) return;
+    const int64_t total = sum_steps(p, s_pre);
+    const int64_t per = max(static_cast<int64_t>(min_per), (total + p.max_ranges - 1) / p.max_ranges);
+    const int ranges = static_cast<int>((total + per - 1) / per);
+    if (!p.direct && lane == 0)
+        for (int i = worker; i < p.max_ranges; i += workers)
+            if (i >= ranges) p.desc[i] = make_int4(0, 0, 0, 0);
+    if (worker >= ranges) return;
+    const auto range_steps = [&](int i) { return static_cast<int>(min(per, total - i * per)); };
+    // the number of the range after this one (its lane 0 asks ahead of time)
+    const auto ask = [&]() { return p.next && lane == 0 ? workers + static_cast<int>(atomicAdd(p.next, 1u)) : INT_MAX; };
     uint8_t* ring = sm + warp * (STAGES * Ly::STAGE);
     const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     const int off_mask = (1 << p.s.log2p) - 1;
     bool bad = false;
 
-    Cursor ld(p, sh.r, static_cast<int64_t>(worker) * sh.per - sh.base);
-    Cursor cs = ld;
-    bool whole = cs.j == cs.row.j0;  // the column's first step is this warp's
+    int64_t base;
+    int range = worker, after = ask();          // the range in work; the loader's next one
+    const int row_at = locate(p, s_pre, range * per, base);
+    Cursor ld(p, row_at, range * per - base);
+    Cursor cs = ld, nx = ld;                    // nx: where the loader began its range, when it is ahead
+    int nx_range = range;
+    int n_left = range_steps(range);            // steps of the range in work
+    bool whole = cs.j == cs.row.j0;             // the column's first step is this range's
     bool first_seg = true;
+    if (!p.direct && lane == 0) p.desc[range] = make_int4(0, 0, 0, 0);
 
     const auto page_of = [&](const Cursor& c) {  // page of the lane's position (lane & 15) of a step
         const int pos = c.j * kStep + (lane & 15);
         const int at = pos >> p.s.log2p;
         return pos < c.row.len ? p.table[static_cast<int64_t>(c.r) * p.s.max_pages + at] : -1;
     };
-    int to_load = sh.left;
+    int to_load = n_left;                       // steps of the loader's range not yet copied
     int pg = page_of(ld);
     uint32_t seen[STAGES];  // positions that count, a bit each, of the steps in the ring, the current one first
 #pragma unroll
@@ -341,6 +339,17 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
             if (--to_load > 0) {
                 ld.advance(p);
                 pg = page_of(ld);
+            } else {  // on to the next range
+                const int i = __shfl_sync(0xffffffffu, after, 0);
+                if (i < ranges) {
+                    const int r = locate(p, s_pre, i * per, base);
+                    ld = Cursor(p, r, i * per - base);
+                    pg = page_of(ld);
+                    nx = ld;
+                    nx_range = i;
+                    to_load = range_steps(i);
+                    after = ask();
+                }
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -388,7 +397,7 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) seen[s] = issue(s);
     int stage = 0;
-    for (int n_left = sh.left; n_left > 0; --n_left) {
+    while (true) {
         {
             const int to = stage + STAGES - 1;
             seen[STAGES - 1] = issue(to >= STAGES ? to - STAGES : to);
@@ -610,7 +619,7 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
             const int64_t row0 = static_cast<int64_t>(cs.r) * p.s.Hq + cs.kh * p.G + h0;
             const bool done = whole && col_end;
             const int slot = first_seg ? 0 : 1;
-            float* part = p.part + (static_cast<int64_t>(worker) * 2 + slot) * kHeads * (D + 2);
+            float* part = p.part + (static_cast<int64_t>(range) * 2 + slot) * p.heads * (D + 4);
 #pragma unroll
             for (int z = 0; z < ROWS; ++z) {
                 float sum = l[z] + __shfl_xor_sync(0xffffffffu, l[z], 1);
@@ -636,8 +645,8 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
                             }
                     if (t == 0) {
                         if (!done) {
-                            part[kHeads * D + 2 * h] = m[z];
-                            part[kHeads * D + 2 * h + 1] = sum;
+                            part[p.heads * D + 2 * h] = m[z];
+                            part[p.heads * D + 2 * h + 1] = sum;
                         } else if (p.lse) {
                             p.lse[row0 + h] = (m[z] + log2f(sum)) * 0.6931471805599453f;
                         }
@@ -645,10 +654,10 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
                 }
             }
             if (lane == 0) {
-                const int col = cs.r * p.HT + cs.col(p), index = p.direct ? col : worker;
+                const int col = cs.r * p.HT + cs.col(p), index = p.direct ? col : range;
                 if (whole && !col_end) {  // first range of a split column
                     const int64_t rest = cs.row.j1 - (cs.j + 1);
-                    p.desc[index] = make_int4(worker, static_cast<int>(1 + (rest + sh.per - 1) / sh.per), slot, col);
+                    p.desc[index] = make_int4(range, static_cast<int>(1 + (rest + per - 1) / per), slot, col);
                 } else if (whole && p.direct) {
                     p.desc[index] = make_int4(0, 0, 0, 0);
                 }
@@ -657,12 +666,21 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
             if (n_left > 1) {
                 cs.advance(p);
                 whole = true;
-                clear();
-                load_q();
+            } else {
+                if (nx_range == range) break;  // the loader found no further range
+                cs = nx;
+                range = nx_range;
+                n_left = range_steps(range) + 1;
+                whole = cs.j == cs.row.j0;
+                first_seg = true;
+                if (!p.direct && lane == 0) p.desc[range] = make_int4(0, 0, 0, 0);
             }
+            clear();
+            load_q();
         } else {
             ++cs.j;
         }
+        --n_left;
         if (++stage == STAGES) stage = 0;
 #pragma unroll
         for (int s = 0; s + 1 < STAGES; ++s) seen[s] = seen[s + 1];
@@ -695,8 +713,8 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs p)
     const int each = (d.y + kWarps - 1) / kWarps, i1 = min(d.y, (warp + 1) * each);
 #pragma unroll 4
     for (int i = warp * each; i < i1; ++i) {
-        const float* part = p.part + ((static_cast<int64_t>(d.x) + i) * 2 + (i ? 0 : d.z)) * kHeads * (D + 2);
-        const float pm = part[kHeads * D + 2 * h], pl = part[kHeads * D + 2 * h + 1];
+        const float* part = p.part + ((static_cast<int64_t>(d.x) + i) * 2 + (i ? 0 : d.z)) * p.heads * (D + 4);
+        const float pm = part[p.heads * D + 2 * h], pl = part[p.heads * D + 2 * h + 1];
         float v[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = part[h * D + lane + 32 * e];
@@ -729,8 +747,10 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs p)
 
 }  // namespace
 
-// Ranges are of at least this many steps, so that few partial sums are written.
-constexpr int kMinSteps = 4;
+// Ranges are of at least kMinSteps steps, so that few partial sums are written (and
+// the loader, at most STAGES - 1 steps ahead, is never two ranges ahead), and there
+// are at most kRanges a warp.
+constexpr int kMinSteps = 6, kRanges = 4;
 
 namespace {
 
@@ -754,21 +774,30 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
     p.lse = lse;
     p.status = c.status_word;
     const int64_t cols = static_cast<int64_t>(s.R) * p.HT;
-    if (cols * ((static_cast<int64_t>(s.max_pages) << s.log2p) / kStep + 2) / workers >= INT_MAX)
-        return cudaErrorInvalidValue;  // a warp's steps are counted in 32 bits
-    p.direct = cols <= workers;
+    const int64_t most = cols * ((static_cast<int64_t>(s.max_pages) << s.log2p) / kStep + 2);  // steps at most
+    if (most / workers >= INT_MAX) return cudaErrorInvalidValue;  // a range's steps are counted in 32 bits
+    const bool single = most <= static_cast<int64_t>(workers) * kMinSteps;
+    p.max_ranges = single ? workers : workers * kRanges;
+    p.heads = std::min(p.G, kHeads);
+    p.direct = cols <= p.max_ranges;
     uint8_t* base = nullptr;
-    const size_t part = sizeof(float) * workers * 2 * kHeads * (D + 2);
-    e = scratch_alloc(c, reinterpret_cast<void**>(&base), part + sizeof(int4) * workers);
+    const size_t part = sizeof(float) * p.max_ranges * 2 * p.heads * (D + 4), desc = sizeof(int4) * p.max_ranges;
+    e = scratch_alloc(c, reinterpret_cast<void**>(&base), plan::up256(part) + desc + 16);
     if (e != cudaSuccess) return e;
     p.part = reinterpret_cast<float*>(base);
-    p.desc = reinterpret_cast<int4*>(base + part);
-    kernel<<<blocks, kThreads, Ly::SMEM, c.stream>>>(q, k, v, K, V, p, kMinSteps);
-    note_launch(2);
-    e = cudaGetLastError();
+    p.desc = reinterpret_cast<int4*>(base + plan::up256(part));
+    if (!single) {
+        p.next = reinterpret_cast<unsigned*>(base + plan::up256(part) + desc);
+        e = cudaMemsetAsync(p.next, 0, 4, c.stream);
+    }
+    if (e == cudaSuccess) {
+        kernel<<<blocks, kThreads, Ly::SMEM, c.stream>>>(q, k, v, K, V, p, kMinSteps);
+        note_launch(2);
+        e = cudaGetLastError();
+    }
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(p.direct ? cols : workers), std::min(p.G, kHeads));
+        cfg.gridDim = dim3(static_cast<unsigned>(p.direct ? cols : p.max_ranges), p.heads);
         cfg.blockDim = dim3(kThreads);
         cfg.stream = c.stream;
         cudaLaunchAttribute at[1];
