@@ -11,11 +11,16 @@
 // that fills the GPU once, whatever the lengths: each block sums up the requests'
 // step counts from their lengths on the device, so a captured call follows them.
 //
-// A warp works alone.  Each lane copies (cp.async) exactly the 16-byte pieces it
-// will use itself as matrix operands, a ring of steps ahead, so there is no
-// barrier: scores are products of the query heads (rows) with 8 keys, outputs
-// products of the weights with 16 value rows, with the contraction index and the
-// output columns in the order in which the pieces lie in memory.
+// A warp works alone, on a ring of steps of its own in shared memory that TMA fills
+// (one box of 16 rows x 128 bytes at a time, 128-byte swizzle), so blocks have no
+// barrier.  (Filled by cp.async, 16 bytes a lane, the same kernel stayed at 5.2 TB/s
+// whatever it computed: the load pipe held back the reads behind the copies.)
+// Steps that are not 16 positions of one page (a request's ends, its new row, pages
+// of fewer than 16) are copied by the lanes, each the pieces it will read.  Scores
+// are products of the query heads (rows) with 8 keys, outputs products of the
+// weights with 16 value rows; the contraction index and the output columns are in
+// such an order that a lane's operands are 16-byte pieces of the rows, read without
+// bank conflicts.
 // bf16 storage: m16n8k16; q, k, v are exact operands, the weights are fp32 and go
 // in as three bf16 terms (24 bits), so no precision is lost against fp32
 // arithmetic.  fp32 storage: m16n8k8 tf32 products of two-term splits (relative
@@ -41,6 +46,7 @@
 #include "la_common.cuh"
 #include "la_launch.h"
 #include "la_plan.h"
+#include "tc_common.cuh"
 
 namespace la {
 namespace {
@@ -50,19 +56,34 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 16;       // positions of a step
 constexpr float kSlack = 8.f;   // log2 by which a score may pass the maximum kept
 
+// A step in shared memory: 16 key rows, then 16 value rows, each as atoms of 16 rows
+// x AB bytes in which 16-byte chunk c of row r lies at chunk c ^ (r & 7) (AB = 128),
+// or c ^ (r / 2 & 3) (AB = 64).  Lane (g, t) = lane / 4, lane % 4 reads KC pieces of
+// keys g and g + 8 (chunks 2 t and 2 t + 1 of each atom; t of a 64-byte row) and NI
+// pieces of VPL values of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (chunk g of each atom).
 template <typename T, int D>
 struct Lay {
     static constexpr int ES = sizeof(T);
-    static constexpr int KC = D * ES / 64;              // 16-byte pieces of a key row per lane
-    static constexpr int VPL = D * ES >= 128 ? 16 / ES : 8 / ES;  // values of a row piece
-    static constexpr int VB = VPL * ES;                 // its bytes
-    static constexpr int NI = D / (8 * VPL);            // pieces of a value row per lane
-    static constexpr int KBYTES = 2 * KC * 512, VBYTES = 4 * NI * VB * 32;
-    static constexpr int STAGE = KBYTES + VBYTES;       // bytes of a step
-    static_assert(STAGE == 2 * kStep * D * ES, "a step");
+    static constexpr int AB = D * ES >= 128 ? 128 : 64;
+    static constexpr int ATOMS = D * ES / AB, ATOM = kStep * AB;
+    static constexpr int KC = D * ES / 64;
+    static constexpr int VB = AB / 8, VPL = VB / ES, NI = ATOMS;  // bytes and values of a value piece
+    static constexpr int HALF = ATOMS * ATOM, STAGE = 2 * HALF;   // bytes of the keys, of a step
     static constexpr int STAGES = STAGE >= 4096 ? 3 : 6;
-    static constexpr int SMEM = kWarps * STAGES * STAGE;
+    static constexpr int SMEM = kWarps * STAGES * STAGE + 1024;
     static constexpr int BLOCKS = STAGE <= 4096 ? 4 : STAGE == 8192 ? 2 : 1;  // per SM
+    // the chunk (of the whole row) and the place of the lane's key piece i in key tile n
+    static __device__ __forceinline__ int kchunk(int t, int i) { return AB == 128 ? (i / 2) * 8 + 2 * t + i % 2 : t; }
+    static __device__ __forceinline__ int kat(int g, int t, int n, int i) {
+        if constexpr (AB == 128) return (i / 2) * ATOM + (8 * n + g) * 128 + (((2 * t + i % 2) ^ g) << 4);
+        else return (8 * n + g) * 64 + ((t ^ (g >> 1 & 3)) << 4);
+    }
+    // the place of the lane's value piece i of row vrow(t, e)
+    static __device__ __forceinline__ int vrow(int t, int e) { return 2 * t + (e & 1) + 8 * (e >> 1); }
+    static __device__ __forceinline__ int vat(int g, int t, int e, int i) {
+        if constexpr (AB == 128) return HALF + i * ATOM + vrow(t, e) * 128 + ((g ^ (2 * t + (e & 1))) << 4);
+        else return HALF + vrow(t, e) * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8;
+    }
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
@@ -108,6 +129,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 struct PagedArgs {
     PagedShape s;
     int G, HT, tiles_per_kh;    // query heads a key head, columns of a request, columns of a key head
+    int tma;                    // the pools have tensor maps
     int append, direct;         // direct: descriptors by column, else by range
     int heads;                  // rows of a partial result: the column's query heads
     int max_ranges;
@@ -212,37 +234,46 @@ __device__ __forceinline__ int locate(const PagedArgs& p, const int64_t* s_pre, 
 }
 
 // fp32 scores of a step by plain products, for the step whose split products gave
-// a NaN (an infinite key or query): the lane's scores of head h (x of keys 2 t and
-// 2 t + 1 of key tile n) from the warp's pieces in the ring and the query row in memory.
+// a NaN (an infinite key or query): the lane's scores of a head (x of keys 2 t and
+// 2 t + 1 of key tile n) from the step in shared memory and the query row in memory.
 template <int D>
 __device__ __noinline__ float2 exact_scores(const uint8_t* st, const float* q, bool on, int n, float sign) {
-    constexpr int KC = Lay<float, D>::KC;
     const int t = threadIdx.x & 3;
     float x[2] = {0.f, 0.f};
-    __syncwarp();  // every lane's pieces have come
+    __syncwarp();  // every lane's copies have come
     if (on)
-        for (int e = 0; e < 2; ++e)
-            for (int c = 0; c < D; ++c)  // value c is word c % 4 of piece c / 16 of lane (key, c / 4 % 4)
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * n + 2 * t + e;
+            for (int c = 0; c < D; ++c)
                 x[e] += sign * q[c] * reinterpret_cast<const float*>(
-                                          st + (n * KC + c / 16) * 512 + ((2 * t + e) * 4 + c / 4 % 4) * 16)[c & 3];
-    __syncwarp();  // before any lane copies into this stage again
+                                          st + c / 32 * Lay<float, D>::ATOM + r * 128 + ((c / 4 % 8 ^ (r & 7)) << 4))[c & 3];
+        }
+    __syncwarp();
     return make_float2(x[0], x[1]);
 }
 
 // kHeads: 8 or 16 query heads a step.
 template <typename T, int D, int kHeads>
 __global__ void __launch_bounds__(kThreads, Lay<T, D>::BLOCKS)
-paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* __restrict__ vn, T* K, T* V,
+paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                    const T* __restrict__ q, const T* __restrict__ kn, const T* __restrict__ vn, T* K, T* V,
                     const PagedArgs p, int min_per) {
     using Ly = Lay<T, D>;
     constexpr int KC = Ly::KC, VPL = Ly::VPL, VB = Ly::VB, NI = Ly::NI, ROWS = kHeads / 8, NT = D / 8;
-    constexpr int STAGES = Ly::STAGES, KOFF = 64 / static_cast<int>(sizeof(T));  // values from piece to piece
+    constexpr int STAGES = Ly::STAGES, PE = 16 / static_cast<int>(sizeof(T));  // values of 16 bytes
     constexpr bool kBf16 = sizeof(T) == 2;
-    extern __shared__ __align__(16) uint8_t sm[];
+    extern __shared__ uint8_t sm_raw[];
+    __shared__ uint64_t s_bar[kWarps][STAGES];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
     const int workers = gridDim.x * kWarps, worker = blockIdx.x * kWarps + warp;
     __shared__ int64_t s_pre[kThreads];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    uint64_t* bar = s_bar[warp];
+    if (lane == 0) {
+        for (int s = 0; s < STAGES; ++s) tc::mbar_init(bar + s, 1);
+        tc::fence_mbar_init();
+    }
     const int64_t total = sum_steps(p, s_pre);
     const int64_t per = max(static_cast<int64_t>(min_per), (total + p.max_ranges - 1) / p.max_ranges);
     const int ranges = static_cast<int>((total + per - 1) / per);
@@ -254,7 +285,6 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
     // the number of the range after this one (its lane 0 asks ahead of time)
     const auto ask = [&]() { return p.next && lane == 0 ? workers + static_cast<int>(atomicAdd(p.next, 1u)) : INT_MAX; };
     uint8_t* ring = sm + warp * (STAGES * Ly::STAGE);
-    const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     const int off_mask = (1 << p.s.log2p) - 1;
     bool bad = false;
 
@@ -280,32 +310,29 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) seen[s] = 0;
 
-    // Copies the lane's pieces of step `ld` into a stage and moves on; returns the
-    // positions that count.
-    const T* const kbase = K + g * D + t * (16 / static_cast<int>(sizeof(T)));
-    const T* const vbase = V + 2 * t * D + g * VPL;
+    // Copies step `ld` into a stage and moves on; returns the positions that count and
+    // whether lanes copied it.
+    constexpr uint32_t kByLanes = 0x10000u;
     const auto issue = [&](int stage) -> uint32_t {
         uint32_t mask = 0xFFFFu;
         if (to_load > 0) {
-            const uint32_t kd = ring32 + stage * Ly::STAGE + lane * 16;
-            const uint32_t vd = ring32 + stage * Ly::STAGE + Ly::KBYTES + lane * VB;
+            uint8_t* dst = ring + stage * Ly::STAGE;
             const int pos0 = ld.j * kStep, page = pg;
-            const bool inside = p.s.log2p >= 4 && pos0 >= ld.row.first && pos0 + kStep <= ld.row.len &&
+            const bool inside = p.tma && pos0 >= ld.row.first && pos0 + kStep <= ld.row.len &&
                                 static_cast<unsigned>(page) < static_cast<unsigned>(p.s.num_pages);
-            if (__all_sync(0xffffffffu, inside)) {  // one page, every position the request's
-                const int64_t row = ((static_cast<int64_t>(page) * p.s.Hkv + ld.kh) << p.s.log2p) + (pos0 & off_mask);
-                const T* kr = kbase + row * D;
-                const T* vr = vbase + row * D;
+            if (__all_sync(0xffffffffu, inside)) {  // 16 positions of one page, and all lanes are done with the stage
+                if (lane == 0) {
+                    const int y = pos0 & off_mask, z = page * p.s.Hkv + ld.kh;
+                    tc::mbar_arrive_expect_tx(bar + stage, Ly::STAGE);
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < KC; ++i) cp16(kd + (n * KC + i) * 512, kr + n * 8 * D + i * KOFF, true);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        cpv<VB>(vd + (e * NI + i) * VB * 32, vr + ((e >> 1) * 8 + (e & 1)) * D + i * 8 * VPL, true);
+                    for (int a = 0; a < Ly::ATOMS; ++a) {
+                        tc::tma_load_3d(dst + a * Ly::ATOM, &kmap, bar + stage, a * 8 * PE, y, z);
+                        tc::tma_load_3d(dst + Ly::HALF + a * Ly::ATOM, &vmap, bar + stage, a * 8 * PE, y, z);
+                    }
+                }
             } else {
+                if (lane == 0) tc::mbar_arrive(bar + stage);
+                const uint32_t d32 = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
                 const int mypos = pos0 + (lane & 15), len = ld.row.len;
                 const bool mine = mypos >= ld.row.first && mypos < ld.row.total;
                 const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.s.num_pages);
@@ -323,18 +350,19 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     bool on;
-                    const T* kr = key_row(8 * n + g, K, kn, on) + t * (16 / static_cast<int>(sizeof(T)));
+                    const T* kr = key_row(8 * n + g, K, kn, on);
 #pragma unroll
-                    for (int i = 0; i < KC; ++i) cp16(kd + (n * KC + i) * 512, on ? kr + i * KOFF : q, on);
+                    for (int i = 0; i < KC; ++i)
+                        cp16(d32 + Ly::kat(g, t, n, i), on ? kr + Ly::kchunk(t, i) * PE : q, on);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     bool on;
-                    const T* vr = key_row((e >> 1) * 8 + 2 * t + (e & 1), V, vn, on) + g * VPL;
+                    const T* vr = key_row(Ly::vrow(t, e), V, vn, on);
 #pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        cpv<VB>(vd + (e * NI + i) * VB * 32, on ? vr + i * 8 * VPL : q, on);
+                    for (int i = 0; i < NI; ++i) cpv<VB>(d32 + Ly::vat(g, t, e, i), on ? vr + (g + 8 * i) * VPL : q, on);
                 }
+                mask |= kByLanes;
             }
             if (--to_load > 0) {
                 ld.advance(p);
@@ -352,7 +380,6 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
                 }
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
         return mask;
     };
 
@@ -366,13 +393,13 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
     const auto load_q = [&]() {
         const int h0 = cs.tile * kHeads;
         const int64_t row = static_cast<int64_t>(cs.r) * p.s.Hq + cs.kh * p.G + h0;
-        const T* src = q + (row + g) * D + t * (16 / static_cast<int>(sizeof(T)));
+        const T* src = q + (row + g) * D;
 #pragma unroll
         for (int z = 0; z < ROWS; ++z)
 #pragma unroll
             for (int i = 0; i < KC; ++i) {
                 uint4 u = make_uint4(0, 0, 0, 0);
-                if (h0 + 8 * z + g < p.G) u = *reinterpret_cast<const uint4*>(src + 8 * z * D + i * KOFF);
+                if (h0 + 8 * z + g < p.G) u = *reinterpret_cast<const uint4*>(src + 8 * z * D + Ly::kchunk(t, i) * PE);
                 const uint32_t w[4] = {u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -397,12 +424,22 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) seen[s] = issue(s);
     int stage = 0;
+    uint32_t phase = 0, limit = tcf::kWaitLimit;
+    bool bad_wait = false;
     while (true) {
         {
             const int to = stage + STAGES - 1;
             seen[STAGES - 1] = issue(to >= STAGES ? to - STAGES : to);
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        const bool by_lanes = seen[0] & kByLanes;
+        if (by_lanes) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            seen[0] &= 0xFFFFu;
+        }
+        if (!tc::mbar_wait(bar + stage, phase, limit)) {  // a copy never came: report it and go on
+            bad_wait = true;
+            limit = 1;
+        }
         const uint8_t* st = ring + stage * Ly::STAGE;
 
         // scores of 16 keys: s[n][2 z + e] of head g + 8 z, key 8 n + 2 t + e
@@ -413,7 +450,7 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
         for (int i = 0; i < KC; ++i) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                const uint4 k = *reinterpret_cast<const uint4*>(st + (n * KC + i) * 512 + lane * 16);
+                const uint4 k = *reinterpret_cast<const uint4*>(st + Ly::kat(g, t, n, i));
                 const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
                 for (int h = 0; h < 4; h += 2) {
@@ -503,7 +540,6 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
                 l[z] += s[n][2 * z] + s[n][2 * z + 1];
             }
         }
-        const uint8_t* vs = st + Ly::KBYTES + lane * VB;
         if constexpr (kBf16) {
             uint32_t w[3][ROWS][2];  // three terms of the weights
 #pragma unroll
@@ -524,10 +560,10 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if constexpr (VB == 16) {
-                        const uint4 f = *reinterpret_cast<const uint4*>(vs + (e * NI + i) * VB * 32);
+                        const uint4 f = *reinterpret_cast<const uint4*>(st + Ly::vat(g, t, e, i));
                         v[e][0] = f.x, v[e][1] = f.y, v[e][2] = f.z, v[e][3] = f.w;
                     } else {
-                        const uint2 f = *reinterpret_cast<const uint2*>(vs + (e * NI + i) * VB * 32);
+                        const uint2 f = *reinterpret_cast<const uint2*>(st + Ly::vat(g, t, e, i));
                         v[e][0] = f.x, v[e][1] = f.y;
                     }
                 }
@@ -563,8 +599,8 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
                     for (int e = 0; e < 2; ++e) split_tf32(__float_as_uint(s[n][2 * z + e]), wh[z][e], wl[z][e]);
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    const uint4 v0 = *reinterpret_cast<const uint4*>(vs + ((2 * n) * NI + i) * VB * 32);
-                    const uint4 v1 = *reinterpret_cast<const uint4*>(vs + ((2 * n + 1) * NI + i) * VB * 32);
+                    const uint4 v0 = *reinterpret_cast<const uint4*>(st + Ly::vat(g, t, 2 * n, i));
+                    const uint4 v1 = *reinterpret_cast<const uint4*>(st + Ly::vat(g, t, 2 * n + 1, i));
                     const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
                     uint32_t h0[4], h1[4], c0[4], c1[4];
 #pragma unroll
@@ -681,12 +717,13 @@ paged_decode_kernel(const T* __restrict__ q, const T* __restrict__ kn, const T* 
             ++cs.j;
         }
         --n_left;
-        if (++stage == STAGES) stage = 0;
+        if (by_lanes) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before TMA writes there again
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
 #pragma unroll
         for (int s = 0; s + 1 < STAGES; ++s) seen[s] = seen[s + 1];
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
     if (bad) atomicOr(p.status, kStatusBadIndex);
+    if (bad_wait) atomicOr(p.status, tcf::kErrWait);
 }
 
 // Joins the ranges of a split column, one block a query head: the maximum of the
@@ -754,6 +791,23 @@ constexpr int kMinSteps = 6, kRanges = 4;
 
 namespace {
 
+// Map over a pool [num_pages * Hkv][page_size][D] with a box of 16 rows x AB bytes.
+template <typename T, int D>
+cudaError_t pool_map(CUtensorMap* m, const void* pool, const PagedShape& s) {
+    using Ly = Lay<T, D>;
+    tcf::EncodeTiled enc = tcf::encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t page = 1ull << s.log2p;
+    cuuint64_t dims[3] = {D, page, static_cast<cuuint64_t>(s.num_pages) * s.Hkv};
+    cuuint64_t strides[2] = {D * sizeof(T), page * D * sizeof(T)};
+    cuuint32_t box[3] = {Ly::AB / sizeof(T), kStep, 1}, es[3] = {1, 1, 1};
+    const CUresult r = enc(m, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                           const_cast<void*>(pool), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           Ly::AB == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <typename T, int D, int kHeads>
 cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K, T* V, const int* table,
                    const int* lens, float* out, float* lse, const PagedShape& s) {
@@ -773,6 +827,10 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
     p.out = out;
     p.lse = lse;
     p.status = c.status_word;
+    CUtensorMap kmap = {}, vmap = {};
+    p.tma = s.log2p >= 4 && s.num_pages > 0 && static_cast<int64_t>(s.num_pages) * s.Hkv < INT_MAX;
+    if (p.tma && ((e = pool_map<T, D>(&kmap, K, s)) != cudaSuccess || (e = pool_map<T, D>(&vmap, V, s)) != cudaSuccess))
+        return e;
     const int64_t cols = static_cast<int64_t>(s.R) * p.HT;
     const int64_t most = cols * ((static_cast<int64_t>(s.max_pages) << s.log2p) / kStep + 2);  // steps at most
     if (most / workers >= INT_MAX) return cudaErrorInvalidValue;  // a range's steps are counted in 32 bits
@@ -791,7 +849,7 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
         e = cudaMemsetAsync(p.next, 0, 4, c.stream);
     }
     if (e == cudaSuccess) {
-        kernel<<<blocks, kThreads, Ly::SMEM, c.stream>>>(q, k, v, K, V, p, kMinSteps);
+        kernel<<<blocks, kThreads, Ly::SMEM, c.stream>>>(kmap, vmap, q, k, v, K, V, p, kMinSteps);
         note_launch(2);
         e = cudaGetLastError();
     }
