@@ -11,9 +11,8 @@
 //
 // The kernels are bound by memory: every element is read once and written once
 // (forward 2 streams in, 1 out; backward 3 in, 2 out).  A tile is 128 rows x 128
-// bytes of a row, worked by 128 threads; a thread owns 8 rows x 16 bytes, copied
-// by cp.async into shared memory slots of its own (no barrier between copy and
-// use), one tile ahead.  Per tile: each thread sums its 8 rows up to (A, B);
+// bytes of a row, filled by TMA and worked by 128 threads; a thread owns 8 rows x 16
+// bytes.  Per tile: each thread sums its 8 rows up to (A, B);
 // one thread per channel folds the 16 row groups, gets the state that enters the
 // tile from the tile before (below), and hands each row group its state; then
 // each thread runs its rows and writes them.
@@ -78,21 +77,12 @@ struct Args {
     unsigned* status;
 };
 
-__device__ __forceinline__ void cp16(void* dst, const void* src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-                 "l"(src), "r"(on ? 16 : 0)
-                 : "memory");
-}
 __device__ __forceinline__ void cp4(void* dst, const void* src, bool on) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
                      static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
                  "l"(src), "r"(on ? 4 : 0)
                  : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // A thread's 16 bytes as fp32 values, and back (round to nearest even).
 __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -151,38 +141,61 @@ __device__ __forceinline__ Place place_of(const Args<T>& p, unsigned tile) {
     return q;
 }
 
-// Copies a tile's streams into the thread's slots of a stage.  kVec: rows are
-// 16-byte aligned and a thread's channels are consecutive; otherwise the
-// channels lane, lane + 8, ... are copied one by one.
+// Tensor maps of the streams (A, X, dOut) for rows that are 16-byte aligned.
+struct Maps {
+    CUtensorMap m[3];
+};
+
+// A thread's 16 bytes of row r of its row group in stream s of a stage.
+template <int s>
+__device__ __forceinline__ uint4& piece(uint4* stage, int r) {
+    return stage[s * TILE * LANES + (static_cast<int>(threadIdx.x) / LANES * R + r) * LANES + threadIdx.x % LANES];
+}
+
+// Copies a tile's streams into a stage.  kVec: by TMA, a box of 128 rows x 128 bytes
+// a stream, which thread 0 asks for when all threads are done with the stage (values
+// past N and C come as 0).  Otherwise each thread copies what it will use itself,
+// the channels lane, lane + 8, ... of its rows one by one.
 template <typename T, bool kVec, int STREAMS>
-__device__ __forceinline__ void issue(const Args<T>& p, const Place& q, uint4* stage) {
+__device__ __forceinline__ void issue(const Args<T>& p, const Maps& maps, const Place& q, uint4* stage,
+                                      uint64_t* bar) {
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
     const int tid = threadIdx.x, lane = tid % LANES, rg = tid / LANES;
-    const T* src[3] = {p.A, p.X, p.G};
-    const int t0 = q.k * TILE + rg * R, c0 = q.cb * CB + (kVec ? lane * VEC : lane);
-    const int64_t at = (static_cast<int64_t>(q.b) * p.N + t0) * p.C + c0;
+    if constexpr (kVec) {
+        if (tid == 0) {
+            tc::mbar_arrive_expect_tx(bar, STREAMS * TILE * LANES * 16);
 #pragma unroll
-    for (int s = 0; s < STREAMS; ++s) {
-        const T* from = src[s] + at;
+            for (int s = 0; s < STREAMS; ++s)
+                tc::tma_load_3d(stage + s * TILE * LANES, &maps.m[s], bar, q.cb * CB, q.k * TILE, q.b);
+        }
+    } else {
+        const T* src[3] = {p.A, p.X, p.G};
+        const int t0 = q.k * TILE + rg * R, c0 = q.cb * CB + lane;
+        const int64_t at = (static_cast<int64_t>(q.b) * p.N + t0) * p.C + c0;
 #pragma unroll
-        for (int r = 0; r < R; ++r, from += p.C) {
-            uint4* slot = stage + (s * R + r) * NT + tid;
-            const bool row = t0 + r < p.N;
-            if constexpr (kVec) {
-                const bool in = row && c0 < p.C;
-                cp16(slot, in ? from : src[s], in);
-            } else {
+        for (int s = 0; s < STREAMS; ++s) {
+            const T* from = src[s] + at;
+#pragma unroll
+            for (int r = 0; r < R; ++r, from += p.C) {
+                T* slot = reinterpret_cast<T*>(stage + s * TILE * LANES + (rg * R + r) * LANES + lane);
+                const bool row = t0 + r < p.N;
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     const bool in = row && c0 + LANES * v < p.C;
-                    T* e = reinterpret_cast<T*>(slot) + v;
-                    if constexpr (sizeof(T) == 4) cp4(e, in ? from + LANES * v : src[s], in);
-                    else *e = in ? from[LANES * v] : from_f<T>(0.f);
+                    if constexpr (sizeof(T) == 4) cp4(slot + v, in ? from + LANES * v : src[s], in);
+                    else slot[v] = in ? from[LANES * v] : from_f<T>(0.f);
                 }
             }
         }
     }
-    cp_commit();
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ void landed(const Args<T>& p, uint64_t* bar, uint32_t phase) {
+    if constexpr (kVec) {
+        if (!tc::mbar_wait(bar, phase, tcf::kWaitLimit)) atomicOr(p.status, tcf::kErrWait);
+    } else {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
 }
 
 template <typename T, bool kVec>
@@ -392,9 +405,9 @@ __device__ __forceinline__ bool fold(const float* a, const float* b, const unsig
 }
 
 template <typename T, bool kLogit, bool kPacked, bool kVec>
-__global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 : FWD_BLOCKS) scan_forward_kernel(const Args<T> p) {
+__global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 : FWD_BLOCKS) scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
-    extern __shared__ __align__(16) uint8_t sm[];
+    extern __shared__ __align__(128) uint8_t sm[];
     uint4* stages = reinterpret_cast<uint4*>(sm);
     float* sa = reinterpret_cast<float*>(stages + FWD_STAGES * 2 * R * NT);
     float* sb = sa + RG * CB;
@@ -403,6 +416,14 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
     unsigned* snext = grp + (kPacked ? RG : 0);
     const int tid = threadIdx.x, rg = tid / LANES;
 
+    __shared__ uint64_t bars[2];
+    uint32_t phase = 0;
+    if (kVec && tid == 0) {
+        tc::mbar_init(bars, 1);
+        tc::mbar_init(bars + 1, 1);
+        tc::fence_mbar_init();
+    }
+    __syncthreads();
     unsigned tile = blockIdx.x;
     if (p.ticket) {
         if (tid == 0) *snext = atomicAdd(p.ticket, 1u) + 1u;
@@ -410,7 +431,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
         tile = *snext;
         __syncthreads();
     }
-    if (tile < p.total) issue<T, kVec, 2>(p, place_of<T, false>(p, tile), stages);
+    if (tile < p.total) issue<T, kVec, 2>(p, maps, place_of<T, false>(p, tile), stages, bars);
     for (int st = 0; tile < p.total; st ^= 1) {
         const Place q = place_of<T, false>(p, tile);
         uint4* stage = stages + (FWD_STAGES > 1 ? st : 0) * (2 * R * NT);
@@ -421,7 +442,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
         const bool on = tid < CB && c < p.C;  // this thread has a channel of the chain
         const int64_t at = static_cast<int64_t>(q.b) * p.tiles * p.C + c;
         const unsigned first = on && q.k ? ld_relaxed(p.incl + at + static_cast<int64_t>(q.k - 1) * p.C) : 0u;
-        cp_wait_all();
+        landed<T, kVec>(p, bars + (FWD_STAGES > 1 ? st : 0), phase);
         // The thread's rows as one map (A, B); rows past N change nothing.
         float s[kLogit ? R : 1][VEC];
         float A[VEC], Bv[VEC];
@@ -430,8 +451,8 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float a[VEC], x[VEC];
-            unpack(stage[r * NT + tid], a);
-            unpack(stage[(R + r) * NT + tid], x);
+            unpack(piece<0>(stage, r), a);
+            unpack(piece<1>(stage, r), x);
             if constexpr (kLogit) {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) s[r][v] = sigmoid(a[v]);
@@ -456,8 +477,8 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
         if (tid == 0) *snext = mine;
         __syncthreads();
         const unsigned next = *snext;
-        if (FWD_STAGES > 1 && next < p.total)
-            issue<T, kVec, 2>(p, place_of<T, false>(p, next), stages + (st ^ 1) * (2 * R * NT));
+        if (FWD_STAGES > 1 && next < p.total)  // every thread is done with the tile before
+            issue<T, kVec, 2>(p, maps, place_of<T, false>(p, next), stages + (st ^ 1) * (2 * R * NT), bars + (st ^ 1));
         if (on) {
             const bool last = q.k + 1 == p.tiles;
             float At, Bt, h = 0.f;
@@ -484,8 +505,8 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
             for (int r = 0; r < R; ++r) {
                 if (t0 + r >= p.N) break;
                 float a[VEC], x[VEC];
-                unpack(stage[r * NT + tid], a);
-                unpack(stage[(R + r) * NT + tid], x);
+                unpack(piece<0>(stage, r), a);
+                unpack(piece<1>(stage, r), x);
                 const int w = kPacked ? info[rg * R + r] : 0, o = w & kOwner;
                 if (kPacked && (w & kBegin))
                     load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr, p,
@@ -500,8 +521,10 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
                     save_state<T, kVec>(p.fin + static_cast<int64_t>(o) * p.C, p, q, h);
             }
         }
-        if (FWD_STAGES == 1 && next < p.total) issue<T, kVec, 2>(p, place_of<T, false>(p, next), stages);
-        if constexpr (kPacked) __syncthreads();  // info is rewritten for the next tile
+        if (kPacked || (kVec && FWD_STAGES == 1)) __syncthreads();  // the stage and info are free
+        if (FWD_STAGES == 1 && next < p.total)
+            issue<T, kVec, 2>(p, maps, place_of<T, false>(p, next), stages, bars);
+        if (FWD_STAGES == 1 || st) phase ^= 1u;
         tile = next;
     }
 }
@@ -509,9 +532,9 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
 // Backward: the forward state enters each tile from its checkpoint (no chain);
 // the carry c comes down the chain from the last tile.
 template <typename T, bool kLogit, bool kPacked, bool kVec>
-__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS + 1) scan_backward_kernel(const Args<T> p) {
+__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS + 1) scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
-    extern __shared__ __align__(16) uint8_t sm[];
+    extern __shared__ __align__(128) uint8_t sm[];
     uint4* stages = reinterpret_cast<uint4*>(sm);
     float* sa = reinterpret_cast<float*>(stages + BWD_STAGES * 3 * R * NT);
     float* sb = sa + RG * CB;
@@ -521,6 +544,14 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
     unsigned* snext = grp + (kPacked ? RG : 0);
     const int tid = threadIdx.x, rg = tid / LANES;
 
+    __shared__ uint64_t bars[2];
+    uint32_t phase = 0;
+    if (kVec && tid == 0) {
+        tc::mbar_init(bars, 1);
+        tc::mbar_init(bars + 1, 1);
+        tc::fence_mbar_init();
+    }
+    __syncthreads();
     unsigned tile = blockIdx.x;
     if (p.ticket) {
         if (tid == 0) *snext = atomicAdd(p.ticket, 1u) + 1u;
@@ -528,7 +559,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
         tile = *snext;
         __syncthreads();
     }
-    if (tile < p.total) issue<T, kVec, 3>(p, place_of<T, true>(p, tile), stages);
+    if (tile < p.total) issue<T, kVec, 3>(p, maps, place_of<T, true>(p, tile), stages, bars);
     for (int st = 0; tile < p.total; st ^= 1) {
         const Place q = place_of<T, true>(p, tile);
         uint4* stage = stages + (BWD_STAGES > 1 ? st : 0) * (3 * R * NT);
@@ -542,7 +573,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
         float h0 = 0.f;  // the state that enters the tile
         if (on && q.k) h0 = p.states[at + static_cast<int64_t>(q.k - 1) * p.C];
         else if (on && !kPacked && p.h_init) h0 = p.h_init[static_cast<int64_t>(q.b) * p.C + c];
-        cp_wait_all();
+        landed<T, kVec>(p, bars + (BWD_STAGES > 1 ? st : 0), phase);
         float s[kLogit ? R : 1][VEC];
         float A[VEC], Bf[VEC], Br[VEC];
 #pragma unroll
@@ -552,9 +583,9 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float a[VEC], x[VEC], g[VEC];
-            unpack(stage[r * NT + tid], a);
-            unpack(stage[(R + r) * NT + tid], x);
-            if constexpr (!kPacked) unpack(stage[(2 * R + r) * NT + tid], g);
+            unpack(piece<0>(stage, r), a);
+            unpack(piece<1>(stage, r), x);
+            if constexpr (!kPacked) unpack(piece<2>(stage, r), g);
             if constexpr (kLogit) {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) s[r][v] = sigmoid(a[v]);
@@ -581,8 +612,8 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
                 if (t0 + r < p.N) {
                     const int w = info[rg * R + r], o = w & kOwner;
                     float a[VEC], g[VEC];
-                    unpack(stage[r * NT + tid], a);
-                    unpack(stage[(2 * R + r) * NT + tid], g);
+                    unpack(piece<0>(stage, r), a);
+                    unpack(piece<2>(stage, r), g);
                     if (w & kEnd)
                         load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr,
                                             p, q, Br);
@@ -597,8 +628,8 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
         if (tid == 0) *snext = mine;
         __syncthreads();
         const unsigned next = *snext;
-        if (BWD_STAGES > 1 && next < p.total)
-            issue<T, kVec, 3>(p, place_of<T, true>(p, next), stages + (st ^ 1) * (3 * R * NT));
+        if (BWD_STAGES > 1 && next < p.total)  // every thread is done with the tile before
+            issue<T, kVec, 3>(p, maps, place_of<T, true>(p, next), stages + (st ^ 1) * (3 * R * NT), bars + (st ^ 1));
         if (on) {
             const bool last = q.k == 0;
             float At, Bt, y = 0.f, h = h0;
@@ -631,8 +662,8 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float a[VEC], x[VEC];
-            unpack(stage[r * NT + tid], a);
-            unpack(stage[(R + r) * NT + tid], x);
+            unpack(piece<0>(stage, r), a);
+            unpack(piece<1>(stage, r), x);
             if constexpr (kPacked) {
                 const int w = info[rg * R + r], o = w & kOwner;
                 if (w & kBegin)
@@ -650,9 +681,9 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
         for (int r = R - 1; r >= 0; --r) {
             if (t0 + r < p.N) {
                 float a[VEC], x[VEC], g[VEC];
-                unpack(stage[r * NT + tid], a);
-                unpack(stage[(R + r) * NT + tid], x);
-                unpack(stage[(2 * R + r) * NT + tid], g);
+                unpack(piece<0>(stage, r), a);
+                unpack(piece<1>(stage, r), x);
+                unpack(piece<2>(stage, r), g);
                 const int w = kPacked ? info[rg * R + r] : 0, o = w & kOwner;
                 if (kPacked && (w & kEnd))
                     load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr, p,
@@ -674,8 +705,10 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
                     save_state<T, kVec>(p.fin + static_cast<int64_t>(o) * p.C, p, q, y);
             }
         }
-        if (BWD_STAGES == 1 && next < p.total) issue<T, kVec, 3>(p, place_of<T, true>(p, next), stages);
-        if constexpr (kPacked) __syncthreads();  // info is rewritten for the next tile
+        if (kPacked || (kVec && BWD_STAGES == 1)) __syncthreads();  // the stage and info are free
+        if (BWD_STAGES == 1 && next < p.total)
+            issue<T, kVec, 3>(p, maps, place_of<T, true>(p, next), stages, bars);
+        if (BWD_STAGES == 1 || st) phase ^= 1u;
         tile = next;
     }
 }

@@ -32,6 +32,21 @@ cudaError_t resident_blocks(K kernel, size_t smem, int num_sms, int* blocks) {
     return e;
 }
 
+// Map over a [B][N][C] tensor with a box of 128 rows x 128 bytes.
+template <typename T>
+cudaError_t stream_map(CUtensorMap* m, const T* base, int B, int N, int C) {
+    tcf::EncodeTiled enc = tcf::encoder();
+    if (!enc) return cudaErrorNotSupported;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(C), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(B)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(C) * sizeof(T), static_cast<cuuint64_t>(N) * C * sizeof(T)};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(Geo<T>::CB), TILE, 1}, es[3] = {1, 1, 1};
+    const CUresult r = enc(m, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                           const_cast<T*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // One pass along the rows (forward, or the backward's carry).  `own_incl` is
 // true when the pass keeps its chain's end states in scratch.
 template <typename T, bool kBwd>
@@ -46,6 +61,11 @@ cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl) {
     a.ncb = static_cast<int>(ncb);
     a.total = static_cast<unsigned>(a.B * tiles * ncb);
     a.status = c.status_word;
+
+    Maps maps = {};
+    const T* streams[3] = {a.A, a.X, a.G};
+    for (int i = 0; vec && i < STREAMS; ++i)
+        if (cudaError_t m = stream_map<T>(&maps.m[i], streams[i], a.B, a.N, a.C)) return m;
 
     const Parts s = parts_of(a.B, a.N, a.C, packed, own_incl);
     uint8_t* base = nullptr;
@@ -74,7 +94,7 @@ cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl) {
         int blocks = 1;
         if (e == cudaSuccess) e = resident_blocks(kernel, smem, c.num_sms, &blocks);
         if (e != cudaSuccess) return;
-        kernel<<<std::min<unsigned>(a.total, blocks), NT, smem, c.stream>>>(a);
+        kernel<<<std::min<unsigned>(a.total, blocks), NT, smem, c.stream>>>(a, maps);
         note_launch();
         e = cudaGetLastError();
     };

@@ -53,6 +53,7 @@ namespace {
 
 constexpr int kWarps = 4;       // warps of a block
 constexpr int kThreads = 32 * kWarps;
+constexpr int kJoinWarps = 8;   // warps of a block of the joining kernel
 constexpr int kStep = 16;       // positions of a step
 constexpr float kSlack = 8.f;   // log2 by which a score may pass the maximum kept
 
@@ -125,6 +126,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&p);
 }
+
+// Ranges: up to kRanges a warp, so that warps that run ahead take more of them
+// (690 us against 700 us with 2, 256 x 16 x 4096 x 64), but below kLongRange steps
+// only two a warp, since each range may leave partial sums (95 us against 105 us at
+// 6 x 4 key heads of up to 65535 positions, D = 128), and not below kMinSteps (the
+// loader, at most STAGES - 1 steps ahead, is then never two ranges ahead).  Calls
+// that cannot give every warp kMinSteps steps take one range a warp (9.6 us with 1 step at least, 11.5 us
+// with 2, at 4 x 4 key heads of up to 300 positions).
+constexpr int kRanges = 4, kLongRange = 32, kMinSteps = 6, kMinSingle = 1;
 
 struct PagedArgs {
     PagedShape s;
@@ -275,7 +285,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         tc::fence_mbar_init();
     }
     const int64_t total = sum_steps(p, s_pre);
-    const int64_t per = max(static_cast<int64_t>(min_per), (total + p.max_ranges - 1) / p.max_ranges);
+    const int64_t two = (total + 2 * workers - 1) / (2 * workers);  // steps of a range with two a warp
+    const int64_t per = max(max(static_cast<int64_t>(min_per), min(two, static_cast<int64_t>(kLongRange))),
+                            (total + p.max_ranges - 1) / p.max_ranges);
     const int ranges = static_cast<int>((total + per - 1) / per);
     if (!p.direct && lane == 0)
         for (int i = worker; i < p.max_ranges; i += workers)
@@ -730,8 +742,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 // ranges' maxima, then sums scaled to it, in the order of the ranges within each
 // of the block's warps and of the warps.
 template <int D, int kHeads>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs p) {
-    __shared__ float s_m[kWarps], s_l[kWarps], s_a[kWarps][D];
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedArgs p) {
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_a[kJoinWarps][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t index = blockIdx.x;
     const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -747,8 +759,8 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs p)
     float m = -INFINITY, l = 0.f, a[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) a[e] = 0.f;
-    const int each = (d.y + kWarps - 1) / kWarps, i1 = min(d.y, (warp + 1) * each);
-#pragma unroll 4
+    const int each = (d.y + kJoinWarps - 1) / kJoinWarps, i1 = min(d.y, (warp + 1) * each);
+#pragma unroll 8
     for (int i = warp * each; i < i1; ++i) {
         const float* part = p.part + ((static_cast<int64_t>(d.x) + i) * 2 + (i ? 0 : d.z)) * p.heads * (D + 4);
         const float pm = part[p.heads * D + 2 * h], pl = part[p.heads * D + 2 * h + 1];
@@ -767,12 +779,12 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs p)
     for (int e = 0; e < E; ++e) s_a[warp][lane + 32 * e] = a[e];
     __syncthreads();
     const int64_t row = r * p.s.Hq + kh * p.G + h0 + h;
-    for (int i = threadIdx.x; i < D; i += kThreads) {
+    for (int i = threadIdx.x; i < D; i += kJoinWarps * 32) {
         float x = -INFINITY, tl = 0.f, ta = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) x = fmaxf(x, s_m[w]);
+        for (int w = 0; w < kJoinWarps; ++w) x = fmaxf(x, s_m[w]);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kJoinWarps; ++w) {
             const float f = s_m[w] == -INFINITY ? (s_l[w] != s_l[w] ? 1.f : 0.f) : s_m[w] == x ? 1.f : ex2(s_m[w] - x);
             tl += s_l[w] * f;
             ta += s_a[w][i] * f;
@@ -783,11 +795,6 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs p)
 }
 
 }  // namespace
-
-// Ranges are of at least kMinSteps steps, so that few partial sums are written (and
-// the loader, at most STAGES - 1 steps ahead, is never two ranges ahead), and there
-// are at most kRanges a warp.
-constexpr int kMinSteps = 6, kRanges = 4;
 
 namespace {
 
@@ -849,14 +856,14 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
         e = cudaMemsetAsync(p.next, 0, 4, c.stream);
     }
     if (e == cudaSuccess) {
-        kernel<<<blocks, kThreads, Ly::SMEM, c.stream>>>(kmap, vmap, q, k, v, K, V, p, kMinSteps);
+        kernel<<<blocks, kThreads, Ly::SMEM, c.stream>>>(kmap, vmap, q, k, v, K, V, p, single ? kMinSingle : kMinSteps);
         note_launch(2);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(p.direct ? cols : p.max_ranges), p.heads);
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(kJoinWarps * 32);
         cfg.stream = c.stream;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
