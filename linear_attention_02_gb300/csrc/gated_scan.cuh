@@ -141,9 +141,10 @@ __device__ __forceinline__ Place place_of(const Args<T>& p, unsigned tile) {
     return q;
 }
 
-// Tensor maps of the streams (A, X, dOut) for rows that are 16-byte aligned.
+// Tensor maps of the streams (A, X, dOut) and outputs (Out; dA, dX) for rows that are
+// 16-byte aligned.
 struct Maps {
-    CUtensorMap m[3];
+    CUtensorMap m[3], o[2];
 };
 
 // A thread's 16 bytes of row r of its row group in stream s of a stage.
@@ -165,8 +166,10 @@ __device__ __forceinline__ void issue(const Args<T>& p, const Maps& maps, const 
         if (tid == 0) {
             tc::mbar_arrive_expect_tx(bar, STREAMS * TILE * LANES * 16);
 #pragma unroll
-            for (int s = 0; s < STREAMS; ++s)
+            for (int s = STREAMS - 1; s >= 0; --s) {
+                if (s == STREAMS - 2) tc::tma_store_wait_read();  // outputs leave from the other slots
                 tc::tma_load_3d(stage + s * TILE * LANES, &maps.m[s], bar, q.cb * CB, q.k * TILE, q.b);
+            }
         }
     } else {
         const T* src[3] = {p.A, p.X, p.G};
@@ -516,17 +519,24 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
                     const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
                     h[v] = fmaf(d, h[v], added<kLogit>(d, x[v]));
                 }
-                if (p.O && (!kPacked || o != kOwner)) store_row<T, kVec>(p.O, p, q, t0 + r, h);
+                if (kVec && !kPacked) piece<0>(stage, r) = pack(h);
+                else if (p.O && (!kPacked || o != kOwner)) store_row<T, kVec>(p.O, p, q, t0 + r, h);
                 if (kPacked && (w & kEnd) && o != kOwner && p.fin)
                     save_state<T, kVec>(p.fin + static_cast<int64_t>(o) * p.C, p, q, h);
             }
         }
-        if (kPacked || (kVec && FWD_STAGES == 1)) __syncthreads();  // the stage and info are free
+        if (kVec && !kPacked && p.O) tc::fence_proxy_async();
+        if (kPacked || kVec) __syncthreads();  // the stage and info are free
+        if (kVec && !kPacked && p.O && tid == 0) {
+            tc::tma_store_3d(&maps.o[0], stage, q.cb * CB, q.k * TILE, q.b);
+            tc::tma_store_commit();
+        }
         if (FWD_STAGES == 1 && next < p.total)
             issue<T, kVec, 2>(p, maps, place_of<T, false>(p, next), stages, bars);
         if (FWD_STAGES == 1 || st) phase ^= 1u;
         tile = next;
     }
+    if (kVec && !kPacked && tid == 0) tc::tma_store_wait_read();  // the block's memory outlives its outputs
 }
 
 // Backward: the forward state enters each tile from its checkpoint (no chain);
@@ -697,7 +707,10 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
                     da[v] = kLogit ? d * dx[v] * (hp[r][v] - x[v]) : tot * hp[r][v];
                     y[v] = d * tot;
                 }
-                if (!kPacked || o != kOwner) {
+                if constexpr (kVec && !kPacked) {
+                    piece<0>(stage, r) = pack(da);
+                    piece<1>(stage, r) = pack(dx);
+                } else if (!kPacked || o != kOwner) {
                     store_row<T, kVec>(p.dA, p, q, t0 + r, da);
                     store_row<T, kVec>(p.dX, p, q, t0 + r, dx);
                 }
@@ -705,12 +718,19 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
                     save_state<T, kVec>(p.fin + static_cast<int64_t>(o) * p.C, p, q, y);
             }
         }
-        if (kPacked || (kVec && BWD_STAGES == 1)) __syncthreads();  // the stage and info are free
+        if (kVec && !kPacked) tc::fence_proxy_async();
+        if (kPacked || kVec) __syncthreads();  // the stage and info are free
+        if (kVec && !kPacked && tid == 0) {
+            tc::tma_store_3d(&maps.o[0], stage, q.cb * CB, q.k * TILE, q.b);
+            tc::tma_store_3d(&maps.o[1], stage + TILE * LANES, q.cb * CB, q.k * TILE, q.b);
+            tc::tma_store_commit();
+        }
         if (BWD_STAGES == 1 && next < p.total)
             issue<T, kVec, 3>(p, maps, place_of<T, true>(p, next), stages, bars);
         if (BWD_STAGES == 1 || st) phase ^= 1u;
         tile = next;
     }
+    if (kVec && !kPacked && tid == 0) tc::tma_store_wait_read();  // the block's memory outlives its outputs
 }
 
 // Packed calls: each tile's first boundary, the states of empty sequences

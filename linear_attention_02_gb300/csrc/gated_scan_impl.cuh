@@ -66,6 +66,9 @@ cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl) {
     const T* streams[3] = {a.A, a.X, a.G};
     for (int i = 0; vec && i < STREAMS; ++i)
         if (cudaError_t m = stream_map<T>(&maps.m[i], streams[i], a.B, a.N, a.C)) return m;
+    const T* outs[2] = {kBwd ? a.dA : a.O, a.dX};
+    for (int i = 0; vec && !packed && i < 2; ++i)
+        if (cudaError_t m = outs[i] ? stream_map<T>(&maps.o[i], outs[i], a.B, a.N, a.C) : cudaSuccess) return m;
 
     const Parts s = parts_of(a.B, a.N, a.C, packed, own_incl);
     uint8_t* base = nullptr;
