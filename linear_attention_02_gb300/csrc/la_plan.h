@@ -117,6 +117,11 @@ inline size_t poly2_tc_scratch(int BH, int N) {
     return sizeof(float) * static_cast<size_t>(BH) * N * (64 + 16);
 }
 
+// Page map: requests whose running sums a block keeps in shared memory; with more,
+// they lie in scratch.
+constexpr int kMapShared = 4096;
+inline size_t page_map_scratch(int R) { return R <= kMapShared ? 0 : 8 * (static_cast<size_t>(R) + 1); }
+
 // Rows between two state checkpoints of the gated scan.
 constexpr int kScanTile = 128;
 

@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 
 #include "la_common.cuh"
@@ -16,7 +17,8 @@
 namespace la {
 namespace {
 
-constexpr int kMapThreads = 1024;
+constexpr int kMapThreads = 256;
+constexpr int kMapShared = plan::kMapShared;
 
 // One request's lengths made valid: cached and new positions that fit a table
 // row of `cap` positions; `rows` keeps the given count of new rows.
@@ -37,54 +39,137 @@ struct Request {
     }
 };
 
-__global__ void __launch_bounds__(kMapThreads)
-page_map_kernel(const int* __restrict__ cached, const int* __restrict__ fresh, int R,
-                const int* __restrict__ free_pages, int num_free, int log2p, int num_pages,
-                int* __restrict__ table, int max_pages, int* __restrict__ slots, int max_tokens,
-                int* __restrict__ starts, int* __restrict__ counts, unsigned* status) {
-    __shared__ int64_t s_tok, s_page;
+struct MapArgs {
+    const int *cached, *fresh, *free_pages;
+    int R, num_free, log2p, num_pages, max_pages, max_tokens;
+    int *table, *slots, *starts, *counts;
+    int2* sums;  // [R + 1] running sums (rows, pages) in memory, for more than kMapShared requests
+    unsigned* status;
+};
+
+__device__ __forceinline__ int clamp_int(int64_t x) { return static_cast<int>(min(x, static_cast<int64_t>(INT_MAX))); }
+
+// Running sums of new rows and of wanted pages before every request, and after the
+// last: sums[0 .. R], cut to INT_MAX.  Returns whether a request's lengths are bad.
+template <int NT>
+__device__ __forceinline__ bool map_sums(const MapArgs& p, int2* sums) {
+    __shared__ int64_t s_row[NT / 32], s_page[NT / 32];
+    const int tid = threadIdx.x, lane = tid & 31, each = (p.R + NT - 1) / NT, r0 = tid * each;
     bool bad = false;
-    if (threadIdx.x == 0) s_tok = s_page = 0;
-    __syncthreads();
-    for (int r = 0; r < R; ++r) {
-        const Request q(cached[r], fresh[r], log2p, max_pages);
+    int64_t rows = 0, pages = 0;
+    for (int i = 0; i < each; ++i) {
+        if (r0 + i >= p.R) break;
+        const Request q(p.cached[r0 + i], p.fresh[r0 + i], p.log2p, p.max_pages);
         bad |= q.bad;
-        const int64_t tok = s_tok, pg = s_page;
-        if (threadIdx.x == 0) starts[r] = static_cast<int>(min(tok, static_cast<int64_t>(INT_MAX)));
-        for (int i = threadIdx.x; i < q.need; i += kMapThreads) {
-            int id = pg + i < num_free ? free_pages[pg + i] : -1;
-            if (id < 0 || id >= num_pages) id = -1, bad = true;
-            table[static_cast<int64_t>(r) * max_pages + q.old_pages + i] = id;
+        rows += q.rows;
+        pages += q.need;
+    }
+    int64_t a = rows, b = pages;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) a += x, b += y;
+    }
+    if (lane == 31) s_row[tid / 32] = a, s_page[tid / 32] = b;
+    __syncthreads();
+    a -= rows;
+    b -= pages;
+    for (int w = 0; w < tid / 32; ++w) a += s_row[w], b += s_page[w];
+    for (int i = 0; i < each; ++i) {
+        if (r0 + i >= p.R) break;
+        sums[r0 + i] = make_int2(clamp_int(a), clamp_int(b));
+        const Request q(p.cached[r0 + i], p.fresh[r0 + i], p.log2p, p.max_pages);
+        a += q.rows;
+        b += q.need;
+    }
+    if (tid == NT - 1) {  // its sums end after the last request, whether it has any or not
+        int64_t x = 0, y = 0;
+        for (int w = 0; w < NT / 32; ++w) x += s_row[w], y += s_page[w];
+        sums[p.R] = make_int2(clamp_int(x), clamp_int(y));
+    }
+    return bad;
+}
+
+// Fills the outputs from the running sums: rows, opened pages and requests in turn
+// over all threads; a row or page finds its request by bisection.
+__device__ __forceinline__ bool map_fill(const MapArgs& p, const int2* sums) {
+    const int id = blockIdx.x * kMapThreads + threadIdx.x, all = gridDim.x * kMapThreads;
+    const int rows = sums[p.R].x, pages = sums[p.R].y, mask = (1 << p.log2p) - 1;
+    bool bad = rows > p.max_tokens;
+    const auto find = [&](int i, bool by_page) {  // last request whose sum before it is <= i
+        int lo = 0, hi = p.R;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            const int2 s = sums[mid];
+            if ((by_page ? s.y : s.x) <= i) lo = mid;
+            else hi = mid;
         }
-        for (int j = threadIdx.x; j < q.rows; j += kMapThreads) {
-            if (tok + j >= max_tokens) {
-                bad = true;
-                break;
-            }
-            int slot = -1;
-            if (j < q.fit) {
+        return lo;
+    };
+    const auto free_page = [&](int i) {  // -1 where there is none
+        const int f = i < p.num_free ? p.free_pages[i] : -1;
+        return static_cast<unsigned>(f) < static_cast<unsigned>(p.num_pages) ? f : -1;
+    };
+    // four rows a thread, with one look for their first request
+    for (int64_t i0 = 4 * static_cast<int64_t>(id); i0 < p.max_tokens; i0 += 4 * static_cast<int64_t>(all)) {
+        const int n = min(4, p.max_tokens - static_cast<int>(i0));
+        int out[4] = {-1, -1, -1, -1};
+        if (i0 < rows) {
+            int r = find(static_cast<int>(i0), false), end = sums[r + 1].x;
+            Request q(p.cached[r], p.fresh[r], p.log2p, p.max_pages);
+            for (int x = 0; x < n; ++x) {
+                const int i = static_cast<int>(i0) + x;
+                if (i >= rows) break;
+                while (i >= end) {
+                    end = sums[++r + 1].x;
+                    q = Request(p.cached[r], p.fresh[r], p.log2p, p.max_pages);
+                }
+                const int j = i - sums[r].x;
+                if (j >= q.fit) continue;
                 const int64_t pos = static_cast<int64_t>(q.cached) + j;
-                const int col = static_cast<int>(pos >> log2p);
-                int id = -1;
-                if (col < q.old_pages) id = table[static_cast<int64_t>(r) * max_pages + col];
-                else if (pg + col - q.old_pages < num_free) id = free_pages[pg + col - q.old_pages];
-                if (id >= 0 && id < num_pages) slot = (id << log2p) + static_cast<int>(pos & ((1 << log2p) - 1));
-                else bad = true;
+                const int col = static_cast<int>(pos >> p.log2p);
+                const int page = col < q.old_pages ? p.table[static_cast<int64_t>(r) * p.max_pages + col]
+                                                   : free_page(clamp_int(static_cast<int64_t>(sums[r].y) + col - q.old_pages));
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages))
+                    out[x] = (page << p.log2p) + static_cast<int>(pos & mask);
+                else
+                    bad = true;
             }
-            slots[tok + j] = slot;
         }
-        __syncthreads();
-        if (threadIdx.x == 0) s_tok += q.rows, s_page += q.need;
-        __syncthreads();
+        int* dst = p.slots + i0;
+        if (n == 4 && (reinterpret_cast<uintptr_t>(p.slots) & 15u) == 0) {
+            *reinterpret_cast<int4*>(dst) = make_int4(out[0], out[1], out[2], out[3]);
+        } else {
+            for (int x = 0; x < n; ++x) dst[x] = out[x];
+        }
     }
-    const int64_t tok = s_tok, pg = s_page;
-    for (int64_t j = tok + threadIdx.x; j < max_tokens; j += kMapThreads) slots[j] = -1;
-    if (tok > max_tokens) bad = true;
-    if (threadIdx.x == 0) {
-        starts[R] = counts[0] = static_cast<int>(min(tok, static_cast<int64_t>(INT_MAX)));
-        counts[1] = static_cast<int>(min(pg, static_cast<int64_t>(INT_MAX)));
+    for (int64_t i = id; i < pages; i += all) {
+        const int r = find(static_cast<int>(i), true), page = free_page(static_cast<int>(i));
+        const Request q(p.cached[r], p.fresh[r], p.log2p, p.max_pages);
+        bad |= page < 0;
+        p.table[static_cast<int64_t>(r) * p.max_pages + q.old_pages + (i - sums[r].y)] = page;
     }
-    if (bad) atomicOr(status, kStatusBadIndex);
+    for (int64_t r = id; r <= p.R; r += all) p.starts[r] = sums[r].x;
+    if (id == 0) p.counts[0] = rows, p.counts[1] = pages;
+    return bad;
+}
+
+// Up to kMapShared requests: every block adds up all lengths for itself (two loads a
+// request from L2, one block-wide sum), so that one launch does it all.
+__global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapArgs p) {
+    __shared__ int2 s_sums[kMapShared + 1];
+    bool bad = map_sums<kMapThreads>(p, s_sums);
+    __syncthreads();
+    bad |= map_fill(p, s_sums);
+    if (bad) atomicOr(p.status, kStatusBadIndex);
+}
+
+// More requests: one block adds up, a second kernel fills.
+__global__ void __launch_bounds__(1024) page_sums_kernel(const MapArgs p) {
+    if (map_sums<1024>(p, p.sums)) atomicOr(p.status, kStatusBadIndex);
+}
+__global__ void __launch_bounds__(kMapThreads) page_fill_kernel(const MapArgs p) {
+    if (map_fill(p, p.sums)) atomicOr(p.status, kStatusBadIndex);
 }
 
 // A thread moves one 16-byte piece of a key row and of a value row.
@@ -113,11 +198,24 @@ __global__ void paged_append_kernel(const uint4* __restrict__ k, const uint4* __
 cudaError_t page_map(const LaunchCtx& c, const int* cached, const int* fresh, int R,
                      const int* free_pages, int num_free, int log2p, int num_pages, int* table,
                      int max_pages, int* slots, int max_tokens, int* starts, int* counts) {
-    page_map_kernel<<<1, kMapThreads, 0, c.stream>>>(cached, fresh, R, free_pages, num_free, log2p,
-                                                    num_pages, table, max_pages, slots, max_tokens,
-                                                    starts, counts, c.status_word);
-    note_launch();
-    return cudaGetLastError();
+    MapArgs p = {cached, fresh, free_pages, R, num_free, log2p, num_pages, max_pages, max_tokens,
+                 table, slots, starts, counts, nullptr, c.status_word};
+    // four rows a thread, or a request a thread, up to two blocks an SM
+    const int64_t work = std::max<int64_t>((static_cast<int64_t>(max_tokens) + 3) / 4, R + 1);
+    const int blocks = static_cast<int>(std::min<int64_t>((work + kMapThreads - 1) / kMapThreads, 2 * c.num_sms));
+    if (R <= kMapShared) {
+        page_map_kernel<<<blocks, kMapThreads, 0, c.stream>>>(p);
+        note_launch();
+        return cudaGetLastError();
+    }
+    cudaError_t e = scratch_alloc(c, reinterpret_cast<void**>(&p.sums), plan::page_map_scratch(R));
+    if (e != cudaSuccess) return e;
+    page_sums_kernel<<<1, 1024, 0, c.stream>>>(p);
+    page_fill_kernel<<<blocks, kMapThreads, 0, c.stream>>>(p);
+    note_launch(2);
+    e = cudaGetLastError();
+    scratch_free(c, p.sums);
+    return e;
 }
 
 cudaError_t paged_append(const LaunchCtx& c, const void* k, const void* v, void* K, void* V,
