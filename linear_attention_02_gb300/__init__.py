@@ -363,28 +363,54 @@ _FORMS = {"decay": _native.LA_GATE_DECAY, "logit": _native.LA_GATE_LOGIT}
 
 
 def _shaped(t, name, shape, dtype, dev):
-    _need(t, name, dtype, dev)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    """Refuses t unless it is a contiguous tensor of this shape and dtype on CUDA device `dev`.
+
+    The entry points below are short calls, so what passes is decided by the cheapest
+    tests; the message is made up only for what does not."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and dev >= 0 and t.is_contiguous()):
+        return
+    _need(t, name, dtype, torch.device("cuda", dev) if dev >= 0 else None)
+    raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _launch(fn, dev, stream, *args):
+    """fn(*args, stream handle) with device `dev` current: `stream`, or dev's current stream."""
+    if _current_device() == dev:
+        s = fn(*args, _raw_stream(dev) if stream is None else int(stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            s = fn(*args, _raw_stream(dev) if stream is None else int(stream.cuda_stream))
+    if s:
+        _check(s)
+
+
+# The raw handle of a device's current stream, and the current device's number, without
+# the objects that torch.cuda's functions make for them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: int(torch.cuda.current_stream(dev).cuda_stream))
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _scan_args(A, X, form, seq_starts):
-    """(B, N, C, sequences, num_seqs, form code) of a gated scan call, its inputs checked."""
+    """(B, N, C, sequences, num_seqs, form code, device) of a gated scan call, its inputs checked."""
     if form not in _FORMS:
         raise ValueError(f"form must be one of {sorted(_FORMS)}, got {form!r}")
     if not isinstance(A, torch.Tensor) or A.dim() != 3:
         raise ValueError("A and X must be [B,N,C]")
-    B, N, C = A.shape
-    _need(A, "A", A.dtype)
-    _shaped(X, "X", (B, N, C), A.dtype, A.device)
+    shape, dev = A.shape, A.get_device()
+    _shaped(A, "A", shape, A.dtype, dev)
+    _shaped(X, "X", shape, A.dtype, dev)
+    B, N, C = shape
     if seq_starts is None:
-        return B, N, C, B, 0, _FORMS[form]
-    _need(seq_starts, "seq_starts", torch.int32, A.device)
-    if seq_starts.dim() != 1 or seq_starts.numel() < 1:
-        raise ValueError("seq_starts must be [num_seqs + 1]")
+        return B, N, C, B, 0, _FORMS[form], dev
+    if not isinstance(seq_starts, torch.Tensor) or seq_starts.dim() != 1 or seq_starts.numel() < 1:
+        raise ValueError("seq_starts must be a tensor [num_seqs + 1]")
+    _shaped(seq_starts, "seq_starts", seq_starts.shape, torch.int32, dev)
     if B != 1:
         raise ValueError(f"packed sequences need B == 1, got {B}")
-    return B, N, C, seq_starts.numel() - 1, seq_starts.numel() - 1, _FORMS[form]
+    S = seq_starts.numel() - 1
+    return B, N, C, S, S, _FORMS[form], dev
 
 
 def la_gated_scan_ckpt_floats(B, N, C):
@@ -393,12 +419,10 @@ def la_gated_scan_ckpt_floats(B, N, C):
 
 
 def _check_scan_ckpt(c, name, B, N, C, dev):
-    if c is None:
-        return
-    _need(c, name, torch.float32, dev)
-    if c.numel() != la_gated_scan_ckpt_floats(B, N, C):
-        raise ValueError(f"{name} must hold la_gated_scan_ckpt_floats(...) = "
-                         f"{la_gated_scan_ckpt_floats(B, N, C)} floats, got {c.numel()}")
+    n = la_gated_scan_ckpt_floats(B, N, C)
+    if not isinstance(c, torch.Tensor) or c.numel() != n:
+        raise ValueError(f"{name} must hold la_gated_scan_ckpt_floats(...) = {n} floats")
+    _shaped(c, name, c.shape, torch.float32, dev)
 
 
 def la_forward_gated_scan(A, X, form="decay", out=None, h_init=None, return_state=False, ckpt=None,
@@ -410,19 +434,19 @@ def la_forward_gated_scan(A, X, form="decay", out=None, h_init=None, return_stat
     sequences; h_init, and the final state with return_state, are then [S,C] (else [B,C]),
     fp32.  ckpt: optional fp32 tensor of la_gated_scan_ckpt_floats(B, N, C) elements that
     receives states for la_backward_gated_scan(Ckpt=...).  Returns Out, or (Out, h_final)."""
-    B, N, C, S, num, code = _scan_args(A, X, form, seq_starts)
-    dev = A.device
+    B, N, C, S, num, code, dev = _scan_args(A, X, form, seq_starts)
+    dt = A.dtype
     if out is None:
         out = torch.empty_like(A)
-    _shaped(out, "out", (B, N, C), A.dtype, dev)
+    else:
+        _shaped(out, "out", (B, N, C), dt, dev)
     if h_init is not None:
         _shaped(h_init, "h_init", (S, C), torch.float32, dev)
-    _check_scan_ckpt(ckpt, "ckpt", B, N, C, dev)
-    h_f = torch.empty((S, C), dtype=torch.float32, device=dev) if return_state else None
-    with torch.cuda.device(dev):
-        _check(_lib.la_forward_gated_scan(_ptr(A), _ptr(X), _ptr(out), B, N, C, _dtype(A), code,
-                                          _ptr(seq_starts), num, _ptr(h_init), _ptr(h_f), _ptr(ckpt),
-                                          _stream_handle(stream)))
+    if ckpt is not None:
+        _check_scan_ckpt(ckpt, "ckpt", B, N, C, dev)
+    h_f = torch.empty((S, C), dtype=torch.float32, device=A.device) if return_state else None
+    _launch(_lib.la_forward_gated_scan, dev, stream, A.data_ptr(), X.data_ptr(), out.data_ptr(), B, N, C,
+            _dtype(A), code, _ptr(seq_starts), num, _ptr(h_init), _ptr(h_f), _ptr(ckpt))
     return (out, h_f) if return_state else out
 
 
@@ -432,22 +456,27 @@ def la_backward_gated_scan(A, X, dOut, form="decay", h_init=None, dh_final=None,
 
     dh_final: optional gradient at the final state; Ckpt: the forward's checkpoints
     (computed by the call when absent)."""
-    B, N, C, S, num, code = _scan_args(A, X, form, seq_starts)
-    dev = A.device
-    _shaped(dOut, "dOut", (B, N, C), A.dtype, dev)
-    dA = torch.empty_like(A) if dA is None else dA
-    dX = torch.empty_like(X) if dX is None else dX
-    _shaped(dA, "dA", (B, N, C), A.dtype, dev)
-    _shaped(dX, "dX", (B, N, C), A.dtype, dev)
-    for t, n in ((h_init, "h_init"), (dh_final, "dh_final")):
-        if t is not None:
-            _shaped(t, n, (S, C), torch.float32, dev)
-    _check_scan_ckpt(Ckpt, "Ckpt", B, N, C, dev)
-    dh = torch.empty((S, C), dtype=torch.float32, device=dev) if return_dh_init else None
-    with torch.cuda.device(dev):
-        _check(_lib.la_backward_gated_scan(_ptr(A), _ptr(X), _ptr(dOut), _ptr(dA), _ptr(dX), B, N, C,
-                                           _dtype(A), code, _ptr(seq_starts), num, _ptr(h_init),
-                                           _ptr(dh_final), _ptr(dh), _ptr(Ckpt), _stream_handle(stream)))
+    B, N, C, S, num, code, dev = _scan_args(A, X, form, seq_starts)
+    dt = A.dtype
+    _shaped(dOut, "dOut", (B, N, C), dt, dev)
+    if dA is None:
+        dA = torch.empty_like(A)
+    else:
+        _shaped(dA, "dA", (B, N, C), dt, dev)
+    if dX is None:
+        dX = torch.empty_like(X)
+    else:
+        _shaped(dX, "dX", (B, N, C), dt, dev)
+    if h_init is not None:
+        _shaped(h_init, "h_init", (S, C), torch.float32, dev)
+    if dh_final is not None:
+        _shaped(dh_final, "dh_final", (S, C), torch.float32, dev)
+    if Ckpt is not None:
+        _check_scan_ckpt(Ckpt, "Ckpt", B, N, C, dev)
+    dh = torch.empty((S, C), dtype=torch.float32, device=A.device) if return_dh_init else None
+    _launch(_lib.la_backward_gated_scan, dev, stream, A.data_ptr(), X.data_ptr(), dOut.data_ptr(),
+            dA.data_ptr(), dX.data_ptr(), B, N, C, _dtype(A), code, _ptr(seq_starts), num, _ptr(h_init),
+            _ptr(dh_final), _ptr(dh), _ptr(Ckpt))
     return (dA, dX, dh) if return_dh_init else (dA, dX)
 
 
@@ -457,17 +486,16 @@ def la_gated_scan_decode_step(a, x, h, form="decay", out=None, stream=None):
         raise ValueError(f"form must be one of {sorted(_FORMS)}, got {form!r}")
     if not isinstance(a, torch.Tensor) or a.dim() != 2:
         raise ValueError("a and x must be [B,C]")
-    B, C = a.shape
-    dev = a.device
-    _need(a, "a", a.dtype)
-    _shaped(x, "x", (B, C), a.dtype, dev)
-    _shaped(h, "h", (B, C), torch.float32, dev)
+    shape, dt, dev = a.shape, a.dtype, a.get_device()
+    _shaped(a, "a", shape, dt, dev)
+    _shaped(x, "x", shape, dt, dev)
+    _shaped(h, "h", shape, torch.float32, dev)
     if out is None:
         out = torch.empty_like(a)
-    _shaped(out, "out", (B, C), a.dtype, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.la_gated_scan_decode_step(_ptr(a), _ptr(x), _ptr(h), _ptr(out), B, C, _dtype(a),
-                                              _FORMS[form], _stream_handle(stream)))
+    else:
+        _shaped(out, "out", shape, dt, dev)
+    _launch(_lib.la_gated_scan_decode_step, dev, stream, a.data_ptr(), x.data_ptr(), h.data_ptr(),
+            out.data_ptr(), shape[0], shape[1], _dtype(a), _FORMS[form])
     return out
 
 
@@ -481,50 +509,53 @@ def la_page_map(cached_lens, new_lens, free_pages, block_table, page_size, num_p
     positions and the pages wanted.  Returns (slot_map, seq_starts, counts)."""
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [R, max_pages]")
+    i32, dev = torch.int32, block_table.get_device()
+    _shaped(block_table, "block_table", block_table.shape, i32, dev)
     R, W = block_table.shape
-    dev = block_table.device
-    i32 = torch.int32
-    _need(block_table, "block_table", i32)
     _shaped(cached_lens, "cached_lens", (R,), i32, dev)
     _shaped(new_lens, "new_lens", (R,), i32, dev)
     for t, n in ((free_pages, "free_pages"), (slot_map, "slot_map")):
-        _need(t, n, i32, dev)
-        if t.dim() != 1:
-            raise ValueError(f"{n} must have one dimension")
-    seq_starts = torch.empty(R + 1, dtype=i32, device=dev) if seq_starts is None else seq_starts
-    counts = torch.empty(2, dtype=i32, device=dev) if counts is None else counts
-    _shaped(seq_starts, "seq_starts", (R + 1,), i32, dev)
-    _shaped(counts, "counts", (2,), i32, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.la_page_map(_ptr(cached_lens), _ptr(new_lens), R, _ptr(free_pages),
-                                free_pages.numel(), int(page_size), int(num_pages), _ptr(block_table), W,
-                                _ptr(slot_map), slot_map.numel(), _ptr(seq_starts), _ptr(counts),
-                                _stream_handle(stream)))
+        if not isinstance(t, torch.Tensor) or t.dim() != 1:
+            raise ValueError(f"{n} must be a tensor of one dimension")
+        _shaped(t, n, t.shape, i32, dev)
+    if seq_starts is None:
+        seq_starts = torch.empty(R + 1, dtype=i32, device=block_table.device)
+    else:
+        _shaped(seq_starts, "seq_starts", (R + 1,), i32, dev)
+    if counts is None:
+        counts = torch.empty(2, dtype=i32, device=block_table.device)
+    else:
+        _shaped(counts, "counts", (2,), i32, dev)
+    _launch(_lib.la_page_map, dev, stream, cached_lens.data_ptr(), new_lens.data_ptr(), R,
+            free_pages.data_ptr(), free_pages.shape[0], int(page_size), int(num_pages),
+            block_table.data_ptr(), W, slot_map.data_ptr(), slot_map.shape[0], seq_starts.data_ptr(),
+            counts.data_ptr())
     return slot_map, seq_starts, counts
 
 
 def _pools(K_pages, V_pages):
+    """(num_pages, Hkv, page_size, D, device) of the pools, checked."""
     if not isinstance(K_pages, torch.Tensor) or K_pages.dim() != 4:
         raise ValueError("K_pages and V_pages must be [num_pages, Hkv, page_size, D]")
-    _need(K_pages, "K_pages", K_pages.dtype)
-    _shaped(V_pages, "V_pages", K_pages.shape, K_pages.dtype, K_pages.device)
-    return K_pages.shape
+    shape, dev = K_pages.shape, K_pages.get_device()
+    _shaped(K_pages, "K_pages", shape, K_pages.dtype, dev)
+    _shaped(V_pages, "V_pages", shape, K_pages.dtype, dev)
+    return (*shape, dev)
 
 
 def la_paged_append(k, v, K_pages, V_pages, slot_map, stream=None):
     """Writes rows k, v [T,Hkv,D] into the slots slot_map [T] (int32; -1 skips a row) of the
     pools K_pages, V_pages [num_pages,Hkv,page_size,D]."""
-    P, Hkv, page, D = _pools(K_pages, V_pages)
-    dev, dt = K_pages.device, K_pages.dtype
+    P, Hkv, page, D, dev = _pools(K_pages, V_pages)
+    dt = K_pages.dtype
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k and v must be [T, Hkv, D]")
     T = k.shape[0]
     _shaped(k, "k", (T, Hkv, D), dt, dev)
     _shaped(v, "v", (T, Hkv, D), dt, dev)
     _shaped(slot_map, "slot_map", (T,), torch.int32, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.la_paged_append(_ptr(k), _ptr(v), _ptr(K_pages), _ptr(V_pages), _ptr(slot_map), T, Hkv,
-                                    D, P, page, _dtype(K_pages), _stream_handle(stream)))
+    _launch(_lib.la_paged_append, dev, stream, k.data_ptr(), v.data_ptr(), K_pages.data_ptr(),
+            V_pages.data_ptr(), slot_map.data_ptr(), T, Hkv, D, P, page, _dtype(K_pages))
 
 
 def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, window=0, scale=None,
@@ -535,8 +566,8 @@ def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, wi
     nothing) and returns out [R,Hq,D] fp32 = softmax(scale q K^T) V over the request's last
     `window` positions (0: all), with return_lse also the log of the sum [R,Hq] fp32.  Rows with a
     negative length are left as they are.  scale None: 1 / sqrt(D)."""
-    P, Hkv, page, D = _pools(K_pages, V_pages)
-    dev, dt = K_pages.device, K_pages.dtype
+    P, Hkv, page, D, dev = _pools(K_pages, V_pages)
+    dt = K_pages.dtype
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [R, Hq, D]")
     R, Hq = q.shape[:2]
@@ -546,22 +577,22 @@ def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, wi
     if k is not None:
         _shaped(k, "k", (R, Hkv, D), dt, dev)
         _shaped(v, "v", (R, Hkv, D), dt, dev)
-    _need(block_table, "block_table", torch.int32, dev)
-    if block_table.dim() != 2 or block_table.shape[0] != R:
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError(f"block_table must be [R, max_pages] with R = {R}")
+    _shaped(block_table, "block_table", block_table.shape, torch.int32, dev)
     _shaped(cached_lens, "cached_lens", (R,), torch.int32, dev)
-    if scale is not None and float(scale) == 0.0:
+    if scale is None:
+        scale = 0.0
+    elif float(scale) == 0.0:
         raise ValueError("scale must not be 0")
     if out is None:
-        out = torch.empty((R, Hq, D), dtype=torch.float32, device=dev)
-    _shaped(out, "out", (R, Hq, D), torch.float32, dev)
-    lse = torch.empty((R, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    with torch.cuda.device(dev):
-        _check(_lib.la_paged_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(K_pages), _ptr(V_pages),
-                                         _ptr(block_table), _ptr(cached_lens), _ptr(out), _ptr(lse), R, Hq,
-                                         Hkv, D, P, page, block_table.shape[1], int(window),
-                                         0.0 if scale is None else float(scale), _dtype(K_pages),
-                                         _stream_handle(stream)))
+        out = torch.empty((R, Hq, D), dtype=torch.float32, device=q.device)
+    else:
+        _shaped(out, "out", (R, Hq, D), torch.float32, dev)
+    lse = torch.empty((R, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    _launch(_lib.la_paged_decode_step, dev, stream, q.data_ptr(), _ptr(k), _ptr(v), K_pages.data_ptr(),
+            V_pages.data_ptr(), block_table.data_ptr(), cached_lens.data_ptr(), out.data_ptr(), _ptr(lse), R,
+            Hq, Hkv, D, P, page, block_table.shape[1], int(window), float(scale), _dtype(K_pages))
     return (out, lse) if return_lse else out
 
 
