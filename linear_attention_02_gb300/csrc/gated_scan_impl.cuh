@@ -22,16 +22,6 @@ Parts parts_of(int B, int N, int C, bool packed, bool own_incl) {
     return s;
 }
 
-template <class K>
-cudaError_t resident_blocks(K kernel, size_t smem, int num_sms, int* blocks) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    int per = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, NT, smem);
-    *blocks = std::max(1, per) * num_sms;
-    return e;
-}
-
 // Map over a [B][N][C] tensor with a box of 128 rows x 128 bytes.
 template <typename T>
 cudaError_t stream_map(CUtensorMap* m, const T* base, int B, int N, int C) {
@@ -93,22 +83,26 @@ cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl) {
         e = cudaMemsetAsync(base, 0xFF, s.words * 4, c.stream);
     }
 
-    const auto go = [&](auto* kernel, size_t smem) {
-        int blocks = 1;
-        if (e == cudaSuccess) e = resident_blocks(kernel, smem, c.num_sms, &blocks);
-        if (e != cudaSuccess) return;
-        kernel<<<std::min<unsigned>(a.total, blocks), NT, smem, c.stream>>>(a, maps);
-        note_launch();
-        e = cudaGetLastError();
-    };
-#define LA_SCAN_GO(L, P, V)                                                                  \
-    if (logit == L && packed == P && vec == V) {                                             \
-        if constexpr (kBwd) go(scan_backward_kernel<T, L, P, V>, smem_bytes<T, P, STREAMS>()); \
-        else go(scan_forward_kernel<T, L, P, V>, smem_bytes<T, P, STREAMS>());               \
+#define LA_SCAN_RUN(K, SMEM)                                                                       \
+    {                                                                                              \
+        int per = 1;                                                                               \
+        if (e == cudaSuccess) e = resident_blocks<K>(c.device, NT, SMEM, &per);                    \
+        if (e == cudaSuccess) {                                                                    \
+            K<<<std::min<unsigned>(a.total, per * c.num_sms), NT, SMEM, c.stream>>>(a, maps);      \
+            note_launch();                                                                         \
+            e = cudaGetLastError();                                                                \
+        }                                                                                          \
+    }
+#define LA_SCAN_GO(L, P, V)                                                                        \
+    if (logit == L && packed == P && vec == V) {                                                   \
+        constexpr int smem = static_cast<int>(smem_bytes<T, P, STREAMS>());                        \
+        if constexpr (kBwd) LA_SCAN_RUN((scan_backward_kernel<T, L, P, V>), smem)                  \
+        else LA_SCAN_RUN((scan_forward_kernel<T, L, P, V>), smem)                                  \
     }
     LA_SCAN_GO(false, false, false) LA_SCAN_GO(false, false, true) LA_SCAN_GO(false, true, false)
     LA_SCAN_GO(false, true, true) LA_SCAN_GO(true, false, false) LA_SCAN_GO(true, false, true)
     LA_SCAN_GO(true, true, false) LA_SCAN_GO(true, true, true)
+#undef LA_SCAN_RUN
 #undef LA_SCAN_GO
     scratch_free(c, base);
     return e;

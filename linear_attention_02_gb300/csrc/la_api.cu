@@ -39,8 +39,6 @@ la_status cuda_fail(cudaError_t e, const char* where) {
     return fail(LA_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-constexpr int kMaxDevices = 64;
-
 struct DeviceState {
     std::atomic<bool> ready{false};  // set (release) once the fields below are filled
     int num_sms = 0;
@@ -85,6 +83,7 @@ la_status get_ctx(cudaStream_t stream, LaunchCtx* ctx) {
     ctx->withhold_unit = g_withhold_unit.exchange(-1);
     ctx->spin_limit = g_spin_limit.exchange(0u);
     ctx->num_sms = d.num_sms;
+    ctx->device = dev;
     ctx->pool = d.pool;
     ctx->status_word = d.status_word;
     return LA_OK;

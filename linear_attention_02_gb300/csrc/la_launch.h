@@ -6,12 +6,17 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace la {
+
+constexpr int kMaxDevices = 64;
 
 // Everything a launcher needs from the device it runs on.
 struct LaunchCtx {
     cudaStream_t stream;
     int num_sms;
+    int device;                  // its ordinal, below kMaxDevices
     cudaMemPool_t pool;          // library-owned pool for stream-ordered scratch
     unsigned int* status_word;   // device error word for bounded waits
     // test hook (la_debug_withhold_publication): the unit whose look-back flag the next
@@ -19,6 +24,23 @@ struct LaunchCtx {
     int withhold_unit;
     unsigned spin_limit;
 };
+
+// Allows `kernel` its shared memory on a device and returns its resident blocks per
+// SM, both asked of the runtime once per device and kernel.
+template <auto kernel>
+cudaError_t resident_blocks(int device, int threads, int smem, int* per_sm) {
+    static std::atomic<int> known[kMaxDevices];
+    int n = known[device].load(std::memory_order_acquire);
+    if (n == 0) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+        if (e != cudaSuccess) return e;
+        if (n == 0) return cudaErrorLaunchOutOfResources;
+        known[device].store(n, std::memory_order_release);
+    }
+    *per_sm = n;
+    return cudaSuccess;
+}
 
 // Counts one kernel launch (la_kernel_launch_count).
 void note_launch(int n = 1);

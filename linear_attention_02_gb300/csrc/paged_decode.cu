@@ -820,9 +820,10 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
                    const int* lens, float* out, float* lse, const PagedShape& s) {
     using Ly = Lay<T, D>;
     auto* kernel = paged_decode_kernel<T, D, kHeads>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM);
+    int per_sm = 1;
+    cudaError_t e = resident_blocks<paged_decode_kernel<T, D, kHeads>>(c.device, kThreads, Ly::SMEM, &per_sm);
     if (e != cudaSuccess) return e;
-    const int blocks = Ly::BLOCKS * c.num_sms, workers = blocks * kWarps;
+    const int blocks = per_sm * c.num_sms, workers = blocks * kWarps;
     PagedArgs p = {};
     p.s = s;
     p.G = s.Hq / s.Hkv;
