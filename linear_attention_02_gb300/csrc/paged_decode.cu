@@ -33,7 +33,9 @@
 // and values is 4 KB of memory traffic, about 170 cycles of an SM's share of the
 // bandwidth, against 24 small products.
 //
-// The maximum is kept lazily: it is raised, and the sums rescaled, only when a
+// Each step's outputs are summed by the matrix unit from zero and added to the running
+// sums in fp32 (summed on through a whole range, the unit's truncation left an error
+// of 3.4e-6 at 4096 positions; so it is KKK2).  The maximum is kept lazily: it is raised, and the sums rescaled, only when a
 // score passes it by more than 2^8, so most steps need no exchange between lanes.
 // A range that starts or ends inside a request leaves partial sums, which a second
 // small kernel joins in the order of the ranges.
@@ -421,14 +423,23 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             }
     };
 
-    // of head g (and g + 8): output sums (with 8 heads in two parts), maximum (log2),
-    // sum of the weights of the lane's positions
-    float o[NT][4], m[ROWS], l[ROWS];
+    // of head g (and g + 8): output sums, maximum (log2), sum of the weights of the lane's positions
+    float o[NT][2 * ROWS], m[ROWS], l[ROWS];
     const auto clear = [&]() {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2 * ROWS; ++e) o[i][e] = 0.f;
 #pragma unroll
         for (int z = 0; z < ROWS; ++z) m[z] = -INFINITY, l[z] = 0.f;
+    };
+    const auto add = [](float(&to)[2 * ROWS], const float(&d)[4]) {  // rows 8 to 15: a second term, or heads
+        if constexpr (ROWS == 1) {
+            to[0] += d[0] + d[2];
+            to[1] += d[1] + d[3];
+        } else {
+            to[0] += d[0], to[1] += d[1], to[2] += d[2], to[3] += d[3];
+        }
     };
     clear();
     load_q();
@@ -537,7 +548,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 for (int i = 0; i < NT; ++i) {
                     o[i][2 * z] *= f;
                     o[i][2 * z + 1] *= f;
-                    if constexpr (ROWS == 1) o[i][2] *= f, o[i][3] *= f;
                 }
             }
         }
@@ -568,7 +578,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 }
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                uint32_t v[4][VPL / 2], b[VPL][2];
+                uint32_t v[4][VPL / 2];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if constexpr (VB == 16) {
@@ -579,67 +589,64 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                         v[e][0] = f.x, v[e][1] = f.y;
                     }
                 }
+                float d[VPL][4];
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
                     const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-                    b[j][0] = __byte_perm(v[0][j / 2], v[1][j / 2], sel);
-                    b[j][1] = __byte_perm(v[2][j / 2], v[3][j / 2], sel);
+                    const uint32_t b0 = __byte_perm(v[0][j / 2], v[1][j / 2], sel);
+                    const uint32_t b1 = __byte_perm(v[2][j / 2], v[3][j / 2], sel);
+                    d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
+                    if constexpr (ROWS == 1) {  // rows: the first two terms, then the third
+                        mma_bf16(d[j], w[0][0][0], w[1][0][0], w[0][0][1], w[1][0][1], b0, b1);
+                        mma_bf16(d[j], w[2][0][0], 0u, w[2][0][1], 0u, b0, b1);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 3; ++u)
+                            mma_bf16(d[j], w[u][0][0], w[u][ROWS - 1][0], w[u][0][1], w[u][ROWS - 1][1], b0, b1);
+                    }
                 }
-                if constexpr (ROWS == 1) {  // rows: the first two terms, then the third
 #pragma unroll
-                    for (int j = 0; j < VPL; ++j)
-                        mma_bf16(o[i * VPL + j], w[0][0][0], w[1][0][0], w[0][0][1], w[1][0][1], b[j][0], b[j][1]);
-#pragma unroll
-                    for (int j = 0; j < VPL; ++j)
-                        mma_bf16(o[i * VPL + j], w[2][0][0], 0u, w[2][0][1], 0u, b[j][0], b[j][1]);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 3; ++u)
-#pragma unroll
-                        for (int j = 0; j < VPL; ++j)
-                            mma_bf16(o[i * VPL + j], w[u][0][0], w[u][ROWS - 1][0], w[u][0][1], w[u][ROWS - 1][1],
-                                     b[j][0], b[j][1]);
-                }
+                for (int j = 0; j < VPL; ++j) add(o[i * VPL + j], d[j]);
             }
         } else {
+            uint32_t wh[2][ROWS][2], wl[2][ROWS][2];  // keys 2t (operand k = t) and 2t + 1 (k = t + 4) of each tile
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                uint32_t wh[ROWS][2], wl[ROWS][2];  // keys 2t (operand k = t) and 2t + 1 (k = t + 4)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int z = 0; z < ROWS; ++z)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) split_tf32(__float_as_uint(s[n][2 * z + e]), wh[z][e], wl[z][e]);
+                    for (int e = 0; e < 2; ++e)
+                        split_tf32(__float_as_uint(s[n][2 * z + e]), wh[n][z][e], wl[n][z][e]);
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const uint4 v0 = *reinterpret_cast<const uint4*>(st + Ly::vat(g, t, 2 * n, i));
-                    const uint4 v1 = *reinterpret_cast<const uint4*>(st + Ly::vat(g, t, 2 * n + 1, i));
-                    const uint32_t x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
-                    uint32_t h0[4], h1[4], c0[4], c1[4];
+            for (int i = 0; i < NI; ++i) {
+                uint32_t v[4][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        split_tf32(x0[j], h0[j], c0[j]);
-                        split_tf32(x1[j], h1[j], c1[j]);
-                    }
-                    if constexpr (ROWS == 1) {  // rows: both terms of the weights
+                for (int e = 0; e < 4; ++e) {
+                    const uint4 f = *reinterpret_cast<const uint4*>(st + Ly::vat(g, t, e, i));
+                    v[e][0] = f.x, v[e][1] = f.y, v[e][2] = f.z, v[e][3] = f.w;
+                }
+                float d[4][4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_tf32(o[i * 4 + j], wh[0][0], wl[0][0], wh[0][1], wl[0][1], h0[j], h1[j]);
+                for (int j = 0; j < 4; ++j) {
+                    d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_tf32(o[i * 4 + j], wh[0][0], wl[0][0], wh[0][1], wl[0][1], c0[j], c1[j]);
-                    } else {
-                        constexpr int Z = ROWS - 1;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_tf32(o[i * 4 + j], wh[0][0], wh[Z][0], wh[0][1], wh[Z][1], h0[j], h1[j]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_tf32(o[i * 4 + j], wh[0][0], wh[Z][0], wh[0][1], wh[Z][1], c0[j], c1[j]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_tf32(o[i * 4 + j], wl[0][0], wl[Z][0], wl[0][1], wl[Z][1], h0[j], h1[j]);
+                    for (int n = 0; n < 2; ++n) {
+                        uint32_t h0, h1, c0, c1;
+                        split_tf32(v[2 * n][j], h0, c0);
+                        split_tf32(v[2 * n + 1][j], h1, c1);
+                        if constexpr (ROWS == 1) {  // rows: both terms of the weights
+                            mma_tf32(d[j], wh[n][0][0], wl[n][0][0], wh[n][0][1], wl[n][0][1], h0, h1);
+                            mma_tf32(d[j], wh[n][0][0], wl[n][0][0], wh[n][0][1], wl[n][0][1], c0, c1);
+                        } else {
+                            constexpr int Z = ROWS - 1;
+                            mma_tf32(d[j], wh[n][0][0], wh[n][Z][0], wh[n][0][1], wh[n][Z][1], h0, h1);
+                            mma_tf32(d[j], wh[n][0][0], wh[n][Z][0], wh[n][0][1], wh[n][Z][1], c0, c1);
+                            mma_tf32(d[j], wl[n][0][0], wl[n][Z][0], wl[n][0][1], wl[n][Z][1], h0, h1);
+                        }
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) add(o[i * 4 + j], d[j]);
             }
         }
 
@@ -685,8 +692,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                                 float y[4];
 #pragma unroll
                                 for (int x = 0; x < 4; ++x) {
-                                    const float(&b)[4] = o[i * VPL + j + x];
-                                    y[x] = (ROWS == 1 ? b[c] + b[2 + c] : b[2 * z + c]) * f;
+                                    y[x] = o[i * VPL + j + x][2 * z + c] * f;
                                 }
                                 *reinterpret_cast<float4*>(dst + (2 * t + c + 8 * i) * VPL + j) =
                                     make_float4(y[0], y[1], y[2], y[3]);
