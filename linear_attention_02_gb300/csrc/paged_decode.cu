@@ -53,8 +53,6 @@
 namespace la {
 namespace {
 
-constexpr int kWarps = 4;       // warps of a block
-constexpr int kThreads = 32 * kWarps;
 constexpr int kJoinWarps = 8;   // warps of a block of the joining kernel
 constexpr int kStep = 16;       // positions of a step
 constexpr float kSlack = 8.f;   // log2 by which a score may pass the maximum kept
@@ -72,9 +70,16 @@ struct Lay {
     static constexpr int KC = D * ES / 64;
     static constexpr int VB = AB / 8, VPL = VB / ES, NI = ATOMS;  // bytes and values of a value piece
     static constexpr int HALF = ATOMS * ATOM, STAGE = 2 * HALF;   // bytes of the keys, of a step
-    static constexpr int STAGES = STAGE >= 4096 ? 3 : 6;
-    static constexpr int SMEM = kWarps * STAGES * STAGE + 1024;
-    static constexpr int BLOCKS = STAGE <= 4096 ? 4 : STAGE == 8192 ? 2 : 1;  // per SM
+    // Warps of a block, blocks of an SM and steps of a ring fill the SM's shared memory
+    // with about 192 KB: enough warps to hide a step's chain of products, exponentials
+    // and products, and as many steps ahead as is left.  Measured, TB/s: 4 KB steps
+    // 6.50 with 12 warps x 4, 6.35 with 16 x 3; 8 KB steps (D = 128, bf16) 5.76 with
+    // 8 x 3, 5.3 with 12 x 2, 5.66 with 6 x 4; 16 KB steps 6.14 with 6 x 2, 5.57 with 4 x 3.
+    static constexpr int WARPS = STAGE == 16384 ? 6 : 4, THREADS = 32 * WARPS;
+    static constexpr int BLOCKS = STAGE == 2048 ? 4 : STAGE == 4096 ? 3 : STAGE == 8192 ? 2 : 1;
+    static constexpr int STAGES = STAGE == 2048 ? 6 : STAGE == 4096 ? 4 : STAGE == 8192 ? 3 : 2;
+    static constexpr int SMEM = WARPS * STAGES * STAGE + 1024;
+    static_assert(STAGES <= 6, "kMinSteps");
     // the chunk (of the whole row) and the place of the lane's key piece i in key tile n
     static __device__ __forceinline__ int kchunk(int t, int i) { return AB == 128 ? (i / 2) * 8 + 2 * t + i % 2 : t; }
     static __device__ __forceinline__ int kat(int g, int t, int n, int i) {
@@ -199,6 +204,7 @@ struct Cursor {
 
 // Inclusive sums of the steps of all requests, chunk by chunk of requests (a chunk
 // a thread); returns their total.  Every block does it for itself (R lengths from L2).
+template <int kThreads>
 __device__ __forceinline__ int64_t sum_steps(const PagedArgs& p, int64_t* s_pre) {
     const int tid = threadIdx.x, lane = tid & 31;
     const int chunk = (p.s.R + kThreads - 1) / kThreads;
@@ -224,6 +230,7 @@ __device__ __forceinline__ int64_t sum_steps(const PagedArgs& p, int64_t* s_pre)
 }
 
 // The request with step u0 < total, and its first step's number.  For a whole warp.
+template <int kThreads>
 __device__ __forceinline__ int locate(const PagedArgs& p, const int64_t* s_pre, int64_t u0, int64_t& base) {
     const int lane = threadIdx.x & 31, chunk = (p.s.R + kThreads - 1) / kThreads;
     int at = 0;
@@ -266,13 +273,14 @@ __device__ __noinline__ float2 exact_scores(const uint8_t* st, const float* q, b
 
 // kHeads: 8 or 16 query heads a step.
 template <typename T, int D, int kHeads>
-__global__ void __launch_bounds__(kThreads, Lay<T, D>::BLOCKS)
+__global__ void __launch_bounds__(Lay<T, D>::THREADS, Lay<T, D>::BLOCKS)
 paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const T* __restrict__ q, const T* __restrict__ kn, const T* __restrict__ vn, T* K, T* V,
                     const PagedArgs p, int min_per) {
     using Ly = Lay<T, D>;
     constexpr int KC = Ly::KC, VPL = Ly::VPL, VB = Ly::VB, NI = Ly::NI, ROWS = kHeads / 8, NT = D / 8;
     constexpr int STAGES = Ly::STAGES, PE = 16 / static_cast<int>(sizeof(T));  // values of 16 bytes
+    constexpr int kWarps = Ly::WARPS, kThreads = Ly::THREADS;
     constexpr bool kBf16 = sizeof(T) == 2;
     extern __shared__ uint8_t sm_raw[];
     __shared__ uint64_t s_bar[kWarps][STAGES];
@@ -286,7 +294,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         for (int s = 0; s < STAGES; ++s) tc::mbar_init(bar + s, 1);
         tc::fence_mbar_init();
     }
-    const int64_t total = sum_steps(p, s_pre);
+    const int64_t total = sum_steps<kThreads>(p, s_pre);
     const int64_t two = (total + 2 * workers - 1) / (2 * workers);  // steps of a range with two a warp
     const int64_t per = max(max(static_cast<int64_t>(min_per), min(two, static_cast<int64_t>(kLongRange))),
                             (total + p.max_ranges - 1) / p.max_ranges);
@@ -304,7 +312,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 
     int64_t base;
     int range = worker, after = ask();          // the range in work; the loader's next one
-    const int row_at = locate(p, s_pre, range * per, base);
+    const int row_at = locate<kThreads>(p, s_pre, range * per, base);
     Cursor ld(p, row_at, range * per - base);
     Cursor cs = ld, nx = ld;                    // nx: where the loader began its range, when it is ahead
     int nx_range = range;
@@ -384,7 +392,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             } else {  // on to the next range
                 const int i = __shfl_sync(0xffffffffu, after, 0);
                 if (i < ranges) {
-                    const int r = locate(p, s_pre, i * per, base);
+                    const int r = locate<kThreads>(p, s_pre, i * per, base);
                     ld = Cursor(p, r, i * per - base);
                     pg = page_of(ld);
                     nx = ld;
@@ -827,9 +835,9 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
     using Ly = Lay<T, D>;
     auto* kernel = paged_decode_kernel<T, D, kHeads>;
     int per_sm = 1;
-    cudaError_t e = resident_blocks<paged_decode_kernel<T, D, kHeads>>(c.device, kThreads, Ly::SMEM, &per_sm);
+    cudaError_t e = resident_blocks<paged_decode_kernel<T, D, kHeads>>(c.device, Ly::THREADS, Ly::SMEM, &per_sm);
     if (e != cudaSuccess) return e;
-    const int blocks = per_sm * c.num_sms, workers = blocks * kWarps;
+    const int blocks = per_sm * c.num_sms, workers = blocks * Ly::WARPS;
     PagedArgs p = {};
     p.s = s;
     p.G = s.Hq / s.Hkv;
@@ -863,7 +871,7 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
         e = cudaMemsetAsync(p.next, 0, 4, c.stream);
     }
     if (e == cudaSuccess) {
-        kernel<<<blocks, kThreads, Ly::SMEM, c.stream>>>(kmap, vmap, q, k, v, K, V, p, single ? kMinSingle : kMinSteps);
+        kernel<<<blocks, Ly::THREADS, Ly::SMEM, c.stream>>>(kmap, vmap, q, k, v, K, V, p, single ? kMinSingle : kMinSteps);
         note_launch(2);
         e = cudaGetLastError();
     }
