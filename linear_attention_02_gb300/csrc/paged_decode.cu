@@ -53,7 +53,6 @@
 namespace la {
 namespace {
 
-constexpr int kJoinWarps = 8;   // warps of a block of the joining kernel
 constexpr int kStep = 16;       // positions of a step
 constexpr float kSlack = 8.f;   // log2 by which a score may pass the maximum kept
 
@@ -79,7 +78,7 @@ struct Lay {
     static constexpr int BLOCKS = STAGE == 2048 ? 4 : STAGE == 4096 ? 3 : STAGE == 8192 ? 2 : 1;
     static constexpr int STAGES = STAGE == 2048 ? 6 : STAGE == 4096 ? 4 : STAGE == 8192 ? 3 : 2;
     static constexpr int SMEM = WARPS * STAGES * STAGE + 1024;
-    static_assert(STAGES <= 6, "kMinSteps");
+    static_assert(STAGES <= 8, "the loader is never two ranges ahead");
     // the chunk (of the whole row) and the place of the lane's key piece i in key tile n
     static __device__ __forceinline__ int kchunk(int t, int i) { return AB == 128 ? (i / 2) * 8 + 2 * t + i % 2 : t; }
     static __device__ __forceinline__ int kat(int g, int t, int n, int i) {
@@ -134,14 +133,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// Ranges: up to kRanges a warp, so that warps that run ahead take more of them
-// (690 us against 700 us with 2, 256 x 16 x 4096 x 64), but below kLongRange steps
-// only two a warp, since each range may leave partial sums (95 us against 105 us at
-// 6 x 4 key heads of up to 65535 positions, D = 128), and not below kMinSteps (the
-// loader, at most STAGES - 1 steps ahead, is then never two ranges ahead).  Calls
-// that cannot give every warp kMinSteps steps take one range a warp (9.6 us with 1 step at least, 11.5 us
-// with 2, at 4 x 4 key heads of up to 300 positions).
-constexpr int kRanges = 4, kLongRange = 32, kMinSteps = 6, kMinSingle = 1;
+// Ranges a warp: 4, so that warps that run ahead take more of them (690 us against
+// 700 us with 2, 256 x 16 x 4096 x 64), but 2 below kFour steps a warp, since each
+// range may leave partial sums (95 us against 105 us at 6 x 4 key heads of up to
+// 65535 positions, D = 128), and 1 below kTwo: a few ranges more than warps would
+// cost a whole range's time.  A range that is followed by another then has at least
+// kTwo / 2 steps, more than the loader runs ahead.
+constexpr int kTwo = 16, kFour = 64;
 
 struct PagedArgs {
     PagedShape s;
@@ -276,7 +274,7 @@ template <typename T, int D, int kHeads>
 __global__ void __launch_bounds__(Lay<T, D>::THREADS, Lay<T, D>::BLOCKS)
 paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const T* __restrict__ q, const T* __restrict__ kn, const T* __restrict__ vn, T* K, T* V,
-                    const PagedArgs p, int min_per) {
+                    const PagedArgs p) {
     using Ly = Lay<T, D>;
     constexpr int KC = Ly::KC, VPL = Ly::VPL, VB = Ly::VB, NI = Ly::NI, ROWS = kHeads / 8, NT = D / 8;
     constexpr int STAGES = Ly::STAGES, PE = 16 / static_cast<int>(sizeof(T));  // values of 16 bytes
@@ -295,9 +293,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         tc::fence_mbar_init();
     }
     const int64_t total = sum_steps<kThreads>(p, s_pre);
-    const int64_t two = (total + 2 * workers - 1) / (2 * workers);  // steps of a range with two a warp
-    const int64_t per = max(max(static_cast<int64_t>(min_per), min(two, static_cast<int64_t>(kLongRange))),
-                            (total + p.max_ranges - 1) / p.max_ranges);
+    const int64_t each = total / workers;  // steps of a warp
+    const int64_t cuts = static_cast<int64_t>(workers) * (p.next == nullptr || each < kTwo ? 1 : each < kFour ? 2 : 4);
+    const int64_t per = max(static_cast<int64_t>(1), (total + cuts - 1) / cuts);
     const int ranges = static_cast<int>((total + per - 1) / per);
     if (!p.direct && lane == 0)
         for (int i = worker; i < p.max_ranges; i += workers)
@@ -755,7 +753,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 // Joins the ranges of a split column, one block a query head: the maximum of the
 // ranges' maxima, then sums scaled to it, in the order of the ranges within each
 // of the block's warps and of the warps.
-template <int D, int kHeads>
+template <int D, int kHeads, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedArgs p) {
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_a[kJoinWarps][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -774,19 +772,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
 #pragma unroll
     for (int e = 0; e < E; ++e) a[e] = 0.f;
     const int each = (d.y + kJoinWarps - 1) / kJoinWarps, i1 = min(d.y, (warp + 1) * each);
-#pragma unroll 8
-    for (int i = warp * each; i < i1; ++i) {
-        const float* part = p.part + ((static_cast<int64_t>(d.x) + i) * 2 + (i ? 0 : d.z)) * p.heads * (D + 4);
-        const float pm = part[p.heads * D + 2 * h], pl = part[p.heads * D + 2 * h + 1];
-        float v[E];
+    constexpr int N = 8;  // ranges fetched at once
+    for (int i0 = warp * each; i0 < i1; i0 += N) {
+        float pm[N], pl[N], v[N][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = part[h * D + lane + 32 * e];
-        const float x = fmaxf(m, pm);
-        const float f = m == x ? 1.f : ex2(m - x), g = pm == -INFINITY ? 0.f : pm == x ? 1.f : ex2(pm - x);
-        l = l * f + pl * g;
+        for (int x = 0; x < N; ++x) {
+            const int i = i0 + x;
+            const float* part = p.part + ((static_cast<int64_t>(d.x) + i) * 2 + (i ? 0 : d.z)) * p.heads * (D + 4);
+            pm[x] = i < i1 ? part[p.heads * D + 2 * h] : -INFINITY;
+            pl[x] = i < i1 ? part[p.heads * D + 2 * h + 1] : 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) a[e] = a[e] * f + v[e] * g;
-        m = x;
+            for (int e = 0; e < E; ++e) v[x][e] = i < i1 ? part[h * D + lane + 32 * e] : 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            const float y = fmaxf(m, pm[x]);
+            const float f = m == y ? 1.f : ex2(m - y), g = pm[x] == -INFINITY ? 0.f : pm[x] == y ? 1.f : ex2(pm[x] - y);
+            l = l * f + pl[x] * g;
+#pragma unroll
+            for (int e = 0; e < E; ++e) a[e] = a[e] * f + v[x][e] * g;
+            m = y;
+        }
     }
     if (lane == 0) s_m[warp] = m, s_l[warp] = l;
 #pragma unroll
@@ -856,8 +862,8 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
     const int64_t cols = static_cast<int64_t>(s.R) * p.HT;
     const int64_t most = cols * ((static_cast<int64_t>(s.max_pages) << s.log2p) / kStep + 2);  // steps at most
     if (most / workers >= INT_MAX) return cudaErrorInvalidValue;  // a range's steps are counted in 32 bits
-    const bool single = most <= static_cast<int64_t>(workers) * kMinSteps;
-    p.max_ranges = single ? workers : workers * kRanges;
+    const bool single = most < static_cast<int64_t>(workers) * kTwo;
+    p.max_ranges = single ? workers : workers * 4;
     p.heads = std::min(p.G, kHeads);
     p.direct = cols <= p.max_ranges;
     uint8_t* base = nullptr;
@@ -871,21 +877,26 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
         e = cudaMemsetAsync(p.next, 0, 4, c.stream);
     }
     if (e == cudaSuccess) {
-        kernel<<<blocks, Ly::THREADS, Ly::SMEM, c.stream>>>(kmap, vmap, q, k, v, K, V, p, single ? kMinSingle : kMinSteps);
+        kernel<<<blocks, Ly::THREADS, Ly::SMEM, c.stream>>>(kmap, vmap, q, k, v, K, V, p);
         note_launch(2);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(p.direct ? cols : p.max_ranges), p.heads);
-        cfg.blockDim = dim3(kJoinWarps * 32);
+        // Few columns are cut into many ranges each and want many warps at them (91 us
+        // against 97 us at 6 x 4 x 8 heads); many columns are cut into few (71 us
+        // against 88 us at 64 x 4 x 16 heads).
+        const bool few = cols * p.heads <= 2 * static_cast<int64_t>(c.num_sms);
+        cfg.blockDim = dim3(few ? 512 : 128);
         cfg.stream = c.stream;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kHeads>, p);
+        e = few ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kHeads, 16>, p)
+                : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kHeads, 4>, p);
     }
     scratch_free(c, base);
     return e;
