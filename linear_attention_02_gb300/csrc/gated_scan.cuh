@@ -332,51 +332,61 @@ __device__ __forceinline__ void st_relaxed(float* p, float x) {
     asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// What a channel knows of the tiles before its chain tile i: the (A, B) of up to
+// kWindow of them, nearest first.  Fetched when the tile begins, under its copy.
+struct Window {
+    unsigned a[kWindow], b[kWindow], near;  // near: the end state of the tile before
+};
+template <typename T>
+__device__ __forceinline__ void peek(Window& w, const Args<T>& p, int i, int64_t at, int64_t step, bool on) {
+#pragma unroll
+    for (int d = 0; d < kWindow; ++d) {
+        const bool in = on && d < i - 1;
+        w.a[d] = in ? ld_relaxed(p.aggA + at + (i - 1 - d) * step) : kUnset;
+        w.b[d] = in ? ld_relaxed(p.aggB + at + (i - 1 - d) * step) : kUnset;
+    }
+    w.near = on && i > 0 ? ld_relaxed(p.incl + at + (i - 1) * step) : kUnset;
+}
+
 // The state that enters chain tile i > 0 (numbered in the chain's direction) of
 // a channel; `at` is the channel's place in tile 0, tiles are `step` words apart.
-// `first`: what the tile before had published when this tile began.  Publishes
-// this tile's own (A, B) if that is not enough (quiet: its end state is out).
+// Publishes the tile's own (A, B) first if the tile before is not done (quiet: its
+// end state is out).  The (A, B) that are out without a gap, nearest first, lead to
+// the end state before them, the first to come; each round trip reads that one, the
+// nearest end state and what is still missing (all words of the window every time
+// slowed the copies down: 210 us against 268 us at 65536 x 2048).
 template <typename T>
-__device__ float look_back(const Args<T>& p, int i, int64_t at, int64_t step, unsigned first, float At,
-                           float Bt, bool quiet) {
-    if (first != kUnset) return __uint_as_float(first);
+__device__ float look_back(const Args<T>& p, Window& w, int i, int64_t at, int64_t step, float At, float Bt,
+                           bool quiet) {
+    if (w.near != kUnset) return __uint_as_float(w.near);
     if (!quiet) {
         st_relaxed(p.aggA + at + i * step, At);
         st_relaxed(p.aggB + at + i * step, Bt);
     }
-    // (A, B) of the tiles before, nearest first, as far as they are out without a
-    // gap; the end state before that run is the first to come.  Only words that
-    // have not come yet are read again.
-    unsigned a[kWindow], b[kWindow];
-#pragma unroll
-    for (int d = 0; d < kWindow; ++d) a[d] = b[d] = kUnset;
-    const int most = min(i - 1, kWindow);
     for (unsigned spin = 0; spin < tcf::kSpinLimit; ++spin) {
-#pragma unroll
-        for (int d = 0; d < kWindow; ++d) {
-            if (d < most && (a[d] == kUnset || b[d] == kUnset)) {
-                const int64_t w = at + (i - 1 - d) * step;
-                a[d] = ld_relaxed(p.aggA + w);
-                b[d] = ld_relaxed(p.aggB + w);
-            }
-        }
         int n = 0;
 #pragma unroll
         for (int d = 0; d < kWindow; ++d)
-            if (n == d && a[d] != kUnset && b[d] != kUnset) n = d + 1;
-        // end states at distance n (before the run) and, when a tile published its
-        // end state alone, the nearest
+            if (n == d && w.a[d] != kUnset && w.b[d] != kUnset) n = d + 1;
         const unsigned far = ld_relaxed(p.incl + at + (i - 1 - n) * step);
         const unsigned near = n ? ld_relaxed(p.incl + at + (i - 1) * step) : kUnset;
-        if (near != kUnset) return __uint_as_float(near);
-        if (far != kUnset) {
-            float h = __uint_as_float(far);
+        float h = __uint_as_float(far);
+        if (far == kUnset && near == kUnset) {
 #pragma unroll
-            for (int d = kWindow - 1; d >= 0; --d)
-                if (d < n) h = fmaf(__uint_as_float(a[d]), h, __uint_as_float(b[d]));
-            return h;
+            for (int d = 0; d < kWindow; ++d) {
+                if (d < i - 1 && (w.a[d] == kUnset || w.b[d] == kUnset)) {
+                    w.a[d] = ld_relaxed(p.aggA + at + (i - 1 - d) * step);
+                    w.b[d] = ld_relaxed(p.aggB + at + (i - 1 - d) * step);
+                }
+            }
+            if (spin > 256) __nanosleep(100);
+            continue;
         }
-        if (spin > 256) __nanosleep(100);
+        if (near != kUnset) return __uint_as_float(near);
+#pragma unroll
+        for (int d = kWindow - 1; d >= 0; --d)
+            if (d < n) h = fmaf(__uint_as_float(w.a[d]), h, __uint_as_float(w.b[d]));
+        return h;
     }
     atomicOr(p.status, tcf::kErrLookback);  // the tiles before never came: report it and go on
     return 0.f;
@@ -444,7 +454,8 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
         const int t0 = q.k * TILE + rg * R, c = q.cb * CB + tid;
         const bool on = tid < CB && c < p.C;  // this thread has a channel of the chain
         const int64_t at = static_cast<int64_t>(q.b) * p.tiles * p.C + c;
-        const unsigned first = on && q.k ? ld_relaxed(p.incl + at + static_cast<int64_t>(q.k - 1) * p.C) : 0u;
+        Window win;
+        peek<T>(win, p, q.k, at, p.C, on);
         landed<T, kVec>(p, bars + (FWD_STAGES > 1 ? st : 0), phase);
         // The thread's rows as one map (A, B); rows past N change nothing.
         float s[kLogit ? R : 1][VEC];
@@ -488,7 +499,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
             const bool cut = fold<CB, kPacked, false>(sa + tid, sb + tid, grp, At, Bt);
             float* out = p.incl + at + static_cast<int64_t>(q.k) * p.C;
             if (cut && !last) st_relaxed(out, Bt);
-            if (q.k) h = look_back<T>(p, q.k, at, p.C, first, At, Bt, cut);
+            if (q.k) h = look_back<T>(p, win, q.k, at, p.C, At, Bt, cut);
             else if (!kPacked && p.init) h = p.init[static_cast<int64_t>(q.b) * p.C + c];
             const float end = cut ? Bt : fmaf(At, h, Bt);
             if (!last && !cut) st_relaxed(out, end);
@@ -579,7 +590,8 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
         const int t0 = q.k * TILE + rg * R, c = q.cb * CB + tid, i = p.tiles - 1 - q.k;
         const bool on = tid < CB && c < p.C;  // this thread has a channel of the chain
         const int64_t at = static_cast<int64_t>(q.b) * p.tiles * p.C + c;
-        const unsigned first = on && i ? ld_relaxed(p.incl + at + static_cast<int64_t>(i - 1) * p.C) : 0u;
+        Window win;
+        peek<T>(win, p, i, at, p.C, on);
         float h0 = 0.f;  // the state that enters the tile
         if (on && q.k) h0 = p.states[at + static_cast<int64_t>(q.k - 1) * p.C];
         else if (on && !kPacked && p.h_init) h0 = p.h_init[static_cast<int64_t>(q.b) * p.C + c];
@@ -646,7 +658,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
             const bool cut = fold<CB, kPacked, true>(sa + tid, sc + tid, grp, At, Bt);
             float* out = p.incl + at + static_cast<int64_t>(i) * p.C;
             if (cut && !last) st_relaxed(out, Bt);
-            if (i) y = look_back<T>(p, i, at, p.C, first, At, Bt, cut);
+            if (i) y = look_back<T>(p, win, i, at, p.C, At, Bt, cut);
             else if (!kPacked && p.init) y = p.init[static_cast<int64_t>(q.b) * p.C + c];
             const float end = cut ? Bt : fmaf(At, y, Bt);
             if (!last && !cut) st_relaxed(out, end);
