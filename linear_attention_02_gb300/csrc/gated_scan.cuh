@@ -67,7 +67,6 @@ struct Args {
     unsigned total;             // B * tiles * ncb
     const int* starts;          // packed sequences
     int S;
-    const int* tile_first;      // [tiles + 1] first boundary at or after a tile's first row
     const float* init;          // forward: h_init; backward: dh_final (state entering the chain)
     float* fin;                 // forward: h_final; backward: dh_init
     const float* h_init;        // backward: the forward's h_init
@@ -282,11 +281,22 @@ __device__ __forceinline__ void row_info(const Args<T>& p, int k, int* info, uns
     static_assert(TILE == 32 * LR && R == LR * PER && (PER == 1 || PER == 2), "lanes over rows");
     const int tid = threadIdx.x, row0 = k * TILE;
     for (int i = tid; i <= TILE; i += NT) info[i] = -1;
+    // f0, the first boundary i in 0 .. S with starts[i] >= row0 (S + 1 if none): 32
+    // probes a round trip, every warp for itself
+    int f0 = 0, f1 = p.S + 1;
+    while (f1 - f0 > 0) {
+        const int step = (f1 - f0 + 31) / 32, i = f0 + (tid & 31) * step;
+        const bool before = i < f1 && min(max(p.starts[i], 0), p.N) < row0;
+        const int n = __popc(__ballot_sync(0xffffffffu, before));  // probes before the tile
+        f1 = n < 32 ? min(f1, f0 + n * step) : f1;
+        f0 = n ? f0 + (n - 1) * step + 1 : f0;
+        if (n == 0) break;
+    }
     __syncthreads();
-    const int f0 = p.tile_first[k], f1 = p.tile_first[k + 1];
-    for (int i = f0 + tid; i <= min(f1, p.S); i += NT) {
+    for (int i = f0 + tid; i <= p.S; i += NT) {
         const int r = min(max(p.starts[i], 0), p.N) - row0;
-        if (r >= 0 && r <= TILE) atomicMax(&info[r], i);  // of equal boundaries the last: the sequence with rows
+        if (r > TILE) break;
+        if (r >= 0) atomicMax(&info[r], i);  // of equal boundaries the last: the sequence with rows
     }
     __syncthreads();
     if (tid < 32) {  // owners: running maximum over the rows
@@ -398,6 +408,19 @@ constexpr size_t smem_bytes() {
            (kPacked ? sizeof(int) * (TILE + 4 + RG) : 0) + 16;
 }
 
+// States of empty packed sequences (to = from, or 0), over all warps of the grid.
+template <typename T>
+__device__ __forceinline__ void empty_sequences(const Args<T>& p, const float* from, float* to) {
+    if (!to) return;
+    const int lane = threadIdx.x & 31, all = gridDim.x * (NT / 32);
+    for (int i = blockIdx.x * (NT / 32) + threadIdx.x / 32; i < p.S; i += all) {
+        const int a = min(max(p.starts[i], 0), p.N), b = min(max(p.starts[i + 1], 0), p.N);
+        if (a < b) continue;
+        const int64_t row = static_cast<int64_t>(i) * p.C;
+        for (int c = lane; c < p.C; c += 32) to[row + c] = from ? from[row + c] : 0.f;
+    }
+}
+
 // One channel's fold over the row groups: the tile's (A, B), and whether a row
 // group replaces the state (its "begin" bit, or for the backward pass "end").
 template <int CB, bool kPacked, bool kRev>
@@ -444,6 +467,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
         tile = *snext;
         __syncthreads();
     }
+    if constexpr (kPacked) empty_sequences(p, p.init, p.fin);
     if (tile < p.total) issue<T, kVec, 2>(p, maps, place_of<T, false>(p, tile), stages, bars);
     for (int st = 0; tile < p.total; st ^= 1) {
         const Place q = place_of<T, false>(p, tile);
@@ -580,6 +604,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
         tile = *snext;
         __syncthreads();
     }
+    if constexpr (kPacked) empty_sequences(p, p.init, p.fin);
     if (tile < p.total) issue<T, kVec, 3>(p, maps, place_of<T, true>(p, tile), stages, bars);
     for (int st = 0; tile < p.total; st ^= 1) {
         const Place q = place_of<T, true>(p, tile);
@@ -743,32 +768,6 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
         tile = next;
     }
     if (kVec && !kPacked && tid == 0) tc::tma_store_wait_read();  // the block's memory outlives its outputs
-}
-
-// Packed calls: each tile's first boundary, the states of empty sequences
-// (to = from, or 0), and the chain's words unset.
-static __global__ void scan_prepare_kernel(const int* __restrict__ starts, int S, int N, int C, int tiles,
-                                           int* __restrict__ tile_first, const float* __restrict__ from,
-                                           float* __restrict__ to, unsigned* __restrict__ chain, size_t words) {
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const int64_t all = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (size_t i = id; i < words; i += all) chain[i] = kUnset;
-    for (int64_t k = id; k <= tiles; k += all) {
-        const int64_t row = k * TILE;
-        int lo = 0, hi = S + 1;  // first i in 0 .. S with starts[i] >= row, S + 1 if none
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (min(max(starts[mid], 0), N) < row) lo = mid + 1;
-            else hi = mid;
-        }
-        tile_first[k] = lo;
-    }
-    if (!to) return;
-    const int lane = threadIdx.x & 31;
-    for (int64_t i = id >> 5; i < S; i += all >> 5) {
-        if (min(max(starts[i], 0), N) < min(max(starts[i + 1], 0), N)) continue;
-        for (int c = lane; c < C; c += 32) to[i * C + c] = from ? from[i * C + c] : 0.f;
-    }
 }
 
 }  // namespace scan

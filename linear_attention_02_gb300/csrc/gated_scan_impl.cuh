@@ -7,18 +7,16 @@ namespace {
 
 using namespace scan;
 
-// Scratch of one pass: [ticket, A, B, end states (unless they go to the caller's
-// checkpoints)], all unset at first, then per-tile first boundaries of a packed call.
+// Scratch of one pass: ticket, A, B, end states (unless they go to the caller's
+// checkpoints), all unset at first.
 struct Parts {
-    size_t states, words, first, bytes;
+    size_t states, bytes;
 };
-Parts parts_of(int B, int N, int C, bool packed, bool own_incl) {
+Parts parts_of(int B, int N, int C, bool own_incl) {
     const size_t tiles = (static_cast<size_t>(N) + TILE - 1) / TILE;
     Parts s = {};
     s.states = tiles > 1 ? static_cast<size_t>(B) * tiles * C : 0;
-    s.words = s.states ? 4 + (own_incl ? 3 : 2) * s.states : 0;
-    s.first = plan::up256(s.words * 4);
-    s.bytes = s.first + (packed ? (tiles + 1) * 4 : 0);
+    s.bytes = s.states ? 4 * (4 + (own_incl ? 3 : 2) * s.states) : 0;
     return s;
 }
 
@@ -60,7 +58,7 @@ cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl) {
     for (int i = 0; vec && !packed && i < 2; ++i)
         if (cudaError_t m = outs[i] ? stream_map<T>(&maps.o[i], outs[i], a.B, a.N, a.C) : cudaSuccess) return m;
 
-    const Parts s = parts_of(a.B, a.N, a.C, packed, own_incl);
+    const Parts s = parts_of(a.B, a.N, a.C, own_incl);
     uint8_t* base = nullptr;
     cudaError_t e = cudaSuccess;
     if (s.bytes && (e = scratch_alloc(c, reinterpret_cast<void**>(&base), s.bytes)) != cudaSuccess) return e;
@@ -71,17 +69,7 @@ cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl) {
         if (own_incl) a.incl = a.aggB + s.states;
         else e = cudaMemsetAsync(a.incl, 0xFF, s.states * 4, c.stream);
     }
-    int* first = reinterpret_cast<int*>(base + s.first);
-    if (packed) {
-        a.tile_first = first;
-        const size_t work = std::max({s.words, tiles + 1, static_cast<size_t>(a.S) * 32});
-        const int blocks = static_cast<int>(std::min<size_t>((work + 255) / 256, 4 * static_cast<size_t>(c.num_sms)));
-        scan_prepare_kernel<<<blocks, 256, 0, c.stream>>>(a.starts, a.S, a.N, a.C, a.tiles, first, a.init, a.fin,
-                                                          a.ticket, s.words);
-        note_launch();
-    } else if (s.words && e == cudaSuccess) {
-        e = cudaMemsetAsync(base, 0xFF, s.words * 4, c.stream);
-    }
+    if (s.bytes && e == cudaSuccess) e = cudaMemsetAsync(base, 0xFF, s.bytes, c.stream);
 
 #define LA_SCAN_RUN(K, SMEM)                                                                       \
     {                                                                                              \
@@ -160,11 +148,11 @@ cudaError_t gated_scan_backward(const LaunchCtx& c, const T* A, const T* X, cons
     return e;
 }
 
-size_t LA_SCAN_SCRATCH(int B, int N, int C, bool packed, bool backward, bool ckpt) {
-    const size_t pass = parts_of(B, N, C, packed, backward || !ckpt).bytes;
+size_t LA_SCAN_SCRATCH(int B, int N, int C, bool backward, bool ckpt) {
+    const size_t pass = parts_of(B, N, C, backward || !ckpt).bytes;
     if (!backward || ckpt || N <= TILE) return pass;
     // the states, and on top of them the larger of the two passes, one after the other
-    const size_t fwd = parts_of(B, N, C, packed, false).bytes;
+    const size_t fwd = parts_of(B, N, C, false).bytes;
     return sizeof(float) * B * ((static_cast<size_t>(N) + TILE - 1) / TILE) * C + std::max(pass, fwd);
 }
 
