@@ -29,7 +29,8 @@
  *   frees caller memory.  Per-call scratch (span states, gradient rows) is
  *   taken stream-ordered from a library-owned CUDA memory pool of the current
  *   device and given back on the same stream; la_workspace_bytes gives its
- *   size for each call.
+ *   size for each call (the gated scan's and the paged cache's calls have
+ *   functions of their own).
  * - Errors: a status code; no exception or abort crosses the ABI.  On error,
  *   la_last_error_message() gives a one-line reason (per host thread).
  *
@@ -253,9 +254,12 @@ la_status la_softmax_decode_step(const void* q, const void* k, const void* v, vo
  *         (of an empty sequence: h_init, or 0)
  *   Ckpt  fp32, nullable (written) la_gated_scan_ckpt_floats(B, N, C) words: the
  *         running state at every 128th row, for the backward
- * Decays lie in [-1, 1]; the state is fp32 throughout.  A sequence's rows do
- * not depend on other sequences, whatever values those hold.  Out, h_final and
- * Ckpt may not alias inputs or each other.
+ * Decays lie in [-1, 1]; the state is fp32 throughout.  Rows are summed up in
+ * parts, whose products of decays may round to 0: behind an infinite or NaN
+ * state, the rows of its channel and sequence are infinite or NaN.  A sequence's
+ * rows do not depend on other sequences, whatever values those hold.  Out,
+ * h_final and Ckpt may not alias inputs or each other.  Results do not depend on
+ * the run: every sum has a fixed order.
  */
 typedef enum { LA_GATE_DECAY = 0, LA_GATE_LOGIT = 1 } la_gate_form;
 la_status la_forward_gated_scan(const void* A, const void* X, void* Out, int B, int N, int C,
@@ -265,6 +269,12 @@ la_status la_forward_gated_scan(const void* A, const void* X, void* Out, int B, 
 /* Size in fp32 words of the gated scan's checkpoints: B * ceil(N / 128) * C, or
  * 0 for non-positive sizes.  Pure arithmetic; no device call. */
 size_t la_gated_scan_ckpt_floats(int B, int N, int C);
+
+/* Scratch bytes that one la_forward_gated_scan (backward == 0) or
+ * la_backward_gated_scan call takes from the library pool, with or without
+ * checkpoints; SIZE_MAX for sizes that the call refuses.  Pure arithmetic.
+ * la_gated_scan_decode_step takes none. */
+size_t la_gated_scan_workspace_bytes(int backward, int B, int N, int C, la_dtype dtype, int ckpt_given);
 
 /*
  * Gradient of la_forward_gated_scan: with s_t the decay and g_t the whole
@@ -357,12 +367,21 @@ la_status la_paged_append(const void* k, const void* v, void* K_pages, void* V_p
  *   scale 0 means 1 / sqrt(D)
  * A request without a position has out 0 and lse -infinity.  Positions whose
  * page is out of range are left out.  D in {32, 64, 128}, Hq a multiple of Hkv.
- * No page may be held by two requests that append to it.
+ * Reads one key and one value row per position and key head, whatever Hq / Hkv;
+ * max_pages * page_size < 2^30.  No page may be held by two requests that append
+ * to it.  Results do not depend on the run.
  */
 la_status la_paged_decode_step(const void* q, const void* k, const void* v, void* K_pages,
                                void* V_pages, const int* block_table, const int* cached_lens, float* out,
                                float* lse, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
                                int max_pages, int window, float scale, la_dtype dtype, void* stream);
+
+/* Scratch bytes that one la_paged_decode_step or la_page_map call takes from the
+ * library pool (la_paged_append takes none); SIZE_MAX for sizes that the call
+ * refuses.  num_sms as in la_workspace_bytes. */
+size_t la_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int page_size, int max_pages,
+                                       la_dtype dtype, int num_sms);
+size_t la_page_map_workspace_bytes(int R);
 
 /*
  * la_forward_noncausal with no device allocation.  The paper has no

@@ -418,6 +418,31 @@ def la_gated_scan_ckpt_floats(B, N, C):
     return int(_lib.la_gated_scan_ckpt_floats(B, N, C))
 
 
+def _bytes(n):
+    if n == _native.SIZE_MAX:
+        raise LinAttnError(_native.LA_ERR_INVALID_ARG, la_last_error_message())
+    return int(n)
+
+
+def la_gated_scan_workspace_bytes(B, N, C, dtype, backward=False, ckpt_given=False):
+    """Scratch bytes of one la_forward_gated_scan or la_backward_gated_scan call."""
+    if dtype not in _DT:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return _bytes(_lib.la_gated_scan_workspace_bytes(int(backward), B, N, C, _DT[dtype], int(ckpt_given)))
+
+
+def la_paged_decode_workspace_bytes(R, Hq, Hkv, D, page_size, max_pages, dtype, num_sms=0):
+    """Scratch bytes of one la_paged_decode_step call; num_sms <= 0 asks the current device."""
+    if dtype not in _DT:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return _bytes(_lib.la_paged_decode_workspace_bytes(R, Hq, Hkv, D, page_size, max_pages, _DT[dtype], num_sms))
+
+
+def la_page_map_workspace_bytes(R):
+    """Scratch bytes of one la_page_map call over R requests."""
+    return _bytes(_lib.la_page_map_workspace_bytes(R))
+
+
 def _check_scan_ckpt(c, name, B, N, C, dev):
     n = la_gated_scan_ckpt_floats(B, N, C)
     if not isinstance(c, torch.Tensor) or c.numel() != n:

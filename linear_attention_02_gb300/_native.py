@@ -40,6 +40,9 @@ SIGNATURES = {
     "la_page_map": [_P, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P],
     "la_paged_append": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P],
     "la_paged_decode_step": [_P, _P, _P, _P, _P, _P, _P, _F, _F, _I, _I, _I, _I, _I, _I, _I, _I, _R, _I, _P],
+    "la_gated_scan_workspace_bytes": [_I, _I, _I, _I, _I, _I],
+    "la_paged_decode_workspace_bytes": [_I, _I, _I, _I, _I, _I, _I, _I],
+    "la_page_map_workspace_bytes": [_I],
     "la_debug_withhold_publication": [_I, ctypes.c_uint],
     "la_check_device_status": [_P],
     "la_selftest_expired_waits": [_P],
@@ -49,6 +52,9 @@ SIGNATURES = {
 }
 _RESTYPES = {"la_status_string": ctypes.c_char_p, "la_last_error_message": ctypes.c_char_p,
              "la_causal_ckpt_floats": ctypes.c_size_t, "la_gated_scan_ckpt_floats": ctypes.c_size_t,
+             "la_gated_scan_workspace_bytes": ctypes.c_size_t,
+             "la_paged_decode_workspace_bytes": ctypes.c_size_t,
+             "la_page_map_workspace_bytes": ctypes.c_size_t,
              "la_workspace_bytes": ctypes.c_size_t,
              "la_scratch_peak_bytes": ctypes.c_size_t,
              "la_kernel_launch_count": ctypes.c_uint64}

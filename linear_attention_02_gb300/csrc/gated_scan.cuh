@@ -24,10 +24,18 @@
 // whichever it finds, since the end state of a tile is always fma(A, state
 // before, B).  A published word is its own flag: the arrays start as all ones, a
 // NaN that no arithmetic gives, so neither side needs a fence (flags beside the
-// data, with their fences, took 1.5 us a hop of the chain).
+// data, with their fences, took 1.5 us a tile in series: 786 us at 65536 x 2048).
 // Tiles are numbered in time order and taken by an atomic ticket, so a tile only
 // waits for tiles that running blocks hold, each block working its own in
 // ascending order: the lowest unfinished one can always go on.
+//
+// Measured (measured copy bandwidth 6.79 TB/s): fp32, 4 x 8192 x 1024, forward 68 us
+// (5.9 TB/s), backward 107 us (6.3 TB/s); bf16 logit form, the same rows, 51 us and
+// 77 us (4.0 and 4.4 TB/s); bf16, 65536 x 2048, forward 169 us (4.8 TB/s).  What is
+// lost there is the chain's wait: without it the same kernels take 38, 61 and 121 us.
+// A word takes 1.3 us from one SM to another and more while the memory is busy, and a
+// tile waits for the slowest of those before it.  It is worst with few channel blocks
+// (B C / 64 below the number of SMs), where many tiles of one chain are under way.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -48,7 +56,13 @@ constexpr int R = 8;                    // rows of a thread
 constexpr int LANES = 8;                // threads across a row: 128 bytes
 constexpr int RG = NT / LANES;          // row groups of a tile
 constexpr int TILE = RG * R;            // rows of a tile
-constexpr int FWD_STAGES = 1, FWD_BLOCKS = 5, BWD_STAGES = 1, BWD_BLOCKS = 3;
+// Blocks per SM, by shared memory (42 KB forward, 63 KB backward a block) and registers.
+// A block waits for its copy, then for the chain: more blocks with one stage each beat
+// fewer with two (51 us against 58 us forward at 4 x 8192 x 1024 bf16).
+template <typename T, bool kLogit>
+constexpr int forward_blocks() { return sizeof(T) == 2 && kLogit ? 4 : 5; }
+template <typename T>
+constexpr int backward_blocks() { return sizeof(T) == 2 ? 3 : 4; }
 static_assert(TILE == plan::kScanTile, "checkpoints lie at tile borders");
 
 template <typename T>
@@ -329,7 +343,8 @@ __device__ __forceinline__ void row_info(const Args<T>& p, int k, int* info, uns
 }
 
 constexpr unsigned kUnset = 0xFFFFFFFFu;  // a word that nothing has been published in
-constexpr int kWindow = 8;                // tiles looked back over at once
+constexpr int kWindow = 8;                // tiles looked back over at once (4: 61 us against 45 us
+                                          // at 65536 x 256; 16: registers, 174 us against 169 us at 65536 x 2048)
 
 __device__ __forceinline__ unsigned ld_relaxed(const float* p) {
     unsigned v;
@@ -404,7 +419,7 @@ __device__ float look_back(const Args<T>& p, Window& w, int i, int64_t at, int64
 
 template <typename T, bool kPacked, int STREAMS>
 constexpr size_t smem_bytes() {
-    return static_cast<size_t>(STREAMS == 2 ? FWD_STAGES : BWD_STAGES) * STREAMS * R * NT * 16 + sizeof(float) * STREAMS * RG * Geo<T>::CB +
+    return static_cast<size_t>(STREAMS) * R * NT * 16 + sizeof(float) * STREAMS * RG * Geo<T>::CB +
            (kPacked ? sizeof(int) * (TILE + 4 + RG) : 0) + 16;
 }
 
@@ -441,22 +456,22 @@ __device__ __forceinline__ bool fold(const float* a, const float* b, const unsig
 }
 
 template <typename T, bool kLogit, bool kPacked, bool kVec>
-__global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 : FWD_BLOCKS) scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(NT, forward_blocks<T, kLogit>())
+scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
     extern __shared__ __align__(128) uint8_t sm[];
-    uint4* stages = reinterpret_cast<uint4*>(sm);
-    float* sa = reinterpret_cast<float*>(stages + FWD_STAGES * 2 * R * NT);
+    uint4* stage = reinterpret_cast<uint4*>(sm);
+    float* sa = reinterpret_cast<float*>(stage + 2 * R * NT);
     float* sb = sa + RG * CB;
     int* info = reinterpret_cast<int*>(sb + RG * CB);
     unsigned* grp = reinterpret_cast<unsigned*>(info + (kPacked ? TILE + 4 : 0));
     unsigned* snext = grp + (kPacked ? RG : 0);
     const int tid = threadIdx.x, rg = tid / LANES;
 
-    __shared__ uint64_t bars[2];
+    __shared__ uint64_t bar;
     uint32_t phase = 0;
     if (kVec && tid == 0) {
-        tc::mbar_init(bars, 1);
-        tc::mbar_init(bars + 1, 1);
+        tc::mbar_init(&bar, 1);
         tc::fence_mbar_init();
     }
     __syncthreads();
@@ -468,10 +483,9 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
         __syncthreads();
     }
     if constexpr (kPacked) empty_sequences(p, p.init, p.fin);
-    if (tile < p.total) issue<T, kVec, 2>(p, maps, place_of<T, false>(p, tile), stages, bars);
-    for (int st = 0; tile < p.total; st ^= 1) {
+    if (tile < p.total) issue<T, kVec, 2>(p, maps, place_of<T, false>(p, tile), stage, &bar);
+    while (tile < p.total) {
         const Place q = place_of<T, false>(p, tile);
-        uint4* stage = stages + (FWD_STAGES > 1 ? st : 0) * (2 * R * NT);
         unsigned mine = 0;
         if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
         if constexpr (kPacked) row_info<T>(p, q.k, info, grp);
@@ -480,7 +494,8 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
         const int64_t at = static_cast<int64_t>(q.b) * p.tiles * p.C + c;
         Window win;
         peek<T>(win, p, q.k, at, p.C, on);
-        landed<T, kVec>(p, bars + (FWD_STAGES > 1 ? st : 0), phase);
+        landed<T, kVec>(p, &bar, phase);
+        phase ^= 1u;
         // The thread's rows as one map (A, B); rows past N change nothing.
         float s[kLogit ? R : 1][VEC];
         float A[VEC], Bv[VEC];
@@ -515,8 +530,6 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
         if (tid == 0) *snext = mine;
         __syncthreads();
         const unsigned next = *snext;
-        if (FWD_STAGES > 1 && next < p.total)  // every thread is done with the tile before
-            issue<T, kVec, 2>(p, maps, place_of<T, false>(p, next), stages + (st ^ 1) * (2 * R * NT), bars + (st ^ 1));
         if (on) {
             const bool last = q.k + 1 == p.tiles;
             float At, Bt, h = 0.f;
@@ -561,14 +574,12 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
             }
         }
         if (kVec && !kPacked && p.O) tc::fence_proxy_async();
-        if (kPacked || kVec) __syncthreads();  // the stage and info are free
+        if (kPacked || kVec) __syncthreads();  // every thread is done with the stage and info
         if (kVec && !kPacked && p.O && tid == 0) {
             tc::tma_store_3d(&maps.o[0], stage, q.cb * CB, q.k * TILE, q.b);
             tc::tma_store_commit();
         }
-        if (FWD_STAGES == 1 && next < p.total)
-            issue<T, kVec, 2>(p, maps, place_of<T, false>(p, next), stages, bars);
-        if (FWD_STAGES == 1 || st) phase ^= 1u;
+        if (next < p.total) issue<T, kVec, 2>(p, maps, place_of<T, false>(p, next), stage, &bar);
         tile = next;
     }
     if (kVec && !kPacked && tid == 0) tc::tma_store_wait_read();  // the block's memory outlives its outputs
@@ -577,11 +588,12 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 && kLogit ? FWD_BLOCKS - 1 
 // Backward: the forward state enters each tile from its checkpoint (no chain);
 // the carry c comes down the chain from the last tile.
 template <typename T, bool kLogit, bool kPacked, bool kVec>
-__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS + 1) scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(NT, backward_blocks<T>())
+scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
     extern __shared__ __align__(128) uint8_t sm[];
-    uint4* stages = reinterpret_cast<uint4*>(sm);
-    float* sa = reinterpret_cast<float*>(stages + BWD_STAGES * 3 * R * NT);
+    uint4* stage = reinterpret_cast<uint4*>(sm);
+    float* sa = reinterpret_cast<float*>(stage + 3 * R * NT);
     float* sb = sa + RG * CB;
     float* sc = sb + RG * CB;
     int* info = reinterpret_cast<int*>(sc + RG * CB);
@@ -589,11 +601,10 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
     unsigned* snext = grp + (kPacked ? RG : 0);
     const int tid = threadIdx.x, rg = tid / LANES;
 
-    __shared__ uint64_t bars[2];
+    __shared__ uint64_t bar;
     uint32_t phase = 0;
     if (kVec && tid == 0) {
-        tc::mbar_init(bars, 1);
-        tc::mbar_init(bars + 1, 1);
+        tc::mbar_init(&bar, 1);
         tc::fence_mbar_init();
     }
     __syncthreads();
@@ -605,10 +616,9 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
         __syncthreads();
     }
     if constexpr (kPacked) empty_sequences(p, p.init, p.fin);
-    if (tile < p.total) issue<T, kVec, 3>(p, maps, place_of<T, true>(p, tile), stages, bars);
-    for (int st = 0; tile < p.total; st ^= 1) {
+    if (tile < p.total) issue<T, kVec, 3>(p, maps, place_of<T, true>(p, tile), stage, &bar);
+    while (tile < p.total) {
         const Place q = place_of<T, true>(p, tile);
-        uint4* stage = stages + (BWD_STAGES > 1 ? st : 0) * (3 * R * NT);
         unsigned mine = 0;
         if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
         if constexpr (kPacked) row_info<T>(p, q.k, info, grp);
@@ -620,7 +630,8 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
         float h0 = 0.f;  // the state that enters the tile
         if (on && q.k) h0 = p.states[at + static_cast<int64_t>(q.k - 1) * p.C];
         else if (on && !kPacked && p.h_init) h0 = p.h_init[static_cast<int64_t>(q.b) * p.C + c];
-        landed<T, kVec>(p, bars + (BWD_STAGES > 1 ? st : 0), phase);
+        landed<T, kVec>(p, &bar, phase);
+        phase ^= 1u;
         float s[kLogit ? R : 1][VEC];
         float A[VEC], Bf[VEC], Br[VEC];
 #pragma unroll
@@ -675,8 +686,6 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
         if (tid == 0) *snext = mine;
         __syncthreads();
         const unsigned next = *snext;
-        if (BWD_STAGES > 1 && next < p.total)  // every thread is done with the tile before
-            issue<T, kVec, 3>(p, maps, place_of<T, true>(p, next), stages + (st ^ 1) * (3 * R * NT), bars + (st ^ 1));
         if (on) {
             const bool last = q.k == 0;
             float At, Bt, y = 0.f, h = h0;
@@ -756,15 +765,13 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? BWD_BLOCKS : BWD_BLOCKS +
             }
         }
         if (kVec && !kPacked) tc::fence_proxy_async();
-        if (kPacked || kVec) __syncthreads();  // the stage and info are free
+        if (kPacked || kVec) __syncthreads();  // every thread is done with the stage and info
         if (kVec && !kPacked && tid == 0) {
             tc::tma_store_3d(&maps.o[0], stage, q.cb * CB, q.k * TILE, q.b);
             tc::tma_store_3d(&maps.o[1], stage + TILE * LANES, q.cb * CB, q.k * TILE, q.b);
             tc::tma_store_commit();
         }
-        if (BWD_STAGES == 1 && next < p.total)
-            issue<T, kVec, 3>(p, maps, place_of<T, true>(p, next), stages, bars);
-        if (BWD_STAGES == 1 || st) phase ^= 1u;
+        if (next < p.total) issue<T, kVec, 3>(p, maps, place_of<T, true>(p, next), stage, &bar);
         tile = next;
     }
     if (kVec && !kPacked && tid == 0) tc::tma_store_wait_read();  // the block's memory outlives its outputs

@@ -631,6 +631,40 @@ la_status la_softmax_decode_step(const void* q, const void* k, const void* v, vo
     return finish(e, fn);
 }
 
+size_t la_gated_scan_workspace_bytes(int backward, int B, int N, int C, la_dtype dtype, int ckpt_given) {
+    static const char* fn = "la_gated_scan_workspace_bytes";
+    la_status s = check_scan(fn, B, N, C, dtype, LA_GATE_DECAY, nullptr, 0);
+    if (s != LA_OK) return SIZE_MAX;
+    if ((size_t)B * N * C == 0) return 0;
+    return dtype == LA_DTYPE_F32 ? gated_scan_scratch_f32(B, N, C, backward != 0, ckpt_given != 0)
+                                 : gated_scan_scratch_bf16(B, N, C, backward != 0, ckpt_given != 0);
+}
+
+size_t la_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int page_size, int max_pages,
+                                       la_dtype dtype, int num_sms) {
+    static const char* fn = "la_paged_decode_workspace_bytes";
+    int log2p = 0;
+    if (check_pages(fn, 0, page_size, &log2p) != LA_OK) return SIZE_MAX;
+    if (dtype != LA_DTYPE_F32 && dtype != LA_DTYPE_BF16)
+        return fail(LA_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dtype), SIZE_MAX;
+    if (!head_ok(D))
+        return fail(LA_ERR_UNSUPPORTED, "%s: D=%d, supported head sizes are 32, 64, 128", fn, D), SIZE_MAX;
+    if (R < 0 || Hq < 0 || Hkv < 0 || max_pages < 0 || (Hq && (Hkv == 0 || Hq % Hkv)) ||
+        (unsigned long long)max_pages * page_size >= (1ull << 30))
+        return fail(LA_ERR_INVALID_ARG, "%s: sizes R=%d Hq=%d Hkv=%d max_pages=%d", fn, R, Hq, Hkv, max_pages),
+               SIZE_MAX;
+    if (num_sms <= 0) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return cuda_fail(e, fn), SIZE_MAX;
+    }
+    const PagedShape sh = {R, Hq, Hkv, 0, log2p, max_pages, 0, 1.f};
+    return paged_decode_scratch(sh, D, dtype == LA_DTYPE_BF16, num_sms);
+}
+
+size_t la_page_map_workspace_bytes(int R) { return R < 0 ? SIZE_MAX : plan::page_map_scratch(R); }
+
 size_t la_gated_scan_ckpt_floats(int B, int N, int C) {
     if (B <= 0 || N <= 0 || C <= 0) return 0;
     return (size_t)B * (((size_t)N + plan::kScanTile - 1) / plan::kScanTile) * (size_t)C;
@@ -795,8 +829,8 @@ la_status la_paged_decode_step(const void* q, const void* k, const void* v, void
     if (!std::isfinite(scale)) return fail(LA_ERR_INVALID_ARG, "%s: scale is not finite", fn);
     if ((k == nullptr) != (v == nullptr))
         return fail(LA_ERR_INVALID_ARG, "%s: k and v must both be given or both NULL", fn);
-    if ((unsigned long long)max_pages * page_size >= (1ull << 31) - 1)
-        return fail(LA_ERR_INVALID_ARG, "%s: max_pages=%d of %d positions: 2^31 - 1 positions or more", fn,
+    if ((unsigned long long)max_pages * page_size >= (1ull << 30))
+        return fail(LA_ERR_INVALID_ARG, "%s: max_pages=%d of %d positions: 2^30 positions or more", fn,
                     max_pages, page_size);
     if ((unsigned long long)R * Hq * D >= (1ull << 31) ||
         (unsigned long long)num_pages * page_size * (Hkv ? Hkv : 1) >= (1ull << 40) / D)

@@ -189,6 +189,8 @@ struct PagedShape {
     int R, Hq, Hkv, num_pages, log2p, max_pages, window;
     float scale;
 };
+// Its scratch bytes (the shape's num_pages, window and scale do not matter).
+size_t paged_decode_scratch(const PagedShape& s, int D, bool bf16, int num_sms);
 template <typename T, int D>
 cudaError_t paged_decode_step(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K, T* V,
                               const int* table, const int* lens, float* out, float* lse,

@@ -7,9 +7,10 @@
 // Bound by memory: every key and value is read once for all query heads that
 // share it (2 D elements a position and key head).  The unit of work is a step:
 // 16 positions of one key head, for up to 16 of its query heads.  The steps of
-// all requests, request-major, are cut into equal ranges, one per warp of a grid
-// that fills the GPU once, whatever the lengths: each block sums up the requests'
-// step counts from their lengths on the device, so a captured call follows them.
+// all requests, request-major, are cut into equal ranges, one to four for each warp of
+// a grid that fills the GPU once, whatever the lengths: each block sums up the requests'
+// step counts from their lengths on the device, so a captured call follows them.  A
+// warp's first range has its own number, the next ones are taken from a counter.
 //
 // A warp works alone, on a ring of steps of its own in shared memory that TMA fills
 // (one box of 16 rows x 128 bytes at a time, 128-byte swizzle), so blocks have no
@@ -26,19 +27,23 @@
 // arithmetic.  fp32 storage: m16n8k8 tf32 products of two-term splits (relative
 // error 2^-21).  With up to 8 query heads a key head (kHeads = 8), the operand's
 // rows 8 to 15 hold a second term of the same heads instead of nothing; with more,
-// they hold heads 8 to 15, and heads past 16 take further passes.  (Keys as rows
-// and heads as columns needs fewer products, but the weights must be transposed
-// between the two: 829 us against 760 us at 256 x 16 x 4096 x 64.)
+// they hold heads 8 to 15, and heads past 16 take further passes.
 // The warp-level matrix instruction is enough here: a step of 16 x 64 bf16 keys
 // and values is 4 KB of memory traffic, about 170 cycles of an SM's share of the
 // bandwidth, against 24 small products.
 //
 // Each step's outputs are summed by the matrix unit from zero and added to the running
 // sums in fp32 (summed on through a whole range, the unit's truncation left an error
-// of 3.4e-6 at 4096 positions; so it is KKK2).  The maximum is kept lazily: it is raised, and the sums rescaled, only when a
-// score passes it by more than 2^8, so most steps need no exchange between lanes.
-// A range that starts or ends inside a request leaves partial sums, which a second
+// of 3.4e-6 at 4096 positions; so it is 2.6e-7, at the same time).  The maximum is kept
+// lazily: it is raised, and the sums rescaled, only when a score passes it by more than
+// 2^8, so most steps need no exchange between lanes.  A range that starts or ends inside a request leaves partial sums, which a second
 // small kernel joins in the order of the ranges.
+//
+// Measured (measured copy bandwidth 6.79 TB/s): 256 requests x 16 heads x 4096 positions,
+// D = 64, bf16: 660 us, 6.5 TB/s; D = 128 bf16 with 8 query heads a key head 5.7 TB/s and
+// with 16 heads 4.6 TB/s, fp32 D = 64 5.5 and D = 128 6.1 TB/s, bf16 D = 32 5.3 TB/s: there
+// a step's chain of products and exponentials on the few warps that shared memory leaves
+// room for bounds it.  A small call (4 requests, up to 300 positions) takes 9.3 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -170,7 +175,7 @@ struct Row {
         total = pad ? 0 : len + p.append;
         first = p.s.window && p.s.window < total ? total - p.s.window : 0;
         j0 = first / kStep;
-        j1 = max((total + kStep - 1) / kStep, j0 + 1);
+        j1 = max((total + kStep - 1) / kStep, j0 + 1);  // positions stay below 2^30
     }
     __device__ int steps() const { return pad ? 0 : j1 - j0; }
 };
@@ -753,7 +758,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 // Joins the ranges of a split column, one block a query head: the maximum of the
 // ranges' maxima, then sums scaled to it, in the order of the ranges within each
 // of the block's warps and of the warps.
-template <int D, int kHeads, int kJoinWarps>
+template <int D, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedArgs p) {
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_a[kJoinWarps][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -765,7 +770,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
     if (d.y == 0) return;
     if (!p.direct) col = d.w;
     const int64_t r = col / p.HT;
-    const int c = static_cast<int>(col - r * p.HT), kh = c / p.tiles_per_kh, h0 = (c - kh * p.tiles_per_kh) * kHeads;
+    const int c = static_cast<int>(col - r * p.HT), kh = c / p.tiles_per_kh, h0 = (c - kh * p.tiles_per_kh) * p.heads;
     if (h0 + h >= p.G) return;
     constexpr int E = D / 32;
     float m = -INFINITY, l = 0.f, a[E];
@@ -835,59 +840,79 @@ cudaError_t pool_map(CUtensorMap* m, const void* pool, const PagedShape& s) {
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Grid, ranges and scratch of a call; pure arithmetic.
+struct Plan {
+    int blocks, workers, tiles_per_kh, heads, max_ranges;
+    int64_t cols, most;  // columns; steps at most
+    bool single;         // one range a warp at most
+    size_t part, desc, bytes;
+};
+template <typename T, int D, int kHeads>
+Plan plan_of(const PagedShape& s, int num_sms) {
+    Plan n = {};
+    const int G = s.Hq / s.Hkv;
+    n.blocks = Lay<T, D>::BLOCKS * num_sms;
+    n.workers = n.blocks * Lay<T, D>::WARPS;
+    n.tiles_per_kh = (G + kHeads - 1) / kHeads;
+    n.heads = std::min(G, kHeads);
+    n.cols = static_cast<int64_t>(s.R) * s.Hkv * n.tiles_per_kh;
+    n.most = n.cols * ((static_cast<int64_t>(s.max_pages) << s.log2p) / kStep + 2);
+    n.single = n.most < static_cast<int64_t>(n.workers) * kTwo;
+    n.max_ranges = n.single ? n.workers : n.workers * 4;
+    n.part = plan::up256(sizeof(float) * n.max_ranges * 2 * n.heads * (D + 4));
+    n.desc = sizeof(int4) * n.max_ranges;
+    n.bytes = n.part + n.desc + 16;
+    return n;
+}
+
 template <typename T, int D, int kHeads>
 cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K, T* V, const int* table,
                    const int* lens, float* out, float* lse, const PagedShape& s) {
     using Ly = Lay<T, D>;
     auto* kernel = paged_decode_kernel<T, D, kHeads>;
+    const Plan n = plan_of<T, D, kHeads>(s, c.num_sms);
+    if (n.most / n.workers >= INT_MAX) return cudaErrorInvalidValue;  // a range's steps are counted in 32 bits
     int per_sm = 1;
     cudaError_t e = resident_blocks<paged_decode_kernel<T, D, kHeads>>(c.device, Ly::THREADS, Ly::SMEM, &per_sm);
     if (e != cudaSuccess) return e;
-    const int blocks = per_sm * c.num_sms, workers = blocks * Ly::WARPS;
     PagedArgs p = {};
     p.s = s;
     p.G = s.Hq / s.Hkv;
-    p.tiles_per_kh = (p.G + kHeads - 1) / kHeads;
-    p.HT = s.Hkv * p.tiles_per_kh;
+    p.tiles_per_kh = n.tiles_per_kh;
+    p.HT = s.Hkv * n.tiles_per_kh;
     p.append = k ? 1 : 0;
     p.table = table;
     p.lens = lens;
     p.out = out;
     p.lse = lse;
     p.status = c.status_word;
+    p.max_ranges = n.max_ranges;
+    p.heads = n.heads;
+    p.direct = n.cols <= n.max_ranges;
     CUtensorMap kmap = {}, vmap = {};
     p.tma = s.log2p >= 4 && s.num_pages > 0 && static_cast<int64_t>(s.num_pages) * s.Hkv < INT_MAX;
     if (p.tma && ((e = pool_map<T, D>(&kmap, K, s)) != cudaSuccess || (e = pool_map<T, D>(&vmap, V, s)) != cudaSuccess))
         return e;
-    const int64_t cols = static_cast<int64_t>(s.R) * p.HT;
-    const int64_t most = cols * ((static_cast<int64_t>(s.max_pages) << s.log2p) / kStep + 2);  // steps at most
-    if (most / workers >= INT_MAX) return cudaErrorInvalidValue;  // a range's steps are counted in 32 bits
-    const bool single = most < static_cast<int64_t>(workers) * kTwo;
-    p.max_ranges = single ? workers : workers * 4;
-    p.heads = std::min(p.G, kHeads);
-    p.direct = cols <= p.max_ranges;
     uint8_t* base = nullptr;
-    const size_t part = sizeof(float) * p.max_ranges * 2 * p.heads * (D + 4), desc = sizeof(int4) * p.max_ranges;
-    e = scratch_alloc(c, reinterpret_cast<void**>(&base), plan::up256(part) + desc + 16);
-    if (e != cudaSuccess) return e;
+    if ((e = scratch_alloc(c, reinterpret_cast<void**>(&base), n.bytes)) != cudaSuccess) return e;
     p.part = reinterpret_cast<float*>(base);
-    p.desc = reinterpret_cast<int4*>(base + plan::up256(part));
-    if (!single) {
-        p.next = reinterpret_cast<unsigned*>(base + plan::up256(part) + desc);
+    p.desc = reinterpret_cast<int4*>(base + n.part);
+    if (!n.single) {
+        p.next = reinterpret_cast<unsigned*>(base + n.part + n.desc);
         e = cudaMemsetAsync(p.next, 0, 4, c.stream);
     }
     if (e == cudaSuccess) {
-        kernel<<<blocks, Ly::THREADS, Ly::SMEM, c.stream>>>(kmap, vmap, q, k, v, K, V, p);
-        note_launch(2);
+        kernel<<<n.blocks, Ly::THREADS, Ly::SMEM, c.stream>>>(kmap, vmap, q, k, v, K, V, p);
+        note_launch();
         e = cudaGetLastError();
     }
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(p.direct ? cols : p.max_ranges), p.heads);
+        cfg.gridDim = dim3(static_cast<unsigned>(p.direct ? n.cols : n.max_ranges), n.heads);
         // Few columns are cut into many ranges each and want many warps at them (91 us
         // against 97 us at 6 x 4 x 8 heads); many columns are cut into few (71 us
         // against 88 us at 64 x 4 x 16 heads).
-        const bool few = cols * p.heads <= 2 * static_cast<int64_t>(c.num_sms);
+        const bool few = n.cols * n.heads <= 2 * static_cast<int64_t>(c.num_sms);
         cfg.blockDim = dim3(few ? 512 : 128);
         cfg.stream = c.stream;
         cudaLaunchAttribute at[1];
@@ -895,8 +920,9 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        e = few ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kHeads, 16>, p)
-                : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kHeads, 4>, p);
+        e = few ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 16>, p)
+                : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 4>, p);
+        note_launch();
     }
     scratch_free(c, base);
     return e;
@@ -910,6 +936,19 @@ cudaError_t paged_decode_step(const LaunchCtx& c, const T* q, const T* k, const 
                               const PagedShape& s) {
     return s.Hq / s.Hkv <= 8 ? launch<T, D, 8>(c, q, k, v, K, V, table, lens, out, lse, s)
                              : launch<T, D, 16>(c, q, k, v, K, V, table, lens, out, lse, s);
+}
+
+size_t paged_decode_scratch(const PagedShape& s, int D, bool bf16, int num_sms) {
+    if (s.R == 0 || s.Hq == 0) return 0;
+#define LA_PD_PLAN(T, d) \
+    if (D == d) return s.Hq / s.Hkv <= 8 ? plan_of<T, d, 8>(s, num_sms).bytes : plan_of<T, d, 16>(s, num_sms).bytes;
+    if (bf16) {
+        LA_PD_PLAN(__nv_bfloat16, 32) LA_PD_PLAN(__nv_bfloat16, 64) LA_PD_PLAN(__nv_bfloat16, 128)
+    } else {
+        LA_PD_PLAN(float, 32) LA_PD_PLAN(float, 64) LA_PD_PLAN(float, 128)
+    }
+#undef LA_PD_PLAN
+    return SIZE_MAX;
 }
 
 #define LA_INST_PD(T, D)                                                                          \

@@ -348,3 +348,46 @@ def test_scan_wrapper_refusals():
     with pytest.raises(la.LinAttnError, match="INVALID_ARG"):  # rows not 16-byte aligned
         b = torch.zeros(33, device="cuda")[1:].view(1, 4, 8)
         la.la_forward_gated_scan(b, b)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_scan_starts_outside_the_rows_are_cut(dt):
+    la = _la()
+    x, d = _inputs(1, 300, 40, dt, "decay", 21, 3)
+    bad = torch.tensor([-5, 100, 2 ** 31 - 1, 10 ** 9], dtype=torch.int32, device="cuda")
+    good = torch.tensor([0, 100, 300, 300], dtype=torch.int32, device="cuda")
+    a = la.la_forward_gated_scan(d["A"], d["X"], h_init=d["h0"], seq_starts=bad, return_state=True)
+    b = la.la_forward_gated_scan(d["A"], d["X"], h_init=d["h0"], seq_starts=good, return_state=True)
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    a = la.la_backward_gated_scan(d["A"], d["X"], d["G"], h_init=d["h0"], seq_starts=bad, return_dh_init=True)
+    b = la.la_backward_gated_scan(d["A"], d["X"], d["G"], h_init=d["h0"], seq_starts=good, return_dh_init=True)
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_scan_many_packed_sequences(dt):
+    # 5000 sequences of 0 to 3 rows: borders found among many, several in each row group
+    lens = [(i * 7) % 4 for i in range(5000)]
+    starts = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    _check_all(1, starts[-1] + 9, 24, dt, "decay", starts=starts, seed=22)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [100, 1000])
+def test_scan_scratch_matches_report(dt, N):
+    la = _la()
+    B, C = 2, 136
+    x, d = _inputs(B, N, C, dt, "logit", 23)
+    ck = torch.empty(la.la_gated_scan_ckpt_floats(B, N, C), device="cuda")
+    calls = [(False, False, lambda: la.la_forward_gated_scan(d["A"], d["X"], form="logit")),
+             (False, True, lambda: la.la_forward_gated_scan(d["A"], d["X"], form="logit", ckpt=ck)),
+             (True, True, lambda: la.la_backward_gated_scan(d["A"], d["X"], d["G"], form="logit", Ckpt=ck)),
+             (True, False, lambda: la.la_backward_gated_scan(d["A"], d["X"], d["G"], form="logit"))]
+    for backward, given, call in calls:
+        want = la.la_gated_scan_workspace_bytes(B, N, C, DT[dt], backward=backward, ckpt_given=given)
+        assert (want == 0) == (N == 100)  # one tile: no chain, no scratch
+        torch.cuda.synchronize()
+        la.la_scratch_peak_bytes(reset=True)
+        call()
+        torch.cuda.synchronize()
+        assert want <= la.la_scratch_peak_bytes() <= want + 2 * (2 << 20)

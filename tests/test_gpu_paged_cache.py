@@ -474,3 +474,71 @@ def test_serving_run(dt):
             w, _ = ref.paged_decode(q[r:r + 1], None, None, kk.double().transpose(0, 1)[None], vv.double().transpose(0, 1)[None],
                                     [[0]], [kk.shape[0]])
             assert np.abs(out[r].double().cpu().numpy() - w[0]).max() <= 1e-4
+
+
+# ---------------------------------------------------------------- many ranges, many columns, scratch
+
+def _exact_on_gpu(d, table, lens, window=0):
+    """fp64 outputs and logs of sums without a new row, one request at a time on the GPU."""
+    q, K, V = d["q"], d["K"], d["V"]
+    R, Hq, D = q.shape
+    Hkv, page = K.shape[1], K.shape[2]
+    out = torch.zeros(R, Hq, D, dtype=torch.float64, device="cuda")
+    lse = torch.full((R, Hq), -math.inf, dtype=torch.float64, device="cuda")
+    for r, n in enumerate(lens):
+        if n == 0:
+            continue
+        pages = torch.tensor(table[r][:-(-n // page)], device="cuda")
+        k = K[pages].double().transpose(0, 1).reshape(Hkv, -1, D)[:, :n]
+        v = V[pages].double().transpose(0, 1).reshape(Hkv, -1, D)[:, :n]
+        s = torch.einsum("hgd,hnd->hgn", q[r].double().view(Hkv, -1, D), k) / math.sqrt(D)
+        out[r] = torch.einsum("hgn,hnd->hgd", torch.softmax(s, 2), v).reshape(Hq, D)
+        lse[r] = torch.logsumexp(s, 2).reshape(Hq)
+    return out, lse
+
+
+@pytest.mark.parametrize("dt,R,Hq,Hkv,D,page,most", [
+    ("bf16", 64, 16, 16, 32, 16, 4100),   # four ranges a warp
+    ("bf16", 40, 64, 8, 64, 32, 4000),    # eight query heads a key head
+    ("bf16", 24, 64, 4, 128, 16, 6000),   # sixteen
+    ("f32", 30, 24, 8, 64, 64, 5000),     # three, fp32
+    ("f32", 20, 48, 4, 128, 16, 4000),    # twelve, fp32
+    ("bf16", 4000, 4, 4, 32, 16, 40),     # more columns than ranges
+    ("f32", 9000, 2, 2, 32, 8, 12),       # likewise, pages shorter than a step
+])
+def test_paged_decode_over_many_ranges(dt, R, Hq, Hkv, D, page, most):
+    la = _la()
+    lens = [(i * 7919) % (most + 1) for i in range(R)]
+    g = torch.Generator(device="cuda").manual_seed(R)
+    need = [-(-n // page) for n in lens]
+    P, W = sum(need) + 1, max(need) + 1
+    order, table, at = np.random.RandomState(R).permutation(P).tolist(), [], 0
+    for n in need:
+        table.append(order[at:at + n] + [-1] * (W - n))
+        at += n
+    d = {n: torch.randn(s, generator=g, device="cuda").to(DT[dt]) for n, s in
+         (("q", (R, Hq, D)), ("K", (P, Hkv, page, D)), ("V", (P, Hkv, page, D)))}
+    out, lse = la.la_paged_decode_step(d["q"], None, None, d["K"], d["V"], _i32(table), _i32(lens), return_lse=True)
+    la.la_check_device_status()
+    wo, wl = _exact_on_gpu(d, table, lens)
+    x = {"q": d["q"], "K": d["K"], "V": d["V"], "k": d["K"][0], "v": d["V"][0]}
+    to, tl = _bounds(x, D)
+    assert float((out.double() - wo).abs().max()) <= to
+    some = torch.isfinite(wl)
+    assert torch.equal(torch.isneginf(lse), torch.isneginf(wl))
+    assert float((lse.double() - wl)[some].abs().max()) <= tl
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_paged_decode_scratch_matches_report(dt):
+    la = _la()
+    for Hq, Hkv, D, page, lens in ((8, 2, 64, 16, [300, 5]), (32, 2, 128, 32, [9000, 20000, 1])):
+        x, table = _decode_case(len(lens), Hq, Hkv, D, page, lens, False, dt)
+        d = {n: t.cuda() for n, t in x.items()}
+        tb, ln = _i32(table), _i32(lens)
+        want = la.la_paged_decode_workspace_bytes(len(lens), Hq, Hkv, D, page, tb.shape[1], DT[dt])
+        torch.cuda.synchronize()
+        la.la_scratch_peak_bytes(reset=True)
+        la.la_paged_decode_step(d["q"], None, None, d["K"], d["V"], tb, ln)
+        torch.cuda.synchronize()
+        assert want <= la.la_scratch_peak_bytes() <= want + (2 << 20)

@@ -125,3 +125,27 @@ def test_binding_refuses_host_tensors_and_shapes():
         la.la_paged_append(a, a, a, a, i)
     with pytest.raises(ValueError, match="K_pages"):
         la.la_paged_decode_step(a, None, None, a, a, i, i)
+
+
+def test_workspace_bytes():
+    f = lib.la_gated_scan_workspace_bytes
+    # 257 rows: 3 tiles; A and B (and the end states without checkpoints) of 2 x 3 x 64 words, 4 words of ticket
+    states = 2 * 3 * 64
+    assert f(0, 2, 257, 64, 0, 1) == 4 * (4 + 2 * states)
+    assert f(0, 2, 257, 64, 1, 0) == 4 * (4 + 3 * states)
+    assert f(1, 2, 257, 64, 1, 1) == 4 * (4 + 3 * states)
+    # backward without checkpoints: the states, and the larger of its two passes on top
+    assert f(1, 2, 257, 64, 0, 0) == 4 * states + 4 * (4 + 3 * states)
+    assert f(1, 2, 128, 64, 0, 0) == 0 and f(0, 0, 257, 64, 0, 0) == 0
+    assert f(0, -1, 257, 64, 0, 0) == _native.SIZE_MAX
+    g = lib.la_paged_decode_workspace_bytes
+    # bf16, D = 64: 3 blocks an SM x 4 warps = 12 x 152 warps, one range each (2 x 8 columns of 5 + 2 steps at
+    # most are fewer than 16 a warp): 2 partial results of 4 heads x 68 words, 16 bytes of descriptor, 16 bytes
+    w = 12 * 152
+    up = lambda x: (x + 255) // 256 * 256  # noqa: E731
+    assert g(2, 32, 8, 64, 16, 5, 1, 152) == up(4 * w * 2 * 4 * 68) + 16 * w + 16
+    # long tables: up to four ranges a warp
+    assert g(200, 32, 8, 64, 16, 5000, 1, 152) == up(4 * 4 * w * 2 * 4 * 68) + 16 * 4 * w + 16
+    assert g(2, 32, 8, 48, 16, 5, 1, 152) == _native.SIZE_MAX and g(2, 30, 8, 64, 16, 5, 1, 152) == _native.SIZE_MAX
+    assert lib.la_page_map_workspace_bytes(4096) == 0 and lib.la_page_map_workspace_bytes(5000) == 8 * 5001
+    assert lib.la_page_map_workspace_bytes(-1) == _native.SIZE_MAX
