@@ -486,8 +486,6 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
     if (tile < p.total) issue<T, kVec, 2>(p, maps, place_of<T, false>(p, tile), stage, &bar);
     while (tile < p.total) {
         const Place q = place_of<T, false>(p, tile);
-        unsigned mine = 0;
-        if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
         if constexpr (kPacked) row_info<T>(p, q.k, info, grp);
         const int t0 = q.k * TILE + rg * R, c = q.cb * CB + tid;
         const bool on = tid < CB && c < p.C;  // this thread has a channel of the chain
@@ -527,9 +525,8 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         }
         put<T, kVec>(sa, A);
         put<T, kVec>(sb, Bv);
-        if (tid == 0) *snext = mine;
         __syncthreads();
-        const unsigned next = *snext;
+        unsigned mine = 0;
         if (on) {
             const bool last = q.k + 1 == p.tiles;
             float At, Bt, h = 0.f;
@@ -539,6 +536,9 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
             if (q.k) h = look_back<T>(p, win, q.k, at, p.C, At, Bt, cut);
             else if (!kPacked && p.init) h = p.init[static_cast<int64_t>(q.b) * p.C + c];
             const float end = cut ? Bt : fmaf(At, h, Bt);
+            // The next tile is taken as late as the copy allows: a block that took it
+            // earlier would hold up the chain with it.
+            if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
             if (!last && !cut) st_relaxed(out, end);
             if (!kPacked && last && p.fin) p.fin[static_cast<int64_t>(q.b) * p.C + c] = end;
 #pragma unroll 8
@@ -574,7 +574,9 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
             }
         }
         if (kVec && !kPacked && p.O) tc::fence_proxy_async();
-        if (kPacked || kVec) __syncthreads();  // every thread is done with the stage and info
+        if (tid == 0) *snext = mine;
+        __syncthreads();  // every thread is done with the stage and info
+        const unsigned next = *snext;
         if (kVec && !kPacked && p.O && tid == 0) {
             tc::tma_store_3d(&maps.o[0], stage, q.cb * CB, q.k * TILE, q.b);
             tc::tma_store_commit();
@@ -619,8 +621,6 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
     if (tile < p.total) issue<T, kVec, 3>(p, maps, place_of<T, true>(p, tile), stage, &bar);
     while (tile < p.total) {
         const Place q = place_of<T, true>(p, tile);
-        unsigned mine = 0;
-        if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
         if constexpr (kPacked) row_info<T>(p, q.k, info, grp);
         const int t0 = q.k * TILE + rg * R, c = q.cb * CB + tid, i = p.tiles - 1 - q.k;
         const bool on = tid < CB && c < p.C;  // this thread has a channel of the chain
@@ -683,9 +683,8 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         put<T, kVec>(sa, A);
         put<T, kVec>(sb, Bf);
         put<T, kVec>(sc, Br);
-        if (tid == 0) *snext = mine;
         __syncthreads();
-        const unsigned next = *snext;
+        unsigned mine = 0;
         if (on) {
             const bool last = q.k == 0;
             float At, Bt, y = 0.f, h = h0;
@@ -695,6 +694,7 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
             if (i) y = look_back<T>(p, win, i, at, p.C, At, Bt, cut);
             else if (!kPacked && p.init) y = p.init[static_cast<int64_t>(q.b) * p.C + c];
             const float end = cut ? Bt : fmaf(At, y, Bt);
+            if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
             if (!last && !cut) st_relaxed(out, end);
             if (!kPacked && last && p.fin) p.fin[static_cast<int64_t>(q.b) * p.C + c] = end;
             // the carry entering each row group replaces its Br, from the last group down
@@ -765,7 +765,9 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
             }
         }
         if (kVec && !kPacked) tc::fence_proxy_async();
-        if (kPacked || kVec) __syncthreads();  // every thread is done with the stage and info
+        if (tid == 0) *snext = mine;
+        __syncthreads();  // every thread is done with the stage and info
+        const unsigned next = *snext;
         if (kVec && !kPacked && tid == 0) {
             tc::tma_store_3d(&maps.o[0], stage, q.cb * CB, q.k * TILE, q.b);
             tc::tma_store_3d(&maps.o[1], stage + TILE * LANES, q.cb * CB, q.k * TILE, q.b);
