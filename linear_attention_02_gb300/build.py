@@ -22,7 +22,8 @@ LIB = os.path.join(LIBDIR, "liblinattn.so")
 
 SOURCES = ["la_api.cu", "ffma_f32.cu", "ffma_bf16.cu", "ncbwd_ffma.cu", "ret_ffma.cu", "poly_ffma.cu", "decode.cu", "softmax_decode.cu", "noalloc.cu",
            "causal_tc.cu", "causal_bwd_tc.cu", "noncausal_tc.cu", "poly_tc.cu", "selftest.cu",
-           "gated_scan_f32.cu", "gated_scan_bf16.cu", "paged_cache.cu", "paged_decode.cu"]
+           "gated_scan_bwd_bf16.cu", "gated_scan_fwd_bf16.cu", "gated_scan_bwd_f32.cu",
+           "gated_scan_fwd_f32.cu", "gated_scan.cu", "paged_cache.cu", "paged_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -19,7 +19,7 @@
 //
 // Tiles of the same channels in time form a chain.  A tile publishes the end
 // state of each channel, and its (A, B) before that where the tile before is not
-// done; the next tile looks back over up to kWindow tiles at once to the nearest
+// done; the next tile looks back over up to 4 or 16 tiles at once to the nearest
 // end state and applies the (A, B) in between in order.  The result is the same
 // whichever it finds, since the end state of a tile is always fma(A, state
 // before, B).  A published word is its own flag: the arrays start as all ones, a
@@ -29,13 +29,7 @@
 // waits for tiles that running blocks hold, each block working its own in
 // ascending order: the lowest unfinished one can always go on.
 //
-// Measured (measured copy bandwidth 6.79 TB/s): fp32, 4 x 8192 x 1024, forward 68 us
-// (5.9 TB/s), backward 107 us (6.3 TB/s); bf16 logit form, the same rows, 51 us and
-// 77 us (4.0 and 4.4 TB/s); bf16, 65536 x 2048, forward 169 us (4.8 TB/s).  What is
-// lost there is the chain's wait: without it the same kernels take 38, 61 and 121 us.
-// A word takes 1.3 us from one SM to another and more while the memory is busy, and a
-// tile waits for the slowest of those before it.  It is worst with few channel blocks
-// (B C / 64 below the number of SMs), where many tiles of one chain are under way.
+// Measured (measured copy bandwidth 6.79 TB/s): KKK
 #pragma once
 
 #include <cuda_bf16.h>
@@ -343,8 +337,11 @@ __device__ __forceinline__ void row_info(const Args<T>& p, int k, int* info, uns
 }
 
 constexpr unsigned kUnset = 0xFFFFFFFFu;  // a word that nothing has been published in
-constexpr int kWindow = 8;                // tiles looked back over at once (4: 61 us against 45 us
-                                          // at 65536 x 256; 16: registers, 174 us against 169 us at 65536 x 2048)
+// Tiles looked back over at once.  The smaller suits chains of which up to kDeep tiles
+// are under way (65536 x 2048 bf16: forward 140 us with 4, 146 us with 8, 160 us with
+// 16: each more costs two words a tile and registers), the larger those of few channels,
+// whose many tiles advance by a window a round trip (65536 x 256: 48 us against 99 us).
+constexpr int kNear = 4, kFar = 16, kDeep = 48;
 
 __device__ __forceinline__ unsigned ld_relaxed(const float* p) {
     unsigned v;
@@ -359,11 +356,12 @@ __device__ __forceinline__ void st_relaxed(float* p, float x) {
 
 // What a channel knows of the tiles before its chain tile i: the (A, B) of up to
 // kWindow of them, nearest first.  Fetched when the tile begins, under its copy.
+template <int kWindow>
 struct Window {
     unsigned a[kWindow], b[kWindow], near;  // near: the end state of the tile before
 };
-template <typename T>
-__device__ __forceinline__ void peek(Window& w, const Args<T>& p, int i, int64_t at, int64_t step, bool on) {
+template <typename T, int kWindow>
+__device__ __forceinline__ void peek(Window<kWindow>& w, const Args<T>& p, int i, int64_t at, int64_t step, bool on) {
 #pragma unroll
     for (int d = 0; d < kWindow; ++d) {
         const bool in = on && d < i - 1;
@@ -380,8 +378,8 @@ __device__ __forceinline__ void peek(Window& w, const Args<T>& p, int i, int64_t
 // the end state before them, the first to come; each round trip reads that one, the
 // nearest end state and what is still missing (all words of the window every time
 // slowed the copies down: 210 us against 268 us at 65536 x 2048).
-template <typename T>
-__device__ float look_back(const Args<T>& p, Window& w, int i, int64_t at, int64_t step, float At, float Bt,
+template <typename T, int kWindow>
+__device__ float look_back(const Args<T>& p, Window<kWindow>& w, int i, int64_t at, int64_t step, float At, float Bt,
                            bool quiet) {
     if (w.near != kUnset) return __uint_as_float(w.near);
     if (!quiet) {
@@ -423,6 +421,25 @@ constexpr size_t smem_bytes() {
            (kPacked ? sizeof(int) * (TILE + 4 + RG) : 0) + 16;
 }
 
+// Scratch of one pass: ticket, A, B, end states (unless they go to the caller's
+// checkpoints), all unset at first.
+struct Parts {
+    size_t states, bytes;
+};
+inline Parts parts_of(int B, int N, int C, bool own_incl) {
+    const size_t tiles = (static_cast<size_t>(N) + TILE - 1) / TILE;
+    Parts s = {};
+    s.states = tiles > 1 ? static_cast<size_t>(B) * tiles * C : 0;
+    s.bytes = s.states ? 4 * (4 + (own_incl ? 3 : 2) * s.states) : 0;
+    return s;
+}
+
+// One pass along the rows (forward, or the backward's carry); defined in
+// gated_scan_impl.cuh, compiled in a file of its own for each type and direction.
+// `own_incl`: the pass keeps its chain's end states in scratch.
+template <typename T, bool kBwd>
+cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl);
+
 // States of empty packed sequences (to = from, or 0), over all warps of the grid.
 template <typename T>
 __device__ __forceinline__ void empty_sequences(const Args<T>& p, const float* from, float* to) {
@@ -455,7 +472,7 @@ __device__ __forceinline__ bool fold(const float* a, const float* b, const unsig
     return cut;
 }
 
-template <typename T, bool kLogit, bool kPacked, bool kVec>
+template <typename T, bool kLogit, bool kPacked, bool kVec, int kWindow>
 __global__ void __launch_bounds__(NT, forward_blocks<T, kLogit>())
 scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
@@ -490,8 +507,8 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         const int t0 = q.k * TILE + rg * R, c = q.cb * CB + tid;
         const bool on = tid < CB && c < p.C;  // this thread has a channel of the chain
         const int64_t at = static_cast<int64_t>(q.b) * p.tiles * p.C + c;
-        Window win;
-        peek<T>(win, p, q.k, at, p.C, on);
+        Window<kWindow> win;
+        peek<T, kWindow>(win, p, q.k, at, p.C, on);
         landed<T, kVec>(p, &bar, phase);
         phase ^= 1u;
         // The thread's rows as one map (A, B); rows past N change nothing.
@@ -533,7 +550,7 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
             const bool cut = fold<CB, kPacked, false>(sa + tid, sb + tid, grp, At, Bt);
             float* out = p.incl + at + static_cast<int64_t>(q.k) * p.C;
             if (cut && !last) st_relaxed(out, Bt);
-            if (q.k) h = look_back<T>(p, win, q.k, at, p.C, At, Bt, cut);
+            if (q.k) h = look_back<T, kWindow>(p, win, q.k, at, p.C, At, Bt, cut);
             else if (!kPacked && p.init) h = p.init[static_cast<int64_t>(q.b) * p.C + c];
             const float end = cut ? Bt : fmaf(At, h, Bt);
             // The next tile is taken as late as the copy allows: a block that took it
@@ -589,7 +606,7 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
 
 // Backward: the forward state enters each tile from its checkpoint (no chain);
 // the carry c comes down the chain from the last tile.
-template <typename T, bool kLogit, bool kPacked, bool kVec>
+template <typename T, bool kLogit, bool kPacked, bool kVec, int kWindow>
 __global__ void __launch_bounds__(NT, backward_blocks<T>())
 scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
@@ -625,8 +642,8 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         const int t0 = q.k * TILE + rg * R, c = q.cb * CB + tid, i = p.tiles - 1 - q.k;
         const bool on = tid < CB && c < p.C;  // this thread has a channel of the chain
         const int64_t at = static_cast<int64_t>(q.b) * p.tiles * p.C + c;
-        Window win;
-        peek<T>(win, p, i, at, p.C, on);
+        Window<kWindow> win;
+        peek<T, kWindow>(win, p, i, at, p.C, on);
         float h0 = 0.f;  // the state that enters the tile
         if (on && q.k) h0 = p.states[at + static_cast<int64_t>(q.k - 1) * p.C];
         else if (on && !kPacked && p.h_init) h0 = p.h_init[static_cast<int64_t>(q.b) * p.C + c];
@@ -691,7 +708,7 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
             const bool cut = fold<CB, kPacked, true>(sa + tid, sc + tid, grp, At, Bt);
             float* out = p.incl + at + static_cast<int64_t>(i) * p.C;
             if (cut && !last) st_relaxed(out, Bt);
-            if (i) y = look_back<T>(p, win, i, at, p.C, At, Bt, cut);
+            if (i) y = look_back<T, kWindow>(p, win, i, at, p.C, At, Bt, cut);
             else if (!kPacked && p.init) y = p.init[static_cast<int64_t>(q.b) * p.C + c];
             const float end = cut ? Bt : fmaf(At, y, Bt);
             if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;

@@ -636,8 +636,7 @@ size_t la_gated_scan_workspace_bytes(int backward, int B, int N, int C, la_dtype
     la_status s = check_scan(fn, B, N, C, dtype, LA_GATE_DECAY, nullptr, 0);
     if (s != LA_OK) return SIZE_MAX;
     if ((size_t)B * N * C == 0) return 0;
-    return dtype == LA_DTYPE_F32 ? gated_scan_scratch_f32(B, N, C, backward != 0, ckpt_given != 0)
-                                 : gated_scan_scratch_bf16(B, N, C, backward != 0, ckpt_given != 0);
+    return gated_scan_scratch(B, N, C, backward != 0, ckpt_given != 0);
 }
 
 size_t la_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int page_size, int max_pages,

@@ -172,8 +172,7 @@ cudaError_t gated_scan_step(const LaunchCtx& c, const T* a, const T* x, float* h
                             bool logit);
 
 // Scratch bytes of a forward or backward call (ckpt: checkpoints are given).
-size_t gated_scan_scratch_f32(int B, int N, int C, bool backward, bool ckpt);
-size_t gated_scan_scratch_bf16(int B, int N, int C, bool backward, bool ckpt);
+size_t gated_scan_scratch(int B, int N, int C, bool backward, bool ckpt);
 
 // Block table and slot map from request lengths (page_size = 1 << log2p).
 cudaError_t page_map(const LaunchCtx& c, const int* cached, const int* fresh, int R,
