@@ -29,7 +29,16 @@
 // waits for tiles that running blocks hold, each block working its own in
 // ascending order: the lowest unfinished one can always go on.
 //
-// Measured (measured copy bandwidth 6.79 TB/s): KKK
+// Measured (the copy bandwidth is 6.79 TB/s): fp32, 4 x 8192 x 1024, forward 67 us
+// (6.0 TB/s), backward 107 us (6.3 TB/s); bf16 logit form, the same rows, 47 us and
+// 73 us (4.2 and 4.6 TB/s); bf16, 65536 x 2048, 140 us and 246 us (5.8 and 5.5 TB/s).
+// What is lost is the chain's wait: without it the same kernels take 38, 61, 121 and
+// 201 us.  A word takes 1.3 us from one SM to another, more while the memory is busy,
+// and a tile waits for the slowest of those before it.  It is worst with few channel
+// blocks (B C / 64 below the number of SMs), where many tiles of one chain are under
+// way.  Blocks of a cluster reading each other's (A, B) in shared memory did not help
+// (172 us, and 81 us for the fp32 rows, against 169 us and 68 us at that stage), nor
+// did more or fewer blocks, or copying the next tile under the wait.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -84,12 +93,10 @@ struct Args {
     unsigned* status;
 };
 
-__device__ __forceinline__ void cp4(void* dst, const void* src, bool on) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-                 "l"(src), "r"(on ? 4 : 0)
-                 : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {  // the rest of the 16 is 0
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+
 // A thread's 16 bytes as fp32 values, and back (round to nearest even).
 __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -160,10 +167,19 @@ __device__ __forceinline__ uint4& piece(uint4* stage, int r) {
     return stage[s * TILE * LANES + (static_cast<int>(threadIdx.x) / LANES * R + r) * LANES + threadIdx.x % LANES];
 }
 
+// Rows that are not 16-byte aligned: the aligned 16-byte chunks that cover a row's 128
+// bytes, up to 9, lie in 36 words, 8 words apart more from row group to row group, so
+// that the 4 rows that a warp reads at once are in different banks.
+constexpr int kLoosePitch = 36, kLooseGroup = R * kLoosePitch + 8, kLooseWords = RG * kLooseGroup;
+
+template <bool kVec>
+constexpr int stream_bytes() { return kVec ? TILE * LANES * 16 : kLooseWords * 4; }
+
 // Copies a tile's streams into a stage.  kVec: by TMA, a box of 128 rows x 128 bytes
 // a stream, which thread 0 asks for when all threads are done with the stage (values
-// past N and C come as 0).  Otherwise each thread copies what it will use itself,
-// the channels lane, lane + 8, ... of its rows one by one.
+// past N and C come as 0).  Otherwise the 8 lanes of a row copy its chunks (cp.async,
+// cut at the end of the tensor; channel by channel the backward took 40 us against
+// 30 us at 5003 x 1001 fp32).
 template <typename T, bool kVec, int STREAMS>
 __device__ __forceinline__ void issue(const Args<T>& p, const Maps& maps, const Place& q, uint4* stage,
                                       uint64_t* bar) {
@@ -180,23 +196,44 @@ __device__ __forceinline__ void issue(const Args<T>& p, const Maps& maps, const 
         }
     } else {
         const T* src[3] = {p.A, p.X, p.G};
-        const int t0 = q.k * TILE + rg * R, c0 = q.cb * CB + lane;
-        const int64_t at = (static_cast<int64_t>(q.b) * p.N + t0) * p.C + c0;
+        const int64_t total = static_cast<int64_t>(p.B) * p.N * p.C;
+        const int width = min(CB, p.C - q.cb * CB);
+        const uint32_t dst = tc::smem_u32(stage) + 4 * (rg * kLooseGroup) + 16 * lane;
 #pragma unroll
-        for (int s = 0; s < STREAMS; ++s) {
-            const T* from = src[s] + at;
+        for (int r = 0; r < R; ++r) {
+            const int t = q.k * TILE + rg * R + r;
+            const int64_t e0 = (static_cast<int64_t>(q.b) * p.N + t) * p.C + q.cb * CB;
+            const int off = static_cast<int>(e0 & (VEC - 1)), used = t < p.N ? off + width : 0;
+            const int64_t from = e0 - off + lane * VEC;
+            const auto bytes = [&](int first) {  // of the chunk of elements first .. first + VEC - 1 of the row
+                const int64_t left = total - (e0 - off + first);
+                return first < used ? static_cast<int>(min(left, static_cast<int64_t>(VEC))) * static_cast<int>(sizeof(T)) : 0;
+            };
+            const int n = bytes(lane * VEC), n8 = lane == 0 ? bytes(8 * VEC) : 0;
 #pragma unroll
-            for (int r = 0; r < R; ++r, from += p.C) {
-                T* slot = reinterpret_cast<T*>(stage + s * TILE * LANES + (rg * R + r) * LANES + lane);
-                const bool row = t0 + r < p.N;
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const bool in = row && c0 + LANES * v < p.C;
-                    if constexpr (sizeof(T) == 4) cp4(slot + v, in ? from + LANES * v : src[s], in);
-                    else slot[v] = in ? from[LANES * v] : from_f<T>(0.f);
-                }
+            for (int s = 0; s < STREAMS; ++s) {
+                const uint32_t to = dst + 4 * (s * kLooseWords + r * kLoosePitch);
+                cp16(to, n ? src[s] + from : src[s], n);
+                if (n8) cp16(to + 128, src[s] + from + 8 * VEC, n8);
             }
         }
+    }
+}
+
+// A thread's channels of row r of its row group in stream s.
+template <typename T, bool kVec, int s>
+__device__ __forceinline__ void fetch(const Args<T>& p, const Place& q, uint4* stage, int r, float (&x)[Geo<T>::VEC]) {
+    constexpr int VEC = Geo<T>::VEC;
+    if constexpr (kVec) {
+        unpack(piece<s>(stage, r), x);
+    } else {
+        const int lane = threadIdx.x % LANES, rg = threadIdx.x / LANES;
+        const unsigned row = static_cast<unsigned>(q.b) * p.N + q.k * TILE + rg * R + r;
+        const T* from = reinterpret_cast<const T*>(reinterpret_cast<const uint32_t*>(stage) + s * kLooseWords +
+                                                   rg * kLooseGroup + r * kLoosePitch) +
+                        (row * static_cast<unsigned>(p.C) & (VEC - 1)) + lane;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) x[v] = to_f(from[LANES * v]);
     }
 }
 template <typename T, bool kVec>
@@ -205,6 +242,7 @@ __device__ __forceinline__ void landed(const Args<T>& p, uint64_t* bar, uint32_t
         if (!tc::mbar_wait(bar, phase, tcf::kWaitLimit)) atomicOr(p.status, tcf::kErrWait);
     } else {
         asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();  // the lanes of a row read each other's chunks
     }
 }
 
@@ -415,9 +453,9 @@ __device__ float look_back(const Args<T>& p, Window<kWindow>& w, int i, int64_t 
     return 0.f;
 }
 
-template <typename T, bool kPacked, int STREAMS>
+template <typename T, bool kPacked, bool kVec, int STREAMS>
 constexpr size_t smem_bytes() {
-    return static_cast<size_t>(STREAMS) * R * NT * 16 + sizeof(float) * STREAMS * RG * Geo<T>::CB +
+    return static_cast<size_t>(STREAMS) * stream_bytes<kVec>() + sizeof(float) * STREAMS * RG * Geo<T>::CB +
            (kPacked ? sizeof(int) * (TILE + 4 + RG) : 0) + 16;
 }
 
@@ -478,7 +516,7 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
     extern __shared__ __align__(128) uint8_t sm[];
     uint4* stage = reinterpret_cast<uint4*>(sm);
-    float* sa = reinterpret_cast<float*>(stage + 2 * R * NT);
+    float* sa = reinterpret_cast<float*>(sm + 2 * stream_bytes<kVec>());
     float* sb = sa + RG * CB;
     int* info = reinterpret_cast<int*>(sb + RG * CB);
     unsigned* grp = reinterpret_cast<unsigned*>(info + (kPacked ? TILE + 4 : 0));
@@ -519,8 +557,8 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float a[VEC], x[VEC];
-            unpack(piece<0>(stage, r), a);
-            unpack(piece<1>(stage, r), x);
+            fetch<T, kVec, 0>(p, q, stage, r, a);
+            fetch<T, kVec, 1>(p, q, stage, r, x);
             if constexpr (kLogit) {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) s[r][v] = sigmoid(a[v]);
@@ -573,8 +611,8 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
             for (int r = 0; r < R; ++r) {
                 if (t0 + r >= p.N) break;
                 float a[VEC], x[VEC];
-                unpack(piece<0>(stage, r), a);
-                unpack(piece<1>(stage, r), x);
+                fetch<T, kVec, 0>(p, q, stage, r, a);
+                fetch<T, kVec, 1>(p, q, stage, r, x);
                 const int w = kPacked ? info[rg * R + r] : 0, o = w & kOwner;
                 if (kPacked && (w & kBegin))
                     load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr, p,
@@ -612,7 +650,7 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
     constexpr int VEC = Geo<T>::VEC, CB = Geo<T>::CB;
     extern __shared__ __align__(128) uint8_t sm[];
     uint4* stage = reinterpret_cast<uint4*>(sm);
-    float* sa = reinterpret_cast<float*>(stage + 3 * R * NT);
+    float* sa = reinterpret_cast<float*>(sm + 3 * stream_bytes<kVec>());
     float* sb = sa + RG * CB;
     float* sc = sb + RG * CB;
     int* info = reinterpret_cast<int*>(sc + RG * CB);
@@ -658,9 +696,9 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float a[VEC], x[VEC], g[VEC];
-            unpack(piece<0>(stage, r), a);
-            unpack(piece<1>(stage, r), x);
-            if constexpr (!kPacked) unpack(piece<2>(stage, r), g);
+            fetch<T, kVec, 0>(p, q, stage, r, a);
+            fetch<T, kVec, 1>(p, q, stage, r, x);
+            if constexpr (!kPacked) fetch<T, kVec, 2>(p, q, stage, r, g);
             if constexpr (kLogit) {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) s[r][v] = sigmoid(a[v]);
@@ -687,8 +725,8 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
                 if (t0 + r < p.N) {
                     const int w = info[rg * R + r], o = w & kOwner;
                     float a[VEC], g[VEC];
-                    unpack(piece<0>(stage, r), a);
-                    unpack(piece<2>(stage, r), g);
+                    fetch<T, kVec, 0>(p, q, stage, r, a);
+                    fetch<T, kVec, 2>(p, q, stage, r, g);
                     if (w & kEnd)
                         load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr,
                                             p, q, Br);
@@ -735,8 +773,8 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float a[VEC], x[VEC];
-            unpack(piece<0>(stage, r), a);
-            unpack(piece<1>(stage, r), x);
+            fetch<T, kVec, 0>(p, q, stage, r, a);
+            fetch<T, kVec, 1>(p, q, stage, r, x);
             if constexpr (kPacked) {
                 const int w = info[rg * R + r], o = w & kOwner;
                 if (w & kBegin)
@@ -754,9 +792,9 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         for (int r = R - 1; r >= 0; --r) {
             if (t0 + r < p.N) {
                 float a[VEC], x[VEC], g[VEC];
-                unpack(piece<0>(stage, r), a);
-                unpack(piece<1>(stage, r), x);
-                unpack(piece<2>(stage, r), g);
+                fetch<T, kVec, 0>(p, q, stage, r, a);
+                fetch<T, kVec, 1>(p, q, stage, r, x);
+                fetch<T, kVec, 2>(p, q, stage, r, g);
                 const int w = kPacked ? info[rg * R + r] : 0, o = w & kOwner;
                 if (kPacked && (w & kEnd))
                     load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr, p,

@@ -69,7 +69,7 @@ cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl) {
     else LA_SCAN_RUN((scan_forward_kernel<T, L, P, V, W>), smem)
 #define LA_SCAN_GO(L, P, V)                                                                        \
     if (logit == L && packed == P && vec == V) {                                                   \
-        constexpr int smem = static_cast<int>(smem_bytes<T, P, STREAMS>());                        \
+        constexpr int smem = static_cast<int>(smem_bytes<T, P, V, STREAMS>());                        \
         constexpr int blocks = kBwd ? backward_blocks<T>() : forward_blocks<T, L>();               \
         if (static_cast<size_t>(blocks) * c.num_sms > kDeep * a.B * ncb) { LA_SCAN_WIN(L, P, V, kFar) } \
         else { LA_SCAN_WIN(L, P, V, kNear) }                                                       \
