@@ -112,13 +112,13 @@ __device__ __forceinline__ void cpv(uint32_t dst, const void* src, bool on) {
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -482,32 +482,45 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         for (int n = 0; n < 2; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
+            uint32_t kw[2][4];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const uint4 k = *reinterpret_cast<const uint4*>(st + Ly::kat(g, t, n, i));
-                const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
+                kw[n][0] = k.x, kw[n][1] = k.y, kw[n][2] = k.z, kw[n][3] = k.w;
+            }
 #pragma unroll
-                for (int h = 0; h < 4; h += 2) {
-                    if constexpr (kBf16) {
+            for (int h = 0; h < 4; h += 2) {
+                if constexpr (kBf16) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
                         mma_bf16(s[n], qf[0][i][h], ROWS == 2 ? qf[ROWS - 1][i][h] : 0u, qf[0][i][h + 1],
-                                 ROWS == 2 ? qf[ROWS - 1][i][h + 1] : 0u, kw[h], kw[h + 1]);
+                                 ROWS == 2 ? qf[ROWS - 1][i][h + 1] : 0u, kw[n][h], kw[n][h + 1]);
+                } else {
+                    uint32_t kh[2][2], kl[2][2];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        split_tf32(kw[n][h], kh[n][0], kl[n][0]);
+                        split_tf32(kw[n][h + 1], kh[n][1], kl[n][1]);
+                    }
+                    if constexpr (ROWS == 1) {  // rows: both terms of q
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+                            mma_tf32(s[n], qf[0][i][h], qf[1][i][h], qf[0][i][h + 1], qf[1][i][h + 1], kh[n][0], kh[n][1]);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+                            mma_tf32(s[n], qf[0][i][h], qf[1][i][h], qf[0][i][h + 1], qf[1][i][h + 1], kl[n][0], kl[n][1]);
                     } else {
-                        uint32_t kh0, kl0, kh1, kl1;
-                        split_tf32(kw[h], kh0, kl0);
-                        split_tf32(kw[h + 1], kh1, kl1);
-                        if constexpr (ROWS == 1) {  // rows: both terms of q
-                            mma_tf32(s[n], qf[0][i][h], qf[1][i][h], qf[0][i][h + 1], qf[1][i][h + 1], kh0, kh1);
-                            mma_tf32(s[n], qf[0][i][h], qf[1][i][h], qf[0][i][h + 1], qf[1][i][h + 1], kl0, kl1);
-                        } else {
-                            uint32_t ah[4], al[4];
-                            split_tf32(qf[0][i][h], ah[0], al[0]);
-                            split_tf32(qf[1][i][h], ah[1], al[1]);
-                            split_tf32(qf[0][i][h + 1], ah[2], al[2]);
-                            split_tf32(qf[1][i][h + 1], ah[3], al[3]);
-                            mma_tf32(s[n], ah[0], ah[1], ah[2], ah[3], kh0, kh1);
-                            mma_tf32(s[n], ah[0], ah[1], ah[2], ah[3], kl0, kl1);
-                            mma_tf32(s[n], al[0], al[1], al[2], al[3], kh0, kh1);
-                        }
+                        uint32_t ah[4], al[4];
+                        split_tf32(qf[0][i][h], ah[0], al[0]);
+                        split_tf32(qf[1][i][h], ah[1], al[1]);
+                        split_tf32(qf[0][i][h + 1], ah[2], al[2]);
+                        split_tf32(qf[1][i][h + 1], ah[3], al[3]);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) mma_tf32(s[n], ah[0], ah[1], ah[2], ah[3], kh[n][0], kh[n][1]);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) mma_tf32(s[n], ah[0], ah[1], ah[2], ah[3], kl[n][0], kl[n][1]);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) mma_tf32(s[n], al[0], al[1], al[2], al[3], kh[n][0], kh[n][1]);
                     }
                 }
             }
