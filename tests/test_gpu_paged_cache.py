@@ -542,3 +542,26 @@ def test_paged_decode_scratch_matches_report(dt):
         la.la_paged_decode_step(d["q"], None, None, d["K"], d["V"], tb, ln)
         torch.cuda.synchronize()
         assert want <= la.la_scratch_peak_bytes() <= want + (2 << 20)
+
+
+@pytest.mark.parametrize("dt,Hq,Hkv", [("bf16", 2, 2), ("bf16", 12, 1), ("f32", 12, 1), ("f32", 20, 1)])
+def test_paged_decode_non_finite_keys_stay_where_they_are(dt, Hq, Hkv):
+    # keys of infinite negative scores count nothing; a NaN key makes its own request NaN and no other
+    la = _la()
+    lens = [40, 40, 70]
+    x, table = _decode_case(3, Hq, Hkv, 32, 16, lens, False, dt, seed=31)
+    x["q"][:] = x["q"].abs() + 0.1
+    x["K"][:] = x["K"].abs()
+    tol, _ = _bounds(x, 32)
+    clean = la.la_paged_decode_step(x["q"].cuda(), None, None, x["K"].cuda(), x["V"].cuda(), _i32(table), _i32(lens))
+    for p in range(35):
+        x["K"][table[0][p // 16], :, p % 16] = float("-inf")
+    x["K"][table[1][0], :, 3] = float("nan")
+    out = la.la_paged_decode_step(x["q"].cuda(), None, None, x["K"].cuda(), x["V"].cuda(), _i32(table), _i32(lens))
+    K5 = torch.stack([x["K"][table[0][p // 16], :, p % 16] for p in range(35, 40)], 1).double()
+    V5 = torch.stack([x["V"][table[0][p // 16], :, p % 16] for p in range(35, 40)], 1).double()
+    s = torch.einsum("hgd,hnd->hgn", x["q"][0].double().view(Hkv, -1, 32), K5) / math.sqrt(32)
+    want = torch.einsum("hgn,hnd->hgd", torch.softmax(s, 2), V5).reshape(Hq, 32)
+    assert float((out[0].cpu().double() - want).abs().max()) <= tol
+    assert bool(torch.isnan(out[1]).all())
+    assert torch.equal(out[2], clean[2])
