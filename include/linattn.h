@@ -333,7 +333,9 @@ la_status la_gated_scan_decode_step(const void* a, const void* x, float* h, void
  *              rows of each request among the packed new rows
  *   counts [2] int32                  (written) new positions, pages wanted
  * A call changes neither lengths nor free_pages: the caller moves on by
- * counts[1] pages and adds new_lens to cached_lens.  A negative length acts as 0.
+ * counts[1] pages and adds new_lens to cached_lens.  A negative length acts as 0 and
+ * is reported, but for a negative cached length without new positions: a row without
+ * a request, as in la_paged_decode_step.
  */
 la_status la_page_map(const int* cached_lens, const int* new_lens, int R, const int* free_pages,
                       int num_free, int page_size, int num_pages, int* block_table, int max_pages,

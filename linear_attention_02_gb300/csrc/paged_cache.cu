@@ -21,13 +21,14 @@ constexpr int kMapThreads = 256;
 constexpr int kMapShared = plan::kMapShared;
 
 // One request's lengths made valid: cached and new positions that fit a table
-// row of `cap` positions; `rows` keeps the given count of new rows.
+// row of `cap` positions; `rows` keeps the given count of new rows.  A negative cached
+// length without new rows is a row of the batch without a request, and not bad.
 struct Request {
     int cached, fit, rows, old_pages, need;
     bool bad;
     __device__ Request(int c, int n, int log2p, int max_pages) {
         const int64_t cap = static_cast<int64_t>(max_pages) << log2p;
-        bad = c < 0 || n < 0 || static_cast<int64_t>(c) + n > cap;
+        bad = n < 0 || (c < 0 && n > 0) || static_cast<int64_t>(c) + n > cap;
         c = max(c, 0);
         rows = max(n, 0);
         cached = static_cast<int>(c < cap ? c : cap);

@@ -77,7 +77,7 @@ def page_map(cached, new, free, table, page, num_pages, max_tokens):
     W = table.shape[1]
     slots, starts, used, bad = [], [0], 0, False
     for r, (have, more) in enumerate(zip(cached, new)):
-        bad |= have < 0 or more < 0 or have + more > W * page
+        bad |= more < 0 or (have < 0 and more > 0) or have + more > W * page
         have, more = min(max(have, 0), W * page), max(more, 0)
         for p in range(have, have + more):
             if p >= W * page:

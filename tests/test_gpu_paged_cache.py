@@ -90,6 +90,21 @@ def test_page_map_reports_what_does_not_fit():
         la.la_check_device_status()  # cleared
 
 
+@pytest.mark.parametrize("R", [7, 4500])
+def test_page_map_of_a_padded_batch(R):
+    # rows without a request (negative cached length, nothing new) change nothing and are not reported
+    la = _la()
+    cached, new, free, table, P = _map_case(R, 4, 9, 3, 2, R)
+    for r in range(0, R, 3):
+        cached[r], new[r] = -1 - r, 0
+    T = sum(new) + 5
+    want = ref.page_map(cached, new, free, table, 4, P, T)
+    assert not want[4]
+    for g, w in zip(_run_map(cached, new, free, table, 4, P, T), want):
+        np.testing.assert_array_equal(g, w)
+    la.la_check_device_status()
+
+
 def test_page_map_without_requests():
     la = _la()
     slots = torch.full((5,), 3, dtype=torch.int32, device="cuda")

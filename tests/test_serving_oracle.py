@@ -84,6 +84,13 @@ def test_page_map_hand_values():
     assert counts.tolist() == [5, 2]
 
 
+def test_page_map_rows_without_a_request():
+    table, slots, starts, counts, bad = ref.page_map([4, -1, 0], [1, 0, 1], [7, 2], [[9, -1], [5, 5], [-1, -1]], 4, 10, 3)
+    assert table.tolist() == [[9, 7], [5, 5], [2, -1]] and not bad
+    assert slots.tolist() == [28, 8, -1] and starts.tolist() == [0, 1, 1, 2] and counts.tolist() == [2, 2]
+    assert ref.page_map([-1], [1], [7], [[-1]], 4, 10, 1)[4]
+
+
 def test_paged_decode_against_softmax():
     g = np.random.RandomState(2)
     P, Hkv, page, D, Hq = 6, 2, 4, 8, 4
