@@ -15,6 +15,8 @@ Shapes: Q, K [B,H,N,D]; V [B,H,N,M]; S [B,H,D,M] fp32; Z [B,H,D] fp32.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _native
@@ -608,8 +610,8 @@ def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, wi
     _shaped(cached_lens, "cached_lens", (R,), torch.int32, dev)
     if scale is None:
         scale = 0.0
-    elif float(scale) == 0.0:
-        raise ValueError("scale must not be 0")
+    elif ctypes.c_float(float(scale)).value == 0.0:  # the C call's 0 means the default
+        raise ValueError("scale must not be 0 in fp32")
     if out is None:
         out = torch.empty((R, Hq, D), dtype=torch.float32, device=q.device)
     else:

@@ -425,8 +425,9 @@ def test_paged_wrapper_refusals():
                        ((q, k[:, :1].contiguous(), k, K, K, tb, ln), "k must be")):
         with pytest.raises(ValueError, match=match):
             la.la_paged_decode_step(*bad)
-    with pytest.raises(ValueError, match="scale"):
-        la.la_paged_decode_step(q, k, k, K, K, tb, ln, scale=0)
+    for scale in (0, 1e-60):  # the second is 0 in fp32
+        with pytest.raises(ValueError, match="scale"):
+            la.la_paged_decode_step(q, k, k, K, K, tb, ln, scale=scale)
     with pytest.raises(la.LinAttnError, match="INVALID_ARG"):
         la.la_paged_decode_step(q, k, k, K, K, tb, ln, window=-2)
     with pytest.raises(la.LinAttnError, match="UNSUPPORTED"):
