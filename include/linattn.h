@@ -254,6 +254,7 @@ la_status la_softmax_decode_step(const void* q, const void* k, const void* v, vo
  *         (of an empty sequence: h_init, or 0)
  *   Ckpt  fp32, nullable (written) la_gated_scan_ckpt_floats(B, N, C) words: the
  *         running state at every 128th row, for the backward
+ * N <= 2^31 - 129, num_seqs < 2^29 - 1 and B * N * C < 2^40.
  * Decays lie in [-1, 1]; the state is fp32 throughout.  Rows are summed up in
  * parts, whose products of decays may round to 0: behind an infinite or NaN
  * state, the rows of its channel and sequence are infinite or NaN.  A sequence's
@@ -314,9 +315,9 @@ la_status la_gated_scan_decode_step(const void* a, const void* x, float* h, void
  * of many requests; position p of request r is on page
  * block_table[r][p / page_size] at offset p % page_size, and its slot number is
  * page * page_size + offset.  page_size is a power of two up to 1024, and
- * num_pages * page_size < 2^31.  Lengths, pages and slots are read on the GPU:
- * one that is out of range has its access skipped and is reported by the next
- * la_check_device_status as LA_ERR_BAD_INDEX.
+ * num_pages * page_size < 2^31; a call takes fewer than 2^30 requests.  Lengths,
+ * pages and slots are read on the GPU: one that is out of range has its access
+ * skipped and is reported by the next la_check_device_status as LA_ERR_BAD_INDEX.
  *
  * la_page_map: the step's bookkeeping, from request lengths.  Request r holds
  * cached_lens[r] positions and gets new_lens[r] more; the pages that these open
@@ -367,8 +368,9 @@ la_status la_paged_append(const void* k, const void* v, void* K_pages, void* V_p
  *   lse [R][Hq] fp32, nullable                                (written) log of the
  *         sum of e^(scale q k); joins outputs over parts of a context
  *   scale 0 means 1 / sqrt(D)
- * A request without a position has out 0 and lse -infinity.  Positions whose
- * page is out of range are left out.  D in {32, 64, 128}, Hq a multiple of Hkv.
+ * A request without a position has out 0 and lse -infinity.  An infinite element of
+ * a value row makes its column of out infinite or NaN.  Positions whose page is out
+ * of range are left out.  D in {32, 64, 128}, Hq a multiple of Hkv.
  * Reads one key and one value row per position and key head, whatever Hq / Hkv;
  * max_pages * page_size < 2^30.  No page may be held by two requests that append
  * to it.  Results do not depend on the run.

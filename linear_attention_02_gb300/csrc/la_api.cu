@@ -157,8 +157,10 @@ la_status check_scan(const char* fn, int B, int N, int C, la_dtype dt, la_gate_f
         return fail(LA_ERR_INVALID_ARG, "%s: num_seqs=%d without seq_starts", fn, num_seqs);
     if (reinterpret_cast<uintptr_t>(starts) & 3u)
         return fail(LA_ERR_INVALID_ARG, "%s: seq_starts is not 4-byte aligned", fn);
+    // rows of a last tile and borders of sequences are counted in 32 bits, the latter beside two flags
     const unsigned long long rows = (unsigned long long)B * N;
-    if (rows >= (1ull << 40) || (C && rows * C >= (1ull << 40)) ||
+    if (N > INT_MAX - plan::kScanTile || num_seqs >= (1 << 29) - 1 || rows >= (1ull << 40) ||
+        (C && rows * C >= (1ull << 40)) ||
         (unsigned long long)(starts ? num_seqs : B) * C >= (1ull << 40))
         return fail(LA_ERR_INVALID_ARG, "%s: tensor too large", fn);
     return LA_OK;
@@ -662,7 +664,9 @@ size_t la_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int page_s
     return paged_decode_scratch(sh, D, dtype == LA_DTYPE_BF16, num_sms);
 }
 
-size_t la_page_map_workspace_bytes(int R) { return R < 0 ? SIZE_MAX : plan::page_map_scratch(R); }
+size_t la_page_map_workspace_bytes(int R) {
+    return R < 0 || R >= (1 << 30) ? SIZE_MAX : plan::page_map_scratch(R);
+}
 
 size_t la_gated_scan_ckpt_floats(int B, int N, int C) {
     if (B <= 0 || N <= 0 || C <= 0) return 0;
@@ -762,6 +766,7 @@ la_status la_page_map(const int* cached_lens, const int* new_lens, int R, const 
     if (R < 0 || num_free < 0 || max_pages < 0 || max_tokens < 0)
         return fail(LA_ERR_INVALID_ARG, "%s: negative size R=%d num_free=%d max_pages=%d max_tokens=%d", fn,
                     R, num_free, max_pages, max_tokens);
+    if (R >= (1 << 30)) return fail(LA_ERR_INVALID_ARG, "%s: R=%d: 2^30 requests or more", fn, R);
     if ((unsigned long long)max_pages * page_size >= (1ull << 31))
         return fail(LA_ERR_INVALID_ARG, "%s: max_pages=%d of %d positions: 2^31 positions or more", fn,
                     max_pages, page_size);
@@ -790,7 +795,7 @@ la_status la_paged_append(const void* k, const void* v, void* K_pages, void* V_p
         return fail(LA_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dtype);
     if (!head_ok(D))
         return fail(LA_ERR_UNSUPPORTED, "%s: D=%d, supported head sizes are 32, 64, 128", fn, D);
-    if ((unsigned long long)T * Hkv * D >= (1ull << 40) ||
+    if ((unsigned long long)T * Hkv * D >= (1ull << 40) || (unsigned long long)Hkv * D >= (1ull << 31) ||
         (unsigned long long)num_pages * page_size * (Hkv ? Hkv : 1) >= (1ull << 40) / D)
         return fail(LA_ERR_INVALID_ARG, "%s: tensor too large", fn);
     if (T == 0 || Hkv == 0) return LA_OK;

@@ -38,6 +38,8 @@ def test_scan_refusals(call):
     assert call(hi=FAKE + 4) == INV and "h_init" in _msg()
     assert call(ck=FAKE + 4) == INV and "Ckpt" in _msg()
     assert call(B=1 << 20, N=1 << 20, C=4) == INV and "too large" in _msg()
+    assert call(B=1, N=(1 << 31) - 1, C=1) == INV and "too large" in _msg()
+    assert call(st=FAKE, ns=1 << 30, C=1) == INV and "too large" in _msg()
     # nothing to do and no state asked for: no device call
     for kw in ({"B": 0}, {"N": 0}, {"C": 0}, {"st": FAKE, "ns": 0}):
         assert call(A=None, X=None, **kw) == OK
@@ -72,6 +74,8 @@ def test_page_map_refusals():
     assert _map(c=None) == INV and "cached_lens is NULL" in _msg()
     assert _map(ss=None) == INV and _map(ct=None) == INV and _map(sm=FAKE + 2) == INV
     assert _map(bt=None) == INV and _map(fp=None) == INV
+    assert _map(R=(1 << 31) - 1) == INV and "2^30" in _msg()
+    assert lib.la_page_map_workspace_bytes((1 << 31) - 1) == _native.SIZE_MAX
 
 
 def _app(k=FAKE, v=FAKE, K=FAKE, V=FAKE, sm=FAKE, T=3, Hkv=2, D=64, P=4, page=16, dt=1):
@@ -83,6 +87,7 @@ def test_append_refusals():
     assert _app(T=-1) == INV and _app(Hkv=-1) == INV
     assert _app(k=FAKE + 4) == INV and "k is not 16-byte" in _msg()
     assert _app(K=None) == INV and _app(sm=None) == INV
+    assert _app(T=1, Hkv=1 << 30, D=32, P=1, page=1) == INV and "too large" in _msg()
     assert _app(T=0, k=None) == OK and _app(Hkv=0, k=None) == OK
 
 
