@@ -19,7 +19,28 @@ Args<T> args_of(const ScanShape& s, const T* A, const T* X) {
     return a;
 }
 
+__global__ void unset_kernel(unsigned* a, size_t na, unsigned* b, size_t nb) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const size_t id = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x, all = static_cast<size_t>(gridDim.x) * 256;
+    const auto fill = [&](unsigned* to, size_t n) {
+        const size_t n4 = n / 4;
+        for (size_t i = id; i < n4; i += all) reinterpret_cast<uint4*>(to)[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
+        if (id < n % 4) to[4 * n4 + id] = kUnset;
+    };
+    fill(a, na);
+    fill(b, nb);
+}
+
 }  // namespace
+
+namespace scan {
+cudaError_t unset_words(const LaunchCtx& c, unsigned* a, size_t na, unsigned* b, size_t nb) {
+    const size_t blocks = (std::max(na, nb) / 4 + 256) / 256;
+    unset_kernel<<<static_cast<unsigned>(std::min<size_t>(blocks, 4 * c.num_sms)), 256, 0, c.stream>>>(a, na, b, nb);
+    note_launch();
+    return cudaGetLastError();
+}
+}  // namespace scan
 
 template <typename T>
 cudaError_t gated_scan_forward(const LaunchCtx& c, const T* A, const T* X, T* O, const ScanShape& s,

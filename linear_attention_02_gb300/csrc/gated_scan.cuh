@@ -472,6 +472,10 @@ inline Parts parts_of(int B, int N, int C, bool own_incl) {
     return s;
 }
 
+// Unsets na words at a and nb words at b (16-byte aligned) by one kernel, which a pass
+// launched behind it may overlap until its griddepcontrol.wait.
+cudaError_t unset_words(const LaunchCtx& c, unsigned* a, size_t na, unsigned* b, size_t nb);
+
 // One pass along the rows (forward, or the backward's carry); defined in
 // gated_scan_impl.cuh, compiled in a file of its own for each type and direction.
 // `own_incl`: the pass keeps its chain's end states in scratch.
@@ -530,6 +534,7 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         tc::fence_mbar_init();
     }
     __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the chain's words are unset
     unsigned tile = blockIdx.x;
     if (p.ticket) {
         if (tid == 0) *snext = atomicAdd(p.ticket, 1u) + 1u;
@@ -665,6 +670,7 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         tc::fence_mbar_init();
     }
     __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the chain's words are unset
     unsigned tile = blockIdx.x;
     if (p.ticket) {
         if (tid == 0) *snext = atomicAdd(p.ticket, 1u) + 1u;

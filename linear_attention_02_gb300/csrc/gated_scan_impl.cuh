@@ -50,18 +50,28 @@ cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl) {
         a.aggA = reinterpret_cast<float*>(base) + 4;
         a.aggB = a.aggA + s.states;
         if (own_incl) a.incl = a.aggB + s.states;
-        else e = cudaMemsetAsync(a.incl, 0xFF, s.states * 4, c.stream);
+        e = unset_words(c, reinterpret_cast<unsigned*>(base), s.bytes / 4, own_incl ? nullptr : reinterpret_cast<unsigned*>(a.incl),
+                        own_incl ? 0 : s.states);
     }
-    if (s.bytes && e == cudaSuccess) e = cudaMemsetAsync(base, 0xFF, s.bytes, c.stream);
+    // After the kernel that unsets the words, this one may start before that has ended.
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(NT);
+    cfg.stream = c.stream;
+    cfg.attrs = early;
+    cfg.numAttrs = tiles > 1 ? 1 : 0;
 
 #define LA_SCAN_RUN(K, SMEM)                                                                       \
     {                                                                                              \
         int per = 1;                                                                               \
         if (e == cudaSuccess) e = resident_blocks<K>(c.device, NT, SMEM, &per);                    \
         if (e == cudaSuccess) {                                                                    \
-            K<<<std::min<unsigned>(a.total, per * c.num_sms), NT, SMEM, c.stream>>>(a, maps);      \
+            cfg.gridDim = dim3(std::min<unsigned>(a.total, per * c.num_sms));                      \
+            cfg.dynamicSmemBytes = SMEM;                                                           \
+            e = cudaLaunchKernelEx(&cfg, K, static_cast<const Args<T>>(a), static_cast<const Maps>(maps)); \
             note_launch();                                                                         \
-            e = cudaGetLastError();                                                                \
         }                                                                                          \
     }
 #define LA_SCAN_WIN(L, P, V, W)                                                                    \
