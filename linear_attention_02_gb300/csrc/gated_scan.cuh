@@ -276,6 +276,16 @@ __device__ __forceinline__ void load_state(const float* row, const Args<T>& p, c
     }
 }
 template <typename T, bool kVec>
+__device__ __forceinline__ void add_state(const float* row, const Args<T>& p, const Place& q,
+                                          float (&y)[Geo<T>::VEC]) {
+    const int lane = threadIdx.x % LANES;
+#pragma unroll
+    for (int v = 0; v < Geo<T>::VEC; ++v) {
+        const int c = q.cb * Geo<T>::CB + (kVec ? lane * Geo<T>::VEC + v : lane + LANES * v);
+        if (c < p.C) y[v] += row[c];
+    }
+}
+template <typename T, bool kVec>
 __device__ __forceinline__ void save_state(float* row, const Args<T>& p, const Place& q,
                                            const float (&y)[Geo<T>::VEC]) {
     const int lane = threadIdx.x % LANES;
@@ -697,48 +707,34 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         float A[VEC], Bf[VEC], Br[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) A[v] = 1.f, Bf[v] = 0.f, Br[v] = 0.f;
-        // forward over the rows: A, the state's Bf, and (without packed borders)
-        // the carry's Br = sum_i (s_0 .. s_i) dOut_i
+        // forward over the rows: A, the state's Bf, and the carry's
+        // Br = sum_i (s_0 .. s_i) dOut_i, up to the first row that ends a sequence
+        bool live = true;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float a[VEC], x[VEC], g[VEC];
             fetch<T, kVec, 0>(p, q, stage, r, a);
             fetch<T, kVec, 1>(p, q, stage, r, x);
-            if constexpr (!kPacked) fetch<T, kVec, 2>(p, q, stage, r, g);
+            fetch<T, kVec, 2>(p, q, stage, r, g);
             if constexpr (kLogit) {
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) s[r][v] = sigmoid(a[v]);
             }
             if (t0 + r < p.N) {
-                if constexpr (kPacked) {
-                    const int w = info[rg * R + r], o = w & kOwner;
-                    if (w & kBegin)
-                        load_state<T, kVec>(
-                            p.h_init && o != kOwner ? p.h_init + static_cast<int64_t>(o) * p.C : nullptr, p, q, Bf);
-                }
+                const int w = kPacked ? info[rg * R + r] : 0, o = w & kOwner;
+                if (kPacked && (w & kBegin))
+                    load_state<T, kVec>(p.h_init && o != kOwner ? p.h_init + static_cast<int64_t>(o) * p.C : nullptr,
+                                        p, q, Bf);
+                if (kPacked && (w & kEnd) && p.init && o != kOwner)
+                    add_state<T, kVec>(p.init + static_cast<int64_t>(o) * p.C, p, q, g);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
                     A[v] *= d;
                     Bf[v] = fmaf(d, Bf[v], added<kLogit>(d, x[v]));
-                    if constexpr (!kPacked) Br[v] = fmaf(A[v], g[v], Br[v]);
+                    Br[v] = live ? fmaf(A[v], g[v], Br[v]) : Br[v];
                 }
-            }
-        }
-        if constexpr (kPacked) {  // the carry row by row, from the last
-#pragma unroll
-            for (int r = R - 1; r >= 0; --r) {
-                if (t0 + r < p.N) {
-                    const int w = info[rg * R + r], o = w & kOwner;
-                    float a[VEC], g[VEC];
-                    fetch<T, kVec, 0>(p, q, stage, r, a);
-                    fetch<T, kVec, 2>(p, q, stage, r, g);
-                    if (w & kEnd)
-                        load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr,
-                                            p, q, Br);
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) Br[v] = (kLogit ? s[kLogit ? r : 0][v] : a[v]) * (g[v] + Br[v]);
-                }
+                if (kPacked && (w & kEnd)) live = false;
             }
         }
         put<T, kVec>(sa, A);
@@ -773,56 +769,66 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
             }
         }
         __syncthreads();
-        float hp[R][VEC], h[VEC], y[VEC];
-        get<T, kVec>(sa, h);
+        // The rows' states are kept for H rows at a time, from the last ones up; the rows
+        // before them are run through again.
+        constexpr int H = kPacked && sizeof(T) == 2 ? R / 2 : R;
+        float y[VEC];
         get<T, kVec>(sc, y);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float a[VEC], x[VEC];
-            fetch<T, kVec, 0>(p, q, stage, r, a);
-            fetch<T, kVec, 1>(p, q, stage, r, x);
-            if constexpr (kPacked) {
-                const int w = info[rg * R + r], o = w & kOwner;
-                if (w & kBegin)
+        for (int r0 = R - H; r0 >= 0; r0 -= H) {
+            float hp[H][VEC], h[VEC];
+            get<T, kVec>(sa, h);
+#pragma unroll
+            for (int r = 0; r < r0 + H; ++r) {
+                if (kPacked && (info[rg * R + r] & kBegin)) {
+                    const int o = info[rg * R + r] & kOwner;
                     load_state<T, kVec>(p.h_init && o != kOwner ? p.h_init + static_cast<int64_t>(o) * p.C : nullptr,
                                         p, q, h);
-            }
+                }
+                if (r >= r0) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
-                hp[r][v] = h[v];
-                h[v] = fmaf(d, h[v], added<kLogit>(d, x[v]));
-            }
-        }
-#pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
-            if (t0 + r < p.N) {
-                float a[VEC], x[VEC], g[VEC];
+                    for (int v = 0; v < VEC; ++v) hp[r >= r0 ? r - r0 : 0][v] = h[v];
+                }
+                if (r + 1 == r0 + H) break;
+                float a[VEC], x[VEC];
                 fetch<T, kVec, 0>(p, q, stage, r, a);
                 fetch<T, kVec, 1>(p, q, stage, r, x);
-                fetch<T, kVec, 2>(p, q, stage, r, g);
-                const int w = kPacked ? info[rg * R + r] : 0, o = w & kOwner;
-                if (kPacked && (w & kEnd))
-                    load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr, p,
-                                        q, y);
-                float da[VEC], dx[VEC];
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
-                    const float tot = g[v] + y[v];
-                    dx[v] = kLogit ? (1.f - d) * tot : tot;
-                    da[v] = kLogit ? d * dx[v] * (hp[r][v] - x[v]) : tot * hp[r][v];
-                    y[v] = d * tot;
+                    h[v] = fmaf(d, h[v], added<kLogit>(d, x[v]));
                 }
-                if constexpr (kVec && !kPacked) {
-                    piece<0>(stage, r) = pack(da);
-                    piece<1>(stage, r) = pack(dx);
-                } else if (!kPacked || o != kOwner) {
-                    store_row<T, kVec>(p.dA, p, q, t0 + r, da);
-                    store_row<T, kVec>(p.dX, p, q, t0 + r, dx);
+            }
+#pragma unroll
+            for (int r = r0 + H - 1; r >= r0; --r) {
+                if (t0 + r < p.N) {
+                    float a[VEC], x[VEC], g[VEC];
+                    fetch<T, kVec, 0>(p, q, stage, r, a);
+                    fetch<T, kVec, 1>(p, q, stage, r, x);
+                    fetch<T, kVec, 2>(p, q, stage, r, g);
+                    const int w = kPacked ? info[rg * R + r] : 0, o = w & kOwner;
+                    if (kPacked && (w & kEnd))
+                        load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr, p,
+                                            q, y);
+                    float da[VEC], dx[VEC];
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) {
+                        const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
+                        const float tot = g[v] + y[v], hv = hp[r - r0][v];
+                        dx[v] = kLogit ? (1.f - d) * tot : tot;
+                        da[v] = kLogit ? d * dx[v] * (hv - x[v]) : tot * hv;
+                        y[v] = d * tot;
+                    }
+                    if constexpr (kVec && !kPacked) {
+                        piece<0>(stage, r) = pack(da);
+                        piece<1>(stage, r) = pack(dx);
+                    } else if (!kPacked || o != kOwner) {
+                        store_row<T, kVec>(p.dA, p, q, t0 + r, da);
+                        store_row<T, kVec>(p.dX, p, q, t0 + r, dx);
+                    }
+                    if (kPacked && (w & kBegin) && o != kOwner && p.fin)
+                        save_state<T, kVec>(p.fin + static_cast<int64_t>(o) * p.C, p, q, y);
                 }
-                if (kPacked && (w & kBegin) && o != kOwner && p.fin)
-                    save_state<T, kVec>(p.fin + static_cast<int64_t>(o) * p.C, p, q, y);
             }
         }
         if (kVec && !kPacked) tc::fence_proxy_async();
