@@ -126,17 +126,95 @@ __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
                       __float_as_uint(x[3]));
 }
 
-// sigmoid(z) = 1 / (1 + 2^(-z log2 e)): an overflow of the power gives 0.
-__device__ __forceinline__ float sigmoid(float z) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + tcf::ex2_approx(-1.4426950408889634f * z)));
+// Arithmetic on a thread's channels, two to an instruction (each rounded as by itself):
+// d = a b, d = a b + c, d = a + k.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ void both(uint64_t x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+template <int V>
+__device__ __forceinline__ void mul(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+        uint64_t r;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(two(a[v], a[v + 1])), "l"(two(b[v], b[v + 1])));
+        both(r, d[v], d[v + 1]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void fma(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+        uint64_t r;
+        asm("fma.rn.f32x2 %0, %1, %2, %3;"
+            : "=l"(r)
+            : "l"(two(a[v], a[v + 1])), "l"(two(b[v], b[v + 1])), "l"(two(c[v], c[v + 1])));
+        both(r, d[v], d[v + 1]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void add(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+        uint64_t r;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(two(a[v], a[v + 1])), "l"(two(b[v], b[v + 1])));
+        both(r, d[v], d[v + 1]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void fill(float (&d)[V], float x) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) d[v] = x;
+}
+template <int V>
+__device__ __forceinline__ void neg(float (&d)[V], const float (&a)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) d[v] = -a[v];
+}
 
-// What a row adds to the state: x, or (1 - d) x as one rounding of x - d x.
-template <bool kLogit>
-__device__ __forceinline__ float added(float d, float x) {
-    return kLogit ? fmaf(-d, x, x) : x;
+// s = sigmoid(z) = 1 / (1 + 2^(-z log2 e)): an overflow of the power gives 0.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float sigmoid(float z) { return rcp_approx(1.f + tcf::ex2_approx(-1.4426950408889634f * z)); }
+template <int V>
+__device__ __forceinline__ void sigmoid(float (&s)[V], const float (&z)[V]) {
+    float k[V], e[V];
+    fill(k, -1.4426950408889634f);
+    mul(e, z, k);
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = tcf::ex2_approx(e[v]);
+    fill(k, 1.f);
+    add(e, e, k);
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = rcp_approx(e[v]);
+}
+
+// h = d h + x, or in the logit form d h + (1 - d) x, whose second term is one rounding
+// of x - d x.
+template <bool kLogit, int V>
+__device__ __forceinline__ void step(float (&h)[V], const float (&d)[V], const float (&x)[V]) {
+    if constexpr (kLogit) {
+        float u[V];
+        neg(u, x);
+        fma(u, d, u, x);
+        fma(h, d, h, u);
+    } else {
+        fma(h, d, h, x);
+    }
+}
+
+// A row's decays: s in the logit form, else the gate a itself.
+template <bool kLogit, int V>
+__device__ __forceinline__ const float (&decay_of(const float (&s)[V], const float (&a)[V]))[V] {
+    if constexpr (kLogit) return s;
+    else return a;
 }
 
 // A tile's place: batch row, time tile, channel block.
@@ -574,10 +652,8 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
             float a[VEC], x[VEC];
             fetch<T, kVec, 0>(p, q, stage, r, a);
             fetch<T, kVec, 1>(p, q, stage, r, x);
-            if constexpr (kLogit) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) s[r][v] = sigmoid(a[v]);
-            }
+            if constexpr (kLogit) sigmoid(s[r], a);
+            const float(&d)[VEC] = decay_of<kLogit>(s[kLogit ? r : 0], a);
             if (t0 + r < p.N) {
                 if constexpr (kPacked) {
                     const int w = info[rg * R + r], o = w & kOwner;
@@ -585,12 +661,8 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
                         load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr,
                                             p, q, Bv);
                 }
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
-                    A[v] *= d;
-                    Bv[v] = fmaf(d, Bv[v], added<kLogit>(d, x[v]));
-                }
+                mul(A, A, d);
+                step<kLogit>(Bv, d, x);
             }
         }
         put<T, kVec>(sa, A);
@@ -632,11 +704,7 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
                 if (kPacked && (w & kBegin))
                     load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr, p,
                                         q, h);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
-                    h[v] = fmaf(d, h[v], added<kLogit>(d, x[v]));
-                }
+                step<kLogit>(h, decay_of<kLogit>(s[kLogit ? r : 0], a), x);
                 if (kVec && !kPacked) piece<0>(stage, r) = pack(h);
                 else if (p.O && (!kPacked || o != kOwner)) store_row<T, kVec>(p.O, p, q, t0 + r, h);
                 if (kPacked && (w & kEnd) && o != kOwner && p.fin)
@@ -716,10 +784,8 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
             fetch<T, kVec, 0>(p, q, stage, r, a);
             fetch<T, kVec, 1>(p, q, stage, r, x);
             fetch<T, kVec, 2>(p, q, stage, r, g);
-            if constexpr (kLogit) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) s[r][v] = sigmoid(a[v]);
-            }
+            if constexpr (kLogit) sigmoid(s[r], a);
+            const float(&d)[VEC] = decay_of<kLogit>(s[kLogit ? r : 0], a);
             if (t0 + r < p.N) {
                 const int w = kPacked ? info[rg * R + r] : 0, o = w & kOwner;
                 if (kPacked && (w & kBegin))
@@ -727,13 +793,9 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
                                         p, q, Bf);
                 if (kPacked && (w & kEnd) && p.init && o != kOwner)
                     add_state<T, kVec>(p.init + static_cast<int64_t>(o) * p.C, p, q, g);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
-                    A[v] *= d;
-                    Bf[v] = fmaf(d, Bf[v], added<kLogit>(d, x[v]));
-                    Br[v] = live ? fmaf(A[v], g[v], Br[v]) : Br[v];
-                }
+                mul(A, A, d);
+                step<kLogit>(Bf, d, x);
+                if (live) fma(Br, A, g, Br);
                 if (kPacked && (w & kEnd)) live = false;
             }
         }
@@ -793,11 +855,7 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
                 float a[VEC], x[VEC];
                 fetch<T, kVec, 0>(p, q, stage, r, a);
                 fetch<T, kVec, 1>(p, q, stage, r, x);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
-                    h[v] = fmaf(d, h[v], added<kLogit>(d, x[v]));
-                }
+                step<kLogit>(h, decay_of<kLogit>(s[kLogit ? r : 0], a), x);
             }
 #pragma unroll
             for (int r = r0 + H - 1; r >= r0; --r) {
@@ -810,14 +868,21 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
                     if (kPacked && (w & kEnd))
                         load_state<T, kVec>(p.init && o != kOwner ? p.init + static_cast<int64_t>(o) * p.C : nullptr, p,
                                             q, y);
-                    float da[VEC], dx[VEC];
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) {
-                        const float d = kLogit ? s[kLogit ? r : 0][v] : a[v];
-                        const float tot = g[v] + y[v], hv = hp[r - r0][v];
-                        dx[v] = kLogit ? (1.f - d) * tot : tot;
-                        da[v] = kLogit ? d * dx[v] * (hv - x[v]) : tot * hv;
-                        y[v] = d * tot;
+                    const float(&d)[VEC] = decay_of<kLogit>(s[kLogit ? r : 0], a);
+                    float da[VEC], dx[VEC], u[VEC], k[VEC];
+                    add(dx, g, y);  // the whole gradient at h_t
+                    mul(y, d, dx);
+                    if constexpr (kLogit) {
+                        neg(u, d);
+                        fill(k, 1.f);
+                        add(u, u, k);
+                        mul(dx, u, dx);
+                        neg(u, x);
+                        add(u, hp[r - r0], u);
+                        mul(da, d, dx);
+                        mul(da, da, u);
+                    } else {
+                        mul(da, dx, hp[r - r0]);
                     }
                     if constexpr (kVec && !kPacked) {
                         piece<0>(stage, r) = pack(da);
