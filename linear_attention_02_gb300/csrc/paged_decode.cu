@@ -40,10 +40,10 @@
 // small kernel joins in the order of the ranges.
 //
 // Measured (measured copy bandwidth 6.79 TB/s): 256 requests x 16 heads x 4096 positions,
-// D = 64, bf16: 660 us, 6.5 TB/s; D = 128 bf16 with 8 query heads a key head 5.7 TB/s and
+// D = 64, bf16: 655 us, 6.5 TB/s; D = 128 bf16 with 8 query heads a key head 5.7 TB/s and
 // with 16 heads 4.6 TB/s, fp32 D = 64 5.5 and D = 128 6.1 TB/s, bf16 D = 32 5.3 TB/s: there
 // a step's chain of products and exponentials on the few warps that shared memory leaves
-// room for bounds it.  A small call (4 requests, up to 300 positions) takes 9.3 us.
+// room for bounds it.  A small call (4 requests, up to 300 positions) takes 8.1 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -778,9 +778,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
     const int64_t index = blockIdx.x;
     const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t col = index;
-    if (p.direct && p.lens[index / p.HT] < 0) return;
-    const int4 d = p.desc[index];
-    if (d.y == 0) return;
+    const int len = p.direct ? p.lens[index / p.HT] : 0;
+    const int4 d = p.desc[index];  // unwritten for a row without a request
+    if (len < 0 || d.y == 0) return;
     if (!p.direct) col = d.w;
     const int64_t r = col / p.HT;
     const int c = static_cast<int>(col - r * p.HT), kh = c / p.tiles_per_kh, h0 = (c - kh * p.tiles_per_kh) * p.heads;
@@ -790,7 +790,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
 #pragma unroll
     for (int e = 0; e < E; ++e) a[e] = 0.f;
     const int each = (d.y + kJoinWarps - 1) / kJoinWarps, i1 = min(d.y, (warp + 1) * each);
-    constexpr int N = 8;  // ranges fetched at once
+    // Ranges fetched at once: 8 where a column has many (13.2 us against 14.2 us with 4 at
+    // 16 requests x 16 heads x 4000 positions), else 4 (48.9 us against 50.2 us with 8 at 64
+    // requests x 4 x 16 heads, D = 64).
+    constexpr int N = kJoinWarps == 16 ? 8 : 4;
     for (int i0 = warp * each; i0 < i1; i0 += N) {
         float pm[N], pl[N], v[N][E];
 #pragma unroll
@@ -799,8 +802,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
             const float* part = p.part + ((static_cast<int64_t>(d.x) + i) * 2 + (i ? 0 : d.z)) * p.heads * (D + 4);
             pm[x] = i < i1 ? part[p.heads * D + 2 * h] : -INFINITY;
             pl[x] = i < i1 ? part[p.heads * D + 2 * h + 1] : 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[x][e] = i < i1 ? part[h * D + lane + 32 * e] : 0.f;
+            const float* row = part + h * D + lane * E;
+            if constexpr (E == 4) {
+                const float4 f = i < i1 ? *reinterpret_cast<const float4*>(row) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[x][0] = f.x, v[x][1] = f.y, v[x][E - 2] = f.z, v[x][E - 1] = f.w;
+            } else if constexpr (E == 2) {
+                const float2 f = i < i1 ? *reinterpret_cast<const float2*>(row) : make_float2(0.f, 0.f);
+                v[x][0] = f.x, v[x][E - 1] = f.y;
+            } else {
+                v[x][0] = i < i1 ? *row : 0.f;
+            }
         }
 #pragma unroll
         for (int x = 0; x < N; ++x) {
@@ -814,7 +825,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
     }
     if (lane == 0) s_m[warp] = m, s_l[warp] = l;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_a[warp][lane + 32 * e] = a[e];
+    for (int e = 0; e < E; ++e) s_a[warp][lane * E + e] = a[e];
     __syncthreads();
     const int64_t row = r * p.s.Hq + kh * p.G + h0 + h;
     for (int i = threadIdx.x; i < D; i += kJoinWarps * 32) {
@@ -922,19 +933,27 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(p.direct ? n.cols : n.max_ranges), n.heads);
-        // Few columns are cut into many ranges each and want many warps at them (91 us
-        // against 97 us at 6 x 4 x 8 heads); many columns are cut into few (71 us
-        // against 88 us at 64 x 4 x 16 heads).
+        // Warps by the ranges that a column can be cut into, so that each fetches its own at
+        // once: 653 us with 2, 656 us with 4 at 256 x 16 key heads (2 ranges a column), 106 us
+        // with 4, 107 us with 2 at 48 requests (about 10), 8.1 us with 8, 8.6 us with 16 at 4 x 4
+        // (about 20).  But 4 at most where the blocks fill the GPU anyway (48.9 us against
+        // 53.7 us with 8 at 64 x 4 x 16 heads).
+        const int64_t most = std::min((n.most + n.cols - 1) / n.cols, n.max_ranges / n.cols + 2);
         const bool few = n.cols * n.heads <= 2 * static_cast<int64_t>(c.num_sms);
-        cfg.blockDim = dim3(few ? 512 : 128);
+        const int warps = most <= 8 ? 2 : most <= 16 || !few ? 4 : most <= 32 ? 8 : 16;
+        cfg.blockDim = dim3(32 * warps);
         cfg.stream = c.stream;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        e = few ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 16>, p)
-                : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 4>, p);
+        e = cudaLaunchKernelEx(&cfg,
+                               warps == 2   ? paged_join_kernel<D, 2>
+                               : warps == 4 ? paged_join_kernel<D, 4>
+                               : warps == 8 ? paged_join_kernel<D, 8>
+                                            : paged_join_kernel<D, 16>,
+                               p);
         note_launch();
     }
     scratch_free(c, base);
