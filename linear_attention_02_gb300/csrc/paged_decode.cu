@@ -25,7 +25,9 @@
 // bf16 storage: m16n8k16; q, k, v are exact operands, the weights are fp32 and go
 // in as three bf16 terms (24 bits), so no precision is lost against fp32
 // arithmetic.  fp32 storage: m16n8k8 tf32 products of two-term splits (relative
-// error 2^-21).  With up to 8 query heads a key head (kHeads = 8), the operand's
+// error 2^-22, the operands of the scores and the weights split by rounding; by cutting
+// off, and with a score's products summed up in one go, the unit's truncation left up to
+// 1.4e-6 in lse and 2.3e-6 in out, so it is 2.3e-7 and 5.8e-7, at 0 to 7% of the time).  With up to 8 query heads a key head (kHeads = 8), the operand's
 // rows 8 to 15 hold a second term of the same heads instead of nothing; with more,
 // they hold heads 8 to 15, and heads past 16 take further passes.
 // The warp-level matrix instruction is enough here: a step of 16 x 64 bf16 keys
@@ -41,7 +43,7 @@
 //
 // Measured (measured copy bandwidth 6.79 TB/s): 256 requests x 16 heads x 4096 positions,
 // D = 64, bf16: 655 us, 6.5 TB/s; D = 128 bf16 with 8 query heads a key head 5.7 TB/s and
-// with 16 heads 4.6 TB/s, fp32 D = 64 5.5 and D = 128 6.1 TB/s, bf16 D = 32 5.3 TB/s: there
+// with 16 heads 4.6 TB/s, fp32 D = 64 5.5 and D = 128 5.8 TB/s, bf16 D = 32 5.3 TB/s: there
 // a step's chain of products and exponentials on the few warps that shared memory leaves
 // room for bounds it.  A small call (4 requests, up to 300 positions) takes 8.1 us.
 #include <cuda_bf16.h>
@@ -131,6 +133,12 @@ __device__ __forceinline__ float ex2(float x) {
 // takes its top 11 bits).  An infinity gives a NaN: see exact_scores.
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
     hi = x & 0xFFFFE000u;
+    lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
+}
+// The same with hi rounded to nearest, so that lo fits its 11 bits but for one at most and
+// has either sign.  For scores, whose error is the sum's own where a request is short.
+__device__ __forceinline__ void split_tf32_rn(uint32_t x, uint32_t& hi, uint32_t& lo) {
+    hi = (x + 0x1000u) & 0xFFFFE000u;
     lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -428,7 +436,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 const uint32_t w[4] = {u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    if constexpr (!kBf16 && ROWS == 1) split_tf32(w[x], qf[0][i][x], qf[1][i][x]);
+                    if constexpr (!kBf16 && ROWS == 1) split_tf32_rn(w[x], qf[0][i][x], qf[1][i][x]);
                     else qf[z][i][x] = w[x];
                 }
             }
@@ -483,6 +491,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
             uint32_t kw[2][4];
+            float from0[2][4] = {};  // fp32 storage: each 64 bytes of the rows from zero, then added in fp32
+            float(&d)[2][4] = kBf16 ? s : from0;
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const uint4 k = *reinterpret_cast<const uint4*>(st + Ly::kat(g, t, n, i));
@@ -493,36 +503,42 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 if constexpr (kBf16) {
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
-                        mma_bf16(s[n], qf[0][i][h], ROWS == 2 ? qf[ROWS - 1][i][h] : 0u, qf[0][i][h + 1],
+                        mma_bf16(d[n], qf[0][i][h], ROWS == 2 ? qf[ROWS - 1][i][h] : 0u, qf[0][i][h + 1],
                                  ROWS == 2 ? qf[ROWS - 1][i][h + 1] : 0u, kw[n][h], kw[n][h + 1]);
                 } else {
                     uint32_t kh[2][2], kl[2][2];
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        split_tf32(kw[n][h], kh[n][0], kl[n][0]);
-                        split_tf32(kw[n][h + 1], kh[n][1], kl[n][1]);
+                        split_tf32_rn(kw[n][h], kh[n][0], kl[n][0]);
+                        split_tf32_rn(kw[n][h + 1], kh[n][1], kl[n][1]);
                     }
                     if constexpr (ROWS == 1) {  // rows: both terms of q
 #pragma unroll
                         for (int n = 0; n < 2; ++n)
-                            mma_tf32(s[n], qf[0][i][h], qf[1][i][h], qf[0][i][h + 1], qf[1][i][h + 1], kh[n][0], kh[n][1]);
+                            mma_tf32(d[n], qf[0][i][h], qf[1][i][h], qf[0][i][h + 1], qf[1][i][h + 1], kh[n][0], kh[n][1]);
 #pragma unroll
                         for (int n = 0; n < 2; ++n)
-                            mma_tf32(s[n], qf[0][i][h], qf[1][i][h], qf[0][i][h + 1], qf[1][i][h + 1], kl[n][0], kl[n][1]);
+                            mma_tf32(d[n], qf[0][i][h], qf[1][i][h], qf[0][i][h + 1], qf[1][i][h + 1], kl[n][0], kl[n][1]);
                     } else {
                         uint32_t ah[4], al[4];
-                        split_tf32(qf[0][i][h], ah[0], al[0]);
-                        split_tf32(qf[1][i][h], ah[1], al[1]);
-                        split_tf32(qf[0][i][h + 1], ah[2], al[2]);
-                        split_tf32(qf[1][i][h + 1], ah[3], al[3]);
+                        split_tf32_rn(qf[0][i][h], ah[0], al[0]);
+                        split_tf32_rn(qf[1][i][h], ah[1], al[1]);
+                        split_tf32_rn(qf[0][i][h + 1], ah[2], al[2]);
+                        split_tf32_rn(qf[1][i][h + 1], ah[3], al[3]);
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) mma_tf32(s[n], ah[0], ah[1], ah[2], ah[3], kh[n][0], kh[n][1]);
+                        for (int n = 0; n < 2; ++n) mma_tf32(d[n], ah[0], ah[1], ah[2], ah[3], kh[n][0], kh[n][1]);
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) mma_tf32(s[n], ah[0], ah[1], ah[2], ah[3], kl[n][0], kl[n][1]);
+                        for (int n = 0; n < 2; ++n) mma_tf32(d[n], ah[0], ah[1], ah[2], ah[3], kl[n][0], kl[n][1]);
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) mma_tf32(s[n], al[0], al[1], al[2], al[3], kh[n][0], kh[n][1]);
+                        for (int n = 0; n < 2; ++n) mma_tf32(d[n], al[0], al[1], al[2], al[3], kh[n][0], kh[n][1]);
                     }
                 }
+            }
+            if constexpr (!kBf16) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][e] += d[n][e];
             }
         }
         if constexpr (!kBf16) {
@@ -640,7 +656,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 for (int z = 0; z < ROWS; ++z)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        split_tf32(__float_as_uint(s[n][2 * z + e]), wh[n][z][e], wl[n][z][e]);
+                        split_tf32_rn(__float_as_uint(s[n][2 * z + e]), wh[n][z][e], wl[n][z][e]);
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 uint32_t v[4][4];
