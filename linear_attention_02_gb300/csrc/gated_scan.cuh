@@ -436,7 +436,10 @@ __device__ __forceinline__ void row_info(const Args<T>& p, int k, int* info, uns
     if (tid < 32) {  // owners: running maximum over the rows
         int m[LR + 1], run = f0 - 1, top = -1;
 #pragma unroll
-        for (int r = 0; r <= LR; ++r) m[r] = info[tid * LR + r];
+        for (int r = 0; r < LR; ++r) m[r] = info[tid * LR + r];
+        // the row behind the lane's own, from its lane: that word of info is written below
+        m[LR] = __shfl_down_sync(0xffffffffu, m[0], 1);
+        if (tid == 31) m[LR] = info[TILE];
 #pragma unroll
         for (int r = 0; r < LR; ++r) top = max(top, m[r]);
 #pragma unroll
@@ -444,7 +447,7 @@ __device__ __forceinline__ void row_info(const Args<T>& p, int k, int* info, uns
             const int up = __shfl_up_sync(0xffffffffu, top, o);
             if (tid >= o) top = max(top, up);
         }
-        const int up = __shfl_up_sync(0xffffffffu, top, 1);  // every lane has read its rows
+        const int up = __shfl_up_sync(0xffffffffu, top, 1);
         if (tid) run = max(run, up);
         unsigned g = 0;
 #pragma unroll
