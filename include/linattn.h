@@ -255,6 +255,8 @@ la_status la_softmax_decode_step(const void* q, const void* k, const void* v, vo
  *   Ckpt  fp32, nullable (written) la_gated_scan_ckpt_floats(B, N, C) words: the
  *         running state at every 128th row, for the backward
  * N <= 2^31 - 129, num_seqs < 2^29 - 1 and B * N * C < 2^40.
+ * The logit form's s_t and 1 - s_t are each formed without cancellation: the
+ * smaller is within (|a_t| + 6) 2^-23 of itself, the other is one less it.
  * Decays lie in [-1, 1]; the state is fp32 throughout.  Rows are summed up in
  * parts, whose products of decays may round to 0: behind an infinite or NaN
  * state, the rows of its channel and sequence are infinite or NaN.  A sequence's

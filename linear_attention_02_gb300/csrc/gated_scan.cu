@@ -106,9 +106,15 @@ __global__ void scan_step_kernel(const T* __restrict__ a, const T* __restrict__ 
             hv[v] = f.x, hv[v + 1] = f.y, hv[v + 2] = f.z, hv[v + 3] = f.w;
         }
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const float d = kLogit ? sigmoid(av[v]) : av[v];
-            hv[v] = fmaf(d, hv[v], kLogit ? (1.f - d) * xv[v] : xv[v]);
+        for (int v = 0; v < VEC; v += 4) {
+            float d[4], h4[4];
+            const float x4[4] = {xv[v], xv[v + 1], xv[v + 2], xv[v + 3]};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = av[v + i], h4[i] = hv[v + i];
+            if constexpr (kLogit) gate(d, d);
+            step<kLogit>(h4, d, x4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) hv[v + i] = h4[i];
         }
 #pragma unroll
         for (int v = 0; v < VEC; v += 4)
@@ -117,10 +123,12 @@ __global__ void scan_step_kernel(const T* __restrict__ a, const T* __restrict__ 
         return;
     }
     for (int64_t i = i0; i < n; ++i) {
-        const float d = kLogit ? sigmoid(to_f(a[i])) : to_f(a[i]);
-        const float y = fmaf(d, h[i], kLogit ? (1.f - d) * to_f(x[i]) : to_f(x[i]));
-        h[i] = y;
-        out[i] = from_f<T>(y);
+        float d[2] = {to_f(a[i]), 0.f}, y[2] = {h[i], 0.f};
+        const float xi[2] = {to_f(x[i]), 0.f};
+        if constexpr (kLogit) gate(d, d);
+        step<kLogit>(y, d, xi);
+        h[i] = y[0];
+        out[i] = from_f<T>(y[0]);
     }
 }
 
