@@ -24,12 +24,15 @@
 // bank conflicts.
 // bf16 storage: m16n8k16; q, k, v are exact operands, the weights are fp32 and go
 // in as three bf16 terms (24 bits), so no precision is lost against fp32
-// arithmetic.  fp32 storage: m16n8k8 tf32 products of two-term splits (relative
-// error 2^-22, the operands of the scores and the weights split by rounding; by cutting
-// off, and with a score's products summed up in one go, the unit's truncation left up to
-// 1.4e-6 in lse and 2.3e-6 in out, so it is 2.3e-7 and 5.8e-7, at 0 to 7% of the time).  With up to 8 query heads a key head (kHeads = 8), the operand's
-// rows 8 to 15 hold a second term of the same heads instead of nothing; with more,
-// they hold heads 8 to 15, and heads past 16 take further passes.
+// arithmetic.  fp32 storage: m16n8k8 tf32 products of splits.  Values go in whole, as two
+// tf32 terms and a bf16 one (in two terms half of them lost a bit or two, always towards 0,
+// even where a request has one position; the third costs 0 to 5% at D = 64, 7% at 32 and 10
+// to 16% at 128).  Queries, keys and weights go in as two terms split by rounding, which keep
+// 23 of 24 bits: a term of a score is off by 2^-22 of itself, no more than D fp32 additions
+// leave, and a weight by 2^-24, a fourth of what the approximate power that makes it does.
+// With up to 8 query heads a key head (kHeads = 8), the operand's rows 8 to 15 hold a
+// second term of the same heads instead of nothing; with more, they hold heads 8 to 15
+// (and the product of two second terms is left out), and heads past 16 take further passes.
 // The warp-level matrix instruction is enough here: a step of 16 x 64 bf16 keys
 // and values is 4 KB of memory traffic, about 170 cycles of an SM's share of the
 // bandwidth, against 24 small products.
@@ -129,14 +132,16 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// x = hi + lo: hi the top 11 significant bits, lo the exact rest (the product
-// takes its top 11 bits).  An infinity gives a NaN: see exact_scores.
-__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
+// x = hi + mid + low, exactly: 11 significant bits, the next 11 and the last 2 (a bf16's
+// bits, in the upper half).  An infinity gives a NaN.
+__device__ __forceinline__ void split3(uint32_t x, uint32_t& hi, uint32_t& mid, uint32_t& low) {
     hi = x & 0xFFFFE000u;
-    lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
+    const uint32_t lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
+    mid = lo & 0xFFFFE000u;
+    low = __float_as_uint(__uint_as_float(lo) - __uint_as_float(mid));
 }
-// The same with hi rounded to nearest, so that lo fits its 11 bits but for one at most and
-// has either sign.  For scores, whose error is the sum's own where a request is short.
+// x = hi + lo in two terms: hi rounded to nearest, so that lo fits its 11 bits but for
+// one at most and has either sign.  An infinity gives a NaN: see exact_scores.
 __device__ __forceinline__ void split_tf32_rn(uint32_t x, uint32_t& hi, uint32_t& lo) {
     hi = (x + 0x1000u) & 0xFFFFE000u;
     lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
@@ -562,6 +567,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 }
             }
         }
+        // to base 2, rounded once for the maximum and for the weights alike: the largest
+        // score's weight is exactly 1, so a single position's row comes out bit for bit
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2 * ROWS; ++e) s[n][e] *= sc;
         if (seen[0] != 0xFFFFu) {
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -573,7 +584,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         float top[ROWS];
 #pragma unroll
         for (int z = 0; z < ROWS; ++z) {
-            top[z] = fmaxf(fmaxf(s[0][2 * z], s[0][2 * z + 1]), fmaxf(s[1][2 * z], s[1][2 * z + 1])) * sc;
+            top[z] = fmaxf(fmaxf(s[0][2 * z], s[0][2 * z + 1]), fmaxf(s[1][2 * z], s[1][2 * z + 1]));
             up |= top[z] > m[z] + kSlack;
         }
         if (__any_sync(0xffffffffu, up)) {
@@ -597,8 +608,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             const float at = m[z] == -INFINITY ? 0.f : m[z];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                s[n][2 * z] = ex2(fmaf(s[n][2 * z], sc, -at));
-                s[n][2 * z + 1] = ex2(fmaf(s[n][2 * z + 1], sc, -at));
+                s[n][2 * z] = ex2(s[n][2 * z] - at);
+                s[n][2 * z + 1] = ex2(s[n][2 * z + 1] - at);
                 l[z] += s[n][2 * z] + s[n][2 * z + 1];
             }
         }
@@ -657,6 +668,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         split_tf32_rn(__float_as_uint(s[n][2 * z + e]), wh[n][z][e], wl[n][z][e]);
+            uint32_t wb[ROWS][2];  // the weights against the values' last bits
+#pragma unroll
+            for (int z = 0; z < ROWS; ++z) wb[z][0] = pack2(s[0][2 * z], s[0][2 * z + 1]), wb[z][1] = pack2(s[1][2 * z], s[1][2 * z + 1]);
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 uint32_t v[4][4];
@@ -669,19 +683,21 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
+                    uint32_t h[4], c[4], r[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) split3(v[e][j], h[e], c[e], r[e]);
+                    mma_bf16(d[j], wb[0][0], ROWS == 2 ? wb[ROWS - 1][0] : 0u, wb[0][1], ROWS == 2 ? wb[ROWS - 1][1] : 0u,
+                             __byte_perm(r[0], r[1], 0x7632u), __byte_perm(r[2], r[3], 0x7632u));
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        uint32_t h0, h1, c0, c1;
-                        split_tf32(v[2 * n][j], h0, c0);
-                        split_tf32(v[2 * n + 1][j], h1, c1);
+                        constexpr int Z = ROWS - 1;
                         if constexpr (ROWS == 1) {  // rows: both terms of the weights
-                            mma_tf32(d[j], wh[n][0][0], wl[n][0][0], wh[n][0][1], wl[n][0][1], h0, h1);
-                            mma_tf32(d[j], wh[n][0][0], wl[n][0][0], wh[n][0][1], wl[n][0][1], c0, c1);
+                            mma_tf32(d[j], wh[n][0][0], wl[n][0][0], wh[n][0][1], wl[n][0][1], c[2 * n], c[2 * n + 1]);
+                            mma_tf32(d[j], wh[n][0][0], wl[n][0][0], wh[n][0][1], wl[n][0][1], h[2 * n], h[2 * n + 1]);
                         } else {
-                            constexpr int Z = ROWS - 1;
-                            mma_tf32(d[j], wh[n][0][0], wh[n][Z][0], wh[n][0][1], wh[n][Z][1], h0, h1);
-                            mma_tf32(d[j], wh[n][0][0], wh[n][Z][0], wh[n][0][1], wh[n][Z][1], c0, c1);
-                            mma_tf32(d[j], wl[n][0][0], wl[n][Z][0], wl[n][0][1], wl[n][Z][1], h0, h1);
+                            mma_tf32(d[j], wh[n][0][0], wh[n][Z][0], wh[n][0][1], wh[n][Z][1], c[2 * n], c[2 * n + 1]);
+                            mma_tf32(d[j], wl[n][0][0], wl[n][Z][0], wl[n][0][1], wl[n][Z][1], h[2 * n], h[2 * n + 1]);
+                            mma_tf32(d[j], wh[n][0][0], wh[n][Z][0], wh[n][0][1], wh[n][Z][1], h[2 * n], h[2 * n + 1]);
                         }
                     }
                 }
