@@ -269,6 +269,15 @@ la_status la_forward_gated_scan(const void* A, const void* X, void* Out, int B, 
                                 la_dtype dtype, la_gate_form form, const int* seq_starts, int num_seqs,
                                 const float* h_init, float* h_final, float* Ckpt, void* stream);
 
+/*
+ * The same for a padded row axis: with fill 1, rows that belong to no packed sequence are
+ * written too, with 0.  (With fill 0 they are left as they are, as by the call above.)
+ */
+la_status la_forward_gated_scan_padded(const void* A, const void* X, void* Out, int B, int N, int C,
+                                       la_dtype dtype, la_gate_form form, const int* seq_starts,
+                                       int num_seqs, const float* h_init, float* h_final, float* Ckpt,
+                                       int fill, void* stream);
+
 /* Size in fp32 words of the gated scan's checkpoints: B * ceil(N / 128) * C, or
  * 0 for non-positive sizes.  Pure arithmetic; no device call. */
 size_t la_gated_scan_ckpt_floats(int B, int N, int C);
@@ -302,6 +311,13 @@ la_status la_backward_gated_scan(const void* A, const void* X, const void* dOut,
                                  const int* seq_starts, int num_seqs, const float* h_init,
                                  const float* dh_final, float* dh_init, const float* Ckpt,
                                  void* stream);
+
+/* The same for a padded row axis: rows of no sequence get 0 in dA (fill 1), dX (2) or both (3). */
+la_status la_backward_gated_scan_padded(const void* A, const void* X, const void* dOut, void* dA,
+                                        void* dX, int B, int N, int C, la_dtype dtype,
+                                        la_gate_form form, const int* seq_starts, int num_seqs,
+                                        const float* h_init, const float* dh_final, float* dh_init,
+                                        const float* Ckpt, int fill, void* stream);
 
 /*
  * One token of the gated recurrence for B sequences: h is updated in place and
@@ -381,6 +397,14 @@ la_status la_paged_decode_step(const void* q, const void* k, const void* v, void
                                void* V_pages, const int* block_table, const int* cached_lens, float* out,
                                float* lse, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
                                int max_pages, int window, float scale, la_dtype dtype, void* stream);
+
+/* The same for a padded batch: rows without a request get 0 in out (fill 1), -infinity in
+ * lse (2) or both (3). */
+la_status la_paged_decode_step_padded(const void* q, const void* k, const void* v, void* K_pages,
+                                      void* V_pages, const int* block_table, const int* cached_lens,
+                                      float* out, float* lse, int R, int Hq, int Hkv, int D,
+                                      int num_pages, int page_size, int max_pages, int window,
+                                      float scale, la_dtype dtype, int fill, void* stream);
 
 /* Scratch bytes that one la_paged_decode_step or la_page_map call takes from the
  * library pool (la_paged_append takes none); SIZE_MAX for sizes that the call

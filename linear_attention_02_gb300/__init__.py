@@ -460,9 +460,12 @@ def la_forward_gated_scan(A, X, form="decay", out=None, h_init=None, return_stat
     seq_starts: optional int32 [S+1] cutting the rows of a B = 1 call into packed
     sequences; h_init, and the final state with return_state, are then [S,C] (else [B,C]),
     fp32.  ckpt: optional fp32 tensor of la_gated_scan_ckpt_floats(B, N, C) elements that
-    receives states for la_backward_gated_scan(Ckpt=...).  Returns Out, or (Out, h_final)."""
+    receives states for la_backward_gated_scan(Ckpt=...).  Returns Out, or (Out, h_final).
+
+    Rows that no packed sequence holds are 0 in an Out that the call allocates, and left as
+    they are in `out`."""
     B, N, C, S, num, code, dev = _scan_args(A, X, form, seq_starts)
-    dt = A.dtype
+    dt, fill = A.dtype, int(out is None)
     if out is None:
         out = torch.empty_like(A)
     else:
@@ -472,8 +475,8 @@ def la_forward_gated_scan(A, X, form="decay", out=None, h_init=None, return_stat
     if ckpt is not None:
         _check_scan_ckpt(ckpt, "ckpt", B, N, C, dev)
     h_f = torch.empty((S, C), dtype=torch.float32, device=A.device) if return_state else None
-    _launch(_lib.la_forward_gated_scan, dev, stream, A.data_ptr(), X.data_ptr(), out.data_ptr(), B, N, C,
-            _dtype(A), code, _ptr(seq_starts), num, _ptr(h_init), _ptr(h_f), _ptr(ckpt))
+    _launch(_lib.la_forward_gated_scan_padded, dev, stream, A.data_ptr(), X.data_ptr(), out.data_ptr(), B, N, C,
+            _dtype(A), code, _ptr(seq_starts), num, _ptr(h_init), _ptr(h_f), _ptr(ckpt), fill)
     return (out, h_f) if return_state else out
 
 
@@ -482,9 +485,10 @@ def la_backward_gated_scan(A, X, dOut, form="decay", h_init=None, dh_final=None,
     """Backward of la_forward_gated_scan; returns (dA, dX) or (dA, dX, dh_init).
 
     dh_final: optional gradient at the final state; Ckpt: the forward's checkpoints
-    (computed by the call when absent)."""
+    (computed by the call when absent).  Rows that no packed sequence holds are 0 in
+    gradients that the call allocates, and left as they are in dA and dX given to it."""
     B, N, C, S, num, code, dev = _scan_args(A, X, form, seq_starts)
-    dt = A.dtype
+    dt, fill = A.dtype, (dA is None) + 2 * (dX is None)
     _shaped(dOut, "dOut", (B, N, C), dt, dev)
     if dA is None:
         dA = torch.empty_like(A)
@@ -501,9 +505,9 @@ def la_backward_gated_scan(A, X, dOut, form="decay", h_init=None, dh_final=None,
     if Ckpt is not None:
         _check_scan_ckpt(Ckpt, "Ckpt", B, N, C, dev)
     dh = torch.empty((S, C), dtype=torch.float32, device=A.device) if return_dh_init else None
-    _launch(_lib.la_backward_gated_scan, dev, stream, A.data_ptr(), X.data_ptr(), dOut.data_ptr(),
+    _launch(_lib.la_backward_gated_scan_padded, dev, stream, A.data_ptr(), X.data_ptr(), dOut.data_ptr(),
             dA.data_ptr(), dX.data_ptr(), B, N, C, _dtype(A), code, _ptr(seq_starts), num, _ptr(h_init),
-            _ptr(dh_final), _ptr(dh), _ptr(Ckpt))
+            _ptr(dh_final), _ptr(dh), _ptr(Ckpt), fill)
     return (dA, dX, dh) if return_dh_init else (dA, dX)
 
 
@@ -586,13 +590,14 @@ def la_paged_append(k, v, K_pages, V_pages, slot_map, stream=None):
 
 
 def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, window=0, scale=None,
-                         out=None, return_lse=False, stream=None):
+                         out=None, return_lse=False, stream=None, lse=None):
     """Softmax attention decode step over a paged KV cache, one request per row.
 
     Appends k, v [R,Hkv,D] at position cached_lens[r] of each request (None, None: appends
     nothing) and returns out [R,Hq,D] fp32 = softmax(scale q K^T) V over the request's last
-    `window` positions (0: all), with return_lse also the log of the sum [R,Hq] fp32.  Rows with a
-    negative length are left as they are.  scale None: 1 / sqrt(D)."""
+    `window` positions (0: all), with return_lse also the log of the sum [R,Hq] fp32 (in `lse` if
+    given).  Rows with a negative length (no request) are left as they are in an out or lse given
+    to the call; in one that it allocates they are 0 and -infinity.  scale None: 1 / sqrt(D)."""
     P, Hkv, page, D, dev = _pools(K_pages, V_pages)
     dt = K_pages.dtype
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
@@ -612,14 +617,20 @@ def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, wi
         scale = 0.0
     elif ctypes.c_float(float(scale)).value == 0.0:  # the C call's 0 means the default
         raise ValueError("scale must not be 0 in fp32")
+    fill = 0
     if out is None:
         out = torch.empty((R, Hq, D), dtype=torch.float32, device=q.device)
+        fill = 1
     else:
         _shaped(out, "out", (R, Hq, D), torch.float32, dev)
-    lse = torch.empty((R, Hq), dtype=torch.float32, device=q.device) if return_lse else None
-    _launch(_lib.la_paged_decode_step, dev, stream, q.data_ptr(), _ptr(k), _ptr(v), K_pages.data_ptr(),
+    if lse is not None:
+        _shaped(lse, "lse", (R, Hq), torch.float32, dev)
+    elif return_lse:
+        lse = torch.empty((R, Hq), dtype=torch.float32, device=q.device)
+        fill |= 2
+    _launch(_lib.la_paged_decode_step_padded, dev, stream, q.data_ptr(), _ptr(k), _ptr(v), K_pages.data_ptr(),
             V_pages.data_ptr(), block_table.data_ptr(), cached_lens.data_ptr(), out.data_ptr(), _ptr(lse), R,
-            Hq, Hkv, D, P, page, block_table.shape[1], int(window), float(scale), _dtype(K_pages))
+            Hq, Hkv, D, P, page, block_table.shape[1], int(window), float(scale), _dtype(K_pages), fill)
     return (out, lse) if return_lse else out
 
 

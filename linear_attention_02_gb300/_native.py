@@ -36,10 +36,13 @@ SIGNATURES = {
     "la_gated_scan_ckpt_floats": [_I, _I, _I],
     "la_forward_gated_scan": [_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _F, _F, _F, _P],
     "la_backward_gated_scan": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _F, _F, _F, _F, _P],
+    "la_forward_gated_scan_padded": [_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _F, _F, _F, _I, _P],
+    "la_backward_gated_scan_padded": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _F, _F, _F, _F, _I, _P],
     "la_gated_scan_decode_step": [_P, _P, _F, _P, _I, _I, _I, _I, _P],
     "la_page_map": [_P, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P],
     "la_paged_append": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P],
     "la_paged_decode_step": [_P, _P, _P, _P, _P, _P, _P, _F, _F, _I, _I, _I, _I, _I, _I, _I, _I, _R, _I, _P],
+    "la_paged_decode_step_padded": [_P, _P, _P, _P, _P, _P, _P, _F, _F, _I, _I, _I, _I, _I, _I, _I, _I, _R, _I, _I, _P],
     "la_gated_scan_workspace_bytes": [_I, _I, _I, _I, _I, _I],
     "la_paged_decode_workspace_bytes": [_I, _I, _I, _I, _I, _I, _I, _I],
     "la_page_map_workspace_bytes": [_I],

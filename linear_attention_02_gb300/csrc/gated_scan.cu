@@ -44,25 +44,26 @@ cudaError_t unset_words(const LaunchCtx& c, unsigned* a, size_t na, unsigned* b,
 
 template <typename T>
 cudaError_t gated_scan_forward(const LaunchCtx& c, const T* A, const T* X, T* O, const ScanShape& s,
-                               const float* h_init, float* h_final, float* Ckpt) {
+                               const float* h_init, float* h_final, float* Ckpt, bool fill) {
     Args<T> a = args_of<T>(s, A, X);
     a.O = O;
     a.init = h_init;
     a.fin = h_final;
     a.incl = Ckpt;
+    a.fill = fill ? 1 : 0;
     return launch<T, false>(c, a, s.logit, Ckpt == nullptr);
 }
 
 template <typename T>
 cudaError_t gated_scan_backward(const LaunchCtx& c, const T* A, const T* X, const T* G, T* dA, T* dX,
                                 const ScanShape& s, const float* h_init, const float* dh_final,
-                                float* dh_init, const float* Ckpt) {
+                                float* dh_init, const float* Ckpt, int fill) {
     float* states = nullptr;
     cudaError_t e = cudaSuccess;
     const size_t tiles = (static_cast<size_t>(s.N) + TILE - 1) / TILE;
     if (!Ckpt && tiles > 1) {  // the forward's tile states, without its output
         e = scratch_alloc(c, reinterpret_cast<void**>(&states), sizeof(float) * s.B * tiles * s.C);
-        if (e == cudaSuccess) e = gated_scan_forward<T>(c, A, X, nullptr, s, h_init, nullptr, states);
+        if (e == cudaSuccess) e = gated_scan_forward<T>(c, A, X, nullptr, s, h_init, nullptr, states, false);
     }
     if (e == cudaSuccess) {
         Args<T> a = args_of<T>(s, A, X);
@@ -73,6 +74,7 @@ cudaError_t gated_scan_backward(const LaunchCtx& c, const T* A, const T* X, cons
         a.init = dh_final;
         a.fin = dh_init;
         a.states = Ckpt ? Ckpt : states;
+        a.fill = fill;
         e = launch<T, true>(c, a, s.logit, true);
     }
     scratch_free(c, states);
@@ -146,10 +148,10 @@ cudaError_t gated_scan_step(const LaunchCtx& c, const T* a, const T* x, float* h
 
 #define LA_INST_SCAN(T)                                                                               \
     template cudaError_t gated_scan_forward<T>(const LaunchCtx&, const T*, const T*, T*,              \
-                                               const ScanShape&, const float*, float*, float*);       \
+                                               const ScanShape&, const float*, float*, float*, bool); \
     template cudaError_t gated_scan_backward<T>(const LaunchCtx&, const T*, const T*, const T*, T*,   \
                                                 T*, const ScanShape&, const float*, const float*,     \
-                                                float*, const float*);                                \
+                                                float*, const float*, int);                           \
     template cudaError_t gated_scan_step<T>(const LaunchCtx&, const T*, const T*, float*, T*, int64_t, \
                                             bool);
 LA_INST_SCAN(float) LA_INST_SCAN(__nv_bfloat16)

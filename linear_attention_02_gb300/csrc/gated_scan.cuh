@@ -84,6 +84,7 @@ struct Args {
     unsigned total;             // B * tiles * ncb
     const int* starts;          // packed sequences
     int S;
+    int fill;                   // outputs that get 0 in rows of no sequence: bit 0 O or dA, bit 1 dX
     const float* init;          // forward: h_init; backward: dh_final (state entering the chain)
     float* fin;                 // forward: h_final; backward: dh_init
     const float* h_init;        // backward: the forward's h_init
@@ -605,6 +606,27 @@ __device__ __forceinline__ void empty_sequences(const Args<T>& p, const float* f
     }
 }
 
+// Zeros to the rows before the first packed sequence and behind the last one, over all
+// threads of the grid: two runs of memory.
+template <typename T>
+__device__ __forceinline__ void clear_padding(const Args<T>& p, T* out, bool on) {
+    if (!on) return;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x, all = static_cast<int64_t>(gridDim.x) * NT;
+    const int a = min(max(p.starts[0], 0), p.N), b = max(min(max(p.starts[p.S], 0), p.N), a);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        constexpr int VEC = Geo<T>::VEC;
+        const int64_t from = static_cast<int64_t>(i ? b : 0) * p.C, to = static_cast<int64_t>(i ? p.N : a) * p.C;
+        const int64_t v0 = (from + VEC - 1) / VEC, v1 = to / VEC;  // whole 16-byte pieces
+        for (int64_t v = v0 + id; v < v1; v += all) reinterpret_cast<uint4*>(out)[v] = make_uint4(0, 0, 0, 0);
+        if (id < VEC) {
+            const int64_t head = from + id, tail = v1 * VEC + id;
+            if (head < min(v0 * VEC, to)) out[head] = from_f<T>(0.f);
+            if (tail >= from && tail < to) out[tail] = from_f<T>(0.f);
+        }
+    }
+}
+
 // One channel's fold over the row groups: the tile's (A, B), and whether a row
 // group replaces the state (its "begin" bit, or for the backward pass "end").
 template <int CB, bool kPacked, bool kRev>
@@ -652,7 +674,10 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         tile = *snext;
         __syncthreads();
     }
-    if constexpr (kPacked) empty_sequences(p, p.init, p.fin);
+    if constexpr (kPacked) {
+        empty_sequences(p, p.init, p.fin);
+        clear_padding(p, p.O, p.fill & 1);
+    }
     if (tile < p.total) issue<T, kVec, 2>(p, maps, place_of<T, false>(p, tile), stage, &bar);
     while (tile < p.total) {
         const Place q = place_of<T, false>(p, tile);
@@ -778,7 +803,11 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         tile = *snext;
         __syncthreads();
     }
-    if constexpr (kPacked) empty_sequences(p, p.init, p.fin);
+    if constexpr (kPacked) {
+        empty_sequences(p, p.init, p.fin);
+        clear_padding(p, p.dA, p.fill & 1);
+        clear_padding(p, p.dX, p.fill & 2);
+    }
     if (tile < p.total) issue<T, kVec, 3>(p, maps, place_of<T, true>(p, tile), stage, &bar);
     while (tile < p.total) {
         const Place q = place_of<T, true>(p, tile);

@@ -173,6 +173,13 @@ cudaError_t copy_state(cudaStream_t st, float* to, const float* from, size_t wor
                 : cudaMemsetAsync(to, 0, words * sizeof(float), st);
 }
 
+size_t elem_bytes(la_dtype dt) { return dt == LA_DTYPE_F32 ? 4 : 2; }
+
+// The outputs whose padding a call fills, a bit each of `all`.
+la_status check_fill(const char* fn, int fill, int all) {
+    return fill & ~all ? fail(LA_ERR_INVALID_ARG, "%s: fill=%d", fn, fill) : LA_OK;
+}
+
 // log2 of a supported page size, or -1.
 int page_log2(int page_size) {
     for (int b = 0; b <= 10; ++b)
@@ -673,9 +680,10 @@ size_t la_gated_scan_ckpt_floats(int B, int N, int C) {
     return (size_t)B * (((size_t)N + plan::kScanTile - 1) / plan::kScanTile) * (size_t)C;
 }
 
-la_status la_forward_gated_scan(const void* A, const void* X, void* Out, int B, int N, int C,
-                                la_dtype dtype, la_gate_form form, const int* seq_starts, int num_seqs,
-                                const float* h_init, float* h_final, float* Ckpt, void* stream) {
+static la_status scan_forward(const void* A, const void* X, void* Out, int B, int N, int C,
+                       la_dtype dtype, la_gate_form form, const int* seq_starts, int num_seqs,
+                       const float* h_init, float* h_final, float* Ckpt, bool fill,
+                       void* stream) {
     static const char* fn = "la_forward_gated_scan";
     la_status s = check_scan(fn, B, N, C, dtype, form, seq_starts, num_seqs);
     if (s != LA_OK) return s;
@@ -684,30 +692,44 @@ la_status la_forward_gated_scan(const void* A, const void* X, void* Out, int B, 
         return s;
     const size_t states = (size_t)(seq_starts ? num_seqs : B) * C;
     const bool empty = (size_t)B * N * C == 0 || (seq_starts && num_seqs == 0);
-    if (empty && (!h_final || states == 0)) return LA_OK;
-    if (!empty) {
+    const bool clear = fill && seq_starts && num_seqs == 0 && (size_t)N * C != 0;  // no row has a sequence
+    if (empty && !clear && (!h_final || states == 0)) return LA_OK;
+    if (!empty || clear) {
         const void* p[] = {A, X, Out};
         const char* nm[] = {"A", "X", "Out"};
         if ((s = check_ptrs(fn, p, nm, 3, 16)) != LA_OK) return s;
     }
     LaunchCtx ctx;
     if ((s = get_ctx((cudaStream_t)stream, &ctx)) != LA_OK) return s;
+    if (clear) return finish(cudaMemsetAsync(Out, 0, elem_bytes(dtype) * N * C, ctx.stream), fn);
     if (empty) return finish(copy_state(ctx.stream, h_final, h_init, states), fn);
     const ScanShape sh = {B, N, C, form == LA_GATE_LOGIT, seq_starts, num_seqs};
     using bf = __nv_bfloat16;
     return finish(dtype == LA_DTYPE_F32
                       ? gated_scan_forward<float>(ctx, (const float*)A, (const float*)X, (float*)Out, sh,
-                                                  h_init, h_final, Ckpt)
+                                                  h_init, h_final, Ckpt, fill)
                       : gated_scan_forward<bf>(ctx, (const bf*)A, (const bf*)X, (bf*)Out, sh, h_init,
-                                               h_final, Ckpt),
+                                               h_final, Ckpt, fill),
                   fn);
 }
 
-la_status la_backward_gated_scan(const void* A, const void* X, const void* dOut, void* dA, void* dX,
-                                 int B, int N, int C, la_dtype dtype, la_gate_form form,
-                                 const int* seq_starts, int num_seqs, const float* h_init,
-                                 const float* dh_final, float* dh_init, const float* Ckpt,
-                                 void* stream) {
+la_status la_forward_gated_scan(const void* A, const void* X, void* Out, int B, int N, int C,
+                                la_dtype dtype, la_gate_form form, const int* seq_starts, int num_seqs,
+                                const float* h_init, float* h_final, float* Ckpt, void* stream) {
+    return scan_forward(A, X, Out, B, N, C, dtype, form, seq_starts, num_seqs, h_init, h_final, Ckpt, false, stream);
+}
+
+la_status la_forward_gated_scan_padded(const void* A, const void* X, void* Out, int B, int N, int C,
+                                       la_dtype dtype, la_gate_form form, const int* seq_starts, int num_seqs,
+                                       const float* h_init, float* h_final, float* Ckpt, int fill, void* stream) {
+    if (la_status s = check_fill("la_forward_gated_scan", fill, 1)) return s;
+    return scan_forward(A, X, Out, B, N, C, dtype, form, seq_starts, num_seqs, h_init, h_final, Ckpt, fill != 0, stream);
+}
+
+static la_status scan_backward(const void* A, const void* X, const void* dOut, void* dA, void* dX,
+                        int B, int N, int C, la_dtype dtype, la_gate_form form,
+                        const int* seq_starts, int num_seqs, const float* h_init,
+                        const float* dh_final, float* dh_init, const float* Ckpt, int fill, void* stream) {
     static const char* fn = "la_backward_gated_scan";
     la_status s = check_scan(fn, B, N, C, dtype, form, seq_starts, num_seqs);
     if (s != LA_OK) return s;
@@ -716,24 +738,50 @@ la_status la_backward_gated_scan(const void* A, const void* X, const void* dOut,
         return s;
     const size_t states = (size_t)(seq_starts ? num_seqs : B) * C;
     const bool empty = (size_t)B * N * C == 0 || (seq_starts && num_seqs == 0);
-    if (empty && (!dh_init || states == 0)) return LA_OK;
-    if (!empty) {
+    const bool clear = fill && seq_starts && num_seqs == 0 && (size_t)N * C != 0;  // no row has a sequence
+    if (empty && !clear && (!dh_init || states == 0)) return LA_OK;
+    if (!empty || clear) {
         const void* p[] = {A, X, dOut, dA, dX};
         const char* nm[] = {"A", "X", "dOut", "dA", "dX"};
         if ((s = check_ptrs(fn, p, nm, 5, 16)) != LA_OK) return s;
     }
     LaunchCtx ctx;
     if ((s = get_ctx((cudaStream_t)stream, &ctx)) != LA_OK) return s;
+    if (clear) {
+        const size_t bytes = elem_bytes(dtype) * N * C;
+        cudaError_t e = fill & 1 ? cudaMemsetAsync(dA, 0, bytes, ctx.stream) : cudaSuccess;
+        if (e == cudaSuccess && (fill & 2)) e = cudaMemsetAsync(dX, 0, bytes, ctx.stream);
+        return finish(e, fn);
+    }
     if (empty) return finish(copy_state(ctx.stream, dh_init, dh_final, states), fn);
     const ScanShape sh = {B, N, C, form == LA_GATE_LOGIT, seq_starts, num_seqs};
     using bf = __nv_bfloat16;
     return finish(dtype == LA_DTYPE_F32
                       ? gated_scan_backward<float>(ctx, (const float*)A, (const float*)X,
                                                    (const float*)dOut, (float*)dA, (float*)dX, sh, h_init,
-                                                   dh_final, dh_init, Ckpt)
+                                                   dh_final, dh_init, Ckpt, fill)
                       : gated_scan_backward<bf>(ctx, (const bf*)A, (const bf*)X, (const bf*)dOut, (bf*)dA,
-                                                (bf*)dX, sh, h_init, dh_final, dh_init, Ckpt),
+                                                (bf*)dX, sh, h_init, dh_final, dh_init, Ckpt, fill),
                   fn);
+}
+
+la_status la_backward_gated_scan(const void* A, const void* X, const void* dOut, void* dA, void* dX,
+                                 int B, int N, int C, la_dtype dtype, la_gate_form form,
+                                 const int* seq_starts, int num_seqs, const float* h_init,
+                                 const float* dh_final, float* dh_init, const float* Ckpt,
+                                 void* stream) {
+    return scan_backward(A, X, dOut, dA, dX, B, N, C, dtype, form, seq_starts, num_seqs, h_init, dh_final, dh_init,
+                         Ckpt, 0, stream);
+}
+
+la_status la_backward_gated_scan_padded(const void* A, const void* X, const void* dOut, void* dA, void* dX,
+                                        int B, int N, int C, la_dtype dtype, la_gate_form form,
+                                        const int* seq_starts, int num_seqs, const float* h_init,
+                                        const float* dh_final, float* dh_init, const float* Ckpt, int fill,
+                                        void* stream) {
+    if (la_status s = check_fill("la_backward_gated_scan", fill, 3)) return s;
+    return scan_backward(A, X, dOut, dA, dX, B, N, C, dtype, form, seq_starts, num_seqs, h_init, dh_final, dh_init,
+                         Ckpt, fill, stream);
 }
 
 la_status la_gated_scan_decode_step(const void* a, const void* x, float* h, void* out, int B, int C,
@@ -812,10 +860,11 @@ la_status la_paged_append(const void* k, const void* v, void* K_pages, void* V_p
                   fn);
 }
 
-la_status la_paged_decode_step(const void* q, const void* k, const void* v, void* K_pages,
-                               void* V_pages, const int* block_table, const int* cached_lens, float* out,
-                               float* lse, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
-                               int max_pages, int window, float scale, la_dtype dtype, void* stream) {
+static la_status paged_step(const void* q, const void* k, const void* v, void* K_pages,
+                     void* V_pages, const int* block_table, const int* cached_lens, float* out,
+                     float* lse, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
+                     int max_pages, int window, float scale, la_dtype dtype, int fill,
+                     void* stream) {
     static const char* fn = "la_paged_decode_step";
     int log2p = 0;
     la_status s = check_pages(fn, num_pages, page_size, &log2p);
@@ -847,6 +896,7 @@ la_status la_paged_decode_step(const void* q, const void* k, const void* v, void
     const void* ip[] = {cached_lens, block_table};
     const char* in[] = {"cached_lens", "block_table"};
     if ((s = check_ptrs(fn, ip, in, max_pages ? 2 : 1, 4)) != LA_OK) return s;
+    if ((fill & 2) && !lse) return fail(LA_ERR_INVALID_ARG, "%s: lse is NULL", fn);
     if (reinterpret_cast<uintptr_t>(lse) & 3u)
         return fail(LA_ERR_INVALID_ARG, "%s: lse is not 4-byte aligned", fn);
     LaunchCtx ctx;
@@ -857,7 +907,7 @@ la_status la_paged_decode_step(const void* q, const void* k, const void* v, void
 #define LA_PD_CASE(Ty, d)                                                                              \
     if (D == d)                                                                                        \
         e = paged_decode_step<Ty, d>(ctx, (const Ty*)q, (const Ty*)k, (const Ty*)v, (Ty*)K_pages,      \
-                                     (Ty*)V_pages, block_table, cached_lens, out, lse, sh);
+                                     (Ty*)V_pages, block_table, cached_lens, out, lse, sh, fill);
     if (dtype == LA_DTYPE_F32) {
         LA_PD_CASE(float, 32) else LA_PD_CASE(float, 64) else LA_PD_CASE(float, 128)
     } else {
@@ -865,6 +915,24 @@ la_status la_paged_decode_step(const void* q, const void* k, const void* v, void
     }
 #undef LA_PD_CASE
     return finish(e, fn);
+}
+
+la_status la_paged_decode_step(const void* q, const void* k, const void* v, void* K_pages,
+                               void* V_pages, const int* block_table, const int* cached_lens, float* out,
+                               float* lse, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
+                               int max_pages, int window, float scale, la_dtype dtype, void* stream) {
+    return paged_step(q, k, v, K_pages, V_pages, block_table, cached_lens, out, lse, R, Hq, Hkv, D, num_pages,
+                      page_size, max_pages, window, scale, dtype, 0, stream);
+}
+
+la_status la_paged_decode_step_padded(const void* q, const void* k, const void* v, void* K_pages,
+                                      void* V_pages, const int* block_table, const int* cached_lens, float* out,
+                                      float* lse, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
+                                      int max_pages, int window, float scale, la_dtype dtype, int fill,
+                                      void* stream) {
+    if (la_status s = check_fill("la_paged_decode_step", fill, 3)) return s;
+    return paged_step(q, k, v, K_pages, V_pages, block_table, cached_lens, out, lse, R, Hq, Hkv, D, num_pages,
+                      page_size, max_pages, window, scale, dtype, fill, stream);
 }
 
 la_status la_selftest_expired_waits(void* stream) {

@@ -152,6 +152,8 @@ cudaError_t poly2_forward(const LaunchCtx& c, const T* Q, const T* K, const T* V
 cudaError_t poly2_forward_tc(const LaunchCtx& c, const __nv_bfloat16* Q, const __nv_bfloat16* K,
                              const __nv_bfloat16* V, __nv_bfloat16* O, int BH, int N, bool causal);
 
+// Below, `fill`: which outputs get 0 in rows of no packed sequence (forward: Out; backward:
+// bit 0 dA, bit 1 dX), or in rows without a request (bit 0: 0 to out, bit 1: -infinity to lse).
 // Rows of a gated scan: [B][N][C], or with `starts` (device, [num_seqs + 1]) one
 // row axis (B = 1) cut into packed sequences.
 struct ScanShape {
@@ -162,11 +164,11 @@ struct ScanShape {
 };
 template <typename T>
 cudaError_t gated_scan_forward(const LaunchCtx& c, const T* A, const T* X, T* O, const ScanShape& s,
-                               const float* h_init, float* h_final, float* Ckpt);
+                               const float* h_init, float* h_final, float* Ckpt, bool fill);
 template <typename T>
 cudaError_t gated_scan_backward(const LaunchCtx& c, const T* A, const T* X, const T* G, T* dA, T* dX,
                                 const ScanShape& s, const float* h_init, const float* dh_final,
-                                float* dh_init, const float* Ckpt);
+                                float* dh_init, const float* Ckpt, int fill);
 template <typename T>
 cudaError_t gated_scan_step(const LaunchCtx& c, const T* a, const T* x, float* h, T* out, int64_t n,
                             bool logit);
@@ -193,7 +195,7 @@ size_t paged_decode_scratch(const PagedShape& s, int D, bool bf16, int num_sms);
 template <typename T, int D>
 cudaError_t paged_decode_step(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K, T* V,
                               const int* table, const int* lens, float* out, float* lse,
-                              const PagedShape& s);
+                              const PagedShape& s, int fill);
 
 template <typename T, int D, int M>
 cudaError_t decode_step(const LaunchCtx& c, const T* q, const T* k, const T* v, float* S,

@@ -29,7 +29,7 @@
 // even where a request has one position; the third costs 0 to 5% at D = 64, 7% at 32 and 10
 // to 16% at 128).  Queries, keys and weights go in as two terms split by rounding, which keep
 // 23 of 24 bits: a term of a score is off by 2^-22 of itself, no more than D fp32 additions
-// leave, and a weight by 2^-24, a fourth of what the approximate power that makes it does.
+// leave, and a weight by 2^-23, half of what the approximate power that makes it leaves.
 // With up to 8 query heads a key head (kHeads = 8), the operand's rows 8 to 15 hold a
 // second term of the same heads instead of nothing; with more, they hold heads 8 to 15
 // (and the product of two second terms is left out), and heads past 16 take further passes.
@@ -169,6 +169,7 @@ struct PagedArgs {
     unsigned* next;             // ranges taken beyond the first of each warp (null: one each is enough)
     const int *table, *lens;
     float *out, *lse;
+    int fill;                   // what rows without a request get: bit 0, out 0; bit 1, lse -infinity
     float* part;                // [ranges][2][heads x (D + 4)]: output sums [heads][D], then maximum, sum of each head
     int4* desc;                 // {first range, ranges, its slot, column} of a split column; ranges 0: none
     unsigned* status;
@@ -806,6 +807,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 template <int D, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedArgs p) {
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps], s_a[kJoinWarps][D];
+    if (p.fill && blockIdx.y == 0)  // rows without a request, under the kernel before
+        for (int r = blockIdx.x; r < p.s.R; r += gridDim.x)
+            if (p.lens[r] < 0) {
+                const int64_t row = static_cast<int64_t>(r) * p.s.Hq;
+                for (int i = threadIdx.x; (p.fill & 1) && i < p.s.Hq * (D / 4); i += kJoinWarps * 32)
+                    reinterpret_cast<float4*>(p.out + row * D)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i = threadIdx.x; (p.fill & 2) && i < p.s.Hq; i += kJoinWarps * 32) p.lse[row + i] = -INFINITY;
+            }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t index = blockIdx.x;
     const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -923,7 +932,7 @@ Plan plan_of(const PagedShape& s, int num_sms) {
 
 template <typename T, int D, int kHeads>
 cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K, T* V, const int* table,
-                   const int* lens, float* out, float* lse, const PagedShape& s) {
+                   const int* lens, float* out, float* lse, const PagedShape& s, int fill) {
     using Ly = Lay<T, D>;
     auto* kernel = paged_decode_kernel<T, D, kHeads>;
     const Plan n = plan_of<T, D, kHeads>(s, c.num_sms);
@@ -941,6 +950,7 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
     p.lens = lens;
     p.out = out;
     p.lse = lse;
+    p.fill = fill;
     p.status = c.status_word;
     p.max_ranges = n.max_ranges;
     p.heads = n.heads;
@@ -997,9 +1007,9 @@ cudaError_t launch(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K,
 template <typename T, int D>
 cudaError_t paged_decode_step(const LaunchCtx& c, const T* q, const T* k, const T* v, T* K, T* V,
                               const int* table, const int* lens, float* out, float* lse,
-                              const PagedShape& s) {
-    return s.Hq / s.Hkv <= 8 ? launch<T, D, 8>(c, q, k, v, K, V, table, lens, out, lse, s)
-                             : launch<T, D, 16>(c, q, k, v, K, V, table, lens, out, lse, s);
+                              const PagedShape& s, int fill) {
+    return s.Hq / s.Hkv <= 8 ? launch<T, D, 8>(c, q, k, v, K, V, table, lens, out, lse, s, fill)
+                             : launch<T, D, 16>(c, q, k, v, K, V, table, lens, out, lse, s, fill);
 }
 
 size_t paged_decode_scratch(const PagedShape& s, int D, bool bf16, int num_sms) {
@@ -1018,7 +1028,7 @@ size_t paged_decode_scratch(const PagedShape& s, int D, bool bf16, int num_sms) 
 #define LA_INST_PD(T, D)                                                                          \
     template cudaError_t paged_decode_step<T, D>(const LaunchCtx&, const T*, const T*, const T*, T*, \
                                                  T*, const int*, const int*, float*, float*,      \
-                                                 const PagedShape&);
+                                                 const PagedShape&, int);
 LA_INST_PD(float, 32) LA_INST_PD(float, 64) LA_INST_PD(float, 128)
 LA_INST_PD(__nv_bfloat16, 32) LA_INST_PD(__nv_bfloat16, 64) LA_INST_PD(__nv_bfloat16, 128)
 
