@@ -171,3 +171,30 @@ def test_results_do_not_depend_on_the_run(N, C, lens, dt):
     first = once()
     for _ in range(5):
         assert all(torch.equal(a, b) for a, b in zip(first, once()))
+
+
+@pytest.mark.parametrize("backward,given", [(False, False), (False, True), (True, True), (True, False)])
+def test_scratch_of_a_large_call_is_what_is_reported(backward, given):
+    # tens of MB, against which the pool's rounding to 2 MB an allocation is small
+    la = _la()
+    B, N, C = 4, 65536, 1024
+    A = torch.full((B, N, C), 0.5, dtype=torch.bfloat16, device="cuda")
+    X, out, dA, dX = (torch.zeros_like(A) for _ in range(4))
+    ck = torch.zeros(la.la_gated_scan_ckpt_floats(B, N, C), device="cuda") if given else None
+
+    def call():
+        if backward:
+            la.la_backward_gated_scan(A, X, X, dA=dA, dX=dX, Ckpt=ck)
+        else:
+            la.la_forward_gated_scan(A, X, out=out, ckpt=ck)
+
+    want = la.la_gated_scan_workspace_bytes(B, N, C, torch.bfloat16, backward=backward, ckpt_given=given)
+    states = 4 * B * (N // 128) * C  # (A, B) of each tile, its end state unless checkpoints hold it; the states
+    assert want == 16 + states * (2 if given and not backward else 4 if backward and not given else 3)
+    call()
+    torch.cuda.synchronize()
+    la.la_scratch_peak_bytes(reset=True)
+    call()
+    torch.cuda.synchronize()
+    slack = 2 * (2 << 20)
+    assert slack < want / 4 and want <= la.la_scratch_peak_bytes() <= want + slack
