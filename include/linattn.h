@@ -480,8 +480,10 @@ size_t la_scratch_peak_bytes(int reset);
 /*
  * Test hook for the failure path of the real kernels, off unless called: the
  * next library call on this process that launches the tensor-core causal
- * forward or backward has unit `unit` of its work split skip its look-back
- * publication (the flag that later units of the same head wait for), and
+ * forward or backward, or the gated scan's, has unit `unit` of its work split
+ * (of the scan: tile `unit` in the order in which its tiles are taken, over all
+ * batch rows and channel blocks) skip its look-back publication (the flag or
+ * words that later units of the same head or channels wait for), and
  * gives every look-back wait of that launch `spin_limit` polls (about 0.3 us
  * each) instead of the default.  The units waiting on the missing flag give
  * up, set the look-back bit (0x2) in the device error word, drain their copies

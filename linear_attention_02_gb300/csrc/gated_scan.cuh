@@ -91,6 +91,8 @@ struct Args {
     const float* states;        // backward: the forward's end state of each tile, [B][tiles][C]
     float *incl, *aggA, *aggB;  // chain of this direction: end states and (A, B), [B][tiles][C]
     unsigned* ticket;           // tiles taken - 1; null: one tile a chain, blocks take tiles by number
+    unsigned withhold;          // test hook: a tile (in the chain's order) that publishes nothing (-1: none)
+    unsigned spin_limit;        // polls of a look-back before it gives up
     unsigned* status;
 };
 
@@ -535,7 +537,7 @@ __device__ float look_back(const Args<T>& p, Window<kWindow>& w, int i, int64_t 
         st_relaxed(p.aggA + at + i * step, At);
         st_relaxed(p.aggB + at + i * step, Bt);
     }
-    for (unsigned spin = 0; spin < tcf::kSpinLimit; ++spin) {
+    for (unsigned spin = 0; spin < p.spin_limit; ++spin) {
         int n = 0;
 #pragma unroll
         for (int d = 0; d < kWindow; ++d)
@@ -719,16 +721,16 @@ scan_forward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         if (on) {
             const bool last = q.k + 1 == p.tiles;
             float At, Bt, h = 0.f;
-            const bool cut = fold<CB, kPacked, false>(sa + tid, sb + tid, grp, At, Bt);
+            const bool cut = fold<CB, kPacked, false>(sa + tid, sb + tid, grp, At, Bt), mute = tile == p.withhold;
             float* out = p.incl + at + static_cast<int64_t>(q.k) * p.C;
-            if (cut && !last) st_relaxed(out, Bt);
-            if (q.k) h = look_back<T, kWindow>(p, win, q.k, at, p.C, At, Bt, cut);
+            if (cut && !last && !mute) st_relaxed(out, Bt);
+            if (q.k) h = look_back<T, kWindow>(p, win, q.k, at, p.C, At, Bt, cut || mute);
             else if (!kPacked && p.init) h = p.init[static_cast<int64_t>(q.b) * p.C + c];
             const float end = cut ? Bt : fmaf(At, h, Bt);
             // The next tile is taken as late as the copy allows: a block that took it
             // earlier would hold up the chain with it.
             if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
-            if (!last && !cut) st_relaxed(out, end);
+            if (!last && !cut && !mute) st_relaxed(out, end);
             if (!kPacked && last && p.fin) p.fin[static_cast<int64_t>(q.b) * p.C + c] = end;
 #pragma unroll 8
             for (int g = 0; g < RG; ++g) {
@@ -858,14 +860,14 @@ scan_backward_kernel(const Args<T> p, const __grid_constant__ Maps maps) {
         if (on) {
             const bool last = q.k == 0;
             float At, Bt, y = 0.f, h = h0;
-            const bool cut = fold<CB, kPacked, true>(sa + tid, sc + tid, grp, At, Bt);
+            const bool cut = fold<CB, kPacked, true>(sa + tid, sc + tid, grp, At, Bt), mute = tile == p.withhold;
             float* out = p.incl + at + static_cast<int64_t>(i) * p.C;
-            if (cut && !last) st_relaxed(out, Bt);
-            if (i) y = look_back<T, kWindow>(p, win, i, at, p.C, At, Bt, cut);
+            if (cut && !last && !mute) st_relaxed(out, Bt);
+            if (i) y = look_back<T, kWindow>(p, win, i, at, p.C, At, Bt, cut || mute);
             else if (!kPacked && p.init) y = p.init[static_cast<int64_t>(q.b) * p.C + c];
             const float end = cut ? Bt : fmaf(At, y, Bt);
             if (tid == 0) mine = p.ticket ? atomicAdd(p.ticket, 1u) + 1u : tile + gridDim.x;
-            if (!last && !cut) st_relaxed(out, end);
+            if (!last && !cut && !mute) st_relaxed(out, end);
             if (!kPacked && last && p.fin) p.fin[static_cast<int64_t>(q.b) * p.C + c] = end;
             // the carry entering each row group replaces its Br, from the last group down
 #pragma unroll 8

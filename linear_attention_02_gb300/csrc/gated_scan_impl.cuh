@@ -31,6 +31,8 @@ cudaError_t launch(const LaunchCtx& c, Args<T> a, bool logit, bool own_incl) {
     a.tiles = static_cast<int>(tiles);
     a.ncb = static_cast<int>(ncb);
     a.total = static_cast<unsigned>(a.B * tiles * ncb);
+    a.withhold = static_cast<unsigned>(c.withhold_unit);
+    a.spin_limit = c.spin_limit ? c.spin_limit : tcf::kSpinLimit;
     a.status = c.status_word;
 
     Maps maps = {};
