@@ -252,8 +252,10 @@ la_status la_softmax_decode_step(const void* q, const void* k, const void* v, vo
  *   h_init  [sequences][C] fp32, nullable (read)     state before the first row
  *   h_final [sequences][C] fp32, nullable (written)  state after the last row
  *         (of an empty sequence: h_init, or 0)
- *   Ckpt  fp32, nullable (written) la_gated_scan_ckpt_floats(B, N, C) words: the
- *         running state at every 128th row, for the backward
+ *   Ckpt  fp32, nullable (written) la_gated_scan_ckpt_floats(B, N, C) words
+ *         [B][ceil(N / 128)][C] for the backward: entry k holds the state after
+ *         row 128 (k + 1) - 1 where a row follows that one; the last entry of
+ *         each batch row, and entries after rows of no sequence, hold no state
  * N <= 2^31 - 129, num_seqs < 2^29 - 1 and B * N * C < 2^40.
  * The logit form's s_t and 1 - s_t are each formed without cancellation: the
  * smaller is within (|a_t| + 6) 2^-23 of itself, the other is one less it.

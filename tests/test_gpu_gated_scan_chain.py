@@ -198,3 +198,24 @@ def test_scratch_of_a_large_call_is_what_is_reported(backward, given):
     torch.cuda.synchronize()
     slack = 2 * (2 << 20)
     assert slack < want / 4 and want <= la.la_scratch_peak_bytes() <= want + slack
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("form", ["decay", "logit"])
+@pytest.mark.parametrize("B,N,C,lens", [(2, 700, 41, None), (1, 2700, 1104, None), (1, 384, 64, None),
+                                        (1, 900, 96, [128, 100, 300, 372]), (1, 900, 33, [1, 0, 800])])
+def test_checkpoints_are_the_states_at_every_128th_row(B, N, C, lens, form, dt):
+    la = _la()
+    g = torch.Generator().manual_seed(N)
+    A, X = _gates_near_one(B, N, C, dt, form, g), torch.randn(B, N, C, generator=g).to(DT[dt])
+    starts = None if lens is None else _starts(lens)
+    S = B if lens is None else len(lens)
+    h0, z = torch.randn(S, C, generator=g), np.zeros((S, C))
+    p = {"A": A.double().numpy(), "X": X.double().numpy(), "G": np.zeros((B, N, C)), "h0": h0.double().numpy(), "dh": z}
+    ck = torch.empty(la.la_gated_scan_ckpt_floats(B, N, C), device="cuda")
+    la.la_forward_gated_scan(A.cuda(), X.cuda(), form=form, h_init=h0.cuda(), ckpt=ck,
+                             seq_starts=None if lens is None else torch.tensor(starts, dtype=torch.int32, device="cuda"))
+    want, bound = _expect(p, form, ref._sequences(B, N, starts))
+    last = N if lens is None else starts[-1]
+    rows = [t for t in range(127, N - 1, 128) if t < last]
+    _near(ck.view(B, -(-N // 128), C)[:, :len(rows)], want[0][:, rows], bound[0][:, rows])
