@@ -391,7 +391,8 @@ la_status la_paged_append(const void* k, const void* v, void* K_pages, void* V_p
  * A request without a position has out 0 and lse -infinity.  An infinite element of
  * a value row makes its column of out infinite or NaN.  Positions whose page is out
  * of range are left out.  D in {32, 64, 128}, Hq a multiple of Hkv.
- * Reads one key and one value row per position and key head, whatever Hq / Hkv;
+ * Reads one key and one value row per position and key head for every 16 query heads
+ * that share it (once for up to 16, twice for up to 32, and so on);
  * max_pages * page_size < 2^30.  No page may be held by two requests that append
  * to it.  Results do not depend on the run.
  */

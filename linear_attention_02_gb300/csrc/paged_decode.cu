@@ -4,7 +4,7 @@
 // over the request's own positions (its pages, then its own new row), and
 // lse = m + ln sum_j e^{s_j - m}.  Query head h reads key head h / (Hq / Hkv).
 //
-// Bound by memory: every key and value is read once for all query heads that
+// Bound by memory: every key and value is read once for up to 16 query heads that
 // share it (2 D elements a position and key head).  The unit of work is a step:
 // 16 positions of one key head, for up to 16 of its query heads.  The steps of
 // all requests, request-major, are cut into equal ranges, one to four for each warp of
