@@ -376,6 +376,22 @@ def _shaped(t, name, shape, dtype, dev):
     raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
+_INT_MAX = 2 ** 31 - 1  # the C calls' sizes are 32 bits wide, and ctypes would cut larger ones
+
+
+def _fits(*sizes):
+    if max(sizes) > _INT_MAX:
+        raise ValueError(f"a size of {max(sizes)} does not fit 32 bits")
+
+
+def _int(x, name):
+    """x as a whole number of 32 bits."""
+    n = int(x)
+    if n != x or not -_INT_MAX <= n <= _INT_MAX:
+        raise ValueError(f"{name} must be a whole number of 32 bits, got {x}")
+    return n
+
+
 def _launch(fn, dev, stream, *args):
     """fn(*args, stream handle) with device `dev` current: `stream`, or dev's current stream."""
     if _current_device() == dev:
@@ -404,6 +420,7 @@ def _scan_args(A, X, form, seq_starts):
     _shaped(A, "A", shape, A.dtype, dev)
     _shaped(X, "X", shape, A.dtype, dev)
     B, N, C = shape
+    _fits(B, N, C)
     if seq_starts is None:
         return B, N, C, B, 0, _FORMS[form], dev
     if not isinstance(seq_starts, torch.Tensor) or seq_starts.dim() != 1 or seq_starts.numel() < 1:
@@ -417,7 +434,7 @@ def _scan_args(A, X, form, seq_starts):
 
 def la_gated_scan_ckpt_floats(B, N, C):
     """fp32 words of the gated scan's checkpoints (la_forward_gated_scan(ckpt=...))."""
-    return int(_lib.la_gated_scan_ckpt_floats(B, N, C))
+    return int(_lib.la_gated_scan_ckpt_floats(_int(B, "B"), _int(N, "N"), _int(C, "C")))
 
 
 def _bytes(n):
@@ -430,6 +447,7 @@ def la_gated_scan_workspace_bytes(B, N, C, dtype, backward=False, ckpt_given=Fal
     """Scratch bytes of one la_forward_gated_scan or la_backward_gated_scan call."""
     if dtype not in _DT:
         raise ValueError(f"unsupported dtype {dtype}")
+    B, N, C = _int(B, "B"), _int(N, "N"), _int(C, "C")
     return _bytes(_lib.la_gated_scan_workspace_bytes(int(backward), B, N, C, _DT[dtype], int(ckpt_given)))
 
 
@@ -437,12 +455,14 @@ def la_paged_decode_workspace_bytes(R, Hq, Hkv, D, page_size, max_pages, dtype, 
     """Scratch bytes of one la_paged_decode_step call; num_sms <= 0 asks the current device."""
     if dtype not in _DT:
         raise ValueError(f"unsupported dtype {dtype}")
-    return _bytes(_lib.la_paged_decode_workspace_bytes(R, Hq, Hkv, D, page_size, max_pages, _DT[dtype], num_sms))
+    sizes = [_int(x, n) for x, n in ((R, "R"), (Hq, "Hq"), (Hkv, "Hkv"), (D, "D"), (page_size, "page_size"),
+                                     (max_pages, "max_pages"))]
+    return _bytes(_lib.la_paged_decode_workspace_bytes(*sizes, _DT[dtype], num_sms))
 
 
 def la_page_map_workspace_bytes(R):
     """Scratch bytes of one la_page_map call over R requests."""
-    return _bytes(_lib.la_page_map_workspace_bytes(R))
+    return _bytes(_lib.la_page_map_workspace_bytes(_int(R, "R")))
 
 
 def _check_scan_ckpt(c, name, B, N, C, dev):
@@ -518,6 +538,7 @@ def la_gated_scan_decode_step(a, x, h, form="decay", out=None, stream=None):
     if not isinstance(a, torch.Tensor) or a.dim() != 2:
         raise ValueError("a and x must be [B,C]")
     shape, dt, dev = a.shape, a.dtype, a.get_device()
+    _fits(*shape)
     _shaped(a, "a", shape, dt, dev)
     _shaped(x, "x", shape, dt, dev)
     _shaped(h, "h", shape, torch.float32, dev)
@@ -549,6 +570,7 @@ def la_page_map(cached_lens, new_lens, free_pages, block_table, page_size, num_p
         if not isinstance(t, torch.Tensor) or t.dim() != 1:
             raise ValueError(f"{n} must be a tensor of one dimension")
         _shaped(t, n, t.shape, i32, dev)
+    _fits(R, W, free_pages.shape[0], slot_map.shape[0])
     if seq_starts is None:
         seq_starts = torch.empty(R + 1, dtype=i32, device=block_table.device)
     else:
@@ -558,7 +580,7 @@ def la_page_map(cached_lens, new_lens, free_pages, block_table, page_size, num_p
     else:
         _shaped(counts, "counts", (2,), i32, dev)
     _launch(_lib.la_page_map, dev, stream, cached_lens.data_ptr(), new_lens.data_ptr(), R,
-            free_pages.data_ptr(), free_pages.shape[0], int(page_size), int(num_pages),
+            free_pages.data_ptr(), free_pages.shape[0], _int(page_size, "page_size"), _int(num_pages, "num_pages"),
             block_table.data_ptr(), W, slot_map.data_ptr(), slot_map.shape[0], seq_starts.data_ptr(),
             counts.data_ptr())
     return slot_map, seq_starts, counts
@@ -571,6 +593,7 @@ def _pools(K_pages, V_pages):
     shape, dev = K_pages.shape, K_pages.get_device()
     _shaped(K_pages, "K_pages", shape, K_pages.dtype, dev)
     _shaped(V_pages, "V_pages", shape, K_pages.dtype, dev)
+    _fits(*shape)
     return (*shape, dev)
 
 
@@ -582,6 +605,7 @@ def la_paged_append(k, v, K_pages, V_pages, slot_map, stream=None):
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k and v must be [T, Hkv, D]")
     T = k.shape[0]
+    _fits(T, Hkv, D)
     _shaped(k, "k", (T, Hkv, D), dt, dev)
     _shaped(v, "v", (T, Hkv, D), dt, dev)
     _shaped(slot_map, "slot_map", (T,), torch.int32, dev)
@@ -603,6 +627,7 @@ def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, wi
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [R, Hq, D]")
     R, Hq = q.shape[:2]
+    _fits(R, Hq)
     _shaped(q, "q", (R, Hq, D), dt, dev)
     if (k is None) != (v is None):
         raise ValueError("give both k and v, or neither")
@@ -612,6 +637,7 @@ def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, wi
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError(f"block_table must be [R, max_pages] with R = {R}")
     _shaped(block_table, "block_table", block_table.shape, torch.int32, dev)
+    _fits(block_table.shape[1])
     _shaped(cached_lens, "cached_lens", (R,), torch.int32, dev)
     if scale is None:
         scale = 0.0
@@ -630,7 +656,7 @@ def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, wi
         fill |= 2
     _launch(_lib.la_paged_decode_step_padded, dev, stream, q.data_ptr(), _ptr(k), _ptr(v), K_pages.data_ptr(),
             V_pages.data_ptr(), block_table.data_ptr(), cached_lens.data_ptr(), out.data_ptr(), _ptr(lse), R,
-            Hq, Hkv, D, P, page, block_table.shape[1], int(window), float(scale), _dtype(K_pages), fill)
+            Hq, Hkv, D, P, page, block_table.shape[1], _int(window, "window"), float(scale), _dtype(K_pages), fill)
     return (out, lse) if return_lse else out
 
 
