@@ -376,7 +376,9 @@ def _shaped(t, name, shape, dtype, dev):
     raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
 
 
-_INT_MAX = 2 ** 31 - 1  # the C calls' sizes are 32 bits wide, and ctypes would cut larger ones
+# The C calls' sizes are 32 bits wide, and ctypes would cut larger ones.  Only sizes that memory
+# has room for are looked at: not the pools', whose rows take 64 bytes and more.
+_INT_MAX = 2 ** 31 - 1
 
 
 def _fits(*sizes):
@@ -386,6 +388,8 @@ def _fits(*sizes):
 
 def _int(x, name):
     """x as a whole number of 32 bits."""
+    if type(x) is int and -_INT_MAX <= x <= _INT_MAX:
+        return x
     n = int(x)
     if n != x or not -_INT_MAX <= n <= _INT_MAX:
         raise ValueError(f"{name} must be a whole number of 32 bits, got {x}")
@@ -593,7 +597,6 @@ def _pools(K_pages, V_pages):
     shape, dev = K_pages.shape, K_pages.get_device()
     _shaped(K_pages, "K_pages", shape, K_pages.dtype, dev)
     _shaped(V_pages, "V_pages", shape, K_pages.dtype, dev)
-    _fits(*shape)
     return (*shape, dev)
 
 
@@ -605,7 +608,6 @@ def la_paged_append(k, v, K_pages, V_pages, slot_map, stream=None):
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k and v must be [T, Hkv, D]")
     T = k.shape[0]
-    _fits(T, Hkv, D)
     _shaped(k, "k", (T, Hkv, D), dt, dev)
     _shaped(v, "v", (T, Hkv, D), dt, dev)
     _shaped(slot_map, "slot_map", (T,), torch.int32, dev)
@@ -627,7 +629,6 @@ def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, wi
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [R, Hq, D]")
     R, Hq = q.shape[:2]
-    _fits(R, Hq)
     _shaped(q, "q", (R, Hq, D), dt, dev)
     if (k is None) != (v is None):
         raise ValueError("give both k and v, or neither")
