@@ -879,7 +879,8 @@ static la_status paged_step(const void* q, const void* k, const void* v, void* K
     if (Hq && (Hkv == 0 || Hq % Hkv))
         return fail(LA_ERR_INVALID_ARG, "%s: Hq=%d query heads over Hkv=%d key heads: not a multiple", fn,
                     Hq, Hkv);
-    if (!std::isfinite(scale)) return fail(LA_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+    if (!std::isfinite(scale * 1.4426950408889634f))  // scores are taken to base 2
+        return fail(LA_ERR_INVALID_ARG, "%s: scale=%g, or its product with log2 e, is not finite", fn, scale);
     if ((k == nullptr) != (v == nullptr))
         return fail(LA_ERR_INVALID_ARG, "%s: k and v must both be given or both NULL", fn);
     if ((unsigned long long)max_pages * page_size >= (1ull << 30))

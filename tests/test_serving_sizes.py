@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import linear_attention_02_gb300 as la
+from linear_attention_02_gb300 import _native
 
 BIG = 2 ** 32 + 8
 
@@ -44,3 +45,21 @@ def test_tensors_past_32_bits():
         la.la_backward_gated_scan(a, a, a)
     with pytest.raises(ValueError, match="32 bits"):
         la.la_gated_scan_decode_step(a[0], a[0], torch.empty(0, device="cuda"))
+
+
+FAKE = 0x10000  # aligned, never dereferenced
+
+
+def _dec(k=FAKE, v=FAKE, R=2, Hq=8, Hkv=2, D=64, scale=0.0):
+    return _native.lib.la_paged_decode_step(FAKE, k, v, FAKE, FAKE, FAKE, FAKE, FAKE, None, R, Hq, Hkv, D, 4, 16, 3, 0,
+                                            scale, 1, None)
+
+
+def _msg():
+    return _native.lib.la_last_error_message().decode()
+
+
+def test_scale_past_fp32_in_base_2():
+    # scores are scaled by scale log2 e: infinite in fp32 from 2.36e38 up, and infinity times a score of 0 is NaN
+    for scale in (2.4e38, -3e38):
+        assert _dec(scale=scale) == _native.LA_ERR_INVALID_ARG and "scale" in _msg()
