@@ -889,6 +889,8 @@ static la_status paged_step(const void* q, const void* k, const void* v, void* K
     if ((unsigned long long)R * Hq * D >= (1ull << 31) ||
         (unsigned long long)num_pages * page_size * (Hkv ? Hkv : 1) >= (1ull << 40) / D)
         return fail(LA_ERR_INVALID_ARG, "%s: tensor too large", fn);
+    if (R && Hkv && k && Hq == 0)
+        return fail(LA_ERR_INVALID_ARG, "%s: new rows but no query heads (la_paged_append appends alone)", fn);
     if (R == 0 || Hq == 0) return LA_OK;
     const void* p[] = {q, out, K_pages, V_pages};
     const char* nm[] = {"q", "out", "K_pages", "V_pages"};

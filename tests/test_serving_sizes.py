@@ -63,3 +63,10 @@ def test_scale_past_fp32_in_base_2():
     # scores are scaled by scale log2 e: infinite in fp32 from 2.36e38 up, and infinity times a score of 0 is NaN
     for scale in (2.4e38, -3e38):
         assert _dec(scale=scale) == _native.LA_ERR_INVALID_ARG and "scale" in _msg()
+
+
+def test_new_rows_without_query_heads():
+    # nothing would be attended, but the rows were not appended either
+    assert _dec(Hq=0) == _native.LA_ERR_INVALID_ARG and "query heads" in _msg()
+    assert _dec(Hq=0, k=None, v=None) == _native.LA_OK and _dec(Hq=0, R=0) == _native.LA_OK
+    assert _dec(Hq=0, Hkv=0) == _native.LA_OK
