@@ -661,6 +661,8 @@ size_t la_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int page_s
         (unsigned long long)max_pages * page_size >= (1ull << 30))
         return fail(LA_ERR_INVALID_ARG, "%s: sizes R=%d Hq=%d Hkv=%d max_pages=%d", fn, R, Hq, Hkv, max_pages),
                SIZE_MAX;
+    if ((unsigned long long)R * Hq * D >= (1ull << 31))
+        return fail(LA_ERR_INVALID_ARG, "%s: tensor too large", fn), SIZE_MAX;
     if (num_sms <= 0) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
@@ -672,7 +674,10 @@ size_t la_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int page_s
 }
 
 size_t la_page_map_workspace_bytes(int R) {
-    return R < 0 || R >= (1 << 30) ? SIZE_MAX : plan::page_map_scratch(R);
+    if (R < 0 || R >= (1 << 30))
+        return fail(LA_ERR_INVALID_ARG, "la_page_map_workspace_bytes: R=%d: negative, or 2^30 requests or more", R),
+               SIZE_MAX;
+    return plan::page_map_scratch(R);
 }
 
 size_t la_gated_scan_ckpt_floats(int B, int N, int C) {

@@ -70,3 +70,11 @@ def test_new_rows_without_query_heads():
     assert _dec(Hq=0) == _native.LA_ERR_INVALID_ARG and "query heads" in _msg()
     assert _dec(Hq=0, k=None, v=None) == _native.LA_OK and _dec(Hq=0, R=0) == _native.LA_OK
     assert _dec(Hq=0, Hkv=0) == _native.LA_OK
+
+
+def test_workspace_of_sizes_that_the_call_refuses():
+    f = _native.lib.la_paged_decode_workspace_bytes
+    assert _dec(R=1 << 20, Hq=64, Hkv=64) == _native.LA_ERR_INVALID_ARG and "too large" in _msg()
+    assert f(1 << 20, 64, 64, 64, 16, 4, 1, 152) == _native.SIZE_MAX and "too large" in _msg()
+    _dec(scale=float("inf"))
+    assert _native.lib.la_page_map_workspace_bytes(1 << 30) == _native.SIZE_MAX and "R=" in _msg()
