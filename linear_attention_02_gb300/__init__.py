@@ -381,9 +381,11 @@ def _shaped(t, name, shape, dtype, dev):
 _INT_MAX = 2 ** 31 - 1
 
 
-def _fits(*sizes):
-    if max(sizes) > _INT_MAX:
-        raise ValueError(f"a size of {max(sizes)} does not fit 32 bits")
+def _fits(*tensors):
+    """Refuses tensors with a size past 32 bits (called where one has that many elements)."""
+    n = max(max(t.shape) for t in tensors)
+    if n > _INT_MAX:
+        raise ValueError(f"a size of {n} does not fit 32 bits")
 
 
 def _int(x, name):
@@ -424,7 +426,8 @@ def _scan_args(A, X, form, seq_starts):
     _shaped(A, "A", shape, A.dtype, dev)
     _shaped(X, "X", shape, A.dtype, dev)
     B, N, C = shape
-    _fits(B, N, C)
+    if A.numel() > _INT_MAX:
+        _fits(A)
     if seq_starts is None:
         return B, N, C, B, 0, _FORMS[form], dev
     if not isinstance(seq_starts, torch.Tensor) or seq_starts.dim() != 1 or seq_starts.numel() < 1:
@@ -542,7 +545,8 @@ def la_gated_scan_decode_step(a, x, h, form="decay", out=None, stream=None):
     if not isinstance(a, torch.Tensor) or a.dim() != 2:
         raise ValueError("a and x must be [B,C]")
     shape, dt, dev = a.shape, a.dtype, a.get_device()
-    _fits(*shape)
+    if a.numel() > _INT_MAX:
+        _fits(a)
     _shaped(a, "a", shape, dt, dev)
     _shaped(x, "x", shape, dt, dev)
     _shaped(h, "h", shape, torch.float32, dev)
@@ -574,7 +578,8 @@ def la_page_map(cached_lens, new_lens, free_pages, block_table, page_size, num_p
         if not isinstance(t, torch.Tensor) or t.dim() != 1:
             raise ValueError(f"{n} must be a tensor of one dimension")
         _shaped(t, n, t.shape, i32, dev)
-    _fits(R, W, free_pages.shape[0], slot_map.shape[0])
+    if block_table.numel() + free_pages.numel() + slot_map.numel() > _INT_MAX:
+        _fits(block_table, free_pages, slot_map)
     if seq_starts is None:
         seq_starts = torch.empty(R + 1, dtype=i32, device=block_table.device)
     else:
@@ -638,7 +643,8 @@ def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, wi
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError(f"block_table must be [R, max_pages] with R = {R}")
     _shaped(block_table, "block_table", block_table.shape, torch.int32, dev)
-    _fits(block_table.shape[1])
+    if block_table.numel() > _INT_MAX:
+        _fits(block_table)
     _shaped(cached_lens, "cached_lens", (R,), torch.int32, dev)
     if scale is None:
         scale = 0.0
