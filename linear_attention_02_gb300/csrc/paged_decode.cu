@@ -24,12 +24,15 @@
 // bank conflicts.
 // bf16 storage: m16n8k16; q, k, v are exact operands, the weights are fp32 and go
 // in as three bf16 terms (24 bits), so no precision is lost against fp32
-// arithmetic.  fp32 storage: m16n8k8 tf32 products of splits.  Values go in whole, as two
-// tf32 terms and a bf16 one (in two terms half of them lost a bit or two, always towards 0,
-// even where a request has one position; the third costs 0 to 5% at D = 64, 7% at 32 and 10
-// to 16% at 128).  Queries, keys and weights go in as two terms split by rounding, which keep
-// 23 of 24 bits: a term of a score is off by 2^-22 of itself, no more than D fp32 additions
-// leave, and a weight by 2^-23, half of what the approximate power that makes it leaves.
+// arithmetic.  fp32 storage: m16n8k8 tf32 products of splits.  Queries, keys and weights
+// go in as two terms split by rounding, which keep 23 of 24 bits: a term of a score is
+// off by 2^-22 of itself, no more than D fp32 additions leave, and a weight by 2^-23, half
+// of what the approximate power that makes it leaves.  Values go in as two terms, the
+// second rounded: off by 2^-22 at most, to either side (cut off, half of all values came
+// out smaller by a bit or two); where a request sees no more than kExact positions, so that
+// no sum hides it, a third term, in bf16, carries the rest.  With all three always, a step
+// takes 2% longer at D = 64 (328 us against 321 us at 64 x 16 x 4096) and 11% at 128 (436 us
+// against 394 us at 64 x 8 key heads x 4096).
 // With up to 8 query heads a key head (kHeads = 8), the operand's rows 8 to 15 hold a
 // second term of the same heads instead of nothing; with more, they hold heads 8 to 15
 // (and the product of two second terms is left out), and heads past 16 take further passes.
@@ -65,6 +68,7 @@ namespace {
 
 constexpr int kStep = 16;       // positions of a step
 constexpr float kSlack = 8.f;   // log2 by which a score may pass the maximum kept
+constexpr int kExact = 32;      // positions up to which fp32 values are weighted with all their bits
 
 // A step in shared memory: 16 key rows, then 16 value rows, each as atoms of 16 rows
 // x AB bytes in which 16-byte chunk c of row r lies at chunk c ^ (r & 7) (AB = 128),
@@ -132,13 +136,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// x = hi + mid + low, exactly: 11 significant bits, the next 11 and the last 2 (a bf16's
-// bits, in the upper half).  An infinity gives a NaN.
-__device__ __forceinline__ void split3(uint32_t x, uint32_t& hi, uint32_t& mid, uint32_t& low) {
+// x = hi + lo, exactly: the top 11 significant bits and the other 13, of which a product
+// takes 11.  An infinity gives a NaN.
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t& hi, uint32_t& lo) {
     hi = x & 0xFFFFE000u;
-    const uint32_t lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
-    mid = lo & 0xFFFFE000u;
-    low = __float_as_uint(__uint_as_float(lo) - __uint_as_float(mid));
+    lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
 }
 // x = hi + lo in two terms: hi rounded to nearest, so that lo fits its 11 bits but for
 // one at most and has either sign.  An infinity gives a NaN: see exact_scores.
@@ -669,9 +671,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         split_tf32_rn(__float_as_uint(s[n][2 * z + e]), wh[n][z][e], wl[n][z][e]);
-            uint32_t wb[ROWS][2];  // the weights against the values' last bits
-#pragma unroll
-            for (int z = 0; z < ROWS; ++z) wb[z][0] = pack2(s[0][2 * z], s[0][2 * z + 1]), wb[z][1] = pack2(s[1][2 * z], s[1][2 * z + 1]);
+            // half a unit of the second term, or 0 where a third one takes what the unit cuts off
+            const uint32_t half = cs.row.total - cs.row.first <= kExact ? 0u : 0x1000u;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 uint32_t v[4][4];
@@ -682,13 +683,30 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 }
                 float d[4][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
-                    uint32_t h[4], c[4], r[4];
+                for (int j = 0; j < 4; ++j) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
+                if (half == 0u) {
+                    const uint32_t a0 = pack2(s[0][0], s[0][1]), a2 = pack2(s[1][0], s[1][1]);
+                    const uint32_t a1 = ROWS == 2 ? pack2(s[0][2], s[0][3]) : 0u, a3 = ROWS == 2 ? pack2(s[1][2], s[1][3]) : 0u;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) split3(v[e][j], h[e], c[e], r[e]);
-                    mma_bf16(d[j], wb[0][0], ROWS == 2 ? wb[ROWS - 1][0] : 0u, wb[0][1], ROWS == 2 ? wb[ROWS - 1][1] : 0u,
-                             __byte_perm(r[0], r[1], 0x7632u), __byte_perm(r[2], r[3], 0x7632u));
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t r[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t hi, lo;
+                            split_tf32(v[e][j], hi, lo);
+                            r[e] = __float_as_uint(__uint_as_float(lo) - __uint_as_float(lo & 0xFFFFE000u));
+                        }
+                        mma_bf16(d[j], a0, a1, a2, a3, __byte_perm(r[0], r[1], 0x7632u), __byte_perm(r[2], r[3], 0x7632u));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t h[4], c[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        split_tf32(v[e][j], h[e], c[e]);
+                        c[e] += half;
+                    }
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
                         constexpr int Z = ROWS - 1;
