@@ -29,11 +29,12 @@
 // waits for tiles that running blocks hold, each block working its own in
 // ascending order: the lowest unfinished one can always go on.
 //
-// Measured (the copy bandwidth is 6.79 TB/s): fp32, 4 x 8192 x 1024, forward 67 us
-// (6.0 TB/s), backward 106 us (6.3 TB/s); bf16 logit form, the same rows, 46 us and
-// 72 us (4.4 and 4.6 TB/s); bf16, 65536 x 2048, 138 us and 243 us (5.8 and 5.5 TB/s).
-// What is lost is the chain's wait: without it the same kernels take 62, 102, 38, 62,
-// 119 and 203 us.  A word takes 1.3 us from one SM to another, more while the memory is busy,
+// Measured on the GPU (the copy bandwidth is 6.79 TB/s), decay form: fp32, 4 x 8192 x
+// 1024, forward 68 us (6.0 TB/s), backward 106 us (6.3 TB/s); bf16, the same rows, 40 us
+// and 68 us (5.0 and 4.9 TB/s); bf16, 65536 x 2048, 142 us and 243 us (5.7 and 5.5 TB/s).
+// Logit form, bf16: 51 and 78 us, 177 and 285 us; fp32 69 and 107 us.
+// What is lost is the chain's wait: without it the same kernels take 63, 103, 34, 59,
+// 121 and 205 us, and in the logit form 42, 70, 140 and 244 us.  A word takes 1.3 us from one SM to another, more while the memory is busy,
 // and a tile waits for the slowest of those before it.  It is worst with few channel
 // blocks (B C / 64 below the number of SMs), where many tiles of one chain are under
 // way.  Blocks of a cluster reading each other's (A, B) in shared memory did not help
@@ -489,9 +490,9 @@ __device__ __forceinline__ void row_info(const Args<T>& p, int k, int* info, uns
 
 constexpr unsigned kUnset = 0xFFFFFFFFu;  // a word that nothing has been published in
 // Tiles looked back over at once.  The smaller suits chains of which up to kDeep tiles
-// are under way (65536 x 2048 bf16: forward 138 us with 4, 146 us with 8, 160 us with
+// are under way (65536 x 2048 bf16: forward 142 us with 4, 146 us with 8, 159 us with
 // 16: each more costs two words a tile and registers), the larger those of few channels,
-// whose many tiles advance by a window a round trip (65536 x 256: 48 us against 99 us).
+// whose many tiles advance by a window a round trip (65536 x 256: 44 us against 94 us).
 constexpr int kNear = 4, kFar = 16, kDeep = 48;
 
 __device__ __forceinline__ unsigned ld_relaxed(const float* p) {

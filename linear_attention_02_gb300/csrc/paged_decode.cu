@@ -47,11 +47,13 @@
 // 2^8, so most steps need no exchange between lanes.  A range that starts or ends inside a request leaves partial sums, which a second
 // small kernel joins in the order of the ranges.
 //
-// Measured (measured copy bandwidth 6.79 TB/s): 256 requests x 16 heads x 4096 positions,
-// D = 64, bf16: 655 us, 6.5 TB/s; D = 128 bf16 with 8 query heads a key head 5.7 TB/s and
-// with 16 heads 4.6 TB/s, fp32 D = 64 5.5 and D = 128 5.8 TB/s, bf16 D = 32 5.3 TB/s: there
-// a step's chain of products and exponentials on the few warps that shared memory leaves
-// room for bounds it.  A small call (4 requests, up to 300 positions) takes 8.1 us.
+// Measured on the GPU (measured copy bandwidth 6.79 TB/s): 256 requests x 16 heads x 4096
+// positions, D = 64, bf16: 670 us, 6.4 TB/s.  64 requests x 4096 positions: bf16, D = 128,
+// 4 key heads, 5.2 TB/s with 8 query heads each and 4.7 TB/s with 16 (with G > 16 the bytes
+// are read ceil(G / 16) times); fp32, 6.6 TB/s at 16 key heads, D = 64, 5.6 at D = 32, 5.4 at 8
+// key heads, D = 128, and 3.8 with 12 query heads each; bf16, D = 32, 5.1 TB/s: there a
+// step's chain of products and exponentials on the few warps that shared memory leaves
+// room for bounds it.  A small call (4 requests, up to 300 positions) takes 8.7 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
