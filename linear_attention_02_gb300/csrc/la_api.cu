@@ -686,9 +686,9 @@ size_t la_gated_scan_ckpt_floats(int B, int N, int C) {
 }
 
 static la_status scan_forward(const void* A, const void* X, void* Out, int B, int N, int C,
-                       la_dtype dtype, la_gate_form form, const int* seq_starts, int num_seqs,
-                       const float* h_init, float* h_final, float* Ckpt, bool fill,
-                       void* stream) {
+                              la_dtype dtype, la_gate_form form, const int* seq_starts, int num_seqs,
+                              const float* h_init, float* h_final, float* Ckpt, bool fill,
+                              void* stream) {
     static const char* fn = "la_forward_gated_scan";
     la_status s = check_scan(fn, B, N, C, dtype, form, seq_starts, num_seqs);
     if (s != LA_OK) return s;
@@ -732,9 +732,9 @@ la_status la_forward_gated_scan_padded(const void* A, const void* X, void* Out, 
 }
 
 static la_status scan_backward(const void* A, const void* X, const void* dOut, void* dA, void* dX,
-                        int B, int N, int C, la_dtype dtype, la_gate_form form,
-                        const int* seq_starts, int num_seqs, const float* h_init,
-                        const float* dh_final, float* dh_init, const float* Ckpt, int fill, void* stream) {
+                               int B, int N, int C, la_dtype dtype, la_gate_form form,
+                               const int* seq_starts, int num_seqs, const float* h_init,
+                               const float* dh_final, float* dh_init, const float* Ckpt, int fill, void* stream) {
     static const char* fn = "la_backward_gated_scan";
     la_status s = check_scan(fn, B, N, C, dtype, form, seq_starts, num_seqs);
     if (s != LA_OK) return s;
@@ -866,10 +866,10 @@ la_status la_paged_append(const void* k, const void* v, void* K_pages, void* V_p
 }
 
 static la_status paged_step(const void* q, const void* k, const void* v, void* K_pages,
-                     void* V_pages, const int* block_table, const int* cached_lens, float* out,
-                     float* lse, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
-                     int max_pages, int window, float scale, la_dtype dtype, int fill,
-                     void* stream) {
+                            void* V_pages, const int* block_table, const int* cached_lens, float* out,
+                            float* lse, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
+                            int max_pages, int window, float scale, la_dtype dtype, int fill,
+                            void* stream) {
     static const char* fn = "la_paged_decode_step";
     int log2p = 0;
     la_status s = check_pages(fn, num_pages, page_size, &log2p);
