@@ -417,6 +417,115 @@ size_t la_paged_decode_workspace_bytes(int R, int Hq, int Hkv, int D, int page_s
 size_t la_page_map_workspace_bytes(int R);
 
 /*
+ * Attention of a chunk of new tokens over the paged cache, the form of
+ * la_paged_decode_step for prompts, for parts of long prompts and for several
+ * drafted tokens at once.  The rows seq_starts[r] .. seq_starts[r + 1] - 1 of q
+ * are request r's new tokens; row i of them stands at position
+ * cached_lens[r] + i, and its key and value are in the cache already
+ * (la_paged_append with la_page_map's slots; seq_starts is la_page_map's too):
+ *   out = softmax(scale q K^T) V over the last `window` positions up to its own
+ * (all of them if window is 0).  Query head h reads key head h / (Hq / Hkv).
+ *   q [T][Hq][D] dtype                                        (read)
+ *   K_pages, V_pages [num_pages][Hkv][page_size][D] dtype     (read)
+ *   block_table [R][max_pages] int32, cached_lens [R] int32   (read) positions
+ *         BEFORE the new ones; a negative length marks a request that is none:
+ *         nothing of its rows is read or written
+ *   seq_starts [R + 1] int32                                  (read) not decreasing,
+ *         within 0 .. T
+ *   out [T][Hq][D] dtype                                      (written)
+ *   lse [T][Hq] fp32, nullable                                (written)
+ *   scale 0 means 1 / sqrt(D);  fill: rows of no request get 0 in out (1),
+ *         -infinity in lse (2) or both (3); else they are left as they are
+ * Positions whose page is out of range are left out; a row that sees none has out
+ * 0 and lse -infinity.  What lies in the cache behind a row's position, or before
+ * its window, does not reach the row, whatever it is.  An infinite element of a value row makes
+ * its column of out infinite or NaN.  bf16: the weights are rounded to bf16 (2^-9 of
+ * themselves, the outputs' own rounding) for the product with the values; their sum and lse are not.
+ * D in {32, 64, 128}, Hq a multiple of Hkv, T * Hq < 2^30, R < 2^20,
+ * max_pages * page_size < 2^30.  Results do not depend on the run.
+ */
+la_status la_paged_prefill(const void* q, const void* K_pages, const void* V_pages, const int* block_table,
+                           const int* cached_lens, const int* seq_starts, void* out, float* lse, int T, int R,
+                           int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages, int window,
+                           float scale, la_dtype dtype, int fill, void* stream);
+
+/*
+ * Rotary positions: pair i of the first `rot` elements of every query and key head,
+ * standing at position p, turns by the angle p theta_i,
+ *   (y0, y1) = magnitude (x0 cos - x1 sin, x0 sin + x1 cos);
+ * LA_ROTARY_HALF pairs elements i and i + rot / 2, LA_ROTARY_INTERLEAVED 2 i and 2 i + 1.
+ * Elements from rot on are copied.
+ *
+ * la_rotary_frequencies (host): the rot / 2 angles a position, as whole numbers of 2^-64
+ * turns, which the calls below read from device memory; with them the phase of any
+ * position is exact.  theta_i = base^(-2 i / rot) (base >= 1), and for contexts `factor`
+ * (>= 1) times longer than trained on
+ *   LA_ROTARY_LINEAR    theta_i / factor
+ *   LA_ROTARY_BASE      base factor^(rot / (rot - 2)) in place of base
+ *   LA_ROTARY_BY_PARTS  theta_i (g + (1 - g) / factor), where g goes from 0 to 1 as the turns
+ *                       of original_len positions, original_len theta_i / 2 pi, go from
+ *                       beta_slow to beta_fast
+ * *magnitude is 0.1 ln(factor) + 1 for the last, else 1.  rot is even, from 2 to 128.
+ *
+ * la_forward_rotary, la_backward_rotary: queries and keys of one call; the backward turns
+ * the upstream gradients by the opposite angles.
+ *   q, k [B][Hq][N][D], [B][Hk][N][D] dtype (read), q_out, k_out (written); with Hk = 0
+ *         the keys may be NULL, with Hq = 0 the queries
+ *   strides  host, nullable: per tensor, in the arguments' order, the distances in elements
+ *         between batch rows, tokens and heads (elements of a head are adjacent); NULL:
+ *         contiguous as above.  Tensors need their element's alignment only; where all
+ *         are 16-byte aligned (so are their strides) and rot is a multiple of 32 bytes, rows
+ *         move in 16-byte pieces
+ *   positions int32, device, [N] for all batch rows (position_rows 1) or [B][N]
+ *         (position_rows B); a negative one marks a row without a token.  NULL
+ *         (position_rows 0): first_position, first_position + 1, ...
+ *   fill  rows without a token get 0 in q_out (1), k_out (2) or both (3); else they are
+ *         left as they are
+ * An output may be its own input (the same address and strides) and may not overlap
+ * another tensor.  B * N < 2^30.
+ */
+typedef enum { LA_ROTARY_HALF = 0, LA_ROTARY_INTERLEAVED = 1 } la_rotary_layout;
+typedef enum { LA_ROTARY_UNSCALED = 0, LA_ROTARY_LINEAR = 1, LA_ROTARY_BASE = 2, LA_ROTARY_BY_PARTS = 3 } la_rotary_scaling;
+
+la_status la_rotary_frequencies(int rot, double base, la_rotary_scaling scaling, double factor, double original_len,
+                                double beta_fast, double beta_slow, uint64_t* freqs, float* magnitude);
+la_status la_forward_rotary(const void* q, const void* k, void* q_out, void* k_out, int B, int N, int Hq, int Hk,
+                            int D, const int64_t* strides, const int* positions, int position_rows,
+                            int first_position, const uint64_t* freqs, int rot, float magnitude,
+                            la_rotary_layout layout, la_dtype dtype, int fill, void* stream);
+la_status la_backward_rotary(const void* dq_out, const void* dk_out, void* dq, void* dk, int B, int N, int Hq, int Hk,
+                             int D, const int64_t* strides, const int* positions, int position_rows,
+                             int first_position, const uint64_t* freqs, int rot, float magnitude,
+                             la_rotary_layout layout, la_dtype dtype, int fill, void* stream);
+
+/*
+ * The same with a norm of every head before the rotation, in one pass:
+ *   n = x / sqrt(mean x^2 + eps) * weight,   y = rotary(n)   (not rounded in between)
+ *   q_weight, k_weight [D] fp32, nullable (1 then), shared by all heads   (read)
+ *   eps > 0
+ * The backward reads the forward's inputs and the upstream gradients, and writes dq, dk and
+ *   dq_weight, dk_weight [D] fp32, nullable   (written) sums over all tokens and heads, in
+ *         fp32 and in an order that does not depend on the run
+ * An output row may be one of its own input rows.  Rows without a token add nothing.
+ */
+la_status la_forward_norm_rotary(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                                 void* q_out, void* k_out, int B, int N, int Hq, int Hk, int D,
+                                 const int64_t* strides, const int* positions, int position_rows,
+                                 int first_position, const uint64_t* freqs, int rot, float magnitude,
+                                 la_rotary_layout layout, float eps, la_dtype dtype, int fill, void* stream);
+la_status la_backward_norm_rotary(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                                  const float* q_weight, const float* k_weight, void* dq, void* dk,
+                                  float* dq_weight, float* dk_weight, int B, int N, int Hq, int Hk, int D,
+                                  const int64_t* strides, const int* positions, int position_rows,
+                                  int first_position, const uint64_t* freqs, int rot, float magnitude,
+                                  la_rotary_layout layout, float eps, la_dtype dtype, int fill, void* stream);
+
+/* Scratch bytes that one la_backward_norm_rotary call with weights' gradients takes from the
+ * library pool (the other rotary calls take none); SIZE_MAX for sizes that the call refuses.
+ * num_sms as in la_workspace_bytes. */
+size_t la_norm_rotary_workspace_bytes(int B, int N, int Hq, int Hk, int D, int num_sms);
+
+/*
  * la_forward_noncausal with no device allocation.  The paper has no
  * counterpart: this is a service for callers that may not allocate device
  * memory inside an op -- a host framework that plans all device memory in

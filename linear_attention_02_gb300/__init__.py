@@ -9,7 +9,8 @@ current CUDA stream; every step of the computation runs in liblinattn.so.
     la_forward_noncausal(Q, K, V, ...)   phi(Q)(phi(K)^T V) / phi(Q) sum phi(K)
     la_decode_step(q, k, v, S, Z, ...)   S += phi(k)v^T, Z += phi(k); read with q
     la_forward_gated_scan(A, X, ...)     h_t = a_t h_{t-1} + x_t per channel; its backward and step
-    la_page_map, la_paged_append, la_paged_decode_step   softmax attention over a paged KV cache
+    la_page_map, la_paged_append, la_paged_decode_step, la_paged_prefill   softmax attention over a paged KV cache
+    la_forward_rotary(q, k, freqs, ...)  rotary positions; la_forward_norm_rotary with a norm of every head; their backward
 
 Shapes: Q, K [B,H,N,D]; V [B,H,N,M]; S [B,H,D,M] fp32; Z [B,H,D] fp32.
 """
@@ -665,6 +666,214 @@ def la_paged_decode_step(q, k, v, K_pages, V_pages, block_table, cached_lens, wi
             V_pages.data_ptr(), block_table.data_ptr(), cached_lens.data_ptr(), out.data_ptr(), _ptr(lse), R,
             Hq, Hkv, D, P, page, block_table.shape[1], _int(window, "window"), float(scale), _dtype(K_pages), fill)
     return (out, lse) if return_lse else out
+
+
+def la_paged_prefill(q, K_pages, V_pages, block_table, cached_lens, seq_starts, window=0, scale=None,
+                     out=None, return_lse=False, stream=None, lse=None):
+    """Softmax attention of each request's new tokens over a paged KV cache that holds them.
+
+    Rows seq_starts[r] .. seq_starts[r+1] - 1 of q [T,Hq,D] are request r's new tokens, at positions
+    cached_lens[r] and on; their keys and values are in the pages already (la_paged_append).  Returns
+    out [T,Hq,D] in q's dtype: each row attends the last `window` positions up to its own (0: all), with
+    return_lse also the log of the sum [T,Hq] fp32 (in `lse` if given).  Rows of no request (behind
+    the last one, or of one with a negative length) are left as they are in an out or lse given to the
+    call; in one that it allocates they are 0 and -infinity.  scale None: 1 / sqrt(D)."""
+    P, Hkv, page, D, dev = _pools(K_pages, V_pages)
+    dt = K_pages.dtype
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    T, Hq = q.shape[:2]
+    _shaped(q, "q", (T, Hq, D), dt, dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [R, max_pages]")
+    R, W = block_table.shape
+    _shaped(block_table, "block_table", (R, W), torch.int32, dev)
+    if block_table.numel() > _INT_MAX or q.numel() > _INT_MAX:
+        _fits(block_table, q)
+    _shaped(cached_lens, "cached_lens", (R,), torch.int32, dev)
+    _shaped(seq_starts, "seq_starts", (R + 1,), torch.int32, dev)
+    if scale is None:
+        scale = 0.0
+    elif ctypes.c_float(float(scale)).value == 0.0:  # the C call's 0 means the default
+        raise ValueError("scale must not be 0 in fp32")
+    fill = 0
+    if out is None:
+        out = torch.empty_like(q)
+        fill = 1
+    else:
+        _shaped(out, "out", (T, Hq, D), dt, dev)
+    if lse is not None:
+        _shaped(lse, "lse", (T, Hq), torch.float32, dev)
+    elif return_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        fill |= 2
+    _launch(_lib.la_paged_prefill, dev, stream, q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(),
+            block_table.data_ptr(), cached_lens.data_ptr(), seq_starts.data_ptr(), out.data_ptr(), _ptr(lse), T, R,
+            Hq, Hkv, D, P, page, W, _int(window, "window"), float(scale), _dtype(K_pages), fill)
+    return (out, lse) if return_lse else out
+
+
+_LAYOUTS = {"half": _native.LA_ROTARY_HALF, "interleaved": _native.LA_ROTARY_INTERLEAVED}
+_SCALINGS = {"none": _native.LA_ROTARY_UNSCALED, "linear": _native.LA_ROTARY_LINEAR,
+             "base": _native.LA_ROTARY_BASE, "by_parts": _native.LA_ROTARY_BY_PARTS}
+
+
+def la_rotary_frequencies(rot, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0,
+                          beta_slow=1.0, device=None):
+    """(freqs, magnitude) of a rotation of `rot` elements: an int64 tensor [rot/2] on `device` of angles a
+    position, in 2^-64 turns, and the factor on the rotated elements (1 but for "by_parts").
+
+    scaling, for contexts `factor` times longer: "linear" (positions divided), "base" (a larger base) or
+    "by_parts" (slow pairs divided, fast ones kept, by their turns over original_len positions)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}, got {scaling!r}")
+    rot = _int(rot, "rot")
+    buf, mag = (ctypes.c_uint64 * max(1, rot // 2 if rot <= 128 else 1))(), ctypes.c_float()
+    _check(_lib.la_rotary_frequencies(rot, float(base), _SCALINGS[scaling], float(factor), float(original_len),
+                                      float(beta_fast), float(beta_slow), buf, ctypes.byref(mag)))
+    freqs = torch.tensor([x - (1 << 64) if x >> 63 else x for x in buf], dtype=torch.int64)
+    return freqs.to("cuda" if device is None else device), mag.value
+
+
+def _rows(t, name, shape, dt, dev, out=False):
+    """Strides (batch row, token, head) of rows [B,H,N,D] or [N,H,D] with adjacent elements, checked."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dt and t.shape == shape and t.get_device() == dev and dev >= 0):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != dt:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dt}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    s = t.stride()
+    if s[-1] != 1 and t.numel():
+        raise ValueError(f"{name} must have adjacent elements (last stride 1), has strides {s}")
+    if out and t.numel() and not t.is_contiguous():
+        # written rows lie apart: each dimension steps over all that lies within its smaller strides
+        span = 1
+        for st, n in sorted((st, n) for st, n in zip(s, t.shape) if n > 1):
+            if st < span:
+                raise ValueError(f"{name} has rows that overlap (strides {s})")
+            span = st * (n - 1) + span
+    return (s[0], s[2], s[1]) if len(s) == 4 else (0, s[0], s[1])
+
+
+def _rotary_sizes(q, k, names):
+    """(lead, B, N, Hq, Hk, D, packed, device): either of q and k may be None."""
+    lead = q if q is not None else k
+    if not isinstance(lead, torch.Tensor) or lead.dim() not in (3, 4):
+        raise ValueError(f"{names[0]} and {names[1]} must be [B,H,N,D] or [N,H,D]")
+    dev, packed = lead.get_device(), lead.dim() == 3
+    B, N, D = (1, lead.shape[0], lead.shape[2]) if packed else (lead.shape[0], lead.shape[2], lead.shape[3])
+    if lead.numel() > _INT_MAX:
+        _fits(lead)
+    heads = []
+    for t, n in ((q, names[0]), (k, names[1])):
+        if t is None:
+            heads.append(0)
+            continue
+        if not isinstance(t, torch.Tensor) or t.dim() != lead.dim():
+            raise ValueError(f"{n} must be a tensor of {lead.dim()} dimensions")
+        heads.append(t.shape[1])
+    return lead, B, N, heads[0], heads[1], D, packed, dev
+
+
+def _rotary_call(fn, ins, names, outs, out_names, weights, grads, freqs, positions, first, layout, magnitude, eps,
+                 stream):
+    """Marshals a call of the rotary family; returns its outputs."""
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+    lead, B, N, Hq, Hk, D, packed, dev = _rotary_sizes(ins[0], ins[1], names)
+    dt, device = lead.dtype, lead.device
+    shapes = [(N, h, D) if packed else (B, h, N, D) for h in (Hq, Hk)]
+    strides, outs, fill = [], list(outs), 0
+    for i, t in enumerate(ins):
+        if ins[i % 2] is None:
+            if t is not None:
+                raise ValueError(f"{names[i]} is given without {names[i % 2]}")
+            strides += (0, 0, 0)
+        else:
+            strides += _rows(t, names[i], shapes[i % 2], dt, dev)
+    for i in (0, 1):
+        if ins[i] is None:
+            if outs[i] is not None:
+                raise ValueError(f"{out_names[i]} is given without {names[i]}")
+            strides += (0, 0, 0)
+            continue
+        if outs[i] is None:
+            outs[i] = torch.empty(shapes[i], dtype=dt, device=device)
+            fill |= 1 << i
+        strides += _rows(outs[i], out_names[i], shapes[i], dt, dev, out=True)
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        raise ValueError("freqs must be la_rotary_frequencies' tensor [rot/2]")
+    _shaped(freqs, "freqs", freqs.shape, torch.int64, dev)
+    prow = 0
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
+            raise ValueError("positions must be [N] or [B,N]")
+        _shaped(positions, "positions", (N,) if positions.dim() == 1 else (B, N), torch.int32, dev)
+        prow = 1 if positions.dim() == 1 else B
+    for t, n in zip(weights, ("q_weight", "k_weight")):
+        if t is not None:
+            _shaped(t, n, (D,), torch.float32, dev)
+    buf = (ctypes.c_int64 * len(strides))(*strides)
+    args = [_ptr(t) for t in ins]
+    args += [_ptr(t) for t in weights] + [_ptr(t) for t in outs] + [_ptr(t) for t in grads]
+    args += [B, N, Hq, Hk, D, buf, _ptr(positions), prow, _int(first, "first_position"), freqs.data_ptr(),
+             2 * freqs.shape[0], float(magnitude), _LAYOUTS[layout]]
+    if eps is not None:
+        args.append(float(eps))
+    _launch(fn, dev, stream, *args, _dtype(lead), fill)
+    return outs
+
+
+def la_forward_rotary(q, k, freqs, positions=None, first_position=0, layout="half", magnitude=1.0, q_out=None,
+                      k_out=None, stream=None):
+    """Rotary positions of queries and keys [B,H,N,D], or packed [N,H,D], of any strides with adjacent
+    elements; returns (q_out, k_out).  k (or q) may be None.
+
+    freqs, magnitude: la_rotary_frequencies'.  positions: int32 [N] or [B,N], a negative one for a row
+    without a token (0 in outputs that the call allocates, else left as it is); None: first_position,
+    first_position + 1, ...  An output may be its own input."""
+    return tuple(_rotary_call(_lib.la_forward_rotary, (q, k), ("q", "k"), (q_out, k_out), ("q_out", "k_out"), (), (),
+                              freqs, positions, first_position, layout, magnitude, None, stream))
+
+
+def la_backward_rotary(dq_out, dk_out, freqs, positions=None, first_position=0, layout="half", magnitude=1.0,
+                       dq=None, dk=None, stream=None):
+    """Backward of la_forward_rotary from the gradients at its outputs; returns (dq, dk)."""
+    return tuple(_rotary_call(_lib.la_backward_rotary, (dq_out, dk_out), ("dq_out", "dk_out"), (dq, dk), ("dq", "dk"),
+                              (), (), freqs, positions, first_position, layout, magnitude, None, stream))
+
+
+def la_forward_norm_rotary(q, k, q_weight, k_weight, freqs, positions=None, first_position=0, layout="half",
+                           magnitude=1.0, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """la_forward_rotary of x / sqrt(mean x^2 + eps) * weight, the norm of every head, in one pass.
+
+    q_weight, k_weight: fp32 [D], shared by the heads, or None for 1."""
+    return tuple(_rotary_call(_lib.la_forward_norm_rotary, (q, k), ("q", "k"), (q_out, k_out), ("q_out", "k_out"),
+                              (q_weight, k_weight), (), freqs, positions, first_position, layout, magnitude, eps,
+                              stream))
+
+
+def la_backward_norm_rotary(q, k, dq_out, dk_out, q_weight, k_weight, freqs, positions=None, first_position=0,
+                            layout="half", magnitude=1.0, eps=1e-6, dq=None, dk=None, stream=None):
+    """Backward of la_forward_norm_rotary from its inputs and the gradients at its outputs; returns
+    (dq, dk, dq_weight, dk_weight), the last two fp32 [D] (None where q or k is)."""
+    grads = tuple(None if t is None or not isinstance(t, torch.Tensor) or not t.is_cuda else
+                  torch.empty(t.shape[-1], dtype=torch.float32, device=t.device) for t in (q, k))
+    dq, dk = _rotary_call(_lib.la_backward_norm_rotary, (q, k, dq_out, dk_out), ("q", "k", "dq_out", "dk_out"),
+                          (dq, dk), ("dq", "dk"), (q_weight, k_weight), grads, freqs, positions, first_position,
+                          layout, magnitude, eps, stream)
+    return dq, dk, grads[0], grads[1]
+
+
+def la_norm_rotary_workspace_bytes(B, N, Hq, Hk, D, num_sms=0):
+    """Scratch bytes of one la_backward_norm_rotary call; num_sms <= 0 asks the current device."""
+    sizes = [_int(x, n) for x, n in ((B, "B"), (N, "N"), (Hq, "Hq"), (Hk, "Hk"), (D, "D"))]
+    return _bytes(_lib.la_norm_rotary_workspace_bytes(*sizes, num_sms))
 
 
 def la_check_device_status(stream=None):

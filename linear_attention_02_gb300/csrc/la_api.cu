@@ -943,6 +943,268 @@ la_status la_paged_decode_step_padded(const void* q, const void* k, const void* 
                       page_size, max_pages, window, scale, dtype, fill, stream);
 }
 
+// A call of the rotary family: its tensors in the order of RotaryShape, checked.
+static la_status rotary_shape(const char* fn, RotaryShape* sh, const void* const* ptrs, const char* const* names,
+                              int tensors, int B, int N, int Hq, int Hk, int D, const int64_t* strides,
+                              const int* positions, int position_rows, int first_position, const uint64_t* freqs,
+                              int rot, float magnitude, la_rotary_layout layout, la_dtype dtype, int fill, bool* empty) {
+    if (B < 0 || N < 0 || Hq < 0 || Hk < 0)
+        return fail(LA_ERR_INVALID_ARG, "%s: negative size B=%d N=%d Hq=%d Hk=%d", fn, B, N, Hq, Hk);
+    if (dtype != LA_DTYPE_F32 && dtype != LA_DTYPE_BF16)
+        return fail(LA_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dtype);
+    if (!head_ok(D))
+        return fail(LA_ERR_UNSUPPORTED, "%s: D=%d, supported head sizes are 32, 64, 128", fn, D);
+    if (layout != LA_ROTARY_HALF && layout != LA_ROTARY_INTERLEAVED)
+        return fail(LA_ERR_UNSUPPORTED, "%s: unknown layout %d", fn, (int)layout);
+    if (rot < 2 || rot > D || rot % 2)
+        return fail(LA_ERR_INVALID_ARG, "%s: rot=%d must be even, from 2 to D=%d", fn, rot, D);
+    if (!std::isfinite(magnitude)) return fail(LA_ERR_INVALID_ARG, "%s: magnitude=%g is not finite", fn, magnitude);
+    if (positions ? position_rows != 1 && position_rows != B : position_rows != 0)
+        return fail(LA_ERR_INVALID_ARG, "%s: position_rows=%d with %s must be %s", fn, position_rows,
+                    positions ? "positions" : "no positions", positions ? "1 or B" : "0");
+    if (positions ? first_position != 0 : first_position < 0 || (long long)first_position + N > INT_MAX)
+        return fail(LA_ERR_INVALID_ARG, "%s: first_position=%d: given beside positions, negative, or past 2^31 with N=%d",
+                    fn, first_position, N);
+    if (la_status s = check_fill(fn, fill, 3)) return s;
+    // tiles of tokens are counted in 32 bits
+    const unsigned long long tokens = (unsigned long long)B * N;
+    if (tokens >= (1ull << 30) || (unsigned long long)Hq * D >= (1ull << 30) || (unsigned long long)Hk * D >= (1ull << 30) ||
+        tokens * ((unsigned long long)Hq + Hk) * D >= (1ull << 40))
+        return fail(LA_ERR_INVALID_ARG, "%s: tensor too large", fn);
+    *empty = tokens == 0 || Hq + Hk == 0;
+    RotaryShape& r = *sh;
+    r = {};
+    r.B = B, r.N = N, r.Hq = Hq, r.Hk = Hk, r.D = D, r.rot = rot;
+    r.interleaved = layout == LA_ROTARY_INTERLEAVED;
+    r.freqs = freqs, r.positions = positions, r.pos_batch = position_rows > 1 ? N : 0, r.first = first_position;
+    r.mag = magnitude, r.fill = fill, r.tensors = tensors;
+    if (*empty) return LA_OK;
+    const size_t es = elem_bytes(dtype);
+    for (int i = 0; i < tensors; ++i) {
+        const int H = i % 2 ? Hk : Hq;
+        if (H == 0) continue;
+        if (!ptrs[i]) return fail(LA_ERR_INVALID_ARG, "%s: %s is NULL", fn, names[i]);
+        if (reinterpret_cast<uintptr_t>(ptrs[i]) % es)
+            return fail(LA_ERR_INVALID_ARG, "%s: %s is not %zu-byte aligned", fn, names[i], es);
+        r.ptr[i] = ptrs[i];
+        const int64_t dense[3] = {(int64_t)H * N * D, D, (int64_t)N * D};  // [B][H][N][D]
+        const int sizes[3] = {B, N, H};
+        for (int d = 0; d < 3; ++d) {
+            const int64_t x = strides ? strides[3 * i + d] : dense[d];
+            if (x >= (1ll << 40) || x <= -(1ll << 40))
+                return fail(LA_ERR_INVALID_ARG, "%s: %s has stride %lld", fn, names[i], (long long)x);
+            r.strides[i][d] = sizes[d] > 1 ? x : 0;  // the stride of a single row is no one's
+        }
+    }
+    const void* p[] = {freqs};
+    const char* nm[] = {"freqs"};
+    if (la_status s = check_ptrs(fn, p, nm, 1, 8)) return s;
+    if (reinterpret_cast<uintptr_t>(positions) & 3u)
+        return fail(LA_ERR_INVALID_ARG, "%s: positions is not 4-byte aligned", fn);
+    return LA_OK;
+}
+
+static la_status norm_args(const char* fn, RotaryShape* sh, const float* q_weight, const float* k_weight, float eps) {
+    if (!(eps > 0.f) || !std::isfinite(eps)) return fail(LA_ERR_INVALID_ARG, "%s: eps=%g must be positive and finite", fn, eps);
+    if ((reinterpret_cast<uintptr_t>(q_weight) | reinterpret_cast<uintptr_t>(k_weight)) & 3u)
+        return fail(LA_ERR_INVALID_ARG, "%s: q_weight or k_weight is not 4-byte aligned", fn);
+    sh->w[0] = q_weight, sh->w[1] = k_weight, sh->eps = eps;
+    return LA_OK;
+}
+
+static la_status run_rotary(const char* fn, const RotaryShape& sh, la_dtype dtype, bool norm, void* stream) {
+    LaunchCtx ctx;
+    if (la_status s = get_ctx((cudaStream_t)stream, &ctx)) return s;
+    return finish(rotary(ctx, sh, dtype == LA_DTYPE_BF16, norm), fn);
+}
+
+la_status la_rotary_frequencies(int rot, double base, la_rotary_scaling scaling, double factor, double original_len,
+                                double beta_fast, double beta_slow, uint64_t* freqs, float* magnitude) {
+    static const char* fn = "la_rotary_frequencies";
+    if (rot < 2 || rot % 2 || rot > 128) return fail(LA_ERR_INVALID_ARG, "%s: rot=%d must be even, from 2 to 128", fn, rot);
+    if (!std::isfinite(base) || !(base >= 1.0)) return fail(LA_ERR_INVALID_ARG, "%s: base=%g must be at least 1", fn, base);
+    if (scaling < LA_ROTARY_UNSCALED || scaling > LA_ROTARY_BY_PARTS)
+        return fail(LA_ERR_UNSUPPORTED, "%s: unknown scaling %d", fn, (int)scaling);
+    if (scaling != LA_ROTARY_UNSCALED && (!std::isfinite(factor) || !(factor >= 1.0)))
+        return fail(LA_ERR_INVALID_ARG, "%s: factor=%g must be at least 1", fn, factor);
+    if (scaling == LA_ROTARY_BY_PARTS &&
+        !(std::isfinite(original_len) && original_len > 0 && std::isfinite(beta_fast) && std::isfinite(beta_slow) &&
+          beta_fast > beta_slow))
+        return fail(LA_ERR_INVALID_ARG, "%s: original_len=%g must be positive and beta_fast=%g above beta_slow=%g", fn,
+                    original_len, beta_fast, beta_slow);
+    if (!freqs || !magnitude) return fail(LA_ERR_INVALID_ARG, "%s: freqs or magnitude is NULL", fn);
+    const double two_pi = 6.283185307179586;
+    const double to_turns = 0.15915494309189535, to_turns_rest = -9.839338337591243e-18;  // 1 / 2 pi in two terms
+    if (scaling == LA_ROTARY_BASE && rot > 2) base *= std::pow(factor, (double)rot / (rot - 2));
+    if (!std::isfinite(base)) return fail(LA_ERR_INVALID_ARG, "%s: factor=%g makes the base infinite", fn, factor);
+    for (int i = 0; i < rot / 2; ++i) {
+        double theta = std::pow(base, -2.0 * i / rot);
+        if (scaling == LA_ROTARY_LINEAR) theta /= factor;
+        if (scaling == LA_ROTARY_BY_PARTS) {
+            const double turns = original_len * theta / two_pi;
+            const double keep = std::fmin(1.0, std::fmax(0.0, (turns - beta_slow) / (beta_fast - beta_slow)));
+            theta = theta / factor * (1.0 - keep) + theta * keep;
+        }
+        // theta <= 1, so below a turn; the product's rounding goes into the second term
+        const double hi = theta * to_turns, lo = std::fma(theta, to_turns, -hi) + theta * to_turns_rest;
+        freqs[i] = (uint64_t)std::ldexp(hi, 64) + (uint64_t)(int64_t)std::llrint(std::ldexp(lo, 64));
+    }
+    *magnitude = scaling == LA_ROTARY_BY_PARTS ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+    return LA_OK;
+}
+
+la_status la_forward_rotary(const void* q, const void* k, void* q_out, void* k_out, int B, int N, int Hq, int Hk,
+                            int D, const int64_t* strides, const int* positions, int position_rows,
+                            int first_position, const uint64_t* freqs, int rot, float magnitude,
+                            la_rotary_layout layout, la_dtype dtype, int fill, void* stream) {
+    static const char* fn = "la_forward_rotary";
+    const void* p[] = {q, k, q_out, k_out};
+    const char* nm[] = {"q", "k", "q_out", "k_out"};
+    RotaryShape sh;
+    bool empty;
+    la_status s = rotary_shape(fn, &sh, p, nm, 4, B, N, Hq, Hk, D, strides, positions, position_rows, first_position,
+                               freqs, rot, magnitude, layout, dtype, fill, &empty);
+    return s != LA_OK || empty ? s : run_rotary(fn, sh, dtype, false, stream);
+}
+
+la_status la_backward_rotary(const void* dq_out, const void* dk_out, void* dq, void* dk, int B, int N, int Hq, int Hk,
+                             int D, const int64_t* strides, const int* positions, int position_rows,
+                             int first_position, const uint64_t* freqs, int rot, float magnitude,
+                             la_rotary_layout layout, la_dtype dtype, int fill, void* stream) {
+    static const char* fn = "la_backward_rotary";
+    const void* p[] = {dq_out, dk_out, dq, dk};
+    const char* nm[] = {"dq_out", "dk_out", "dq", "dk"};
+    RotaryShape sh;
+    bool empty;
+    la_status s = rotary_shape(fn, &sh, p, nm, 4, B, N, Hq, Hk, D, strides, positions, position_rows, first_position,
+                               freqs, rot, magnitude, layout, dtype, fill, &empty);
+    sh.backward = true;
+    return s != LA_OK || empty ? s : run_rotary(fn, sh, dtype, false, stream);
+}
+
+la_status la_forward_norm_rotary(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                                 void* q_out, void* k_out, int B, int N, int Hq, int Hk, int D, const int64_t* strides,
+                                 const int* positions, int position_rows, int first_position, const uint64_t* freqs,
+                                 int rot, float magnitude, la_rotary_layout layout, float eps, la_dtype dtype,
+                                 int fill, void* stream) {
+    static const char* fn = "la_forward_norm_rotary";
+    const void* p[] = {q, k, q_out, k_out};
+    const char* nm[] = {"q", "k", "q_out", "k_out"};
+    RotaryShape sh;
+    bool empty;
+    la_status s = rotary_shape(fn, &sh, p, nm, 4, B, N, Hq, Hk, D, strides, positions, position_rows, first_position,
+                               freqs, rot, magnitude, layout, dtype, fill, &empty);
+    if (s != LA_OK || (s = norm_args(fn, &sh, q_weight, k_weight, eps)) != LA_OK || empty) return s;
+    return run_rotary(fn, sh, dtype, true, stream);
+}
+
+la_status la_backward_norm_rotary(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                                  const float* q_weight, const float* k_weight, void* dq, void* dk, float* dq_weight,
+                                  float* dk_weight, int B, int N, int Hq, int Hk, int D, const int64_t* strides,
+                                  const int* positions, int position_rows, int first_position, const uint64_t* freqs,
+                                  int rot, float magnitude, la_rotary_layout layout, float eps, la_dtype dtype,
+                                  int fill, void* stream) {
+    static const char* fn = "la_backward_norm_rotary";
+    const void* p[] = {q, k, dq_out, dk_out, dq, dk};
+    const char* nm[] = {"q", "k", "dq_out", "dk_out", "dq", "dk"};
+    RotaryShape sh;
+    bool empty;
+    la_status s = rotary_shape(fn, &sh, p, nm, 6, B, N, Hq, Hk, D, strides, positions, position_rows, first_position,
+                               freqs, rot, magnitude, layout, dtype, fill, &empty);
+    if (s != LA_OK || (s = norm_args(fn, &sh, q_weight, k_weight, eps)) != LA_OK) return s;
+    if ((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u)
+        return fail(LA_ERR_INVALID_ARG, "%s: dq_weight or dk_weight is not 4-byte aligned", fn);
+    if (empty && !dq_weight && !dk_weight) return LA_OK;
+    LaunchCtx ctx;
+    if ((s = get_ctx((cudaStream_t)stream, &ctx)) != LA_OK) return s;
+    if (empty) {  // sums over no rows
+        cudaError_t e = dq_weight ? cudaMemsetAsync(dq_weight, 0, sizeof(float) * D, ctx.stream) : cudaSuccess;
+        if (e == cudaSuccess && dk_weight) e = cudaMemsetAsync(dk_weight, 0, sizeof(float) * D, ctx.stream);
+        return finish(e, fn);
+    }
+    sh.backward = true;
+    return finish(norm_rotary_grad(ctx, sh, dtype == LA_DTYPE_BF16, dq_weight, dk_weight), fn);
+}
+
+size_t la_norm_rotary_workspace_bytes(int B, int N, int Hq, int Hk, int D, int num_sms) {
+    static const char* fn = "la_norm_rotary_workspace_bytes";
+    if (!head_ok(D))
+        return fail(LA_ERR_UNSUPPORTED, "%s: D=%d, supported head sizes are 32, 64, 128", fn, D), SIZE_MAX;
+    if (B < 0 || N < 0 || Hq < 0 || Hk < 0 || (unsigned long long)B * N >= (1ull << 30) ||
+        (unsigned long long)Hq * D >= (1ull << 30) || (unsigned long long)Hk * D >= (1ull << 30) ||
+        (unsigned long long)B * N * ((unsigned long long)Hq + Hk) * D >= (1ull << 40))
+        return fail(LA_ERR_INVALID_ARG, "%s: sizes B=%d N=%d Hq=%d Hk=%d", fn, B, N, Hq, Hk), SIZE_MAX;
+    if (num_sms <= 0) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return cuda_fail(e, fn), SIZE_MAX;
+    }
+    return rotary_grad_scratch(B, N, Hq, Hk, D, true, num_sms);
+}
+
+// Sizes of a prefill call.
+static la_status check_prefill(const char* fn, int T, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
+                               int max_pages, int window, la_dtype dtype, int* log2p) {
+    la_status s = check_pages(fn, num_pages, page_size, log2p);
+    if (s != LA_OK) return s;
+    if (T < 0 || R < 0 || Hq < 0 || Hkv < 0 || max_pages < 0 || window < 0)
+        return fail(LA_ERR_INVALID_ARG, "%s: negative size T=%d R=%d Hq=%d Hkv=%d max_pages=%d window=%d", fn, T, R, Hq,
+                    Hkv, max_pages, window);
+    if (dtype != LA_DTYPE_F32 && dtype != LA_DTYPE_BF16)
+        return fail(LA_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dtype);
+    if (!head_ok(D))
+        return fail(LA_ERR_UNSUPPORTED, "%s: D=%d, supported head sizes are 32, 64, 128", fn, D);
+    if (Hq && (Hkv == 0 || Hq % Hkv))
+        return fail(LA_ERR_INVALID_ARG, "%s: Hq=%d query heads over Hkv=%d key heads: not a multiple", fn, Hq, Hkv);
+    if ((unsigned long long)max_pages * page_size >= (1ull << 30))
+        return fail(LA_ERR_INVALID_ARG, "%s: max_pages=%d of %d positions: 2^30 positions or more", fn, max_pages, page_size);
+    if (R >= (1 << 20)) return fail(LA_ERR_INVALID_ARG, "%s: R=%d: 2^20 requests or more", fn, R);
+    // rows of a request and head are counted in 32 bits
+    if (T >= (1 << 30) || (unsigned long long)T * Hq >= (1ull << 30) || Hkv >= (1 << 16) ||
+        (unsigned long long)num_pages * page_size * (Hkv ? Hkv : 1) >= (1ull << 40) / D)
+        return fail(LA_ERR_INVALID_ARG, "%s: tensor too large", fn);
+    return LA_OK;
+}
+
+la_status la_paged_prefill(const void* q, const void* K_pages, const void* V_pages, const int* block_table,
+                           const int* cached_lens, const int* seq_starts, void* out, float* lse, int T, int R, int Hq,
+                           int Hkv, int D, int num_pages, int page_size, int max_pages, int window, float scale,
+                           la_dtype dtype, int fill, void* stream) {
+    static const char* fn = "la_paged_prefill";
+    int log2p = 0;
+    la_status s = check_prefill(fn, T, R, Hq, Hkv, D, num_pages, page_size, max_pages, window, dtype, &log2p);
+    if (s != LA_OK || (s = check_fill(fn, fill, 3)) != LA_OK) return s;
+    if (!std::isfinite(scale * 1.4426950408889634f))  // scores are taken to base 2
+        return fail(LA_ERR_INVALID_ARG, "%s: scale=%g, or its product with log2 e, is not finite", fn, scale);
+    if (T == 0 || Hq == 0 || (R == 0 && !fill)) return LA_OK;
+    const void* p[] = {q, out, K_pages, V_pages};
+    const char* nm[] = {"q", "out", "K_pages", "V_pages"};
+    if ((s = check_ptrs(fn, p, nm, num_pages ? 4 : 2, 16)) != LA_OK) return s;
+    const void* ip[] = {cached_lens, seq_starts, block_table};
+    const char* in[] = {"cached_lens", "seq_starts", "block_table"};
+    if (R && (s = check_ptrs(fn, ip, in, max_pages ? 3 : 2, 4)) != LA_OK) return s;
+    if ((fill & 2) && !lse) return fail(LA_ERR_INVALID_ARG, "%s: lse is NULL", fn);
+    if (reinterpret_cast<uintptr_t>(lse) & 3u)
+        return fail(LA_ERR_INVALID_ARG, "%s: lse is not 4-byte aligned", fn);
+    LaunchCtx ctx;
+    if ((s = get_ctx((cudaStream_t)stream, &ctx)) != LA_OK) return s;
+    const PrefillShape sh = {T, R, Hq, Hkv, num_pages, log2p, max_pages, window,
+                             scale == 0.f ? 1.f / sqrtf((float)D) : scale};
+    cudaError_t e = cudaErrorInvalidValue;
+#define LA_PP_CASE(Ty, d)                                                                               \
+    if (D == d)                                                                                         \
+        e = paged_prefill<Ty, d>(ctx, (const Ty*)q, (const Ty*)K_pages, (const Ty*)V_pages, block_table, \
+                                 cached_lens, seq_starts, (Ty*)out, lse, sh, fill);
+    if (dtype == LA_DTYPE_F32) {
+        LA_PP_CASE(float, 32) else LA_PP_CASE(float, 64) else LA_PP_CASE(float, 128)
+    } else {
+        LA_PP_CASE(__nv_bfloat16, 32) else LA_PP_CASE(__nv_bfloat16, 64) else LA_PP_CASE(__nv_bfloat16, 128)
+    }
+#undef LA_PP_CASE
+    return finish(e, fn);
+}
+
 la_status la_selftest_expired_waits(void* stream) {
     LaunchCtx ctx;
     la_status s = get_ctx((cudaStream_t)stream, &ctx);

@@ -198,6 +198,41 @@ cudaError_t paged_decode_step(const LaunchCtx& c, const T* q, const T* k, const 
                               const int* table, const int* lens, float* out, float* lse,
                               const PagedShape& s, int fill);
 
+// Attention of each request's rows [starts[r], starts[r + 1]) of T over its pages, whose last
+// positions are the rows' own.
+struct PrefillShape {
+    int T, R, Hq, Hkv, num_pages, log2p, max_pages, window;
+    float scale;
+};
+template <typename T, int D>
+cudaError_t paged_prefill(const LaunchCtx& c, const T* q, const T* K, const T* V, const int* table,
+                          const int* lens, const int* starts, T* out, float* lse,
+                          const PrefillShape& s, int fill);
+
+// Rotary positions of queries (0) and keys (1): ptr and strides (batch row, token, head, in
+// elements) are the inputs' q, k, with a norm's gradient the upstream gradients' next, and
+// last the outputs'.  positions null: first, first + 1, ...; a negative one marks a row
+// without a token, which gets 0 in the outputs whose bit is in `fill`.
+struct RotaryShape {
+    int B, N, Hq, Hk, D, rot;
+    bool interleaved, backward;
+    const uint64_t* freqs;
+    const int* positions;
+    int64_t pos_batch;
+    int first;
+    float mag, eps;
+    int tensors;
+    const void* ptr[6];
+    int64_t strides[6][3];
+    const float* w[2];
+    int fill;
+};
+cudaError_t rotary(const LaunchCtx& c, const RotaryShape& s, bool bf16, bool norm);
+cudaError_t norm_rotary_grad(const LaunchCtx& c, const RotaryShape& s, bool bf16, float* dwq, float* dwk);
+// Blocks that sum up the weights' gradients on each side at most, and a call's scratch bytes.
+int rotary_grad_blocks(int num_sms);
+size_t rotary_grad_scratch(int B, int N, int Hq, int Hk, int D, bool weights, int num_sms);
+
 template <typename T, int D, int M>
 cudaError_t decode_step(const LaunchCtx& c, const T* q, const T* k, const T* v, float* S,
                         float* Z, float* out, int BH);

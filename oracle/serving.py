@@ -1,4 +1,4 @@
-"""fp64 plain forms of the gated scan and of the paged key-value cache.
+"""fp64 plain forms of the gated scan, of the paged key-value cache and of the rotary positions.
 
 Written from the definitions, one row, position or request at a time, on numpy
 arrays; used by the tests only.  Packed sequences are given by `starts`
@@ -141,3 +141,85 @@ def paged_decode(q, k, v, K, V, table, lens, window=0, scale=None):
             out[r, h] = w @ np.array(vs) / w.sum()
             lse[r, h] = m + np.log(w.sum())
     return out, lse
+
+
+def paged_prefill(q, K, V, table, lens, starts, window=0, scale=None):
+    """(out, lse, size): size is the weighted mean of |v| of every output; rows of no request are NaN.
+    Positions on a page outside the pool are left out."""
+    q, K, V = _f64(q), _f64(K), _f64(V)
+    T, Hq, D = q.shape
+    P, Hkv, page, _ = K.shape
+    scale = 1 / np.sqrt(D) if scale is None else scale
+    out, size, lse = np.full((T, Hq, D), np.nan), np.full((T, Hq, D), np.nan), np.full((T, Hq), np.nan)
+    for r in range(len(lens)):
+        if int(lens[r]) < 0:
+            continue
+        a, b = int(starts[r]), int(starts[r + 1])
+        for t in range(a, b):
+            pos = int(lens[r]) + t - a
+            first = max(0, pos - window + 1) if window else 0
+            at = [(int(table[r][p // page]), p % page) for p in range(first, min(pos + 1, len(table[r]) * page))]
+            at = [(i, o) for i, o in at if 0 <= i < P]
+            if not at:
+                out[t], size[t], lse[t] = 0, 0, -np.inf
+                continue
+            i, o = np.array(at).T
+            k, v = K[i, :, o], V[i, :, o]  # [positions, Hkv, D]
+            for h in range(Hq):
+                g = h // (Hq // Hkv)
+                x = scale * (k[:, g] @ q[t, h])
+                m = x.max()
+                w = np.exp(x - m)
+                out[t, h], size[t, h] = w @ v[:, g] / w.sum(), w @ np.abs(v[:, g]) / w.sum()
+                lse[t, h] = m + np.log(w.sum())
+    return out, lse, size
+
+
+def rotary_theta(rot, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0, beta_slow=1.0):
+    """(angles a position [rot / 2], magnitude)."""
+    i = np.arange(rot // 2)
+    if scaling == "base" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    theta = np.array([float(base) ** (-2.0 * j / rot) for j in i])
+    if scaling == "linear":
+        theta = theta / factor
+    if scaling == "by_parts":
+        g = np.clip((original_len * theta / (2 * np.pi) - beta_slow) / (beta_fast - beta_slow), 0, 1)
+        theta = theta * (g + (1 - g) / factor)
+    return theta, 1 + 0.1 * np.log(factor) if scaling == "by_parts" else 1.0
+
+
+def rotary_angles(freqs, positions):
+    """Angles [.., rot / 2] of whole-number positions, from frequencies in 2^-64 turns: whole numbers, so exact
+    until the last step."""
+    f = [int(x) % (1 << 64) for x in freqs]
+    pos = np.asarray(positions)
+    a = [[2 * np.pi * ((int(p) * u % (1 << 64)) / 2.0 ** 64) for u in f] for p in pos.reshape(-1)]
+    return np.array(a).reshape(*pos.shape, len(f))
+
+
+def rotary(x, angles, layout="half", magnitude=1.0):
+    """Rows [.., D] turned by angles [.., rot / 2] that broadcast against them."""
+    x = _f64(x)
+    n = angles.shape[-1]
+    a, b = (slice(0, n), slice(n, 2 * n)) if layout == "half" else (slice(0, 2 * n, 2), slice(1, 2 * n, 2))
+    y = x.copy()
+    c, s = magnitude * np.cos(angles), magnitude * np.sin(angles)
+    y[..., a] = x[..., a] * c - x[..., b] * s
+    y[..., b] = x[..., a] * s + x[..., b] * c
+    return y
+
+
+def norm_rotary(x, w, angles, layout="half", magnitude=1.0, eps=1e-6):
+    x = _f64(x)
+    w = 1.0 if w is None else _f64(w)
+    return rotary(x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * w, angles, layout, magnitude)
+
+
+def norm_rotary_backward(x, dy, w, angles, layout="half", magnitude=1.0, eps=1e-6):
+    """(dx, dw)."""
+    x, w = _f64(x), 1.0 if w is None else _f64(w)
+    g = rotary(dy, -angles, layout, magnitude)
+    r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    u, h = x * r, g * w
+    return r * (h - u * (u * h).mean(-1, keepdims=True)), (g * u).reshape(-1, x.shape[-1]).sum(0)
