@@ -24,7 +24,7 @@ SOURCES = ["la_api.cu", "ffma_f32.cu", "ffma_bf16.cu", "ncbwd_ffma.cu", "ret_ffm
            "causal_tc.cu", "causal_bwd_tc.cu", "noncausal_tc.cu", "poly_tc.cu", "selftest.cu",
            "gated_scan_bwd_bf16.cu", "gated_scan_fwd_bf16.cu", "gated_scan_bwd_f32.cu",
            "gated_scan_fwd_f32.cu", "gated_scan.cu", "paged_cache.cu", "paged_decode.cu",
-           "paged_prefill.cu", "rotary.cu"]
+           "paged_prefill.cu", "paged_prefill_tc.cu", "rotary.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -209,6 +209,13 @@ cudaError_t paged_prefill(const LaunchCtx& c, const T* q, const T* K, const T* V
                           const int* lens, const int* starts, T* out, float* lse,
                           const PrefillShape& s, int fill);
 
+// bf16 on the tensor core, and its scratch bytes.
+template <int D>
+cudaError_t paged_prefill_tc(const LaunchCtx& c, const __nv_bfloat16* q, const __nv_bfloat16* K, const __nv_bfloat16* V,
+                             const int* table, const int* lens, const int* starts, __nv_bfloat16* out, float* lse,
+                             const PrefillShape& s, int fill);
+size_t paged_prefill_tc_scratch(int D, int num_sms);
+
 // Rotary positions of queries (0) and keys (1): ptr and strides (batch row, token, head, in
 // elements) are the inputs' q, k, with a norm's gradient the upstream gradients' next, and
 // last the outputs'.  positions null: first, first + 1, ...; a negative one marks a row

@@ -177,6 +177,7 @@ template <typename T, int D>
 cudaError_t paged_prefill(const LaunchCtx& c, const T* q, const T* K, const T* V, const int* table,
                           const int* lens, const int* starts, T* out, float* lse,
                           const PrefillShape& s, int fill) {
+    if constexpr (sizeof(T) == 2) return paged_prefill_tc<D>(c, q, K, V, table, lens, starts, out, lse, s, fill);
     PrefillArgs p = {s, s.Hq / s.Hkv, table, lens, starts, lse, fill, c.status_word};
     const int64_t tiles = (static_cast<int64_t>(s.T) * p.G + kRows - 1) / kRows + s.R;
     paged_prefill_kernel<T, D><<<dim3(static_cast<unsigned>(tiles), s.Hkv), kThreads, 0, c.stream>>>(q, K, V, out, p);

@@ -1,0 +1,759 @@
+// paged_prefill_tc.cu -- attention of each request's new tokens over its pages, bf16, on the
+// tensor core (the formulas are paged_prefill.cu's).
+//
+// Bound by the tensor core for long chunks (4 D operations a query head and visible
+// position), by memory for a few tokens over long contexts.  One block an SM takes a range of
+// steps (prefill_plan.cuh): 256 rows of a request and key head, as two subtiles of 128, against
+// 128 key positions.  Warps:
+//   0-3, 4-7  softmax of subtile 0 and 1, a row a thread, and the rows' outputs
+//   8         every matrix product, issued by one thread
+//   9         keys and values by TMA, a page a lane, into a ring of tiles
+//   10, 11    queries, and the values of tiles that some row sees only in part
+// S = Q K^T goes to tensor memory, a thread turns its row's 128 scores into weights there, and
+// O += P V reads the weights from tensor memory.  The two subtiles take turns: while one's
+// scores become weights, the tensor core works for the other.
+//
+// The maximum is kept lazily: it is raised, and the sums so far rescaled in tensor memory, only when
+// a score passes it by more than 2^8.  The weights are rounded to bf16 for the product with
+// the values (2^-8 of a weight at most, which the rounding of the outputs equals); their sums are fp32
+// sums of the unrounded ones.
+//
+// Values that a row does not see have weight 0, but 0 times an infinity or NaN is no 0.
+// So in tiles that some row sees in part, warps 10 and 11 clear the value rows that no row
+// sees, and replace what is not finite in the others by 0; a row that does see such an
+// element gets NaN in that column at the end.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "la_common.cuh"
+#include "la_launch.h"
+#include "la_plan.h"
+#include "prefill_plan.cuh"
+#include "tc_common.cuh"
+
+namespace la {
+namespace {
+
+using namespace la::tc;
+using prefill::Args;
+using prefill::Keys;
+using prefill::Request;
+using prefill::Segment;
+using bf16 = __nv_bfloat16;
+
+constexpr int TM = 256, KT = 128, OVER = 1, NT = 384;
+constexpr int kMasks = 16;            // steps whose masks are kept: more than the loader is ahead of the softmax
+constexpr float kSlack = 8.f;         // log2 by which a score may pass the maximum kept
+constexpr uint32_t kAtom = 16384;     // 128 rows x 128 bytes
+constexpr uint32_t kLimit = 1u << 22; // polls of a wait
+
+template <int D>
+struct Lay {
+    static constexpr int DP = D == 128 ? 128 : 64;  // columns in shared memory: heads of 32 are padded with zeros
+    static constexpr int ATOMS = DP / 64;
+    static constexpr int TILE = ATOMS * kAtom;      // bytes of 128 rows
+    static constexpr int STAGES = D == 128 ? 5 : 8;
+    static constexpr int Q = 2 * TILE;
+    static constexpr int SMEM = Q + STAGES * TILE + 1024;
+    static constexpr uint32_t T_O = 256;            // column of subtile 0's outputs in tensor memory
+    // How often a stage has held values before tile `it` (an odd one) of the ring: keys and values
+    // take turns in a stage if the stages are odd in number.
+    __device__ static __forceinline__ uint32_t value_turn(uint32_t it) { return STAGES % 2 ? it / STAGES / 2 : it / STAGES; }
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// (a0, a1) * (b, b) + (c, c)
+__device__ __forceinline__ float2 fma2(float a0, float a1, float b, float c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+// 32 columns of the thread's row, not waited for.
+__device__ __forceinline__ void ld32(uint32_t taddr, float* v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// The wait for the loads above; their registers pass through it, so that no use moves before it.
+__device__ __forceinline__ void ld_wait(float* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 128; ++i) asm volatile("" : "+f"(v[i]));
+}
+// 16 words of the thread's row, not waited for.
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ bool not_finite2(uint32_t pair) {  // either of two bf16 values
+    return (pair & 0x7F80u) == 0x7F80u || (pair & 0x7F800000u) == 0x7F800000u;
+}
+
+// What steps of a segment a subtile takes part in: [a, b) of the tile's steps.
+struct Part {
+    int a, b, rows;  // rows of the subtile
+    Keys<KT> k;
+    __device__ __forceinline__ Part(const Args& p, const Request& q, const Segment& g, int k0, int w)
+        : rows(min(max(g.rows - g.m0 - 128 * w, 0), 128)),
+          k(p, q, rows ? g.m0 + 128 * w : g.m0, rows ? g.m0 + 128 * w + rows : g.m0 + 1) {
+        a = max(g.a, k.k0 - k0);
+        b = rows ? min(g.b, k.k1 - k0) : a;
+        b = max(b, a);
+    }
+    __device__ __forceinline__ bool on(int j) const { return j >= a && j < b; }
+};
+
+// The columns of [i, i + 32), a bit each, in which a row sees a value that is not finite in a key
+// tile, if that is one in which such values were replaced: one that some row from position
+// `first` to `last` sees in part.
+template <int D>
+__device__ __noinline__ uint32_t odd_columns(const Args& p, const bf16* V, int r, int kh, int first, int last, int end,
+                                             int tile, int from, int pos, int i) {
+    const int x0 = tile * KT, mask = (1 << p.s.log2p) - 1;
+    const int* table = p.table + static_cast<int64_t>(r) * p.s.max_pages;
+    uint32_t bits = 0;
+    bool all = x0 + KT - 1 <= first && (p.s.window == 0 || x0 > last - p.s.window) && x0 + KT <= end;
+    for (int x = x0; all && x < x0 + KT; x += mask + 1)
+        all = static_cast<unsigned>(table[x >> p.s.log2p]) < static_cast<unsigned>(p.s.num_pages);
+    if (all) return 0;
+    for (int x = max(x0, max(from + 1, 0)); x < min(x0 + KT, min(pos + 1, end)); ++x) {
+        const int page = table[x >> p.s.log2p];
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.s.num_pages)) continue;
+        const bf16* v = V + (((static_cast<int64_t>(page) * p.s.Hkv + kh) << p.s.log2p) + (x & mask)) * D + i;
+        for (int y = 0; y < 32; ++y)
+            if (!(fabsf(__bfloat162float(v[y])) < INFINITY)) bits |= 1u << y;
+    }
+    return bits;
+}
+
+template <int D>
+__global__ void __launch_bounds__(NT, 1)
+prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+               const __grid_constant__ CUtensorMap qmap, const bf16* __restrict__ q, const bf16* __restrict__ K,
+               const bf16* __restrict__ V, bf16* __restrict__ out, const Args p, const int q_tma, const int kv_tma) {
+    using Ly = Lay<D>;
+    constexpr int DP = Ly::DP, ATOMS = Ly::ATOMS, STAGES = Ly::STAGES;
+    using Plan = prefill::Planner<TM, KT, OVER, NT>;
+    using Walk = prefill::Walk<TM, KT, OVER>;
+    extern __shared__ uint8_t sm_raw[];
+    __shared__ uint64_t s_full[STAGES], s_empty[STAGES], s_vready[STAGES];
+    __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_end;
+    __shared__ uint32_t s_mask[kMasks][4];   // positions of a step that are on a page, a bit each
+    __shared__ volatile int s_odd[4];        // by segment: a value that was not finite was replaced
+    __shared__ volatile int s_abort;
+    __shared__ uint32_t s_tmem;
+    __shared__ prefill::Start s_start;
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* ring = sm + Ly::Q;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (tid == 0) {
+        for (int i = 0; i < STAGES; ++i) mbar_init(s_full + i, 1), mbar_init(s_empty + i, 1), mbar_init(s_vready + i, 64);
+        mbar_init(&s_qfull, 64);
+        mbar_init(&s_qempty, 1);
+        mbar_init(&s_end, 1);
+        for (int w = 0; w < 2; ++w) mbar_init(s_sfull + w, 1), mbar_init(s_pfull + w, 128), mbar_init(s_odone + w, 1);
+        s_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(&s_tmem, 512);
+        tmem_relinquish();
+    }
+    if (tid < 2) p.desc[2 * blockIdx.x + tid] = make_int4(0, 0, 0, 0);
+    Plan& plan = *reinterpret_cast<Plan*>(sm);  // before anything else is in there
+    plan.run(p);
+    if (tid == 0) s_start = plan.start;
+    fence_before_sync();
+    fence_proxy_async();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tm = s_tmem;
+    const prefill::Start st = s_start;
+    const auto fail = [&]() {
+        s_abort = 1;
+        atomicOr(p.status, tcf::kErrWait);
+    };
+    // Waits give up after kLimit polls, or once any of them has.
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const int e = mbar_wait_or(bar, parity & 1u, kLimit, const_cast<const volatile int*>(&s_abort));
+        if (e == 2) fail();
+        return e == 0;
+    };
+    const auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+
+    if (st.any) {
+        Walk walk(p, st.r, st.kh, st.mt, st.off, st.left);
+        Segment g;
+        if (warp < 8) {
+            // ---------------------------------------------------------------- softmax
+            const int w = warp >> 2, row = tid & 127;
+            const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's quarter of the lanes
+            const uint32_t ts = tm + 128 * w + lanes, to = tm + Ly::T_O + DP * w + lanes;
+            const float c = fabsf(p.s.scale) * 1.4426950408889634f;
+            uint32_t n_s = 0, n_o = 0, step = 0;  // phases seen, steps of the block
+            for (int seg = 0; walk.next(p, g); ++seg) {
+                const Request rq(p, g.r);
+                const Keys<KT> kt(p, rq, g.m0, min(g.m0 + TM, g.rows));
+                const int k0 = kt.k0;
+                const Part mine(p, rq, g, k0, w);
+                const int m = g.m0 + 128 * w + row;
+                const bool live = row < mine.rows;
+                const int pos = rq.cached + m / p.G;              // of the row
+                const int from = p.s.window ? pos - p.s.window : -1;  // it sees positions past this one
+                float top = -INFINITY, sum = 0.f;
+                bool ok = true;
+                for (int j = g.a; j < g.b; ++j, ++step) {
+                    if (!mine.on(j)) continue;
+                    if (!(ok = warp_wait(s_sfull + w, n_s++))) break;
+                    fence_after_sync();
+                    float s[128];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ld32(ts + 32 * i, s + 32 * i);
+                    const int x0 = (k0 + j) * KT;
+                    const uint32_t* mask = s_mask[step % kMasks];
+                    const uint32_t m0 = mask[0], m1 = mask[1], m2 = mask[2], m3 = mask[3];
+                    const bool all = x0 + KT - 1 <= mine.k.first && (p.s.window == 0 || x0 > mine.k.last - p.s.window) &&
+                                     (m0 & m1 & m2 & m3) == 0xFFFFFFFFu;
+                    ld_wait(s);
+                    if (!all) {
+                        const int c0 = from + 1 - x0, c1 = pos - x0;  // columns [c0, c1] of the tile are seen
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) {
+                            const uint32_t bits = i < 32 ? m0 : i < 64 ? m1 : i < 96 ? m2 : m3;
+                            s[i] = i >= c0 && i <= c1 && (bits >> (i & 31) & 1u) ? s[i] : -INFINITY;
+                        }
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx[i] = fmaxf(s[i], s[4 + i]);
+#pragma unroll
+                    for (int i = 8; i < 128; i += 8)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], s[i + x], s[i + 4 + x]);
+                    const float best = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+                    const bool raise = best > top + kSlack;  // also from -infinity
+                    if (__any_sync(0xffffffffu, raise) ) {
+                        const float f = raise ? (top == -INFINITY ? 0.f : ex2(top - best)) : 1.f;
+                        if (raise) top = best;
+                        sum *= f;
+                        if (j > mine.a) {  // the product before this one has finished: the scores came behind it
+#pragma unroll 1
+                            for (int i = 0; i < DP; i += 16) {
+                                float o[16];
+                                tmem_ld16(to + i, o);
+#pragma unroll
+                                for (int x = 0; x < 16; ++x) o[x] *= f;
+                                tmem_st16(to + i, o);
+                            }
+                        }
+                    }
+                    const float base = top == -INFINITY ? 0.f : -top;
+                    float2 t0 = make_float2(0.f, 0.f), t1 = t0;
+#pragma unroll
+                    for (int i = 0; i < 128; i += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int x = 0; x < 16; x += 2) {
+                            float2 a = fma2(s[i + 2 * x], s[i + 2 * x + 1], c, base);
+                            float2 b = fma2(s[i + 2 * x + 2], s[i + 2 * x + 3], c, base);
+                            a.x = ex2(a.x), a.y = ex2(a.y), b.x = ex2(b.x), b.y = ex2(b.y);
+                            t0 = add2(t0, a);
+                            t1 = add2(t1, b);
+                            pk[x] = pack_bf16(a.x, a.y);
+                            pk[x + 1] = pack_bf16(b.x, b.y);
+                        }
+                        st16(ts + i / 2, pk);
+                    }
+                    t0 = add2(t0, t1);
+                    sum += t0.x + t0.y;
+                    st_wait();
+                    fence_before_sync();
+                    mbar_arrive(s_pfull + w);
+                }
+                if (!ok) break;
+                // ------------------------------------------------------------ the rows' outputs
+                const bool some = mine.b > mine.a;
+                if (some) {
+                    if (!warp_wait(s_odone + w, n_o++)) break;
+                    fence_after_sync();
+                }
+                const bool whole = g.whole();
+                const int slot = 2 * blockIdx.x + (g.a == 0 ? 1 : 0);
+                const bool good = sum > 0.f || sum != sum;
+                const float inv = !whole ? 1.f : good ? 1.f / sum : 0.f;
+                const int64_t at = (static_cast<int64_t>(rq.first) + m / p.G) * p.s.Hq + static_cast<int64_t>(g.kh) * p.G + m % p.G;
+                float* part = p.part + (static_cast<int64_t>(slot) * TM + 128 * w + row) * D;
+#pragma unroll 1
+                for (int i = 0; i < D; i += 32) {
+                    float o[32];
+                    if (some) {
+                        tmem_ld32(to + i, o);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = 0.f;
+                    }
+                    if (s_odd[seg & 3]) {  // rare: does this row see one of the replaced values?
+                        uint32_t bits = 0;
+                        for (int j = mine.a; live && j < mine.b; ++j)
+                            bits |= odd_columns<D>(p, V, g.r, g.kh, kt.first, kt.last, rq.end, k0 + j, from, pos, i);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (bits >> x & 1u) o[x] = __uint_as_float(0x7FFFFFFFu);
+                    }
+                    if (live) {
+                    if (whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(out + at * D + i);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            dst[x] = make_uint4(pack_bf16(o[8 * x] * inv, o[8 * x + 1] * inv), pack_bf16(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
+                                                pack_bf16(o[8 * x + 4] * inv, o[8 * x + 5] * inv), pack_bf16(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4) *reinterpret_cast<float4*>(part + i + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                    }
+                    }
+                    __syncwarp();
+                }
+                if (live) {
+                    if (!whole) p.ml[static_cast<int64_t>(slot) * TM + 128 * w + row] = make_float2(top, sum);
+                    else if (p.lse) p.lse[at] = good ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                }
+                fence_before_sync();  // the outputs' columns are free with the next arrival
+            }
+        } else if (warp == 8) {
+            // ---------------------------------------------------------------- products
+            if (lane == 0) {
+                constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_O = idesc_bf16(128, DP, false, true);
+                const uint32_t sq = smem_u32(sm), sr = smem_u32(ring);
+                uint32_t item = 0, n_q = 0, n_p[2] = {0, 0};  // tiles taken from the ring: K, V, K, V, ...
+                bool ok = true;
+                const auto scores = [&](int w, uint32_t it) {
+                    const uint32_t a = sq + w * Ly::TILE, b = sr + it % STAGES * Ly::TILE;
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) {
+                        const uint32_t off = (k >> 2) * kAtom + 32 * (k & 3);
+                        mma_bf16(tm + 128 * w, sdesc(a + off, 16, 1024), sdesc(b + off, 16, 1024), ID_S, k > 0 ? 1u : 0u);
+                    }
+                    mma_commit(s_sfull + w);
+                };
+                while (ok && walk.next(p, g)) {
+                    const Request rq(p, g.r);
+                    const int k0 = Keys<KT>(p, rq, g.m0, min(g.m0 + TM, g.rows)).k0;
+                    const Part part[2] = {Part(p, rq, g, k0, 0), Part(p, rq, g, k0, 1)};
+                    if (!(ok = wait(&s_qfull, n_q++))) break;
+                    fence_after_sync();
+                    if (!(ok = wait(s_full + item % STAGES, item / STAGES))) break;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w)
+                        if (part[w].on(g.a)) scores(w, item);
+                    mma_commit(s_empty + item % STAGES);
+                    if (g.a + 1 == g.b) mma_commit(&s_qempty);
+                    for (int j = g.a; ok && j < g.b; ++j, item += 2) {
+                        const uint32_t v = item + 1, nk = item + 2;
+                        bool have_v = false, have_k = false;
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            if (part[w].on(j)) {
+                                if (!(ok = wait(s_pfull + w, n_p[w]++))) break;
+                                if (!have_v && !(ok = wait(s_vready + v % STAGES, Ly::value_turn(v)))) break;
+                                have_v = true;
+                                fence_after_sync();
+                                const uint32_t b = sr + v % STAGES * Ly::TILE;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    mma_bf16_ts(tm + Ly::T_O + DP * w, tm + 128 * w + 8 * k, sdesc(b + 2048 * k, kAtom, 1024), ID_O,
+                                                j > part[w].a || k > 0 ? 1u : 0u);
+                                if (j + 1 == part[w].b) mma_commit(s_odone + w);
+                            }
+                            if (j + 1 < g.b && part[w].on(j + 1)) {
+                                if (!have_k && !(ok = wait(s_full + nk % STAGES, nk / STAGES))) break;
+                                have_k = true;
+                                scores(w, nk);
+                            }
+                        }
+                        if (!ok) break;
+                        if (!have_v && !(ok = wait(s_vready + v % STAGES, Ly::value_turn(v)))) break;
+                        mma_commit(s_empty + v % STAGES);
+                        if (j + 1 < g.b) {
+                            if (!have_k && !(ok = wait(s_full + nk % STAGES, nk / STAGES))) break;
+                            mma_commit(s_empty + nk % STAGES);
+                            if (j + 2 == g.b) mma_commit(&s_qempty);
+                        }
+                    }
+                }
+                // nothing may be under way when the block ends
+                mma_commit(&s_end);
+                if (!mbar_wait(&s_end, 0, kLimit)) fail();
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ---------------------------------------------------------------- keys and values
+            const int log2p = p.s.log2p, page = 1 << log2p, off_mask = page - 1;
+            const int rows = min(page, KT);              // of a copy
+            const int copies = KT / rows;                // of a tile and atom column
+            uint32_t item = 0, step = 0, issued = 0;
+            bool ok = true, bad = false;
+            while (ok && walk.next(p, g)) {
+                const Request rq(p, g.r);
+                const Keys<KT> k(p, rq, g.m0, min(g.m0 + TM, g.rows));
+                const int* table = p.table + static_cast<int64_t>(g.r) * p.s.max_pages;
+                const auto page_of = [&](int x) {  // the page of position x < end, or -1
+                    const int i = table[x >> log2p];
+                    const bool in = static_cast<unsigned>(i) < static_cast<unsigned>(p.s.num_pages);
+                    return in ? i : -1;
+                };
+                const int mine = kv_tma ? lane % copies : 0, atom = kv_tma ? lane / copies : 0;  // the lane's copy of a tile
+                const auto fetch = [&](int j) {
+                    const int x = (k.k0 + j) * KT + mine * rows;
+                    return kv_tma && j < g.b && x < k.hi ? page_of(x) : -2;
+                };
+                int id = fetch(g.a);
+                for (int j = g.a; ok && j < g.b; ++j, ++step, item += 2) {
+                    const int x0 = (k.k0 + j) * KT, x = x0 + mine * rows, now = id;
+                    id = fetch(j + 1);
+                    if (kv_tma) {
+                        const bool copy = now >= 0 && lane < copies * ATOMS;
+                        bad |= now == -1;
+                        const unsigned lost = __ballot_sync(0xffffffffu, now == -1) & (copies == 32 ? 0xFFFFFFFFu : (1u << copies) - 1u);
+                        const unsigned who = __ballot_sync(0xffffffffu, copy);
+                        for (int kv = 0; ok && kv < 2; ++kv) {
+                            const uint32_t it = item + kv, sg = it % STAGES;
+                            if (!(ok = warp_wait(s_empty + sg, it / STAGES + 1))) break;
+                            if (kv == 0 && lane < 4) {  // 32 positions a word: those on a lost page, or past the table, are off
+                                uint32_t m = 0xFFFFFFFFu;
+                                for (int i = 0; i < 32 && (lost || x0 + KT > rq.end); ++i) {
+                                    const int y = 32 * lane + i;
+                                    if ((lost >> (y / rows) & 1u) || x0 + y >= rq.end) m &= ~(1u << i);
+                                }
+                                s_mask[step % kMasks][lane] = m;
+                            }
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (who) mbar_arrive_expect_tx(s_full + sg, __popc(who) * rows * 128);
+                                else mbar_arrive(s_full + sg);
+                            }
+                            __syncwarp();
+                            if (copy)
+                                tma_load_3d(ring + sg * Ly::TILE + atom * kAtom + mine * rows * 128, kv ? &vmap : &kmap, s_full + sg,
+                                            atom * 64, x & off_mask, now * p.s.Hkv + g.kh);
+                            issued = it + 1;
+                        }
+                    } else {
+                        // pages of fewer than eight positions: four rows a lane, 16 bytes at a time
+                        int ids[4];
+                        uint32_t mask[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int y = x0 + 32 * i + lane;
+                            ids[i] = y < k.hi ? page_of(y) : -2;
+                            bad |= ids[i] == -1;
+                            mask[i] = __ballot_sync(0xffffffffu, ids[i] != -1 && y < rq.end);
+                        }
+                        for (int kv = 0; ok && kv < 2; ++kv) {
+                            const uint32_t it = item + kv, sg = it % STAGES;
+                            if (!(ok = warp_wait(s_empty + sg, it / STAGES + 1))) break;
+                            const uint32_t dst = smem_u32(ring + sg * Ly::TILE);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int y = 32 * i + lane;
+                                const int64_t src = ids[i] < 0 ? 0 : (((static_cast<int64_t>(ids[i]) * p.s.Hkv + g.kh) << log2p) + ((x0 + y) & off_mask)) * D;
+                                for (int e = 0; e < DP / 8; ++e) {
+                                    const bool on = ids[i] >= 0 && e < D / 8;
+                                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (e >> 3) * kAtom + swz(y, e & 7)),
+                                                 "l"((kv ? V : K) + (on ? src + e * 8 : 0)), "r"(on ? 16 : 0)
+                                                 : "memory");
+                                }
+                            }
+                            asm volatile("cp.async.wait_all;" ::: "memory");
+                            if (kv == 0 && lane == 0)
+                                for (int i = 0; i < 4; ++i) s_mask[step % kMasks][i] = mask[i];
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(s_full + sg);
+                        }
+                    }
+                }
+            }
+            if (bad) atomicOr(p.status, kStatusBadIndex);
+            // copies under way end before the block does
+            for (uint32_t it = issued > STAGES ? issued - STAGES : 0; it < issued; ++it)
+                if (!mbar_wait(s_full + it % STAGES, it / STAGES & 1u, kLimit)) fail();
+        } else {
+            // ---------------------------------------------------------------- queries, values seen in part
+            const int t = tid - 320;
+            uint32_t item = 0, n_q = 0, step = 0;
+            bool ok = true;
+            for (int seg = 0; ok && walk.next(p, g); ++seg) {
+                const Request rq(p, g.r);
+                const Keys<KT> k(p, rq, g.m0, min(g.m0 + TM, g.rows));
+                if (n_q && !(ok = warp_wait(&s_qempty, n_q - 1))) break;
+                ++n_q;
+                if (t == 0) s_odd[seg & 3] = 0;
+                const int subs = g.rows - g.m0 > 128 ? 2 : 1;
+                if (q_tma) {
+                    if (t == 0) {
+                        mbar_arrive_expect_tx(&s_qfull, subs * Ly::TILE);
+                        for (int w = 0; w < subs; ++w)
+                            for (int a = 0; a < ATOMS; ++a)
+                                tma_load_3d(sm + w * Ly::TILE + a * kAtom, &qmap, &s_qfull, 64 * a, g.kh * p.G, rq.first + (g.m0 + 128 * w) / p.G);
+                    } else {
+                        mbar_arrive(&s_qfull);
+                    }
+                } else {
+                    // any number of heads, or a negative scale: 16 bytes at a time, the sign turned here
+                    const uint32_t flip = p.s.scale < 0.f ? 0x80008000u : 0u;
+                    constexpr int CH = DP / 8;
+                    for (int i0 = t; i0 < subs * 128 * CH; i0 += 64 * 8) {
+                        uint4 x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int e = i0 + 64 * i, y = e / CH, ch = e % CH, m = g.m0 + y;
+                            x[i] = make_uint4(0u, 0u, 0u, 0u);
+                            if (m < g.rows && ch < D / 8)
+                                x[i] = *reinterpret_cast<const uint4*>(
+                                    q + ((static_cast<int64_t>(rq.first) + m / p.G) * p.s.Hq + static_cast<int64_t>(g.kh) * p.G + m % p.G) * D + ch * 8);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int e = i0 + 64 * i, y = e / CH, ch = e % CH;
+                            x[i].x ^= flip, x[i].y ^= flip, x[i].z ^= flip, x[i].w ^= flip;
+                            *reinterpret_cast<uint4*>(sm + (y >> 7) * Ly::TILE + (ch >> 3) * kAtom + swz(y & 127, ch & 7)) = x[i];
+                        }
+                    }
+                    fence_proxy_async();
+                    mbar_arrive(&s_qfull);
+                }
+                for (int j = g.a; ok && j < g.b; ++j, ++step, item += 2) {
+                    const uint32_t v = item + 1, sg = v % STAGES;
+                    if (!(ok = warp_wait(s_full + sg, v / STAGES))) break;
+                    const int x0 = (k.k0 + j) * KT;
+                    const uint32_t* mask = s_mask[step % kMasks];
+                    const bool all = x0 + KT - 1 <= k.first && (p.s.window == 0 || x0 > k.last - p.s.window) &&
+                                     (mask[0] & mask[1] & mask[2] & mask[3]) == 0xFFFFFFFFu;
+                    if (!all) {
+                        uint8_t* tile = ring + sg * Ly::TILE;
+                        bool odd = false;
+                        for (int e = t; e < 128 * ATOMS * 8; e += 64) {  // 16 bytes of a row
+                            const int y = e >> 3 & 127, x = x0 + y;
+                            uint4* at = reinterpret_cast<uint4*>(tile + e * 16);
+                            if (x < k.lo || x >= k.hi || !(mask[y >> 5] >> (y & 31) & 1u)) {
+                                *at = make_uint4(0u, 0u, 0u, 0u);
+                                continue;
+                            }
+                            uint4 u = *at;
+                            if (not_finite2(u.x) || not_finite2(u.y) || not_finite2(u.z) || not_finite2(u.w)) {
+                                odd = true;
+                                uint32_t* z = &u.x;
+                                for (int i = 0; i < 4; ++i) {
+                                    if ((z[i] & 0x7F80u) == 0x7F80u) z[i] &= 0xFFFF0000u;
+                                    if ((z[i] & 0x7F800000u) == 0x7F800000u) z[i] &= 0xFFFFu;
+                                }
+                                *at = u;
+                            }
+                        }
+                        if (odd) s_odd[seg & 3] = 1;
+                        fence_proxy_async();
+                    }
+                    mbar_arrive(s_vready + sg);
+                }
+            }
+            if (q_tma && n_q && t == 0 && !mbar_wait(&s_qfull, (n_q - 1) & 1u, kLimit)) fail();
+        }
+    }
+    // rows of no request
+    if (p.fill) {
+        const int64_t wide = static_cast<int64_t>(p.s.Hq) * (D / 8);
+        const auto clear = [&](int64_t t0, int64_t t1) {
+            if (p.fill & 1)
+                for (int64_t e = t0 * wide + tid; e < t1 * wide; e += NT) reinterpret_cast<uint4*>(out)[e] = make_uint4(0u, 0u, 0u, 0u);
+            if (p.fill & 2)
+                for (int64_t e = t0 * p.s.Hq + tid; e < t1 * p.s.Hq; e += NT) p.lse[e] = -INFINITY;
+        };
+        const int last = p.s.R ? min(max(p.starts[p.s.R], 0), p.s.T) : 0;
+        for (int64_t t0 = last + 16 * static_cast<int64_t>(blockIdx.x); t0 < p.s.T; t0 += 16 * static_cast<int64_t>(gridDim.x))
+            clear(t0, min(t0 + 16, static_cast<int64_t>(p.s.T)));
+        for (int r = blockIdx.x; r < p.s.R; r += gridDim.x) {
+            const Request rq(p, r);
+            if (rq.pad && rq.n) clear(rq.first, rq.first + rq.n);
+        }
+    }
+    // the cut tile that starts in this range
+    if (st.any && tid == 0 && !s_abort) {
+        Walk walk(p, st.r, st.kh, st.mt, st.off, st.left);
+        Segment g, last = {};
+        while (walk.next(p, g)) last = g;
+        if (last.b > 0 && last.a == 0 && !last.whole()) {
+            p.desc[2 * blockIdx.x] = make_int4(last.r, last.kh, last.m0, last.rows);
+            p.desc[2 * blockIdx.x + 1] = make_int4(prefill::ranges_of<OVER>(last, st.left, st.per), 0, 0, 0);
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 8) {
+        fence_after_sync();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// Joins the partial sums of the cut tile that starts in range blockIdx.x: a warp a row.
+constexpr int kJoinWarps = 8, kJoinRows = 32;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Args p, bf16* __restrict__ out) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int ranges = p.desc[2 * blockIdx.x + 1].x;
+    if (ranges == 0) return;
+    const int4 d = p.desc[2 * blockIdx.x];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Request rq(p, d.x);
+    constexpr int E = D / 32, N = 4;
+    for (int i = warp; i < kJoinRows; i += kJoinWarps) {
+        const int row = blockIdx.y * kJoinRows + i, m = d.z + row;
+        if (m >= d.w) return;
+        float top = -INFINITY, sum = 0.f, o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        for (int x0 = 0; x0 < ranges; x0 += N) {
+            float2 ml[N];
+            float v[N][E];
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                const int64_t at = (2 * (static_cast<int64_t>(blockIdx.x) + x0 + x) + (x0 + x == 0 ? 1 : 0)) * TM + row;
+                ml[x] = x0 + x < ranges ? p.ml[at] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[x][e] = x0 + x < ranges ? p.part[at * D + lane + 32 * e] : 0.f;
+            }
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                const float y = fmaxf(top, ml[x].x);
+                const float f = top == y ? 1.f : ex2(top - y);
+                const float h = ml[x].x == y ? 1.f : ml[x].x == -INFINITY ? 0.f : ex2(ml[x].x - y);
+                sum = sum * f + ml[x].y * h;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = o[e] * f + v[x][e] * h;
+                top = y;
+            }
+        }
+        const bool good = sum > 0.f || sum != sum;
+        const int64_t at = (static_cast<int64_t>(rq.first) + m / p.G) * p.s.Hq + static_cast<int64_t>(d.y) * p.G + m % p.G;
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[at * D + lane + 32 * e] = __float2bfloat16_rn(good ? o[e] / sum : 0.f);
+        if (lane == 0 && p.lse) p.lse[at] = good ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
+cudaError_t encode(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3], const cuuint32_t (&box)[3]) {
+    tcf::EncodeTiled enc = tcf::encoder();
+    if (!enc) return cudaErrorNotSupported;
+    cuuint64_t strides[2] = {dims[0] * 2, dims[0] * dims[1] * 2};
+    cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+size_t part_bytes(int D, int num_sms) { return sizeof(float) * 2 * num_sms * TM * D; }
+size_t ml_bytes(int num_sms) { return sizeof(float2) * 2 * num_sms * TM; }
+
+}  // namespace
+
+size_t paged_prefill_tc_scratch(int D, int num_sms) { return part_bytes(D, num_sms) + ml_bytes(num_sms) + sizeof(int4) * 2 * num_sms; }
+
+template <int D>
+cudaError_t paged_prefill_tc(const LaunchCtx& c, const bf16* q, const bf16* K, const bf16* V, const int* table,
+                             const int* lens, const int* starts, bf16* out, float* lse, const PrefillShape& s, int fill) {
+    using Ly = Lay<D>;
+    Args p = {};
+    p.s = s, p.G = s.Hq / s.Hkv, p.least = 4, p.table = table, p.lens = lens, p.starts = starts, p.lse = lse, p.fill = fill;
+    p.status = c.status_word;
+    int per_sm = 1;
+    cudaError_t e = resident_blocks<prefill_kernel<D>>(c.device, NT, Ly::SMEM, &per_sm);
+    if (e != cudaSuccess) return e;
+    CUtensorMap kmap = {}, vmap = {}, qmap = {};
+    const int page = 1 << s.log2p;
+    const int kv_tma = s.log2p >= 3 && s.num_pages > 0 && static_cast<int64_t>(s.num_pages) * s.Hkv < INT_MAX;
+    if (kv_tma) {
+        const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(s.num_pages) * s.Hkv};
+        const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(std::min(page, KT)), 1};
+        if ((e = encode(&kmap, K, dims, box)) != cudaSuccess || (e = encode(&vmap, V, dims, box)) != cudaSuccess) return e;
+    }
+    const int q_tma = s.scale > 0.f && p.G <= 128 && 128 % p.G == 0;
+    if (q_tma) {
+        const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(s.Hq), static_cast<cuuint64_t>(s.T)};
+        const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(128 / p.G)};
+        if ((e = encode(&qmap, q, dims, box)) != cudaSuccess) return e;
+    }
+    uint8_t* base = nullptr;
+    if ((e = scratch_alloc(c, reinterpret_cast<void**>(&base), paged_prefill_tc_scratch(D, c.num_sms))) != cudaSuccess) return e;
+    p.part = reinterpret_cast<float*>(base);
+    p.ml = reinterpret_cast<float2*>(base + part_bytes(D, c.num_sms));
+    p.desc = reinterpret_cast<int4*>(base + part_bytes(D, c.num_sms) + ml_bytes(c.num_sms));
+    prefill_kernel<D><<<c.num_sms, NT, Ly::SMEM, c.stream>>>(kmap, vmap, qmap, q, K, V, out, p, q_tma, kv_tma);
+    note_launch();
+    e = cudaGetLastError();
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(c.num_sms, TM / kJoinRows);
+        cfg.blockDim = dim3(kJoinWarps * 32);
+        cfg.stream = c.stream;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, prefill_join_kernel<D>, p, out);
+        note_launch();
+    }
+    scratch_free(c, base);
+    return e;
+}
+
+#define LA_INST_PT(D)                                                                                                   \
+    template cudaError_t paged_prefill_tc<D>(const LaunchCtx&, const bf16*, const bf16*, const bf16*, const int*, \
+                                             const int*, const int*, bf16*, float*, const PrefillShape&, int);
+LA_INST_PT(32) LA_INST_PT(64) LA_INST_PT(128)
+
+}  // namespace la
