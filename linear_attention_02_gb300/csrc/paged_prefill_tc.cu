@@ -44,7 +44,8 @@ using prefill::Request;
 using prefill::Segment;
 using bf16 = __nv_bfloat16;
 
-constexpr int TM = 256, KT = 128, OVER = 1, NT = 384;
+constexpr int TM = 256, KT = 128, NT = 384;
+constexpr int kLeast = 6 * KT;        // cost of a range at least, so that small calls are not cut too fine
 constexpr int kMasks = 16;            // steps whose masks are kept: more than the loader is ahead of the softmax
 constexpr float kSlack = 8.f;         // log2 by which a score may pass the maximum kept
 constexpr uint32_t kAtom = 16384;     // 128 rows x 128 bytes
@@ -126,8 +127,53 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* v) {
         : "memory");
 }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ bool not_finite2(uint32_t pair) {  // either of two bf16 values
-    return (pair & 0x7F80u) == 0x7F80u || (pair & 0x7F800000u) == 0x7F800000u;
+// Bits lo .. hi of a word, those of them that it has.
+__device__ __forceinline__ uint32_t span(int lo, int hi) {
+    const uint32_t to = hi < 0 ? 0u : hi >= 31 ? 0xFFFFFFFFu : (2u << hi) - 1u;
+    return lo <= 0 ? to : lo > 31 ? 0u : to & (0xFFFFFFFFu << lo);
+}
+// Bits 15 and 31 where one of two bf16 values is an infinity or NaN (all exponent bits set).
+__device__ __forceinline__ uint32_t not_finite2(uint32_t pair) { return ((pair & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// One lane of the warp, always the same: the compiler sees a single thread in what follows.
+__device__ __forceinline__ bool elect() {
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
+
+// x * 0 + z for two bf16 values.
+__device__ __forceinline__ uint32_t zero2(uint32_t x, uint32_t z) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(z));
+    return r;
+}
+
+// Products over K = 128 (or 64) elements in steps of 16, issued by one thread.  S += Q K^T: both operands
+// with K along rows of 128 bytes, 64 elements an atom column.
+#define LA_MMA_SS(A, B) "tcgen05.mma.cta_group::1.kind::f16 [%0], " A ", " B ", %3, q;\n\t"
+#define LA_MMA_SS_NEXT(N) "add.s64 a, %1, " N ";\n\tadd.s64 b, %2, " N ";\n\t" LA_MMA_SS("a", "b")
+template <int STEPS>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    static_assert(STEPS == 4 || STEPS == 8, "64 or 128 columns");
+    if constexpr (STEPS == 4)
+        asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, 0, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+                     LA_MMA_SS_NEXT("2") LA_MMA_SS_NEXT("4") LA_MMA_SS_NEXT("6") "}" ::"r"(d), "l"(a), "l"(b), "r"(idesc) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, 0, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+                     LA_MMA_SS_NEXT("2") LA_MMA_SS_NEXT("4") LA_MMA_SS_NEXT("6") LA_MMA_SS_NEXT("1024") LA_MMA_SS_NEXT("1026")
+                     LA_MMA_SS_NEXT("1028") LA_MMA_SS_NEXT("1030") "}" ::"r"(d), "l"(a), "l"(b), "r"(idesc) : "memory");
+}
+// O += P V over 128 keys: P from tensor memory (8 columns a step), V with keys along atoms of 2048 bytes.
+#define LA_MMA_TS_NEXT(N, M) "add.s32 a, %1, " N ";\n\tadd.s64 b, %2, " M ";\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+                 LA_MMA_TS_NEXT("8", "128") LA_MMA_TS_NEXT("16", "256") LA_MMA_TS_NEXT("24", "384") LA_MMA_TS_NEXT("32", "512")
+                 LA_MMA_TS_NEXT("40", "640") LA_MMA_TS_NEXT("48", "768") LA_MMA_TS_NEXT("56", "896") "}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add)
+                 : "memory");
 }
 
 // What steps of a segment a subtile takes part in: [a, b) of the tile's steps.
@@ -174,8 +220,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                const bf16* __restrict__ V, bf16* __restrict__ out, const Args p, const int q_tma, const int kv_tma) {
     using Ly = Lay<D>;
     constexpr int DP = Ly::DP, ATOMS = Ly::ATOMS, STAGES = Ly::STAGES;
-    using Plan = prefill::Planner<TM, KT, OVER, NT>;
-    using Walk = prefill::Walk<TM, KT, OVER>;
+    using Plan = prefill::Planner<TM, KT, NT>;
+    using Walk = prefill::Walk<TM, KT>;
     extern __shared__ uint8_t sm_raw[];
     __shared__ uint64_t s_full[STAGES], s_empty[STAGES], s_vready[STAGES];
     __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_end;
@@ -183,18 +229,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     __shared__ volatile int s_odd[4];        // by segment: a value that was not finite was replaced
     __shared__ volatile int s_abort;
     __shared__ uint32_t s_tmem;
-    __shared__ prefill::Start s_start;
+    __shared__ prefill::Range s_range;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* ring = sm + Ly::Q;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) < 4 ? (tid >> 5) + 8 : (tid >> 5) - 4;  // by role
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (tid == 0) {
-        for (int i = 0; i < STAGES; ++i) mbar_init(s_full + i, 1), mbar_init(s_empty + i, 1), mbar_init(s_vready + i, 64);
-        mbar_init(&s_qfull, 64);
+        for (int i = 0; i < STAGES; ++i) mbar_init(s_full + i, 1), mbar_init(s_empty + i, 1), mbar_init(s_vready + i, 2);
+        mbar_init(&s_qfull, 2);
         mbar_init(&s_qempty, 1);
         mbar_init(&s_end, 1);
-        for (int w = 0; w < 2; ++w) mbar_init(s_sfull + w, 1), mbar_init(s_pfull + w, 128), mbar_init(s_odone + w, 1);
+        for (int w = 0; w < 2; ++w) mbar_init(s_sfull + w, 1), mbar_init(s_pfull + w, 4), mbar_init(s_odone + w, 1);
         s_abort = 0;
         fence_mbar_init();
     }
@@ -205,13 +251,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     if (tid < 2) p.desc[2 * blockIdx.x + tid] = make_int4(0, 0, 0, 0);
     Plan& plan = *reinterpret_cast<Plan*>(sm);  // before anything else is in there
     plan.run(p);
-    if (tid == 0) s_start = plan.start;
+    if (tid == 0) s_range = plan.range;
     fence_before_sync();
     fence_proxy_async();
     __syncthreads();
     fence_after_sync();
     const uint32_t tm = s_tmem;
-    const prefill::Start st = s_start;
+    const prefill::Range range = s_range;
     const auto fail = [&]() {
         s_abort = 1;
         atomicOr(p.status, tcf::kErrWait);
@@ -224,12 +270,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     };
     const auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
-    if (st.any) {
-        Walk walk(p, st.r, st.kh, st.mt, st.off, st.left);
-        Segment g;
+    // The launch's 168 registers a thread become 208 for the softmax and 88 for the rest.
+    if (range.any) {
         if (warp < 8) {
             // ---------------------------------------------------------------- softmax
-            const int w = warp >> 2, row = tid & 127;
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+            Walk walk(p, range);
+            Segment g;
+            const int w = warp >> 2, row = 32 * (warp & 3) + lane;
             const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's quarter of the lanes
             const uint32_t ts = tm + 128 * w + lanes, to = tm + Ly::T_O + DP * w + lanes;
             const float c = fabsf(p.s.scale) * 1.4426950408889634f;
@@ -260,11 +308,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     ld_wait(s);
                     if (!all) {
                         const int c0 = from + 1 - x0, c1 = pos - x0;  // columns [c0, c1] of the tile are seen
+                        const uint32_t bits[4] = {m0 & span(c0, c1), m1 & span(c0 - 32, c1 - 32), m2 & span(c0 - 64, c1 - 64),
+                                                  m3 & span(c0 - 96, c1 - 96)};
 #pragma unroll
-                        for (int i = 0; i < 128; ++i) {
-                            const uint32_t bits = i < 32 ? m0 : i < 64 ? m1 : i < 96 ? m2 : m3;
-                            s[i] = i >= c0 && i <= c1 && (bits >> (i & 31) & 1u) ? s[i] : -INFINITY;
-                        }
+                        for (int i = 0; i < 128; ++i) s[i] = bits[i >> 5] & (1u << (i & 31)) ? s[i] : -INFINITY;
                     }
                     float mx[4];
 #pragma unroll
@@ -311,7 +358,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     sum += t0.x + t0.y;
                     st_wait();
                     fence_before_sync();
-                    mbar_arrive(s_pfull + w);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_pfull + w);
                 }
                 if (!ok) break;
                 // ------------------------------------------------------------ the rows' outputs
@@ -363,72 +411,68 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 }
                 fence_before_sync();  // the outputs' columns are free with the next arrival
             }
-        } else if (warp == 8) {
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+            Walk walk(p, range);
+            Segment g;
+            if (warp == 8) {
             // ---------------------------------------------------------------- products
-            if (lane == 0) {
-                constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_O = idesc_bf16(128, DP, false, true);
-                const uint32_t sq = smem_u32(sm), sr = smem_u32(ring);
-                uint32_t item = 0, n_q = 0, n_p[2] = {0, 0};  // tiles taken from the ring: K, V, K, V, ...
-                bool ok = true;
-                const auto scores = [&](int w, uint32_t it) {
-                    const uint32_t a = sq + w * Ly::TILE, b = sr + it % STAGES * Ly::TILE;
-#pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        const uint32_t off = (k >> 2) * kAtom + 32 * (k & 3);
-                        mma_bf16(tm + 128 * w, sdesc(a + off, 16, 1024), sdesc(b + off, 16, 1024), ID_S, k > 0 ? 1u : 0u);
-                    }
-                    mma_commit(s_sfull + w);
-                };
-                while (ok && walk.next(p, g)) {
-                    const Request rq(p, g.r);
-                    const int k0 = Keys<KT>(p, rq, g.m0, min(g.m0 + TM, g.rows)).k0;
-                    const Part part[2] = {Part(p, rq, g, k0, 0), Part(p, rq, g, k0, 1)};
-                    if (!(ok = wait(&s_qfull, n_q++))) break;
-                    fence_after_sync();
-                    if (!(ok = wait(s_full + item % STAGES, item / STAGES))) break;
+            constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_O = idesc_bf16(128, DP, false, true);
+            const uint64_t dq = sdesc(smem_u32(sm), 16, 1024), dk = sdesc(smem_u32(ring), 16, 1024), dv = sdesc(smem_u32(ring), kAtom, 1024);
+            constexpr uint32_t STEP = Ly::TILE >> 4;  // of a descriptor, from tile to tile
+            uint32_t item = 0, n_q = 0, n_p[2] = {0, 0};  // item: tiles taken from the ring: K, V, K, V, ...
+            bool ok = true;
+            while (ok && walk.next(p, g)) {
+                const Request rq(p, g.r);
+                const int k0 = Keys<KT>(p, rq, g.m0, min(g.m0 + TM, g.rows)).k0;
+                const Part part0(p, rq, g, k0, 0), part1(p, rq, g, k0, 1);
+                if (!(ok = warp_wait(&s_qfull, n_q++) && warp_wait(s_full + item % STAGES, item / STAGES))) break;
+                fence_after_sync();
+                if (elect()) {
+                    const uint64_t k = dk + item % STAGES * STEP;
 #pragma unroll
                     for (int w = 0; w < 2; ++w)
-                        if (part[w].on(g.a)) scores(w, item);
+                        if ((w ? part1 : part0).on(g.a)) {
+                            mma_scores<DP / 16>(tm + 128 * w, dq + w * STEP, k, ID_S);
+                            mma_commit(s_sfull + w);
+                        }
                     mma_commit(s_empty + item % STAGES);
                     if (g.a + 1 == g.b) mma_commit(&s_qempty);
-                    for (int j = g.a; ok && j < g.b; ++j, item += 2) {
-                        const uint32_t v = item + 1, nk = item + 2;
-                        bool have_v = false, have_k = false;
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            if (part[w].on(j)) {
-                                if (!(ok = wait(s_pfull + w, n_p[w]++))) break;
-                                if (!have_v && !(ok = wait(s_vready + v % STAGES, Ly::value_turn(v)))) break;
-                                have_v = true;
-                                fence_after_sync();
-                                const uint32_t b = sr + v % STAGES * Ly::TILE;
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    mma_bf16_ts(tm + Ly::T_O + DP * w, tm + 128 * w + 8 * k, sdesc(b + 2048 * k, kAtom, 1024), ID_O,
-                                                j > part[w].a || k > 0 ? 1u : 0u);
-                                if (j + 1 == part[w].b) mma_commit(s_odone + w);
-                            }
-                            if (j + 1 < g.b && part[w].on(j + 1)) {
-                                if (!have_k && !(ok = wait(s_full + nk % STAGES, nk / STAGES))) break;
-                                have_k = true;
-                                scores(w, nk);
-                            }
-                        }
-                        if (!ok) break;
-                        if (!have_v && !(ok = wait(s_vready + v % STAGES, Ly::value_turn(v)))) break;
-                        mma_commit(s_empty + v % STAGES);
-                        if (j + 1 < g.b) {
-                            if (!have_k && !(ok = wait(s_full + nk % STAGES, nk / STAGES))) break;
-                            mma_commit(s_empty + nk % STAGES);
-                            if (j + 2 == g.b) mma_commit(&s_qempty);
-                        }
-                    }
                 }
-                // nothing may be under way when the block ends
-                mma_commit(&s_end);
-                if (!mbar_wait(&s_end, 0, kLimit)) fail();
+                __syncwarp();
+                for (int j = g.a; j < g.b; ++j, item += 2) {
+                    const uint32_t sv = (item + 1) % STAGES, sk = (item + 2) % STAGES;
+                    const bool more = j + 1 < g.b;
+                    // the values of this step and the keys of the next are mostly here before the weights
+                    if (!(ok = warp_wait(s_vready + sv, Ly::value_turn(item + 1)))) break;
+                    if (more && !(ok = warp_wait(s_full + sk, (item + 2) / STAGES))) break;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const Part& part = w ? part1 : part0;
+                        if (part.on(j) && !(ok = warp_wait(s_pfull + w, n_p[w]++))) break;
+                        fence_after_sync();
+                        if (elect()) {
+                            if (part.on(j)) mma_values(tm + Ly::T_O + DP * w, tm + 128 * w, dv + sv * STEP, ID_O, j > part.a ? 1u : 0u);
+                            if (more && part.on(j + 1)) {
+                                mma_scores<DP / 16>(tm + 128 * w, dq + w * STEP, dk + sk * STEP, ID_S);
+                                mma_commit(s_sfull + w);
+                            }
+                            if (part.on(j) && j + 1 == part.b) mma_commit(s_odone + w);
+                            if (w == 1) {
+                                mma_commit(s_empty + sv);
+                                if (more) mma_commit(s_empty + sk);
+                                if (j + 2 == g.b) mma_commit(&s_qempty);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                }
             }
+            // nothing may be under way when the block ends
+            if (elect()) mma_commit(&s_end);
             __syncwarp();
+            if (!mbar_wait(&s_end, 0, kLimit)) fail();
         } else if (warp == 9) {
             // ---------------------------------------------------------------- keys and values
             const int log2p = p.s.log2p, page = 1 << log2p, off_mask = page - 1;
@@ -523,7 +567,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 if (!mbar_wait(s_full + it % STAGES, it / STAGES & 1u, kLimit)) fail();
         } else {
             // ---------------------------------------------------------------- queries, values seen in part
-            const int t = tid - 320;
+            const int t = 32 * (warp - 10) + lane;
             uint32_t item = 0, n_q = 0, step = 0;
             bool ok = true;
             for (int seg = 0; ok && walk.next(p, g); ++seg) {
@@ -535,11 +579,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 const int subs = g.rows - g.m0 > 128 ? 2 : 1;
                 if (q_tma) {
                     if (t == 0) {
-                        mbar_arrive_expect_tx(&s_qfull, subs * Ly::TILE);
+                        mbar_arrive_expect_tx(&s_qfull, subs * Ly::TILE);  // (the second of the two arrivals is warp 11's)
                         for (int w = 0; w < subs; ++w)
                             for (int a = 0; a < ATOMS; ++a)
                                 tma_load_3d(sm + w * Ly::TILE + a * kAtom, &qmap, &s_qfull, 64 * a, g.kh * p.G, rq.first + (g.m0 + 128 * w) / p.G);
-                    } else {
+                    } else if (t == 32) {
                         mbar_arrive(&s_qfull);
                     }
                 } else {
@@ -564,7 +608,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         }
                     }
                     fence_proxy_async();
-                    mbar_arrive(&s_qfull);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_qfull);
                 }
                 for (int j = g.a; ok && j < g.b; ++j, ++step, item += 2) {
                     const uint32_t v = item + 1, sg = v % STAGES;
@@ -576,31 +621,46 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     if (!all) {
                         uint8_t* tile = ring + sg * Ly::TILE;
                         bool odd = false;
-                        for (int e = t; e < 128 * ATOMS * 8; e += 64) {  // 16 bytes of a row
-                            const int y = e >> 3 & 127, x = x0 + y;
-                            uint4* at = reinterpret_cast<uint4*>(tile + e * 16);
-                            if (x < k.lo || x >= k.hi || !(mask[y >> 5] >> (y & 31) & 1u)) {
-                                *at = make_uint4(0u, 0u, 0u, 0u);
+                        // rows that every row sees, [in0, in1), stay as they are
+                        const int in0 = p.s.window ? k.last - p.s.window + 1 - x0 : 0, in1 = k.first + 1 - x0;
+#pragma unroll 1
+                        for (int e = t; e < 128 * ATOMS; e += 64) {  // 128 bytes of a row
+                            const int y = e & 127, x = x0 + y;
+                            const bool lost = x < k.lo || x >= k.hi || !(mask[y >> 5] >> (y & 31) & 1u);
+                            if (!lost && y >= in0 && y < in1) continue;
+                            uint4* at = reinterpret_cast<uint4*>(tile + e * 128);
+                            if (lost) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) at[i ^ (t & 7)] = make_uint4(0u, 0u, 0u, 0u);  // each lane another bank
                                 continue;
                             }
-                            uint4 u = *at;
-                            if (not_finite2(u.x) || not_finite2(u.y) || not_finite2(u.z) || not_finite2(u.w)) {
-                                odd = true;
-                                uint32_t* z = &u.x;
-                                for (int i = 0; i < 4; ++i) {
-                                    if ((z[i] & 0x7F80u) == 0x7F80u) z[i] &= 0xFFFF0000u;
-                                    if ((z[i] & 0x7F800000u) == 0x7F800000u) z[i] &= 0xFFFFu;
+                            uint4 u[8];
+                            uint32_t z0 = 0, z1 = 0;  // 0, or NaN after a value that is not finite
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                u[i] = at[i ^ (t & 7)];
+                                z0 = zero2(u[i].x, z0), z1 = zero2(u[i].y, z1), z0 = zero2(u[i].z, z0), z1 = zero2(u[i].w, z1);
+                            }
+                            if (!(not_finite2(z0) | not_finite2(z1))) continue;
+                            odd = true;
+#pragma unroll 1
+                            for (int i = 0; i < 8; ++i) {
+                                uint32_t* z = reinterpret_cast<uint32_t*>(at + i);
+                                for (int w = 0; w < 4; ++w) {
+                                    const uint32_t b = not_finite2(z[w]);
+                                    z[w] &= ~((b & 0x8000u ? 0xFFFFu : 0u) | (b & 0x80000000u ? 0xFFFF0000u : 0u));
                                 }
-                                *at = u;
                             }
                         }
                         if (odd) s_odd[seg & 3] = 1;
                         fence_proxy_async();
                     }
-                    mbar_arrive(s_vready + sg);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_vready + sg);
                 }
             }
             if (q_tma && n_q && t == 0 && !mbar_wait(&s_qfull, (n_q - 1) & 1u, kLimit)) fail();
+        }
         }
     }
     // rows of no request
@@ -620,16 +680,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if (rq.pad && rq.n) clear(rq.first, rq.first + rq.n);
         }
     }
-    // the cut tile that starts in this range
-    if (st.any && tid == 0 && !s_abort) {
-        Walk walk(p, st.r, st.kh, st.mt, st.off, st.left);
+    // the cut tile whose first step is in this range
+    if (range.any && tid == 0 && !s_abort) {
+        Walk walk(p, range);
         Segment g, last = {};
         while (walk.next(p, g)) last = g;
         if (last.b > 0 && last.a == 0 && !last.whole()) {
             p.desc[2 * blockIdx.x] = make_int4(last.r, last.kh, last.m0, last.rows);
-            p.desc[2 * blockIdx.x + 1] = make_int4(prefill::ranges_of<OVER>(last, st.left, st.per), 0, 0, 0);
+            p.desc[2 * blockIdx.x + 1] = make_int4(range.ranges, 0, 0, 0);
         }
     }
+    // a range inside a tile that has no whole step adds nothing to it
+    if (range.any && range.from.a > 0 && range.from.a == range.to.a && range.from.r == range.to.r && range.from.kh == range.to.kh &&
+        range.from.mt == range.to.mt && tid < TM)
+        p.ml[2 * static_cast<int64_t>(blockIdx.x) * TM + tid] = make_float2(-INFINITY, 0.f);
     fence_before_sync();
     __syncthreads();
     if (warp == 8) {
@@ -669,10 +733,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Arg
             for (int x = 0; x < N; ++x) {
                 const float y = fmaxf(top, ml[x].x);
                 const float f = top == y ? 1.f : ex2(top - y);
-                const float h = ml[x].x == y ? 1.f : ml[x].x == -INFINITY ? 0.f : ex2(ml[x].x - y);
+                // nothing of a part without a key is read; one whose scores are NaN carries them on
+                const float h = ml[x].x == -INFINITY ? (ml[x].y != ml[x].y ? 1.f : 0.f) : ml[x].x == y ? 1.f : ex2(ml[x].x - y);
                 sum = sum * f + ml[x].y * h;
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = o[e] * f + v[x][e] * h;
+                for (int e = 0; e < E; ++e) o[e] = o[e] * f + (h > 0.f ? v[x][e] * h : 0.f);
                 top = y;
             }
         }
@@ -707,7 +772,7 @@ cudaError_t paged_prefill_tc(const LaunchCtx& c, const bf16* q, const bf16* K, c
                              const int* lens, const int* starts, bf16* out, float* lse, const PrefillShape& s, int fill) {
     using Ly = Lay<D>;
     Args p = {};
-    p.s = s, p.G = s.Hq / s.Hkv, p.least = 4, p.table = table, p.lens = lens, p.starts = starts, p.lse = lse, p.fill = fill;
+    p.s = s, p.G = s.Hq / s.Hkv, p.least = kLeast, p.table = table, p.lens = lens, p.starts = starts, p.lse = lse, p.fill = fill;
     p.status = c.status_word;
     int per_sm = 1;
     cudaError_t e = resident_blocks<prefill_kernel<D>>(c.device, NT, Ly::SMEM, &per_sm);

@@ -1,13 +1,16 @@
-// prefill_plan.cuh -- the work of a prefill call cut into equal ranges, one a block, from
-// lengths in device memory.
+// prefill_plan.cuh -- the work of a prefill call cut into ranges, one a block, from lengths
+// in device memory.
 //
 // The rows of a request and key head are its tokens' query heads, token after token: row
 // m is token m / G, head m % G of the key head.  A tile is TM rows; a step is KT key
-// positions (aligned in the request) against a tile.  The steps of all tiles, request after
-// request, key head after key head, tile after tile, with `over` units in front of each
-// tile for its queries and outputs, are cut into equal ranges; a tile that a range's
-// border cuts leaves partial sums, which a second kernel joins in the order of the ranges.
-// So every block has the same work, whatever the lengths, and a captured call follows them.
+// positions (aligned in the request) against a tile.  A tile's cost is taken as the
+// positions that its last row sees, and a constant for its queries and outputs: a formula
+// whose sums over tiles are one too, so that a thread sums up a request, and a block finds
+// the borders of its range in a few steps, whatever the lengths.  The costs of all tiles,
+// request after request, key head after key head, are cut into equal ranges, the border
+// inside a tile set back to a whole step.  A tile that a border cuts leaves partial sums, which
+// a second kernel joins in the order of the ranges.  So all blocks have the same work but for a
+// step, and a captured call follows the lengths.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -21,19 +24,19 @@ namespace prefill {
 
 struct Args {
     PrefillShape s;
-    int G, least;  // least: units of a range at least
+    int G, least;  // least: cost of a range at least
     const int *table, *lens, *starts;
     float* lse;
     int fill;
     float* part;   // [blocks][2][TM][D] output sums of cut tiles
     float2* ml;    // [blocks][2][TM] their maxima (to base 2) and sums
-    int4* desc;    // [blocks][2] a cut tile that starts in the block's range: {request, key head, tile, 0}, {ranges, -, -, -}
+    int4* desc;    // [blocks][2] the cut tile whose first step is in the block's range: {request, key head, first row, rows}, {ranges, -, -, -}
     unsigned* status;
 };
 
 // A request's rows and positions made valid.
 struct Request {
-    int first, n, cached;  // its first row of T, its tokens (0: none to do), positions before them
+    int first, n, cached;  // its first row of T, its tokens, positions before them
     int end;               // positions that its table has room for
     bool bad, pad;
     __device__ __forceinline__ Request(const Args& p, int r) {
@@ -55,8 +58,8 @@ struct Keys {
     int first, last;  // positions of the first and the last row
     int lo, hi, k0, k1;
     __device__ __forceinline__ Keys(const Args& p, const Request& q, int m0, int m1) {
-        first = q.cached + m0 / p.G;
-        last = q.cached + (m1 - 1) / p.G;
+        first = q.cached + static_cast<int>(static_cast<unsigned>(m0) / static_cast<unsigned>(p.G));
+        last = q.cached + static_cast<int>(static_cast<unsigned>(m1 - 1) / static_cast<unsigned>(p.G));
         lo = p.s.window ? max(first - p.s.window + 1, 0) : 0;
         hi = min(last + 1, q.end);
         k0 = min(lo, hi) / KT;
@@ -74,35 +77,41 @@ struct Segment {
     __device__ __forceinline__ bool whole() const { return a == 0 && b == steps; }
 };
 
+// A border of a range: step a of tile mt of a request and key head.
+struct Place {
+    int r, kh, mt, a;
+};
+struct Range {
+    Place from, to;     // to.r = R: the end of all
+    int ranges;         // that tile `to` touches, from this block on
+    int any;
+};
+
 // Walks over a range; every role of the block has its own.
-template <int TM, int KT, int OVER>
+template <int TM, int KT>
 struct Walk {
-    int r, kh, mt, off;   // the place: units into tile mt
-    int64_t left;         // units still to do
+    Place at, to;
     Request q;
-    __device__ __forceinline__ Walk(const Args& p, int r_, int kh_, int mt_, int off_, int64_t left_)
-        : r(r_), kh(kh_), mt(mt_), off(off_), left(left_), q(p, r_) {}
+    __device__ __forceinline__ Walk(const Args& p, const Range& g) : at(g.from), to(g.to), q(p, g.from.r) {}
     // The next segment with a step; false at the range's end.
     __device__ __forceinline__ bool next(const Args& p, Segment& g) {
-        while (left > 0) {
-            const int rows = q.rows(p), m0 = mt * TM;
+        while (at.r < p.s.R) {
+            const int rows = q.rows(p), m0 = at.mt * TM;
+            const bool last = at.r == to.r && at.kh == to.kh && at.mt == to.mt;
             const Keys<KT> k(p, q, m0, min(m0 + TM, rows));
-            const int units = k.k1 - k.k0 + OVER;
-            const int take = static_cast<int>(min(static_cast<int64_t>(units - off), left));
-            g = {r, kh, m0, rows, max(off - OVER, 0), off + take - OVER, k.k1 - k.k0};
-            left -= take;
-            off += take;
-            if (off == units && left > 0) {  // on to the next tile
-                off = 0;
-                if (++mt == tile_count<TM>(rows)) {
-                    mt = 0;
-                    if (++kh == p.s.Hkv) {
-                        kh = 0;
-                        do {
-                            ++r;
-                            if (r >= p.s.R) return g.b > g.a ? (left = 0, true) : false;
-                            q = Request(p, r);
-                        } while (q.rows(p) == 0);
+            g = {at.r, at.kh, m0, rows, at.a, last ? to.a : k.k1 - k.k0, k.k1 - k.k0};
+            if (last) {
+                at.r = p.s.R;
+            } else {  // on to the next tile
+                at.a = 0;
+                if ((++at.mt) * static_cast<int64_t>(TM) >= rows) {
+                    at.mt = 0;
+                    if (++at.kh == p.s.Hkv) {
+                        at.kh = 0;
+                        while (++at.r < p.s.R) {
+                            q = Request(p, at.r);
+                            if (q.rows(p)) break;
+                        }
                     }
                 }
             }
@@ -112,176 +121,140 @@ struct Walk {
     }
 };
 
-// Block-wide inclusive sums over threads (s holds NT words).
-template <int NT>
-__device__ __forceinline__ void block_sums(int64_t x, int64_t* s) {
-    const int tid = threadIdx.x, lane = tid & 31;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    s[tid] = x;
-    __syncthreads();
-    int64_t before = 0;
-    for (int w = 0; w < tid / 32; ++w) before += s[w * 32 + 31];
-    __syncthreads();
-    s[tid] = x + before;
-    __syncthreads();
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // of numbers that mostly have 32 bits
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
 }
 
-// Number of entries of s[0 .. NT) that are <= x; s does not decrease.
-template <int NT>
-__device__ __forceinline__ int count_to(const int64_t* s, int64_t x) {
-    int lo = 0, hi = NT;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s[mid] <= x) lo = mid + 1;
-        else hi = mid;
+// The cost of a request's tiles: cost(mt) of the tiles before mt.
+template <int TM, int KT>
+struct Cost {
+    // Of a tile's queries, outputs and of the step that its border cuts: as much as 1.5 steps.
+    static constexpr int kTile = KT + KT / 2;
+    int tiles, each;      // positions from a tile to the next
+    int64_t base, limit;  // cost of tile i: min(base + each i, limit)
+    int grow;             // tiles whose cost grows
+    __device__ __forceinline__ Cost(const Args& p, const Request& q) {
+        tiles = tile_count<TM>(q.rows(p));
+        each = max(TM / p.G, 1);
+        base = static_cast<int64_t>(q.cached) + each + kTile;
+        limit = p.s.window ? static_cast<int64_t>(p.s.window) + each + kTile : INT64_MAX;
+        grow = p.s.window == 0 ? tiles : limit <= base ? 0 : static_cast<int>(min(divide(limit - base, each) + 1, static_cast<int64_t>(tiles)));
     }
-    return lo;
-}
-
-// Where a block's range starts, found by all its threads from the lengths.
-struct Start {
-    int r, kh, mt, off;
-    int64_t left, per;   // units of the range; of every range but the last
-    bool any;
+    __device__ __forceinline__ int64_t operator()(int mt) const {
+        const int64_t g = min(mt, grow);
+        return g * base + g * (g - 1) / 2 * each + (mt > grow ? (mt - grow) * limit : 0);
+    }
 };
 
-template <int TM, int KT, int OVER, int NT>
+// Finds a block's range, by all its NT threads.
+template <int TM, int KT, int NT>
 struct Planner {
-    int64_t tiles[NT], units[NT];  // inclusive sums: of tiles over chunks of requests, of units over chunks of tiles
-    Start start;
+    int64_t sums[NT];     // inclusive sums of costs over chunks of requests
+    int64_t warps[NT / 32];
+    Range range;
+    int64_t tile_end;     // cost up to the end of tile range.to
 
-    __device__ __forceinline__ static int chunk(int n) { return (n + NT - 1) / NT; }
-
-    // Request and tile of tile number i (below the number of tiles).
-    __device__ __forceinline__ void tile_at(const Args& p, int64_t i, int& r, int& mt) const {
-        const int c = count_to<NT>(tiles, i);
-        int64_t rest = i - (c ? tiles[c - 1] : 0);
-        for (r = min(c * chunk(p.s.R), p.s.R - 1); r < p.s.R - 1; ++r) {
-            const int n = tile_count<TM>(Request(p, r).rows(p));
-            if (rest < n) break;
-            rest -= n;
-        }
-        mt = static_cast<int>(rest);
-    }
-    __device__ __forceinline__ static int units_of(const Args& p, const Request& q, int mt) {
-        const int rows = q.rows(p);
-        const Keys<KT> k(p, q, mt * TM, min(mt * TM + TM, rows));
-        return k.k1 - k.k0 + OVER;
-    }
-    // Units of the tiles before number i, by a warp.
-    __device__ __forceinline__ int64_t before(const Args& p, int64_t i, int64_t per) const {
-        const int64_t c = i / per;
-        int64_t x = 0;
-        for (int64_t j = c * per + (threadIdx.x & 31); j < i; j += 32) {
-            int r, mt;
-            tile_at(p, j, r, mt);
-            x += units_of(p, Request(p, r), mt);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        return x + (c ? units[c - 1] : 0);
-    }
-    // The tile with unit x of the sums over tiles, and the units before it, by a warp.
-    __device__ __forceinline__ int64_t find(const Args& p, int64_t x, int64_t count, int64_t per, int64_t& base) const {
-        const int c = count_to<NT>(units, x), lane = threadIdx.x & 31;
-        base = c ? units[c - 1] : 0;
-        for (int64_t i = c * per;; i += 32) {
-            int64_t u = 0;
-            if (i + lane < count) {
-                int r, mt;
-                tile_at(p, i + lane, r, mt);
-                u = units_of(p, Request(p, r), mt);
+    // The border at cost u < total, by a warp; `end` gets the cost up to its tile's end.
+    __device__ __forceinline__ Place locate(const Args& p, int64_t u, int64_t& end) const {
+        const int lane = threadIdx.x & 31, each = (p.s.R + NT - 1) / NT;
+        int c = __popc(__ballot_sync(0xffffffffu, lane < NT / 32 && sums[min(lane, NT / 32 - 1) * 32 + 31] <= u));
+        c = min(c, NT / 32 - 1);
+        c = 32 * c + min(__popc(__ballot_sync(0xffffffffu, sums[32 * c + lane] <= u)), 31);
+        int64_t before = c ? sums[c - 1] : 0, total = 0;
+        int r = c * each;
+        for (;; r += 32) {  // 32 requests at once
+            int64_t x = 0;
+            if (r + lane < min((c + 1) * each, p.s.R)) {
+                const Cost<TM, KT> cost(p, Request(p, r + lane));
+                x = cost(cost.tiles) * p.s.Hkv;
             }
+            int64_t s = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, u, o);
-                if (lane >= o) u += y;
+                const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += y;
             }
-            const int n = __popc(__ballot_sync(0xffffffffu, base + u <= x));
-            const int64_t skip = __shfl_sync(0xffffffffu, u, n ? n - 1 : 0);
-            if (n) base += skip;
-            if (n < 32 || i + 32 >= count) return min(i + n, count - 1);
+            const int n = __popc(__ballot_sync(0xffffffffu, before + s <= u));
+            if (n == 32 && r + 32 < (c + 1) * each) {
+                before += __shfl_sync(0xffffffffu, s, 31);
+                continue;
+            }
+            const int i = min(n, 31);
+            total = __shfl_sync(0xffffffffu, x, i);
+            before += __shfl_sync(0xffffffffu, s, i) - total;
+            r = min(r + i, p.s.R - 1);
+            break;
         }
+        const Request q(p, r);
+        const Cost<TM, KT> cost(p, q);
+        const int64_t one = max(cost(cost.tiles), static_cast<int64_t>(1));
+        const int64_t kh = min(divide(u - before, one), static_cast<int64_t>(p.s.Hkv - 1));
+        const int64_t x = u - before - kh * one;
+        int lo = 0, hi = max(cost.tiles, 1);  // cost(lo) <= x < cost(hi)
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32;
+            const int n = __popc(__ballot_sync(0xffffffffu, lo + (lane + 1) * static_cast<int64_t>(step) < hi && cost(lo + (lane + 1) * step) <= x));
+            lo += n * step;
+            hi = min(hi, lo + step);
+        }
+        const int rows = q.rows(p);
+        const Keys<KT> k(p, q, lo * TM, min(lo * TM + TM, rows));
+        const int64_t c0 = cost(lo), c1 = cost(lo + 1);
+        end = before + kh * one + c1;
+        const int a = static_cast<int>(divide((x - c0) * (k.k1 - k.k0), max(c1 - c0, static_cast<int64_t>(1))));
+        return {r, static_cast<int>(kh), lo, a};
     }
 
-    // Fills `start`, by all threads.
     __device__ __forceinline__ void run(const Args& p) {
-        const int tid = threadIdx.x;
-        const int each = chunk(p.s.R);
-        int64_t mine = 0;
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, each = (p.s.R + NT - 1) / NT;
+        int64_t x = 0;
         bool bad = false;
         for (int i = 0; i < each; ++i) {
             const int r = tid * each + i;
             if (r >= p.s.R) break;
             const Request q(p, r);
             bad |= q.bad;
-            mine += tile_count<TM>(q.rows(p));
+            const Cost<TM, KT> cost(p, q);
+            x += cost(cost.tiles);
         }
+        x *= p.s.Hkv;
         if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
-        block_sums<NT>(mine, tiles);
-        const int64_t count = tiles[NT - 1], per = (count + NT - 1) / NT;
-        mine = 0;
-        if (static_cast<int64_t>(tid) * per < count) {
-            int r, mt;
-            tile_at(p, tid * per, r, mt);
-            Request q(p, r);
-            int n = tile_count<TM>(q.rows(p));
-            const int64_t stop = min(count, (tid + 1) * per);
-            for (int64_t i = tid * per;;) {
-                mine += units_of(p, q, mt);
-                if (++i == stop) break;
-                if (++mt == n) {
-                    mt = 0;
-                    do {
-                        q = Request(p, ++r);
-                        n = tile_count<TM>(q.rows(p));
-                    } while (n == 0 && r < p.s.R - 1);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) warps[warp] = x;
+        __syncthreads();
+        int64_t before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            const int64_t y = warps[w];
+            before += w < warp ? y : 0;
+            total += y;
+        }
+        sums[tid] = x + before;
+        __syncthreads();
+        if (warp < 2) {  // one finds the first border, one the last
+            const int64_t per = max(divide(total + gridDim.x - 1, gridDim.x), static_cast<int64_t>(p.least));
+            const int64_t u = per * (blockIdx.x + warp);
+            Place at = {p.s.R, 0, 0, 0};
+            int64_t end = 0;
+            if (u < total) at = locate(p, u, end);
+            if (lane == 0) {
+                if (warp == 0) {
+                    range.from = at;
+                    range.any = u < total;
+                } else {
+                    range.to = at;
+                    range.ranges = u < total ? static_cast<int>(divide(end - 1, per)) - static_cast<int>(blockIdx.x) + 1 : 0;
                 }
             }
-        }
-        block_sums<NT>(mine, units);
-        if (tid < 32) {
-            const int64_t total = units[NT - 1] * p.s.Hkv;
-            const int64_t range = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(p.least));
-            const int64_t u0 = range * blockIdx.x;
-            Start st = {};
-            st.per = range;
-            st.any = u0 < total;
-            if (st.any) {
-                st.left = min(range, total - u0);
-                int64_t base;
-                int r, mt;
-                tile_at(p, find(p, u0 / p.s.Hkv, count, per, base), r, mt);  // a tile of the request
-                const int c = r / each;
-                int64_t first = c ? tiles[c - 1] : 0;  // its first tile's number
-                for (int i = c * each; i < r; ++i) first += tile_count<TM>(Request(p, i).rows(p));
-                const int64_t w0 = before(p, first, per);
-                const int64_t w1 = before(p, first + tile_count<TM>(Request(p, r).rows(p)), per);
-                const int64_t in = u0 - w0 * p.s.Hkv, one = w1 - w0;
-                st.kh = static_cast<int>(in / one);
-                const int64_t x = w0 + in - st.kh * one;
-                const int64_t tile = find(p, x, count, per, base);
-                st.r = r;
-                st.mt = static_cast<int>(tile - first);
-                st.off = static_cast<int>(x - base);
-            }
-            if (tid == 0) start = st;
         }
         __syncthreads();
     }
 };
-
-// Ranges that the tile of segment g touches when it starts in this block's range: `done` units of
-// the range were taken with the segment's last one.
-template <int OVER>
-__device__ __forceinline__ int ranges_of(const Segment& g, int64_t done, int64_t per) {
-    const int64_t end = done + (g.steps - g.b);  // the tile's end, in units from the range's start
-    return static_cast<int>((end + per - 1) / per);
-}
 
 }  // namespace prefill
 }  // namespace la
