@@ -7,8 +7,8 @@
 // 128 key positions.  Warps:
 //   0-3, 4-7  softmax of subtile 0 and 1, a row a thread, and the rows' outputs
 //   8         every matrix product, issued by one thread
-//   9         keys and values by TMA, a page a lane, into a ring of tiles
-//   10, 11    queries, and the values of tiles that some row sees only in part
+//   9, 10     keys and values by TMA, page by page, into a ring of tiles
+//   12 to 15  queries, and the values of tiles that some row sees only in part
 // S = Q K^T goes to tensor memory, a thread turns its row's 128 scores into weights there, and
 // O += P V reads the weights from tensor memory.  The two subtiles take turns: while one's
 // scores become weights, the tensor core works for the other.
@@ -19,7 +19,7 @@
 // sums of the unrounded ones.
 //
 // Values that a row does not see have weight 0, but 0 times an infinity or NaN is no 0.
-// So in tiles that some row sees in part, warps 10 and 11 clear the value rows that no row
+// So in tiles that some row sees in part, warps 12 to 15 clear the value rows that no row
 // sees, and replace what is not finite in the others by 0; a row that does see such an
 // element gets NaN in that column at the end.
 #include <cuda_bf16.h>
@@ -44,7 +44,8 @@ using prefill::Request;
 using prefill::Segment;
 using bf16 = __nv_bfloat16;
 
-constexpr int TM = 256, KT = 128, NT = 384;
+constexpr int TM = 256, KT = 128, NT = 512;
+constexpr int kAux = 128;             // threads of warps 12 to 15
 constexpr int kLeast = 6 * KT;        // cost of a range at least, so that small calls are not cut too fine
 constexpr int kMasks = 16;            // steps whose masks are kept: more than the loader is ahead of the softmax
 constexpr float kSlack = 8.f;         // log2 by which a score may pass the maximum kept
@@ -225,19 +226,19 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     extern __shared__ uint8_t sm_raw[];
     __shared__ uint64_t s_full[STAGES], s_empty[STAGES], s_vready[STAGES];
     __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_end;
-    __shared__ uint32_t s_mask[kMasks][4];   // positions of a step that are on a page, a bit each
+    __shared__ uint32_t s_mask[2][kMasks][4];  // positions of a step that are on a page, a bit each, as keys' and values' loader saw them
     __shared__ volatile int s_odd[4];        // by segment: a value that was not finite was replaced
     __shared__ volatile int s_abort;
     __shared__ uint32_t s_tmem;
     __shared__ prefill::Range s_range;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* ring = sm + Ly::Q;
-    const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) < 4 ? (tid >> 5) + 8 : (tid >> 5) - 4;  // by role
+    const int tid = threadIdx.x, lane = tid & 31, warp = (tid >> 5) ^ 8;  // by role
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (tid == 0) {
-        for (int i = 0; i < STAGES; ++i) mbar_init(s_full + i, 1), mbar_init(s_empty + i, 1), mbar_init(s_vready + i, 2);
-        mbar_init(&s_qfull, 2);
+        for (int i = 0; i < STAGES; ++i) mbar_init(s_full + i, 1), mbar_init(s_empty + i, 1), mbar_init(s_vready + i, kAux / 32);
+        mbar_init(&s_qfull, kAux / 32);
         mbar_init(&s_qempty, 1);
         mbar_init(&s_end, 1);
         for (int w = 0; w < 2; ++w) mbar_init(s_sfull + w, 1), mbar_init(s_pfull + w, 4), mbar_init(s_odone + w, 1);
@@ -270,11 +271,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     };
     const auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
-    // The launch's 168 registers a thread become 208 for the softmax and 88 for the rest.
+    // The launch's 128 registers a thread become 192 for the softmax and 64 for the rest.
     if (range.any) {
         if (warp < 8) {
             // ---------------------------------------------------------------- softmax
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
             Walk walk(p, range);
             Segment g;
             const int w = warp >> 2, row = 32 * (warp & 3) + lane;
@@ -301,7 +302,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll
                     for (int i = 0; i < 4; ++i) ld32(ts + 32 * i, s + 32 * i);
                     const int x0 = (k0 + j) * KT;
-                    const uint32_t* mask = s_mask[step % kMasks];
+                    const uint32_t* mask = s_mask[0][step % kMasks];
                     const uint32_t m0 = mask[0], m1 = mask[1], m2 = mask[2], m3 = mask[3];
                     const bool all = x0 + KT - 1 <= mine.k.first && (p.s.window == 0 || x0 > mine.k.last - p.s.window) &&
                                      (m0 & m1 & m2 & m3) == 0xFFFFFFFFu;
@@ -412,7 +413,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 fence_before_sync();  // the outputs' columns are free with the next arrival
             }
         } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
             Walk walk(p, range);
             Segment g;
             if (warp == 8) {
@@ -443,9 +444,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 for (int j = g.a; j < g.b; ++j, item += 2) {
                     const uint32_t sv = (item + 1) % STAGES, sk = (item + 2) % STAGES;
                     const bool more = j + 1 < g.b;
-                    // the values of this step and the keys of the next are mostly here before the weights
+                    // the values of this step and the keys of the next, mostly here before the weights
                     if (!(ok = warp_wait(s_vready + sv, Ly::value_turn(item + 1)))) break;
-                    if (more && !(ok = warp_wait(s_full + sk, (item + 2) / STAGES))) break;
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         const Part& part = w ? part1 : part0;
@@ -473,57 +473,66 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if (elect()) mma_commit(&s_end);
             __syncwarp();
             if (!mbar_wait(&s_end, 0, kLimit)) fail();
-        } else if (warp == 9) {
-            // ---------------------------------------------------------------- keys and values
+        } else if (warp < 11) {
+            // ---------------------------------------------------------------- keys (warp 9), values (warp 10)
+            const int kv = warp - 9;
+            const bf16* pool = kv ? V : K;
+            const CUtensorMap* map = kv ? &vmap : &kmap;
             const int log2p = p.s.log2p, page = 1 << log2p, off_mask = page - 1;
             const int rows = min(page, KT);              // of a copy
-            const int copies = KT / rows;                // of a tile and atom column
-            uint32_t item = 0, step = 0, issued = 0;
+            const int copies = KT / rows;                // of a tile
+            uint32_t it = kv, step = 0;                  // the ring's tiles: K, V, K, V, ...
             bool ok = true, bad = false;
             while (ok && walk.next(p, g)) {
                 const Request rq(p, g.r);
                 const Keys<KT> k(p, rq, g.m0, min(g.m0 + TM, g.rows));
                 const int* table = p.table + static_cast<int64_t>(g.r) * p.s.max_pages;
-                const auto page_of = [&](int x) {  // the page of position x < end, or -1
-                    const int i = table[x >> log2p];
-                    const bool in = static_cast<unsigned>(i) < static_cast<unsigned>(p.s.num_pages);
-                    return in ? i : -1;
+                // Page i of the request; -1 if it is none of the pool, -2 if no row sees a position of it.
+                const auto page_of = [&](int64_t i) {
+                    if ((i << log2p) >= k.hi || ((i + 1) << log2p) <= k.lo) return -2;
+                    const int id = table[i];
+                    return static_cast<unsigned>(id) < static_cast<unsigned>(p.s.num_pages) ? id : -1;
                 };
-                const int mine = kv_tma ? lane % copies : 0, atom = kv_tma ? lane / copies : 0;  // the lane's copy of a tile
-                const auto fetch = [&](int j) {
-                    const int x = (k.k0 + j) * KT + mine * rows;
-                    return kv_tma && j < g.b && x < k.hi ? page_of(x) : -2;
-                };
-                int id = fetch(g.a);
-                for (int j = g.a; ok && j < g.b; ++j, ++step, item += 2) {
-                    const int x0 = (k.k0 + j) * KT, x = x0 + mine * rows, now = id;
-                    id = fetch(j + 1);
+                // Page numbers are fetched 32 at a time, a group ahead.
+                int group = ((k.k0 + g.a) * KT >> log2p) >> 5;
+                int now = -2, next = -2;
+                if (kv_tma) now = page_of(32ll * group + lane), next = page_of(32ll * group + 32 + lane);
+                for (int j = g.a; j < g.b; ++j, ++step, it += 2) {
+                    const int x0 = (k.k0 + j) * KT, first = x0 >> log2p;
+                    const uint32_t sg = it % STAGES;
                     if (kv_tma) {
-                        const bool copy = now >= 0 && lane < copies * ATOMS;
-                        bad |= now == -1;
-                        const unsigned lost = __ballot_sync(0xffffffffu, now == -1) & (copies == 32 ? 0xFFFFFFFFu : (1u << copies) - 1u);
-                        const unsigned who = __ballot_sync(0xffffffffu, copy);
-                        for (int kv = 0; ok && kv < 2; ++kv) {
-                            const uint32_t it = item + kv, sg = it % STAGES;
-                            if (!(ok = warp_wait(s_empty + sg, it / STAGES + 1))) break;
-                            if (kv == 0 && lane < 4) {  // 32 positions a word: those on a lost page, or past the table, are off
-                                uint32_t m = 0xFFFFFFFFu;
-                                for (int i = 0; i < 32 && (lost || x0 + KT > rq.end); ++i) {
-                                    const int y = 32 * lane + i;
-                                    if ((lost >> (y / rows) & 1u) || x0 + y >= rq.end) m &= ~(1u << i);
-                                }
-                                s_mask[step % kMasks][lane] = m;
+                        if (first >> 5 != group) {
+                            group = first >> 5;
+                            now = next;
+                            next = page_of(32ll * group + 32 + lane);
+                        }
+                        const uint32_t in = ((1u << copies) - 1u) << (first & 31);
+                        const uint32_t who = __ballot_sync(0xffffffffu, now >= 0) & in;
+                        const uint32_t lost = (__ballot_sync(0xffffffffu, now == -1) & in) >> (first & 31);
+                        bad |= lost != 0;
+                        if (!(ok = warp_wait(s_empty + sg, it / STAGES + 1))) break;
+                        if (lane < 4) {  // 32 positions a word: those on a lost page, or past the table, are off
+                            uint32_t m = 0xFFFFFFFFu;
+                            for (int i = 0; i < 32 && (lost || x0 + KT > rq.end); ++i) {
+                                const int y = 32 * lane + i;
+                                if ((lost >> (y / rows) & 1u) || x0 + y >= rq.end) m &= ~(1u << i);
                             }
-                            __syncwarp();
-                            if (lane == 0) {
-                                if (who) mbar_arrive_expect_tx(s_full + sg, __popc(who) * rows * 128);
-                                else mbar_arrive(s_full + sg);
+                            s_mask[kv][step % kMasks][lane] = m;
+                        }
+                        __syncwarp();
+                        const bool one = elect();
+                        if (one) {
+                            if (who) mbar_arrive_expect_tx(s_full + sg, __popc(who) * rows * ATOMS * 128);
+                            else mbar_arrive(s_full + sg);
+                        }
+                        uint8_t* dst = ring + sg * Ly::TILE;
+                        for (int c = 0; c < copies; ++c, dst += rows * 128) {
+                            const int to = __shfl_sync(0xffffffffu, now, (first + c) & 31);
+                            if (to >= 0 && one) {
+#pragma unroll
+                                for (int a = 0; a < ATOMS; ++a)
+                                    tma_load_3d(dst + a * kAtom, map, s_full + sg, 64 * a, x0 & off_mask, to * p.s.Hkv + g.kh);
                             }
-                            __syncwarp();
-                            if (copy)
-                                tma_load_3d(ring + sg * Ly::TILE + atom * kAtom + mine * rows * 128, kv ? &vmap : &kmap, s_full + sg,
-                                            atom * 64, x & off_mask, now * p.s.Hkv + g.kh);
-                            issued = it + 1;
                         }
                     } else {
                         // pages of fewer than eight positions: four rows a lane, 16 bytes at a time
@@ -532,42 +541,39 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int y = x0 + 32 * i + lane;
-                            ids[i] = y < k.hi ? page_of(y) : -2;
+                            ids[i] = page_of(y >> log2p);
                             bad |= ids[i] == -1;
                             mask[i] = __ballot_sync(0xffffffffu, ids[i] != -1 && y < rq.end);
                         }
-                        for (int kv = 0; ok && kv < 2; ++kv) {
-                            const uint32_t it = item + kv, sg = it % STAGES;
-                            if (!(ok = warp_wait(s_empty + sg, it / STAGES + 1))) break;
-                            const uint32_t dst = smem_u32(ring + sg * Ly::TILE);
+                        if (!(ok = warp_wait(s_empty + sg, it / STAGES + 1))) break;
+                        const uint32_t dst = smem_u32(ring + sg * Ly::TILE);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int y = 32 * i + lane;
-                                const int64_t src = ids[i] < 0 ? 0 : (((static_cast<int64_t>(ids[i]) * p.s.Hkv + g.kh) << log2p) + ((x0 + y) & off_mask)) * D;
-                                for (int e = 0; e < DP / 8; ++e) {
-                                    const bool on = ids[i] >= 0 && e < D / 8;
-                                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (e >> 3) * kAtom + swz(y, e & 7)),
-                                                 "l"((kv ? V : K) + (on ? src + e * 8 : 0)), "r"(on ? 16 : 0)
-                                                 : "memory");
-                                }
+                        for (int i = 0; i < 4; ++i) {
+                            const int y = 32 * i + lane;
+                            const int64_t src = ids[i] < 0 ? 0 : (((static_cast<int64_t>(ids[i]) * p.s.Hkv + g.kh) << log2p) + ((x0 + y) & off_mask)) * D;
+                            for (int e = 0; e < DP / 8; ++e) {
+                                const bool on = ids[i] >= 0 && e < D / 8;
+                                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (e >> 3) * kAtom + swz(y, e & 7)),
+                                             "l"(pool + (on ? src + e * 8 : 0)), "r"(on ? 16 : 0)
+                                             : "memory");
                             }
-                            asm volatile("cp.async.wait_all;" ::: "memory");
-                            if (kv == 0 && lane == 0)
-                                for (int i = 0; i < 4; ++i) s_mask[step % kMasks][i] = mask[i];
-                            fence_proxy_async();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(s_full + sg);
                         }
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        if (lane == 0)
+                            for (int i = 0; i < 4; ++i) s_mask[kv][step % kMasks][i] = mask[i];
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(s_full + sg);
                     }
                 }
             }
             if (bad) atomicOr(p.status, kStatusBadIndex);
-            // copies under way end before the block does
-            for (uint32_t it = issued > STAGES ? issued - STAGES : 0; it < issued; ++it)
-                if (!mbar_wait(s_full + it % STAGES, it / STAGES & 1u, kLimit)) fail();
-        } else {
+            // copies under way end before the block does: the last ones of each stage (it is the first tile not issued)
+            for (uint32_t i = it > 2 * STAGES ? it - 2 * STAGES : kv; i < it; i += 2)
+                if (i + STAGES >= it && !mbar_wait(s_full + i % STAGES, i / STAGES & 1u, kLimit)) fail();
+        } else if (warp >= 12) {
             // ---------------------------------------------------------------- queries, values seen in part
-            const int t = 32 * (warp - 10) + lane;
+            const int t = 32 * (warp - 12) + lane;
             uint32_t item = 0, n_q = 0, step = 0;
             bool ok = true;
             for (int seg = 0; ok && walk.next(p, g); ++seg) {
@@ -579,30 +585,30 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 const int subs = g.rows - g.m0 > 128 ? 2 : 1;
                 if (q_tma) {
                     if (t == 0) {
-                        mbar_arrive_expect_tx(&s_qfull, subs * Ly::TILE);  // (the second of the two arrivals is warp 11's)
+                        mbar_arrive_expect_tx(&s_qfull, subs * Ly::TILE);  // (one of the barrier's arrivals, the others are the other warps')
                         for (int w = 0; w < subs; ++w)
                             for (int a = 0; a < ATOMS; ++a)
                                 tma_load_3d(sm + w * Ly::TILE + a * kAtom, &qmap, &s_qfull, 64 * a, g.kh * p.G, rq.first + (g.m0 + 128 * w) / p.G);
-                    } else if (t == 32) {
+                    } else if (lane == 0) {
                         mbar_arrive(&s_qfull);
                     }
                 } else {
                     // any number of heads, or a negative scale: 16 bytes at a time, the sign turned here
                     const uint32_t flip = p.s.scale < 0.f ? 0x80008000u : 0u;
                     constexpr int CH = DP / 8;
-                    for (int i0 = t; i0 < subs * 128 * CH; i0 += 64 * 8) {
-                        uint4 x[8];
+                    for (int i0 = t; i0 < subs * 128 * CH; i0 += kAux * 4) {
+                        uint4 x[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int e = i0 + 64 * i, y = e / CH, ch = e % CH, m = g.m0 + y;
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = i0 + kAux * i, y = e / CH, ch = e % CH, m = g.m0 + y;
                             x[i] = make_uint4(0u, 0u, 0u, 0u);
                             if (m < g.rows && ch < D / 8)
                                 x[i] = *reinterpret_cast<const uint4*>(
                                     q + ((static_cast<int64_t>(rq.first) + m / p.G) * p.s.Hq + static_cast<int64_t>(g.kh) * p.G + m % p.G) * D + ch * 8);
                         }
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int e = i0 + 64 * i, y = e / CH, ch = e % CH;
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = i0 + kAux * i, y = e / CH, ch = e % CH;
                             x[i].x ^= flip, x[i].y ^= flip, x[i].z ^= flip, x[i].w ^= flip;
                             *reinterpret_cast<uint4*>(sm + (y >> 7) * Ly::TILE + (ch >> 3) * kAtom + swz(y & 127, ch & 7)) = x[i];
                         }
@@ -615,7 +621,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     const uint32_t v = item + 1, sg = v % STAGES;
                     if (!(ok = warp_wait(s_full + sg, v / STAGES))) break;
                     const int x0 = (k.k0 + j) * KT;
-                    const uint32_t* mask = s_mask[step % kMasks];
+                    const uint32_t* mask = s_mask[1][step % kMasks];
                     const bool all = x0 + KT - 1 <= k.first && (p.s.window == 0 || x0 > k.last - p.s.window) &&
                                      (mask[0] & mask[1] & mask[2] & mask[3]) == 0xFFFFFFFFu;
                     if (!all) {
@@ -624,7 +630,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         // rows that every row sees, [in0, in1), stay as they are
                         const int in0 = p.s.window ? k.last - p.s.window + 1 - x0 : 0, in1 = k.first + 1 - x0;
 #pragma unroll 1
-                        for (int e = t; e < 128 * ATOMS; e += 64) {  // 128 bytes of a row
+                        for (int e = t; e < 128 * ATOMS; e += kAux) {  // 128 bytes of a row
                             const int y = e & 127, x = x0 + y;
                             const bool lost = x < k.lo || x >= k.hi || !(mask[y >> 5] >> (y & 31) & 1u);
                             if (!lost && y >= in0 && y < in1) continue;
@@ -655,6 +661,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         if (odd) s_odd[seg & 3] = 1;
                         fence_proxy_async();
                     }
+                    // and the next step's keys, so that the products wait once
+                    if (j + 1 < g.b && !(ok = warp_wait(s_full + (v + 1) % STAGES, (v + 1) / STAGES))) break;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_vready + sg);
                 }
