@@ -42,6 +42,7 @@ using prefill::Args;
 using prefill::Keys;
 using prefill::Request;
 using prefill::Segment;
+using prefill::token_of;
 using bf16 = __nv_bfloat16;
 
 constexpr int TM = 256, KT = 128, NT = 512;
@@ -117,6 +118,17 @@ __device__ __forceinline__ void ld_wait(float* v) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 128; ++i) asm volatile("" : "+f"(v[i]));
+}
+// 32 bytes of a thread, at a 32-byte boundary if `wide`.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                     "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
 }
 // 16 words of the thread's row, not waited for.
 __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* v) {
@@ -269,7 +281,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         if (e == 2) fail();
         return e == 0;
     };
-    const auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    const auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1u))) return true;
+        return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
+    };
 
     // The launch's 128 registers a thread become 192 for the softmax and 64 for the rest.
     if (range.any) {
@@ -281,6 +296,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             const int w = warp >> 2, row = 32 * (warp & 3) + lane;
             const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's quarter of the lanes
             const uint32_t ts = tm + 128 * w + lanes, to = tm + Ly::T_O + DP * w + lanes;
+            const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
             const float c = fabsf(p.s.scale) * 1.4426950408889634f;
             uint32_t n_s = 0, n_o = 0, step = 0;  // phases seen, steps of the block
             for (int seg = 0; walk.next(p, g); ++seg) {
@@ -290,7 +306,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 const Part mine(p, rq, g, k0, w);
                 const int m = g.m0 + 128 * w + row;
                 const bool live = row < mine.rows;
-                const int pos = rq.cached + m / p.G;              // of the row
+                const int pos = rq.cached + token_of(p, m);              // of the row
                 const int from = p.s.window ? pos - p.s.window : -1;  // it sees positions past this one
                 float top = -INFINITY, sum = 0.f;
                 bool ok = true;
@@ -373,7 +389,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 const int slot = 2 * blockIdx.x + (g.a == 0 ? 1 : 0);
                 const bool good = sum > 0.f || sum != sum;
                 const float inv = !whole ? 1.f : good ? 1.f / sum : 0.f;
-                const int64_t at = (static_cast<int64_t>(rq.first) + m / p.G) * p.s.Hq + static_cast<int64_t>(g.kh) * p.G + m % p.G;
+                const int token = token_of(p, m);
+                const int64_t at = (static_cast<int64_t>(rq.first) + token) * p.s.Hq + static_cast<int64_t>(g.kh) * p.G + (m - token * p.G);
                 float* part = p.part + (static_cast<int64_t>(slot) * TM + 128 * w + row) * D;
 #pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
@@ -393,16 +410,22 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             if (bits >> x & 1u) o[x] = __uint_as_float(0x7FFFFFFFu);
                     }
                     if (live) {
-                    if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(out + at * D + i);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            dst[x] = make_uint4(pack_bf16(o[8 * x] * inv, o[8 * x + 1] * inv), pack_bf16(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
-                                                pack_bf16(o[8 * x + 4] * inv, o[8 * x + 5] * inv), pack_bf16(o[8 * x + 6] * inv, o[8 * x + 7] * inv));
-                    } else {
+                        for (int x = 0; x < 32; x += 16) {
+                            uint32_t v[8];
+                            if (whole) {
 #pragma unroll
-                        for (int x = 0; x < 32; x += 4) *reinterpret_cast<float4*>(part + i + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-                    }
+                                for (int y = 0; y < 8; ++y) v[y] = pack_bf16(o[x + 2 * y] * inv, o[x + 2 * y + 1] * inv);
+                                store32(out + at * D + i + x, v, wide);
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < 16; h += 8) {
+#pragma unroll
+                                    for (int y = 0; y < 8; ++y) v[y] = __float_as_uint(o[x + h + y]);
+                                    store32(part + i + x + h, v, true);
+                                }
+                            }
+                        }
                     }
                     __syncwarp();
                 }
@@ -588,7 +611,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         mbar_arrive_expect_tx(&s_qfull, subs * Ly::TILE);  // (one of the barrier's arrivals, the others are the other warps')
                         for (int w = 0; w < subs; ++w)
                             for (int a = 0; a < ATOMS; ++a)
-                                tma_load_3d(sm + w * Ly::TILE + a * kAtom, &qmap, &s_qfull, 64 * a, g.kh * p.G, rq.first + (g.m0 + 128 * w) / p.G);
+                                tma_load_3d(sm + w * Ly::TILE + a * kAtom, &qmap, &s_qfull, 64 * a, g.kh * p.G, rq.first + token_of(p, g.m0 + 128 * w));
                     } else if (lane == 0) {
                         mbar_arrive(&s_qfull);
                     }
@@ -602,9 +625,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         for (int i = 0; i < 4; ++i) {
                             const int e = i0 + kAux * i, y = e / CH, ch = e % CH, m = g.m0 + y;
                             x[i] = make_uint4(0u, 0u, 0u, 0u);
+                            const int token = token_of(p, m);
                             if (m < g.rows && ch < D / 8)
                                 x[i] = *reinterpret_cast<const uint4*>(
-                                    q + ((static_cast<int64_t>(rq.first) + m / p.G) * p.s.Hq + static_cast<int64_t>(g.kh) * p.G + m % p.G) * D + ch * 8);
+                                    q + ((static_cast<int64_t>(rq.first) + token) * p.s.Hq + static_cast<int64_t>(g.kh) * p.G + (m - token * p.G)) * D + ch * 8);
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -750,7 +774,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Arg
             }
         }
         const bool good = sum > 0.f || sum != sum;
-        const int64_t at = (static_cast<int64_t>(rq.first) + m / p.G) * p.s.Hq + static_cast<int64_t>(d.y) * p.G + m % p.G;
+        const int token = token_of(p, m);
+        const int64_t at = (static_cast<int64_t>(rq.first) + token) * p.s.Hq + static_cast<int64_t>(d.y) * p.G + (m - token * p.G);
 #pragma unroll
         for (int e = 0; e < E; ++e) out[at * D + lane + 32 * e] = __float2bfloat16_rn(good ? o[e] / sum : 0.f);
         if (lane == 0 && p.lse) p.lse[at] = good ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
@@ -780,7 +805,8 @@ cudaError_t paged_prefill_tc(const LaunchCtx& c, const bf16* q, const bf16* K, c
                              const int* lens, const int* starts, bf16* out, float* lse, const PrefillShape& s, int fill) {
     using Ly = Lay<D>;
     Args p = {};
-    p.s = s, p.G = s.Hq / s.Hkv, p.least = kLeast, p.table = table, p.lens = lens, p.starts = starts, p.lse = lse, p.fill = fill;
+    prefill::set_group(p, s.Hq / s.Hkv);
+    p.s = s, p.least = kLeast, p.table = table, p.lens = lens, p.starts = starts, p.lse = lse, p.fill = fill;
     p.status = c.status_word;
     int per_sm = 1;
     cudaError_t e = resident_blocks<prefill_kernel<D>>(c.device, NT, Ly::SMEM, &per_sm);

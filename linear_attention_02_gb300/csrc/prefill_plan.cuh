@@ -25,6 +25,7 @@ namespace prefill {
 struct Args {
     PrefillShape s;
     int G, least;  // least: cost of a range at least
+    unsigned g_mul, g_shift;  // m / G = m g_mul >> g_shift for m < 2^31 (set_group)
     const int *table, *lens, *starts;
     float* lse;
     int fill;
@@ -33,6 +34,19 @@ struct Args {
     int4* desc;    // [blocks][2] the cut tile whose first step is in the block's range: {request, key head, first row, rows}, {ranges, -, -, -}
     unsigned* status;
 };
+
+// Rounding 2^s / G up with s = 31 + ceil(log2 G) is off by less than 2^(s - 31) / 2^s of a
+// quotient below 2^31, so the product's floor is the quotient's.
+inline void set_group(Args& p, int G) {
+    int log = 0;
+    while ((1 << log) < G) ++log;  // G < 2^30
+    p.G = G;
+    p.g_shift = 31 + log;
+    p.g_mul = static_cast<unsigned>((1ull << p.g_shift) / G + 1);
+}
+__device__ __forceinline__ int token_of(const Args& p, int m) {  // of row m
+    return static_cast<int>(static_cast<uint64_t>(static_cast<unsigned>(m)) * p.g_mul >> p.g_shift);
+}
 
 // A request's rows and positions made valid.
 struct Request {
@@ -58,8 +72,8 @@ struct Keys {
     int first, last;  // positions of the first and the last row
     int lo, hi, k0, k1;
     __device__ __forceinline__ Keys(const Args& p, const Request& q, int m0, int m1) {
-        first = q.cached + static_cast<int>(static_cast<unsigned>(m0) / static_cast<unsigned>(p.G));
-        last = q.cached + static_cast<int>(static_cast<unsigned>(m1 - 1) / static_cast<unsigned>(p.G));
+        first = q.cached + token_of(p, m0);
+        last = q.cached + token_of(p, m1 - 1);
         lo = p.s.window ? max(first - p.s.window + 1, 0) : 0;
         hi = min(last + 1, q.end);
         k0 = min(lo, hi) / KT;
