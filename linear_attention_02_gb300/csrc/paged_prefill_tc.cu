@@ -47,7 +47,6 @@ using bf16 = __nv_bfloat16;
 
 constexpr int TM = 256, KT = 128, NT = 512;
 constexpr int kAux = 128;             // threads of warps 12 to 15
-constexpr int kLeast = 6 * KT;        // cost of a range at least, so that small calls are not cut too fine
 constexpr int kMasks = 16;            // steps whose masks are kept: more than the loader is ahead of the softmax
 constexpr float kSlack = 8.f;         // log2 by which a score may pass the maximum kept
 constexpr uint32_t kAtom = 16384;     // 128 rows x 128 bytes
@@ -805,8 +804,8 @@ cudaError_t paged_prefill_tc(const LaunchCtx& c, const bf16* q, const bf16* K, c
                              const int* lens, const int* starts, bf16* out, float* lse, const PrefillShape& s, int fill) {
     using Ly = Lay<D>;
     Args p = {};
-    prefill::set_group(p, s.Hq / s.Hkv);
-    p.s = s, p.least = kLeast, p.table = table, p.lens = lens, p.starts = starts, p.lse = lse, p.fill = fill;
+    prefill::set_group(p, s.Hq / s.Hkv, TM);
+    p.s = s, p.table = table, p.lens = lens, p.starts = starts, p.lse = lse, p.fill = fill;
     p.status = c.status_word;
     int per_sm = 1;
     cudaError_t e = resident_blocks<prefill_kernel<D>>(c.device, NT, Ly::SMEM, &per_sm);

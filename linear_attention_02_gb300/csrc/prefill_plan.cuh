@@ -24,7 +24,7 @@ namespace prefill {
 
 struct Args {
     PrefillShape s;
-    int G, least;  // least: cost of a range at least
+    int G, tile_tokens;       // query heads a key head; tokens from a tile of rows to the next, 1 at least
     unsigned g_mul, g_shift;  // m / G = m g_mul >> g_shift for m < 2^31 (set_group)
     const int *table, *lens, *starts;
     float* lse;
@@ -37,8 +37,9 @@ struct Args {
 
 // Rounding 2^s / G up with s = 31 + ceil(log2 G) is off by less than 2^(s - 31) / 2^s of a
 // quotient below 2^31, so the product's floor is the quotient's.
-inline void set_group(Args& p, int G) {
+inline void set_group(Args& p, int G, int tile_rows) {
     int log = 0;
+    p.tile_tokens = tile_rows / G > 1 ? tile_rows / G : 1;
     while ((1 << log) < G) ++log;  // G < 2^30
     p.G = G;
     p.g_shift = 31 + log;
@@ -145,12 +146,15 @@ template <int TM, int KT>
 struct Cost {
     // Of a tile's queries, outputs and of the step that its border cuts: as much as 1.5 steps.
     static constexpr int kTile = KT + KT / 2;
+    // A tile of few steps is not cut, and the others by four steps at least: joining costs more than
+    // they would take.  And a range is at least about a small tile, so that it has one.
+    static constexpr int kWhole = 12, kCut = 4, kLeast = KT * 5 / 2;
     int tiles, each;      // positions from a tile to the next
     int64_t base, limit;  // cost of tile i: min(base + each i, limit)
     int grow;             // tiles whose cost grows
     __device__ __forceinline__ Cost(const Args& p, const Request& q) {
         tiles = tile_count<TM>(q.rows(p));
-        each = max(TM / p.G, 1);
+        each = p.tile_tokens;
         base = static_cast<int64_t>(q.cached) + each + kTile;
         limit = p.s.window ? static_cast<int64_t>(p.s.window) + each + kTile : INT64_MAX;
         grow = p.s.window == 0 ? tiles : limit <= base ? 0 : static_cast<int>(min(divide(limit - base, each) + 1, static_cast<int64_t>(tiles)));
@@ -216,7 +220,9 @@ struct Planner {
         const Keys<KT> k(p, q, lo * TM, min(lo * TM + TM, rows));
         const int64_t c0 = cost(lo), c1 = cost(lo + 1);
         end = before + kh * one + c1;
-        const int a = static_cast<int>(divide((x - c0) * (k.k1 - k.k0), max(c1 - c0, static_cast<int64_t>(1))));
+        int a = 0;
+        if (k.k1 - k.k0 >= Cost<TM, KT>::kWhole)
+            a = static_cast<int>(divide((x - c0) * (k.k1 - k.k0), max(c1 - c0, static_cast<int64_t>(1)))) / Cost<TM, KT>::kCut * Cost<TM, KT>::kCut;
         return {r, static_cast<int>(kh), lo, a};
     }
 
@@ -251,7 +257,7 @@ struct Planner {
         sums[tid] = x + before;
         __syncthreads();
         if (warp < 2) {  // one finds the first border, one the last
-            const int64_t per = max(divide(total + gridDim.x - 1, gridDim.x), static_cast<int64_t>(p.least));
+            const int64_t per = max(divide(total + gridDim.x - 1, gridDim.x), static_cast<int64_t>(Cost<TM, KT>::kLeast));
             const int64_t u = per * (blockIdx.x + warp);
             Place at = {p.s.R, 0, 0, 0};
             int64_t end = 0;
