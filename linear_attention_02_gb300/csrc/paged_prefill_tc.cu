@@ -240,6 +240,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     __shared__ uint32_t s_mask[2][kMasks][4];  // positions of a step that are on a page, a bit each, as keys' and values' loader saw them
     __shared__ volatile int s_odd[4];        // by segment: a value that was not finite was replaced
     __shared__ volatile int s_abort;
+    __shared__ volatile int s_issued[2];     // tiles of keys, of values that their loaders have begun
     __shared__ uint32_t s_tmem;
     __shared__ prefill::Range s_range;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -253,7 +254,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         mbar_init(&s_qempty, 1);
         mbar_init(&s_end, 1);
         for (int w = 0; w < 2; ++w) mbar_init(s_sfull + w, 1), mbar_init(s_pfull + w, 4), mbar_init(s_odone + w, 1);
-        s_abort = 0;
+        s_abort = 0, s_issued[0] = 0, s_issued[1] = 0;
         fence_mbar_init();
     }
     if (warp == 8) {
@@ -443,31 +444,31 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_O = idesc_bf16(128, DP, false, true);
             const uint64_t dq = sdesc(smem_u32(sm), 16, 1024), dk = sdesc(smem_u32(ring), 16, 1024), dv = sdesc(smem_u32(ring), kAtom, 1024);
             constexpr uint32_t STEP = Ly::TILE >> 4;  // of a descriptor, from tile to tile
-            uint32_t item = 0, n_q = 0, n_p[2] = {0, 0};  // item: tiles taken from the ring: K, V, K, V, ...
+            uint32_t n_q = 0, n_p[2] = {0, 0}, sk = 0, tk = 0, sv = 1, n_v = 0;  // stages of the next keys and values, turns of the ring, value tiles
             bool ok = true;
             while (ok && walk.next(p, g)) {
                 const Request rq(p, g.r);
                 const int k0 = Keys<KT>(p, rq, g.m0, min(g.m0 + TM, g.rows)).k0;
                 const Part part0(p, rq, g, k0, 0), part1(p, rq, g, k0, 1);
-                if (!(ok = warp_wait(&s_qfull, n_q++) && warp_wait(s_full + item % STAGES, item / STAGES))) break;
+                if (!(ok = warp_wait(&s_qfull, n_q++) && warp_wait(s_full + sk, tk))) break;
                 fence_after_sync();
                 if (elect()) {
-                    const uint64_t k = dk + item % STAGES * STEP;
+                    const uint64_t k = dk + sk * STEP;
 #pragma unroll
                     for (int w = 0; w < 2; ++w)
                         if ((w ? part1 : part0).on(g.a)) {
                             mma_scores<DP / 16>(tm + 128 * w, dq + w * STEP, k, ID_S);
                             mma_commit(s_sfull + w);
                         }
-                    mma_commit(s_empty + item % STAGES);
+                    mma_commit(s_empty + sk);
                     if (g.a + 1 == g.b) mma_commit(&s_qempty);
                 }
                 __syncwarp();
-                for (int j = g.a; j < g.b; ++j, item += 2) {
-                    const uint32_t sv = (item + 1) % STAGES, sk = (item + 2) % STAGES;
+                if ((sk += 2) >= STAGES) sk -= STAGES, ++tk;
+                for (int j = g.a; j < g.b; ++j, ++n_v) {
                     const bool more = j + 1 < g.b;
                     // the values of this step and the keys of the next, mostly here before the weights
-                    if (!(ok = warp_wait(s_vready + sv, Ly::value_turn(item + 1)))) break;
+                    if (!(ok = warp_wait(s_vready + sv, Ly::value_turn(2 * n_v + 1)))) break;
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         const Part& part = w ? part1 : part0;
@@ -489,6 +490,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         __syncwarp();
                     }
                     if (!ok) break;
+                    if ((sv += 2) >= STAGES) sv -= STAGES;
+                    if (more && (sk += 2) >= STAGES) sk -= STAGES, ++tk;
                 }
             }
             // nothing may be under way when the block ends
@@ -505,6 +508,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             const int copies = KT / rows;                // of a tile
             uint32_t it = kv, step = 0;                  // the ring's tiles: K, V, K, V, ...
             bool ok = true, bad = false;
+            // With an odd number of stages keys and values take turns in each.  A stage's phase then tells whether it
+            // is free only once the other loader has begun its last turn there.
+            const auto in_turn = [&](uint32_t tile) {
+                if (STAGES % 2 == 0) return true;
+                const int need = tile < STAGES ? 0 : static_cast<int>(tile - STAGES) / 2 + 1;
+                uint32_t i = 0;
+                while (s_issued[1 - kv] < need && !s_abort && ++i < kLimit) {}
+                if (i == kLimit) fail();
+                const bool there = s_issued[1 - kv] >= need;
+                __threadfence_block();
+                return __all_sync(0xffffffffu, there) != 0;
+            };
             while (ok && walk.next(p, g)) {
                 const Request rq(p, g.r);
                 const Keys<KT> k(p, rq, g.m0, min(g.m0 + TM, g.rows));
@@ -529,6 +544,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             next = page_of(32ll * group + 32 + lane);
                         }
                         const uint32_t in = ((1u << copies) - 1u) << (first & 31);
+                        if (!(ok = in_turn(it))) break;
                         const uint32_t who = __ballot_sync(0xffffffffu, now >= 0) & in;
                         const uint32_t lost = (__ballot_sync(0xffffffffu, now == -1) & in) >> (first & 31);
                         bad |= lost != 0;
@@ -567,6 +583,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             bad |= ids[i] == -1;
                             mask[i] = __ballot_sync(0xffffffffu, ids[i] != -1 && y < rq.end);
                         }
+                        if (!(ok = in_turn(it))) break;
                         if (!(ok = warp_wait(s_empty + sg, it / STAGES + 1))) break;
                         const uint32_t dst = smem_u32(ring + sg * Ly::TILE);
 #pragma unroll
@@ -587,6 +604,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         __syncwarp();
                         if (lane == 0) mbar_arrive(s_full + sg);
                     }
+                    if (STAGES % 2 && lane == 0) s_issued[kv] = static_cast<int>(it / 2) + 1;
                 }
             }
             if (bad) atomicOr(p.status, kStatusBadIndex);
@@ -640,6 +658,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s_qfull);
                 }
+                if (!(ok = warp_wait(s_full + item % STAGES, item / STAGES))) break;  // every tile of the ring, so that no phase is missed
                 for (int j = g.a; ok && j < g.b; ++j, ++step, item += 2) {
                     const uint32_t v = item + 1, sg = v % STAGES;
                     if (!(ok = warp_wait(s_full + sg, v / STAGES))) break;
