@@ -17,6 +17,7 @@ Shapes: Q, K [B,H,N,D]; V [B,H,N,M]; S [B,H,D,M] fp32; Z [B,H,D] fp32.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -735,77 +736,96 @@ def la_rotary_frequencies(rot, base=10000.0, scaling="none", factor=1.0, origina
     return freqs.to("cuda" if device is None else device), mag.value
 
 
-def _rows(t, name, shape, dt, dev, out=False):
-    """Strides (batch row, token, head) of rows [B,H,N,D] or [N,H,D] with adjacent elements, checked."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dt and t.shape == shape and t.get_device() == dev and dev >= 0):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.dtype != dt:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {dt}")
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+def _refuse_rows(t, name, shape, dt, dev):
+    """The message for rows that are not of this shape and dtype, with adjacent elements, on CUDA device `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dt:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dt}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have adjacent elements (last stride 1), has strides {t.stride()}")
+
+
+def _rows(t, name, shape, dt, dev):
+    """Strides (batch row, token, head) of rows [B,H,N,D] or [N,H,D], checked."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dt and t.shape == shape and t.get_device() == dev and dev >= 0):
+        _refuse_rows(t, name, shape, dt, dev)
     s = t.stride()
     if s[-1] != 1 and t.numel():
-        raise ValueError(f"{name} must have adjacent elements (last stride 1), has strides {s}")
-    if out and t.numel() and not t.is_contiguous():
-        # written rows lie apart: each dimension steps over all that lies within its smaller strides
-        span = 1
-        for st, n in sorted((st, n) for st, n in zip(s, t.shape) if n > 1):
-            if st < span:
-                raise ValueError(f"{name} has rows that overlap (strides {s})")
-            span = st * (n - 1) + span
+        _refuse_rows(t, name, shape, dt, dev)
     return (s[0], s[2], s[1]) if len(s) == 4 else (0, s[0], s[1])
 
 
-def _rotary_sizes(q, k, names):
-    """(lead, B, N, Hq, Hk, D, packed, device): either of q and k may be None."""
-    lead = q if q is not None else k
-    if not isinstance(lead, torch.Tensor) or lead.dim() not in (3, 4):
-        raise ValueError(f"{names[0]} and {names[1]} must be [B,H,N,D] or [N,H,D]")
-    dev, packed = lead.get_device(), lead.dim() == 3
-    B, N, D = (1, lead.shape[0], lead.shape[2]) if packed else (lead.shape[0], lead.shape[2], lead.shape[3])
-    if lead.numel() > _INT_MAX:
-        _fits(lead)
-    heads = []
-    for t, n in ((q, names[0]), (k, names[1])):
-        if t is None:
-            heads.append(0)
-            continue
-        if not isinstance(t, torch.Tensor) or t.dim() != lead.dim():
-            raise ValueError(f"{n} must be a tensor of {lead.dim()} dimensions")
-        heads.append(t.shape[1])
-    return lead, B, N, heads[0], heads[1], D, packed, dev
+def _rows_apart(t, name):
+    """Refuses rows to be written that overlap: each dimension has to step over all that lies within its smaller strides."""
+    span = 1
+    for st, n in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
+        if st < span:
+            raise ValueError(f"{name} has rows that overlap (strides {t.stride()})")
+        span += st * (n - 1)
+
+
+_STRIDES = {2: struct.Struct("=12q"), 3: struct.Struct("=18q")}  # three a tensor, for inputs of 2 or 4 and outputs of 2
+_NONE = (0, 0, 0)
 
 
 def _rotary_call(fn, ins, names, outs, out_names, weights, grads, freqs, positions, first, layout, magnitude, eps,
                  stream):
     """Marshals a call of the rotary family; returns its outputs."""
-    if layout not in _LAYOUTS:
+    code = _LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
-    lead, B, N, Hq, Hk, D, packed, dev = _rotary_sizes(ins[0], ins[1], names)
-    dt, device = lead.dtype, lead.device
-    shapes = [(N, h, D) if packed else (B, h, N, D) for h in (Hq, Hk)]
-    strides, outs, fill = [], list(outs), 0
+    q, k = ins[0], ins[1]
+    lead = q if q is not None else k
+    if not isinstance(lead, torch.Tensor) or lead.dim() not in (3, 4):
+        raise ValueError(f"{names[0]} and {names[1]} must be [B,H,N,D] or [N,H,D]")
+    shape, dt, dev = lead.shape, lead.dtype, lead.get_device()
+    if lead.numel() > _INT_MAX:
+        _fits(lead)
+    packed = len(shape) == 3
+    B, N, D = (1, shape[0], shape[2]) if packed else (shape[0], shape[2], shape[3])
+    heads, strides, ptrs, fill, written = [], [], [], 0, [None, None]
     for i, t in enumerate(ins):
-        if ins[i % 2] is None:
+        if ins[i & 1] is None:
             if t is not None:
-                raise ValueError(f"{names[i]} is given without {names[i % 2]}")
-            strides += (0, 0, 0)
-        else:
-            strides += _rows(t, names[i], shapes[i % 2], dt, dev)
-    for i in (0, 1):
-        if ins[i] is None:
-            if outs[i] is not None:
-                raise ValueError(f"{out_names[i]} is given without {names[i]}")
-            strides += (0, 0, 0)
+                raise ValueError(f"{names[i]} is given without {names[i & 1]}")
+            strides += _NONE
+            ptrs.append(None)
+            if i < 2:
+                heads.append((0, None))
             continue
-        if outs[i] is None:
-            outs[i] = torch.empty(shapes[i], dtype=dt, device=device)
+        if i < 2:
+            if not isinstance(t, torch.Tensor) or t.dim() != len(shape):
+                raise ValueError(f"{names[i]} must be a tensor of {len(shape)} dimensions")
+            h = t.shape[1]
+            heads.append((h, (N, h, D) if packed else (B, h, N, D)))
+        strides += _rows(t, names[i], heads[i & 1][1], dt, dev)
+        ptrs.append(t.data_ptr())
+    out_ptrs = []
+    for i in (0, 1):
+        t = outs[i]
+        if ins[i] is None:
+            if t is not None:
+                raise ValueError(f"{out_names[i]} is given without {names[i]}")
+            strides += _NONE
+            out_ptrs.append(None)
+            continue
+        if t is None:
+            t = torch.empty(heads[i][1], dtype=dt, device=lead.device)
             fill |= 1 << i
-        strides += _rows(outs[i], out_names[i], shapes[i], dt, dev, out=True)
+            s = t.stride()
+            strides += (0, s[0], s[1]) if packed else (s[0], s[2], s[1])
+        else:
+            strides += _rows(t, out_names[i], heads[i][1], dt, dev)
+            if not t.is_contiguous():
+                _rows_apart(t, out_names[i])
+        written[i] = t
+        out_ptrs.append(t.data_ptr())
     if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
         raise ValueError("freqs must be la_rotary_frequencies' tensor [rot/2]")
     _shaped(freqs, "freqs", freqs.shape, torch.int64, dev)
@@ -813,20 +833,20 @@ def _rotary_call(fn, ins, names, outs, out_names, weights, grads, freqs, positio
     if positions is not None:
         if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
             raise ValueError("positions must be [N] or [B,N]")
-        _shaped(positions, "positions", (N,) if positions.dim() == 1 else (B, N), torch.int32, dev)
         prow = 1 if positions.dim() == 1 else B
+        _shaped(positions, "positions", (N,) if positions.dim() == 1 else (B, N), torch.int32, dev)
     for t, n in zip(weights, ("q_weight", "k_weight")):
         if t is not None:
             _shaped(t, n, (D,), torch.float32, dev)
-    buf = (ctypes.c_int64 * len(strides))(*strides)
-    args = [_ptr(t) for t in ins]
-    args += [_ptr(t) for t in weights] + [_ptr(t) for t in outs] + [_ptr(t) for t in grads]
-    args += [B, N, Hq, Hk, D, buf, _ptr(positions), prow, _int(first, "first_position"), freqs.data_ptr(),
-             2 * freqs.shape[0], float(magnitude), _LAYOUTS[layout]]
-    if eps is not None:
-        args.append(float(eps))
-    _launch(fn, dev, stream, *args, _dtype(lead), fill)
-    return outs
+        ptrs.append(_ptr(t))
+    ptrs += out_ptrs
+    for t in grads:
+        ptrs.append(_ptr(t))
+    tail = (float(magnitude), code) if eps is None else (float(magnitude), code, float(eps))
+    _launch(fn, dev, stream, *ptrs, B, N, heads[0][0], heads[1][0], D, _STRIDES[len(ins) // 2 + 1].pack(*strides),
+            _ptr(positions), prow, _int(first, "first_position"), freqs.data_ptr(), 2 * freqs.shape[0], *tail,
+            _dtype(lead), fill)
+    return written
 
 
 def la_forward_rotary(q, k, freqs, positions=None, first_position=0, layout="half", magnitude=1.0, q_out=None,

@@ -9,17 +9,20 @@
 //
 // Angles.  theta_i is kept as a whole number f_i of 2^-64 turns, so that the phase of any
 // position is p f_i modulo 2^64: an integer product, exact for every position.  Its upper
-// 32 bits are taken to the nearest quarter turn and a rest of at most an eighth, whose
-// sine and cosine are those of an fp32 number with a rounding of 2^-25 of itself: an angle
-// is off by 2.4e-8 at most, whether the position is 1 or 2^31.
+// 32 bits are taken to the nearest quarter turn and a rest of at most an eighth, an fp32
+// number with a rounding of 2^-25 of itself: an angle is off by 2.4e-8 at most, whether the
+// position is 1 or 2^31.  Its sine and cosine are summed from their series.
 //
 // Bound by memory: a row is read once and written once (with the norm's gradient, two are
 // read).  A thread holds one unit of a row: two pieces of 16 bytes whose elements are paired
 // with each other (half layout) or among themselves; D / (2 VEC) neighbouring lanes hold a
-// row and sum up its squares between them.  A block takes a tile of tokens with all heads
-// of the queries or of the keys, works out the tile's sines and cosines once for all heads
-// into shared memory, and has four rows a thread in flight.  Rows that are not 16-byte aligned, or whose
-// rotated part is not a whole number of units, take units of two single elements.
+// row and sum up its squares between them.  A thread keeps to its token and takes every HS-th
+// head of the queries, then of the keys: so a token's sines and cosines are worked out once for
+// all of them, lie in registers, and a row costs no index arithmetic.  (With rows dealt
+// out one by one, and the sines read from shared memory for each, the same work took twice the
+// instructions: 389 us against LA_TIME us for 65536 x (32 + 4) x 128 bf16.)  Products are on pairs of elements
+// (fma.rn.f32x2).  Rows that are not 16-byte aligned, or whose rotated part is not a whole
+// number of units, take units of two single elements.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,13 +36,17 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kTrig = 3;  // a token's sines, in rows
 
 // Sine and cosine of a phase in units of 2^-32 turns.
 __device__ __forceinline__ void turn(uint32_t phase, float& s, float& c) {
     const uint32_t quarter = (phase + 0x20000000u) >> 30;                   // nearest
     const int rest = static_cast<int>(phase - (quarter << 30));             // within +- 2^29
-    float a, b;
-    sincospif(static_cast<float>(rest) * 4.656612873077393e-10f, &a, &b);   // rest / 2^31 half turns
+    const float x = static_cast<float>(rest) * 4.656612873077393e-10f;      // half turns, within +- 1/4
+    // Taylor's series of sin(pi x) and cos(pi x); their next terms are below 2e-9 there.
+    const float z = x * x;
+    const float a = x * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 0.08214589f, -0.5992645f), 2.550164f), -5.1677128f), 3.1415927f);
+    const float b = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -0.025806891f, 0.23533063f), -1.3352628f), 4.058712f), -4.934802f), 1.f);
     s = quarter & 1 ? b : a;
     c = quarter & 1 ? a : b;
     if (quarter & 2) s = -s;
@@ -53,6 +60,10 @@ struct Piece<float, 4> { using type = float4; };
 template <>
 struct Piece<__nv_bfloat16, 8> { using type = uint4; };
 template <>
+struct Piece<float, 2> { using type = float2; };
+template <>
+struct Piece<__nv_bfloat16, 2> { using type = uint32_t; };
+template <>
 struct Piece<float, 1> { using type = float; };
 template <>
 struct Piece<__nv_bfloat16, 1> { using type = __nv_bfloat16; };
@@ -61,8 +72,12 @@ template <typename T, int VEC>
 __device__ __forceinline__ void unpack(const typename Piece<T, VEC>::type& p, float* x) {
     if constexpr (VEC == 1) {
         x[0] = to_f<T>(p);
+    } else if constexpr (sizeof(T) == 4 && VEC == 2) {
+        x[0] = p.x, x[1] = p.y;
     } else if constexpr (sizeof(T) == 4) {
         x[0] = p.x, x[1] = p.y, x[2] = p.z, x[3] = p.w;
+    } else if constexpr (VEC == 2) {
+        x[0] = __uint_as_float(p << 16), x[1] = __uint_as_float(p & 0xFFFF0000u);
     } else {
         const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
@@ -76,8 +91,13 @@ template <typename T, int VEC>
 __device__ __forceinline__ typename Piece<T, VEC>::type pack(const float* x) {
     if constexpr (VEC == 1) {
         return from_f<T>(x[0]);
+    } else if constexpr (sizeof(T) == 4 && VEC == 2) {
+        return make_float2(x[0], x[1]);
     } else if constexpr (sizeof(T) == 4) {
         return make_float4(x[0], x[1], x[2], x[3]);
+    } else if constexpr (VEC == 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[0], x[1]);
+        return *reinterpret_cast<const uint32_t*>(&h);
     } else {
         uint32_t w[4];
 #pragma unroll
@@ -89,6 +109,20 @@ __device__ __forceinline__ typename Piece<T, VEC>::type pack(const float* x) {
     }
 }
 
+// d = a b + c (or a b) on two elements; d may be an operand.
+__device__ __forceinline__ void fma2(float* d, const float* a, const float* b, const float* c) {
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d[0]), "=f"(d[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
+}
+__device__ __forceinline__ void mul2(float* d, const float* a, const float* b) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d[0]), "=f"(d[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+
 // One side of a call, the queries or the keys.
 struct Side {
     const void *x, *g;  // input rows; with a norm's gradient also the gradient's rows
@@ -96,12 +130,14 @@ struct Side {
     int64_t xs[3], gs[3], ys[3];  // strides in elements: batch row, token, head
     const float* w;
     float* part;                  // partial sums of dw, one row of D a block (null: none)
-    int H, fill, tile, tiles, blocks;  // tokens of a tile; tiles of all batch rows; blocks
+    int H, fill;
+    int tokens, tiles, blocks;    // of a tile; of all batch rows; that do this side (both sides the same if `both`)
 };
 
 struct RotaryArgs {
     Side side[2];
     int B, N, rot, interleaved, backward;
+    int both;                     // a block does both sides
     const uint64_t* freqs;
     const int* pos;
     int64_t pos_batch;
@@ -112,177 +148,289 @@ struct RotaryArgs {
 enum { kPlain, kNorm, kNormGrad };
 
 template <typename T, int D, int VEC, int MODE>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs p) {
-    using P = typename Piece<T, VEC>::type;
-    constexpr int UNITS = D / (2 * VEC);                 // of a row
-    constexpr int LANES = UNITS < 32 ? UNITS : 32;       // that hold it
-    constexpr int EACH = UNITS / LANES;                  // units of a lane
-    constexpr int ROWS = kThreads / LANES;               // rows a block has at once
-    constexpr int FLY = (EACH > 1 ? 2 : MODE == kNormGrad ? 2 : 4);  // rows of a thread in flight
-    constexpr int E = 2 * VEC;                           // elements of a unit
-    extern __shared__ float2 s_trig[];                   // [tile][rot / 2]: cosine, sine
-    const bool second = static_cast<int>(blockIdx.x) >= p.side[0].blocks;
-    const Side& sd = p.side[second];
-    const int block = blockIdx.x - (second ? p.side[0].blocks : 0);
-    const int lane = threadIdx.x % LANES, row0 = threadIdx.x / LANES;
-    const int pairs = p.rot / 2, rotated = pairs / VEC;  // units that turn
-    const T* x = static_cast<const T*>(sd.x);
-    const T* g = static_cast<const T*>(sd.g);
-    T* y = static_cast<T*>(sd.y);
+struct Shape {
+    static constexpr int UNITS = D / (2 * VEC);               // of a row
+    static constexpr int LANES = UNITS < 32 ? UNITS : 32;     // that hold it
+    static constexpr int EACH = UNITS / LANES;                // units of a lane
+    static constexpr int ROWS = kThreads / LANES;             // rows a block has at once
+    static constexpr int E = 2 * VEC;                         // elements of a unit
+    static constexpr bool RING = VEC > 1;                     // rows come through shared memory
+    static constexpr int PIECES = MODE == kNormGrad ? 4 : 2;  // of a row in a stage of a thread
+    static constexpr int STAGES = MODE == kNormGrad ? 3 : 4;
+    // Blocks of an SM: three where a thread's registers allow it without rows waiting for one another.  Measured, us, with
+    // two and three: 65536 x 36 x 128 bf16 192, 204; 5003 x 16 x 64 fp32 9.9, 8.3, in pieces of two 13.3, 12.0.
+    static constexpr int BLOCKS = MODE == kNormGrad || (sizeof(T) == 2 && VEC == 8) ? 2 : 3;
+    static constexpr int RING_BYTES = RING ? STAGES * PIECES * VEC * static_cast<int>(sizeof(T)) * kThreads : 0;
+    static constexpr int TABLE = 2 * ROWS * D;                // floats: two tables of [tokens][2][rot / 2]
+    // Before the tables: frequencies, weights of both sides, positions of three tiles.
+    static constexpr int HEAD = 64 * 8 + 2 * D * 4 + 3 * ROWS * 4;
+    static constexpr int SMEM = HEAD + RING_BYTES + (TABLE > ROWS * (D + 1) ? TABLE : ROWS * (D + 1)) * 4;
+};
 
-    int at[EACH], to[EACH], unit[EACH];                  // first elements of a unit's pieces
-    float w[MODE == kPlain ? 1 : EACH * E], dw[MODE == kNormGrad ? EACH * E : 1];
+template <int BYTES>
+__device__ __forceinline__ void copy(void* to, const void* from, bool on) {
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if constexpr (BYTES == 16) {
+        if (on) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    } else {
+        if (on) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
+    }
+}
+
+template <typename T, int D, int VEC, int MODE>
+__global__ void __launch_bounds__(kThreads, (Shape<T, D, VEC, MODE>::BLOCKS)) rotary_kernel(const RotaryArgs p) {
+    using P = typename Piece<T, VEC>::type;
+    using S = Shape<T, D, VEC, MODE>;
+    constexpr int LANES = S::LANES, EACH = S::EACH, ROWS = S::ROWS, E = S::E, ALL = EACH * E, STAGES = S::STAGES, PIECES = S::PIECES;
+    extern __shared__ __align__(16) uint8_t s_raw[];
+    P* ring = reinterpret_cast<P*>(s_raw) + threadIdx.x;      // [stage][piece][thread]
+    uint64_t* s_freqs = reinterpret_cast<uint64_t*>(s_raw + S::RING_BYTES);
+    float* s_w = reinterpret_cast<float*>(s_freqs + 64);      // [2][D]
+    int* s_pos = reinterpret_cast<int*>(s_w + 2 * D);         // [3][ROWS]
+    float* s_trig = reinterpret_cast<float*>(s_pos + 3 * ROWS);  // by turns: [tokens][2][rot / 2] cosines, sines
+    const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES;
+    const int pairs = p.rot / 2, rotated = pairs / VEC;       // units that turn
+    const int only = !p.both && static_cast<int>(blockIdx.x) >= p.side[0].blocks ? 1 : 0, last = p.both ? 1 : only;  // sides
+    const int block = blockIdx.x - only * p.side[0].blocks, blocks = p.side[only].blocks, tiles = p.side[only].tiles;
+    const int per_tile = p.side[only].tokens;
+    const int my = slot % per_tile, h0 = slot / per_tile, HS = ROWS / per_tile;  // token of the tile, first head, from head to head
+
+    int at[EACH], to[EACH];                                   // first elements of a unit's pieces
+    bool turns[EACH];
 #pragma unroll
     for (int u = 0; u < EACH; ++u) {
-        unit[u] = lane + u * LANES;
-        const bool half = !p.interleaved && unit[u] < rotated;
-        at[u] = unit[u] * (half ? VEC : E);
+        const int unit = lane + u * LANES;
+        turns[u] = unit < rotated;
+        const bool half = !p.interleaved && turns[u];
+        at[u] = unit * (half ? VEC : E);
         to[u] = at[u] + (half ? pairs : VEC);
-        if constexpr (MODE != kPlain) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                w[u * E + i] = sd.w ? sd.w[at[u] + i] : 1.f;
-                w[u * E + VEC + i] = sd.w ? sd.w[to[u] + i] : 1.f;
-            }
-        }
-        if constexpr (MODE == kNormGrad) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) dw[u * E + i] = 0.f;
-        }
     }
-    // tokens of the tile run fastest where they are nearer to each other than heads
-    const bool by_token = sd.xs[1] < sd.xs[2] || sd.H == 1;
-    const int per = (p.N + sd.tile - 1) / sd.tile;       // tiles of a batch row
+    float dw[MODE == kNormGrad ? ALL : 1];
+#pragma unroll
+    for (int i = 0; i < (MODE == kNormGrad ? ALL : 1); ++i) dw[i] = 0.f;
+    const int per = (p.N + per_tile - 1) / per_tile;            // tiles of a batch row
 
-    for (int tile = block; tile < sd.tiles; tile += sd.blocks) {
-        const int b = tile / per, n0 = (tile - b * per) * sd.tile;
-        const int tokens = min(sd.tile, p.N - n0), rows = tokens * sd.H;
-        const int* pos = p.pos ? p.pos + b * p.pos_batch + n0 : nullptr;
-        // The first rows are on their way while the sines are worked out.
-        P px[FLY][EACH][2], pg[MODE == kNormGrad ? FLY : 1][EACH][2];
-        int hd[FLY], tk[FLY];
-        const auto load = [&](int base) {
-#pragma unroll
-            for (int f = 0; f < FLY; ++f) {
-                const int i = base + row0 + f * ROWS;
-                tk[f] = -1;
-                if (i >= rows) continue;
-                const int a = by_token ? i / tokens : i / sd.H;
-                tk[f] = by_token ? i - a * tokens : a;
-                hd[f] = by_token ? a : i - a * sd.H;
-                const int64_t n = n0 + tk[f];
-                const T* row = x + b * sd.xs[0] + n * sd.xs[1] + hd[f] * sd.xs[2];
-                const T* grow = MODE == kNormGrad ? g + b * sd.gs[0] + n * sd.gs[1] + hd[f] * sd.gs[2] : nullptr;
-#pragma unroll
-                for (int u = 0; u < EACH; ++u) {
-                    px[f][u][0] = *reinterpret_cast<const P*>(row + at[u]);
-                    px[f][u][1] = *reinterpret_cast<const P*>(row + to[u]);
-                    if constexpr (MODE == kNormGrad) {
-                        pg[f][u][0] = *reinterpret_cast<const P*>(grow + at[u]);
-                        pg[f][u][1] = *reinterpret_cast<const P*>(grow + to[u]);
-                    }
+    // The loader runs STAGES - 1 rows ahead of the work, over heads, sides and tiles: every thread copies the
+    // pieces that it will read itself, so no barrier is needed.
+    int l_tile = block, l_side = only, l_h = 0, l_stage = 0;
+    bool l_there = false;
+    const T *l_x = nullptr, *l_g = nullptr;
+    const auto l_base = [&]() {                               // the thread's token of tile l_tile, side l_side
+        const int b = l_tile / per, n = (l_tile - b * per) * per_tile + my;
+        const Side& sd = p.side[l_side];
+        l_there = l_tile < tiles && n < p.N;
+        l_x = static_cast<const T*>(sd.x) + b * sd.xs[0] + n * sd.xs[1];
+        if constexpr (MODE == kNormGrad) l_g = static_cast<const T*>(sd.g) + b * sd.gs[0] + n * sd.gs[1];
+    };
+    const auto l_skip = [&]() {                               // past a side without heads, or done with
+        while (l_tile < tiles && l_h >= p.side[l_side].H) {
+            l_h = 0;
+            if (++l_side > last) l_side = only, l_tile += blocks;
+        }
+        l_base();
+    };
+    const auto fetch = [&]() {
+        if constexpr (S::RING) {
+            if (l_tile < tiles) {
+                const Side& sd = p.side[l_side];
+                const int h = l_h + h0;
+                const bool on = l_there && h < sd.H;
+                const T* row = l_x + h * sd.xs[2];
+                P* dst = ring + l_stage * PIECES * kThreads;
+                copy<sizeof(P)>(dst, row + at[0], on);
+                copy<sizeof(P)>(dst + kThreads, row + to[0], on);
+                if constexpr (MODE == kNormGrad) {
+                    const T* grow = l_g + h * sd.gs[2];
+                    copy<sizeof(P)>(dst + 2 * kThreads, grow + at[0], on);
+                    copy<sizeof(P)>(dst + 3 * kThreads, grow + to[0], on);
                 }
+                l_h += HS;
+                if (l_h >= sd.H) l_skip();
             }
-        };
-        load(0);
-        __syncthreads();  // the last tile's rows have read its sines
-        for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
-            const int t = i / pairs;
-            const int n = pos ? pos[t] : p.first + n0 + t;
-            const uint64_t ph = static_cast<uint64_t>(static_cast<int64_t>(n)) * p.freqs[i - t * pairs] + 0x80000000u;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (++l_stage == STAGES) l_stage = 0;
+        }
+    };
+    static_assert(!S::RING || EACH == 1, "a lane's unit");
+    l_skip();
+#pragma unroll 1
+    for (int i = 0; S::RING && i < STAGES - 1; ++i) fetch();
+
+    // Positions are fetched two tiles ahead, sines worked out one tile ahead, under the rows of the tile before:
+    // so a tile starts with what lies in shared memory.
+    const auto position = [&](int tile, int t) {              // of token t of a tile, which may be past the last
+        const int b = tile / per, n = (tile - b * per) * per_tile + t;
+        if (tile >= tiles || t >= per_tile || n >= p.N) return -1;
+        return p.pos ? p.pos[b * p.pos_batch + n] : p.first + n;
+    };
+    const auto sines = [&](const int* pos, float* table) {
+        int t = threadIdx.x / pairs, j = threadIdx.x - t * pairs;
+        const int dt = kThreads / pairs, dj = kThreads - dt * pairs;
+        for (; t < per_tile; t += dt, j += dj) {
+            if (j >= pairs) {
+                j -= pairs;
+                if (++t >= per_tile) break;
+            }
+            const uint64_t ph = static_cast<uint64_t>(static_cast<int64_t>(pos[t])) * s_freqs[j] + 0x80000000u;
             float s, c;
             turn(static_cast<uint32_t>(ph >> 32), s, c);
-            s_trig[i] = make_float2(c * p.mag, (p.backward ? -s : s) * p.mag);
+            table[2 * t * pairs + j] = c * p.mag;
+            table[(2 * t + 1) * pairs + j] = (p.backward ? -s : s) * p.mag;
         }
-        __syncthreads();
-        for (int base = 0; base < rows; base += FLY * ROWS) {
-            if (base) load(base);
+    };
+    static_assert(ROWS <= kThreads, "a position a thread");
+    for (int i = threadIdx.x; i < pairs; i += kThreads) s_freqs[i] = p.freqs[i];
+    if constexpr (MODE != kPlain)
+        for (int i = threadIdx.x; i < 2 * D; i += kThreads) s_w[i] = p.side[i / D].w ? p.side[i / D].w[i % D] : 1.f;
+    if (static_cast<int>(threadIdx.x) < per_tile) {
+        s_pos[threadIdx.x] = position(block, threadIdx.x);
+        s_pos[ROWS + threadIdx.x] = position(block + blocks, threadIdx.x);
+    }
+    __syncthreads();
+    sines(s_pos, s_trig);
+    __syncthreads();
+
+    int stage = 0;
+    for (int tile = block, turn_no = 0, third = 0; tile < tiles; tile += blocks, turn_no ^= 1, third = third == 2 ? 0 : third + 1) {
+        const int b = tile / per, n0 = (tile - b * per) * per_tile, tokens = min(per_tile, p.N - n0);
+        const bool there = my < tokens;
+        const bool live = there && s_pos[third * ROWS + my] >= 0;  // a row of a token
+        const int ahead = static_cast<int>(threadIdx.x) < per_tile ? position(tile + 2 * blocks, threadIdx.x) : 0;
+        const float* table = s_trig + turn_no * (per_tile * p.rot);
+        float cs[EACH * VEC], sn[EACH * VEC];
 #pragma unroll
-            for (int f = 0; f < FLY; ++f) {
-                const int t = tk[f];
-                const bool live = t >= 0 && !(pos && pos[t] < 0);  // a row of a token
-                float v[EACH * E];
+        for (int u = 0; u < EACH; ++u)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int j = (lane + u * LANES) * VEC + i;
+                cs[u * VEC + i] = there && turns[u] ? table[2 * my * pairs + j] : 1.f;
+                sn[u * VEC + i] = there && turns[u] ? table[(2 * my + 1) * pairs + j] : 0.f;
+            }
+#pragma unroll 1
+        for (int side = only; side <= last; ++side) {
+            const Side& sd = p.side[side];
+            float w[MODE == kPlain ? 1 : ALL];
+            if constexpr (MODE != kPlain) {
+#pragma unroll
+                for (int u = 0; u < EACH; ++u)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        w[u * E + i] = s_w[side * D + at[u] + i];
+                        w[u * E + VEC + i] = s_w[side * D + to[u] + i];
+                    }
+            }
+            const int64_t n = n0 + my;
+            T* y = static_cast<T*>(sd.y) + b * sd.ys[0] + n * sd.ys[1];
+#pragma unroll 1
+            for (int hb = 0; hb < sd.H; hb += HS) {           // the same for all threads of the block
+                const int h = hb + h0;
+                const bool mine = there && h < sd.H, count = live && mine;
+                P px[EACH][PIECES];
+                if constexpr (S::RING) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i) px[0][i] = ring[(stage * PIECES + i) * kThreads];
+                    if (++stage == STAGES) stage = 0;
+                    fetch();                                  // into the stage of the row before
+                } else if (mine) {
+                    const T* row = static_cast<const T*>(sd.x) + b * sd.xs[0] + n * sd.xs[1] + h * sd.xs[2];
+                    const T* grow = MODE == kNormGrad ? static_cast<const T*>(sd.g) + b * sd.gs[0] + n * sd.gs[1] + h * sd.gs[2] : nullptr;
+#pragma unroll
+                    for (int u = 0; u < EACH; ++u) {
+                        px[u][0] = *reinterpret_cast<const P*>(row + at[u]);
+                        px[u][1] = *reinterpret_cast<const P*>(row + to[u]);
+                        if constexpr (MODE == kNormGrad) {
+                            px[u][2] = *reinterpret_cast<const P*>(grow + at[u]);
+                            px[u][3] = *reinterpret_cast<const P*>(grow + to[u]);
+                        }
+                    }
+                }
+                float v[ALL], z[MODE == kNormGrad ? ALL : 1];
+                float* m = MODE == kNormGrad ? z : v;         // what is turned
 #pragma unroll
                 for (int u = 0; u < EACH; ++u) {
-                    if (!live) {
+                    unpack<T, VEC>(px[u][0], v + u * E);
+                    unpack<T, VEC>(px[u][1], v + u * E + VEC);
+                    if constexpr (MODE == kNormGrad) {
+                        unpack<T, VEC>(px[u][2], z + u * E);
+                        unpack<T, VEC>(px[u][3], z + u * E + VEC);
+                    }
+                }
+                if (!count) {  // (also what was not loaded)
 #pragma unroll
-                        for (int i = 0; i < E; ++i) v[u * E + i] = 0.f;
-                    } else {
-                        unpack<T, VEC>(px[f][u][0], v + u * E);
-                        unpack<T, VEC>(px[f][u][1], v + u * E + VEC);
+                    for (int i = 0; i < ALL; ++i) {
+                        v[i] = 0.f;
+                        if constexpr (MODE == kNormGrad) z[i] = 0.f;
                     }
                 }
                 float r = 1.f;
                 if constexpr (MODE != kPlain) {
-                    float q = 0.f;
+                    float q[2] = {0.f, 0.f};
 #pragma unroll
-                    for (int i = 0; i < EACH * E; ++i) q = fmaf(v[i], v[i], q);
+                    for (int i = 0; i < ALL; i += 2) fma2(q, v + i, v + i, q);
+                    q[0] += q[1];
 #pragma unroll
-                    for (int o = LANES / 2; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-                    r = 1.f / sqrtf(q * (1.f / D) + p.eps);
+                    for (int o = LANES / 2; o; o >>= 1) q[0] += __shfl_xor_sync(0xffffffffu, q[0], o);
+                    r = 1.f / sqrtf(q[0] * (1.f / D) + p.eps);
                 }
-                float z[MODE == kNormGrad ? EACH * E : 1];
-                float mean = 0.f;
+                if constexpr (MODE == kNorm) {
+#pragma unroll
+                    for (int i = 0; i < ALL; i += 2) mul2(v + i, v + i, w + i);
+                }
 #pragma unroll
                 for (int u = 0; u < EACH; ++u) {
-                    float* m = v + u * E;  // what is turned
-                    if constexpr (MODE == kNorm) {
+                    float* e = m + u * E;
+                    const float *c = cs + u * VEC, *s = sn + u * VEC;
+                    if (VEC == 1 || (p.interleaved && turns[u])) {
 #pragma unroll
-                        for (int i = 0; i < E; ++i) m[i] = m[i] * r * w[u * E + i];
-                    }
-                    if constexpr (MODE == kNormGrad) {
-                        m = z + u * E;
-                        if (!live) {
+                        for (int i = 0; i < VEC; ++i) {
+                            const float e0 = e[2 * i], e1 = e[2 * i + 1];
+                            e[2 * i] = e0 * c[i] - e1 * s[i];
+                            e[2 * i + 1] = e0 * s[i] + e1 * c[i];
+                        }
+                    } else if constexpr (VEC > 1) {
 #pragma unroll
-                            for (int i = 0; i < E; ++i) m[i] = 0.f;
-                        } else {
-                            unpack<T, VEC>(pg[f][u][0], m);
-                            unpack<T, VEC>(pg[f][u][1], m + VEC);
+                        for (int i = 0; i < VEC; i += 2) {
+                            float t0[2], t1[2];
+                            const float neg[2] = {-e[VEC + i], -e[VEC + i + 1]};
+                            mul2(t0, e + i, c + i);
+                            mul2(t1, e + i, s + i);
+                            fma2(e + i, neg, s + i, t0);
+                            fma2(e + VEC + i, e + VEC + i, c + i, t1);
                         }
                     }
-                    if (live && unit[u] < rotated) {
-                        const float2* cs = s_trig + t * pairs + unit[u] * VEC;
-                        if (p.interleaved) {
+                }
+                if constexpr (MODE == kNorm) {
+                    const float rr[2] = {r, r};
 #pragma unroll
-                            for (int i = 0; i < VEC; ++i) {
-                                const float2 a = cs[i];
-                                const float m0 = m[2 * i], m1 = m[2 * i + 1];
-                                m[2 * i] = m0 * a.x - m1 * a.y;
-                                m[2 * i + 1] = m0 * a.y + m1 * a.x;
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < VEC; ++i) {
-                                const float2 a = cs[i];
-                                const float m0 = m[i], m1 = m[VEC + i];
-                                m[i] = m0 * a.x - m1 * a.y;
-                                m[VEC + i] = m0 * a.y + m1 * a.x;
-                            }
-                        }
-                    }
-                    if constexpr (MODE == kNormGrad) {
-#pragma unroll
-                        for (int i = 0; i < E; ++i) {
-                            float& n = v[u * E + i];
-                            n *= r;
-                            dw[u * E + i] = fmaf(m[i], n, dw[u * E + i]);
-                            m[i] *= w[u * E + i];
-                            mean = fmaf(m[i], n, mean);
-                        }
-                    }
+                    for (int i = 0; i < ALL; i += 2) mul2(v + i, v + i, rr);
                 }
                 if constexpr (MODE == kNormGrad) {
+                    const float rr[2] = {r, r};
+                    float mean[2] = {0.f, 0.f};
 #pragma unroll
-                    for (int o = LANES / 2; o; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
-                    mean *= 1.f / D;
+                    for (int i = 0; i < ALL; i += 2) {
+                        mul2(v + i, v + i, rr);
+                        fma2(dw + i, z + i, v + i, dw + i);
+                        mul2(z + i, z + i, w + i);
+                        fma2(mean, z + i, v + i, mean);
+                    }
+                    mean[0] += mean[1];
 #pragma unroll
-                    for (int i = 0; i < EACH * E; ++i) v[i] = r * (z[i] - v[i] * mean);
+                    for (int o = LANES / 2; o; o >>= 1) mean[0] += __shfl_xor_sync(0xffffffffu, mean[0], o);
+                    mean[0] *= -1.f / D;
+                    mean[1] = mean[0];
+#pragma unroll
+                    for (int i = 0; i < ALL; i += 2) {
+                        fma2(v + i, v + i, mean, z + i);
+                        mul2(v + i, v + i, rr);
+                    }
                 }
-                if (live || (t >= 0 && sd.fill)) {
-                    T* out = y + b * sd.ys[0] + static_cast<int64_t>(n0 + t) * sd.ys[1] + hd[f] * sd.ys[2];
-                    if (!live) {  // whatever the weights are
+                if (count || (mine && sd.fill)) {
+                    T* out = y + h * sd.ys[2];
+                    if (!count) {  // whatever the weights are
 #pragma unroll
-                        for (int i = 0; i < EACH * E; ++i) v[i] = 0.f;
+                        for (int i = 0; i < ALL; ++i) v[i] = 0.f;
                     }
 #pragma unroll
                     for (int u = 0; u < EACH; ++u) {
@@ -292,24 +440,31 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs p) {
                 }
             }
         }
+        if (tile + blocks < tiles) {
+            const int next = third == 2 ? 0 : third + 1;
+            if (static_cast<int>(threadIdx.x) < per_tile) s_pos[(next == 2 ? 0 : next + 1) * ROWS + threadIdx.x] = ahead;
+            sines(s_pos + next * ROWS, s_trig + (turn_no ^ 1) * (per_tile * p.rot));
+            __syncthreads();
+        }
     }
+    if constexpr (S::RING) asm volatile("cp.async.wait_all;" ::: "memory");
     if constexpr (MODE == kNormGrad) {
         // The block's sums: units over the block's rows, in the order of the rows.
-        if (sd.part == nullptr) return;
-        float* s_dw = reinterpret_cast<float*>(s_trig);  // [ROWS][D + 1]
+        float* part = p.side[only].part;
+        if (part == nullptr) return;
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < EACH; ++u)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                s_dw[row0 * (D + 1) + at[u] + i] = dw[u * E + i];
-                s_dw[row0 * (D + 1) + to[u] + i] = dw[u * E + VEC + i];
+                s_trig[slot * (D + 1) + at[u] + i] = dw[u * E + i];
+                s_trig[slot * (D + 1) + to[u] + i] = dw[u * E + VEC + i];
             }
         __syncthreads();
         for (int c = threadIdx.x; c < D; c += kThreads) {
             float a = 0.f;
-            for (int i = 0; i < ROWS; ++i) a += s_dw[i * (D + 1) + c];
-            sd.part[static_cast<int64_t>(block) * D + c] = a;
+            for (int i = 0; i < ROWS; ++i) a += s_trig[i * (D + 1) + c];
+            part[static_cast<int64_t>(block) * D + c] = a;
         }
     }
 }
@@ -333,74 +488,84 @@ __global__ void __launch_bounds__(1024) rotary_weight_kernel(const float* q_part
     if (x == 0) dw[c0 + i0] = a;
 }
 
-// Largest common piece: every row's units are whole 16-byte pieces.
+// Every row's units are whole pieces of `vec` elements.
 bool aligned(const RotaryShape& s, int rot, int vec, int es) {
     if (rot % (2 * vec)) return false;
     for (int i = 0; i < s.tensors; ++i) {
         if (s.ptr[i] == nullptr) continue;
-        if (reinterpret_cast<uintptr_t>(s.ptr[i]) & 15u) return false;
+        if (reinterpret_cast<uintptr_t>(s.ptr[i]) % (vec * es)) return false;
         for (int d = 0; d < 3; ++d)
-            if (s.strides[i][d] % (16 / es)) return false;
+            if (s.strides[i][d] % vec) return false;
     }
     return true;
 }
 
 template <typename T, int D, int VEC, int MODE>
 cudaError_t launch(const LaunchCtx& c, const RotaryShape& s, float* dwq, float* dwk) {
-    constexpr int UNITS = D / (2 * VEC), LANES = UNITS < 32 ? UNITS : 32, ROWS = kThreads / LANES;
+    using S = Shape<T, D, VEC, MODE>;
     RotaryArgs p = {};
     p.B = s.B, p.N = s.N, p.rot = s.rot, p.interleaved = s.interleaved, p.backward = s.backward;
     p.freqs = s.freqs, p.pos = s.positions, p.pos_batch = s.pos_batch, p.first = s.first;
     p.mag = s.mag, p.eps = s.eps;
-    int smem = 0;
+    p.both = MODE != kNormGrad;
+    // tensors: q, k, [gradients of q, k,] outputs of q, k
+    constexpr int out = MODE == kNormGrad ? 4 : 2;
     for (int i = 0; i < 2; ++i) {
         Side& d = p.side[i];
-        const int H = i ? s.Hk : s.Hq;
-        d.H = H;
-        // tensors: q, k, [gradients of q, k,] outputs of q, k
-        const int out = MODE == kNormGrad ? 4 : 2;
+        d.H = i ? s.Hk : s.Hq;
         d.x = s.ptr[i], d.g = s.ptr[2 + i], d.y = const_cast<void*>(s.ptr[out + i]);
         for (int j = 0; j < 3; ++j) d.xs[j] = s.strides[i][j], d.gs[j] = s.strides[2 + i][j], d.ys[j] = s.strides[out + i][j];
         d.w = s.w[i];
         d.fill = s.fill >> i & 1;
-        if (H == 0) continue;
-        // A tile's rows: enough for a few turns of the block where the call is large, few where
-        // it is small, so that all SMs have some.
-        const int64_t all = static_cast<int64_t>(s.B) * s.N * H;
-        const int64_t want = std::min<int64_t>(std::max<int64_t>(all / (8 * c.num_sms), ROWS), 8 * ROWS);
-        int64_t tile = std::max<int64_t>(1, want / H);
-        tile = std::min<int64_t>(std::min<int64_t>(tile, 64), s.N);
-        d.tile = static_cast<int>(tile);
-        const int64_t tiles = (s.N + tile - 1) / tile * s.B;
-        if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-        d.tiles = static_cast<int>(tiles);
-        d.blocks = d.tiles;
-        if (MODE == kNormGrad) d.blocks = std::min(d.tiles, rotary_grad_blocks(c.num_sms));
-        smem = std::max(smem, static_cast<int>(tile) * (s.rot / 2) * 8);
     }
-    float* part = nullptr;
-    if (MODE == kNormGrad) {
-        smem = std::max(smem, ROWS * (D + 1) * 4);
-        if (dwq || dwk) {
-            cudaError_t e = scratch_alloc(c, reinterpret_cast<void**>(&part), rotary_grad_scratch(s.B, s.N, s.Hq, s.Hk, D, dwq || dwk, c.num_sms));
-            if (e != cudaSuccess) return e;
-            if (dwq) p.side[0].part = part;
-            if (dwk) p.side[1].part = part + static_cast<int64_t>(rotary_grad_blocks(c.num_sms)) * D;
+    // As many blocks as an SM has room for, whose loaders never stop; with the gradient, whose sums are of one
+    // side, dealt out by its work.
+    const auto side_work = [&](int H) { return H ? static_cast<int64_t>(H) + kTrig : 0; };
+    const int most = S::BLOCKS * c.num_sms;
+    const int64_t q_work = side_work(s.Hq), work = q_work + side_work(s.Hk);
+    const int q_blocks = static_cast<int>((most * q_work + work / 2) / work);
+    int grid = 0, tokens = 1;
+    for (int i = 0; i < (p.both ? 1 : 2); ++i) {
+        Side& d = p.side[i];
+        const int limit = p.both ? most : std::max(1, i ? most - q_blocks : q_blocks);
+        if (!p.both && d.H == 0) continue;
+        // Tokens of a tile: the power of two with the least time, counted in rows a thread for the block with most
+        // tiles: its heads, a row or so for the tile's start, and its sines.
+        double best = 0;
+        for (int t = 1; t <= S::ROWS; t *= 2) {
+            const int HS = S::ROWS / t;
+            const auto rows = [&](int H) { return (H + HS - 1) / HS; };
+            const int64_t tiles = (s.N + t - 1) / t * static_cast<int64_t>(s.B);
+            const double cost = ((tiles + limit - 1) / limit) *
+                                ((p.both ? rows(s.Hq) + rows(s.Hk) : rows(d.H)) + 1 + t * (s.rot / 2) / static_cast<double>(kThreads));
+            if (t == 1 || cost < best) best = cost, d.tokens = t, d.tiles = static_cast<int>(tiles);
+            if (tiles > INT32_MAX / 2 && t == 1) return cudaErrorInvalidValue;
         }
+        d.blocks = std::min(d.tiles, limit);
+        grid += d.blocks;
+        tokens = std::max(tokens, d.tokens);
     }
-    static_assert(ROWS * (D + 1) * 4 <= 160 * 1024, "shared memory");
-    auto* kernel = rotary_kernel<T, D, VEC, MODE>;
-    cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && p.side[0].blocks + p.side[1].blocks > 0) {
-        kernel<<<p.side[0].blocks + p.side[1].blocks, kThreads, smem, c.stream>>>(p);
+    if (p.both) p.side[1].tokens = p.side[0].tokens, p.side[1].tiles = p.side[0].tiles, p.side[1].blocks = p.side[0].blocks;
+    float* part = nullptr;
+    if (MODE == kNormGrad && (dwq || dwk)) {
+        cudaError_t e = scratch_alloc(c, reinterpret_cast<void**>(&part), rotary_grad_scratch(s.B, s.N, s.Hq, s.Hk, D, true, c.num_sms));
+        if (e != cudaSuccess) return e;
+        if (dwq) p.side[0].part = part;
+        if (dwk) p.side[1].part = part + static_cast<int64_t>(rotary_grad_blocks(c.num_sms)) * D;
+    }
+    int smem = 2 * tokens * s.rot * static_cast<int>(sizeof(float));
+    if (MODE == kNormGrad) smem = std::max(smem, S::ROWS * (D + 1) * 4);
+    smem += S::HEAD + S::RING_BYTES;
+    int per_sm = 0;
+    cudaError_t e = resident_blocks<rotary_kernel<T, D, VEC, MODE>>(c.device, kThreads, S::SMEM, &per_sm);
+    if (e == cudaSuccess) {
+        rotary_kernel<T, D, VEC, MODE><<<grid, kThreads, smem, c.stream>>>(p);
         note_launch();
         e = cudaGetLastError();
     }
     if (MODE == kNormGrad && (dwq || dwk)) {
         if (e == cudaSuccess) {
-            rotary_weight_kernel<<<2 * (D / 32), 1024, 0, c.stream>>>(part, p.side[1].part, p.side[0].blocks,
-                                                                     p.side[1].blocks, D, dwq, dwk);
+            rotary_weight_kernel<<<2 * (D / 32), 1024, 0, c.stream>>>(part, p.side[1].part, p.side[0].blocks, p.side[1].blocks, D, dwq, dwk);
             note_launch();
             e = cudaGetLastError();
         }
@@ -409,11 +574,13 @@ cudaError_t launch(const LaunchCtx& c, const RotaryShape& s, float* dwq, float* 
     return e;
 }
 
+// Pieces of 16 bytes, of two elements, or single ones.
 template <typename T, int D, int MODE>
 cudaError_t by_alignment(const LaunchCtx& c, const RotaryShape& s, float* dwq, float* dwk) {
     constexpr int VEC = 16 / sizeof(T);
-    return aligned(s, s.rot, VEC, sizeof(T)) ? launch<T, D, VEC, MODE>(c, s, dwq, dwk)
-                                             : launch<T, D, 1, MODE>(c, s, dwq, dwk);
+    if (aligned(s, s.rot, VEC, sizeof(T))) return launch<T, D, VEC, MODE>(c, s, dwq, dwk);
+    if (aligned(s, s.rot, 2, sizeof(T))) return launch<T, D, 2, MODE>(c, s, dwq, dwk);
+    return launch<T, D, 1, MODE>(c, s, dwq, dwk);
 }
 
 template <typename T, int MODE>
@@ -425,7 +592,7 @@ cudaError_t by_size(const LaunchCtx& c, const RotaryShape& s, float* dwq, float*
 
 }  // namespace
 
-int rotary_grad_blocks(int num_sms) { return 4 * num_sms; }
+int rotary_grad_blocks(int num_sms) { return 2 * num_sms; }
 
 size_t rotary_grad_scratch(int B, int N, int Hq, int Hk, int D, bool weights, int num_sms) {
     if (!weights || static_cast<int64_t>(B) * N * (Hq + Hk) == 0) return 0;

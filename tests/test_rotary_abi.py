@@ -115,6 +115,6 @@ def test_binding_refusals():
 
 def test_norm_workspace():
     f = lib.la_norm_rotary_workspace_bytes
-    assert f(2, 100, 8, 2, 64, 152) == 2 * 4 * 4 * 152 * 64
+    assert f(2, 100, 8, 2, 64, 152) == 2 * 4 * 2 * 152 * 64  # rows of 64 sums, two blocks an SM for each side at most
     assert f(0, 100, 8, 2, 64, 152) == 0 and f(2, 100, 0, 0, 64, 152) == 0
     assert f(2, 100, 8, 2, 48, 152) == _native.SIZE_MAX and f(-1, 100, 8, 2, 64, 152) == _native.SIZE_MAX
