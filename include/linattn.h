@@ -449,6 +449,10 @@ la_status la_paged_prefill(const void* q, const void* K_pages, const void* V_pag
                            int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages, int window,
                            float scale, la_dtype dtype, int fill, void* stream);
 
+/* Scratch bytes that one la_paged_prefill call with rows takes from the library pool, whatever its
+ * sizes: partial sums of two cut tiles for every block.  num_sms as in la_workspace_bytes. */
+size_t la_paged_prefill_workspace_bytes(int D, la_dtype dtype, int num_sms);
+
 /*
  * Rotary positions: pair i of the first `rot` elements of every query and key head,
  * standing at position p, turns by the angle p theta_i,

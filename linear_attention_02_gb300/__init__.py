@@ -714,6 +714,13 @@ def la_paged_prefill(q, K_pages, V_pages, block_table, cached_lens, seq_starts, 
     return (out, lse) if return_lse else out
 
 
+def la_paged_prefill_workspace_bytes(D, dtype, num_sms=0):
+    """Scratch bytes of one la_paged_prefill call; num_sms <= 0 asks the current device."""
+    if dtype not in _DT:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return _bytes(_lib.la_paged_prefill_workspace_bytes(_int(D, "D"), _DT[dtype], num_sms))
+
+
 _LAYOUTS = {"half": _native.LA_ROTARY_HALF, "interleaved": _native.LA_ROTARY_INTERLEAVED}
 _SCALINGS = {"none": _native.LA_ROTARY_UNSCALED, "linear": _native.LA_ROTARY_LINEAR,
              "base": _native.LA_ROTARY_BASE, "by_parts": _native.LA_ROTARY_BY_PARTS}

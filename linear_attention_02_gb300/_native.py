@@ -47,6 +47,7 @@ SIGNATURES = {
     "la_paged_decode_step": [_P, _P, _P, _P, _P, _P, _P, _F, _F, _I, _I, _I, _I, _I, _I, _I, _I, _R, _I, _P],
     "la_paged_decode_step_padded": [_P, _P, _P, _P, _P, _P, _P, _F, _F, _I, _I, _I, _I, _I, _I, _I, _I, _R, _I, _I, _P],
     "la_paged_prefill": [_P, _P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _I, _I, _I, _I, _I, _R, _I, _I, _P],
+    "la_paged_prefill_workspace_bytes": [_I, _I, _I],
     "la_rotary_frequencies": [_I, _D, _I, _D, _D, _D, _D, _P, _P],
     "la_forward_rotary": [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P, _I, _R, _I, _I, _I, _P],
     "la_backward_rotary": [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P, _I, _R, _I, _I, _I, _P],
@@ -69,6 +70,7 @@ _RESTYPES = {"la_status_string": ctypes.c_char_p, "la_last_error_message": ctype
              "la_paged_decode_workspace_bytes": ctypes.c_size_t,
              "la_page_map_workspace_bytes": ctypes.c_size_t,
              "la_norm_rotary_workspace_bytes": ctypes.c_size_t,
+             "la_paged_prefill_workspace_bytes": ctypes.c_size_t,
              "la_workspace_bytes": ctypes.c_size_t,
              "la_scratch_peak_bytes": ctypes.c_size_t,
              "la_kernel_launch_count": ctypes.c_uint64}

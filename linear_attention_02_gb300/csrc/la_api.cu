@@ -1167,6 +1167,21 @@ static la_status check_prefill(const char* fn, int T, int R, int Hq, int Hkv, in
     return LA_OK;
 }
 
+size_t la_paged_prefill_workspace_bytes(int D, la_dtype dtype, int num_sms) {
+    static const char* fn = "la_paged_prefill_workspace_bytes";
+    if (dtype != LA_DTYPE_F32 && dtype != LA_DTYPE_BF16)
+        return fail(LA_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dtype), SIZE_MAX;
+    if (!head_ok(D))
+        return fail(LA_ERR_UNSUPPORTED, "%s: D=%d, supported head sizes are 32, 64, 128", fn, D), SIZE_MAX;
+    if (num_sms <= 0) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return cuda_fail(e, fn), SIZE_MAX;
+    }
+    return paged_prefill_scratch(D, dtype == LA_DTYPE_BF16, num_sms);
+}
+
 la_status la_paged_prefill(const void* q, const void* K_pages, const void* V_pages, const int* block_table,
                            const int* cached_lens, const int* seq_starts, void* out, float* lse, int T, int R, int Hq,
                            int Hkv, int D, int num_pages, int page_size, int max_pages, int window, float scale,

@@ -215,6 +215,8 @@ cudaError_t paged_prefill_tc(const LaunchCtx& c, const __nv_bfloat16* q, const _
                              const int* table, const int* lens, const int* starts, __nv_bfloat16* out, float* lse,
                              const PrefillShape& s, int fill);
 size_t paged_prefill_tc_scratch(int D, int num_sms);
+// Scratch bytes of a call with rows.
+size_t paged_prefill_scratch(int D, bool bf16, int num_sms);
 
 // Rotary positions of queries (0) and keys (1): ptr and strides (batch row, token, head, in
 // elements) are the inputs' q, k, with a norm's gradient the upstream gradients' next, and

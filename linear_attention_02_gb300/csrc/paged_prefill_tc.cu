@@ -202,29 +202,6 @@ struct Part {
     __device__ __forceinline__ bool on(int j) const { return j >= a && j < b; }
 };
 
-// The columns of [i, i + 32), a bit each, in which a row sees a value that is not finite in a key
-// tile, if that is one in which such values were replaced: one that some row from position
-// `first` to `last` sees in part.
-template <int D>
-__device__ __noinline__ uint32_t odd_columns(const Args& p, const bf16* V, int r, int kh, int first, int last, int end,
-                                             int tile, int from, int pos, int i) {
-    const int x0 = tile * KT, mask = (1 << p.s.log2p) - 1;
-    const int* table = p.table + static_cast<int64_t>(r) * p.s.max_pages;
-    uint32_t bits = 0;
-    bool all = x0 + KT - 1 <= first && (p.s.window == 0 || x0 > last - p.s.window) && x0 + KT <= end;
-    for (int x = x0; all && x < x0 + KT; x += mask + 1)
-        all = static_cast<unsigned>(table[x >> p.s.log2p]) < static_cast<unsigned>(p.s.num_pages);
-    if (all) return 0;
-    for (int x = max(x0, max(from + 1, 0)); x < min(x0 + KT, min(pos + 1, end)); ++x) {
-        const int page = table[x >> p.s.log2p];
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.s.num_pages)) continue;
-        const bf16* v = V + (((static_cast<int64_t>(page) * p.s.Hkv + kh) << p.s.log2p) + (x & mask)) * D + i;
-        for (int y = 0; y < 32; ++y)
-            if (!(fabsf(__bfloat162float(v[y])) < INFINITY)) bits |= 1u << y;
-    }
-    return bits;
-}
-
 template <int D>
 __global__ void __launch_bounds__(NT, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -404,7 +381,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     if (s_odd[seg & 3]) {  // rare: does this row see one of the replaced values?
                         uint32_t bits = 0;
                         for (int j = mine.a; live && j < mine.b; ++j)
-                            bits |= odd_columns<D>(p, V, g.r, g.kh, kt.first, kt.last, rq.end, k0 + j, from, pos, i);
+                            bits |= prefill::odd_columns<bf16, D, KT>(p, V, g.r, g.kh, kt.first, kt.last, rq.end, k0 + j, from, pos, i);
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
                             if (bits >> x & 1u) o[x] = __uint_as_float(0x7FFFFFFFu);
@@ -713,90 +690,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         }
         }
     }
-    // rows of no request
-    if (p.fill) {
-        const int64_t wide = static_cast<int64_t>(p.s.Hq) * (D / 8);
-        const auto clear = [&](int64_t t0, int64_t t1) {
-            if (p.fill & 1)
-                for (int64_t e = t0 * wide + tid; e < t1 * wide; e += NT) reinterpret_cast<uint4*>(out)[e] = make_uint4(0u, 0u, 0u, 0u);
-            if (p.fill & 2)
-                for (int64_t e = t0 * p.s.Hq + tid; e < t1 * p.s.Hq; e += NT) p.lse[e] = -INFINITY;
-        };
-        const int last = p.s.R ? min(max(p.starts[p.s.R], 0), p.s.T) : 0;
-        for (int64_t t0 = last + 16 * static_cast<int64_t>(blockIdx.x); t0 < p.s.T; t0 += 16 * static_cast<int64_t>(gridDim.x))
-            clear(t0, min(t0 + 16, static_cast<int64_t>(p.s.T)));
-        for (int r = blockIdx.x; r < p.s.R; r += gridDim.x) {
-            const Request rq(p, r);
-            if (rq.pad && rq.n) clear(rq.first, rq.first + rq.n);
-        }
-    }
-    // the cut tile whose first step is in this range
-    if (range.any && tid == 0 && !s_abort) {
-        Walk walk(p, range);
-        Segment g, last = {};
-        while (walk.next(p, g)) last = g;
-        if (last.b > 0 && last.a == 0 && !last.whole()) {
-            p.desc[2 * blockIdx.x] = make_int4(last.r, last.kh, last.m0, last.rows);
-            p.desc[2 * blockIdx.x + 1] = make_int4(range.ranges, 0, 0, 0);
-        }
-    }
-    // a range inside a tile that has no whole step adds nothing to it
-    if (range.any && range.from.a > 0 && range.from.a == range.to.a && range.from.r == range.to.r && range.from.kh == range.to.kh &&
-        range.from.mt == range.to.mt && tid < TM)
-        p.ml[2 * static_cast<int64_t>(blockIdx.x) * TM + tid] = make_float2(-INFINITY, 0.f);
+    prefill::finish_range<bf16, D, TM, KT, NT>(p, range, !s_abort, out);
     fence_before_sync();
     __syncthreads();
     if (warp == 8) {
         fence_after_sync();
         tmem_dealloc(tm, 512);
-    }
-}
-
-// Joins the partial sums of the cut tile that starts in range blockIdx.x: a warp a row.
-constexpr int kJoinWarps = 8, kJoinRows = 32;
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Args p, bf16* __restrict__ out) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int ranges = p.desc[2 * blockIdx.x + 1].x;
-    if (ranges == 0) return;
-    const int4 d = p.desc[2 * blockIdx.x];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Request rq(p, d.x);
-    constexpr int E = D / 32, N = 4;
-    for (int i = warp; i < kJoinRows; i += kJoinWarps) {
-        const int row = blockIdx.y * kJoinRows + i, m = d.z + row;
-        if (m >= d.w) return;
-        float top = -INFINITY, sum = 0.f, o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.f;
-        for (int x0 = 0; x0 < ranges; x0 += N) {
-            float2 ml[N];
-            float v[N][E];
-#pragma unroll
-            for (int x = 0; x < N; ++x) {
-                const int64_t at = (2 * (static_cast<int64_t>(blockIdx.x) + x0 + x) + (x0 + x == 0 ? 1 : 0)) * TM + row;
-                ml[x] = x0 + x < ranges ? p.ml[at] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-                for (int e = 0; e < E; ++e) v[x][e] = x0 + x < ranges ? p.part[at * D + lane + 32 * e] : 0.f;
-            }
-#pragma unroll
-            for (int x = 0; x < N; ++x) {
-                const float y = fmaxf(top, ml[x].x);
-                const float f = top == y ? 1.f : ex2(top - y);
-                // nothing of a part without a key is read; one whose scores are NaN carries them on
-                const float h = ml[x].x == -INFINITY ? (ml[x].y != ml[x].y ? 1.f : 0.f) : ml[x].x == y ? 1.f : ex2(ml[x].x - y);
-                sum = sum * f + ml[x].y * h;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = o[e] * f + (h > 0.f ? v[x][e] * h : 0.f);
-                top = y;
-            }
-        }
-        const bool good = sum > 0.f || sum != sum;
-        const int token = token_of(p, m);
-        const int64_t at = (static_cast<int64_t>(rq.first) + token) * p.s.Hq + static_cast<int64_t>(d.y) * p.G + (m - token * p.G);
-#pragma unroll
-        for (int e = 0; e < E; ++e) out[at * D + lane + 32 * e] = __float2bfloat16_rn(good ? o[e] / sum : 0.f);
-        if (lane == 0 && p.lse) p.lse[at] = good ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     }
 }
 
@@ -811,12 +710,9 @@ cudaError_t encode(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3]
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-size_t part_bytes(int D, int num_sms) { return sizeof(float) * 2 * num_sms * TM * D; }
-size_t ml_bytes(int num_sms) { return sizeof(float2) * 2 * num_sms * TM; }
-
 }  // namespace
 
-size_t paged_prefill_tc_scratch(int D, int num_sms) { return part_bytes(D, num_sms) + ml_bytes(num_sms) + sizeof(int4) * 2 * num_sms; }
+size_t paged_prefill_tc_scratch(int D, int num_sms) { return prefill::scratch_bytes(D, TM, num_sms); }
 
 template <int D>
 cudaError_t paged_prefill_tc(const LaunchCtx& c, const bf16* q, const bf16* K, const bf16* V, const int* table,
@@ -845,25 +741,11 @@ cudaError_t paged_prefill_tc(const LaunchCtx& c, const bf16* q, const bf16* K, c
     }
     uint8_t* base = nullptr;
     if ((e = scratch_alloc(c, reinterpret_cast<void**>(&base), paged_prefill_tc_scratch(D, c.num_sms))) != cudaSuccess) return e;
-    p.part = reinterpret_cast<float*>(base);
-    p.ml = reinterpret_cast<float2*>(base + part_bytes(D, c.num_sms));
-    p.desc = reinterpret_cast<int4*>(base + part_bytes(D, c.num_sms) + ml_bytes(c.num_sms));
+    prefill::set_scratch(p, base, D, TM, c.num_sms);
     prefill_kernel<D><<<c.num_sms, NT, Ly::SMEM, c.stream>>>(kmap, vmap, qmap, q, K, V, out, p, q_tma, kv_tma);
     note_launch();
     e = cudaGetLastError();
-    if (e == cudaSuccess) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(c.num_sms, TM / kJoinRows);
-        cfg.blockDim = dim3(kJoinWarps * 32);
-        cfg.stream = c.stream;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, prefill_join_kernel<D>, p, out);
-        note_launch();
-    }
+    if (e == cudaSuccess) e = prefill::launch_join<bf16, D, TM>(p, out, c.num_sms, c.stream);
     scratch_free(c, base);
     return e;
 }

@@ -144,11 +144,11 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // of numbers
 // The cost of a request's tiles: cost(mt) of the tiles before mt.
 template <int TM, int KT>
 struct Cost {
-    // Of a tile's queries, outputs and of the step that its border cuts: as much as 1.5 steps.
-    static constexpr int kTile = KT + KT / 2;
-    // A tile of few steps is not cut, and the others by four steps at least: joining costs more than
-    // they would take.  And a range is at least about a small tile, so that it has one.
-    static constexpr int kWhole = 12, kCut = 4, kLeast = KT * 5 / 2;
+    // Of a tile's queries, outputs and of the step that its border cuts: as much as 192 positions.
+    static constexpr int kTile = 192;
+    // A tile of few steps (below 1536 positions) is not cut, and the others by 512 positions at least: joining
+    // costs more than they would take.  And a range is at least about a small tile, so that it has one.
+    static constexpr int kWhole = 1536 / KT, kCut = 512 / KT, kLeast = 320;
     int tiles, each;      // positions from a tile to the next
     int64_t base, limit;  // cost of tile i: min(base + each i, limit)
     int grow;             // tiles whose cost grows
@@ -275,6 +275,146 @@ struct Planner {
         __syncthreads();
     }
 };
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The columns of [i, i + 32), a bit each, in which a row sees a value that is not finite in a key
+// tile, if that is one in which such values were replaced: one that some row from position
+// `first` to `last` sees in part.
+template <typename T, int D, int KT>
+__device__ __noinline__ uint32_t odd_columns(const Args& p, const T* V, int r, int kh, int first, int last, int end,
+                                             int tile, int from, int pos, int i) {
+    const int x0 = tile * KT, mask = (1 << p.s.log2p) - 1;
+    const int* table = p.table + static_cast<int64_t>(r) * p.s.max_pages;
+    uint32_t bits = 0;
+    bool all = x0 + KT - 1 <= first && (p.s.window == 0 || x0 > last - p.s.window) && x0 + KT <= end;
+    for (int x = x0; all && x < x0 + KT; x += mask + 1)
+        all = static_cast<unsigned>(table[x >> p.s.log2p]) < static_cast<unsigned>(p.s.num_pages);
+    if (all) return 0;
+    for (int x = max(x0, max(from + 1, 0)); x < min(x0 + KT, min(pos + 1, end)); ++x) {
+        const int page = table[x >> p.s.log2p];
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.s.num_pages)) continue;
+        const T* v = V + (((static_cast<int64_t>(page) * p.s.Hkv + kh) << p.s.log2p) + (x & mask)) * D + i;
+        for (int y = 0; y < 32; ++y)
+            if (!(fabsf(to_f<T>(v[y])) < INFINITY)) bits |= 1u << y;
+    }
+    return bits;
+}
+
+// Joins the partial sums of the cut tile that starts in range blockIdx.x: a warp a row.
+constexpr int kJoinWarps = 8, kJoinRows = 32;
+template <typename T, int D, int TM>
+__global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Args p, T* __restrict__ out) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int ranges = p.desc[2 * blockIdx.x + 1].x;
+    if (ranges == 0) return;
+    const int4 d = p.desc[2 * blockIdx.x];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Request rq(p, d.x);
+    constexpr int E = D / 32, N = 4;
+    for (int i = warp; i < kJoinRows; i += kJoinWarps) {
+        const int row = blockIdx.y * kJoinRows + i, m = d.z + row;
+        if (m >= d.w) return;
+        float top = -INFINITY, sum = 0.f, o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        for (int x0 = 0; x0 < ranges; x0 += N) {
+            float2 ml[N];
+            float v[N][E];
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                const int64_t at = (2 * (static_cast<int64_t>(blockIdx.x) + x0 + x) + (x0 + x == 0 ? 1 : 0)) * TM + row;
+                ml[x] = x0 + x < ranges ? p.ml[at] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[x][e] = x0 + x < ranges ? p.part[at * D + lane + 32 * e] : 0.f;
+            }
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                const float y = fmaxf(top, ml[x].x);
+                const float f = top == y ? 1.f : exp2_approx(top - y);
+                // nothing of a part without a key is read; one whose scores are NaN carries them on
+                const float h = ml[x].x == -INFINITY ? (ml[x].y != ml[x].y ? 1.f : 0.f) : ml[x].x == y ? 1.f : exp2_approx(ml[x].x - y);
+                sum = sum * f + ml[x].y * h;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = o[e] * f + (h > 0.f ? v[x][e] * h : 0.f);
+                top = y;
+            }
+        }
+        const bool good = sum > 0.f || sum != sum;
+        const int token = token_of(p, m);
+        const int64_t at = (static_cast<int64_t>(rq.first) + token) * p.s.Hq + static_cast<int64_t>(d.y) * p.G + (m - token * p.G);
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[at * D + lane + 32 * e] = from_f<T>(good ? o[e] / sum : 0.f);
+        if (lane == 0 && p.lse) p.lse[at] = good ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
+// Launches the join behind the kernel whose ranges it joins, as its programmatic dependent.
+template <typename T, int D, int TM>
+cudaError_t launch_join(const Args& p, T* out, int ranges, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranges, TM / kJoinRows);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_join_kernel<T, D, TM>, p, out);
+    note_launch();
+    return e;
+}
+
+// Scratch of `ranges` ranges: partial sums, their maxima and sums, and the cut tiles.
+inline size_t part_bytes(int D, int TM, int ranges) { return sizeof(float) * 2 * ranges * TM * D; }
+inline size_t ml_bytes(int TM, int ranges) { return sizeof(float2) * 2 * ranges * TM; }
+inline size_t scratch_bytes(int D, int TM, int ranges) { return part_bytes(D, TM, ranges) + ml_bytes(TM, ranges) + sizeof(int4) * 2 * ranges; }
+inline void set_scratch(Args& p, uint8_t* base, int D, int TM, int ranges) {
+    p.part = reinterpret_cast<float*>(base);
+    p.ml = reinterpret_cast<float2*>(base + part_bytes(D, TM, ranges));
+    p.desc = reinterpret_cast<int4*>(base + part_bytes(D, TM, ranges) + ml_bytes(TM, ranges));
+}
+
+// The end of a block's work, by all its NT threads: the cut tile whose first step is in its range, a
+// range without a step, and rows of no request (T: the outputs' type).
+template <typename T, int D, int TM, int KT, int NT>
+__device__ __forceinline__ void finish_range(const Args& p, const Range& range, bool complete, T* out) {
+    const int tid = threadIdx.x;
+    if (range.any && tid == 0 && complete) {
+        Walk<TM, KT> walk(p, range);
+        Segment g, last = {};
+        while (walk.next(p, g)) last = g;
+        if (last.b > 0 && last.a == 0 && !last.whole()) {
+            p.desc[2 * blockIdx.x] = make_int4(last.r, last.kh, last.m0, last.rows);
+            p.desc[2 * blockIdx.x + 1] = make_int4(range.ranges, 0, 0, 0);
+        }
+    }
+    // a range inside a tile that has no whole step adds nothing to it
+    if (range.any && range.from.a > 0 && range.from.a == range.to.a && range.from.r == range.to.r && range.from.kh == range.to.kh &&
+        range.from.mt == range.to.mt)
+        for (int i = tid; i < TM; i += NT) p.ml[2 * static_cast<int64_t>(blockIdx.x) * TM + i] = make_float2(-INFINITY, 0.f);
+    if (p.fill) {
+        const int64_t wide = static_cast<int64_t>(p.s.Hq) * D * sizeof(T) / 16;
+        const auto clear = [&](int64_t t0, int64_t t1) {
+            if (p.fill & 1)
+                for (int64_t e = t0 * wide + tid; e < t1 * wide; e += NT) reinterpret_cast<uint4*>(out)[e] = make_uint4(0u, 0u, 0u, 0u);
+            if (p.fill & 2)
+                for (int64_t e = t0 * p.s.Hq + tid; e < t1 * p.s.Hq; e += NT) p.lse[e] = -INFINITY;
+        };
+        const int last = p.s.R ? min(max(p.starts[p.s.R], 0), p.s.T) : 0;
+        for (int64_t t0 = last + 16 * static_cast<int64_t>(blockIdx.x); t0 < p.s.T; t0 += 16 * static_cast<int64_t>(gridDim.x))
+            clear(t0, min(t0 + 16, static_cast<int64_t>(p.s.T)));
+        for (int r = blockIdx.x; r < p.s.R; r += gridDim.x) {
+            const Request rq(p, r);
+            if (rq.pad && rq.n) clear(rq.first, rq.first + rq.n);
+        }
+    }
+}
 
 }  // namespace prefill
 }  // namespace la

@@ -201,6 +201,30 @@ def test_bad_pages_lengths_and_starts_are_reported(dt):
     la.la_check_device_status()
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_infinite_keys_and_queries(dt):
+    # a score of -infinity is a weight of 0, one of +infinity no number; other rows do not notice
+    la = _la()
+    D, cached, new = 64, 20, 90
+    x, table, starts = _case(2, 1, D, 16, [cached], [new], dt)
+    x["q"][:, :, 7] = 1.0
+    for what in (-math.inf, math.inf):
+        y = {n: t.clone() for n, t in x.items()}
+        y["K"][table[0][2], 0, 5, 7] = what  # position 37
+        _, _, _ = d = tuple(y[n].cuda() for n in ("q", "K", "V"))
+        out, lse = la.la_paged_prefill(*d, _i32(table), _i32([cached]), _i32(starts), return_lse=True)
+        with np.errstate(invalid="ignore"):
+            wo, wl, size = ref.paged_prefill(y["q"], y["K"], y["V"], table, [cached], starts)
+        err = _score_error(x, D, None)
+        tol = (2 * err + 64 * 2.0 ** -23 + (HALF[dt] if dt == "bf16" else 0)) * size + HALF[dt] * np.abs(wo)
+        got = out.double().cpu().numpy()
+        assert np.array_equal(np.isfinite(got), np.isfinite(wo))
+        fin = np.isfinite(wo)
+        assert np.all(np.abs(got - wo)[fin] <= 1.01 * tol[fin])
+        if what > 0:
+            assert not np.isfinite(got[37 - cached:]).any() and np.isfinite(got[:37 - cached]).all()
+
+
 def test_serving_run():
     """Prompts in chunks through page map, norm and rotation, append and prefill; then single tokens by the decode step;
     against one pass over the whole sequences."""
@@ -281,6 +305,21 @@ def test_other_stream_and_captured_graphs_follow_the_lengths():
         torch.cuda.synchronize()
         for o in outs:
             assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_scratch(dt):
+    la = _la()
+    from linear_attention_02_gb300 import _native
+    cached, new = [300, 20], [100, 30]
+    x, table, starts = _case(8, 2, 128, 16, cached, new, dt)
+    d = {n: t.cuda() for n, t in x.items()}
+    for _ in range(2):
+        _native.lib.la_scratch_peak_bytes(1)
+        la.la_paged_prefill(d["q"], d["K"], d["V"], _i32(table), _i32(cached), _i32(starts))
+        torch.cuda.synchronize()
+    want = la.la_paged_prefill_workspace_bytes(128, DT[dt])
+    assert want <= _native.lib.la_scratch_peak_bytes(1) <= want + (2 << 20)
 
 
 def test_repeatable():

@@ -113,6 +113,16 @@ def test_binding_refusals():
     assert freqs.dtype == torch.int64 and freqs.shape == (32,) and mag == 1.0
 
 
+def test_prefill_workspace():
+    f = lib.la_paged_prefill_workspace_bytes
+    # bf16: 152 blocks; two partial tiles each of 256 rows of D sums, a maximum and a sum, and two descriptors of 16 bytes
+    for D in (32, 64, 128):
+        assert f(D, 1, 152) == 152 * 2 * (256 * (4 * D + 8) + 16)
+    # fp32: tiles of 128 rows, two blocks an SM up to D = 64
+    assert f(64, 0, 152) == 304 * 2 * (128 * (4 * 64 + 8) + 16) and f(128, 0, 152) == 152 * 2 * (128 * (4 * 128 + 8) + 16)
+    assert f(48, 1, 152) == _native.SIZE_MAX and f(64, 2, 152) == _native.SIZE_MAX
+
+
 def test_norm_workspace():
     f = lib.la_norm_rotary_workspace_bytes
     assert f(2, 100, 8, 2, 64, 152) == 2 * 4 * 2 * 152 * 64  # rows of 64 sums, two blocks an SM for each side at most
