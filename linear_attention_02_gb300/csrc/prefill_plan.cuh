@@ -146,9 +146,9 @@ template <int TM, int KT>
 struct Cost {
     // Of a tile's queries, outputs and of the step that its border cuts: as much as 192 positions.
     static constexpr int kTile = 192;
-    // A tile of few steps (below 1536 positions) is not cut, and the others by 512 positions at least: joining
-    // costs more than they would take.  And a range is at least about a small tile, so that it has one.
-    static constexpr int kWhole = 1536 / KT, kCut = 512 / KT, kLeast = 320;
+    // A tile of few steps is not cut, and the others by four steps at least: joining costs more than they
+    // would take (bf16, 4 short requests: 15 us, 27 us cut by the step).  And a range is at least about a small tile, so that it has one.
+    static constexpr int kWhole = KT == 128 ? 12 : 16, kCut = 4, kLeast = 320;
     int tiles, each;      // positions from a tile to the next
     int64_t base, limit;  // cost of tile i: min(base + each i, limit)
     int grow;             // tiles whose cost grows
