@@ -431,11 +431,13 @@ size_t la_page_map_workspace_bytes(int R);
  *         BEFORE the new ones; a negative length marks a request that is none:
  *         nothing of its rows is read or written
  *   seq_starts [R + 1] int32                                  (read) not decreasing,
- *         within 0 .. T
+ *         within 0 .. T; starts that go back are reported, and nothing is done where the
+ *         requests' rows are then more than T
  *   out [T][Hq][D] dtype                                      (written)
  *   lse [T][Hq] fp32, nullable                                (written)
  *   scale 0 means 1 / sqrt(D);  fill: rows of no request get 0 in out (1),
  *         -infinity in lse (2) or both (3); else they are left as they are
+ * out may not overlap another tensor.
  * Positions whose page is out of range are left out; a row that sees none has out
  * 0 and lse -infinity.  What lies in the cache behind a row's position, or before
  * its window, does not reach the row, whatever it is.  An infinite element of a value row makes

@@ -50,7 +50,7 @@ constexpr int kAux = 128;             // threads of warps 12 to 15
 constexpr int kMasks = 16;            // steps whose masks are kept: more than the loader is ahead of the softmax
 constexpr float kSlack = 8.f;         // log2 by which a score may pass the maximum kept
 constexpr uint32_t kAtom = 16384;     // 128 rows x 128 bytes
-constexpr uint32_t kLimit = 1u << 22; // polls of a wait
+constexpr uint32_t kLimit = 1u << 26; // polls of a wait: the queries' warps wait as long as a tile takes
 
 template <int D>
 struct Lay {

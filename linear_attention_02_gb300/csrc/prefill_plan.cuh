@@ -169,7 +169,7 @@ struct Cost {
 template <int TM, int KT, int NT>
 struct Planner {
     int64_t sums[NT];     // inclusive sums of costs over chunks of requests
-    int64_t warps[NT / 32];
+    int64_t warps[NT / 32], tokens[NT / 32];
     Range range;
     int64_t tile_end;     // cost up to the end of tile range.to
 
@@ -228,18 +228,21 @@ struct Planner {
 
     __device__ __forceinline__ void run(const Args& p) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, each = (p.s.R + NT - 1) / NT;
-        int64_t x = 0;
+        int64_t x = 0, n = 0;
         bool bad = false;
         for (int i = 0; i < each; ++i) {
             const int r = tid * each + i;
             if (r >= p.s.R) break;
             const Request q(p, r);
             bad |= q.bad;
+            n += q.n;
             const Cost<TM, KT> cost(p, q);
             x += cost(cost.tiles);
         }
         x *= p.s.Hkv;
-        if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        if (lane == 0) tokens[warp] = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -248,12 +251,17 @@ struct Planner {
         if (lane == 31) warps[warp] = x;
         __syncthreads();
         int64_t before = 0, total = 0;
+        n = 0;
 #pragma unroll
         for (int w = 0; w < NT / 32; ++w) {
+            n += tokens[w];
             const int64_t y = warps[w];
             before += w < warp ? y : 0;
             total += y;
         }
+        // More rows than there are: starts that go back.  Nothing is done, however long that would take.
+        if (n > p.s.T) bad = true, total = 0;
+        if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
         sums[tid] = x + before;
         __syncthreads();
         if (warp < 2) {  // one finds the first border, one the last

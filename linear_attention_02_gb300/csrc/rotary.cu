@@ -20,7 +20,7 @@
 // head of the queries, then of the keys: so a token's sines and cosines are worked out once for
 // all of them, lie in registers, and a row costs no index arithmetic.  (With rows dealt
 // out one by one, and the sines read from shared memory for each, the same work took twice the
-// instructions: 389 us against LA_TIME us for 65536 x (32 + 4) x 128 bf16.)  Products are on pairs of elements
+// instructions: 389 us against 196 us for 65536 x (32 + 4) x 128 bf16.)  Products are on pairs of elements
 // (fma.rn.f32x2).  Rows that are not 16-byte aligned, or whose rotated part is not a whole
 // number of units, take units of two single elements.
 #include <cuda_bf16.h>

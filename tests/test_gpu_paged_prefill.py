@@ -199,6 +199,14 @@ def test_bad_pages_lengths_and_starts_are_reported(dt):
         with pytest.raises(la.LinAttnError, match="BAD_INDEX"):
             la.la_check_device_status()
     la.la_check_device_status()
+    # starts that go back and forth: more rows than there are, nothing is done
+    R, T = 40, 59
+    t3 = torch.zeros((R, 8), dtype=torch.int32, device="cuda")
+    keep = torch.full_like(d["q"][:T], 9.5)
+    la.la_paged_prefill(d["q"][:T].contiguous(), d["K"], d["V"], t3, _i32([0] * R), _i32([0, T] * (R // 2) + [0]), out=keep)
+    with pytest.raises(la.LinAttnError, match="BAD_INDEX"):
+        la.la_check_device_status()
+    assert bool((keep == 9.5).all())
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
