@@ -215,7 +215,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     __shared__ uint64_t s_full[STAGES], s_empty[STAGES], s_vready[STAGES];
     __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_end;
     __shared__ uint32_t s_mask[2][kMasks][4];  // positions of a step that are on a page, a bit each, as keys' and values' loader saw them
-    __shared__ volatile int s_odd[4];        // by segment: a value that was not finite was replaced
+    // A value that was not finite was replaced, in this or an earlier segment: it stays set, as the warps that
+    // replace may be segments ahead of a subtile's outputs.
+    __shared__ volatile int s_odd;
     __shared__ volatile int s_abort;
     __shared__ volatile int s_issued[2];     // tiles of keys, of values that their loaders have begun
     __shared__ uint32_t s_tmem;
@@ -231,7 +233,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         mbar_init(&s_qempty, 1);
         mbar_init(&s_end, 1);
         for (int w = 0; w < 2; ++w) mbar_init(s_sfull + w, 1), mbar_init(s_pfull + w, 4), mbar_init(s_odone + w, 1);
-        s_abort = 0, s_issued[0] = 0, s_issued[1] = 0;
+        s_abort = 0, s_odd = 0, s_issued[0] = 0, s_issued[1] = 0;
         fence_mbar_init();
     }
     if (warp == 8) {
@@ -276,7 +278,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
             const float c = fabsf(p.s.scale) * 1.4426950408889634f;
             uint32_t n_s = 0, n_o = 0, step = 0;  // phases seen, steps of the block
-            for (int seg = 0; walk.next(p, g); ++seg) {
+            while (walk.next(p, g)) {
                 const Request rq(p, g.r);
                 const Keys<KT> kt(p, rq, g.m0, min(g.m0 + TM, g.rows));
                 const int k0 = kt.k0;
@@ -316,7 +318,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], s[i + x], s[i + 4 + x]);
                     const float best = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
                     const bool raise = best > top + kSlack;  // also from -infinity
-                    if (__any_sync(0xffffffffu, raise) ) {
+                    if (__any_sync(0xffffffffu, raise)) {
                         const float f = raise ? (top == -INFINITY ? 0.f : ex2(top - best)) : 1.f;
                         if (raise) top = best;
                         sum *= f;
@@ -378,7 +380,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll
                         for (int x = 0; x < 32; ++x) o[x] = 0.f;
                     }
-                    if (s_odd[seg & 3]) {  // rare: does this row see one of the replaced values?
+                    if (s_odd) {  // rare: does this row see one of the replaced values?
                         uint32_t bits = 0;
                         for (int j = mine.a; live && j < mine.b; ++j)
                             bits |= prefill::odd_columns<bf16, D, KT>(p, V, g.r, g.kh, kt.first, kt.last, rq.end, k0 + j, from, pos, i);
@@ -593,12 +595,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             const int t = 32 * (warp - 12) + lane;
             uint32_t item = 0, n_q = 0, step = 0;
             bool ok = true;
-            for (int seg = 0; ok && walk.next(p, g); ++seg) {
+            while (ok && walk.next(p, g)) {
                 const Request rq(p, g.r);
                 const Keys<KT> k(p, rq, g.m0, min(g.m0 + TM, g.rows));
                 if (n_q && !(ok = warp_wait(&s_qempty, n_q - 1))) break;
                 ++n_q;
-                if (t == 0) s_odd[seg & 3] = 0;
                 const int subs = g.rows - g.m0 > 128 ? 2 : 1;
                 if (q_tma) {
                     if (t == 0) {
@@ -677,7 +678,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                                 }
                             }
                         }
-                        if (odd) s_odd[seg & 3] = 1;
+                        if (odd) s_odd = 1;
                         fence_proxy_async();
                     }
                     // and the next step's keys, so that the products wait once

@@ -164,6 +164,27 @@ def test_a_later_tokens_values_do_not_reach_earlier_rows(Hq, Hkv, cached, new, a
                 assert bool(torch.isnan(out[sees]).all())
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("new", [20, 150])
+def test_values_that_are_not_finite_in_some_of_many_requests(new, dt):
+    # many tiles a block, a few of them with a NaN that only the request's later rows see
+    la = _la()
+    R, H, D, page, at = 2000, 2, 64, 16, 11
+    W = -(-new // page)
+    g = torch.Generator().manual_seed(5)
+    q, K, V = (torch.randn(s, generator=g).to(DT[dt]).cuda() for s in ((R * new, H, D), (R * W, H, page, D), (R * W, H, page, D)))
+    table = torch.randperm(R * W, generator=g).to(torch.int32).cuda().view(R, W)
+    lens, starts = torch.zeros(R, dtype=torch.int32, device="cuda"), torch.arange(R + 1, device="cuda", dtype=torch.int32) * new
+    want = la.la_paged_prefill(q, K, V, table, lens, starts).view(R, new, H, D)
+    hit = torch.arange(0, R, 7, device="cuda")
+    V[table[hit, 0].long(), :, at, 9] = math.nan
+    got = la.la_paged_prefill(q, K, V, table, lens, starts).view(R, new, H, D)
+    sees = torch.zeros((R, new, H, D), dtype=torch.bool, device="cuda")
+    sees[hit, at:, :, 9] = True
+    assert torch.equal(torch.isnan(got), sees)
+    assert torch.equal(got[~sees], want[~sees])
+
+
 def test_rows_of_no_request():
     la = _la()
     cached, new = [5, -1, 9, -7], [3, 4, 0, 2]
