@@ -480,8 +480,9 @@ size_t la_paged_prefill_workspace_bytes(int D, la_dtype dtype, int num_sms);
  *   strides  host, nullable: per tensor, in the arguments' order, the distances in elements
  *         between batch rows, tokens and heads (elements of a head are adjacent); NULL:
  *         contiguous as above.  Tensors need their element's alignment only; where all
- *         are 16-byte aligned (so are their strides) and rot is a multiple of 32 bytes, rows
- *         move in 16-byte pieces
+ *         are 16-byte aligned (so are their strides) and rot is a multiple of 32 bytes (16 for
+ *         pairs of neighbours), rows move in 16-byte pieces, else in pieces of two elements
+ *         or one
  *   positions int32, device, [N] for all batch rows (position_rows 1) or [B][N]
  *         (position_rows B); a negative one marks a row without a token.  NULL
  *         (position_rows 0): first_position, first_position + 1, ...

@@ -60,7 +60,7 @@ def _rand(shape, dt, seed, scale=1.0):
 SHAPES = [  # B (0: packed), N, Hq, Hk, D, rot
     (0, 1, 1, 1, 32, 32), (0, 5, 3, 1, 64, 64), (0, 300, 16, 4, 64, 64), (0, 7, 32, 4, 128, 128), (1, 1, 1, 1, 128, 2),
     (2, 33, 2, 2, 64, 32), (3, 129, 4, 2, 32, 16), (2, 500, 3, 1, 128, 64), (0, 77, 5, 5, 64, 20), (2, 19, 2, 1, 128, 126),
-    (0, 1000, 8, 1, 32, 2)]
+    (0, 1000, 8, 1, 32, 2), (0, 50, 3, 2, 64, 24), (2, 21, 2, 2, 128, 40)]
 
 
 def _positions(kind, B, N, seed):
@@ -99,6 +99,29 @@ def test_rotary(B, N, Hq, Hk, D, rot, dt, layout):
             _near(y, ref.rotary(x64, a, layout, m), tol, dt)
             _near(z, ref.rotary(x64, -a, layout, m), tol, dt)
     la.la_check_device_status()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D,rot", [(32, 8), (64, 20), (64, 32), (128, 2), (128, 40), (128, 62)])
+def test_what_does_not_turn_is_kept(D, rot, dt, layout):
+    # every element of the rest as it was, whatever lies beside it; the turned part does not notice
+    la = _la()
+    N, H = 19, 3
+    x = _rand((N, H, D), dt, 7).cuda()
+    freqs, mag = la.la_rotary_frequencies(rot, scaling="by_parts", factor=4.0, original_len=512)
+    want, _ = la.la_forward_rotary(x, None, freqs, layout=layout, magnitude=mag)
+    for what in (math.inf, -math.inf, math.nan, -0.0):
+        y = x.clone()
+        for n in range(N):
+            y[n, :, rot + (5 * n) % (D - rot)] = what
+        for f in (la.la_forward_rotary, la.la_backward_rotary):
+            got, _ = f(y, None, freqs, layout=layout, magnitude=mag)
+            a, b = got[..., rot:], y[..., rot:]  # a NaN stays one, in whichever of its bits
+            assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(0.0, math.inf, -math.inf), b.nan_to_num(0.0, math.inf, -math.inf))
+            assert torch.equal(torch.signbit(a)[~a.isnan()], torch.signbit(b)[~b.isnan()])
+        got, _ = la.la_forward_rotary(y, None, freqs, layout=layout, magnitude=mag)
+        assert torch.equal(got[..., :rot], want[..., :rot])
 
 
 def _norm_bounds(x, dy, w, a, layout, mag, eps):
