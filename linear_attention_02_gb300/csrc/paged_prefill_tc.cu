@@ -455,7 +455,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_O = idesc_bf16(128, DP, false, true);
             const uint64_t dq = sdesc(smem_u32(sm), 16, 1024), dk = sdesc(smem_u32(ring), 16, 1024), dv = sdesc(smem_u32(ring), kAtom, 1024);
             constexpr uint32_t STEP = Ly::TILE >> 4;  // of a descriptor, from tile to tile
-            uint32_t n_q = 0, n_p[2] = {0, 0}, sk = 0, tk = 0, sv = 1, n_v = 0;  // stages of the next keys and values, turns of the ring, value tiles
+            uint32_t n_q = 0, n_p = 0, sk = 0, tk = 0, sv = 1, n_v = 0;  // stages of the next keys and values, turns of the ring, value tiles
             bool ok = true;
             while (ok && walk.next(p, g)) {
                 const Request rq(p, g.r);
@@ -465,7 +465,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 fence_after_sync();
                 if (elect()) {
                     const uint64_t k = dk + sk * STEP;
-#pragma unroll
+#pragma unroll 1
                     for (int w = 0; w < 2; ++w)
                         if ((w ? part1 : part0).on(g.a)) {
                             mma_scores<DP / 16>(tm + 128 * w, dq + w * STEP, k, ID_S);
@@ -480,10 +480,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     const bool more = j + 1 < g.b;
                     // the values of this step and the keys of the next, mostly here before the weights
                     if (!(ok = warp_wait(s_vready + sv, Ly::value_turn(2 * n_v + 1)))) break;
-#pragma unroll
+#pragma unroll 1
                     for (int w = 0; w < 2; ++w) {
                         const Part& part = w ? part1 : part0;
-                        if (part.on(j) && !(ok = warp_wait(s_pfull + w, n_p[w]++))) break;
+                        const bool on = part.on(j);
+                        if (on && !(ok = warp_wait(s_pfull + w, n_p >> w & 1u))) break;
+                        if (on) n_p ^= 1u << w;
                         fence_after_sync();
                         if (elect()) {
                             if (part.on(j)) mma_values(tm + Ly::T_O + DP * w, tm + 128 * w, dv + sv * STEP, ID_O, j > part.a ? 1u : 0u);

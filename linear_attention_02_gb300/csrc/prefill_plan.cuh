@@ -165,45 +165,49 @@ struct Cost {
     }
 };
 
-// Finds a block's range, by all its NT threads.
+// Finds a block's range, by all its NT threads.  What it costs is paid by the smallest calls, and it
+// is code that runs once: so sums over warps and the search in them are left to the two warps that look for borders.
 template <int TM, int KT, int NT>
 struct Planner {
-    int64_t sums[NT];     // inclusive sums of costs over chunks of requests
-    int64_t warps[NT / 32], tokens[NT / 32];
+    static_assert(NT / 32 <= 32, "a lane a warp");
+    int64_t sums[NT];     // of costs over chunks of requests, inclusive within a warp
+    int64_t warps[NT / 32];
     Range range;
-    int64_t tile_end;     // cost up to the end of tile range.to
 
-    // The border at cost u < total, by a warp; `end` gets the cost up to its tile's end.
-    __device__ __forceinline__ Place locate(const Args& p, int64_t u, int64_t& end) const {
+    __device__ __forceinline__ static int64_t scan(int64_t x, int lane) {  // inclusive, over a warp
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    }
+
+    // The border at cost u < total, by a warp, from the sum `s` of the costs of lane's and earlier warps' chunks; `end`
+    // gets the cost up to its tile's end.
+    __device__ __forceinline__ Place locate(const Args& p, int64_t u, int64_t s, int64_t& end) const {
         const int lane = threadIdx.x & 31, each = (p.s.R + NT - 1) / NT;
-        int c = __popc(__ballot_sync(0xffffffffu, lane < NT / 32 && sums[min(lane, NT / 32 - 1) * 32 + 31] <= u));
-        c = min(c, NT / 32 - 1);
-        c = 32 * c + min(__popc(__ballot_sync(0xffffffffu, sums[32 * c + lane] <= u)), 31);
-        int64_t before = c ? sums[c - 1] : 0, total = 0;
-        int r = c * each;
-        for (;; r += 32) {  // 32 requests at once
+        // the warp, the chunk, and with more than one request in it the request whose cost passes u
+        const int w = min(__popc(__ballot_sync(0xffffffffu, s <= u)), NT / 32 - 1);
+        int64_t before = w ? __shfl_sync(0xffffffffu, s, max(w - 1, 0)) : 0;
+        s = before + sums[32 * w + lane];
+        const int c = min(__popc(__ballot_sync(0xffffffffu, s <= u)), 31);
+        if (c) before = __shfl_sync(0xffffffffu, s, c - 1);
+        int r = (32 * w + c) * each;
+        const int r1 = min(r + each, p.s.R);
+        while (each > 1) {  // 32 requests at once
             int64_t x = 0;
-            if (r + lane < min((c + 1) * each, p.s.R)) {
+            if (r + lane < r1) {
                 const Cost<TM, KT> cost(p, Request(p, r + lane));
                 x = cost(cost.tiles) * p.s.Hkv;
             }
-            int64_t s = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += y;
-            }
-            const int n = __popc(__ballot_sync(0xffffffffu, before + s <= u));
-            if (n == 32 && r + 32 < (c + 1) * each) {
-                before += __shfl_sync(0xffffffffu, s, 31);
-                continue;
-            }
-            const int i = min(n, 31);
-            total = __shfl_sync(0xffffffffu, x, i);
-            before += __shfl_sync(0xffffffffu, s, i) - total;
-            r = min(r + i, p.s.R - 1);
-            break;
+            x = before + scan(x, lane);
+            const int n = __popc(__ballot_sync(0xffffffffu, x <= u));
+            if (n) before = __shfl_sync(0xffffffffu, x, n - 1);
+            r += n;
+            if (n < 32 || r >= r1) break;
         }
+        r = min(r, p.s.R - 1);
         const Request q(p, r);
         const Cost<TM, KT> cost(p, q);
         const int64_t one = max(cost(cost.tiles), static_cast<int64_t>(1));
@@ -228,48 +232,31 @@ struct Planner {
 
     __device__ __forceinline__ void run(const Args& p) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, each = (p.s.R + NT - 1) / NT;
-        int64_t x = 0, n = 0;
-        bool bad = false;
+        int64_t x = 0;
+        bool bad = false, back = false;
         for (int i = 0; i < each; ++i) {
             const int r = tid * each + i;
             if (r >= p.s.R) break;
             const Request q(p, r);
             bad |= q.bad;
-            n += q.n;
+            back |= p.starts[r + 1] < p.starts[r];
             const Cost<TM, KT> cost(p, q);
             x += cost(cost.tiles);
         }
-        x *= p.s.Hkv;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-        if (lane == 0) tokens[warp] = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
+        x = scan(x * p.s.Hkv, lane);
+        sums[tid] = x;
         if (lane == 31) warps[warp] = x;
-        __syncthreads();
-        int64_t before = 0, total = 0;
-        n = 0;
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w) {
-            n += tokens[w];
-            const int64_t y = warps[w];
-            before += w < warp ? y : 0;
-            total += y;
-        }
-        // More rows than there are: starts that go back.  Nothing is done, however long that would take.
-        if (n > p.s.T) bad = true, total = 0;
         if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
-        sums[tid] = x + before;
-        __syncthreads();
+        // Starts that go back can name more rows than there are.  Nothing is done, however long that would take.
+        const bool none = __syncthreads_or(back);
         if (warp < 2) {  // one finds the first border, one the last
+            const int64_t s = scan(lane < NT / 32 && !none ? warps[min(lane, NT / 32 - 1)] : 0, lane);
+            const int64_t total = __shfl_sync(0xffffffffu, s, 31);
             const int64_t per = max(divide(total + gridDim.x - 1, gridDim.x), static_cast<int64_t>(Cost<TM, KT>::kLeast));
             const int64_t u = per * (blockIdx.x + warp);
             Place at = {p.s.R, 0, 0, 0};
             int64_t end = 0;
-            if (u < total) at = locate(p, u, end);
+            if (u < total) at = locate(p, u, s, end);
             if (lane == 0) {
                 if (warp == 0) {
                     range.from = at;
