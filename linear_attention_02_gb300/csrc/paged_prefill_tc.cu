@@ -8,6 +8,7 @@
 //   0-3, 4-7  softmax of subtile 0 and 1, a row a thread, and the rows' outputs
 //   8         every matrix product, issued by one thread
 //   9, 10     keys and values by TMA, page by page, into a ring of tiles
+//   11        the range's segments, worked out for all the others
 //   12 to 15  queries, and the values of tiles that some row sees only in part
 // S = Q K^T goes to tensor memory, a thread turns its row's 128 scores into weights there, and
 // O += P V reads the weights from tensor memory.  The two subtiles take turns: while one's
@@ -63,6 +64,10 @@ struct Lay {
     // Scores of a tile that a row sees in part are masked in tensor memory, by a short loop, instead of in registers.
     // Measured, us, in memory and in registers: 32 x 2048 of 16 heads of 64 516, 562; 16 x 2048 of 128 356, 341.
     static constexpr bool MASK_THERE = DP == 64;
+    // The kernel's code is more than an SM's nearest instruction memory holds, and short tiles run through most of it.  So what
+    // the subtiles do is one piece of code where it can be.  Of the products, one for both or one each, measured, us:
+    // 32 x 2048 of 16 heads of 64 460, 510; 256 over 65k of 16 heads of 128 131, 127 and long chunks of 128 2277, 2199.
+    static constexpr int COPIES = DP == 64 ? 1 : 2;
     static constexpr uint32_t T_O = 256;            // column of subtile 0's outputs in tensor memory
     // How often a stage has held values before tile `it` (an odd one) of the ring: keys and values
     // take turns in a stage if the stages are odd in number.
@@ -191,19 +196,31 @@ __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint64_t b, u
                  : "memory");
 }
 
-// What steps of a segment a subtile takes part in: [a, b) of the tile's steps.
-struct Part {
-    int a, b, rows;  // rows of the subtile
-    Keys<KT> k;
-    __device__ __forceinline__ Part(const Args& p, const Request& q, const Segment& g, int k0, int w)
-        : rows(min(max(g.rows - g.m0 - 128 * w, 0), 128)),
-          k(p, q, rows ? g.m0 + 128 * w : g.m0, rows ? g.m0 + 128 * w + rows : g.m0 + 1) {
-        a = max(g.a, k.k0 - k0);
-        b = rows ? min(g.b, k.k1 - k0) : a;
-        b = max(b, a);
+// A segment of the block's range as its roles need it, worked out by one warp for all of them.
+struct Job {
+    Segment g;                    // g.rows < 0: no further one
+    int row, cached, end;         // the request's first row of T, positions before its tokens, room of its table
+    int k0, first, last, lo, hi;  // the tile's first step, positions of its first and last row, positions that it sees
+    // Of each subtile: steps [a, b) of the tile's in which it takes part, rows, positions of its first and last row.
+    int a[2], b[2], n[2], from[2], to[2];
+    __device__ __forceinline__ void set(const Args& p, const Segment& s) {
+        const Request q(p, s.r);
+        const Keys<KT> k(p, q, s.m0, min(s.m0 + TM, s.rows));
+        g = s, row = q.first, cached = q.cached, end = q.end;
+        k0 = k.k0, first = k.first, last = k.last, lo = k.lo, hi = k.hi;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            n[w] = min(max(s.rows - s.m0 - 128 * w, 0), 128);
+            const int m = n[w] ? s.m0 + 128 * w : s.m0;
+            const Keys<KT> y(p, q, m, m + max(n[w], 1));
+            from[w] = y.first, to[w] = y.last;
+            a[w] = max(s.a, y.k0 - k0);
+            b[w] = max(a[w], n[w] ? min(s.b, y.k1 - k0) : a[w]);
+        }
     }
-    __device__ __forceinline__ bool on(int j) const { return j >= a && j < b; }
 };
+constexpr int kJobs = 8;
+constexpr int kReaders = 15;  // warps that read a job
 
 template <int D>
 __global__ void __launch_bounds__(NT, 1)
@@ -216,6 +233,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     using Walk = prefill::Walk<TM, KT>;
     extern __shared__ uint8_t sm_raw[];
     __shared__ uint64_t s_full[STAGES], s_empty[STAGES], s_vready[STAGES];
+    __shared__ Job s_jobs[kJobs];
+    __shared__ uint64_t s_jfull[kJobs], s_jfree[kJobs];
     __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_end;
     __shared__ uint32_t s_mask[2][kMasks][4];  // positions of a step that are on a page, a bit each, as keys' and values' loader saw them
     // A value that was not finite was replaced, in this or an earlier segment: it stays set, as the warps that
@@ -232,6 +251,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) mbar_init(s_full + i, 1), mbar_init(s_empty + i, 1), mbar_init(s_vready + i, kAux / 32);
+        for (int i = 0; i < kJobs; ++i) mbar_init(s_jfull + i, 1), mbar_init(s_jfree + i, kReaders);
         mbar_init(&s_qfull, kAux / 32);
         mbar_init(&s_qempty, 1);
         mbar_init(&s_end, 1);
@@ -268,32 +288,41 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
     };
 
+    // The role's next segment, copied; its place is free then.
+    uint32_t n_job = 0;
+    const auto next = [&](Job& x) {
+        const uint32_t at = n_job % kJobs;
+        if (!warp_wait(s_jfull + at, n_job / kJobs)) return false;
+        x = s_jobs[at];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_jfree + at);
+        ++n_job;
+        return x.g.rows >= 0;
+    };
+
     // The launch's 128 registers a thread become 192 for the softmax and 64 for the rest.
     if (range.any) {
         if (warp < 8) {
             // ---------------------------------------------------------------- softmax
             asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-            Walk walk(p, range);
-            Segment g;
             const int w = warp >> 2, row = 32 * (warp & 3) + lane;
             const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's quarter of the lanes
             const uint32_t ts = tm + 128 * w + lanes, to = tm + Ly::T_O + DP * w + lanes;
             const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
             const float c = fabsf(p.s.scale) * 1.4426950408889634f;
             uint32_t n_s = 0, n_o = 0, step = 0;  // phases seen, steps of the block
-            while (walk.next(p, g)) {
-                const Request rq(p, g.r);
-                const Keys<KT> kt(p, rq, g.m0, min(g.m0 + TM, g.rows));
-                const int k0 = kt.k0;
-                const Part mine(p, rq, g, k0, w);
-                const int m = g.m0 + 128 * w + row;
-                const bool live = row < mine.rows;
-                const int pos = rq.cached + token_of(p, m);              // of the row
+            for (Job x; next(x);) {
+                const Segment& g = x.g;
+                const int k0 = x.k0, m = g.m0 + 128 * w + row;
+                const int part_a = w ? x.a[1] : x.a[0], part_b = w ? x.b[1] : x.b[0];
+                const int part_from = w ? x.from[1] : x.from[0], part_to = w ? x.to[1] : x.to[0];
+                const bool live = row < (w ? x.n[1] : x.n[0]);
+                const int pos = x.cached + token_of(p, m);             // of the row
                 const int from = p.s.window ? pos - p.s.window : -1;  // it sees positions past this one
                 float top = -INFINITY, sum = 0.f;
                 bool ok = true;
                 for (int j = g.a; j < g.b; ++j, ++step) {
-                    if (!mine.on(j)) continue;
+                    if (j < part_a || j >= part_b) continue;
                     if (!(ok = warp_wait(s_sfull + w, n_s++))) break;
                     fence_after_sync();
                     float s[128];
@@ -305,7 +334,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     const int x0 = (k0 + j) * KT;
                     const uint32_t* mask = s_mask[0][step % kMasks];
                     const uint32_t m0 = mask[0], m1 = mask[1], m2 = mask[2], m3 = mask[3];
-                    const bool all = x0 + KT - 1 <= mine.k.first && (p.s.window == 0 || x0 > mine.k.last - p.s.window) &&
+                    const bool all = x0 + KT - 1 <= part_from && (p.s.window == 0 || x0 > part_to - p.s.window) &&
                                      (m0 & m1 & m2 & m3) == 0xFFFFFFFFu;
                     const int c0 = from + 1 - x0, c1 = pos - x0;  // columns [c0, c1] of the tile are seen
                     const auto seen = [&](int i) { return (i ? i == 1 ? m1 : i == 2 ? m2 : m3 : m0) & span(c0 - 32 * i, c1 - 32 * i); };
@@ -354,7 +383,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         const float f = raise ? (top == -INFINITY ? 0.f : ex2(top - best)) : 1.f;
                         if (raise) top = best;
                         sum *= f;
-                        if (j > mine.a) {  // the product before this one has finished: the scores came behind it
+                        if (j > part_a) {  // the product before this one has finished: the scores came behind it
 #pragma unroll 1
                             for (int i = 0; i < DP; i += 16) {
                                 float o[16];
@@ -391,7 +420,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 }
                 if (!ok) break;
                 // ------------------------------------------------------------ the rows' outputs
-                const bool some = mine.b > mine.a;
+                const bool some = part_b > part_a;
                 if (some) {
                     if (!warp_wait(s_odone + w, n_o++)) break;
                     fence_after_sync();
@@ -401,7 +430,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 const bool good = sum > 0.f || sum != sum;
                 const float inv = !whole ? 1.f : good ? 1.f / sum : 0.f;
                 const int token = token_of(p, m);
-                const int64_t at = (static_cast<int64_t>(rq.first) + token) * p.s.Hq + static_cast<int64_t>(g.kh) * p.G + (m - token * p.G);
+                const int64_t at = (static_cast<int64_t>(x.row) + token) * p.s.Hq + static_cast<int64_t>(g.kh) * p.G + (m - token * p.G);
                 float* part = p.part + (static_cast<int64_t>(slot) * TM + 128 * w + row) * D;
 #pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
@@ -414,8 +443,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     }
                     if (s_odd) {  // rare: does this row see one of the replaced values?
                         uint32_t bits = 0;
-                        for (int j = mine.a; live && j < mine.b; ++j)
-                            bits |= prefill::odd_columns<bf16, D, KT>(p, V, g.r, g.kh, kt.first, kt.last, rq.end, k0 + j, from, pos, i);
+                        for (int j = part_a; live && j < part_b; ++j)
+                            bits |= prefill::odd_columns<bf16, D, KT>(p, V, g.r, g.kh, x.first, x.last, x.end, k0 + j, from, pos, i);
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
                             if (bits >> x & 1u) o[x] = __uint_as_float(0x7FFFFFFFu);
@@ -448,8 +477,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             }
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-            Walk walk(p, range);
-            Segment g;
             if (warp == 8) {
             // ---------------------------------------------------------------- products
             constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false), ID_O = idesc_bf16(128, DP, false, true);
@@ -457,17 +484,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             constexpr uint32_t STEP = Ly::TILE >> 4;  // of a descriptor, from tile to tile
             uint32_t n_q = 0, n_p = 0, sk = 0, tk = 0, sv = 1, n_v = 0;  // stages of the next keys and values, turns of the ring, value tiles
             bool ok = true;
-            while (ok && walk.next(p, g)) {
-                const Request rq(p, g.r);
-                const int k0 = Keys<KT>(p, rq, g.m0, min(g.m0 + TM, g.rows)).k0;
-                const Part part0(p, rq, g, k0, 0), part1(p, rq, g, k0, 1);
+            for (Job x; ok && next(x);) {
+                const Segment& g = x.g;
                 if (!(ok = warp_wait(&s_qfull, n_q++) && warp_wait(s_full + sk, tk))) break;
                 fence_after_sync();
                 if (elect()) {
                     const uint64_t k = dk + sk * STEP;
 #pragma unroll 1
                     for (int w = 0; w < 2; ++w)
-                        if ((w ? part1 : part0).on(g.a)) {
+                        if (g.a >= (w ? x.a[1] : x.a[0]) && g.a < (w ? x.b[1] : x.b[0])) {
                             mma_scores<DP / 16>(tm + 128 * w, dq + w * STEP, k, ID_S);
                             mma_commit(s_sfull + w);
                         }
@@ -480,20 +505,20 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     const bool more = j + 1 < g.b;
                     // the values of this step and the keys of the next, mostly here before the weights
                     if (!(ok = warp_wait(s_vready + sv, Ly::value_turn(2 * n_v + 1)))) break;
-#pragma unroll 1
+#pragma unroll Ly::COPIES
                     for (int w = 0; w < 2; ++w) {
-                        const Part& part = w ? part1 : part0;
-                        const bool on = part.on(j);
+                        const int part_a = w ? x.a[1] : x.a[0], part_b = w ? x.b[1] : x.b[0];
+                        const bool on = j >= part_a && j < part_b, on_next = j + 1 >= part_a && j + 1 < part_b;
                         if (on && !(ok = warp_wait(s_pfull + w, n_p >> w & 1u))) break;
                         if (on) n_p ^= 1u << w;
                         fence_after_sync();
                         if (elect()) {
-                            if (part.on(j)) mma_values(tm + Ly::T_O + DP * w, tm + 128 * w, dv + sv * STEP, ID_O, j > part.a ? 1u : 0u);
-                            if (more && part.on(j + 1)) {
+                            if (on) mma_values(tm + Ly::T_O + DP * w, tm + 128 * w, dv + sv * STEP, ID_O, j > part_a ? 1u : 0u);
+                            if (more && on_next) {
                                 mma_scores<DP / 16>(tm + 128 * w, dq + w * STEP, dk + sk * STEP, ID_S);
                                 mma_commit(s_sfull + w);
                             }
-                            if (part.on(j) && j + 1 == part.b) mma_commit(s_odone + w);
+                            if (on && j + 1 == part_b) mma_commit(s_odone + w);
                             if (w == 1) {
                                 mma_commit(s_empty + sv);
                                 if (more) mma_commit(s_empty + sk);
@@ -533,9 +558,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 __threadfence_block();
                 return __all_sync(0xffffffffu, there) != 0;
             };
-            while (ok && walk.next(p, g)) {
-                const Request rq(p, g.r);
-                const Keys<KT> k(p, rq, g.m0, min(g.m0 + TM, g.rows));
+            for (Job k; ok && next(k);) {
+                const Segment& g = k.g;
                 const int* table = p.table + static_cast<int64_t>(g.r) * p.s.max_pages;
                 // Page i of the request; -1 if it is none of the pool, -2 if no row sees a position of it.
                 const auto page_of = [&](int64_t i) {
@@ -564,9 +588,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         if (!(ok = warp_wait(s_empty + sg, it / STAGES + 1))) break;
                         if (lane < 4) {  // 32 positions a word: those on a lost page, or past the table, are off
                             uint32_t m = 0xFFFFFFFFu;
-                            for (int i = 0; i < 32 && (lost || x0 + KT > rq.end); ++i) {
+                            for (int i = 0; i < 32 && (lost || x0 + KT > k.end); ++i) {
                                 const int y = 32 * lane + i;
-                                if ((lost >> (y / rows) & 1u) || x0 + y >= rq.end) m &= ~(1u << i);
+                                if ((lost >> (y / rows) & 1u) || x0 + y >= k.end) m &= ~(1u << i);
                             }
                             s_mask[kv][step % kMasks][lane] = m;
                         }
@@ -594,7 +618,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             const int y = x0 + 32 * i + lane;
                             ids[i] = page_of(y >> log2p);
                             bad |= ids[i] == -1;
-                            mask[i] = __ballot_sync(0xffffffffu, ids[i] != -1 && y < rq.end);
+                            mask[i] = __ballot_sync(0xffffffffu, ids[i] != -1 && y < k.end);
                         }
                         if (!(ok = in_turn(it))) break;
                         if (!(ok = warp_wait(s_empty + sg, it / STAGES + 1))) break;
@@ -624,14 +648,28 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             // copies under way end before the block does: the last ones of each stage (it is the first tile not issued)
             for (uint32_t i = it > 2 * STAGES ? it - 2 * STAGES : kv; i < it; i += 2)
                 if (i + STAGES >= it && !mbar_wait(s_full + i % STAGES, i / STAGES & 1u, kLimit)) fail();
-        } else if (warp >= 12) {
+        } else if (warp == 11) {
+            // ---------------------------------------------------------------- the segments, for all
+            Walk walk(p, range);
+            Segment g;
+            bool any = true;
+            for (uint32_t i = 0; any; ++i) {
+                any = walk.next(p, g);
+                Job x = {};
+                x.g.rows = -1;
+                if (any) x.set(p, g);
+                if (!warp_wait(s_jfree + i % kJobs, i / kJobs + 1)) break;
+                if (lane == 0) s_jobs[i % kJobs] = x;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_jfull + i % kJobs);
+            }
+        } else {
             // ---------------------------------------------------------------- queries, values seen in part
             const int t = 32 * (warp - 12) + lane;
             uint32_t item = 0, n_q = 0, step = 0;
             bool ok = true;
-            while (ok && walk.next(p, g)) {
-                const Request rq(p, g.r);
-                const Keys<KT> k(p, rq, g.m0, min(g.m0 + TM, g.rows));
+            for (Job k; ok && next(k);) {
+                const Segment& g = k.g;
                 if (n_q && !(ok = warp_wait(&s_qempty, n_q - 1))) break;
                 ++n_q;
                 const int subs = g.rows - g.m0 > 128 ? 2 : 1;
@@ -640,7 +678,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         mbar_arrive_expect_tx(&s_qfull, subs * Ly::TILE);  // (one of the barrier's arrivals, the others are the other warps')
                         for (int w = 0; w < subs; ++w)
                             for (int a = 0; a < ATOMS; ++a)
-                                tma_load_3d(sm + w * Ly::TILE + a * kAtom, &qmap, &s_qfull, 64 * a, g.kh * p.G, rq.first + token_of(p, g.m0 + 128 * w));
+                                tma_load_3d(sm + w * Ly::TILE + a * kAtom, &qmap, &s_qfull, 64 * a, g.kh * p.G, k.row + token_of(p, g.m0 + 128 * w));
                     } else if (lane == 0) {
                         mbar_arrive(&s_qfull);
                     }
@@ -657,7 +695,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             const int token = token_of(p, m);
                             if (m < g.rows && ch < D / 8)
                                 x[i] = *reinterpret_cast<const uint4*>(
-                                    q + ((static_cast<int64_t>(rq.first) + token) * p.s.Hq + static_cast<int64_t>(g.kh) * p.G + (m - token * p.G)) * D + ch * 8);
+                                    q + ((static_cast<int64_t>(k.row) + token) * p.s.Hq + static_cast<int64_t>(g.kh) * p.G + (m - token * p.G)) * D + ch * 8);
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
