@@ -12,7 +12,15 @@
 //   12 to 15  queries, and the values of tiles that some row sees only in part
 // S = Q K^T goes to tensor memory, a thread turns its row's 128 scores into weights there, and
 // O += P V reads the weights from tensor memory.  The two subtiles take turns: while one's
-// scores become weights, the tensor core works for the other.
+// scores become weights, the tensor core works for the other.  The products are issued by an elected
+// thread (by lane 0 of a diverged warp they took three times as long); two warps load, as one does not keep
+// up with 2 KB copies of pages of 16 positions; they share a ring, whose stages serve either.
+//
+// Measured: chunks of 2048 tokens over 30 to 63 thousand positions, 32 heads of 128, 4 key heads: 2.12 ms,
+// 1.49 PFLOP/s.  32 prompts of 2048, 16 heads of 64: 465 us, 590 TFLOP/s, bound by the softmax's latency: a
+// step of a subtile is about 1400 cycles of loads, exponentials (4 a clock and quarter of an SM, 512 cycles at
+// least) and stores, and 800 until its next scores are there.  48 requests of 1 to 8 tokens over 500 to 16000
+// positions: 156 us, 5.2 TB/s.
 //
 // The maximum is kept lazily: it is raised, and the sums so far rescaled in tensor memory, only when
 // a score passes it by more than 2^8.  The weights are rounded to bf16 for the product with
@@ -61,12 +69,10 @@ struct Lay {
     static constexpr int STAGES = D == 128 ? 5 : 8;
     static constexpr int Q = 2 * TILE;
     static constexpr int SMEM = Q + STAGES * TILE + 1024;
-    // Scores of a tile that a row sees in part are masked in tensor memory, by a short loop, instead of in registers.
-    // Measured, us, in memory and in registers: 32 x 2048 of 16 heads of 64 516, 562; 16 x 2048 of 128 356, 341.
-    static constexpr bool MASK_THERE = DP == 64;
-    // The kernel's code is more than an SM's nearest instruction memory holds, and short tiles run through most of it.  So what
-    // the subtiles do is one piece of code where it can be.  Of the products, one for both or one each, measured, us:
-    // 32 x 2048 of 16 heads of 64 460, 510; 256 over 65k of 16 heads of 128 131, 127 and long chunks of 128 2277, 2199.
+    // Copies of the products' code, one for both subtiles or one each.  The whole kernel's code is more than the
+    // instruction memory next to an SM's quarters holds, and short tiles run through most of it, so less of it is faster;
+    // over long tiles the products' few addresses count.  Measured, us, with one and two: 32 x 2048 of 16 heads of 64 460,
+    // 510; of 128, 256 over 65k of 16 heads 131, 127, long chunks 2277, 2199.
     static constexpr int COPIES = DP == 64 ? 1 : 2;
     static constexpr uint32_t T_O = 256;            // column of subtile 0's outputs in tensor memory
     // How often a stage has held values before tile `it` (an odd one) of the ring: keys and values
@@ -203,8 +209,7 @@ struct Job {
     int k0, first, last, lo, hi;  // the tile's first step, positions of its first and last row, positions that it sees
     // Of each subtile: steps [a, b) of the tile's in which it takes part, rows, positions of its first and last row.
     int a[2], b[2], n[2], from[2], to[2];
-    __device__ __forceinline__ void set(const Args& p, const Segment& s) {
-        const Request q(p, s.r);
+    __device__ __forceinline__ void set(const Args& p, const Request& q, const Segment& s) {
         const Keys<KT> k(p, q, s.m0, min(s.m0 + TM, s.rows));
         g = s, row = q.first, cached = q.cached, end = q.end;
         k0 = k.k0, first = k.first, last = k.last, lo = k.lo, hi = k.hi;
@@ -326,43 +331,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     if (!(ok = warp_wait(s_sfull + w, n_s++))) break;
                     fence_after_sync();
                     float s[128];
-                    const auto load = [&]() {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) ld32(ts + 32 * i, s + 32 * i);
-                    };
-                    if (!Ly::MASK_THERE) load();
+                    for (int i = 0; i < 4; ++i) ld32(ts + 32 * i, s + 32 * i);
                     const int x0 = (k0 + j) * KT;
                     const uint32_t* mask = s_mask[0][step % kMasks];
                     const uint32_t m0 = mask[0], m1 = mask[1], m2 = mask[2], m3 = mask[3];
                     const bool all = x0 + KT - 1 <= part_from && (p.s.window == 0 || x0 > part_to - p.s.window) &&
                                      (m0 & m1 & m2 & m3) == 0xFFFFFFFFu;
-                    const int c0 = from + 1 - x0, c1 = pos - x0;  // columns [c0, c1] of the tile are seen
-                    const auto seen = [&](int i) { return (i ? i == 1 ? m1 : i == 2 ? m2 : m3 : m0) & span(c0 - 32 * i, c1 - 32 * i); };
-                    if (Ly::MASK_THERE) {
-                        if (!all) {
-                            uint32_t b0 = seen(0), b1 = seen(1), b2 = seen(2), b3 = seen(3);
-#pragma unroll 1
-                            for (int i = 0; i < 128; i += 16) {
-                                const uint32_t bits = b0 & 0xFFFFu;
-                                b0 = __funnelshift_r(b0, b1, 16), b1 = __funnelshift_r(b1, b2, 16), b2 = __funnelshift_r(b2, b3, 16), b3 >>= 16;
-                                const bool every = __all_sync(0xffffffffu, bits == 0xFFFFu), any = __any_sync(0xffffffffu, bits);
-                                if (every) continue;
-                                float o[16];
-                                uint32_t v[16];
-#pragma unroll
-                                for (int x = 0; x < 16; ++x) o[x] = 0.f;
-                                if (any) tmem_ld16(ts + i, o);
-#pragma unroll
-                                for (int x = 0; x < 16; ++x) v[x] = bits >> x & 1u ? __float_as_uint(o[x]) : 0xFF800000u;
-                                st16(ts + i, v);
-                            }
-                            st_wait();
-                        }
-                        load();
-                    }
                     ld_wait(s);
-                    if (!Ly::MASK_THERE && !all) {
-                        const uint32_t bits[4] = {seen(0), seen(1), seen(2), seen(3)};
+                    if (!all) {
+                        const int c0 = from + 1 - x0, c1 = pos - x0;  // columns [c0, c1] of the tile are seen
+                        const uint32_t bits[4] = {m0 & span(c0, c1), m1 & span(c0 - 32, c1 - 32), m2 & span(c0 - 64, c1 - 64),
+                                                  m3 & span(c0 - 96, c1 - 96)};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             if (__all_sync(0xffffffffu, bits[i] == 0xFFFFFFFFu)) continue;
@@ -654,10 +634,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             Segment g;
             bool any = true;
             for (uint32_t i = 0; any; ++i) {
+                const Request rq = walk.q;  // of the segment that comes
                 any = walk.next(p, g);
-                Job x = {};
+                Job x;
                 x.g.rows = -1;
-                if (any) x.set(p, g);
+                if (any) x.set(p, rq, g);
                 if (!warp_wait(s_jfree + i % kJobs, i / kJobs + 1)) break;
                 if (lane == 0) s_jobs[i % kJobs] = x;
                 __syncwarp();
