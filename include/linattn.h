@@ -431,8 +431,7 @@ size_t la_page_map_workspace_bytes(int R);
  *         BEFORE the new ones; a negative length marks a request that is none:
  *         nothing of its rows is read or written
  *   seq_starts [R + 1] int32                                  (read) not decreasing,
- *         within 0 .. T; starts that go back are reported, and nothing is done where the
- *         requests' rows are then more than T
+ *         within 0 .. T; if any go back, that is reported and no request is done
  *   out [T][Hq][D] dtype                                      (written)
  *   lse [T][Hq] fp32, nullable                                (written)
  *   scale 0 means 1 / sqrt(D);  fill: rows of no request get 0 in out (1),
@@ -441,7 +440,7 @@ size_t la_page_map_workspace_bytes(int R);
  * Positions whose page is out of range are left out; a row that sees none has out
  * 0 and lse -infinity.  What lies in the cache behind a row's position, or before
  * its window, does not reach the row, whatever it is.  An infinite element of a value row makes
- * its column of out infinite or NaN.  bf16: the weights are rounded to bf16 (2^-9 of
+ * its column of out infinite or NaN.  bf16: the weights are rounded to bf16 (2^-8 of
  * themselves, the outputs' own rounding) for the product with the values; their sum and lse are not.
  * D in {32, 64, 128}, Hq a multiple of Hkv, T * Hq < 2^30, R < 2^20,
  * max_pages * page_size < 2^30.  Results do not depend on the run.

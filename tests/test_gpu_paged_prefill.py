@@ -220,7 +220,7 @@ def test_bad_pages_lengths_and_starts_are_reported(dt):
         with pytest.raises(la.LinAttnError, match="BAD_INDEX"):
             la.la_check_device_status()
     la.la_check_device_status()
-    # starts that go back and forth: more rows than there are, nothing is done
+    # starts that go back and forth, and would name more rows than there are: no request is done
     R, T = 40, 59
     t3 = torch.zeros((R, 8), dtype=torch.int32, device="cuda")
     keep = torch.full_like(d["q"][:T], 9.5)

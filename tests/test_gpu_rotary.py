@@ -295,7 +295,8 @@ def test_weights_gradient_over_many_rows_is_repeatable():
     turned = torch.cat([gd[..., :32] * c + gd[..., 32:] * s, gd[..., 32:] * c - gd[..., :32] * s], -1)
     terms = turned * xd / torch.sqrt((xd * xd).mean(-1, keepdim=True) + 1e-6)
     want, size = terms.sum((0, 1, 2)), terms.abs().sum((0, 1, 2))
-    # a thread adds up 96000 x 4 / (4 x 152 x 64) / ... rows, below 40; then 64, 19 and 5 additions: 128 u, and 50 u a term
+    # a side's rows over 152 blocks of 64: ten a thread (below 40 however they are dealt out); then 64, 5 and 5 additions:
+    # within 128 u, and 50 u a term
     for dw in runs[0][2:]:
         assert bool(((dw.double() - want).abs() <= 178 * U * size).all())
 
