@@ -634,7 +634,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             Segment g;
             bool any = true;
             for (uint32_t i = 0; any; ++i) {
-                const Request rq = walk.q;  // of the segment that comes
+                const Request rq = walk.q;  // of the segment that comes (only the last can be without a step)
                 any = walk.next(p, g);
                 Job x;
                 x.g.rows = -1;

@@ -305,6 +305,37 @@ def test_serving_run():
         assert np.all(np.abs(got - wo) <= tol + 2.0 ** -24)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_requests_that_share_pages(dt):
+    # a common beginning held once, and a page that one table names twice
+    cached, new, page, D = [32, 32, 40], [9, 150, 3], 16, 64
+    x, table, starts = _case(4, 2, D, page, cached, new, dt)
+    for r in (1, 2):
+        table[r][:2] = table[0][:2]
+    table[2][1] = table[2][0]
+    _check(x, table, cached, starts, D, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_calls_at_once_on_two_streams(dt):
+    la = _la()
+    cases = []
+    for seed, cached, new in ((1, [900, 0, 300], [40, 500, 1]), (2, [0] * 40, [70] * 40)):
+        x, table, starts = _case(8, 2, 64, 16, cached, new, dt, seed=seed)
+        cases.append((*(x[n].cuda() for n in "qKV"), _i32(table), _i32(cached), _i32(starts)))
+    want = [la.la_paged_prefill(*c) for c in cases]
+    streams, got = [torch.cuda.Stream() for _ in cases], [[], []]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for s, c, g in zip(streams, cases, got):
+            with torch.cuda.stream(s):
+                g.append(la.la_paged_prefill(*c))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, o) for o in g)
+    la.la_check_device_status()
+
+
 def test_other_stream_and_captured_graphs_follow_the_lengths():
     la = _la()
     cached, new = [40, 10, 70], [30, 20, 9]
