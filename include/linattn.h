@@ -484,7 +484,8 @@ size_t la_paged_prefill_workspace_bytes(int D, la_dtype dtype, int num_sms);
  *         or one
  *   positions int32, device, [N] for all batch rows (position_rows 1) or [B][N]
  *         (position_rows B); a negative one marks a row without a token.  NULL
- *         (position_rows 0): first_position, first_position + 1, ...
+ *         (position_rows 0): first_position, first_position + 1, ...; with B * N = 0 the
+ *         array has no element, and may be NULL beside any of these position_rows
  *   fill  rows without a token get 0 in q_out (1), k_out (2) or both (3); else they are
  *         left as they are
  * An output may be its own input (the same address and strides) and may not overlap

@@ -959,7 +959,9 @@ static la_status rotary_shape(const char* fn, RotaryShape* sh, const void* const
     if (rot < 2 || rot > D || rot % 2)
         return fail(LA_ERR_INVALID_ARG, "%s: rot=%d must be even, from 2 to D=%d", fn, rot, D);
     if (!std::isfinite(magnitude)) return fail(LA_ERR_INVALID_ARG, "%s: magnitude=%g is not finite", fn, magnitude);
-    if (positions ? position_rows != 1 && position_rows != B : position_rows != 0)
+    // positions of no token are an array without an element, which may be NULL
+    const bool no_token = B == 0 || N == 0;
+    if (positions || (no_token && position_rows != 0) ? position_rows != 1 && position_rows != B : position_rows != 0)
         return fail(LA_ERR_INVALID_ARG, "%s: position_rows=%d with %s must be %s", fn, position_rows,
                     positions ? "positions" : "no positions", positions ? "1 or B" : "0");
     if (positions ? first_position != 0 : first_position < 0 || (long long)first_position + N > INT_MAX)
