@@ -401,9 +401,14 @@ __device__ __forceinline__ void finish_range(const Args& p, const Range& range, 
             if (p.fill & 2)
                 for (int64_t e = t0 * p.s.Hq + tid; e < t1 * p.s.Hq; e += NT) p.lse[e] = -INFINITY;
         };
-        const int last = p.s.R ? min(max(p.starts[p.s.R], 0), p.s.T) : 0;
-        for (int64_t t0 = last + 16 * static_cast<int64_t>(blockIdx.x); t0 < p.s.T; t0 += 16 * static_cast<int64_t>(gridDim.x))
-            clear(t0, min(t0 + 16, static_cast<int64_t>(p.s.T)));
+        // rows before the first request and behind the last one, by all blocks, 16 at a time
+        const int first = p.s.R ? min(max(p.starts[0], 0), p.s.T) : 0, last = p.s.R ? min(max(p.starts[p.s.R], 0), p.s.T) : 0;
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+            const int64_t from = side ? last : 0, to = side ? p.s.T : first;
+            for (int64_t t0 = from + 16 * static_cast<int64_t>(blockIdx.x); t0 < to; t0 += 16 * static_cast<int64_t>(gridDim.x))
+                clear(t0, min(t0 + 16, to));
+        }
         for (int r = blockIdx.x; r < p.s.R; r += gridDim.x) {
             const Request rq(p, r);
             if (rq.pad && rq.n) clear(rq.first, rq.first + rq.n);

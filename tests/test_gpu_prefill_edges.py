@@ -1,0 +1,47 @@
+"""Edges of the prefill over the paged cache: rows of no request, starts that go back, values that are not
+finite in cut tiles and in segments that follow one another, the largest finite values, a pool without pages.
+Tolerances are test_gpu_paged_prefill.py's."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving as ref
+from test_gpu_paged_prefill import DT, HALF, _case, _check, _i32, _la, _score_error
+
+pytestmark = pytest.mark.gpu
+
+
+def _filled(d, table, cached, starts, fill=3):
+    """(out, lse) of the C call with `fill`, on outputs that hold 9.5."""
+    from linear_attention_02_gb300 import _native
+    (T, Hq, D), (P, Hkv, page, _) = d["q"].shape, d["K"].shape
+    R, W = table.shape
+    out, lse = torch.full_like(d["q"], 9.5), torch.full((T, Hq), 9.5, device="cuda")
+    dt = _native.LA_DTYPE_BF16 if out.dtype == torch.bfloat16 else _native.LA_DTYPE_F32
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert _native.lib.la_paged_prefill(d["q"].data_ptr(), d["K"].data_ptr(), d["V"].data_ptr(), table.data_ptr(),
+                                        cached.data_ptr(), starts.data_ptr(), out.data_ptr(), lse.data_ptr(), T, R, Hq,
+                                        Hkv, D, P, page, W, 0, 0.0, dt, fill, s) == _native.LA_OK
+    torch.cuda.synchronize()
+    return out, lse
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("before,tail", [(1, 0), (5, 6), (200, 1)])
+def test_rows_before_the_first_request(before, tail, dt):
+    cached, new = [20, -1, 7], [9, 3, 40]
+    x, table, starts = _case(4, 2, 64, 16, cached, new, dt, tail=before + tail)
+    starts = [before + s for s in starts]
+    out, lse = _check(x, table, cached, starts, 64, dt)
+    d = {n: t.cuda() for n, t in x.items()}
+    own = torch.zeros(len(x["q"]), dtype=torch.bool)
+    own[starts[0]:starts[1]], own[starts[2]:starts[3]] = True, True
+    o2, l2 = _filled(d, _i32(table), _i32(cached), _i32(starts))
+    assert torch.equal(o2[own], out[own]) and torch.equal(l2[own], lse[own])
+    assert bool((o2[~own] == 0).all()) and bool(torch.isneginf(l2[~own]).all())
+    o1, l1 = _filled(d, _i32(table), _i32(cached), _i32(starts), fill=1)
+    assert torch.equal(o1, o2) and bool((l1[~own] == 9.5).all())
+    _la().la_check_device_status()
