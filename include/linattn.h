@@ -431,7 +431,8 @@ size_t la_page_map_workspace_bytes(int R);
  *         BEFORE the new ones; a negative length marks a request that is none:
  *         nothing of its rows is read or written
  *   seq_starts [R + 1] int32                                  (read) not decreasing,
- *         within 0 .. T; if any go back, that is reported and no request is done
+ *         within 0 .. T; if any go back, that is reported and no request is done (all
+ *         rows are rows of no request then)
  *   out [T][Hq][D] dtype                                      (written)
  *   lse [T][Hq] fp32, nullable                                (written)
  *   scale 0 means 1 / sqrt(D);  fill: rows of no request get 0 in out (1),

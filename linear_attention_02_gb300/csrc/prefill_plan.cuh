@@ -100,6 +100,7 @@ struct Range {
     Place from, to;     // to.r = R: the end of all
     int ranges;         // that tile `to` touches, from this block on
     int any;
+    int none;           // the starts go back: no request is done
 };
 
 // Walks over a range; every role of the block has its own.
@@ -261,6 +262,7 @@ struct Planner {
                 if (warp == 0) {
                     range.from = at;
                     range.any = u < total;
+                    range.none = none;
                 } else {
                     range.to = at;
                     range.ranges = u < total ? static_cast<int>(divide(end - 1, per)) - static_cast<int>(blockIdx.x) + 1 : 0;
@@ -401,15 +403,17 @@ __device__ __forceinline__ void finish_range(const Args& p, const Range& range, 
             if (p.fill & 2)
                 for (int64_t e = t0 * p.s.Hq + tid; e < t1 * p.s.Hq; e += NT) p.lse[e] = -INFINITY;
         };
-        // rows before the first request and behind the last one, by all blocks, 16 at a time
-        const int first = p.s.R ? min(max(p.starts[0], 0), p.s.T) : 0, last = p.s.R ? min(max(p.starts[p.s.R], 0), p.s.T) : 0;
+        // Rows before the first request and behind the last one, by all blocks, 16 at a time.  Starts that go back may name
+        // rows many times over, so then all rows are cleared, once.
+        const bool some = p.s.R && !range.none;
+        const int first = some ? min(max(p.starts[0], 0), p.s.T) : 0, last = some ? min(max(p.starts[p.s.R], 0), p.s.T) : 0;
 #pragma unroll 1
         for (int side = 0; side < 2; ++side) {
             const int64_t from = side ? last : 0, to = side ? p.s.T : first;
             for (int64_t t0 = from + 16 * static_cast<int64_t>(blockIdx.x); t0 < to; t0 += 16 * static_cast<int64_t>(gridDim.x))
                 clear(t0, min(t0 + 16, to));
         }
-        for (int r = blockIdx.x; r < p.s.R; r += gridDim.x) {
+        for (int r = blockIdx.x; some && r < p.s.R; r += gridDim.x) {
             const Request rq(p, r);
             if (rq.pad && rq.n) clear(rq.first, rq.first + rq.n);
         }

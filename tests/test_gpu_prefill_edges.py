@@ -45,3 +45,24 @@ def test_rows_before_the_first_request(before, tail, dt):
     o1, l1 = _filled(d, _i32(table), _i32(cached), _i32(starts), fill=1)
     assert torch.equal(o1, o2) and bool((l1[~own] == 9.5).all())
     _la().la_check_device_status()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("R", [3, 40, 5000])
+@pytest.mark.parametrize("length", [0, -1])
+def test_starts_that_go_back_leave_no_row_undefined(length, R, dt):
+    # back and forth over all rows: reported, no request done, and every row cleared once, however many requests
+    la = _la()
+    T = 59
+    x, _, _ = _case(4, 2, 64, 16, [0], [T], dt)
+    d = {n: t.cuda() for n, t in x.items()}
+    table = torch.zeros((R, 8), dtype=torch.int32, device="cuda")
+    starts = ([0, T] * R)[:R] + [3]  # the last row that a request names is not the last of all
+    out, lse = _filled(d, table, _i32([length] * R), _i32(starts))
+    with pytest.raises(la.LinAttnError, match="BAD_INDEX"):
+        la.la_check_device_status()
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    out, lse = _filled(d, table, _i32([length] * R), _i32(starts), fill=0)
+    assert bool((out == 9.5).all()) and bool((lse == 9.5).all())
+    with pytest.raises(la.LinAttnError, match="BAD_INDEX"):
+        la.la_check_device_status()
