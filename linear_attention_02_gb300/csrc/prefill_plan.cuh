@@ -30,7 +30,7 @@ struct Args {
     float* lse;
     int fill;
     float* part;   // [blocks][2][TM][D] output sums of cut tiles
-    float2* ml;    // [blocks][2][TM] their maxima (to base 2) and sums
+    float2* ml;    // [blocks][2][TM] their maxima (to base 2) and sums; a negative sum: no part
     int4* desc;    // [blocks][2] the cut tile whose first step is in the block's range: {request, key head, first row, rows}, {ranges, -, -, -}
     unsigned* status;
 };
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Arg
 #pragma unroll
             for (int x = 0; x < N; ++x) {
                 const int64_t at = (2 * (static_cast<int64_t>(blockIdx.x) + x0 + x) + (x0 + x == 0 ? 1 : 0)) * TM + row;
-                ml[x] = x0 + x < ranges ? p.ml[at] : make_float2(-INFINITY, 0.f);
+                ml[x] = x0 + x < ranges ? p.ml[at] : make_float2(-INFINITY, -1.f);
 #pragma unroll
                 for (int e = 0; e < E; ++e) v[x][e] = x0 + x < ranges ? p.part[at * D + lane + 32 * e] : 0.f;
             }
@@ -333,11 +333,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Arg
             for (int x = 0; x < N; ++x) {
                 const float y = fmaxf(top, ml[x].x);
                 const float f = top == y ? 1.f : exp2_approx(top - y);
-                // nothing of a part without a key is read; one whose scores are NaN carries them on
+                // a part whose scores are NaN carries them on; what is infinite or NaN in a part comes through a factor
+                // of 0 too, as it does in a tile that is not cut; what a block without a part has not written does not
                 const float h = ml[x].x == -INFINITY ? (ml[x].y != ml[x].y ? 1.f : 0.f) : ml[x].x == y ? 1.f : exp2_approx(ml[x].x - y);
+                const bool none = ml[x].y < 0.f;
                 sum = sum * f + ml[x].y * h;
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = o[e] * f + (h > 0.f ? v[x][e] * h : 0.f);
+                for (int e = 0; e < E; ++e) o[e] = o[e] * f + (none ? 0.f : v[x][e] * h);
                 top = y;
             }
         }
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_join_kernel(const Arg
         const int token = token_of(p, m);
         const int64_t at = (static_cast<int64_t>(rq.first) + token) * p.s.Hq + static_cast<int64_t>(d.y) * p.G + (m - token * p.G);
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[at * D + lane + 32 * e] = from_f<T>(good ? o[e] / sum : 0.f);
+        for (int e = 0; e < E; ++e) out[at * D + lane + 32 * e] = from_f<T>(good ? o[e] / sum : o[e]);
         if (lane == 0 && p.lse) p.lse[at] = good ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     }
 }
@@ -394,7 +396,7 @@ __device__ __forceinline__ void finish_range(const Args& p, const Range& range, 
     // a range inside a tile that has no whole step adds nothing to it
     if (range.any && range.from.a > 0 && range.from.a == range.to.a && range.from.r == range.to.r && range.from.kh == range.to.kh &&
         range.from.mt == range.to.mt)
-        for (int i = tid; i < TM; i += NT) p.ml[2 * static_cast<int64_t>(blockIdx.x) * TM + i] = make_float2(-INFINITY, 0.f);
+        for (int i = tid; i < TM; i += NT) p.ml[2 * static_cast<int64_t>(blockIdx.x) * TM + i] = make_float2(-INFINITY, -1.f);
     if (p.fill) {
         const int64_t wide = static_cast<int64_t>(p.s.Hq) * D * sizeof(T) / 16;
         const auto clear = [&](int64_t t0, int64_t t1) {

@@ -66,3 +66,33 @@ def test_starts_that_go_back_leave_no_row_undefined(length, R, dt):
     assert bool((out == 9.5).all()) and bool((lse == 9.5).all())
     with pytest.raises(la.LinAttnError, match="BAD_INDEX"):
         la.la_check_device_status()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("far", [-40.0, -math.inf])
+@pytest.mark.parametrize("early", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,D,new", [(1, 1, 64, 1), (8, 1, 128, 3), (2, 2, 32, 40)])
+def test_an_infinite_value_of_weight_0_in_a_cut_tile(Hq, Hkv, D, new, early, far, dt):
+    # One half's keys score so far below the others that their weights are 0 in fp32: by the definition
+    # and in an uncut tile 0 times an infinity is NaN, and so it is where another block had that half.
+    la = _la()
+    page, cached, at, col = 16, 6000, 100 if early else 5000, 5
+    x, table, starts = _case(Hq, Hkv, D, page, [cached], [new], dt)
+    x["q"][:, :, 0] = 40.0
+    n = cached + new
+    pages, offs = np.array(table[0])[np.arange(n) // page], np.arange(n) % page
+    low = torch.tensor((np.arange(n) < 3000) == early)
+    k0 = torch.where(low, torch.tensor(far), torch.tensor(40.0)).to(DT[dt])
+    x["K"][pages, :, offs, 0] = k0[:, None]
+    d = {m: t.cuda() for m, t in x.items()}
+    args = (_i32(table), _i32([cached]), _i32(starts))
+    want, wl = la.la_paged_prefill(d["q"], d["K"], d["V"], *args, return_lse=True)
+    assert bool(torch.isfinite(want).all())
+    rest = [c for c in range(D) if c != col]
+    for what in (math.inf, -math.inf, math.nan):
+        V = d["V"].clone()
+        V[table[0][at // page], :, at % page, col] = what
+        got, gl = la.la_paged_prefill(d["q"], d["K"], V, *args, return_lse=True)
+        assert not bool(torch.isfinite(got[..., col]).any()), what
+        assert torch.equal(got[..., rest], want[..., rest]) and torch.equal(gl, wl)
+    la.la_check_device_status()
