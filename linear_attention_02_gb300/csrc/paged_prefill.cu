@@ -318,7 +318,7 @@ prefill_f32_kernel(const float* __restrict__ q, const float* __restrict__ K, con
                     if (s_odd) {  // rare: does this row see one of the replaced values?
                         uint32_t bits = 0;
                         for (int j = sg.a; j < sg.b; ++j)
-                            bits |= prefill::odd_columns<float, D, KT>(p, V, sg.r, sg.kh, k.first, k.last, rq.end, k.k0 + j, from[i], pos[i], 32 * a);
+                            bits |= prefill::odd_columns<float, D, KT, true>(p, V, sg.r, sg.kh, k.first, k.last, rq.end, k.k0 + j, from[i], pos[i], 32 * a);
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
                             if (bits >> (8 * t + x) & 1u) v[x] = __uint_as_float(0x7FFFFFFFu);

@@ -29,8 +29,8 @@
 //
 // Values that a row does not see have weight 0, but 0 times an infinity or NaN is no 0.
 // So in tiles that some row sees in part, warps 12 to 15 clear the value rows that no row
-// sees, and replace what is not finite in the others by 0; a row that does see such an
-// element gets NaN in that column at the end.
+// sees, and replace what is not finite in those that some rows see by 0; a row that does see such an
+// element gets NaN in that column at the end.  Value rows that all rows see stay as they are.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -242,8 +242,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     __shared__ uint64_t s_jfull[kJobs], s_jfree[kJobs];
     __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_end;
     __shared__ uint32_t s_mask[2][kMasks][4];  // positions of a step that are on a page, a bit each, as keys' and values' loader saw them
-    // A value that was not finite was replaced, in this or an earlier segment: it stays set, as the warps that
-    // replace may be segments ahead of a subtile's outputs.
+    // A value that was not finite was replaced, in this or an earlier segment, or in a later one: it stays set, as the
+    // warps that replace may be segments ahead of a subtile's outputs.  So it only says whether to look.
     __shared__ volatile int s_odd;
     __shared__ volatile int s_abort;
     __shared__ volatile int s_issued[2];     // tiles of keys, of values that their loaders have begun
@@ -424,7 +424,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     if (s_odd) {  // rare: does this row see one of the replaced values?
                         uint32_t bits = 0;
                         for (int j = part_a; live && j < part_b; ++j)
-                            bits |= prefill::odd_columns<bf16, D, KT>(p, V, g.r, g.kh, x.first, x.last, x.end, k0 + j, from, pos, i);
+                            bits |= prefill::odd_columns<bf16, D, KT, false>(p, V, g.r, g.kh, x.first, x.last, x.end, k0 + j, from, pos, i);
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
                             if (bits >> x & 1u) o[x] = __uint_as_float(0x7FFFFFFFu);

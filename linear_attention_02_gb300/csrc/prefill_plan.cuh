@@ -281,8 +281,8 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 // The columns of [i, i + 32), a bit each, in which a row sees a value that is not finite in a key
 // tile, if that is one in which such values were replaced: one that some row from position
-// `first` to `last` sees in part.
-template <typename T, int D, int KT>
+// `first` to `last` sees in part.  COMMON: positions that all rows see were replaced too.
+template <typename T, int D, int KT, bool COMMON>
 __device__ __noinline__ uint32_t odd_columns(const Args& p, const T* V, int r, int kh, int first, int last, int end,
                                              int tile, int from, int pos, int i) {
     const int x0 = tile * KT, mask = (1 << p.s.log2p) - 1;
@@ -295,6 +295,7 @@ __device__ __noinline__ uint32_t odd_columns(const Args& p, const T* V, int r, i
     for (int x = max(x0, max(from + 1, 0)); x < min(x0 + KT, min(pos + 1, end)); ++x) {
         const int page = table[x >> p.s.log2p];
         if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.s.num_pages)) continue;
+        if (!COMMON && x <= first && (p.s.window == 0 || x > last - p.s.window)) continue;
         const T* v = V + (((static_cast<int64_t>(page) * p.s.Hkv + kh) << p.s.log2p) + (x & mask)) * D + i;
         for (int y = 0; y < 32; ++y)
             if (!(fabsf(to_f<T>(v[y])) < INFINITY)) bits |= 1u << y;

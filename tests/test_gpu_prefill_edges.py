@@ -96,3 +96,28 @@ def test_an_infinite_value_of_weight_0_in_a_cut_tile(Hq, Hkv, D, new, early, far
         assert not bool(torch.isfinite(got[..., col]).any()), what
         assert torch.equal(got[..., rest], want[..., rest]) and torch.equal(gl, wl)
     la.la_check_device_status()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_values_replaced_elsewhere_do_not_change_an_infinity_that_all_rows_see(dt):
+    # many requests a block; position 0 is seen by every row, position 11 by the later ones only
+    la = _la()
+    R, new, H, D, page = 1500, 150, 2, 64, 16
+    W = -(-new // page)
+    g = torch.Generator().manual_seed(7)
+    q, K, V = (torch.randn(s, generator=g).to(DT[dt]).cuda() for s in ((R * new, H, D), (R * W, H, page, D), (R * W, H, page, D)))
+    table = torch.randperm(R * W, generator=g).to(torch.int32).cuda().view(R, W)
+    lens, starts = torch.zeros(R, dtype=torch.int32, device="cuda"), torch.arange(R + 1, device="cuda", dtype=torch.int32) * new
+    run = lambda: la.la_paged_prefill(q, K, V, table, lens, starts).view(R, new, H, D)  # noqa: E731
+    V[table[:, 0].long(), :, 0, 3] = math.inf
+    want = run()
+    assert not bool(torch.isfinite(want[..., 3]).any())
+    hit = torch.arange(0, R, 7, device="cuda")
+    V[table[hit, 0].long(), :, 11, 9] = math.nan
+    touched = torch.zeros((R, new, H, D), dtype=torch.bool, device="cuda")
+    touched[hit, 11:, :, 9] = True
+    bits = lambda t: t[~touched].view(torch.int16 if dt == "bf16" else torch.int32)  # noqa: E731  NaN equals NaN here
+    for _ in range(3):
+        got = run()
+        assert torch.equal(bits(got), bits(want))
+        assert bool(torch.isnan(got[touched]).all())
