@@ -16,6 +16,9 @@
 // columns are in such an order that a lane's operands are 16-byte pieces of the rows, read
 // without bank conflicts, and the weights of a lane are its operand of the second product.
 //
+// A value within 2^-12 of the largest fp32 number has an infinite first term.  Keeping it finite costs two
+// operations a value (6% of the time), so a segment with a NaN among its outputs is computed again, from halved values.
+//
 // Measured: 16 prompts of 1024 tokens, 16 heads of 64: 750 us, 46 TFLOP/s; 8 x 1024 of 8 heads of 128: 430 us;
 // 13 ragged requests up to 700 tokens with a window of 1000: 370 to 400 us (1940 with the products on the
 // fp32 units), the matrix unit's pipe half full and what stalls most.
@@ -148,14 +151,12 @@ prefill_f32_kernel(const float* __restrict__ q, const float* __restrict__ K, con
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
-            load(sg.a, 0);
             for (int e = tid; e < TM * CH; e += NT) {
                 const int y = e / CH, ch = e % CH, m = sg.m0 + y, token = token_of(p, m);
                 const bool on = m < sg.rows;
                 const int64_t at = on ? (static_cast<int64_t>(rq.first) + token) * p.s.Hq + static_cast<int64_t>(sg.kh) * p.G + (m - token * p.G) : 0;
                 copy16(s_q + y * KS + 4 * ch, q + at * D + 4 * ch, on);
             }
-            if (tid == 0) s_odd = 0;
             asm volatile("cp.async.commit_group;" ::: "memory");
 
             const int r0 = sg.m0 + 16 * warp, r1 = min(r0 + 16, sg.rows);  // the warp's rows
@@ -168,133 +169,149 @@ prefill_f32_kernel(const float* __restrict__ q, const float* __restrict__ K, con
                 pos[i] = rq.cached + token_of(p, r0 + g + 8 * i);
                 from[i] = p.s.window ? pos[i] - p.s.window : -1;
             }
-            float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, o[GR][4][4];
+            float top[2], sum[2], o[GR][4][4], half = 1.f;
+#pragma unroll 1
+            for (;; half = 0.5f) {
+                load(sg.a, 0);
+                if (tid == 0) s_odd = 0;
 #pragma unroll
-            for (int a = 0; a < GR; ++a)
+                for (int i = 0; i < 2; ++i) top[i] = -INFINITY, sum[i] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int a = 0; a < GR; ++a)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[a][i][e] = 0.f;
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[a][i][e] = 0.f;
 
 #pragma unroll 1
-            for (int j = sg.a; j < sg.b; ++j) {
-                const int stage = (j - sg.a) & 1, x0 = (k.k0 + j) * KT;
-                if (j + 1 < sg.b) load(j + 1, stage ^ 1);
-                else asm volatile("cp.async.commit_group;" ::: "memory");
-                asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the next step's
-                __syncthreads();
-                const float *sk = sm + TM * KS + stage * Ly::STAGE, *sv = sk + KT * KS;
-                const uint32_t mask = s_mask[stage];
-                const bool whole_tile = x0 + KT - 1 <= k.first && (p.s.window == 0 || x0 > k.last - p.s.window) && mask == 0xFFFFFFFFu;
-                if (!whole_tile) {
-                    // Values that a row does not see have weight 0, but 0 times an infinity or NaN is none: in tiles that
-                    // some row sees in part they are replaced, and rows that do see them marked at the end.
-                    float* v = const_cast<float*>(sv);
-                    for (int e = tid; e < KT * CH; e += NT) {
-                        float4* at = reinterpret_cast<float4*>(v + e / CH * VS + 4 * (e % CH));
-                        float4 x = *at;
-                        if (!(fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY && fabsf(x.z) < INFINITY && fabsf(x.w) < INFINITY)) {
-                            x.x = fabsf(x.x) < INFINITY ? x.x : 0.f, x.y = fabsf(x.y) < INFINITY ? x.y : 0.f;
-                            x.z = fabsf(x.z) < INFINITY ? x.z : 0.f, x.w = fabsf(x.w) < INFINITY ? x.w : 0.f;
-                            *at = x;
-                            s_odd = 1;
-                        }
-                    }
+                for (int j = sg.a; j < sg.b; ++j) {
+                    const int stage = (j - sg.a) & 1, x0 = (k.k0 + j) * KT;
+                    if (j + 1 < sg.b) load(j + 1, stage ^ 1);
+                    else asm volatile("cp.async.commit_group;" ::: "memory");
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the next step's
                     __syncthreads();
+                    const float *sk = sm + TM * KS + stage * Ly::STAGE, *sv = sk + KT * KS;
+                    const uint32_t mask = s_mask[stage];
+                    const bool whole_tile = x0 + KT - 1 <= k.first && (p.s.window == 0 || x0 > k.last - p.s.window) && mask == 0xFFFFFFFFu;
+                    if (!whole_tile || half < 1.f) {
+                        // Values that a row does not see have weight 0, but 0 times an infinity or NaN is none: in tiles that
+                        // some row sees in part they are replaced, and rows that do see them marked at the end.
+                        float* v = const_cast<float*>(sv);
+                        for (int e = tid; e < KT * CH; e += NT) {
+                            float4* at = reinterpret_cast<float4*>(v + e / CH * VS + 4 * (e % CH));
+                            float4 x = *at;
+                            if (!whole_tile && !(fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY && fabsf(x.z) < INFINITY && fabsf(x.w) < INFINITY)) {
+                                x.x = fabsf(x.x) < INFINITY ? x.x : 0.f, x.y = fabsf(x.y) < INFINITY ? x.y : 0.f;
+                                x.z = fabsf(x.z) < INFINITY ? x.z : 0.f, x.w = fabsf(x.w) < INFINITY ? x.w : 0.f;
+                                *at = x;
+                                s_odd = 1;
+                            }
+                            if (half < 1.f) *at = make_float4(x.x * half, x.y * half, x.z * half, x.w * half);
+                        }
+                        __syncthreads();
+                    }
+                    if (work && x0 <= wlast && x0 + KT > wlo) {
+                        float s[KT / 8][4];
+#pragma unroll
+                        for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+                        const float* qa = s_q + (16 * warp + g) * KS + 4 * t;
+                        const float* kb = sk + g * KS + 4 * t;
+#pragma unroll
+                        for (int d = 0; d < D; d += 16) {
+                            const float4 a = *reinterpret_cast<const float4*>(qa + d), b = *reinterpret_cast<const float4*>(qa + 8 * KS + d);
+                            uint32_t h[2][4], l[2][4];
+                            split(a.x, h[0][0], l[0][0]), split(b.x, h[0][1], l[0][1]), split(a.y, h[0][2], l[0][2]), split(b.y, h[0][3], l[0][3]);
+                            split(a.z, h[1][0], l[1][0]), split(b.z, h[1][1], l[1][1]), split(a.w, h[1][2], l[1][2]), split(b.w, h[1][3], l[1][3]);
+#pragma unroll
+                            for (int n = 0; n < KT / 8; ++n) {
+                                const float4 f = *reinterpret_cast<const float4*>(kb + 8 * n * KS + d);
+                                mma3(s[n], h[0], l[0], f.x, f.y);
+                                mma3(s[n], h[1], l[1], f.z, f.w);
+                            }
+                        }
+                        float nan = 0.f;
+#pragma unroll
+                        for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) nan = max_nan(nan, s[n][e]);
+                        if (__any_sync(0xffffffffu, nan != nan)) {
+#pragma unroll
+                            for (int n = 0; n < KT / 8; ++n) {
+                                const float4 f = plain_scores<D>(s_q + 16 * warp * KS, sk, n);
+                                // the others stay as they are, whatever rows they share the step with
+                                s[n][0] = s[n][0] != s[n][0] ? f.x : s[n][0], s[n][1] = s[n][1] != s[n][1] ? f.y : s[n][1];
+                                s[n][2] = s[n][2] != s[n][2] ? f.z : s[n][2], s[n][3] = s[n][3] != s[n][3] ? f.w : s[n][3];
+                            }
+                        }
+                        const bool all = x0 + KT - 1 <= wfirst && (p.s.window == 0 || x0 > wlast - p.s.window) && mask == 0xFFFFFFFFu;
+                        float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int y = 8 * n + 2 * t + (e & 1), x = x0 + y;
+                                s[n][e] *= c;
+                                if (!all && !(x <= pos[e >> 1] && x > from[e >> 1] && (mask >> y & 1u))) s[n][e] = -INFINITY;
+                                best[e >> 1] = fmaxf(best[e >> 1], s[n][e]);
+                            }
+                        float f[2], base[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 1));
+                            best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 2));
+                            const float m = fmaxf(top[i], best[i]);
+                            f[i] = m == top[i] ? 1.f : exp2_approx(top[i] - m);
+                            top[i] = m;
+                            base[i] = m == -INFINITY ? 0.f : m;
+                            sum[i] *= f[i];
+                        }
+                        uint32_t wh[KT / 8][4], wl[KT / 8][4];  // a lane's weights, as the operand of the second product
+#pragma unroll
+                        for (int n = 0; n < KT / 8; ++n) {
+                            float w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                w[e] = exp2_approx(s[n][e] - base[e >> 1]);
+                                sum[e >> 1] += w[e];
+                            }
+                            split(w[0], wh[n][0], wl[n][0]), split(w[2], wh[n][1], wl[n][1]);
+                            split(w[1], wh[n][2], wl[n][2]), split(w[3], wh[n][3], wl[n][3]);
+                        }
+                        const float* vb = sv + 2 * t * VS + 4 * g;
+#pragma unroll
+                        for (int a = 0; a < GR; ++a) {
+                            float z[4][4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) z[i][e] = 0.f;
+#pragma unroll
+                            for (int n = 0; n < KT / 8; ++n) {
+                                const float4 u = *reinterpret_cast<const float4*>(vb + 8 * n * VS + 32 * a);
+                                const float4 v = *reinterpret_cast<const float4*>(vb + (8 * n + 1) * VS + 32 * a);
+                                mma3(z[0], wh[n], wl[n], u.x, v.x);
+                                mma3(z[1], wh[n], wl[n], u.y, v.y);
+                                mma3(z[2], wh[n], wl[n], u.z, v.z);
+                                mma3(z[3], wh[n], wl[n], u.w, v.w);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[a][i][e] = fmaf(o[a][i][e], f[e >> 1], z[i][e]);
+                        }
+                    }
+                    __syncthreads();  // before the stage is filled again
                 }
-                if (work && x0 <= wlast && x0 + KT > wlo) {
-                    float s[KT / 8][4];
+                bool nan = false;
 #pragma unroll
-                    for (int n = 0; n < KT / 8; ++n)
+                for (int a = 0; a < GR; ++a)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-                    const float* qa = s_q + (16 * warp + g) * KS + 4 * t;
-                    const float* kb = sk + g * KS + 4 * t;
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int d = 0; d < D; d += 16) {
-                        const float4 a = *reinterpret_cast<const float4*>(qa + d), b = *reinterpret_cast<const float4*>(qa + 8 * KS + d);
-                        uint32_t h[2][4], l[2][4];
-                        split(a.x, h[0][0], l[0][0]), split(b.x, h[0][1], l[0][1]), split(a.y, h[0][2], l[0][2]), split(b.y, h[0][3], l[0][3]);
-                        split(a.z, h[1][0], l[1][0]), split(b.z, h[1][1], l[1][1]), split(a.w, h[1][2], l[1][2]), split(b.w, h[1][3], l[1][3]);
-#pragma unroll
-                        for (int n = 0; n < KT / 8; ++n) {
-                            const float4 f = *reinterpret_cast<const float4*>(kb + 8 * n * KS + d);
-                            mma3(s[n], h[0], l[0], f.x, f.y);
-                            mma3(s[n], h[1], l[1], f.z, f.w);
-                        }
-                    }
-                    float nan = 0.f;
-#pragma unroll
-                    for (int n = 0; n < KT / 8; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) nan = max_nan(nan, s[n][e]);
-                    if (__any_sync(0xffffffffu, nan != nan)) {
-#pragma unroll
-                        for (int n = 0; n < KT / 8; ++n) {
-                            const float4 f = plain_scores<D>(s_q + 16 * warp * KS, sk, n);
-                            // the others stay as they are, whatever rows they share the step with
-                            s[n][0] = s[n][0] != s[n][0] ? f.x : s[n][0], s[n][1] = s[n][1] != s[n][1] ? f.y : s[n][1];
-                            s[n][2] = s[n][2] != s[n][2] ? f.z : s[n][2], s[n][3] = s[n][3] != s[n][3] ? f.w : s[n][3];
-                        }
-                    }
-                    const bool all = x0 + KT - 1 <= wfirst && (p.s.window == 0 || x0 > wlast - p.s.window) && mask == 0xFFFFFFFFu;
-                    float best[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int n = 0; n < KT / 8; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int y = 8 * n + 2 * t + (e & 1), x = x0 + y;
-                            s[n][e] *= c;
-                            if (!all && !(x <= pos[e >> 1] && x > from[e >> 1] && (mask >> y & 1u))) s[n][e] = -INFINITY;
-                            best[e >> 1] = fmaxf(best[e >> 1], s[n][e]);
-                        }
-                    float f[2], base[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 1));
-                        best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 2));
-                        const float m = fmaxf(top[i], best[i]);
-                        f[i] = m == top[i] ? 1.f : exp2_approx(top[i] - m);
-                        top[i] = m;
-                        base[i] = m == -INFINITY ? 0.f : m;
-                        sum[i] *= f[i];
-                    }
-                    uint32_t wh[KT / 8][4], wl[KT / 8][4];  // a lane's weights, as the operand of the second product
-#pragma unroll
-                    for (int n = 0; n < KT / 8; ++n) {
-                        float w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            w[e] = exp2_approx(s[n][e] - base[e >> 1]);
-                            sum[e >> 1] += w[e];
-                        }
-                        split(w[0], wh[n][0], wl[n][0]), split(w[2], wh[n][1], wl[n][1]);
-                        split(w[1], wh[n][2], wl[n][2]), split(w[3], wh[n][3], wl[n][3]);
-                    }
-                    const float* vb = sv + 2 * t * VS + 4 * g;
-#pragma unroll
-                    for (int a = 0; a < GR; ++a) {
-                        float z[4][4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) z[i][e] = 0.f;
-#pragma unroll
-                        for (int n = 0; n < KT / 8; ++n) {
-                            const float4 u = *reinterpret_cast<const float4*>(vb + 8 * n * VS + 32 * a);
-                            const float4 v = *reinterpret_cast<const float4*>(vb + (8 * n + 1) * VS + 32 * a);
-                            mma3(z[0], wh[n], wl[n], u.x, v.x);
-                            mma3(z[1], wh[n], wl[n], u.y, v.y);
-                            mma3(z[2], wh[n], wl[n], u.z, v.z);
-                            mma3(z[3], wh[n], wl[n], u.w, v.w);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[a][i][e] = fmaf(o[a][i][e], f[e >> 1], z[i][e]);
-                    }
-                }
-                __syncthreads();  // before the stage is filled again
+                        for (int e = 0; e < 4; ++e) nan |= o[a][i][e] != o[a][i][e];
+                if (half < 1.f || !__syncthreads_or(nan)) break;
             }
             // the rows' outputs: 8 columns of each 32 a lane
             const bool whole = sg.whole();
@@ -309,7 +326,7 @@ prefill_f32_kernel(const float* __restrict__ q, const float* __restrict__ K, con
                 const int token = token_of(p, m);
                 const int64_t at = (static_cast<int64_t>(rq.first) + token) * p.s.Hq + static_cast<int64_t>(sg.kh) * p.G + (m - token * p.G);
                 float* to = whole ? out + at * D : p.part + (static_cast<int64_t>(slot) * TM + y) * D;
-                const float inv = whole ? (good ? sum[i] : INFINITY) : 1.f;
+                const float inv = (whole ? (good ? sum[i] : INFINITY) : 1.f) * half;
 #pragma unroll
                 for (int a = 0; a < GR; ++a) {
                     float v[8];

@@ -121,3 +121,26 @@ def test_values_replaced_elsewhere_do_not_change_an_infinity_that_all_rows_see(d
         got = run()
         assert torch.equal(bits(got), bits(want))
         assert bool(torch.isnan(got[touched]).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_the_largest_finite_values(D, dt):
+    cached, new = [3, 0], [40, 200]
+    x, table, starts = _case(4, 2, D, 16, cached, new, dt)
+    top = torch.finfo(DT[dt]).max
+    g = torch.Generator().manual_seed(D)
+    near = torch.rand(x["V"].shape, generator=g, dtype=torch.float64) * 2.0 ** -11  # on both sides of 2^-12 below the largest
+    sign = torch.where(torch.rand(x["V"].shape, generator=g) < 0.5, -1.0, 1.0)
+    y = dict(x, V=((1 - near) * top * sign).to(DT[dt]))
+    assert bool(torch.isfinite(y["V"]).all()) and bool((y["V"].abs() == top).any())
+    _check(y, table, cached, starts, D, dt, window=1)  # each row sees its own value only
+    # one such value beside ordinary ones, in whole and in partly seen tiles: no sum passes it
+    y = dict(x, V=x["V"].clone())
+    for r in range(2):
+        y["V"][table[r][0], :, 0] = (sign * top)[table[r][0], :, 0].to(DT[dt])
+    y["K"] = x["K"].clone()
+    for r in range(2):
+        y["K"][table[r][0], :, 0] = 0  # its score is 0: a weight of at most the largest
+    _check(y, table, cached, starts, D, dt)
+    _la().la_check_device_status()
