@@ -610,7 +610,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             for (int e = 0; e < DP / 8; ++e) {
                                 const bool on = ids[i] >= 0 && e < D / 8;
                                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (e >> 3) * kAtom + swz(y, e & 7)),
-                                             "l"(pool + (on ? src + e * 8 : 0)), "r"(on ? 16 : 0)
+                                             "l"(on ? pool + src + e * 8 : q), "r"(on ? 16 : 0)
                                              : "memory");
                             }
                         }

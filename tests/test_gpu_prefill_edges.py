@@ -144,3 +144,16 @@ def test_the_largest_finite_values(D, dt):
         y["K"][table[r][0], :, 0] = 0  # its score is 0: a weight of at most the largest
     _check(y, table, cached, starts, D, dt)
     _la().la_check_device_status()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("page", [4, 16])
+def test_a_pool_without_pages(page, dt):
+    la = _la()
+    x, _, _ = _case(4, 2, 64, page, [20, 0], [9, 150], dt)
+    q, K = x["q"].cuda(), torch.empty((0, 2, page, 64), device="cuda", dtype=DT[dt])
+    table = torch.zeros((2, 64), dtype=torch.int32, device="cuda")
+    out, lse = la.la_paged_prefill(q, K, K.clone(), table, _i32([20, 0]), _i32([0, 9, 159]), return_lse=True)
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    with pytest.raises(la.LinAttnError, match="BAD_INDEX"):
+        la.la_check_device_status()
