@@ -59,7 +59,9 @@ constexpr int kAux = 128;             // threads of warps 12 to 15
 constexpr int kMasks = 16;            // steps whose masks are kept: more than the loader is ahead of the softmax
 constexpr float kSlack = 8.f;         // log2 by which a score may pass the maximum kept
 constexpr uint32_t kAtom = 16384;     // 128 rows x 128 bytes
-constexpr uint32_t kLimit = 1u << 26; // polls of a wait: the queries' warps wait as long as a tile takes
+// Polls of a wait for another role (a poll that fails takes 3.4 us, so about a minute; the queries' warps wait as long as
+// a tile takes, a second for 10^8 positions), and of one for what is under way when a block ends: microseconds.
+constexpr uint32_t kLimit = tcf::kWaitLimit, kDrain = 1u << 16;
 
 template <int D>
 struct Lay {
@@ -282,9 +284,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         s_abort = 1;
         atomicOr(p.status, tcf::kErrWait);
     };
-    // Waits give up after kLimit polls, or once any of them has.
+    // Waits give up after p.limit polls, or once any of them has.
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const int e = mbar_wait_or(bar, parity & 1u, kLimit, const_cast<const volatile int*>(&s_abort));
+        const int e = mbar_wait_or(bar, parity & 1u, p.limit, const_cast<const volatile int*>(&s_abort));
         if (e == 2) fail();
         return e == 0;
     };
@@ -515,7 +517,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             // nothing may be under way when the block ends
             if (elect()) mma_commit(&s_end);
             __syncwarp();
-            if (!mbar_wait(&s_end, 0, kLimit)) fail();
+            if (!mbar_wait(&s_end, 0, kDrain)) fail();
         } else if (warp < 11) {
             // ---------------------------------------------------------------- keys (warp 9), values (warp 10)
             const int kv = warp - 9;
@@ -627,7 +629,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if (bad) atomicOr(p.status, kStatusBadIndex);
             // copies under way end before the block does: the last ones of each stage (it is the first tile not issued)
             for (uint32_t i = it > 2 * STAGES ? it - 2 * STAGES : kv; i < it; i += 2)
-                if (i + STAGES >= it && !mbar_wait(s_full + i % STAGES, i / STAGES & 1u, kLimit)) fail();
+                if (i + STAGES >= it && !mbar_wait(s_full + i % STAGES, i / STAGES & 1u, kDrain)) fail();
         } else if (warp == 11) {
             // ---------------------------------------------------------------- the segments, for all
             Walk walk(p, range);
@@ -648,6 +650,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             // ---------------------------------------------------------------- queries, values seen in part
             const int t = 32 * (warp - 12) + lane;
             uint32_t item = 0, n_q = 0, step = 0;
+            const bool mute = warp == 12 && static_cast<int>(blockIdx.x) == p.withhold;
             bool ok = true;
             for (Job k; ok && next(k);) {
                 const Segment& g = k.g;
@@ -737,10 +740,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     // and the next step's keys, so that the products wait once
                     if (j + 1 < g.b && !(ok = warp_wait(s_full + (v + 1) % STAGES, (v + 1) / STAGES))) break;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(s_vready + sg);
+                    if (lane == 0 && (step || !mute)) mbar_arrive(s_vready + sg);
                 }
             }
-            if (q_tma && n_q && t == 0 && !mbar_wait(&s_qfull, (n_q - 1) & 1u, kLimit)) fail();
+            if (q_tma && n_q && t == 0 && !mbar_wait(&s_qfull, (n_q - 1) & 1u, kDrain)) fail();
         }
         }
     }
@@ -776,6 +779,8 @@ cudaError_t paged_prefill_tc(const LaunchCtx& c, const bf16* q, const bf16* K, c
     prefill::set_group(p, s.Hq / s.Hkv, TM);
     p.s = s, p.table = table, p.lens = lens, p.starts = starts, p.lse = lse, p.fill = fill;
     p.status = c.status_word;
+    p.withhold = c.withhold_unit;
+    p.limit = c.spin_limit ? c.spin_limit : kLimit;
     int per_sm = 1;
     cudaError_t e = resident_blocks<prefill_kernel<D>>(c.device, NT, Ly::SMEM, &per_sm);
     if (e != cudaSuccess) return e;
