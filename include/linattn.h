@@ -611,9 +611,9 @@ size_t la_scratch_peak_bytes(int reset);
  * hang; its outputs are then undefined, and la_check_device_status reports
  * LA_ERR_TIMEOUT.  The setting is consumed by that one call.  LA_ERR_INVALID_ARG
  * for unit < 0 or spin_limit == 0.
- * la_paged_prefill in bf16: block `unit` does not announce the values of its first step,
- * and every wait has `spin_limit` polls (about 3.4 us each); it ends the same way with the
- * wait bit (0x1), and rows of other blocks' tiles alone are as ever.
+ * la_paged_prefill in bf16: block `unit` gets no queries, and the wait for them gives up
+ * after `spin_limit` polls (about 3.4 us each), and with it the block's other waits; it ends
+ * the same way with the wait bit (0x1), and rows of other blocks' tiles alone are as ever.
  */
 la_status la_debug_withhold_publication(int unit, unsigned spin_limit);
 

@@ -20,9 +20,8 @@ struct LaunchCtx {
     cudaMemPool_t pool;          // library-owned pool for stream-ordered scratch
     unsigned int* status_word;   // device error word for bounded waits
     // test hook (la_debug_withhold_publication): the unit whose look-back flag the next
-    // tensor-core causal or gated scan launch leaves unset, or the block whose first values
-    // the next bf16 prefill launch does not announce (-1: none), and the limit of the polls
-    // (0: default)
+    // tensor-core causal or gated scan launch leaves unset, or the block that gets no queries
+    // in the next bf16 prefill launch (-1: none), and the limit of the polls (0: default)
     int withhold_unit;
     unsigned spin_limit;
 };

@@ -284,9 +284,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         s_abort = 1;
         atomicOr(p.status, tcf::kErrWait);
     };
-    // Waits give up after p.limit polls, or once any of them has.
+    // Waits give up after kLimit polls, or once any of them has.
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const int e = mbar_wait_or(bar, parity & 1u, p.limit, const_cast<const volatile int*>(&s_abort));
+        const int e = mbar_wait_or(bar, parity & 1u, kLimit, const_cast<const volatile int*>(&s_abort));
         if (e == 2) fail();
         return e == 0;
     };
@@ -650,8 +650,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             // ---------------------------------------------------------------- queries, values seen in part
             const int t = 32 * (warp - 12) + lane;
             uint32_t item = 0, n_q = 0, step = 0;
-            const bool mute = warp == 12 && static_cast<int>(blockIdx.x) == p.withhold;
             bool ok = true;
+            if (warp == 12 && static_cast<int>(blockIdx.x) == p.withhold) {
+                // (test hook) no queries come: this wait for them gives up, and with it all the others
+                if (!mbar_wait(&s_qfull, 0, p.limit)) fail();
+                ok = false;
+            }
             for (Job k; ok && next(k);) {
                 const Segment& g = k.g;
                 if (n_q && !(ok = warp_wait(&s_qempty, n_q - 1))) break;
@@ -740,7 +744,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     // and the next step's keys, so that the products wait once
                     if (j + 1 < g.b && !(ok = warp_wait(s_full + (v + 1) % STAGES, (v + 1) / STAGES))) break;
                     __syncwarp();
-                    if (lane == 0 && (step || !mute)) mbar_arrive(s_vready + sg);
+                    if (lane == 0) mbar_arrive(s_vready + sg);
                 }
             }
             if (q_tma && n_q && t == 0 && !mbar_wait(&s_qfull, (n_q - 1) & 1u, kDrain)) fail();
@@ -780,7 +784,7 @@ cudaError_t paged_prefill_tc(const LaunchCtx& c, const bf16* q, const bf16* K, c
     p.s = s, p.table = table, p.lens = lens, p.starts = starts, p.lse = lse, p.fill = fill;
     p.status = c.status_word;
     p.withhold = c.withhold_unit;
-    p.limit = c.spin_limit ? c.spin_limit : kLimit;
+    p.limit = c.spin_limit;
     int per_sm = 1;
     cudaError_t e = resident_blocks<prefill_kernel<D>>(c.device, NT, Ly::SMEM, &per_sm);
     if (e != cudaSuccess) return e;

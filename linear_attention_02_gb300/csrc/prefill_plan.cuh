@@ -33,8 +33,8 @@ struct Args {
     float2* ml;    // [blocks][2][TM] their maxima (to base 2) and sums; a negative sum: no part
     int4* desc;    // [blocks][2] the cut tile whose first step is in the block's range: {request, key head, first row, rows}, {ranges, -, -, -}
     unsigned* status;
-    int withhold;    // test hook: a block that does not announce its first values (-1: none)
-    unsigned limit;  // polls of a wait
+    int withhold;    // test hook: a block that gets no queries (-1: none), and the polls of its wait for them
+    unsigned limit;
 };
 
 // Rounding 2^s / G up with s = 31 + ceil(log2 G) is off by less than 2^(s - 31) / 2^s of a

@@ -1,4 +1,4 @@
-"""The bf16 prefill's waits give up on values that are never announced, report it, and end."""
+"""The bf16 prefill's waits give up on queries that never come, report it, and end."""
 import pytest
 import torch
 
@@ -18,8 +18,8 @@ def _timed_out(la):
 @pytest.mark.parametrize("page", [4, 16])                                                   # both pages' ways
 @pytest.mark.parametrize("R,cached,new", [(1500, 0, 100), (40, 6000, 20)])                  # whole tiles, cut ones
 @pytest.mark.parametrize("unit", [0, 7])
-def test_values_that_are_not_announced(Hq, Hkv, D, page, R, cached, new, unit):
-    # (test hook) block `unit` does not announce the values of its first step: its waits give up after 20000 polls
+def test_queries_that_do_not_come(Hq, Hkv, D, page, R, cached, new, unit):
+    # (test hook) block `unit` gets no queries: its wait for them gives up after 20000 polls, and all others with it
     import linear_attention_02_gb300 as la
     la.la_check_device_status()
     W = -(-(cached + new) // page)
