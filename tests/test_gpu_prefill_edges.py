@@ -157,3 +157,20 @@ def test_a_pool_without_pages(page, dt):
     assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
     with pytest.raises(la.LinAttnError, match="BAD_INDEX"):
         la.la_check_device_status()
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_fp32_scores_do_not_lose_bits_with_the_heads_length(D):
+    # Rows that see one key, so lse is the score, a sum of D products of one sign.  Parts of 32 products are 12 sums on the matrix
+    # unit, each cut off by half a unit of the last place (2^-23) in the mean, of i / 12 of the part at the i-th: 3.25 x 2^-23.
+    # The operands' terms are off by 2^-22 of a product at most, by half of that in the mean, and what follows rounds
+    # three times, by 2^-24 each.  (In one chain of 48 sums: 12.25 x 2^-23.)
+    la = _la()
+    T = 700
+    g = torch.Generator().manual_seed(D)
+    q, K = (torch.rand(s, generator=g) * 0.2 + 0.9 for s in ((T, 2, D), (T, 1, 8, D)))
+    i32 = lambda n: torch.arange(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    _, lse = la.la_paged_prefill(q.cuda(), K.cuda(), K.cuda(), i32(T).view(T, 1), 0 * i32(T), i32(T + 1), return_lse=True)
+    want = torch.einsum("thd,td->th", q.double(), K[:, 0, 0].double()) / math.sqrt(D)
+    off = float(((lse.cpu().double() - want) / want).abs().mean())
+    assert off <= (3.25 + 1 + 1.5) * 2.0 ** -23
