@@ -441,8 +441,12 @@ size_t la_page_map_workspace_bytes(int R);
  * Positions whose page is out of range are left out; a row that sees none has out
  * 0 and lse -infinity.  What lies in the cache behind a row's position, or before
  * its window, does not reach the row, whatever it is.  An infinite element of a value row makes
- * its column of out infinite or NaN.  bf16: the weights are rounded to bf16 (2^-8 of
- * themselves, the outputs' own rounding) for the product with the values; their sum and lse are not.
+ * its column of out infinite or NaN.  Weighted values are summed in fp32 before the division by
+ * the weights' sum: where the sum of the |values| that a row sees (bf16: of 256 times them)
+ * passes the largest fp32 number, its column may be infinite or NaN too.  bf16: the weights are
+ * rounded to bf16 (2^-8 of themselves, the outputs' own rounding) for the product with the values;
+ * their sum and lse are not (la_paged_decode_step keeps its weights whole and returns fp32, so the
+ * same token's outputs of the two calls differ by these roundings).
  * D in {32, 64, 128}, Hq a multiple of Hkv, T * Hq < 2^30, R < 2^20,
  * max_pages * page_size < 2^30.  Results do not depend on the run.
  */
@@ -463,8 +467,9 @@ size_t la_paged_prefill_workspace_bytes(int D, la_dtype dtype, int num_sms);
  * Elements from rot on are copied.
  *
  * la_rotary_frequencies (host): the rot / 2 angles a position, as whole numbers of 2^-64
- * turns, which the calls below read from device memory; with them the phase of any
- * position is exact.  theta_i = base^(-2 i / rot) (base >= 1), and for contexts `factor`
+ * turns, which the calls below read from device memory; of these numbers the phase of any
+ * position is exact.  They are worked out in double, which puts an angle off by about
+ * p theta_i 2^-53 (at most 1.6e-7 at position 2^31).  theta_i = base^(-2 i / rot) (base >= 1), and for contexts `factor`
  * (>= 1) times longer than trained on
  *   LA_ROTARY_LINEAR    theta_i / factor
  *   LA_ROTARY_BASE      base factor^(rot / (rot - 2)) in place of base

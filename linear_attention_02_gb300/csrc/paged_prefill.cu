@@ -5,11 +5,11 @@
 // Query head h reads key head h / (Hq / Hkv).  Here fp32; bf16 is paged_prefill_tc.cu.
 //
 // Bound by the matrix unit: fp32 operands enter tf32 products (m16n8k8) as two terms split by
-// rounding, three products for each (the fourth, of two second terms, is below 2^-24 of the
-// whole).  A term of a score or an output is off by 2^-22 of itself at most, as much as D fp32
-// additions leave.  (The tensor core's sums in tensor memory are no way here: over thousands of keys
-// their truncation shows in fp32.  So each step's outputs are summed by the unit from zero and
-// added to the running sums in fp32.)
+// rounding, three products for each (the fourth, of two second terms, is below 2^-22 of the
+// whole, 2^-24 in the mean).  A term of a score or an output is off by 2^-21 of itself at most, 2^-23 in the mean.
+// The unit cuts off its sums: so scores are summed by it over 32 columns and outputs over a step, from zero,
+// and those added to the running sums in fp32.  (Running sums in the tensor core's own memory are cut off in
+// the same way; parts of them from zero, read back every step, were not tried.)
 //
 // A block takes a range of steps (prefill_plan.cuh): 128 rows of a request and key head, 16 a
 // warp, against 32 key positions that cp.async brings a step ahead.  The contraction index and the output
@@ -19,9 +19,10 @@
 // A value within 2^-12 of the largest fp32 number has an infinite first term.  Keeping it finite costs two
 // operations a value (6% of the time), so a segment with a NaN among its outputs is computed again, from halved values.
 //
-// Measured: 16 prompts of 1024 tokens, 16 heads of 64: 750 us, 46 TFLOP/s; 8 x 1024 of 8 heads of 128: 430 us;
-// 13 ragged requests up to 700 tokens with a window of 1000: 370 to 400 us (1940 with the products on the
-// fp32 units), the matrix unit's pipe half full and what stalls most.
+// Measured: 16 prompts of 1024 tokens, 16 heads of 64: 763 us, 45 TFLOP/s; 8 x 1024 of 8 heads of 128: 437 us;
+// 13 ragged requests up to 700 tokens with a window of 1000: 375 to 410 us (1940 with the products on the
+// fp32 units), the matrix unit's pipe half full and what stalls most.  48 requests of 1 to 8 tokens over 500 to
+// 16000 positions: 1390 us, as few rows leave most warps idle.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

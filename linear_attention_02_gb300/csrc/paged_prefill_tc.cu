@@ -16,11 +16,13 @@
 // thread (by lane 0 of a diverged warp they took three times as long); two warps load, as one does not keep
 // up with 2 KB copies of pages of 16 positions; they share a ring, whose stages serve either.
 //
-// Measured: chunks of 2048 tokens over 30 to 63 thousand positions, 32 heads of 128, 4 key heads: 2.12 ms,
-// 1.49 PFLOP/s.  32 prompts of 2048, 16 heads of 64: 465 us, 590 TFLOP/s, bound by the softmax's latency: a
-// step of a subtile is about 1400 cycles of loads, exponentials (4 a clock and quarter of an SM, 512 cycles at
-// least) and stores, and 800 until its next scores are there.  48 requests of 1 to 8 tokens over 500 to 16000
-// positions: 156 us, 5.2 TB/s.
+// Measured: chunks of 2048 tokens over 30 to 63 thousand positions, 32 heads of 128, 4 key heads: 2.12 to 2.32 ms
+// from run to run (the power limit), 1.36 to 1.49 PFLOP/s.  32 prompts of 2048, 16 heads of 64: 451 us, 610
+// TFLOP/s, bound by the softmax's latency: a step of 256 rows takes 1.86 us, in tiles of 512 steps 1.77 us, so it
+// is not what a tile begins and ends with.  A subtile's step is 4096 exponentials a quarter of an SM (8 a clock,
+// 512 cycles), loads and stores of tensor memory, and the wait for its next scores.  48 requests of 1 to 8 tokens
+// over 500 to 16000 positions: 158 us, 5.2 TB/s.  Where the compiler puts code moves short tiles by up to 15%
+// (a limit of the waits that was read from the arguments: 470 -> 540 us).
 //
 // The maximum is kept lazily: it is raised, and the sums so far rescaled in tensor memory, only when
 // a score passes it by more than 2^8.  The weights are rounded to bf16 for the product with

@@ -10,8 +10,10 @@
 // Angles.  theta_i is kept as a whole number f_i of 2^-64 turns, so that the phase of any
 // position is p f_i modulo 2^64: an integer product, exact for every position.  Its upper
 // 32 bits are taken to the nearest quarter turn and a rest of at most an eighth, an fp32
-// number with a rounding of 2^-25 of itself: an angle is off by 2.4e-8 at most, whether the
-// position is 1 or 2^31.  Its sine and cosine are summed from their series.
+// number with a rounding of 2^-25 of itself: an angle is off by 2.4e-8 at most from the position times the
+// stored frequency, whether the position is 1 or 2^31.  (The frequency itself comes from a theta_i in double, so
+// that theta_i's angle is off by another p theta_i 2^-53 or so: at most 1.6e-7 at position 2^31 for bases from 10^4
+// to 10^6.)  Its sine and cosine are summed from their series.
 //
 // Bound by memory: a row is read once and written once (with the norm's gradient, two are
 // read).  A thread holds one unit of a row: two pieces of 16 bytes whose elements are paired

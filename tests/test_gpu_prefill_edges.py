@@ -163,7 +163,7 @@ def test_a_pool_without_pages(page, dt):
 def test_fp32_scores_do_not_lose_bits_with_the_heads_length(D):
     # Rows that see one key, so lse is the score, a sum of D products of one sign.  Parts of 32 products are 12 sums on the matrix
     # unit, each cut off by half a unit of the last place (2^-23) in the mean, of i / 12 of the part at the i-th: 3.25 x 2^-23.
-    # The operands' terms are off by 2^-22 of a product at most, by half of that in the mean, and what follows rounds
+    # The operands' terms are off by 2^-21 of a product at most, by 2^-23 in the mean, and what follows rounds
     # three times, by 2^-24 each.  (In one chain of 48 sums: 12.25 x 2^-23.)
     la = _la()
     T = 700
